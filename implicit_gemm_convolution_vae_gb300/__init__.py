@@ -24,6 +24,8 @@ __all__ = [
     "selftest_wait_timeout", "conv3x3_nhwc", "conv3x3_nhwc_rms", "conv3x3_nhwc_gn", "conv3x3_gn_workspace_bytes", "groupnorm_apply",
     "conv1x1", "rmsnorm_silu", "groupnorm_silu",
     "groupnorm_workspace_bytes", "cast_f16", "mid_attention", "mid_attention_workspace_bytes",
+    "layernorm", "layernorm_backward", "layernorm_backward_workspace_bytes", "RopePlan", "rope",
+    "attention", "attention_workspace_bytes", "attention_backward", "attention_backward_workspace_bytes",
     "Decoder", "DecodeGraph", "pack_conv3x3", "pack_conv1x1",
     "UPSAMPLE2X", "PAD_REPLICATE", "PAD_REFLECT", "DOWNSAMPLE2X", "EPI_SILU", "OUT_F16", "FAMILY_GN", "FAMILY_RMS",
     "NORM_GROUP", "NORM_RMS",
@@ -73,6 +75,15 @@ SIGNATURES = {
     "vae_cast_f16": ([_P, _SZ, _I, _P, _F, _P, _P], _I),
     "vae_mid_attention_workspace_bytes": ([_I, _I, _I], _SZ),
     "vae_mid_attention": ([_P, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "vae_layernorm": ([_P, _I, _I, _I, _P, _P, _F, _P, _I, _P], _I),
+    "vae_layernorm_backward_workspace_bytes": ([_I, _I], _SZ),
+    "vae_layernorm_backward": ([_P, _I, _P, _I, _I, _I, _P, _F, _P, _P, _P, _P, _SZ, _P], _I),
+    "vae_rope_plan_init": ([_P, _I, _P, ctypes.c_double, _I], _I),
+    "vae_rope": ([_P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P], _I),
+    "vae_attention_workspace_bytes": ([_P], _SZ),
+    "vae_attention": ([_P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "vae_attention_backward_workspace_bytes": ([_P], _SZ),
+    "vae_attention_backward": ([_P] * 11 + [_SZ, _P], _I),
     "vae_decoder_create": ([_P, ctypes.POINTER(_P)], _I),
     "vae_decoder_destroy": ([_P], _I),
     "vae_decode_workspace": ([_P, _I, _I, _P, ctypes.POINTER(_SZ)], _I),
@@ -400,6 +411,301 @@ def mid_attention(x, norm_kind: int, gamma, beta, wq, bq, wk, bk, wv, bv, wo, bo
                                    _ptr(bo), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                    _stream(stream)))
     return x
+
+
+# ───────────────────────── operators on latent tokens ─────────────────────────
+
+def _type(t, name):
+    """The C ABI's element type of a tensor or torch dtype."""
+    import torch
+    dt = t if isinstance(t, torch.dtype) else t.dtype
+    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dt)
+    if code is None:
+        raise VaeError(-1, f"{name} must be float32, float16 or bfloat16, got {dt}")
+    return code
+
+
+class _On:
+    """For a call: checks that ``tensors`` (a dict by name) share a device, makes it the current one,
+    and ``stream``, where one is given, the current stream, so that what the call allocates and
+    fills belongs to the stream that it runs on."""
+
+    def __init__(self, tensors, stream):
+        first = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise VaeError(-1, f"{name} must be a CUDA tensor")
+            if first is None:
+                first = t.device
+            elif t.device != first:
+                raise VaeError(-1, f"{name} is on {t.device}, the others on {first}")
+        self.index, self.stream = first.index, None
+        if stream is not None:
+            import torch
+            if stream.device.index != self.index:
+                raise VaeError(-1, f"the stream is on {stream.device}, the tensors on {first}")
+            self.stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        import torch
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.back != self.index:
+            import torch
+            torch.cuda.set_device(self.back)
+
+
+def _given(tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise VaeError(-1, f"{name} is needed")
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise VaeError(-2, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t, name):
+    if t.dim() != 2:
+        raise VaeError(-2, f"{name} must have 2 dims, got {t.dim()}")
+    if not t.is_contiguous():
+        raise VaeError(-1, f"{name} must be contiguous")
+
+
+def layernorm(x, gamma=None, beta=None, eps: float = 1e-6, out_dtype=None, out=None, stream=None):
+    """Layer norm of each row of x [m][c] (f32, f16 or bf16); gamma, beta f32 [c] or None.
+    The result has ``out_dtype`` (default: x's), or is written into ``out``."""
+    import torch
+    _given({"x": x})
+    with _On({"x": x, "gamma": gamma, "beta": beta, "out": out}, stream):
+        _rows(x, "x")
+        m, c = x.shape
+        for t, nm in ((gamma, "gamma"), (beta, "beta")):
+            _need(t, torch.float32, nm, 1)
+            _shape(t, (c,), nm)
+        if out is None:
+            out = torch.empty((m, c), dtype=out_dtype or x.dtype, device=x.device)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise VaeError(-1, f"out must be {out_dtype}, got {out.dtype}")
+        _rows(out, "out")
+        _shape(out, (m, c), "out")
+        _check(lib().vae_layernorm(_ptr(x), _type(x, "x"), m, c, _ptr(gamma), _ptr(beta), float(eps), _ptr(out),
+                                   _type(out, "out"), _stream(stream)))
+    return out
+
+
+def layernorm_backward_workspace_bytes(m: int, c: int) -> int:
+    return int(lib().vae_layernorm_backward_workspace_bytes(m, c))
+
+
+def layernorm_backward(dy, x, gamma=None, eps: float = 1e-6, weight_grads: bool = True, dx=None, dgamma=None,
+                       dbeta=None, workspace=None, stream=None):
+    """The gradient of layernorm at x [m][c] for dy [m][c]: (dx of x's type, dgamma, dbeta f32 [c]);
+    with ``weight_grads`` False the last two are None and not computed."""
+    import torch
+    _given({"dy": dy, "x": x})
+    with _On({"dy": dy, "x": x, "gamma": gamma, "dx": dx, "dgamma": dgamma, "dbeta": dbeta, "workspace": workspace}, stream):
+        _rows(x, "x")
+        _rows(dy, "dy")
+        m, c = x.shape
+        _shape(dy, (m, c), "dy")
+        if dx is None:
+            dx = torch.empty_like(x)
+        _need(dx, x.dtype, "dx", 2)
+        _shape(dx, (m, c), "dx")
+        if weight_grads:
+            dgamma = torch.empty((c,), dtype=torch.float32, device=x.device) if dgamma is None else dgamma
+            dbeta = torch.empty((c,), dtype=torch.float32, device=x.device) if dbeta is None else dbeta
+            if workspace is None:
+                workspace = torch.empty(max(layernorm_backward_workspace_bytes(m, c), 16), dtype=torch.uint8,
+                                        device=x.device)
+        elif dgamma is not None or dbeta is not None:
+            raise VaeError(-1, "dgamma and dbeta need weight_grads")
+        for t, nm in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")):
+            _need(t, torch.float32, nm, 1)
+            _shape(t, (c,), nm)
+        _check(lib().vae_layernorm_backward(_ptr(dy), _type(dy, "dy"), _ptr(x), _type(x, "x"), m, c, _ptr(gamma),
+                                            float(eps), _ptr(dx), _ptr(dgamma), _ptr(dbeta), *_work(workspace),
+                                            _stream(stream)))
+    return dx, dgamma, dbeta
+
+
+def _work(workspace):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise VaeError(-1, "workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("naxes", _I), ("pairs", _I), ("interleaved", _I), ("turns_hi", _F * 128), ("turns_lo", _F * 128),
+                ("axis", ctypes.c_ubyte * 128)]
+
+
+class RopePlan:
+    """The pairs and frequencies of a rotary embedding: ``axes`` channels per axis (even numbers),
+    ``theta`` the base, pairs (2p, 2p + 1) when ``interleaved``, else (p, p + R/2)."""
+
+    def __init__(self, axes, theta: float = 10000.0, interleaved: bool = True):
+        self.axes = tuple(int(a) for a in axes)
+        self._plan = _RopePlan()
+        dims = (_I * max(1, len(self.axes)))(*self.axes)
+        _check(lib().vae_rope_plan_init(ctypes.byref(self._plan), len(self.axes), dims, float(theta),
+                                        int(bool(interleaved))))
+
+
+def _strides3(t, name):
+    """{batch, token, head} strides of a [b][n][heads][d] tensor whose channels are contiguous."""
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise VaeError(-1, f"{name}'s last dim must be contiguous")
+    return (ctypes.c_longlong * 3)(t.stride(0), t.stride(1), t.stride(2))
+
+
+def rope(x, positions, plan: RopePlan, inverse: bool = False, out=None, stream=None):
+    """Turns the pairs of x [b][s][h][d] (strides free, channels contiguous) by their angles at
+    ``positions`` [s][axes] or [b][s][axes] (f32 or int32); ``inverse`` turns back (the gradient).
+    ``out`` may be x."""
+    import torch
+    _given({"x": x, "positions": positions})
+    with _On({"x": x, "positions": positions, "out": out}, stream):
+        if x.dim() != 4:
+            raise VaeError(-2, f"x must have 4 dims, got {x.dim()}")
+        b, s, h, d = x.shape
+        if positions.dtype not in (torch.float32, torch.int32):
+            raise VaeError(-1, f"positions must be float32 or int32, got {positions.dtype}")
+        if not positions.is_contiguous():
+            raise VaeError(-1, "positions must be contiguous")
+        na = len(plan.axes)
+        pb = positions.shape[0] if positions.dim() == 3 else 1
+        _shape(positions, (s, na) if positions.dim() == 2 else (pb, s, na), "positions")
+        if out is None:
+            out = torch.empty((b, s, h, d), dtype=x.dtype, device=x.device)
+        _shape(out, (b, s, h, d), "out")
+        if out.dtype != x.dtype:
+            raise VaeError(-1, f"out must be {x.dtype}, got {out.dtype}")
+        _check(lib().vae_rope(_ptr(x), _type(x, "x"), b, s, h, d, _strides3(x, "x"), _ptr(positions),
+                              int(positions.dtype == torch.int32), pb, ctypes.byref(plan._plan), int(bool(inverse)),
+                              _ptr(out), _strides3(out, "out"), _stream(stream)))
+    return out
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("type", _I), ("b", _I), ("sq", _I), ("sk", _I), ("hq", _I), ("hkv", _I), ("d", _I), ("scale", _F),
+                ("block", _I), ("q_len", _P), ("k_len", _P)] + \
+               [(n + "_stride", ctypes.c_longlong * 3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")]
+
+
+def _attention_desc(q, k, v, scale, q_len, k_len, block):
+    """The desc of a call without the outputs' strides; checks the tensors' shapes and types."""
+    import torch
+    for t, nm in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != 4:
+            raise VaeError(-2, f"{nm} must have 4 dims, got {t.dim()}")
+        if t.dtype != q.dtype:
+            raise VaeError(-1, f"{nm} must be {q.dtype}, got {t.dtype}")
+    b, sq, hq, d = q.shape
+    sk, hkv = k.shape[1], k.shape[2]
+    _shape(k, (b, sk, hkv, d), "k")
+    _shape(v, (b, sk, hkv, d), "v")
+    for t, nm in ((q_len, "q_len"), (k_len, "k_len")):
+        _need(t, torch.int32, nm, 1)
+        _shape(t, (b,), nm)
+    a = AttentionDesc(_type(q, "q"), b, sq, sk, hq, hkv, d, 1.0 / d ** 0.5 if scale is None else float(scale),
+                      int(block), _ptr(q_len), _ptr(k_len))
+    a.q_stride, a.k_stride, a.v_stride = _strides3(q, "q"), _strides3(k, "k"), _strides3(v, "v")
+    return a
+
+
+def _like(t, ref, shape, name, lens):
+    """``t`` checked, or a new tensor (zeros where ``lens`` leaves rows unwritten)."""
+    import torch
+    if t is None:
+        return (torch.empty if lens is None else torch.zeros)(shape, dtype=ref.dtype, device=ref.device)
+    _shape(t, shape, name)
+    if t.dtype != ref.dtype:
+        raise VaeError(-1, f"{name} must be {ref.dtype}, got {t.dtype}")
+    return t
+
+
+def _dense(b, n, h, d):
+    return (ctypes.c_longlong * 3)(n * h * d, h * d, d)
+
+
+def attention_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
+    a = AttentionDesc(1, b, sq, sk, hq, hkv, d, 1.0, block)
+    a.q_stride = a.o_stride = _dense(b, sq, hq, d)
+    a.k_stride = a.v_stride = _dense(b, sk, hkv, d)
+    return int(lib().vae_attention_workspace_bytes(ctypes.byref(a)))
+
+
+def attention(q, k, v, scale: Optional[float] = None, q_len=None, k_len=None, block: int = 0, out=None, lse=None,
+              workspace=None, stream=None):
+    """Multi-head attention of q [b][sq][hq][d] over k, v [b][sk][hkv][d] (f16 or bf16, strides free,
+    channels contiguous; scale default 1/sqrt(d)). q_len, k_len int32 [b]: the valid rows of a padded
+    batch. block 0: every valid key; block > 0: the keys of the query's own block of that many
+    positions and of the earlier ones (1: causal). Returns (o, lse f32 [b][hq][sq]); rows behind q_len
+    are left as they were in ``out`` and ``lse``, 0 and -inf in new ones."""
+    import torch
+    _given({"q": q, "k": k, "v": v})
+    with _On({"q": q, "k": k, "v": v, "q_len": q_len, "k_len": k_len, "out": out, "lse": lse,
+                  "workspace": workspace}, stream):
+        a = _attention_desc(q, k, v, scale, q_len, k_len, block)
+        out = _like(out, q, (a.b, a.sq, a.hq, a.d), "out", q_len)
+        a.o_stride = _strides3(out, "out")
+        if lse is None:
+            lse = torch.empty((a.b, a.hq, a.sq), dtype=torch.float32, device=q.device) if q_len is None else \
+                torch.full((a.b, a.hq, a.sq), -float("inf"), dtype=torch.float32, device=q.device)
+        _need(lse, torch.float32, "lse", 3)
+        _shape(lse, (a.b, a.hq, a.sq), "lse")
+        if workspace is None:
+            nb = lib().vae_attention_workspace_bytes(ctypes.byref(a))
+            workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+        _check(lib().vae_attention(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                   *_work(workspace), _stream(stream)))
+    return out, lse
+
+
+def attention_backward_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
+    a = AttentionDesc(1, b, sq, sk, hq, hkv, d, 1.0, block)
+    a.q_stride = a.o_stride = a.do_stride = a.dq_stride = _dense(b, sq, hq, d)
+    a.k_stride = a.v_stride = a.dk_stride = a.dv_stride = _dense(b, sk, hkv, d)
+    return int(lib().vae_attention_backward_workspace_bytes(ctypes.byref(a)))
+
+
+def attention_backward(do, q, k, v, o, lse, scale: Optional[float] = None, q_len=None, k_len=None, block: int = 0,
+                       dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """The gradient of attention for do [b][sq][hq][d], from o and lse of the same call: (dq, dk, dv).
+    Rows behind q_len and k_len are left as they were, 0 in new tensors."""
+    import torch
+    _given({"do": do, "q": q, "k": k, "v": v, "o": o, "lse": lse})
+    with _On({"do": do, "q": q, "k": k, "v": v, "o": o, "lse": lse, "q_len": q_len, "k_len": k_len, "dq": dq,
+                  "dk": dk, "dv": dv, "workspace": workspace}, stream):
+        a = _attention_desc(q, k, v, scale, q_len, k_len, block)
+        do, o = _like(do, q, q.shape, "do", None), _like(o, q, q.shape, "o", None)
+        _need(lse, torch.float32, "lse", 3)
+        _shape(lse, (a.b, a.hq, a.sq), "lse")
+        dq = _like(dq, q, q.shape, "dq", q_len)
+        dk, dv = _like(dk, k, k.shape, "dk", k_len), _like(dv, k, k.shape, "dv", k_len)
+        for nm, t in (("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
+            setattr(a, nm + "_stride", _strides3(t, nm))
+        if workspace is None:
+            nb = lib().vae_attention_backward_workspace_bytes(ctypes.byref(a))
+            workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
+        _check(lib().vae_attention_backward(ctypes.byref(a), _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                            _ptr(dq), _ptr(dk), _ptr(dv), *_work(workspace), _stream(stream)))
+    return dq, dk, dv
 
 
 # ───────────────────────────── weight layouts ─────────────────────────────

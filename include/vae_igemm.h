@@ -337,6 +337,133 @@ int vae_mid_attention(float* x_dev, int m, int c, int norm_kind, int groups, flo
                       const void* wv_dev, const float* bv_dev, const void* wo_dev, const float* bo_dev,
                       void* workspace_dev, size_t workspace_bytes, vae_stream_t stream);
 
+/* ───────────────────── operators on latent tokens ─────────────────────
+ *
+ * What stands around the decoders in a model that makes latents, and in its
+ * training: layer norm, rotary positions over (time, height, width) and
+ * multi-head attention within padded batches or from frame to earlier
+ * frames, each with its gradient. Tokens are the pixels of a latent grid;
+ * the projections between them are vae_conv1x1. */
+
+/* Element types. Statistics, sums and softmax run in f32 whatever the type;
+ * a result is rounded to its type once (to nearest, ties to even). */
+enum { VAE_F32 = 0, VAE_F16 = 1, VAE_BF16 = 2 };
+
+/*
+ * Layer norm of each row:
+ *   mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps),
+ *   y = (x - mu) * rstd * gamma + beta.
+ *   x_dev [m][c] of x_type; y_dev [m][c] of y_type (may equal x_dev when the
+ *   types are the same); gamma_dev, beta_dev f32 [c], each or both NULL
+ *   (1 and 0).
+ * Requirements: m >= 1, 1 <= c <= 16384, eps >= 0 and finite; pointers
+ * 16-byte aligned. Rows of c % 8 == 0 take 16-byte loads, others scalar ones.
+ */
+int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamma_dev, const float* beta_dev,
+                  float eps, void* y_dev, int y_type, vae_stream_t stream);
+
+/*
+ * Its gradient. With n = (x - mu) * rstd (recomputed from x: nothing is kept
+ * from the forward call) and g = dy * gamma,
+ *   dx = rstd * (g - mean(g) - n * mean(g * n)),
+ *   dgamma = sum over rows of dy * n,  dbeta = sum over rows of dy.
+ *   dy_dev [m][c] of dy_type; x_dev, dx_dev [m][c] of x_type (dx_dev may equal
+ *   x_dev); dgamma_dev, dbeta_dev f32 [c], written (not added to), both or
+ *   neither NULL (NULL: not computed); gamma_dev as above.
+ *   workspace_dev of vae_layernorm_backward_workspace_bytes(m, c) bytes,
+ *   16-byte aligned, contents ignored on entry; NULL is fine when dgamma_dev
+ *   is NULL. The row sums are taken in a fixed order: the same inputs give the
+ *   same bits.
+ */
+size_t vae_layernorm_backward_workspace_bytes(int m, int c);
+int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, int x_type, int m, int c,
+                           const float* gamma_dev, float eps, void* dx_dev, float* dgamma_dev, float* dbeta_dev,
+                           void* workspace_dev, size_t workspace_bytes, vae_stream_t stream);
+
+/*
+ * Rotary positions over up to four axes. dims[a] channels (even; 0: the axis
+ * turns nothing) of each head turn with axis a; pair i of them by the angle
+ * position[a] * theta^(-2 i / dims[a]). The pairs of axis 0 come first, then
+ * those of axis 1, ...; with R = the sum of dims, pair p is the channels
+ * (2p, 2p + 1) when interleaved, else (p, p + R/2). Channels from R on are
+ * copied. A plan is plain host memory that the caller owns; it holds each
+ * pair's turns per position as two floats, so that far positions keep their
+ * angle (an error of a few 2^-24 turns up to |position| ~ 2^24).
+ * vae_rope_plan_init: 1 <= naxes <= 4, R <= 256, R >= 2, theta >= 1 and finite.
+ */
+enum { VAE_ROPE_MAX_PAIRS = 128 };
+typedef struct {
+    int naxes, pairs, interleaved;
+    float turns_hi[VAE_ROPE_MAX_PAIRS], turns_lo[VAE_ROPE_MAX_PAIRS];
+    unsigned char axis[VAE_ROPE_MAX_PAIRS];
+} vae_rope_plan;
+int vae_rope_plan_init(vae_rope_plan* plan, int naxes, const int* dims, double theta, int interleaved);
+
+/*
+ * Turns every pair of x by its angle (inverse != 0: by its negative, which is
+ * also the gradient): (a, b) -> (a cos - b sin, a sin + b cos), in f32, rounded
+ * once.
+ *   x_dev [b][s][h][d] of `type`, strides in elements x_stride = {batch, token,
+ *   head}, channels contiguous; y_dev likewise with y_stride (may be x_dev with
+ *   the same strides, else the two must not overlap). Queries and keys that lie
+ *   beside one another turn in one call.
+ *   pos_dev [pos_batch][s][naxes], f32 or int32 (pos_int != 0), pos_batch = 1
+ *   (shared by the batch) or b.
+ * Requirements: b, s, h >= 1, 2 * plan pairs <= d <= 256, strides >= 0.
+ */
+int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long long x_stride[3],
+             const void* pos_dev, int pos_int, int pos_batch, const vae_rope_plan* plan, int inverse,
+             void* y_dev, const long long y_stride[3], vae_stream_t stream);
+
+/*
+ * Multi-head attention: o = softmax(scale * q k^T over the keys a query sees) v
+ * and lse = log(sum of exp) of each row.
+ *   q [b][sq][hq][d], k, v [b][sk][hkv][d], o [b][sq][hq][d], all of `type`
+ *   (VAE_F16 or VAE_BF16); query head h reads key head h / (hq / hkv).
+ *   *_stride: {batch, token, head} in elements, channels contiguous.
+ *   lse_dev f32 [b][hq][sq].
+ *   q_len_dev, k_len_dev int32 [b] on the device or NULL (all of sq, sk): the
+ *   valid rows of a padded batch; values outside [0, sq], [0, sk] are clamped.
+ *   block: 0: a query sees every valid key. block > 0 (frames of `block`
+ *   tokens; 1: causal): with ql, kl the valid lengths, query i stands at
+ *   position i + kl - ql and sees the keys of its own block and the earlier
+ *   ones, j < (floor(position / block) + 1) * block; at a negative position none.
+ * A row that sees no key gives o = 0, lse = -infinity. Rows from ql on are not
+ * written. Keys and values from kl on, and queries from ql on, may hold
+ * anything; a key within kl that a row does not see must be finite.
+ * vae_attention_backward: with P = exp(scale q k^T - lse), D = sum(do * o),
+ *   dv = P^T do, dS = P * (do v^T - D) * scale, dq = dS k, dk = dS^T q,
+ *   summed over the query heads that share a key head; o and lse from
+ *   vae_attention of the same inputs. P is recomputed; dk and dv are formed per
+ *   key tile and dq per query tile, in a fixed order: the same inputs give the
+ *   same bits. dq rows from ql on and dk, dv rows from kl on are not written.
+ * Requirements: b, sq, sk >= 1; hq % hkv == 0; d % 8 == 0, 8 <= d <= 128;
+ * scale > 0 and finite; pointers 16-byte aligned; strides multiples of 8,
+ * positive where the dimension is over 1 (a broadcast is not taken: give k and
+ * v their hkv heads). b * hq * sq and b * hkv * sk at most 2^31 - 256.
+ * workspace_dev: vae_attention_workspace_bytes(desc) /
+ * vae_attention_backward_workspace_bytes(desc) bytes, 16-byte aligned, contents
+ * ignored on entry, NULL where that is 0. Both depend on the desc's sizes alone.
+ */
+typedef struct {
+    int type;
+    int b, sq, sk, hq, hkv, d;
+    float scale;
+    int block;
+    const int* q_len_dev;
+    const int* k_len_dev;
+    long long q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+    /* backward only */
+    long long do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+} vae_attention_desc;
+size_t vae_attention_workspace_bytes(const vae_attention_desc* desc);
+int vae_attention(const vae_attention_desc* desc, const void* q_dev, const void* k_dev, const void* v_dev,
+                  void* o_dev, float* lse_dev, void* workspace_dev, size_t workspace_bytes, vae_stream_t stream);
+size_t vae_attention_backward_workspace_bytes(const vae_attention_desc* desc);
+int vae_attention_backward(const vae_attention_desc* desc, const void* do_dev, const void* q_dev, const void* k_dev,
+                           const void* v_dev, const void* o_dev, const float* lse_dev, void* dq_dev, void* dk_dev,
+                           void* dv_dev, void* workspace_dev, size_t workspace_bytes, vae_stream_t stream);
+
 /* ───────────────────────────── whole decoder ───────────────────────────── */
 
 /* Host-side description of a decoder, mirroring "vae.rs" VaeChainArgs and
