@@ -1,16 +1,15 @@
 // Multi-head attention on latent tokens and its gradient (public entry points
 // at the end).
 //
-// Four threads share a row and hold a quarter of its channels each in
-// registers; the other side's rows pass through shared memory in tiles of 32,
-// converted to f32. The forward is one pass with a running maximum and sum.
-// The gradient runs twice over the pairs: once per query row for dq, once per
+// The gradient: four threads share a row and hold a quarter of its channels
+// each in registers; the other side's rows pass through shared memory in tiles
+// of 32, converted to f32. It runs twice over the pairs: once per query row for dq, once per
 // key row (over the queries and the heads that share the key) for dk and dv;
 // the probabilities are recomputed from lse in both, and nothing is added
 // across threads in an order that could change.
 #include <cmath>
 
-#include "vae_mha.cuh"
+#include "vae_mha_fwd.h"
 
 namespace vae {
 
@@ -52,9 +51,29 @@ int mha_check(const vae_attention_desc* a, bool backward, MhaShape* s) {
     s->g = a->hq / a->hkv;
     s->d = a->d;
     s->block = a->block;
+    // gp: the largest power of two in g, a tile's rows at most
+    s->gp_log2 = 0;
+    while (s->gp_log2 < 7 && s->g % (2 << s->gp_log2) == 0) ++s->gp_log2;
+    s->nsub = s->g >> s->gp_log2;
+    const long long rows = static_cast<long long>(a->sq) << s->gp_log2;
+    s->ntile = static_cast<int>((rows + kMhaTile - 1) / kMhaTile);
+    s->nkb = (a->sk - 1) / kMhaTile + 1;
     s->q_len = a->q_len_dev;
     s->k_len = a->k_len_dev;
     return VAE_OK;
+}
+
+int mha_map(CUtensorMap* map, const vae_attention_desc* a, const void* p, const long long* stride, int n, int h,
+            int heads, int tokens) {
+    const uint64_t dims[4] = {static_cast<uint64_t>(a->d), static_cast<uint64_t>(h), static_cast<uint64_t>(n),
+                              static_cast<uint64_t>(a->b)};
+    // (the stride of a dimension of one is never used: any valid value)
+    const uint64_t st[3] = {h > 1 ? static_cast<uint64_t>(stride[2]) * 2 : 16,
+                            n > 1 ? static_cast<uint64_t>(stride[1]) * 2 : 16,
+                            a->b > 1 ? static_cast<uint64_t>(stride[0]) * 2 : 16};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(heads), static_cast<uint32_t>(tokens), 1};
+    return encode_tiled(map, a->type == VAE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        p, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 namespace {
@@ -119,45 +138,6 @@ __device__ __forceinline__ void store_row_q(void* p, long long off, int d, int p
         const int at = (e / 8 * 4 + part) * 8;
         if (at < d) store8<T>(x + at, t);
     }
-}
-
-template <int T>
-__global__ void __launch_bounds__(kThreads) mha_fwd_kernel(MhaShape s, float scale, const void* q, Strides qs, const void* k,
-                                                           Strides ks, const void* v, Strides vs, void* o, Strides os,
-                                                           float* lse) {
-    __shared__ float kt[kTile][kPitch], vt[kTile][kPitch];
-    pdl_wait();
-    const int e = blockIdx.z, h = blockIdx.y, hk = h / s.g, part = threadIdx.x & 3;
-    const int i = blockIdx.x * kRows + threadIdx.x / 4;
-    const int ql = mha_len(s.q_len, e, s.sq), kl = mha_len(s.k_len, e, s.sk);
-    const int lim = i < ql ? mha_key_limit(i, ql, kl, s.block) : 0;
-    const int i1 = min(ql, static_cast<int>(blockIdx.x + 1) * kRows) - 1;  // the block's last row sees the most
-    const int blim = i1 >= static_cast<int>(blockIdx.x) * kRows ? mha_key_limit(i1, ql, kl, s.block) : 0;
-    float a[kQuarter], acc[kQuarter];
-    load_row_q<T>(q, e * qs.b + static_cast<long long>(i) * qs.s + h * qs.h, s.d, part, i < ql, a);
-#pragma unroll
-    for (int c = 0; c < kQuarter; ++c) acc[c] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int j0 = 0; j0 < blim; j0 += kTile) {
-        __syncthreads();
-        load_tile<T>(k, e * ks.b + hk * ks.h, ks.s, j0, kl, s.d, kt);
-        load_tile<T>(v, e * vs.b + hk * vs.h, vs.s, j0, kl, s.d, vt);
-        __syncthreads();
-        for (int j = 0; j < kTile; ++j) {
-            const float x = part_dot(a, kt[j], part) * scale;
-            if (j0 + j >= lim) continue;
-            const float mn = fmaxf(m, x);
-            const float w = expf(x - mn), al = expf(m - mn);
-            m = mn;
-            l = l * al + w;
-#pragma unroll
-            for (int c = 0; c < kQuarter; ++c) acc[c] *= al;
-            part_axpy(acc, w, vt[j], part);
-        }
-    }
-    if (i >= ql) return;
-    store_row_q<T>(o, e * os.b + static_cast<long long>(i) * os.s + h * os.h, s.d, part, acc, l > 0.f ? 1.f / l : 0.f);
-    if (part == 0) lse[(static_cast<long long>(e) * s.hq + h) * s.sq + i] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 // D = sum(do * o) of each row.
@@ -257,14 +237,6 @@ size_t bwd_bytes(const MhaShape& s) {
 }
 
 template <int T>
-cudaError_t fwd_launch(const vae_attention_desc* a, const MhaShape& s, const void* q, const void* k, const void* v, void* o,
-                       float* lse, cudaStream_t st) {
-    const dim3 grid((s.sq + kRows - 1) / kRows, s.hq, s.b);
-    return launch_kernel(mha_fwd_kernel<T>, grid, dim3(kThreads), 0, st, s, a->scale, q, strides(a->q_stride), k,
-                         strides(a->k_stride), v, strides(a->v_stride), o, strides(a->o_stride), lse);
-}
-
-template <int T>
 cudaError_t bwd_launch(const vae_attention_desc* a, const MhaShape& s, const void* dout, const void* q, const void* k,
                        const void* v, const void* o, const float* lse, void* dq, void* dk, void* dv, float* delta,
                        cudaStream_t st) {
@@ -290,7 +262,8 @@ extern "C" {
 
 size_t vae_attention_workspace_bytes(const vae_attention_desc* desc) {
     clear_error();
-    return 0;
+    MhaShape s;
+    return mha_check(desc, false, &s) == VAE_OK ? mha_fwd_bytes(s) : 0;
 }
 
 int vae_attention(const vae_attention_desc* desc, const void* q_dev, const void* k_dev, const void* v_dev, void* o_dev,
@@ -304,14 +277,12 @@ int vae_attention(const vae_attention_desc* desc, const void* q_dev, const void*
     if (!aligned16(q_dev) || !aligned16(k_dev) || !aligned16(v_dev) || !aligned16(o_dev) || !aligned16(lse_dev) ||
         !aligned16(workspace_dev))
         return set_error(VAE_ERR_ALIGN, "attention: pointers must be 16-byte aligned");
-    const size_t need = vae_attention_workspace_bytes(desc);
+    const size_t need = mha_fwd_bytes(s);
     if (need > 0 && (workspace_dev == nullptr || workspace_bytes < need))
         return set_error(VAE_ERR_NOMEM, "attention: workspace of %zu bytes, %zu needed", workspace_bytes, need);
     if ((rc = check_device()) != VAE_OK) return rc;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    VAE_CUDA_CHECK(desc->type == VAE_F16 ? fwd_launch<VAE_F16>(desc, s, q_dev, k_dev, v_dev, o_dev, lse_dev, st)
-                                         : fwd_launch<VAE_BF16>(desc, s, q_dev, k_dev, v_dev, o_dev, lse_dev, st));
-    return VAE_OK;
+    return mha_fwd_run(desc, s, q_dev, k_dev, v_dev, o_dev, lse_dev, workspace_dev,
+                       reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t vae_attention_backward_workspace_bytes(const vae_attention_desc* desc) {

@@ -1,5 +1,13 @@
 // Multi-head attention on latent tokens: what the forward and the gradient
-// kernels share. Which keys a row sees, argument checks, sizes.
+// kernels share. Which keys a row sees, how rows are tiled, argument checks,
+// and the tcgen05 pieces that the mid attention does not use: operands stored
+// with the contraction index outside (MN-major) and left operands in TMEM.
+//
+// Rows. The query heads that share a key head stand side by side as rows: with
+// gp the largest power of two that divides g = hq / hkv (128 at most), row
+// r = token * gp + head of the group, so that one 128-row tile of q (a TMA box
+// of 128/gp tokens x gp heads) meets each key tile once for all of them. What
+// is left of g (sub = g / gp) are tiles of their own.
 #pragma once
 
 #include "vae_types.cuh"
@@ -8,8 +16,14 @@ namespace vae {
 
 struct MhaShape {
     int b, sq, sk, hq, hkv, g, d, block;
+    int gp_log2, nsub;  // gp = 1 << gp_log2, nsub = g / gp
+    int ntile;          // 128-row tiles of sq * gp rows
+    int nkb;            // 128-key tiles of sk
     const int *q_len, *k_len;
 };
+
+constexpr int kMhaTile = 128;          // rows of q and keys per tile
+constexpr int kMhaChunkBytes = 16384;  // 128 rows x 64 channels of 16 bits, 128-byte swizzle
 
 // The valid length of batch entry `e`: lens[e] clamped to [0, n], or n.
 __device__ __forceinline__ int mha_len(const int* lens, int e, int n) {
@@ -30,5 +44,90 @@ __device__ __forceinline__ int mha_key_limit(int i, int ql, int kl, int block) {
 
 // Checks the desc (backward: the gradients' strides too); fills `s`.
 int mha_check(const vae_attention_desc* d, bool backward, MhaShape* s);
+
+struct MhaStrides {
+    long long b, s, h;
+};
+inline MhaStrides mha_strides(const long long* st) { return {st[0], st[1], st[2]}; }
+
+// Tensor map of a [b][n][h][d] tensor of 16-bit elements: boxes of 64 channels
+// x `heads` heads x `tokens` tokens; what lies behind d or n reads as 0.
+int mha_map(CUtensorMap* map, const vae_attention_desc* a, const void* p, const long long* stride, int n, int h,
+            int heads, int tokens);
+
+// ───────────────────────────── tcgen05 pieces ─────────────────────────────
+
+// Instruction descriptor of kind::f16 with f32 accumulators: A K-major (or in
+// TMEM), B K-major, or MN-major when trans_b.
+__host__ __device__ constexpr uint32_t mha_idesc(int type, int M, int N, bool trans_b) {
+    return (1u << 4) | ((type == VAE_BF16 ? 1u : 0u) << 7) | ((type == VAE_BF16 ? 1u : 0u) << 10) |
+           ((trans_b ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Descriptor of an MN-major operand tile as TMA leaves a [rows][64 channels]
+// box with the 128-byte swizzle, read with the rows as the contraction index:
+// 8-row groups 1024 bytes apart (stride offset), the next 64 channels a chunk
+// further (leading offset). Sixteen rows on: 2048 bytes.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kMhaChunkBytes >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// D(tmem) (+)= A(tmem: 16-bit pairs per column, a row per lane) * B(smem desc).
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 2^x, approximate (relative error near 2^-22); under 2^-126 it is 0.
+__device__ __forceinline__ float mha_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Pairs of f32 in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// Zeroes rows [from, 128) of a tile of `chunks` chunks in shared memory; the
+// whole warp. The caller fences towards the async proxy.
+__device__ __forceinline__ void mha_zero_rows(uint8_t* tile, int from, int chunks, int lane) {
+    for (int c = 0; c < chunks; ++c)
+        for (int i = from * 8 + lane; i < kMhaTile * 8; i += 32)
+            *reinterpret_cast<uint4*>(tile + c * kMhaChunkBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
 
 }  // namespace vae

@@ -1,0 +1,651 @@
+// Multi-head attention, forward (the C entry point is in vae_mha.cu).
+//
+// o = softmax(scale q k^T) v in one pass over the keys: S = Q K^T of a 128-row
+// and a 128-key tile accumulates in TMEM, four softmax warps (a row per thread)
+// read it, keep the running maximum m and sum l, and write P = 2^(S - m) back
+// over S as 16-bit pairs; O += P V takes P from TMEM and V as TMA left it
+// (MN-major), so that nothing but Q, K and V passes through shared memory.
+//
+// A CTA runs two such streams, because one stream alone would leave the tensor
+// cores idle while its softmax runs: while the MMA thread issues PV and the
+// next S of one stream, the softmax warps of the other work.
+//   Two query tiles (pair): both streams meet the same key tiles; K and V are
+//   read once for 256 rows.
+//   One query tile (alt, where there are too few tiles to fill the GPU): the
+//   streams take every other key tile and their (m, l, O) join at the end
+//   through shared memory; the keys are further split over CTAs, whose f32
+//   partial rows a second kernel joins in a fixed order.
+//
+// P is held as 2^(S - m + kBias) with m moved only when the new maximum is 2^8
+// over it: at most 2^14, exact scaling, and f16 keeps P down to 2^-20 of the
+// row's largest at full precision. O is scaled when m moves (rare); the S of a
+// stream is issued behind the PV before it, so S having arrived means that O
+// may be touched. Rows and keys of tensors behind their lengths may hold NaN:
+// masked scores are replaced before the maximum, and V's rows are zeroed in
+// shared memory on the one tile that the length ends in.
+#include <cmath>
+
+#include "vae_mha_fwd.h"
+
+namespace vae {
+
+namespace {
+
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr uint32_t kTmemCols = 512;  // S0 | S1 | O0 | O1, 128 columns each
+constexpr int kTargetCtas = 152;     // one CTA per SM
+
+template <int kCh>
+struct FwdCfg {
+    static constexpr int kTileBytes = kCh * kMhaChunkBytes;
+    static constexpr int kStages = kCh == 2 ? 5 : 8;
+    static constexpr int kRing = 2 * kTileBytes;  // behind the two Q tiles
+    static constexpr int kBars = kRing + kStages * kTileBytes;
+    static constexpr int kSmem = 1024 + kBars + 512;
+};
+static_assert(FwdCfg<2>::kSmem <= 232448 && FwdCfg<1>::kSmem <= 232448, "attention shared memory over 227 KB");
+
+struct FwdParams {
+    MhaShape s;
+    int alt, nsplit, bps;  // key tiles per split
+    float scale_log2;
+    void* o;
+    MhaStrides os;
+    float* lse;
+    float *po, *plse;  // partials of the splits: [nsplit][b * hq * sq][d], [nsplit][b * hq * sq] (log2)
+    DevStatus* status;
+    unsigned long long timeout_ns;
+};
+
+struct FwdSmem {
+    uint8_t *q, *ring;
+    uint64_t *full, *empty;             // [kStages]
+    uint64_t *s_full, *p_full, *o_full;  // [2 streams]
+    uint64_t *q_full, *fix, *drain;
+    uint32_t* tmem_slot;
+    int* abort_flag;
+    float* ml;  // [2][128]: (m, l) of the second stream's rows (alt)
+};
+
+template <int kCh>
+__device__ __forceinline__ FwdSmem fwd_carve(uint8_t* raw) {
+    using C = FwdCfg<kCh>;
+    FwdSmem s;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    s.q = base;
+    s.ring = base + C::kRing;
+    uint64_t* b = reinterpret_cast<uint64_t*>(base + C::kBars);
+    s.full = b;
+    s.empty = b + C::kStages;
+    s.s_full = b + 2 * C::kStages;
+    s.p_full = s.s_full + 2;
+    s.o_full = s.p_full + 2;
+    s.q_full = s.o_full + 2;
+    s.fix = s.q_full + 1;
+    s.drain = s.fix + 1;
+    s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
+    s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
+    s.ml = reinterpret_cast<float*>(s.ring + 128 * 128 * 4 / (kCh == 2 ? 1 : 2));  // behind the exchanged O
+    return s;
+}
+
+__device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, const FwdSmem& s, const FwdParams& p) {
+    return mbar_wait(smem_u32(bar), parity, s.abort_flag, p.timeout_ns, p.status, kWhereAttn);
+}
+
+// What a CTA works on; the same values in every thread.
+struct FwdWork {
+    int e, hk, sub;   // batch entry, key head, part of the group
+    int tile[2];      // the streams' 128-row tiles (alt: the same)
+    int split;
+    int ql, kl;
+    int kb0, n;       // key tiles [kb0, kb0 + n)
+    int streams;
+};
+
+__device__ __forceinline__ int tile_limit(const MhaShape& s, int tile, int ql, int kl) {
+    const int i0 = (tile * kMhaTile) >> s.gp_log2;
+    int i1 = ((tile + 1) * kMhaTile - 1) >> s.gp_log2;
+    if (tile >= s.ntile || i0 >= ql) return 0;
+    if (i1 >= ql) i1 = ql - 1;
+    return mha_key_limit(i1, ql, kl, s.block);
+}
+
+__device__ __forceinline__ FwdWork fwd_work(const FwdParams& p) {
+    const MhaShape& s = p.s;
+    FwdWork w;
+    const int nt = p.alt ? s.ntile : (s.ntile + 1) / 2;
+    int r = blockIdx.x;
+    const int t = nt - 1 - r % nt;  // the last tiles see the most keys where blocks limit them: first
+    r /= nt;
+    w.split = r % p.nsplit;
+    r /= p.nsplit;
+    w.sub = r % s.nsub;
+    r /= s.nsub;
+    w.hk = r % s.hkv;
+    w.e = r / s.hkv;
+    w.tile[0] = p.alt ? t : 2 * t;
+    w.tile[1] = p.alt ? t : 2 * t + 1;
+    w.ql = mha_len(s.q_len, w.e, s.sq);
+    w.kl = mha_len(s.k_len, w.e, s.sk);
+    const int l0 = tile_limit(s, w.tile[0], w.ql, w.kl), l1 = p.alt ? 0 : tile_limit(s, w.tile[1], w.ql, w.kl);
+    const int nb = ((l0 > l1 ? l0 : l1) + kMhaTile - 1) / kMhaTile;
+    w.kb0 = w.split * p.bps;
+    const int end = w.kb0 + p.bps < nb ? w.kb0 + p.bps : nb;
+    w.n = end > w.kb0 ? end - w.kb0 : 0;
+    w.streams = p.alt ? (w.n >= 2 ? 2 : 1) : ((w.tile[1] * kMhaTile) >> s.gp_log2) < w.ql && w.tile[1] < s.ntile ? 2 : 1;
+    return w;
+}
+
+template <int kCh>
+__device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork& w, const CUtensorMap* mq,
+                             const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
+    using C = FwdCfg<kCh>;
+    const uint64_t pol = policy_evict_normal();
+    const int gp = 1 << p.s.gp_log2;
+    const int h0 = w.hk * p.s.g + w.sub * gp;
+    const int nq = p.alt ? 1 : w.streams;
+    uint32_t armed = 0, arm_par = 0;
+    if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(s.q_full), static_cast<uint32_t>(nq * C::kTileBytes));
+        for (int t = 0; t < nq; ++t)
+            for (int c = 0; c < kCh; ++c)
+                tma_load_4d(smem_u32(s.q + t * C::kTileBytes + c * kMhaChunkBytes), mq, smem_u32(s.q_full), c * 64, h0,
+                            (w.tile[t] * kMhaTile) >> p.s.gp_log2, w.e, pol);
+    }
+    const int ahead = p.alt ? 2 : 1;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true, fixed = false;
+    // K tiles run `ahead` tiles before V: the order in which the MMA thread takes them
+    auto load = [&](bool is_v, int j) {
+        const int kb = w.kb0 + j;
+        if (!warp_all(fwait(&s.empty[stage], phase ^ 1u, s, p))) return false;
+        // the tile that a length ends in, inside the tensor: rows behind it may hold anything
+        const bool fix = is_v && (kb + 1) * kMhaTile > w.kl && w.kl < p.s.sk;
+        const uint32_t fb = smem_u32(fix ? s.fix : &s.full[stage]);
+        uint8_t* dst = s.ring + stage * C::kTileBytes;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(fb, static_cast<uint32_t>(C::kTileBytes));
+            for (int c = 0; c < kCh; ++c)
+                tma_load_4d(smem_u32(dst + c * kMhaChunkBytes), is_v ? mv : mk, fb, c * 64, w.hk, kb * kMhaTile, w.e, pol);
+        }
+        if (fix) {
+            armed &= ~(1u << stage);  // (its copy completes on the fix barrier)
+            fixed = true;
+            __syncwarp();
+            if (!warp_all(fwait(s.fix, 0u, s, p))) return false;
+            mha_zero_rows(dst, w.kl - kb * kMhaTile, kCh, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.full[stage]));
+        } else {
+            armed |= 1u << stage;
+            arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
+        }
+        if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        return true;
+    };
+    for (int j = 0; ok && j < ahead && j < w.n; ++j) ok = load(false, j);
+    for (int j = 0; ok && j < w.n; ++j) {
+        ok = load(true, j);
+        if (ok && j + ahead < w.n) ok = load(false, j + ahead);
+    }
+    // Every copy lands before the CTA can exit.
+    if (lane == 0) {
+        int never = 0;
+        (void)mbar_wait(smem_u32(s.q_full), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+        if (fixed) (void)mbar_wait(smem_u32(s.fix), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+        for (int i = 0; i < C::kStages; ++i)
+            if (armed & (1u << i))
+                (void)mbar_wait(smem_u32(&s.full[i]), (arm_par >> i) & 1u, &never, p.timeout_ns, p.status, kWhereDrain);
+    }
+    __syncwarp();
+}
+
+template <int T, int kCh>
+__device__ void fwd_mma(const FwdParams& p, const FwdSmem& s, const FwdWork& w, uint32_t tmem) {
+    using C = FwdCfg<kCh>;
+    const int kd = (p.s.d + 15) / 16;  // 16-channel steps of S
+    const uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kd * 16, true);
+    const uint64_t qd = sw128_kmajor_desc(smem_u32(s.q));
+    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(s.ring)), vdesc = sw128_mnmajor_desc(smem_u32(s.ring));
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t pp[2] = {0u, 0u};
+    bool ok = fwait(s.q_full, 0u, s, p);
+    auto next = [&]() {
+        if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    };
+    auto issue_s = [&](int t, int st) {
+        const uint64_t a0 = qd + (p.alt ? 0u : static_cast<uint32_t>(t * C::kTileBytes) >> 4);
+        const uint64_t b0 = kdesc + (static_cast<uint32_t>(st * C::kTileBytes) >> 4);
+#pragma unroll 1
+        for (int k = 0; k < kd; ++k) {
+            const uint32_t off = static_cast<uint32_t>((k >> 2) * (kMhaChunkBytes >> 4) + (k & 3) * 2);
+            umma_f16(tmem + static_cast<uint32_t>(t * 128), a0 + off, b0 + off, id_s, k != 0 ? 1u : 0u);
+        }
+        umma_commit(smem_u32(&s.s_full[t]));
+    };
+    const int ahead = p.alt ? 2 : 1;
+    for (int j = 0; ok && j < ahead && j < w.n; ++j) {
+        ok = fwait(&s.full[stage], phase, s, p);
+        if (!ok) break;
+        tc_fence_after();
+        if (p.alt) {
+            issue_s(j & 1, stage);
+        } else {
+            for (int t = 0; t < w.streams; ++t) issue_s(t, stage);
+        }
+        umma_commit(smem_u32(&s.empty[stage]));
+        next();
+    }
+    for (int j = 0; ok && j < w.n; ++j) {
+        ok = fwait(&s.full[stage], phase, s, p);
+        if (!ok) break;
+        const int vst = stage;
+        next();
+        const bool more = j + ahead < w.n;
+        const int kst = stage;
+        const uint32_t kph = phase;
+        if (more) next();
+        const int t0 = p.alt ? j & 1 : 0, t1 = p.alt ? t0 + 1 : w.streams;
+        for (int t = t0; ok && t < t1; ++t) {
+            ok = fwait(&s.p_full[t], pp[t], s, p);
+            if (!ok) break;
+            pp[t] ^= 1u;
+            tc_fence_after();
+            const uint64_t b0 = vdesc + (static_cast<uint32_t>(vst * C::kTileBytes) >> 4);
+            const uint32_t dO = tmem + 256u + static_cast<uint32_t>(t * 128), aP = tmem + static_cast<uint32_t>(t * 128);
+            const uint32_t first = (p.alt ? j < 2 : j == 0) ? 0u : 1u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                umma_f16_ts(dO, aP + 8u * k, b0 + (2048u >> 4) * k, id_o, k != 0 ? 1u : first);
+            if (t + 1 == t1) umma_commit(smem_u32(&s.empty[vst]));
+            if (more) {
+                if (t == t0) {
+                    ok = fwait(&s.full[kst], kph, s, p);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                issue_s(t, kst);
+                if (t + 1 == t1) umma_commit(smem_u32(&s.empty[kst]));
+            } else {
+                umma_commit(smem_u32(&s.o_full[t]));
+            }
+        }
+    }
+    umma_commit(smem_u32(s.drain));
+    int never = 0;
+    (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+}
+
+// One row's result: `inv` scales O, lse2 is in units of log 2.
+template <int T, int kCh>
+__device__ void fwd_store(const FwdParams& p, const FwdWork& w, uint32_t tO, int i, int h, bool live, float w0,
+                          const float* o1, float w1, float inv, float lse2) {
+    const int d = p.s.d;
+    const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
+    for (int c = 0; c < d; c += 16) {
+        uint32_t r[16];
+        __syncwarp();
+        tmem_ld16(tO + static_cast<uint32_t>(c), r);
+        tmem_ld_wait_regs(r);
+        if (!live) continue;
+#pragma unroll
+        for (int u = 0; u < 16; u += 8) {
+            if (c + u >= d) continue;
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = __uint_as_float(r[u + k]) * w0;
+                if (o1 != nullptr) v[k] += o1[(c + u + k) * 128] * w1;
+                v[k] *= inv;
+            }
+            if (p.nsplit > 1)
+                store8<VAE_F32>(p.po + (static_cast<long long>(w.split) * p.s.b * p.s.hq * p.s.sq + row) * d + c + u, v);
+            else
+                store8<T>(static_cast<typename Elem<T>::type*>(p.o) + w.e * p.os.b + i * p.os.s + h * p.os.h + c + u, v);
+        }
+    }
+    if (!live) return;
+    if (p.nsplit > 1) p.plse[static_cast<long long>(w.split) * p.s.b * p.s.hq * p.s.sq + row] = lse2;
+    else p.lse[row] = lse2 * 0.69314718055994530942f;
+}
+
+template <int T, int kCh>
+__device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork& w, uint32_t tmem, int warp, int lane) {
+    // f16 holds P 2^kBias high (the sum l too): 2^(8 + 6) at most
+    constexpr float kBias = T == VAE_F16 ? 6.f : 0.f;
+    const int t = warp >> 2, quad = warp & 3;
+    const int gp = 1 << p.s.gp_log2;
+    const int r = w.tile[t] * kMhaTile + quad * 32 + lane;
+    const int i = r >> p.s.gp_log2, h = w.hk * p.s.g + w.sub * gp + (r & (gp - 1));
+    const bool live = i < w.ql;
+    const int lim = live ? mha_key_limit(i, w.ql, w.kl, p.s.block) : 0;
+    const int wmin = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);  // (no live row: nothing is computed)
+    const bool any_live = __any_sync(0xffffffffu, live);
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(t * 128), tO = tS + 256u;
+    const int dn = (p.s.d + 15) / 16 * 16;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    const int step = p.alt ? 2 : 1;
+    uint32_t par = 0;
+    const bool runs = t < w.streams;
+    for (int j = p.alt ? t : 0; runs && j < w.n; j += step, par ^= 1u) {
+        ok = warp_all(fwait(&s.s_full[t], par, s, p));
+        if (!ok) break;
+        if (any_live) {
+            tc_fence_after();
+            uint32_t x[8][16];
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) tmem_ld16(tS + static_cast<uint32_t>(c * 16), x[c]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) tmem_ld_wait_regs(x[c]);
+            const int k0 = (w.kb0 + j) * kMhaTile;
+            if (k0 + kMhaTile > wmin) {
+                const int left = lim - k0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (c * 16 + k >= left) x[c][k] = 0xff800000u;  // -infinity
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[c][k]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            if (j < step) {  // the stream's first tile
+                m = top;
+            } else {
+                const bool up = top > m + 8.f;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float alpha = up ? mha_ex2(m - top) : 1.f;
+                    if (up) m = top;
+                    l *= alpha;
+                    for (int c = 0; c < dn; c += 16) {
+                        uint32_t o[16];
+                        __syncwarp();
+                        tmem_ld16(tO + static_cast<uint32_t>(c), o);
+                        tmem_ld_wait_regs(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tmem_st16(tO + static_cast<uint32_t>(c), o);
+                    }
+                }
+            }
+            const float sub = m == -INFINITY ? 0.f : kBias - m;
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), sub2 = make_float2(sub, sub);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+                uint32_t h2[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const uint32_t* y = x[c + (k >> 3)] + 2 * (k & 7);
+                    float2 f = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, sub2);
+                    f.x = mha_ex2(f.x);
+                    f.y = mha_ex2(f.y);
+                    sum[k & 1] = add2(sum[k & 1], f);
+                    h2[k] = pack2<T>(f.x, f.y);
+                }
+                tmem_st16(tS + static_cast<uint32_t>(c * 8), h2);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st_wait();
+            tc_fence_before();
+        }
+        mbar_arrive(smem_u32(&s.p_full[t]));
+    }
+    const bool join = p.alt && w.streams == 2;
+    if (runs && ok) ok = warp_all(fwait(&s.o_full[t], 0u, s, p));
+    if (join) {
+        // the second stream's rows pass through the ring, which every MMA has read by then
+        if (ok && t == 1) ok = warp_all(fwait(&s.o_full[0], 0u, s, p));
+        float* o1 = reinterpret_cast<float*>(s.ring);
+        const int rr = quad * 32 + lane;
+        if (t == 1 && ok && any_live) {
+            tc_fence_after();
+            for (int c = 0; c < dn; c += 16) {
+                uint32_t o[16];
+                __syncwarp();
+                tmem_ld16(tO + static_cast<uint32_t>(c), o);
+                tmem_ld_wait_regs(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o1[(c + k) * 128 + rr] = __uint_as_float(o[k]);
+            }
+            s.ml[rr] = m;
+            s.ml[128 + rr] = l;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // (every softmax warp comes here, timed out or not)
+        if (t == 0 && ok && any_live && *static_cast<volatile int*>(s.abort_flag) == 0) {
+            tc_fence_after();
+            const float m1 = s.ml[rr], l1 = s.ml[128 + rr];
+            const float mm = fmaxf(m, m1);
+            const float w0 = m == -INFINITY ? 0.f : mha_ex2(m - mm), w1 = m1 == -INFINITY ? 0.f : mha_ex2(m1 - mm);
+            const float ll = w0 * l + w1 * l1;
+            fwd_store<T, kCh>(p, w, tO, i, h, live, w0, o1 + rr, w1, mm == -INFINITY ? 0.f : 1.f / ll,
+                              mm == -INFINITY ? -INFINITY : mm - kBias + log2f(ll));
+        }
+    } else if (runs && ok && any_live) {
+        tc_fence_after();
+        const bool none = m == -INFINITY;
+        fwd_store<T, kCh>(p, w, tO, i, h, live, 1.f, nullptr, 0.f, none ? 0.f : 1.f / l,
+                          none ? -INFINITY : m - kBias + log2f(l));
+    }
+}
+
+template <int T, int kCh>
+__global__ void __launch_bounds__(kThreads, 1)
+    mha_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const FwdParams p) {
+    using C = FwdCfg<kCh>;
+    extern __shared__ uint8_t smem_raw[];
+    const FwdSmem s = fwd_carve<kCh>(smem_raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    pdl_wait();
+    const FwdWork w = fwd_work(p);
+    if (w.n == 0) {  // no key: rows within the length give 0 and -infinity
+        const int gp = 1 << p.s.gp_log2;
+        for (int t = 0; t < (p.alt ? 1 : 2); ++t) {
+            const int r = w.tile[t] * kMhaTile + threadIdx.x;
+            const int i = r >> p.s.gp_log2, h = w.hk * p.s.g + w.sub * gp + (r & (gp - 1));
+            if (threadIdx.x >= kMhaTile || w.tile[t] >= p.s.ntile || i >= w.ql) continue;
+            const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
+            if (p.nsplit > 1) {
+                p.plse[static_cast<long long>(w.split) * p.s.b * p.s.hq * p.s.sq + row] = -INFINITY;
+            } else {
+                const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                for (int c = 0; c < p.s.d; c += 8)
+                    store8<T>(static_cast<typename Elem<T>::type*>(p.o) + w.e * p.os.b + i * p.os.s + h * p.os.h + c, z);
+                p.lse[row] = -INFINITY;
+            }
+        }
+        return;
+    }
+    if (threadIdx.x == 0) {
+        *s.abort_flag = 0;
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1u);
+            mbar_init(smem_u32(&s.empty[i]), 1u);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&s.s_full[i]), 1u);
+            mbar_init(smem_u32(&s.p_full[i]), 128u);
+            mbar_init(smem_u32(&s.o_full[i]), 1u);
+        }
+        mbar_init(smem_u32(s.q_full), 1u);
+        mbar_init(smem_u32(s.fix), 1u);
+        mbar_init(smem_u32(s.drain), 1u);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s.tmem_slot;
+    if (warp < kSoftWarps) {
+        fwd_softmax<T, kCh>(p, s, w, tmem, warp, lane);
+    } else if (warp == kTmaWarp) {
+        fwd_producer<kCh>(p, s, w, &mq, &mk, &mv, lane);
+    } else if (lane == 0) {
+        fwd_mma<T, kCh>(p, s, w, tmem);
+    }
+    pdl_launch_dependents();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the splits' partial rows: a warp per row, splits in order.
+template <int T>
+__global__ void __launch_bounds__(128) mha_join_kernel(const FwdParams p) {
+    pdl_wait();
+    const MhaShape& s = p.s;
+    const long long rows = static_cast<long long>(s.b) * s.hq * s.sq;
+    const long long row = static_cast<long long>(blockIdx.x) * 4 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (row >= rows) return;
+    const int i = static_cast<int>(row % s.sq), h = static_cast<int>(row / s.sq % s.hq);
+    const int e = static_cast<int>(row / s.sq / s.hq);
+    if (i >= mha_len(s.q_len, e, s.sq)) return;
+    float mm = -INFINITY;
+    for (int k = lane; k < p.nsplit; k += 32) mm = fmaxf(mm, p.plse[k * rows + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float ll = 0.f;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < p.nsplit; ++k) {
+        const float x = p.plse[k * rows + row];
+        if (x == -INFINITY) continue;
+        const float wt = mha_ex2(x - mm);
+        ll += wt;
+        if (lane * 4 < s.d) {
+            const float4 f = *reinterpret_cast<const float4*>(p.po + (k * rows + row) * s.d + lane * 4);
+            v[0] += f.x * wt;
+            v[1] += f.y * wt;
+            v[2] += f.z * wt;
+            v[3] += f.w * wt;
+        }
+    }
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    if (lane * 4 < s.d) {
+        uint2* dst = reinterpret_cast<uint2*>(static_cast<typename Elem<T>::type*>(p.o) + e * p.os.b + i * p.os.s +
+                                              h * p.os.h + lane * 4);
+        *dst = make_uint2(pack2<T>(v[0] * inv, v[1] * inv), pack2<T>(v[2] * inv, v[3] * inv));
+    }
+    if (lane == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+}
+
+// Pair form where 256-row work items give every SM one; else one tile per CTA
+// with the keys split so that about every SM has work, two key tiles (one per
+// stream) per CTA at least.
+struct FwdPlan {
+    int alt, nsplit, bps;
+    long long items;
+};
+FwdPlan fwd_plan(const MhaShape& s) {
+    FwdPlan f;
+    const long long heads = static_cast<long long>(s.b) * s.hkv * s.nsub;
+    const long long pairs = heads * ((s.ntile + 1) / 2);
+    f.alt = pairs < kTargetCtas;
+    f.nsplit = 1;
+    f.bps = s.nkb;
+    f.items = pairs;
+    if (f.alt) {
+        f.items = heads * s.ntile;
+        const long long want = kTargetCtas / f.items, most = s.nkb / 2;
+        long long n = want < most ? want : most;
+        if (n < 1) n = 1;
+        f.bps = static_cast<int>((s.nkb + n - 1) / n);
+        f.nsplit = (s.nkb + f.bps - 1) / f.bps;
+    }
+    f.items *= f.nsplit;
+    return f;
+}
+
+template <int T, int kCh>
+int fwd_launch(const vae_attention_desc* a, const FwdPlan& f, const CUtensorMap (&map)[3], const FwdParams& p,
+               cudaStream_t st) {
+    static CtxOnce once;
+    static std::mutex mu;
+    using C = FwdCfg<kCh>;
+    {
+        int dev;
+        VAE_CUDA_CHECK(cudaGetDevice(&dev));
+        std::lock_guard<std::mutex> lk(mu);
+        if (!once.done(dev)) {
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_fwd_kernel<T, kCh>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                C::kSmem));
+            once.mark(dev);
+        }
+    }
+    VAE_CUDA_CHECK(launch_kernel(mha_fwd_kernel<T, kCh>, dim3(static_cast<unsigned>(f.items)), dim3(kThreads), C::kSmem,
+                                 st, map[0], map[1], map[2], p));
+    if (f.nsplit > 1) {
+        const long long rows = static_cast<long long>(a->b) * a->hq * a->sq;
+        VAE_CUDA_CHECK(launch_kernel(mha_join_kernel<T>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p));
+    }
+    return VAE_OK;
+}
+
+}  // namespace
+
+size_t mha_fwd_bytes(const MhaShape& s) {
+    const FwdPlan f = fwd_plan(s);
+    if (f.nsplit == 1) return 0;
+    const size_t rows = static_cast<size_t>(s.b) * s.hq * s.sq;
+    return static_cast<size_t>(f.nsplit) * rows * s.d * sizeof(float) + (f.nsplit * rows * sizeof(float) + 15) / 16 * 16;
+}
+
+int mha_fwd_run(const vae_attention_desc* a, const MhaShape& s, const void* q, const void* k, const void* v, void* o,
+                float* lse, void* ws, cudaStream_t st) {
+    const FwdPlan f = fwd_plan(s);
+    if (f.items > 0x7fffffffLL) return set_error(VAE_ERR_SHAPE, "attention: too many tiles");
+    const int gp = 1 << s.gp_log2;
+    CUtensorMap map[3];
+    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, kMhaTile / gp);
+    if (rc == VAE_OK) rc = mha_map(&map[1], a, k, a->k_stride, s.sk, s.hkv, 1, kMhaTile);
+    if (rc == VAE_OK) rc = mha_map(&map[2], a, v, a->v_stride, s.sk, s.hkv, 1, kMhaTile);
+    if (rc != VAE_OK) return rc;
+    FwdParams p{};
+    p.s = s;
+    p.alt = f.alt;
+    p.nsplit = f.nsplit;
+    p.bps = f.bps;
+    p.scale_log2 = a->scale * 1.4426950408889634074f;
+    p.o = o;
+    p.os = mha_strides(a->o_stride);
+    p.lse = lse;
+    p.po = static_cast<float*>(ws);
+    p.plse = p.po + static_cast<size_t>(f.nsplit) * s.b * s.hq * s.sq * s.d;
+    p.status = device_status_ptr();
+    p.timeout_ns = wait_timeout_ns();
+    if (p.status == nullptr) return VAE_ERR_CUDA;
+    if (a->type == VAE_F16)
+        return s.d > 64 ? fwd_launch<VAE_F16, 2>(a, f, map, p, st) : fwd_launch<VAE_F16, 1>(a, f, map, p, st);
+    return s.d > 64 ? fwd_launch<VAE_BF16, 2>(a, f, map, p, st) : fwd_launch<VAE_BF16, 1>(a, f, map, p, st);
+}
+
+}  // namespace vae
