@@ -1,0 +1,1030 @@
+// Gradient of multi-head attention (the C entry point is in vae_mha.cu).
+//
+//   P = 2^(S scale log2(e) - lse log2(e)),  dV = P^T dO,  dP = dO V^T,
+//   D = rowsum(dO * O),  dS = P * (dP - D),  dQ = scale dS K,  dK = scale dS^T Q.
+//
+// Five products over every pair of tiles would do if one kernel could keep dQ,
+// dK and dV at once; dQ's sum runs over the key tiles that other CTAs hold, so
+// that form adds dQ with atomics, whose order changes the result. Here two
+// kernels run over the pairs, one per key tile (S^T, dP^T, dV, dK: four
+// products) and one per query tile (S, dP, dQ: three): seven products, P twice,
+// no atomics on results and nothing of the pairs' size in memory.
+//
+// Key-tile kernel: lanes of TMEM are keys, columns are query rows. S^T = K Q^T
+// and dP^T = V dO^T come from shared memory, eight softmax warps turn them into
+// P^T and dS^T over the same TMEM columns, and these are the left operands of
+// dV += P^T dO and dK += dS^T Q, for which the Q and dO tiles that TMA brought
+// are read again with the rows as the contraction index. While the warps form
+// dS^T, the tensor cores run dV and the next S^T; while they form the next
+// P^T, dK and the next dP^T.
+// Query-tile kernel: the same with lanes as query rows; P stays in registers.
+//
+// 16 bits. P and dS are rounded to the tensors' type for the products, half a
+// step of 2^-8 or 2^-11 relative, as the forward's P. f16 would lose long rows'
+// P ~ 1/n below 2^-14, so it holds P 2^14 and dS c, with c the power of two
+// that brings 2 max|dO| max|V| (a bound on |dP - D| by Cauchy-Schwarz, from a
+// first kernel) to 2^14 .. 2^15; both factors leave in the epilogue. The
+// maximum is taken by an atomic maximum, which has no order.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "vae_mha_bwd.h"
+
+namespace vae {
+
+namespace {
+
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kTargetCtas = 152;   // one CTA per SM
+constexpr int kPLog2 = 14;         // f16: P is held as P 2^14
+constexpr int kSideFloats = 256;   // of a row tile: 128 x (kPLog2 - lse log2(e)), 128 x D
+constexpr int kSideBytes = kSideFloats * 4;
+
+template <int kCh>
+struct BwdCfg {
+    static constexpr int kTileBytes = kCh * kMhaChunkBytes;
+    static constexpr int kStages = kCh == 2 ? 2 : 4;
+    static constexpr int kRing = 2 * kTileBytes;  // behind the two resident tiles
+    static constexpr int kSide = kRing + kStages * 2 * kTileBytes;
+    static constexpr int kBars = kSide + kStages * kSideBytes;
+    static constexpr int kSmem = 1024 + kBars + 512;
+};
+static_assert(BwdCfg<2>::kSmem <= 232448 && BwdCfg<1>::kSmem <= 232448, "attention shared memory over 227 KB");
+
+struct BwdParams {
+    MhaShape s;
+    float scale, scale_log2;
+    int nsplit_q, nsplit_k;
+    const float* side;          // [b][hkv][nsub][ntile][256]
+    const unsigned* maxima;     // f16: bits of max |dO|^2, max |V|^2
+    void *dq, *dk, *dv;
+    MhaStrides dqs, dks, dvs;
+    float *part_q, *part_kv;    // [nsplit_q][b][hq][sq][d], [nsplit_k][2][b][hkv][sk][d]
+    DevStatus* status;
+    unsigned long long timeout_ns;
+};
+
+// c of the file comment.
+template <int T>
+__device__ __forceinline__ float ds_factor(const unsigned* maxima) {
+    if constexpr (T == VAE_BF16) {
+        return 1.f;
+    } else {
+        const float bound = 2.f * sqrtf(__uint_as_float(maxima[0])) * sqrtf(__uint_as_float(maxima[1]));
+        if (!(bound > 0.f) || bound > 1e30f) return 1.f;
+        const int k = 14 - ilogbf(bound);
+        return scalbnf(1.f, k < -100 ? -100 : (k > 100 ? 100 : k));
+    }
+}
+
+// ───────────────────────────── rows beforehand ─────────────────────────────
+
+struct PrepParams {
+    MhaShape s;
+    const void *dout, *o, *v;
+    MhaStrides gs, os, vs;
+    const float* lse;
+    float* side;
+    unsigned* maxima;
+    int row_tiles;  // of all heads; the key tiles' blocks (f16) follow
+};
+
+// A block per row tile: 16 lanes a row. Then (f16) a block per key tile for max |V|.
+template <int T>
+__global__ void __launch_bounds__(256) mha_prep_kernel(const PrepParams p) {
+    pdl_wait();
+    const MhaShape& s = p.s;
+    const int part = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    float big = 0.f;
+    unsigned* maximum = p.maxima;
+    if (static_cast<int>(blockIdx.x) < p.row_tiles) {
+        int x = blockIdx.x;
+        const int tile = x % s.ntile;
+        x /= s.ntile;
+        const int sub = x % s.nsub;
+        x /= s.nsub;
+        const int hk = x % s.hkv, e = x / s.hkv;
+        const int ql = mha_len(s.q_len, e, s.sq);
+        const int gp = 1 << s.gp_log2;
+        float* side = p.side + static_cast<long long>(blockIdx.x) * kSideFloats;
+#pragma unroll 2
+        for (int k = 0; k < kMhaTile / 16; ++k) {
+            const int rr = r0 + k * 16, r = tile * kMhaTile + rr;
+            const int i = r >> s.gp_log2, h = hk * s.g + sub * gp + (r & (gp - 1));
+            const bool live = i < ql;
+            float d = 0.f, n = 0.f;
+            if (live && part * 8 < s.d) {
+                float a[8], b[8];
+                load8<T>(static_cast<const typename Elem<T>::type*>(p.dout) + e * p.gs.b + i * p.gs.s + h * p.gs.h + part * 8, a);
+                load8<T>(static_cast<const typename Elem<T>::type*>(p.o) + e * p.os.b + i * p.os.s + h * p.os.h + part * 8, b);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    d += a[u] * b[u];
+                    n += a[u] * a[u];
+                }
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) {
+                d += __shfl_xor_sync(0xffffffffu, d, w);
+                n += __shfl_xor_sync(0xffffffffu, n, w);
+            }
+            big = fmaxf(big, n);
+            if (part == 0) {
+                const float l = live ? p.lse[(static_cast<long long>(e) * s.hq + h) * s.sq + i] : -INFINITY;
+                side[rr] = l == -INFINITY ? -INFINITY : (T == VAE_F16 ? kPLog2 : 0) - l * 1.4426950408889634074f;
+                side[128 + rr] = live ? d : 0.f;
+            }
+        }
+    } else {
+        int x = blockIdx.x - p.row_tiles;
+        const int kb = x % s.nkb;
+        x /= s.nkb;
+        const int hk = x % s.hkv, e = x / s.hkv;
+        const int kl = mha_len(s.k_len, e, s.sk);
+        maximum = p.maxima + 1;
+#pragma unroll 4
+        for (int k = 0; k < kMhaTile / 16; ++k) {
+            const int j = kb * kMhaTile + r0 + k * 16;
+            float n = 0.f;
+            if (j < kl && part * 8 < s.d) {
+                float a[8];
+                load8<T>(static_cast<const typename Elem<T>::type*>(p.v) + e * p.vs.b + j * p.vs.s + hk * p.vs.h + part * 8, a);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) n += a[u] * a[u];
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
+            big = fmaxf(big, n);
+        }
+    }
+    if constexpr (T == VAE_F16) {
+        // (values >= 0: their bits order as unsigned numbers do)
+        const unsigned b = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+        if ((threadIdx.x & 31) == 0 && b != 0u) atomicMax(maximum, b);
+    }
+}
+
+// ───────────────────────────── shared structure ─────────────────────────────
+
+struct BwdSmem {
+    uint8_t *res, *ring, *side;
+    uint64_t *a_full, *b_full, *empty;  // [kStages]: first tile (+ side), second tile, both free
+    uint64_t *res_full, *s_full, *x_full, *p_full, *ds_full, *done, *fix, *drain;
+    uint32_t* tmem_slot;
+    int* abort_flag;
+};
+
+template <int kCh>
+__device__ __forceinline__ BwdSmem bwd_carve(uint8_t* raw) {
+    using C = BwdCfg<kCh>;
+    BwdSmem s;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    s.res = base;
+    s.ring = base + C::kRing;
+    s.side = base + C::kSide;
+    uint64_t* b = reinterpret_cast<uint64_t*>(base + C::kBars);
+    s.a_full = b;
+    s.b_full = b + C::kStages;
+    s.empty = b + 2 * C::kStages;
+    b += 3 * C::kStages;
+    s.res_full = b;
+    s.s_full = b + 1;
+    s.x_full = b + 2;  // dP has been formed
+    s.p_full = b + 3;  // key-tile kernel: P^T is in TMEM; query-tile kernel: S has been read
+    s.ds_full = b + 4;
+    s.done = b + 5;
+    s.fix = b + 6;
+    s.drain = b + 7;
+    s.tmem_slot = reinterpret_cast<uint32_t*>(b + 8);
+    s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
+    return s;
+}
+
+__device__ __forceinline__ bool bwait(uint64_t* bar, uint32_t parity, const BwdSmem& s, const BwdParams& p) {
+    return mbar_wait(smem_u32(bar), parity, s.abort_flag, p.timeout_ns, p.status, kWhereAttn);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+template <int kCh>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int head, int token, int e,
+                                          uint64_t pol) {
+    for (int c = 0; c < kCh; ++c)
+        tma_load_4d(smem_u32(dst + c * kMhaChunkBytes), map, bar, c * 64, head, token, e, pol);
+}
+
+// Set-up and tear-down common to both kernels.
+template <int kCh>
+__device__ __forceinline__ uint32_t bwd_begin(const BwdSmem& s, int warp) {
+    using C = BwdCfg<kCh>;
+    if (threadIdx.x == 0) {
+        *s.abort_flag = 0;
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_u32(&s.a_full[i]), 1u);
+            mbar_init(smem_u32(&s.b_full[i]), 1u);
+            mbar_init(smem_u32(&s.empty[i]), 1u);
+        }
+        mbar_init(smem_u32(s.res_full), 1u);
+        mbar_init(smem_u32(s.s_full), 1u);
+        mbar_init(smem_u32(s.x_full), 1u);
+        mbar_init(smem_u32(s.p_full), kSoftWarps * 32u);
+        mbar_init(smem_u32(s.ds_full), kSoftWarps * 32u);
+        mbar_init(smem_u32(s.done), 1u);
+        mbar_init(smem_u32(s.fix), 1u);
+        mbar_init(smem_u32(s.drain), 1u);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return *s.tmem_slot;
+}
+__device__ __forceinline__ void bwd_end(uint32_t tmem, int warp) {
+    pdl_launch_dependents();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// The ring's producer state: what is in flight when a wait runs out has to
+// land before the CTA may exit.
+template <int kN>
+struct BwdRing {
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, arm_par = 0, fixes = 0;
+    __device__ __forceinline__ void arm() {
+        armed |= 1u << stage;
+        arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
+    }
+    __device__ __forceinline__ void next() {
+        if (++stage == kN) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void drain(const BwdSmem& s, const BwdParams& p) const {
+        int never = 0;
+        (void)mbar_wait(smem_u32(s.res_full), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+        if (fixes > 0)
+            (void)mbar_wait(smem_u32(s.fix), (fixes - 1u) & 1u, &never, p.timeout_ns, p.status, kWhereDrain);
+        for (int i = 0; i < kN; ++i)
+            if (armed & (1u << i)) {
+                (void)mbar_wait(smem_u32(&s.a_full[i]), (arm_par >> i) & 1u, &never, p.timeout_ns, p.status, kWhereDrain);
+                (void)mbar_wait(smem_u32(&s.b_full[i]), (arm_par >> i) & 1u, &never, p.timeout_ns, p.status, kWhereDrain);
+            }
+    }
+};
+
+// One product D (+)= A B^T of two K-major tiles in shared memory, 128 x 128.
+// (The loop stays a loop: unrolled with a test per step, the predicated MMAs
+// were seen to take wrong operands.)
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, int steps) {
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t off = static_cast<uint32_t>((k >> 2) * (kMhaChunkBytes >> 4) + (k & 3) * 2);
+        umma_f16(d_tmem, a + off, b + off, id, k != 0 ? 1u : 0u);
+    }
+}
+// D += A B with A in TMEM: its columns in two halves of 64, 32 used of each.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        umma_f16_ts(d_tmem, a_tmem + static_cast<uint32_t>((k >> 2) * 64 + (k & 3) * 8), b + (2048u >> 4) * k, id,
+                    k != 0 ? 1u : acc);
+}
+
+__device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p) {
+    umma_commit(smem_u32(s.drain));
+    int never = 0;
+    (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+}
+
+// 64 columns of this warp's lanes.
+__device__ __forceinline__ void load64(uint32_t t, uint32_t (&x)[4][16]) {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld16(t + static_cast<uint32_t>(c * 16), x[c]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld_wait_regs(x[c]);
+}
+
+// A row of an accumulator, times `f`, to the 16-bit tensor or an f32 partial.
+template <int T>
+__device__ __forceinline__ void store_acc(uint32_t t, int d, bool live, bool any, float f, void* out, long long off, float* part,
+                                          long long poff) {
+    for (int c = 0; c < d; c += 16) {
+        uint32_t r[16];
+        if (any) {
+            __syncwarp();
+            tmem_ld16(t + static_cast<uint32_t>(c), r);
+            tmem_ld_wait_regs(r);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) r[k] = 0u;  // no pair was met
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int u = 0; u < 16; u += 8) {
+            if (c + u >= d) continue;
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[u + k]) * f;
+            if (part != nullptr) store8<VAE_F32>(part + poff + c + u, v);
+            else store8<T>(static_cast<typename Elem<T>::type*>(out) + off + c + u, v);
+        }
+    }
+}
+
+// ───────────────────────────── dK and dV, per key tile ─────────────────────────────
+
+struct KvWork {
+    int e, hk, kb, split;
+    int ql, kl;
+    int t0, nt;      // row tiles [t0, nt) of each part of the group see this key tile
+    int first, n;    // this split's share of the nsub * (nt - t0) tiles
+};
+
+__device__ __forceinline__ KvWork kv_work(const BwdParams& p) {
+    const MhaShape& s = p.s;
+    KvWork w;
+    int r = blockIdx.x;
+    w.kb = r % s.nkb;
+    r /= s.nkb;
+    w.split = r % p.nsplit_k;
+    r /= p.nsplit_k;
+    w.hk = r % s.hkv;
+    w.e = r / s.hkv;
+    w.ql = mha_len(s.q_len, w.e, s.sq);
+    w.kl = mha_len(s.k_len, w.e, s.sk);
+    const long long rows = static_cast<long long>(w.ql) << s.gp_log2;
+    w.nt = static_cast<int>((rows + kMhaTile - 1) / kMhaTile);
+    int i0 = 0;  // the first query that sees a key of the tile
+    if (s.block > 0) {
+        i0 = w.kb * kMhaTile / s.block * s.block - (w.kl - w.ql);
+        if (i0 < 0) i0 = 0;
+    }
+    const long long t0 = (static_cast<long long>(i0) << s.gp_log2) / kMhaTile;
+    w.t0 = t0 < w.nt ? static_cast<int>(t0) : w.nt;
+    const int all = w.kb * kMhaTile < w.kl ? s.nsub * (w.nt - w.t0) : 0;
+    const int per = (all + p.nsplit_k - 1) / p.nsplit_k;
+    w.first = w.split * per < all ? w.split * per : all;
+    w.n = (w.first + per < all ? w.first + per : all) - w.first;
+    return w;
+}
+
+template <int kCh>
+__device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& w, const CUtensorMap* mq,
+                            const CUtensorMap* mg, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
+    using C = BwdCfg<kCh>;
+    const uint64_t pol = policy_evict_normal();
+    const MhaShape& sh = p.s;
+    const int gp = 1 << sh.gp_log2;
+    if (lane == 0) {
+        const uint32_t rb = smem_u32(s.res_full);
+        mbar_arrive_expect_tx(rb, 2u * C::kTileBytes);
+        load_tile<kCh>(s.res, mk, rb, w.hk, w.kb * kMhaTile, w.e, pol);
+        load_tile<kCh>(s.res + C::kTileBytes, mv, rb, w.hk, w.kb * kMhaTile, w.e, pol);
+    }
+    BwdRing<C::kStages> r;
+    const int per = w.nt - w.t0;
+    for (int x = 0; x < w.n; ++x) {
+        const int sub = (w.first + x) / per, tile = w.t0 + (w.first + x) % per;
+        const int head = w.hk * sh.g + sub * gp, token = (tile * kMhaTile) >> sh.gp_log2;
+        if (!warp_all(bwait(&s.empty[r.stage], r.phase ^ 1u, s, p))) break;
+        uint8_t* dst = s.ring + r.stage * 2 * C::kTileBytes;
+        uint8_t* sd = s.side + r.stage * kSideBytes;
+        const float* src = p.side + (((static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.nsub + sub) * sh.ntile + tile) * kSideFloats;
+        // rows behind the length, inside the tensor, may hold anything: zeroed before the MMAs may read
+        const long long valid = (static_cast<long long>(w.ql) << sh.gp_log2) - static_cast<long long>(tile) * kMhaTile;
+        const bool fix = valid < kMhaTile && w.ql < sh.sq;
+        const uint32_t ab = smem_u32(fix ? s.fix : &s.a_full[r.stage]), bb = smem_u32(fix ? s.fix : &s.b_full[r.stage]);
+        if (lane == 0) {
+            if (fix) {
+                mbar_arrive_expect_tx(ab, 2u * C::kTileBytes + kSideBytes);
+            } else {
+                mbar_arrive_expect_tx(ab, C::kTileBytes + kSideBytes);
+                mbar_arrive_expect_tx(bb, C::kTileBytes);
+            }
+            load_tile<kCh>(dst, mq, ab, head, token, w.e, pol);
+            bulk_load(smem_u32(sd), src, kSideBytes, ab);
+            load_tile<kCh>(dst + C::kTileBytes, mg, bb, head, token, w.e, pol);
+        }
+        if (fix) {
+            r.armed &= ~(1u << r.stage);  // (its copies complete on the fix barrier)
+            const uint32_t par = r.fixes & 1u;
+            ++r.fixes;
+            __syncwarp();
+            if (!warp_all(bwait(s.fix, par, s, p))) break;
+            mha_zero_rows(dst, static_cast<int>(valid), kCh, lane);
+            mha_zero_rows(dst + C::kTileBytes, static_cast<int>(valid), kCh, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&s.a_full[r.stage]));
+                mbar_arrive(smem_u32(&s.b_full[r.stage]));
+            }
+        } else {
+            r.arm();
+        }
+        r.next();
+    }
+    if (lane == 0) r.drain(s, p);
+    __syncwarp();
+}
+
+template <int T, int kCh>
+__device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w, uint32_t tmem) {
+    using C = BwdCfg<kCh>;
+    const int kd = (p.s.d + 15) / 16;
+    const uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kd * 16, true);
+    const uint32_t tS = tmem, tX = tmem + 128u, tV = tmem + 256u, tK = tmem + 384u;
+    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(s.res)), vdesc = kdesc + (C::kTileBytes >> 4);
+    const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
+    const uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
+    bool ok = bwait(s.res_full, 0u, s, p);
+    auto score = [&](int st, uint32_t ph) {
+        if (!bwait(&s.a_full[st], ph, s, p)) return false;
+        tc_fence_after();
+        mma_ss(tS, kdesc, ring_k + st * stage_units, id_s, kd);
+        umma_commit(smem_u32(s.s_full));
+        return true;
+    };
+    auto cross = [&](int st, uint32_t ph) {
+        if (!bwait(&s.b_full[st], ph, s, p)) return false;
+        tc_fence_after();
+        mma_ss(tX, vdesc, ring_k + st * stage_units + second, id_s, kd);
+        umma_commit(smem_u32(s.x_full));
+        return true;
+    };
+    int st = 0;
+    uint32_t ph = 0;
+    ok = ok && score(0, 0u) && cross(0, 0u);
+    for (int x = 0; ok && x < w.n; ++x) {
+        const uint32_t par = static_cast<uint32_t>(x) & 1u;
+        int st1 = st + 1;
+        uint32_t ph1 = ph;
+        if (st1 == C::kStages) {
+            st1 = 0;
+            ph1 ^= 1u;
+        }
+        ok = bwait(s.p_full, par, s, p);
+        if (!ok) break;
+        tc_fence_after();
+        mma_ts(tV, tS, ring_m + st * stage_units + second, id_o, x != 0 ? 1u : 0u);
+        if (x + 1 < w.n && !(ok = score(st1, ph1))) break;
+        ok = bwait(s.ds_full, par, s, p);
+        if (!ok) break;
+        tc_fence_after();
+        mma_ts(tK, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
+        umma_commit(smem_u32(&s.empty[st]));
+        if (x + 1 < w.n && !(ok = cross(st1, ph1))) break;
+        st = st1;
+        ph = ph1;
+    }
+    if (ok) umma_commit(smem_u32(s.done));
+    mma_finish(s, p);
+}
+
+template <int T, int kCh>
+__device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w, uint32_t tmem, int warp, int lane) {
+    using C = BwdCfg<kCh>;
+    const int quad = warp & 3, half = warp >> 2;
+    const MhaShape& sh = p.s;
+    const int j = w.kb * kMhaTile + quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
+    const float c = ds_factor<T>(p.maxima);
+    const float f = T == VAE_F16 ? c * (1.f / (1 << kPLog2)) : 1.f;  // dS c = (P 2^14) (dP - D) f
+    // the first row of the group's packing that sees key j
+    long long see = 0;
+    if (sh.block > 0) see = static_cast<long long>(j / sh.block * sh.block - (w.kl - w.ql)) * (1 << sh.gp_log2);
+    const int per = w.nt - w.t0;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    bool ok = true;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int x = 0; x < w.n; ++x) {
+        const uint32_t par = static_cast<uint32_t>(x) & 1u;
+        const int tile = w.t0 + (w.first + x) % per;
+        ok = warp_all(bwait(&s.a_full[st], ph, s, p));  // the side rows
+        if (!ok) break;
+        const float* side = reinterpret_cast<const float*>(s.side + st * kSideBytes) + half * 64;
+        ok = warp_all(bwait(s.s_full, par, s, p));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t xr[4][16];
+        float pr[64];
+        load64(tS, xr);
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+            const float4 nl = *reinterpret_cast<const float4*>(side + k);
+            const uint32_t* y = xr[k >> 4] + (k & 15);
+            const float2 a = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, make_float2(nl.x, nl.y));
+            const float2 b = fma2(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), sc2, make_float2(nl.z, nl.w));
+            pr[k] = mha_ex2(a.x);
+            pr[k + 1] = mha_ex2(a.y);
+            pr[k + 2] = mha_ex2(b.x);
+            pr[k + 3] = mha_ex2(b.y);
+        }
+        const long long before = see - static_cast<long long>(tile) * kMhaTile - half * 64;
+        const int hide = before > 64 ? 64 : (before < 0 ? 0 : static_cast<int>(before));  // columns that do not see the key
+        if (__any_sync(0xffffffffu, hide > 0)) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                if (k < hide) pr[k] = 0.f;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t h2[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) h2[u] = pack2<T>(pr[k * 32 + 2 * u], pr[k * 32 + 2 * u + 1]);
+            tmem_st16(tS + static_cast<uint32_t>(k * 16), h2);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(s.p_full));
+        ok = warp_all(bwait(s.x_full, par, s, p));
+        if (!ok) break;
+        tc_fence_after();
+        load64(tX, xr);
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+            const float4 D = *reinterpret_cast<const float4*>(side + 128 + k);
+            uint32_t* y = xr[k >> 4] + (k & 15);
+            float2 a = add2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), make_float2(-D.x, -D.y));
+            float2 b = add2(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), make_float2(-D.z, -D.w));
+            a = mul2(a, make_float2(pr[k], pr[k + 1]));
+            b = mul2(b, make_float2(pr[k + 2], pr[k + 3]));
+            if constexpr (T == VAE_F16) {
+                a = mul2(a, make_float2(f, f));
+                b = mul2(b, make_float2(f, f));
+            }
+            pr[k] = a.x;
+            pr[k + 1] = a.y;
+            pr[k + 2] = b.x;
+            pr[k + 3] = b.y;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t h2[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) h2[u] = pack2<T>(pr[k * 32 + 2 * u], pr[k * 32 + 2 * u + 1]);
+            tmem_st16(tX + static_cast<uint32_t>(k * 16), h2);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(s.ds_full));
+        if (++st == C::kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+    if (ok) ok = warp_all(bwait(s.done, 0u, s, p));
+    if (!ok) return;
+    tc_fence_after();
+    // dV by the first four warps, dK by the others
+    const long long rows = static_cast<long long>(sh.b) * sh.hkv * sh.sk;
+    const long long row = (static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.sk + j;
+    const bool split = p.nsplit_k > 1;
+    const MhaStrides os = half == 0 ? p.dvs : p.dks;
+    const float g = half == 0 ? (T == VAE_F16 ? 1.f / (1 << kPLog2) : 1.f) : p.scale / c;
+    store_acc<T>(tmem + lane_off + 256u + static_cast<uint32_t>(half * 128), sh.d, j < w.kl, true, g,
+                 half == 0 ? p.dv : p.dk, w.e * os.b + j * os.s + w.hk * os.h, split ? p.part_kv : nullptr,
+                 ((w.split * 2 + half) * rows + row) * sh.d);
+}
+
+template <int T, int kCh>
+__global__ void __launch_bounds__(kThreads, 1)
+    mha_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
+                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const BwdSmem s = bwd_carve<kCh>(smem_raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    pdl_wait();
+    const KvWork w = kv_work(p);
+    if (w.n == 0) {  // no query: zeros within the length
+        const int j = w.kb * kMhaTile + (threadIdx.x & 127);
+        if (threadIdx.x < 2 * kMhaTile && j < w.kl) {
+            const int half = threadIdx.x / kMhaTile;
+            const long long rows = static_cast<long long>(p.s.b) * p.s.hkv * p.s.sk;
+            const long long row = (static_cast<long long>(w.e) * p.s.hkv + w.hk) * p.s.sk + j;
+            const MhaStrides os = half == 0 ? p.dvs : p.dks;
+            store_acc<T>(0u, p.s.d, true, false, 0.f, half == 0 ? p.dv : p.dk, w.e * os.b + j * os.s + w.hk * os.h,
+                         p.nsplit_k > 1 ? p.part_kv : nullptr, ((w.split * 2 + half) * rows + row) * p.s.d);
+        }
+        return;
+    }
+    const uint32_t tmem = bwd_begin<kCh>(s, warp);
+    if (warp < kSoftWarps) kv_softmax<T, kCh>(p, s, w, tmem, warp, lane);
+    else if (warp == kTmaWarp) kv_producer<kCh>(p, s, w, &mq, &mg, &mk, &mv, lane);
+    else if (lane == 0) kv_mma<T, kCh>(p, s, w, tmem);
+    bwd_end(tmem, warp);
+}
+
+// ───────────────────────────── dQ, per row tile ─────────────────────────────
+
+struct QWork {
+    int e, hk, sub, tile, split;
+    int ql, kl;
+    int kb0, n;  // this split's key tiles
+};
+
+__device__ __forceinline__ QWork q_work(const BwdParams& p) {
+    const MhaShape& s = p.s;
+    QWork w;
+    int r = blockIdx.x;
+    w.tile = s.ntile - 1 - r % s.ntile;  // the tiles that see the most keys first
+    r /= s.ntile;
+    w.split = r % p.nsplit_q;
+    r /= p.nsplit_q;
+    w.sub = r % s.nsub;
+    r /= s.nsub;
+    w.hk = r % s.hkv;
+    w.e = r / s.hkv;
+    w.ql = mha_len(s.q_len, w.e, s.sq);
+    w.kl = mha_len(s.k_len, w.e, s.sk);
+    const int i0 = (w.tile * kMhaTile) >> s.gp_log2;
+    int i1 = ((w.tile + 1) * kMhaTile - 1) >> s.gp_log2;
+    if (i1 >= w.ql) i1 = w.ql - 1;
+    const int lim = i0 < w.ql ? mha_key_limit(i1, w.ql, w.kl, s.block) : 0;
+    const int all = (lim + kMhaTile - 1) / kMhaTile;
+    const int per = (all + p.nsplit_q - 1) / p.nsplit_q;
+    w.kb0 = w.split * per < all ? w.split * per : all;
+    w.n = (w.kb0 + per < all ? w.kb0 + per : all) - w.kb0;
+    return w;
+}
+
+template <int kCh>
+__device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w, const CUtensorMap* mq,
+                           const CUtensorMap* mg, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
+    using C = BwdCfg<kCh>;
+    const uint64_t pol = policy_evict_normal();
+    const MhaShape& sh = p.s;
+    if (lane == 0) {
+        const uint32_t rb = smem_u32(s.res_full);
+        const int head = w.hk * sh.g + (w.sub << sh.gp_log2), token = (w.tile * kMhaTile) >> sh.gp_log2;
+        mbar_arrive_expect_tx(rb, 2u * C::kTileBytes);
+        load_tile<kCh>(s.res, mq, rb, head, token, w.e, pol);
+        load_tile<kCh>(s.res + C::kTileBytes, mg, rb, head, token, w.e, pol);
+    }
+    BwdRing<C::kStages> r;
+    for (int x = 0; x < w.n; ++x) {
+        const int kb = w.kb0 + x;
+        if (!warp_all(bwait(&s.empty[r.stage], r.phase ^ 1u, s, p))) break;
+        uint8_t* dst = s.ring + r.stage * 2 * C::kTileBytes;
+        const bool fix = (kb + 1) * kMhaTile > w.kl && w.kl < sh.sk;  // the tile that the length ends in: the last
+        const uint32_t ab = smem_u32(fix ? s.fix : &s.a_full[r.stage]), bb = smem_u32(fix ? s.fix : &s.b_full[r.stage]);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(ab, (fix ? 2u : 1u) * C::kTileBytes);
+            if (!fix) mbar_arrive_expect_tx(bb, C::kTileBytes);
+            load_tile<kCh>(dst, mk, ab, w.hk, kb * kMhaTile, w.e, pol);
+            load_tile<kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, w.e, pol);
+        }
+        if (fix) {
+            r.armed &= ~(1u << r.stage);
+            const uint32_t par = r.fixes & 1u;
+            ++r.fixes;
+            __syncwarp();
+            if (!warp_all(bwait(s.fix, par, s, p))) break;
+            mha_zero_rows(dst, w.kl - kb * kMhaTile, kCh, lane);
+            mha_zero_rows(dst + C::kTileBytes, w.kl - kb * kMhaTile, kCh, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&s.a_full[r.stage]));
+                mbar_arrive(smem_u32(&s.b_full[r.stage]));
+            }
+        } else {
+            r.arm();
+        }
+        r.next();
+    }
+    if (lane == 0) r.drain(s, p);
+    __syncwarp();
+}
+
+template <int T, int kCh>
+__device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w, uint32_t tmem) {
+    using C = BwdCfg<kCh>;
+    const int kd = (p.s.d + 15) / 16;
+    const uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kd * 16, true);
+    const uint32_t tS = tmem, tX = tmem + 128u, tQ = tmem + 256u;
+    const uint64_t qdesc = sw128_kmajor_desc(smem_u32(s.res)), gdesc = qdesc + (C::kTileBytes >> 4);
+    const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
+    const uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
+    bool ok = bwait(s.res_full, 0u, s, p);
+    auto score = [&](int st, uint32_t ph) {
+        if (!bwait(&s.a_full[st], ph, s, p)) return false;
+        tc_fence_after();
+        mma_ss(tS, qdesc, ring_k + st * stage_units, id_s, kd);
+        umma_commit(smem_u32(s.s_full));
+        return true;
+    };
+    auto cross = [&](int st, uint32_t ph) {
+        if (!bwait(&s.b_full[st], ph, s, p)) return false;
+        tc_fence_after();
+        mma_ss(tX, gdesc, ring_k + st * stage_units + second, id_s, kd);
+        umma_commit(smem_u32(s.x_full));
+        return true;
+    };
+    int st = 0;
+    uint32_t ph = 0;
+    ok = ok && score(0, 0u) && cross(0, 0u);
+    for (int x = 0; ok && x < w.n; ++x) {
+        const uint32_t par = static_cast<uint32_t>(x) & 1u;
+        int st1 = st + 1;
+        uint32_t ph1 = ph;
+        if (st1 == C::kStages) {
+            st1 = 0;
+            ph1 ^= 1u;
+        }
+        if (x + 1 < w.n) {
+            ok = bwait(s.p_full, par, s, p);  // S has been read
+            if (!ok) break;
+            tc_fence_after();
+            if (!(ok = score(st1, ph1))) break;
+        }
+        ok = bwait(s.ds_full, par, s, p);
+        if (!ok) break;
+        tc_fence_after();
+        mma_ts(tQ, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
+        umma_commit(smem_u32(&s.empty[st]));
+        if (x + 1 < w.n && !(ok = cross(st1, ph1))) break;
+        st = st1;
+        ph = ph1;
+    }
+    if (ok) umma_commit(smem_u32(s.done));
+    mma_finish(s, p);
+}
+
+template <int T, int kCh>
+__device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, uint32_t tmem, int warp, int lane) {
+    const int quad = warp & 3, half = warp >> 2;
+    const MhaShape& sh = p.s;
+    const int gp = 1 << sh.gp_log2;
+    const int rr = quad * 32 + lane, r = w.tile * kMhaTile + rr;
+    const int i = r >> sh.gp_log2, h = w.hk * sh.g + w.sub * gp + (r & (gp - 1));
+    const bool live = i < w.ql;
+    const int lim = live ? mha_key_limit(i, w.ql, w.kl, sh.block) : 0;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
+    const float* side = p.side + (((static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.nsub + w.sub) * sh.ntile + w.tile) * kSideFloats;
+    const float nl = side[rr], D = side[128 + rr];
+    const float c = ds_factor<T>(p.maxima);
+    const float f = T == VAE_F16 ? c * (1.f / (1 << kPLog2)) : 1.f;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl), D2 = make_float2(-D, -D);
+    bool ok = true;
+    for (int x = 0; x < w.n; ++x) {
+        const uint32_t par = static_cast<uint32_t>(x) & 1u;
+        ok = warp_all(bwait(s.s_full, par, s, p));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t xr[4][16];
+        float pr[64];
+        load64(tS, xr);
+        tc_fence_before();
+        mbar_arrive(smem_u32(s.p_full));
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+            const uint32_t* y = xr[k >> 4] + (k & 15);
+            const float2 a = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, nl2);
+            pr[k] = mha_ex2(a.x);
+            pr[k + 1] = mha_ex2(a.y);
+        }
+        const int left = lim - (w.kb0 + x) * kMhaTile - half * 64;
+        if (__any_sync(0xffffffffu, left < 64)) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                if (k >= left) pr[k] = 0.f;
+        }
+        ok = warp_all(bwait(s.x_full, par, s, p));
+        if (!ok) break;
+        tc_fence_after();
+        load64(tX, xr);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t h2[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int at = k * 32 + 2 * u;
+                const uint32_t* y = xr[at >> 4] + (at & 15);
+                float2 a = add2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), D2);
+                a = mul2(a, make_float2(pr[at], pr[at + 1]));
+                if constexpr (T == VAE_F16) a = mul2(a, make_float2(f, f));
+                h2[u] = pack2<T>(a.x, a.y);
+            }
+            tmem_st16(tX + static_cast<uint32_t>(k * 16), h2);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(s.ds_full));
+    }
+    if (ok) ok = warp_all(bwait(s.done, 0u, s, p));
+    if (!ok || half != 0) return;
+    tc_fence_after();
+    const long long rows = static_cast<long long>(sh.b) * sh.hq * sh.sq;
+    const long long row = (static_cast<long long>(w.e) * sh.hq + h) * sh.sq + i;
+    store_acc<T>(tmem + lane_off + 256u, sh.d, live, true, p.scale / c, p.dq, w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h,
+                 p.nsplit_q > 1 ? p.part_q : nullptr, (w.split * rows + row) * sh.d);
+}
+
+template <int T, int kCh>
+__global__ void __launch_bounds__(kThreads, 1)
+    mha_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
+                  const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const BwdSmem s = bwd_carve<kCh>(smem_raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    pdl_wait();
+    const QWork w = q_work(p);
+    if (w.n == 0) {  // no key: zeros within the length
+        const int r = w.tile * kMhaTile + threadIdx.x;
+        const int i = r >> p.s.gp_log2, h = w.hk * p.s.g + (w.sub << p.s.gp_log2) + (r & ((1 << p.s.gp_log2) - 1));
+        if (threadIdx.x < kMhaTile && i < w.ql) {
+            const long long rows = static_cast<long long>(p.s.b) * p.s.hq * p.s.sq;
+            const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
+            store_acc<T>(0u, p.s.d, true, false, 0.f, p.dq, w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h,
+                         p.nsplit_q > 1 ? p.part_q : nullptr, (w.split * rows + row) * p.s.d);
+        }
+        return;
+    }
+    const uint32_t tmem = bwd_begin<kCh>(s, warp);
+    if (warp < kSoftWarps) q_softmax<T, kCh>(p, s, w, tmem, warp, lane);
+    else if (warp == kTmaWarp) q_producer<kCh>(p, s, w, &mq, &mg, &mk, &mv, lane);
+    else if (lane == 0) q_mma<T, kCh>(p, s, w, tmem);
+    bwd_end(tmem, warp);
+}
+
+// ───────────────────────────── joining the splits ─────────────────────────────
+
+// out[row] = sum of the splits' partial rows in order, rounded once; four
+// channels a thread. Rows [b][h][n], valid below the length.
+template <int T>
+__global__ void __launch_bounds__(256)
+    mha_sum_kernel(const float* __restrict__ part, long long split_stride, int nsplit, int b, int h, int n, int d,
+                   const int* len, void* out, MhaStrides os) {
+    pdl_wait();
+    const long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const int d4 = d / 4;
+    const long long row = x / d4;
+    if (row >= static_cast<long long>(b) * h * n) return;
+    const int c = static_cast<int>(x - row * d4) * 4;
+    const int i = static_cast<int>(row % n), hh = static_cast<int>(row / n % h), e = static_cast<int>(row / n / h);
+    if (i >= mha_len(len, e, n)) return;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < nsplit; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(part + k * split_stride + row * d + c);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(static_cast<typename Elem<T>::type*>(out) + e * os.b + i * os.s + hh * os.h + c) =
+        make_uint2(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w));
+}
+
+// Splits where tiles alone would leave SMs without work: two tiles of the other
+// side per CTA at least.
+struct BwdPlan {
+    int nsplit_q, nsplit_k;
+    long long q_items, k_items, row_tiles, key_tiles;
+    size_t side, part_q, part_kv;  // floats
+};
+int splits(long long items, long long most) {
+    const long long want = items < kTargetCtas ? kTargetCtas / items : 1;
+    return static_cast<int>(std::max<long long>(1, std::min(want, most / 2)));
+}
+BwdPlan bwd_plan(const MhaShape& s) {
+    BwdPlan f;
+    f.row_tiles = static_cast<long long>(s.b) * s.hkv * s.nsub * s.ntile;
+    f.key_tiles = static_cast<long long>(s.b) * s.hkv * s.nkb;
+    f.nsplit_q = splits(f.row_tiles, s.nkb);
+    f.nsplit_k = splits(f.key_tiles, static_cast<long long>(s.nsub) * s.ntile);
+    f.q_items = f.row_tiles * f.nsplit_q;
+    f.k_items = f.key_tiles * f.nsplit_k;
+    f.side = static_cast<size_t>(f.row_tiles) * kSideFloats;
+    f.part_q = f.nsplit_q > 1 ? static_cast<size_t>(f.nsplit_q) * s.b * s.hq * s.sq * s.d : 0;
+    f.part_kv = f.nsplit_k > 1 ? static_cast<size_t>(f.nsplit_k) * 2 * s.b * s.hkv * s.sk * s.d : 0;
+    return f;
+}
+constexpr size_t kMaximaFloats = 64;  // two words used; keeps what follows aligned
+
+template <int T, int kCh>
+int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap (&map)[4], const PrepParams& pp,
+               const BwdParams& p, cudaStream_t st) {
+    static CtxOnce once;
+    static std::mutex mu;
+    using C = BwdCfg<kCh>;
+    {
+        int dev;
+        VAE_CUDA_CHECK(cudaGetDevice(&dev));
+        std::lock_guard<std::mutex> lk(mu);
+        if (!once.done(dev)) {
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dkv_kernel<T, kCh>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dq_kernel<T, kCh>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+            once.mark(dev);
+        }
+    }
+    if (T == VAE_F16) VAE_CUDA_CHECK(cudaMemsetAsync(pp.maxima, 0, 2 * sizeof(unsigned), st));
+    const long long prep = f.row_tiles + (T == VAE_F16 ? f.key_tiles : 0);
+    VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
+    VAE_CUDA_CHECK(launch_kernel(mha_dkv_kernel<T, kCh>, dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), C::kSmem,
+                                 st, map[0], map[1], map[2], map[3], p));
+    VAE_CUDA_CHECK(launch_kernel(mha_dq_kernel<T, kCh>, dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), C::kSmem,
+                                 st, map[0], map[1], map[2], map[3], p));
+    const MhaShape& s = p.s;
+    if (f.nsplit_k > 1) {
+        const long long rows = static_cast<long long>(s.b) * s.hkv * s.sk;
+        const unsigned grid = static_cast<unsigned>((rows * (s.d / 4) + 255) / 256);
+        for (int k = 0; k < 2; ++k)
+            VAE_CUDA_CHECK(launch_kernel(mha_sum_kernel<T>, dim3(grid), dim3(256), 0, st,
+                                         static_cast<const float*>(p.part_kv) + k * rows * s.d, 2 * rows * s.d, f.nsplit_k,
+                                         s.b, s.hkv, s.sk, s.d, s.k_len, k == 0 ? p.dv : p.dk, k == 0 ? p.dvs : p.dks));
+    }
+    if (f.nsplit_q > 1) {
+        const long long rows = static_cast<long long>(s.b) * s.hq * s.sq;
+        const unsigned grid = static_cast<unsigned>((rows * (s.d / 4) + 255) / 256);
+        VAE_CUDA_CHECK(launch_kernel(mha_sum_kernel<T>, dim3(grid), dim3(256), 0, st, static_cast<const float*>(p.part_q),
+                                     rows * s.d, f.nsplit_q, s.b, s.hq, s.sq, s.d, s.q_len, p.dq, p.dqs));
+    }
+    return VAE_OK;
+}
+
+}  // namespace
+
+size_t mha_bwd_bytes(const MhaShape& s) {
+    const BwdPlan f = bwd_plan(s);
+    return ((kMaximaFloats + f.side + f.part_q + f.part_kv) * sizeof(float) + 15) / 16 * 16;
+}
+
+int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout, const void* q, const void* k,
+                const void* v, const void* o, const float* lse, void* dq, void* dk, void* dv, void* ws,
+                cudaStream_t st) {
+    const BwdPlan f = bwd_plan(s);
+    if (f.q_items > 0x7fffffffLL || f.k_items > 0x7fffffffLL || f.row_tiles + f.key_tiles > 0x7fffffffLL)
+        return set_error(VAE_ERR_SHAPE, "attention: too many tiles");
+    const int gp = 1 << s.gp_log2;
+    CUtensorMap map[4];
+    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, kMhaTile / gp);
+    if (rc == VAE_OK) rc = mha_map(&map[1], a, dout, a->do_stride, s.sq, s.hq, gp, kMhaTile / gp);
+    if (rc == VAE_OK) rc = mha_map(&map[2], a, k, a->k_stride, s.sk, s.hkv, 1, kMhaTile);
+    if (rc == VAE_OK) rc = mha_map(&map[3], a, v, a->v_stride, s.sk, s.hkv, 1, kMhaTile);
+    if (rc != VAE_OK) return rc;
+    float* w = static_cast<float*>(ws);
+    PrepParams pp{};
+    pp.s = s;
+    pp.dout = dout;
+    pp.o = o;
+    pp.v = v;
+    pp.gs = mha_strides(a->do_stride);
+    pp.os = mha_strides(a->o_stride);
+    pp.vs = mha_strides(a->v_stride);
+    pp.lse = lse;
+    pp.maxima = static_cast<unsigned*>(ws);
+    pp.side = w + kMaximaFloats;
+    pp.row_tiles = static_cast<int>(f.row_tiles);
+    BwdParams p{};
+    p.s = s;
+    p.scale = a->scale;
+    p.scale_log2 = a->scale * 1.4426950408889634074f;
+    p.nsplit_q = f.nsplit_q;
+    p.nsplit_k = f.nsplit_k;
+    p.side = pp.side;
+    p.maxima = pp.maxima;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.dqs = mha_strides(a->dq_stride);
+    p.dks = mha_strides(a->dk_stride);
+    p.dvs = mha_strides(a->dv_stride);
+    p.part_q = pp.side + f.side;
+    p.part_kv = p.part_q + f.part_q;
+    p.status = device_status_ptr();
+    p.timeout_ns = wait_timeout_ns();
+    if (p.status == nullptr) return VAE_ERR_CUDA;
+    if (a->type == VAE_F16)
+        return s.d > 64 ? bwd_launch<VAE_F16, 2>(a, f, map, pp, p, st) : bwd_launch<VAE_F16, 1>(a, f, map, pp, p, st);
+    return s.d > 64 ? bwd_launch<VAE_BF16, 2>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 1>(a, f, map, pp, p, st);
+}
+
+}  // namespace vae
