@@ -89,11 +89,46 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// One lane of a converged warp, always the same. The MMA warps run their loops
+// with all lanes and issue under this predicate: a loop that only one lane
+// entered cannot keep the descriptors in uniform registers, and each M = 128,
+// N = 128 MMA (64 cycles of tensor work) then took about 114 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
+
+// D = A B^T of two K-major tiles in shared memory, kSteps x 16 channels.
+template <int kSteps>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        const uint32_t off = static_cast<uint32_t>((k >> 2) * (kMhaChunkBytes >> 4) + (k & 3) * 2);
+        umma_f16(d_tmem, a + off, b + off, id, k != 0 ? 1u : 0u);
+    }
+}
+// D (+)= A B with 128 columns of A as 16-bit pairs in TMEM: two halves kHalf
+// columns apart, 32 columns each; B MN-major.
+template <int kHalf>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        umma_f16_ts(d_tmem, a_tmem + static_cast<uint32_t>((k >> 2) * kHalf + (k & 3) * 8), b + (2048u >> 4) * k, id,
+                    k != 0 ? 1u : acc);
+}
+
 // 2^x, approximate (relative error near 2^-22); under 2^-126 it is 0.
 __device__ __forceinline__ float mha_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Pairs of f32 in one instruction.

@@ -235,8 +235,8 @@ __device__ __forceinline__ uint32_t bwd_begin(const BwdSmem& s, int warp) {
         mbar_init(smem_u32(s.res_full), 1u);
         mbar_init(smem_u32(s.s_full), 1u);
         mbar_init(smem_u32(s.x_full), 1u);
-        mbar_init(smem_u32(s.p_full), kSoftWarps * 32u);
-        mbar_init(smem_u32(s.ds_full), kSoftWarps * 32u);
+        mbar_init(smem_u32(s.p_full), kSoftWarps);
+        mbar_init(smem_u32(s.ds_full), kSoftWarps);
         mbar_init(smem_u32(s.done), 1u);
         mbar_init(smem_u32(s.fix), 1u);
         mbar_init(smem_u32(s.drain), 1u);
@@ -560,7 +560,8 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(s.p_full));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(s.p_full));
         ok = warp_all(bwait(s.x_full, par, s, p));
         if (!ok) break;
         tc_fence_after();
@@ -592,7 +593,8 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(s.ds_full));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(s.ds_full));
         if (++st == C::kStages) {
             st = 0;
             ph ^= 1u;
@@ -802,7 +804,8 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
         float pr[64];
         load64(tS, xr);
         tc_fence_before();
-        mbar_arrive(smem_u32(s.p_full));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(s.p_full));
 #pragma unroll
         for (int k = 0; k < 64; k += 2) {
             const uint32_t* y = xr[k >> 4] + (k & 15);
@@ -837,7 +840,8 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(s.ds_full));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(s.ds_full));
     }
     if (ok) ok = warp_all(bwait(s.done, 0u, s, p));
     if (!ok || half != 0) return;

@@ -37,15 +37,16 @@ constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr uint32_t kTmemCols = 512;  // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kTargetCtas = 152;     // one CTA per SM
 
-template <int kCh>
+template <int kSteps>  // 16-channel steps of a row
 struct FwdCfg {
+    static constexpr int kCh = kSteps > 4 ? 2 : 1;  // 64-channel chunks
     static constexpr int kTileBytes = kCh * kMhaChunkBytes;
     static constexpr int kStages = kCh == 2 ? 5 : 8;
     static constexpr int kRing = 2 * kTileBytes;  // behind the two Q tiles
     static constexpr int kBars = kRing + kStages * kTileBytes;
     static constexpr int kSmem = 1024 + kBars + 512;
 };
-static_assert(FwdCfg<2>::kSmem <= 232448 && FwdCfg<1>::kSmem <= 232448, "attention shared memory over 227 KB");
+static_assert(FwdCfg<8>::kSmem <= 232448 && FwdCfg<4>::kSmem <= 232448, "attention shared memory over 227 KB");
 
 struct FwdParams {
     MhaShape s;
@@ -69,9 +70,9 @@ struct FwdSmem {
     float* ml;  // [2][128]: (m, l) of the second stream's rows (alt)
 };
 
-template <int kCh>
+template <int kSteps>
 __device__ __forceinline__ FwdSmem fwd_carve(uint8_t* raw) {
-    using C = FwdCfg<kCh>;
+    using C = FwdCfg<kSteps>;
     FwdSmem s;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.q = base;
@@ -87,7 +88,7 @@ __device__ __forceinline__ FwdSmem fwd_carve(uint8_t* raw) {
     s.drain = s.fix + 1;
     s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
     s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
-    s.ml = reinterpret_cast<float*>(s.ring + 128 * 128 * 4 / (kCh == 2 ? 1 : 2));  // behind the exchanged O
+    s.ml = reinterpret_cast<float*>(s.ring + 128 * 128 * 4 / (C::kCh == 2 ? 1 : 2));  // behind the exchanged O
     return s;
 }
 
@@ -139,10 +140,10 @@ __device__ __forceinline__ FwdWork fwd_work(const FwdParams& p) {
     return w;
 }
 
-template <int kCh>
+template <int kSteps>
 __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork& w, const CUtensorMap* mq,
                              const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
-    using C = FwdCfg<kCh>;
+    using C = FwdCfg<kSteps>;
     const uint64_t pol = policy_evict_normal();
     const int gp = 1 << p.s.gp_log2;
     const int h0 = w.hk * p.s.g + w.sub * gp;
@@ -151,7 +152,7 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
     if (lane == 0) {
         mbar_arrive_expect_tx(smem_u32(s.q_full), static_cast<uint32_t>(nq * C::kTileBytes));
         for (int t = 0; t < nq; ++t)
-            for (int c = 0; c < kCh; ++c)
+            for (int c = 0; c < C::kCh; ++c)
                 tma_load_4d(smem_u32(s.q + t * C::kTileBytes + c * kMhaChunkBytes), mq, smem_u32(s.q_full), c * 64, h0,
                             (w.tile[t] * kMhaTile) >> p.s.gp_log2, w.e, pol);
     }
@@ -169,7 +170,7 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
         uint8_t* dst = s.ring + stage * C::kTileBytes;
         if (lane == 0) {
             mbar_arrive_expect_tx(fb, static_cast<uint32_t>(C::kTileBytes));
-            for (int c = 0; c < kCh; ++c)
+            for (int c = 0; c < C::kCh; ++c)
                 tma_load_4d(smem_u32(dst + c * kMhaChunkBytes), is_v ? mv : mk, fb, c * 64, w.hk, kb * kMhaTile, w.e, pol);
         }
         if (fix) {
@@ -177,7 +178,7 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
             fixed = true;
             __syncwarp();
             if (!warp_all(fwait(s.fix, 0u, s, p))) return false;
-            mha_zero_rows(dst, w.kl - kb * kMhaTile, kCh, lane);
+            mha_zero_rows(dst, w.kl - kb * kMhaTile, C::kCh, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.full[stage]));
@@ -208,17 +209,16 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
     __syncwarp();
 }
 
-template <int T, int kCh>
-__device__ void fwd_mma(const FwdParams& p, const FwdSmem& s, const FwdWork& w, uint32_t tmem) {
-    using C = FwdCfg<kCh>;
-    const int kd = (p.s.d + 15) / 16;  // 16-channel steps of S
-    const uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kd * 16, true);
+template <int T, int kSteps>
+__device__ void fwd_mma(const FwdParams& p, const FwdSmem& s, const FwdWork& w) {
+    using C = FwdCfg<kSteps>;
+    constexpr uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kSteps * 16, true);
     const uint64_t qd = sw128_kmajor_desc(smem_u32(s.q));
     const uint64_t kdesc = sw128_kmajor_desc(smem_u32(s.ring)), vdesc = sw128_mnmajor_desc(smem_u32(s.ring));
     int stage = 0;
     uint32_t phase = 0;
     uint32_t pp[2] = {0u, 0u};
-    bool ok = fwait(s.q_full, 0u, s, p);
+    auto wait = [&](uint64_t* bar, uint32_t par) { return warp_all(fwait(bar, par, s, p)); };
     auto next = [&]() {
         if (++stage == C::kStages) {
             stage = 0;
@@ -226,30 +226,30 @@ __device__ void fwd_mma(const FwdParams& p, const FwdSmem& s, const FwdWork& w, 
         }
     };
     auto issue_s = [&](int t, int st) {
-        const uint64_t a0 = qd + (p.alt ? 0u : static_cast<uint32_t>(t * C::kTileBytes) >> 4);
-        const uint64_t b0 = kdesc + (static_cast<uint32_t>(st * C::kTileBytes) >> 4);
-#pragma unroll 1
-        for (int k = 0; k < kd; ++k) {
-            const uint32_t off = static_cast<uint32_t>((k >> 2) * (kMhaChunkBytes >> 4) + (k & 3) * 2);
-            umma_f16(tmem + static_cast<uint32_t>(t * 128), a0 + off, b0 + off, id_s, k != 0 ? 1u : 0u);
-        }
+        mma_ss<kSteps>(static_cast<uint32_t>(t * 128), qd + (p.alt ? 0u : static_cast<uint32_t>(t) * (C::kTileBytes >> 4)),
+                       kdesc + static_cast<uint32_t>(st) * (C::kTileBytes >> 4), id_s);
         umma_commit(smem_u32(&s.s_full[t]));
     };
+    bool ok = wait(s.q_full, 0u);
     const int ahead = p.alt ? 2 : 1;
     for (int j = 0; ok && j < ahead && j < w.n; ++j) {
-        ok = fwait(&s.full[stage], phase, s, p);
+        ok = wait(&s.full[stage], phase);
         if (!ok) break;
         tc_fence_after();
-        if (p.alt) {
-            issue_s(j & 1, stage);
-        } else {
-            for (int t = 0; t < w.streams; ++t) issue_s(t, stage);
+        if (elect_one()) {
+            if (p.alt) {
+                issue_s(j & 1, stage);
+            } else {
+                issue_s(0, stage);
+                if (w.streams == 2) issue_s(1, stage);
+            }
+            umma_commit(smem_u32(&s.empty[stage]));
         }
-        umma_commit(smem_u32(&s.empty[stage]));
+        __syncwarp();
         next();
     }
     for (int j = 0; ok && j < w.n; ++j) {
-        ok = fwait(&s.full[stage], phase, s, p);
+        ok = wait(&s.full[stage], phase);
         if (!ok) break;
         const int vst = stage;
         next();
@@ -259,37 +259,39 @@ __device__ void fwd_mma(const FwdParams& p, const FwdSmem& s, const FwdWork& w, 
         if (more) next();
         const int t0 = p.alt ? j & 1 : 0, t1 = p.alt ? t0 + 1 : w.streams;
         for (int t = t0; ok && t < t1; ++t) {
-            ok = fwait(&s.p_full[t], pp[t], s, p);
+            ok = wait(&s.p_full[t], t == 0 ? pp[0] : pp[1]);
             if (!ok) break;
-            pp[t] ^= 1u;
-            tc_fence_after();
-            const uint64_t b0 = vdesc + (static_cast<uint32_t>(vst * C::kTileBytes) >> 4);
-            const uint32_t dO = tmem + 256u + static_cast<uint32_t>(t * 128), aP = tmem + static_cast<uint32_t>(t * 128);
-            const uint32_t first = (p.alt ? j < 2 : j == 0) ? 0u : 1u;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                umma_f16_ts(dO, aP + 8u * k, b0 + (2048u >> 4) * k, id_o, k != 0 ? 1u : first);
-            if (t + 1 == t1) umma_commit(smem_u32(&s.empty[vst]));
-            if (more) {
-                if (t == t0) {
-                    ok = fwait(&s.full[kst], kph, s, p);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                issue_s(t, kst);
-                if (t + 1 == t1) umma_commit(smem_u32(&s.empty[kst]));
-            } else {
-                umma_commit(smem_u32(&s.o_full[t]));
+            if (t == 0) pp[0] ^= 1u;
+            else pp[1] ^= 1u;
+            if (more && t == t0) {
+                ok = wait(&s.full[kst], kph);
+                if (!ok) break;
             }
+            tc_fence_after();
+            if (elect_one()) {
+                mma_ts<32>(256u + static_cast<uint32_t>(t * 128), static_cast<uint32_t>(t * 128),
+                           vdesc + static_cast<uint32_t>(vst) * (C::kTileBytes >> 4), id_o, (p.alt ? j < 2 : j == 0) ? 0u : 1u);
+                if (t + 1 == t1) umma_commit(smem_u32(&s.empty[vst]));
+                if (more) {
+                    issue_s(t, kst);
+                    if (t + 1 == t1) umma_commit(smem_u32(&s.empty[kst]));
+                } else {
+                    umma_commit(smem_u32(&s.o_full[t]));
+                }
+            }
+            __syncwarp();
         }
     }
-    umma_commit(smem_u32(s.drain));
-    int never = 0;
-    (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+    if (elect_one()) {
+        umma_commit(smem_u32(s.drain));
+        int never = 0;
+        (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+    }
+    __syncwarp();
 }
 
 // One row's result: `inv` scales O, lse2 is in units of log 2.
-template <int T, int kCh>
+template <int T, int kSteps>
 __device__ void fwd_store(const FwdParams& p, const FwdWork& w, uint32_t tO, int i, int h, bool live, float w0,
                           const float* o1, float w1, float inv, float lse2) {
     const int d = p.s.d;
@@ -321,7 +323,7 @@ __device__ void fwd_store(const FwdParams& p, const FwdWork& w, uint32_t tO, int
     else p.lse[row] = lse2 * 0.69314718055994530942f;
 }
 
-template <int T, int kCh>
+template <int T, int kSteps>
 __device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork& w, uint32_t tmem, int warp, int lane) {
     // f16 holds P 2^kBias high (the sum l too): 2^(8 + 6) at most
     constexpr float kBias = T == VAE_F16 ? 6.f : 0.f;
@@ -408,7 +410,8 @@ __device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork&
             tmem_st_wait();
             tc_fence_before();
         }
-        mbar_arrive(smem_u32(&s.p_full[t]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.p_full[t]));
     }
     const bool join = p.alt && w.streams == 2;
     if (runs && ok) ok = warp_all(fwait(&s.o_full[t], 0u, s, p));
@@ -437,24 +440,24 @@ __device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork&
             const float mm = fmaxf(m, m1);
             const float w0 = m == -INFINITY ? 0.f : mha_ex2(m - mm), w1 = m1 == -INFINITY ? 0.f : mha_ex2(m1 - mm);
             const float ll = w0 * l + w1 * l1;
-            fwd_store<T, kCh>(p, w, tO, i, h, live, w0, o1 + rr, w1, mm == -INFINITY ? 0.f : 1.f / ll,
+            fwd_store<T, kSteps>(p, w, tO, i, h, live, w0, o1 + rr, w1, mm == -INFINITY ? 0.f : 1.f / ll,
                               mm == -INFINITY ? -INFINITY : mm - kBias + log2f(ll));
         }
     } else if (runs && ok && any_live) {
         tc_fence_after();
         const bool none = m == -INFINITY;
-        fwd_store<T, kCh>(p, w, tO, i, h, live, 1.f, nullptr, 0.f, none ? 0.f : 1.f / l,
+        fwd_store<T, kSteps>(p, w, tO, i, h, live, 1.f, nullptr, 0.f, none ? 0.f : 1.f / l,
                           none ? -INFINITY : m - kBias + log2f(l));
     }
 }
 
-template <int T, int kCh>
+template <int T, int kSteps>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const FwdParams p) {
-    using C = FwdCfg<kCh>;
+    using C = FwdCfg<kSteps>;
     extern __shared__ uint8_t smem_raw[];
-    const FwdSmem s = fwd_carve<kCh>(smem_raw);
+    const FwdSmem s = fwd_carve<kSteps>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const FwdWork w = fwd_work(p);
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s.s_full[i]), 1u);
-            mbar_init(smem_u32(&s.p_full[i]), 128u);
+            mbar_init(smem_u32(&s.p_full[i]), 4u);
             mbar_init(smem_u32(&s.o_full[i]), 1u);
         }
         mbar_init(smem_u32(s.q_full), 1u);
@@ -499,13 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s.tmem_slot;
+    constexpr uint32_t tmem = 0u;  // all 512 columns are this CTA's: they start at 0
     if (warp < kSoftWarps) {
-        fwd_softmax<T, kCh>(p, s, w, tmem, warp, lane);
+        fwd_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
     } else if (warp == kTmaWarp) {
-        fwd_producer<kCh>(p, s, w, &mq, &mk, &mv, lane);
-    } else if (lane == 0) {
-        fwd_mma<T, kCh>(p, s, w, tmem);
+        fwd_producer<kSteps>(p, s, w, &mq, &mk, &mv, lane);
+    } else {
+        fwd_mma<T, kSteps>(p, s, w);
     }
     pdl_launch_dependents();
     __syncwarp();
@@ -585,23 +588,23 @@ FwdPlan fwd_plan(const MhaShape& s) {
     return f;
 }
 
-template <int T, int kCh>
+template <int T, int kSteps>
 int fwd_launch(const vae_attention_desc* a, const FwdPlan& f, const CUtensorMap (&map)[3], const FwdParams& p,
                cudaStream_t st) {
     static CtxOnce once;
     static std::mutex mu;
-    using C = FwdCfg<kCh>;
+    using C = FwdCfg<kSteps>;
     {
         int dev;
         VAE_CUDA_CHECK(cudaGetDevice(&dev));
         std::lock_guard<std::mutex> lk(mu);
         if (!once.done(dev)) {
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_fwd_kernel<T, kCh>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_fwd_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                 C::kSmem));
             once.mark(dev);
         }
     }
-    VAE_CUDA_CHECK(launch_kernel(mha_fwd_kernel<T, kCh>, dim3(static_cast<unsigned>(f.items)), dim3(kThreads), C::kSmem,
+    VAE_CUDA_CHECK(launch_kernel(mha_fwd_kernel<T, kSteps>, dim3(static_cast<unsigned>(f.items)), dim3(kThreads), C::kSmem,
                                  st, map[0], map[1], map[2], p));
     if (f.nsplit > 1) {
         const long long rows = static_cast<long long>(a->b) * a->hq * a->sq;
@@ -643,9 +646,10 @@ int mha_fwd_run(const vae_attention_desc* a, const MhaShape& s, const void* q, c
     p.status = device_status_ptr();
     p.timeout_ns = wait_timeout_ns();
     if (p.status == nullptr) return VAE_ERR_CUDA;
-    if (a->type == VAE_F16)
-        return s.d > 64 ? fwd_launch<VAE_F16, 2>(a, f, map, p, st) : fwd_launch<VAE_F16, 1>(a, f, map, p, st);
-    return s.d > 64 ? fwd_launch<VAE_BF16, 2>(a, f, map, p, st) : fwd_launch<VAE_BF16, 1>(a, f, map, p, st);
+    const bool h = a->type == VAE_F16;
+    if (s.d <= 64) return h ? fwd_launch<VAE_F16, 4>(a, f, map, p, st) : fwd_launch<VAE_BF16, 4>(a, f, map, p, st);
+    if (s.d <= 96) return h ? fwd_launch<VAE_F16, 6>(a, f, map, p, st) : fwd_launch<VAE_BF16, 6>(a, f, map, p, st);
+    return h ? fwd_launch<VAE_F16, 8>(a, f, map, p, st) : fwd_launch<VAE_BF16, 8>(a, f, map, p, st);
 }
 
 }  // namespace vae
