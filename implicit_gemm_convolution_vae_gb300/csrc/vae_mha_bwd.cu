@@ -44,8 +44,9 @@ constexpr int kPLog2 = 14;         // f16: P is held as P 2^14
 constexpr int kSideFloats = 256;   // of a row tile: 128 x (kPLog2 - lse log2(e)), 128 x D
 constexpr int kSideBytes = kSideFloats * 4;
 
-template <int kCh>
+template <int kSteps>  // 16-channel steps of a row
 struct BwdCfg {
+    static constexpr int kCh = kSteps > 4 ? 2 : 1;  // 64-channel chunks
     static constexpr int kTileBytes = kCh * kMhaChunkBytes;
     static constexpr int kStages = kCh == 2 ? 2 : 4;
     static constexpr int kRing = 2 * kTileBytes;  // behind the two resident tiles
@@ -53,7 +54,7 @@ struct BwdCfg {
     static constexpr int kBars = kSide + kStages * kSideBytes;
     static constexpr int kSmem = 1024 + kBars + 512;
 };
-static_assert(BwdCfg<2>::kSmem <= 232448 && BwdCfg<1>::kSmem <= 232448, "attention shared memory over 227 KB");
+static_assert(BwdCfg<8>::kSmem <= 232448 && BwdCfg<4>::kSmem <= 232448, "attention shared memory over 227 KB");
 
 struct BwdParams {
     MhaShape s;
@@ -178,9 +179,9 @@ struct BwdSmem {
     int* abort_flag;
 };
 
-template <int kCh>
+template <int kSteps>
 __device__ __forceinline__ BwdSmem bwd_carve(uint8_t* raw) {
-    using C = BwdCfg<kCh>;
+    using C = BwdCfg<kSteps>;
     BwdSmem s;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.res = base;
@@ -214,17 +215,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-template <int kCh>
+template <int kChunks>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int head, int token, int e,
                                           uint64_t pol) {
-    for (int c = 0; c < kCh; ++c)
+    for (int c = 0; c < kChunks; ++c)
         tma_load_4d(smem_u32(dst + c * kMhaChunkBytes), map, bar, c * 64, head, token, e, pol);
 }
 
 // Set-up and tear-down common to both kernels.
-template <int kCh>
+template <int kSteps>
 __device__ __forceinline__ uint32_t bwd_begin(const BwdSmem& s, int warp) {
-    using C = BwdCfg<kCh>;
+    using C = BwdCfg<kSteps>;
     if (threadIdx.x == 0) {
         *s.abort_flag = 0;
         for (int i = 0; i < C::kStages; ++i) {
@@ -249,7 +250,7 @@ __device__ __forceinline__ uint32_t bwd_begin(const BwdSmem& s, int warp) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    return *s.tmem_slot;
+    return 0u;  // all 512 columns are this CTA's: they start at 0
 }
 __device__ __forceinline__ void bwd_end(uint32_t tmem, int warp) {
     pdl_launch_dependents();
@@ -292,28 +293,14 @@ struct BwdRing {
     }
 };
 
-// One product D (+)= A B^T of two K-major tiles in shared memory, 128 x 128.
-// (The loop stays a loop: unrolled with a test per step, the predicated MMAs
-// were seen to take wrong operands.)
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, int steps) {
-#pragma unroll 1
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t off = static_cast<uint32_t>((k >> 2) * (kMhaChunkBytes >> 4) + (k & 3) * 2);
-        umma_f16(d_tmem, a + off, b + off, id, k != 0 ? 1u : 0u);
+__device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p, bool ok) {
+    if (elect_one()) {
+        if (ok) umma_commit(smem_u32(s.done));
+        umma_commit(smem_u32(s.drain));
+        int never = 0;
+        (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
     }
-}
-// D += A B with A in TMEM: its columns in two halves of 64, 32 used of each.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        umma_f16_ts(d_tmem, a_tmem + static_cast<uint32_t>((k >> 2) * 64 + (k & 3) * 8), b + (2048u >> 4) * k, id,
-                    k != 0 ? 1u : acc);
-}
-
-__device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p) {
-    umma_commit(smem_u32(s.drain));
-    int never = 0;
-    (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
+    __syncwarp();
 }
 
 // 64 columns of this warp's lanes.
@@ -389,18 +376,18 @@ __device__ __forceinline__ KvWork kv_work(const BwdParams& p) {
     return w;
 }
 
-template <int kCh>
+template <int kSteps>
 __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& w, const CUtensorMap* mq,
                             const CUtensorMap* mg, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
-    using C = BwdCfg<kCh>;
+    using C = BwdCfg<kSteps>;
     const uint64_t pol = policy_evict_normal();
     const MhaShape& sh = p.s;
     const int gp = 1 << sh.gp_log2;
     if (lane == 0) {
         const uint32_t rb = smem_u32(s.res_full);
         mbar_arrive_expect_tx(rb, 2u * C::kTileBytes);
-        load_tile<kCh>(s.res, mk, rb, w.hk, w.kb * kMhaTile, w.e, pol);
-        load_tile<kCh>(s.res + C::kTileBytes, mv, rb, w.hk, w.kb * kMhaTile, w.e, pol);
+        load_tile<C::kCh>(s.res, mk, rb, w.hk, w.kb * kMhaTile, w.e, pol);
+        load_tile<C::kCh>(s.res + C::kTileBytes, mv, rb, w.hk, w.kb * kMhaTile, w.e, pol);
     }
     BwdRing<C::kStages> r;
     const int per = w.nt - w.t0;
@@ -422,9 +409,9 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
                 mbar_arrive_expect_tx(ab, C::kTileBytes + kSideBytes);
                 mbar_arrive_expect_tx(bb, C::kTileBytes);
             }
-            load_tile<kCh>(dst, mq, ab, head, token, w.e, pol);
+            load_tile<C::kCh>(dst, mq, ab, head, token, w.e, pol);
             bulk_load(smem_u32(sd), src, kSideBytes, ab);
-            load_tile<kCh>(dst + C::kTileBytes, mg, bb, head, token, w.e, pol);
+            load_tile<C::kCh>(dst + C::kTileBytes, mg, bb, head, token, w.e, pol);
         }
         if (fix) {
             r.armed &= ~(1u << r.stage);  // (its copies complete on the fix barrier)
@@ -432,8 +419,8 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
             ++r.fixes;
             __syncwarp();
             if (!warp_all(bwait(s.fix, par, s, p))) break;
-            mha_zero_rows(dst, static_cast<int>(valid), kCh, lane);
-            mha_zero_rows(dst + C::kTileBytes, static_cast<int>(valid), kCh, lane);
+            mha_zero_rows(dst, static_cast<int>(valid), C::kCh, lane);
+            mha_zero_rows(dst + C::kTileBytes, static_cast<int>(valid), C::kCh, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -449,62 +436,64 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
     __syncwarp();
 }
 
-template <int T, int kCh>
-__device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w, uint32_t tmem) {
-    using C = BwdCfg<kCh>;
-    const int kd = (p.s.d + 15) / 16;
-    const uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kd * 16, true);
-    const uint32_t tS = tmem, tX = tmem + 128u, tV = tmem + 256u, tK = tmem + 384u;
-    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(s.res)), vdesc = kdesc + (C::kTileBytes >> 4);
+template <int T, int kSteps>
+__device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
+    using C = BwdCfg<kSteps>;
+    constexpr uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kSteps * 16, true);
+    constexpr uint32_t tS = 0u, tX = 128u, tV = 256u, tK = 384u;
+    constexpr uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
+    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(s.res)), vdesc = kdesc + second;
     const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
-    const uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
-    bool ok = bwait(s.res_full, 0u, s, p);
-    auto score = [&](int st, uint32_t ph) {
-        if (!bwait(&s.a_full[st], ph, s, p)) return false;
-        tc_fence_after();
-        mma_ss(tS, kdesc, ring_k + st * stage_units, id_s, kd);
+    auto wait = [&](uint64_t* bar, uint32_t par) { return warp_all(bwait(bar, par, s, p)); };
+    auto score = [&](uint32_t st) {
+        mma_ss<kSteps>(tS, kdesc, ring_k + st * stage_units, id_s);
         umma_commit(smem_u32(s.s_full));
-        return true;
     };
-    auto cross = [&](int st, uint32_t ph) {
-        if (!bwait(&s.b_full[st], ph, s, p)) return false;
-        tc_fence_after();
-        mma_ss(tX, vdesc, ring_k + st * stage_units + second, id_s, kd);
+    auto cross = [&](uint32_t st) {
+        mma_ss<kSteps>(tX, vdesc, ring_k + st * stage_units + second, id_s);
         umma_commit(smem_u32(s.x_full));
-        return true;
     };
-    int st = 0;
-    uint32_t ph = 0;
-    ok = ok && score(0, 0u) && cross(0, 0u);
+    uint32_t st = 0, ph = 0;
+    bool ok = wait(s.res_full, 0u) && wait(&s.a_full[0], 0u) && wait(&s.b_full[0], 0u);
+    if (ok) {
+        tc_fence_after();
+        if (elect_one()) {
+            score(0);
+            cross(0);
+        }
+        __syncwarp();
+    }
     for (int x = 0; ok && x < w.n; ++x) {
         const uint32_t par = static_cast<uint32_t>(x) & 1u;
-        int st1 = st + 1;
-        uint32_t ph1 = ph;
-        if (st1 == C::kStages) {
-            st1 = 0;
-            ph1 ^= 1u;
+        const bool more = x + 1 < w.n;
+        const bool wrap = st + 1 == C::kStages;
+        const uint32_t st1 = wrap ? 0u : st + 1u, ph1 = wrap ? ph ^ 1u : ph;
+        ok = wait(s.p_full, par) && (!more || wait(&s.a_full[st1], ph1));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+            mma_ts<64>(tV, tS, ring_m + st * stage_units + second, id_o, x != 0 ? 1u : 0u);
+            if (more) score(st1);
         }
-        ok = bwait(s.p_full, par, s, p);
+        __syncwarp();
+        ok = wait(s.ds_full, par) && (!more || wait(&s.b_full[st1], ph1));
         if (!ok) break;
         tc_fence_after();
-        mma_ts(tV, tS, ring_m + st * stage_units + second, id_o, x != 0 ? 1u : 0u);
-        if (x + 1 < w.n && !(ok = score(st1, ph1))) break;
-        ok = bwait(s.ds_full, par, s, p);
-        if (!ok) break;
-        tc_fence_after();
-        mma_ts(tK, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
-        umma_commit(smem_u32(&s.empty[st]));
-        if (x + 1 < w.n && !(ok = cross(st1, ph1))) break;
+        if (elect_one()) {
+            mma_ts<64>(tK, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
+            umma_commit(smem_u32(&s.empty[st]));
+            if (more) cross(st1);
+        }
+        __syncwarp();
         st = st1;
         ph = ph1;
     }
-    if (ok) umma_commit(smem_u32(s.done));
-    mma_finish(s, p);
+    mma_finish(s, p, ok);
 }
 
-template <int T, int kCh>
+template <int T, int kSteps>
 __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w, uint32_t tmem, int warp, int lane) {
-    using C = BwdCfg<kCh>;
+    using C = BwdCfg<kSteps>;
     const int quad = warp & 3, half = warp >> 2;
     const MhaShape& sh = p.s;
     const int j = w.kb * kMhaTile + quad * 32 + lane;
@@ -614,12 +603,12 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
                  ((w.split * 2 + half) * rows + row) * sh.d);
 }
 
-template <int T, int kCh>
+template <int T, int kSteps>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
-    const BwdSmem s = bwd_carve<kCh>(smem_raw);
+    const BwdSmem s = bwd_carve<kSteps>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const KvWork w = kv_work(p);
@@ -635,10 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    const uint32_t tmem = bwd_begin<kCh>(s, warp);
-    if (warp < kSoftWarps) kv_softmax<T, kCh>(p, s, w, tmem, warp, lane);
-    else if (warp == kTmaWarp) kv_producer<kCh>(p, s, w, &mq, &mg, &mk, &mv, lane);
-    else if (lane == 0) kv_mma<T, kCh>(p, s, w, tmem);
+    const uint32_t tmem = bwd_begin<kSteps>(s, warp);
+    if (warp < kSoftWarps) kv_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
+    else if (warp == kTmaWarp) kv_producer<kSteps>(p, s, w, &mq, &mg, &mk, &mv, lane);
+    else kv_mma<T, kSteps>(p, s, w);
     bwd_end(tmem, warp);
 }
 
@@ -675,18 +664,18 @@ __device__ __forceinline__ QWork q_work(const BwdParams& p) {
     return w;
 }
 
-template <int kCh>
+template <int kSteps>
 __device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w, const CUtensorMap* mq,
                            const CUtensorMap* mg, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
-    using C = BwdCfg<kCh>;
+    using C = BwdCfg<kSteps>;
     const uint64_t pol = policy_evict_normal();
     const MhaShape& sh = p.s;
     if (lane == 0) {
         const uint32_t rb = smem_u32(s.res_full);
         const int head = w.hk * sh.g + (w.sub << sh.gp_log2), token = (w.tile * kMhaTile) >> sh.gp_log2;
         mbar_arrive_expect_tx(rb, 2u * C::kTileBytes);
-        load_tile<kCh>(s.res, mq, rb, head, token, w.e, pol);
-        load_tile<kCh>(s.res + C::kTileBytes, mg, rb, head, token, w.e, pol);
+        load_tile<C::kCh>(s.res, mq, rb, head, token, w.e, pol);
+        load_tile<C::kCh>(s.res + C::kTileBytes, mg, rb, head, token, w.e, pol);
     }
     BwdRing<C::kStages> r;
     for (int x = 0; x < w.n; ++x) {
@@ -698,8 +687,8 @@ __device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w,
         if (lane == 0) {
             mbar_arrive_expect_tx(ab, (fix ? 2u : 1u) * C::kTileBytes);
             if (!fix) mbar_arrive_expect_tx(bb, C::kTileBytes);
-            load_tile<kCh>(dst, mk, ab, w.hk, kb * kMhaTile, w.e, pol);
-            load_tile<kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, w.e, pol);
+            load_tile<C::kCh>(dst, mk, ab, w.hk, kb * kMhaTile, w.e, pol);
+            load_tile<C::kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, w.e, pol);
         }
         if (fix) {
             r.armed &= ~(1u << r.stage);
@@ -707,8 +696,8 @@ __device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w,
             ++r.fixes;
             __syncwarp();
             if (!warp_all(bwait(s.fix, par, s, p))) break;
-            mha_zero_rows(dst, w.kl - kb * kMhaTile, kCh, lane);
-            mha_zero_rows(dst + C::kTileBytes, w.kl - kb * kMhaTile, kCh, lane);
+            mha_zero_rows(dst, w.kl - kb * kMhaTile, C::kCh, lane);
+            mha_zero_rows(dst + C::kTileBytes, w.kl - kb * kMhaTile, C::kCh, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -724,61 +713,61 @@ __device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w,
     __syncwarp();
 }
 
-template <int T, int kCh>
-__device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w, uint32_t tmem) {
-    using C = BwdCfg<kCh>;
-    const int kd = (p.s.d + 15) / 16;
-    const uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kd * 16, true);
-    const uint32_t tS = tmem, tX = tmem + 128u, tQ = tmem + 256u;
-    const uint64_t qdesc = sw128_kmajor_desc(smem_u32(s.res)), gdesc = qdesc + (C::kTileBytes >> 4);
+template <int T, int kSteps>
+__device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
+    using C = BwdCfg<kSteps>;
+    constexpr uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kSteps * 16, true);
+    constexpr uint32_t tS = 0u, tX = 128u, tQ = 256u;
+    constexpr uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
+    const uint64_t qdesc = sw128_kmajor_desc(smem_u32(s.res)), gdesc = qdesc + second;
     const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
-    const uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
-    bool ok = bwait(s.res_full, 0u, s, p);
-    auto score = [&](int st, uint32_t ph) {
-        if (!bwait(&s.a_full[st], ph, s, p)) return false;
-        tc_fence_after();
-        mma_ss(tS, qdesc, ring_k + st * stage_units, id_s, kd);
+    auto wait = [&](uint64_t* bar, uint32_t par) { return warp_all(bwait(bar, par, s, p)); };
+    auto score = [&](uint32_t st) {
+        mma_ss<kSteps>(tS, qdesc, ring_k + st * stage_units, id_s);
         umma_commit(smem_u32(s.s_full));
-        return true;
     };
-    auto cross = [&](int st, uint32_t ph) {
-        if (!bwait(&s.b_full[st], ph, s, p)) return false;
-        tc_fence_after();
-        mma_ss(tX, gdesc, ring_k + st * stage_units + second, id_s, kd);
+    auto cross = [&](uint32_t st) {
+        mma_ss<kSteps>(tX, gdesc, ring_k + st * stage_units + second, id_s);
         umma_commit(smem_u32(s.x_full));
-        return true;
     };
-    int st = 0;
-    uint32_t ph = 0;
-    ok = ok && score(0, 0u) && cross(0, 0u);
+    uint32_t st = 0, ph = 0;
+    bool ok = wait(s.res_full, 0u) && wait(&s.a_full[0], 0u) && wait(&s.b_full[0], 0u);
+    if (ok) {
+        tc_fence_after();
+        if (elect_one()) {
+            score(0);
+            cross(0);
+        }
+        __syncwarp();
+    }
     for (int x = 0; ok && x < w.n; ++x) {
         const uint32_t par = static_cast<uint32_t>(x) & 1u;
-        int st1 = st + 1;
-        uint32_t ph1 = ph;
-        if (st1 == C::kStages) {
-            st1 = 0;
-            ph1 ^= 1u;
-        }
-        if (x + 1 < w.n) {
-            ok = bwait(s.p_full, par, s, p);  // S has been read
+        const bool more = x + 1 < w.n;
+        const bool wrap = st + 1 == C::kStages;
+        const uint32_t st1 = wrap ? 0u : st + 1u, ph1 = wrap ? ph ^ 1u : ph;
+        if (more) {  // S has been read
+            ok = wait(s.p_full, par) && wait(&s.a_full[st1], ph1);
             if (!ok) break;
             tc_fence_after();
-            if (!(ok = score(st1, ph1))) break;
+            if (elect_one()) score(st1);
+            __syncwarp();
         }
-        ok = bwait(s.ds_full, par, s, p);
+        ok = wait(s.ds_full, par) && (!more || wait(&s.b_full[st1], ph1));
         if (!ok) break;
         tc_fence_after();
-        mma_ts(tQ, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
-        umma_commit(smem_u32(&s.empty[st]));
-        if (x + 1 < w.n && !(ok = cross(st1, ph1))) break;
+        if (elect_one()) {
+            mma_ts<64>(tQ, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
+            umma_commit(smem_u32(&s.empty[st]));
+            if (more) cross(st1);
+        }
+        __syncwarp();
         st = st1;
         ph = ph1;
     }
-    if (ok) umma_commit(smem_u32(s.done));
-    mma_finish(s, p);
+    mma_finish(s, p, ok);
 }
 
-template <int T, int kCh>
+template <int T, int kSteps>
 __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, uint32_t tmem, int warp, int lane) {
     const int quad = warp & 3, half = warp >> 2;
     const MhaShape& sh = p.s;
@@ -852,12 +841,12 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
                  p.nsplit_q > 1 ? p.part_q : nullptr, (w.split * rows + row) * sh.d);
 }
 
-template <int T, int kCh>
+template <int T, int kSteps>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
-    const BwdSmem s = bwd_carve<kCh>(smem_raw);
+    const BwdSmem s = bwd_carve<kSteps>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const QWork w = q_work(p);
@@ -872,10 +861,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    const uint32_t tmem = bwd_begin<kCh>(s, warp);
-    if (warp < kSoftWarps) q_softmax<T, kCh>(p, s, w, tmem, warp, lane);
-    else if (warp == kTmaWarp) q_producer<kCh>(p, s, w, &mq, &mg, &mk, &mv, lane);
-    else if (lane == 0) q_mma<T, kCh>(p, s, w, tmem);
+    const uint32_t tmem = bwd_begin<kSteps>(s, warp);
+    if (warp < kSoftWarps) q_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
+    else if (warp == kTmaWarp) q_producer<kSteps>(p, s, w, &mq, &mg, &mk, &mv, lane);
+    else q_mma<T, kSteps>(p, s, w);
     bwd_end(tmem, warp);
 }
 
@@ -933,28 +922,28 @@ BwdPlan bwd_plan(const MhaShape& s) {
 }
 constexpr size_t kMaximaFloats = 64;  // two words used; keeps what follows aligned
 
-template <int T, int kCh>
+template <int T, int kSteps>
 int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap (&map)[4], const PrepParams& pp,
                const BwdParams& p, cudaStream_t st) {
     static CtxOnce once;
     static std::mutex mu;
-    using C = BwdCfg<kCh>;
+    using C = BwdCfg<kSteps>;
     {
         int dev;
         VAE_CUDA_CHECK(cudaGetDevice(&dev));
         std::lock_guard<std::mutex> lk(mu);
         if (!once.done(dev)) {
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dkv_kernel<T, kCh>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dq_kernel<T, kCh>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dkv_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dq_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
             once.mark(dev);
         }
     }
     if (T == VAE_F16) VAE_CUDA_CHECK(cudaMemsetAsync(pp.maxima, 0, 2 * sizeof(unsigned), st));
     const long long prep = f.row_tiles + (T == VAE_F16 ? f.key_tiles : 0);
     VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
-    VAE_CUDA_CHECK(launch_kernel(mha_dkv_kernel<T, kCh>, dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), C::kSmem,
+    VAE_CUDA_CHECK(launch_kernel(mha_dkv_kernel<T, kSteps>, dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), C::kSmem,
                                  st, map[0], map[1], map[2], map[3], p));
-    VAE_CUDA_CHECK(launch_kernel(mha_dq_kernel<T, kCh>, dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), C::kSmem,
+    VAE_CUDA_CHECK(launch_kernel(mha_dq_kernel<T, kSteps>, dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), C::kSmem,
                                  st, map[0], map[1], map[2], map[3], p));
     const MhaShape& s = p.s;
     if (f.nsplit_k > 1) {
@@ -1026,9 +1015,10 @@ int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout
     p.status = device_status_ptr();
     p.timeout_ns = wait_timeout_ns();
     if (p.status == nullptr) return VAE_ERR_CUDA;
-    if (a->type == VAE_F16)
-        return s.d > 64 ? bwd_launch<VAE_F16, 2>(a, f, map, pp, p, st) : bwd_launch<VAE_F16, 1>(a, f, map, pp, p, st);
-    return s.d > 64 ? bwd_launch<VAE_BF16, 2>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 1>(a, f, map, pp, p, st);
+    const bool h = a->type == VAE_F16;
+    if (s.d <= 64) return h ? bwd_launch<VAE_F16, 4>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 4>(a, f, map, pp, p, st);
+    if (s.d <= 96) return h ? bwd_launch<VAE_F16, 6>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 6>(a, f, map, pp, p, st);
+    return h ? bwd_launch<VAE_F16, 8>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 8>(a, f, map, pp, p, st);
 }
 
 }  // namespace vae
