@@ -468,23 +468,31 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
         const bool more = x + 1 < w.n;
         const bool wrap = st + 1 == C::kStages;
         const uint32_t st1 = wrap ? 0u : st + 1u, ph1 = wrap ? ph ^ 1u : ph;
-        ok = wait(s.p_full, par) && (!more || wait(&s.a_full[st1], ph1));
+        ok = wait(s.p_full, par);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {
-            mma_ts<64>(tV, tS, ring_m + st * stage_units + second, id_o, x != 0 ? 1u : 0u);
-            if (more) score(st1);
-        }
+        if (elect_one()) mma_ts<64>(tV, tS, ring_m + st * stage_units + second, id_o, x != 0 ? 1u : 0u);
         __syncwarp();
-        ok = wait(s.ds_full, par) && (!more || wait(&s.b_full[st1], ph1));
+        if (more) {
+            ok = wait(&s.a_full[st1], ph1);
+            if (!ok) break;
+            if (elect_one()) score(st1);
+            __syncwarp();
+        }
+        ok = wait(s.ds_full, par);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
             mma_ts<64>(tK, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
             umma_commit(smem_u32(&s.empty[st]));
-            if (more) cross(st1);
         }
         __syncwarp();
+        if (more) {
+            ok = wait(&s.b_full[st1], ph1);
+            if (!ok) break;
+            if (elect_one()) cross(st1);
+            __syncwarp();
+        }
         st = st1;
         ph = ph1;
     }
@@ -752,15 +760,20 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
             if (elect_one()) score(st1);
             __syncwarp();
         }
-        ok = wait(s.ds_full, par) && (!more || wait(&s.b_full[st1], ph1));
+        ok = wait(s.ds_full, par);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
             mma_ts<64>(tQ, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
             umma_commit(smem_u32(&s.empty[st]));
-            if (more) cross(st1);
         }
         __syncwarp();
+        if (more) {
+            ok = wait(&s.b_full[st1], ph1);
+            if (!ok) break;
+            if (elect_one()) cross(st1);
+            __syncwarp();
+        }
         st = st1;
         ph = ph1;
     }
