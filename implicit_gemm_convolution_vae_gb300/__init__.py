@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -414,93 +415,122 @@ def mid_attention(x, norm_kind: int, gamma, beta, wq, bq, wk, bk, wv, bv, wo, bo
 
 
 # ───────────────────────── operators on latent tokens ─────────────────────────
+#
+# Small calls are bound by what happens on the host, so this part builds no
+# temporary ctypes objects and asks PyTorch for each thing once.
 
-def _type(t, name):
-    """The C ABI's element type of a tensor or torch dtype."""
-    import torch
-    dt = t if isinstance(t, torch.dtype) else t.dtype
-    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dt)
+_DTYPES = None  # torch dtype -> the C ABI's element type
+
+
+def _type(dt, name):
+    """The C ABI's element type of a torch dtype."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    code = _DTYPES.get(dt)
     if code is None:
         raise VaeError(-1, f"{name} must be float32, float16 or bfloat16, got {dt}")
     return code
 
 
-class _On:
-    """For a call: checks that ``tensors`` (a dict by name) share a device, makes it the current one,
-    and ``stream``, where one is given, the current stream, so that what the call allocates and
-    fills belongs to the stream that it runs on."""
+def _device_of(named):
+    """The index of the device that the given tensors (pairs of a name and a tensor or None) share."""
+    index = None
+    for name, t in named:
+        if t is not None:
+            i = t.get_device()
+            if i != index:
+                if i < 0:
+                    raise VaeError(-1, f"{name} must be a CUDA tensor")
+                if index is not None:
+                    raise VaeError(-1, f"{name} is on cuda:{i}, the others on cuda:{index}")
+                index = i
+    return index
 
-    def __init__(self, tensors, stream):
-        first = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise VaeError(-1, f"{name} must be a CUDA tensor")
-            if first is None:
-                first = t.device
-            elif t.device != first:
-                raise VaeError(-1, f"{name} is on {t.device}, the others on {first}")
-        self.index, self.stream = first.index, None
-        if stream is not None:
-            import torch
-            if stream.device.index != self.index:
-                raise VaeError(-1, f"the stream is on {stream.device}, the tensors on {first}")
-            self.stream = torch.cuda.stream(stream)
+
+class _On:
+    """Makes the tensors' device the current one for a call, and ``stream``, where one is given, the
+    current stream, so that what the call allocates and fills belongs to the stream that it runs on."""
+
+    def __init__(self, index, stream):
+        import torch
+        if stream is not None and stream.device.index != index:
+            raise VaeError(-1, f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        self.device = torch.cuda.device(index)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        import torch
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
+        self.device.__enter__()
         if self.stream is not None:
             self.stream.__enter__()
 
     def __exit__(self, *exc):
         if self.stream is not None:
             self.stream.__exit__(*exc)
-        if self.back != self.index:
-            import torch
-            torch.cuda.set_device(self.back)
+        self.device.__exit__(*exc)
 
 
-def _given(tensors):
+def _call(index, stream, f, *args):
+    """f(*args, raw stream) on the tensors' device and the given or current stream."""
+    from torch import _C
+    if stream is None and index == _C._cuda_getDevice():
+        return f(*args, _C._cuda_getCurrentRawStream(index))
+    with _On(index, stream):
+        return f(*args, _C._cuda_getCurrentRawStream(index))
+
+
+def _given(**tensors):
     for name, t in tensors.items():
         if t is None:
             raise VaeError(-1, f"{name} is needed")
 
 
-def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _tensor(t, name, dtype, shape):
+    """Checks a tensor's type, shape and that it is contiguous."""
+    if t.dtype != dtype:
+        raise VaeError(-1, f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise VaeError(-2, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _rows(t, name):
-    if t.dim() != 2:
-        raise VaeError(-2, f"{name} must have 2 dims, got {t.dim()}")
     if not t.is_contiguous():
         raise VaeError(-1, f"{name} must be contiguous")
+
+
+def _work(workspace):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise VaeError(-1, "workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def layernorm(x, gamma=None, beta=None, eps: float = 1e-6, out_dtype=None, out=None, stream=None):
     """Layer norm of each row of x [m][c] (f32, f16 or bf16); gamma, beta f32 [c] or None.
     The result has ``out_dtype`` (default: x's), or is written into ``out``."""
+    if x is None:
+        _given(x=x)
+    index = _device_of((("x", x), ("gamma", gamma), ("beta", beta), ("out", out)))
+    return _call(index, stream, _layernorm, x, gamma, beta, eps, out_dtype, out)
+
+
+def _layernorm(x, gamma, beta, eps, out_dtype, out, stream):
     import torch
-    _given({"x": x})
-    with _On({"x": x, "gamma": gamma, "beta": beta, "out": out}, stream):
-        _rows(x, "x")
-        m, c = x.shape
-        for t, nm in ((gamma, "gamma"), (beta, "beta")):
-            _need(t, torch.float32, nm, 1)
-            _shape(t, (c,), nm)
-        if out is None:
-            out = torch.empty((m, c), dtype=out_dtype or x.dtype, device=x.device)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise VaeError(-1, f"out must be {out_dtype}, got {out.dtype}")
-        _rows(out, "out")
-        _shape(out, (m, c), "out")
-        _check(lib().vae_layernorm(_ptr(x), _type(x, "x"), m, c, _ptr(gamma), _ptr(beta), float(eps), _ptr(out),
-                                   _type(out, "out"), _stream(stream)))
+    if x.dim() != 2:
+        raise VaeError(-2, f"x must have 2 dims, got {x.dim()}")
+    shape = x.shape
+    m, c = shape
+    _tensor(x, "x", x.dtype, shape)
+    if gamma is not None:
+        _tensor(gamma, "gamma", torch.float32, (c,))
+    if beta is not None:
+        _tensor(beta, "beta", torch.float32, (c,))
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    else:
+        _tensor(out, "out", out_dtype or out.dtype, shape)
+    _check(lib().vae_layernorm(x.data_ptr(), _type(x.dtype, "x"), m, c, _ptr(gamma), _ptr(beta), eps, out.data_ptr(),
+                               _type(out.dtype, "out"), stream))
     return out
 
 
@@ -512,41 +542,43 @@ def layernorm_backward(dy, x, gamma=None, eps: float = 1e-6, weight_grads: bool 
                        dbeta=None, workspace=None, stream=None):
     """The gradient of layernorm at x [m][c] for dy [m][c]: (dx of x's type, dgamma, dbeta f32 [c]);
     with ``weight_grads`` False the last two are None and not computed."""
+    if dy is None or x is None:
+        _given(dy=dy, x=x)
+    index = _device_of((("dy", dy), ("x", x), ("gamma", gamma), ("dx", dx), ("dgamma", dgamma), ("dbeta", dbeta),
+                        ("workspace", workspace)))
+    return _call(index, stream, _layernorm_backward, dy, x, gamma, eps, weight_grads, dx, dgamma, dbeta, workspace)
+
+
+def _layernorm_backward(dy, x, gamma, eps, weight_grads, dx, dgamma, dbeta, workspace, stream):
     import torch
-    _given({"dy": dy, "x": x})
-    with _On({"dy": dy, "x": x, "gamma": gamma, "dx": dx, "dgamma": dgamma, "dbeta": dbeta, "workspace": workspace}, stream):
-        _rows(x, "x")
-        _rows(dy, "dy")
-        m, c = x.shape
-        _shape(dy, (m, c), "dy")
-        if dx is None:
-            dx = torch.empty_like(x)
-        _need(dx, x.dtype, "dx", 2)
-        _shape(dx, (m, c), "dx")
-        if weight_grads:
-            dgamma = torch.empty((c,), dtype=torch.float32, device=x.device) if dgamma is None else dgamma
-            dbeta = torch.empty((c,), dtype=torch.float32, device=x.device) if dbeta is None else dbeta
-            if workspace is None:
-                workspace = torch.empty(max(layernorm_backward_workspace_bytes(m, c), 16), dtype=torch.uint8,
-                                        device=x.device)
-        elif dgamma is not None or dbeta is not None:
-            raise VaeError(-1, "dgamma and dbeta need weight_grads")
-        for t, nm in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")):
-            _need(t, torch.float32, nm, 1)
-            _shape(t, (c,), nm)
-        _check(lib().vae_layernorm_backward(_ptr(dy), _type(dy, "dy"), _ptr(x), _type(x, "x"), m, c, _ptr(gamma),
-                                            float(eps), _ptr(dx), _ptr(dgamma), _ptr(dbeta), *_work(workspace),
-                                            _stream(stream)))
+    if x.dim() != 2:
+        raise VaeError(-2, f"x must have 2 dims, got {x.dim()}")
+    shape = x.shape
+    m, c = shape
+    _tensor(x, "x", x.dtype, shape)
+    _tensor(dy, "dy", dy.dtype, shape)
+    if gamma is not None:
+        _tensor(gamma, "gamma", torch.float32, (c,))
+    if dx is None:
+        dx = torch.empty_like(x)
+    else:
+        _tensor(dx, "dx", x.dtype, shape)
+    if weight_grads:
+        if dgamma is None and dbeta is None:
+            dgamma, dbeta = torch.empty((2, (c + 3) // 4 * 4), dtype=torch.float32, device=x.device)[:, :c]
+        dgamma = torch.empty((c,), dtype=torch.float32, device=x.device) if dgamma is None else dgamma
+        dbeta = torch.empty((c,), dtype=torch.float32, device=x.device) if dbeta is None else dbeta
+        _tensor(dgamma, "dgamma", torch.float32, (c,))
+        _tensor(dbeta, "dbeta", torch.float32, (c,))
+        if workspace is None:
+            workspace = torch.empty(max(lib().vae_layernorm_backward_workspace_bytes(m, c), 16), dtype=torch.uint8,
+                                    device=x.device)
+    elif dgamma is not None or dbeta is not None:
+        raise VaeError(-1, "dgamma and dbeta need weight_grads")
+    _check(lib().vae_layernorm_backward(dy.data_ptr(), _type(dy.dtype, "dy"), x.data_ptr(), _type(x.dtype, "x"), m, c,
+                                        _ptr(gamma), eps, dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), *_work(workspace),
+                                        stream))
     return dx, dgamma, dbeta
-
-
-def _work(workspace):
-    """(pointer, bytes) of a workspace tensor or None."""
-    if workspace is None:
-        return None, 0
-    if not workspace.is_contiguous():
-        raise VaeError(-1, "workspace must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 class _RopePlan(ctypes.Structure):
@@ -564,90 +596,105 @@ class RopePlan:
         dims = (_I * max(1, len(self.axes)))(*self.axes)
         _check(lib().vae_rope_plan_init(ctypes.byref(self._plan), len(self.axes), dims, float(theta),
                                         int(bool(interleaved))))
+        self._at = ctypes.addressof(self._plan)
+
+
+_STRIDES = struct.Struct("=3q")
 
 
 def _strides3(t, name):
-    """{batch, token, head} strides of a [b][n][heads][d] tensor whose channels are contiguous."""
-    if t.stride(3) != 1 and t.shape[3] > 1:
+    """The {batch, token, head} strides of a [b][n][heads][d] tensor whose channels are contiguous."""
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
         raise VaeError(-1, f"{name}'s last dim must be contiguous")
-    return (ctypes.c_longlong * 3)(t.stride(0), t.stride(1), t.stride(2))
+    return st[:3]
 
 
 def rope(x, positions, plan: RopePlan, inverse: bool = False, out=None, stream=None):
     """Turns the pairs of x [b][s][h][d] (strides free, channels contiguous) by their angles at
     ``positions`` [s][axes] or [b][s][axes] (f32 or int32); ``inverse`` turns back (the gradient).
     ``out`` may be x."""
+    if x is None or positions is None or plan is None:
+        _given(x=x, positions=positions, plan=plan)
+    index = _device_of((("x", x), ("positions", positions), ("out", out)))
+    return _call(index, stream, _rope, x, positions, plan, inverse, out)
+
+
+def _rope(x, positions, plan, inverse, out, stream):
     import torch
-    _given({"x": x, "positions": positions})
-    with _On({"x": x, "positions": positions, "out": out}, stream):
-        if x.dim() != 4:
-            raise VaeError(-2, f"x must have 4 dims, got {x.dim()}")
-        b, s, h, d = x.shape
-        if positions.dtype not in (torch.float32, torch.int32):
-            raise VaeError(-1, f"positions must be float32 or int32, got {positions.dtype}")
-        if not positions.is_contiguous():
-            raise VaeError(-1, "positions must be contiguous")
-        na = len(plan.axes)
-        pb = positions.shape[0] if positions.dim() == 3 else 1
-        _shape(positions, (s, na) if positions.dim() == 2 else (pb, s, na), "positions")
-        if out is None:
-            out = torch.empty((b, s, h, d), dtype=x.dtype, device=x.device)
-        _shape(out, (b, s, h, d), "out")
-        if out.dtype != x.dtype:
-            raise VaeError(-1, f"out must be {x.dtype}, got {out.dtype}")
-        _check(lib().vae_rope(_ptr(x), _type(x, "x"), b, s, h, d, _strides3(x, "x"), _ptr(positions),
-                              int(positions.dtype == torch.int32), pb, ctypes.byref(plan._plan), int(bool(inverse)),
-                              _ptr(out), _strides3(out, "out"), _stream(stream)))
+    if x.dim() != 4:
+        raise VaeError(-2, f"x must have 4 dims, got {x.dim()}")
+    shape = x.shape
+    b, s, h, d = shape
+    ints = positions.dtype == torch.int32
+    if not ints and positions.dtype != torch.float32:
+        raise VaeError(-1, f"positions must be float32 or int32, got {positions.dtype}")
+    pb = positions.shape[0] if positions.dim() == 3 else 1
+    na = len(plan.axes)
+    _tensor(positions, "positions", positions.dtype, (pb, s, na) if positions.dim() == 3 else (s, na))
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif out.shape != shape:
+        raise VaeError(-2, f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    elif out.dtype != x.dtype:
+        raise VaeError(-1, f"out must be {x.dtype}, got {out.dtype}")
+    _check(lib().vae_rope(x.data_ptr(), _type(x.dtype, "x"), b, s, h, d, _STRIDES.pack(*_strides3(x, "x")),
+                          positions.data_ptr(), ints, pb, plan._at, bool(inverse), out.data_ptr(),
+                          _STRIDES.pack(*_strides3(out, "out")), stream))
     return out
 
 
-class AttentionDesc(ctypes.Structure):
-    _fields_ = [("type", _I), ("b", _I), ("sq", _I), ("sk", _I), ("hq", _I), ("hkv", _I), ("d", _I), ("scale", _F),
-                ("block", _I), ("q_len", _P), ("k_len", _P)] + \
-               [(n + "_stride", ctypes.c_longlong * 3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")]
+# struct vae_attention_desc: type .. d, scale, block (and its padding), the two lengths, eight times three strides
+_DESC = struct.Struct("=7ifi4x2Q24q")
+_NO_STRIDES = (0,) * 12
 
 
-def _attention_desc(q, k, v, scale, q_len, k_len, block):
-    """The desc of a call without the outputs' strides; checks the tensors' shapes and types."""
+def _attention_args(q, k, v, scale, q_len, k_len, block):
+    """(the desc's fields up to v's strides, b, sq, hq) of a call; checks q, k, v and the lengths."""
     import torch
+    dtype = q.dtype
     for t, nm in ((q, "q"), (k, "k"), (v, "v")):
         if t.dim() != 4:
             raise VaeError(-2, f"{nm} must have 4 dims, got {t.dim()}")
-        if t.dtype != q.dtype:
-            raise VaeError(-1, f"{nm} must be {q.dtype}, got {t.dtype}")
+        if t.dtype != dtype:
+            raise VaeError(-1, f"{nm} must be {dtype}, got {t.dtype}")
     b, sq, hq, d = q.shape
-    sk, hkv = k.shape[1], k.shape[2]
-    _shape(k, (b, sk, hkv, d), "k")
-    _shape(v, (b, sk, hkv, d), "v")
-    for t, nm in ((q_len, "q_len"), (k_len, "k_len")):
-        _need(t, torch.int32, nm, 1)
-        _shape(t, (b,), nm)
-    a = AttentionDesc(_type(q, "q"), b, sq, sk, hq, hkv, d, 1.0 / d ** 0.5 if scale is None else float(scale),
-                      int(block), _ptr(q_len), _ptr(k_len))
-    a.q_stride, a.k_stride, a.v_stride = _strides3(q, "q"), _strides3(k, "k"), _strides3(v, "v")
-    return a
+    kshape = k.shape
+    _, sk, hkv, _ = kshape
+    if kshape[0] != b or kshape[3] != d:
+        raise VaeError(-2, f"k must be {(b, sk, hkv, d)}, got {tuple(kshape)}")
+    if v.shape != kshape:
+        raise VaeError(-2, f"v must be {tuple(kshape)}, got {tuple(v.shape)}")
+    if q_len is not None:
+        _tensor(q_len, "q_len", torch.int32, (b,))
+    if k_len is not None:
+        _tensor(k_len, "k_len", torch.int32, (b,))
+    return (_type(dtype, "q"), b, sq, sk, hq, hkv, d, 1.0 / d ** 0.5 if scale is None else scale, block,
+            0 if q_len is None else q_len.data_ptr(), 0 if k_len is None else k_len.data_ptr(), *_strides3(q, "q"),
+            *_strides3(k, "k"), *_strides3(v, "v"))
 
 
-def _like(t, ref, shape, name, lens):
-    """``t`` checked, or a new tensor (zeros where ``lens`` leaves rows unwritten)."""
+def _like(t, ref, name, lens):
+    """``t`` checked against ``ref``'s shape and type, or a new dense tensor (zeros where ``lens`` leaves
+    rows unwritten)."""
     import torch
     if t is None:
-        return (torch.empty if lens is None else torch.zeros)(shape, dtype=ref.dtype, device=ref.device)
-    _shape(t, shape, name)
+        return (torch.empty if lens is None else torch.zeros)(ref.shape, dtype=ref.dtype, device=ref.device)
+    if t.shape != ref.shape:
+        raise VaeError(-2, f"{name} must be {tuple(ref.shape)}, got {tuple(t.shape)}")
     if t.dtype != ref.dtype:
         raise VaeError(-1, f"{name} must be {ref.dtype}, got {t.dtype}")
     return t
 
 
-def _dense(b, n, h, d):
-    return (ctypes.c_longlong * 3)(n * h * d, h * d, d)
+def _dense(n, h, d):
+    return n * h * d, h * d, d
 
 
 def attention_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
-    a = AttentionDesc(1, b, sq, sk, hq, hkv, d, 1.0, block)
-    a.q_stride = a.o_stride = _dense(b, sq, hq, d)
-    a.k_stride = a.v_stride = _dense(b, sk, hkv, d)
-    return int(lib().vae_attention_workspace_bytes(ctypes.byref(a)))
+    q, k = _dense(sq, hq, d), _dense(sk, hkv, d)
+    return int(lib().vae_attention_workspace_bytes(_DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, *q, *k, *k, *q,
+                                                              *_NO_STRIDES)))
 
 
 def attention(q, k, v, scale: Optional[float] = None, q_len=None, k_len=None, block: int = 0, out=None, lse=None,
@@ -657,54 +704,70 @@ def attention(q, k, v, scale: Optional[float] = None, q_len=None, k_len=None, bl
     batch. block 0: every valid key; block > 0: the keys of the query's own block of that many
     positions and of the earlier ones (1: causal). Returns (o, lse f32 [b][hq][sq]); rows behind q_len
     are left as they were in ``out`` and ``lse``, 0 and -inf in new ones."""
+    if q is None or k is None or v is None:
+        _given(q=q, k=k, v=v)
+    index = _device_of((("q", q), ("k", k), ("v", v), ("q_len", q_len), ("k_len", k_len), ("out", out), ("lse", lse),
+                        ("workspace", workspace)))
+    return _call(index, stream, _attention, q, k, v, scale, q_len, k_len, block, out, lse, workspace)
+
+
+def _attention(q, k, v, scale, q_len, k_len, block, out, lse, workspace, stream):
     import torch
-    _given({"q": q, "k": k, "v": v})
-    with _On({"q": q, "k": k, "v": v, "q_len": q_len, "k_len": k_len, "out": out, "lse": lse,
-                  "workspace": workspace}, stream):
-        a = _attention_desc(q, k, v, scale, q_len, k_len, block)
-        out = _like(out, q, (a.b, a.sq, a.hq, a.d), "out", q_len)
-        a.o_stride = _strides3(out, "out")
-        if lse is None:
-            lse = torch.empty((a.b, a.hq, a.sq), dtype=torch.float32, device=q.device) if q_len is None else \
-                torch.full((a.b, a.hq, a.sq), -float("inf"), dtype=torch.float32, device=q.device)
-        _need(lse, torch.float32, "lse", 3)
-        _shape(lse, (a.b, a.hq, a.sq), "lse")
-        if workspace is None:
-            nb = lib().vae_attention_workspace_bytes(ctypes.byref(a))
-            workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
-        _check(lib().vae_attention(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                   *_work(workspace), _stream(stream)))
+    args = _attention_args(q, k, v, scale, q_len, k_len, block)
+    b, sq, hq, _ = q.shape
+    out = _like(out, q, "out", q_len)
+    if lse is not None:
+        _tensor(lse, "lse", torch.float32, (b, hq, sq))
+    elif q_len is None:
+        lse = torch.empty((b, hq, sq), dtype=torch.float32, device=q.device)
+    else:
+        lse = torch.full((b, hq, sq), -float("inf"), dtype=torch.float32, device=q.device)
+    desc = _DESC.pack(*args, *_strides3(out, "out"), *_NO_STRIDES)
+    L = lib()
+    if workspace is None:
+        nb = L.vae_attention_workspace_bytes(desc)
+        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    _check(L.vae_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                           *_work(workspace), stream))
     return out, lse
 
 
 def attention_backward_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
-    a = AttentionDesc(1, b, sq, sk, hq, hkv, d, 1.0, block)
-    a.q_stride = a.o_stride = a.do_stride = a.dq_stride = _dense(b, sq, hq, d)
-    a.k_stride = a.v_stride = a.dk_stride = a.dv_stride = _dense(b, sk, hkv, d)
-    return int(lib().vae_attention_backward_workspace_bytes(ctypes.byref(a)))
+    q, k = _dense(sq, hq, d), _dense(sk, hkv, d)
+    return int(lib().vae_attention_backward_workspace_bytes(
+        _DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, *q, *k, *k, *q, *q, *q, *k, *k)))
 
 
 def attention_backward(do, q, k, v, o, lse, scale: Optional[float] = None, q_len=None, k_len=None, block: int = 0,
                        dq=None, dk=None, dv=None, workspace=None, stream=None):
     """The gradient of attention for do [b][sq][hq][d], from o and lse of the same call: (dq, dk, dv).
     Rows behind q_len and k_len are left as they were, 0 in new tensors."""
+    if do is None or q is None or k is None or v is None or o is None or lse is None:
+        _given(do=do, q=q, k=k, v=v, o=o, lse=lse)
+    index = _device_of((("do", do), ("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse), ("q_len", q_len),
+                        ("k_len", k_len), ("dq", dq), ("dk", dk), ("dv", dv), ("workspace", workspace)))
+    return _call(index, stream, _attention_backward, do, q, k, v, o, lse, scale, q_len, k_len, block, dq, dk, dv,
+                 workspace)
+
+
+def _attention_backward(do, q, k, v, o, lse, scale, q_len, k_len, block, dq, dk, dv, workspace, stream):
     import torch
-    _given({"do": do, "q": q, "k": k, "v": v, "o": o, "lse": lse})
-    with _On({"do": do, "q": q, "k": k, "v": v, "o": o, "lse": lse, "q_len": q_len, "k_len": k_len, "dq": dq,
-                  "dk": dk, "dv": dv, "workspace": workspace}, stream):
-        a = _attention_desc(q, k, v, scale, q_len, k_len, block)
-        do, o = _like(do, q, q.shape, "do", None), _like(o, q, q.shape, "o", None)
-        _need(lse, torch.float32, "lse", 3)
-        _shape(lse, (a.b, a.hq, a.sq), "lse")
-        dq = _like(dq, q, q.shape, "dq", q_len)
-        dk, dv = _like(dk, k, k.shape, "dk", k_len), _like(dv, k, k.shape, "dv", k_len)
-        for nm, t in (("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
-            setattr(a, nm + "_stride", _strides3(t, nm))
-        if workspace is None:
-            nb = lib().vae_attention_backward_workspace_bytes(ctypes.byref(a))
-            workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
-        _check(lib().vae_attention_backward(ctypes.byref(a), _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
-                                            _ptr(dq), _ptr(dk), _ptr(dv), *_work(workspace), _stream(stream)))
+    args = _attention_args(q, k, v, scale, q_len, k_len, block)
+    b, sq, hq, _ = q.shape
+    _like(do, q, "do", None)
+    _like(o, q, "o", None)
+    _tensor(lse, "lse", torch.float32, (b, hq, sq))
+    dq = _like(dq, q, "dq", q_len)
+    dk, dv = _like(dk, k, "dk", k_len), _like(dv, k, "dv", k_len)
+    desc = _DESC.pack(*args, *_strides3(o, "o"), *_strides3(do, "do"), *_strides3(dq, "dq"), *_strides3(dk, "dk"),
+                      *_strides3(dv, "dv"))
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(max(L.vae_attention_backward_workspace_bytes(desc), 16), dtype=torch.uint8,
+                                device=q.device)
+    _check(L.vae_attention_backward(desc, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *_work(workspace),
+                                    stream))
     return dq, dk, dv
 
 

@@ -87,13 +87,31 @@ def test_rope_refusals(L):
     assert rc(x=FAKE + 1) == -3 and rc(pos=FAKE + 2) == -3
 
 
+class AttentionDesc(ctypes.Structure):
+    """vae_attention_desc as the header declares it."""
+    _fields_ = [(n, ctypes.c_int) for n in ("type", "b", "sq", "sk", "hq", "hkv", "d")] + \
+        [("scale", ctypes.c_float), ("block", ctypes.c_int), ("q_len", ctypes.c_void_p), ("k_len", ctypes.c_void_p)] + \
+        [(n + "_stride", ctypes.c_longlong * 3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")]
+
+
+def test_binding_packs_the_desc_as_declared(L):
+    a = AttentionDesc(2, 3, 4, 5, 6, 7, 8, 0.5, 9, 1 << 40, 1 << 41)
+    for i, n in enumerate(("q", "k", "v", "o", "do", "dq", "dk", "dv")):
+        setattr(a, n + "_stride", (ctypes.c_longlong * 3)(*[(i * 3 + j + 1) << 33 for j in range(3)]))
+    assert bytes(a) == vg._DESC.pack(2, 3, 4, 5, 6, 7, 8, 0.5, 9, 1 << 40, 1 << 41, *[(i + 1) << 33 for i in range(24)])
+
+
+def _dense(b, n, h, d):
+    return (ctypes.c_longlong * 3)(n * h * d, h * d, d)
+
+
 def _desc(**kw):
     b, sq, sk, hq, hkv, d = (kw.pop(k, v) for k, v in (("b", 2), ("sq", 40), ("sk", 50), ("hq", 6), ("hkv", 3), ("d", 64)))
-    a = vg.AttentionDesc(kw.pop("type", F16), b, sq, sk, hq, hkv, d, kw.pop("scale", 0.125), kw.pop("block", 0))
+    a = AttentionDesc(kw.pop("type", F16), b, sq, sk, hq, hkv, d, kw.pop("scale", 0.125), kw.pop("block", 0))
     for n in ("q", "o", "do", "dq"):
-        setattr(a, n + "_stride", vg._dense(b, sq, hq, d))
+        setattr(a, n + "_stride", _dense(b, sq, hq, d))
     for n in ("k", "v", "dk", "dv"):
-        setattr(a, n + "_stride", vg._dense(b, sk, hkv, d))
+        setattr(a, n + "_stride", _dense(b, sk, hkv, d))
     for k, v in kw.items():
         setattr(a, k, (ctypes.c_longlong * 3)(*v))
     return a
