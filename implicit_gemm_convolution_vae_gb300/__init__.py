@@ -419,16 +419,30 @@ def mid_attention(x, norm_kind: int, gamma, beta, wq, bq, wk, bk, wv, bv, wo, bo
 # Small calls are bound by what happens on the host, so this part builds no
 # temporary ctypes objects and asks PyTorch for each thing once.
 
-_DTYPES = None  # torch dtype -> the C ABI's element type
+_T = None  # torch, once a call needs it
+
+
+class _Torch:
+    """What the calls below take from torch, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.torch, self.empty, self.zeros = torch, torch.empty, torch.zeros
+        self.f32, self.i32, self.u8 = torch.float32, torch.int32, torch.uint8
+        self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.types = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _torch():
+    global _T
+    if _T is None:
+        _T = _Torch()
+    return _T
 
 
 def _type(dt, name):
     """The C ABI's element type of a torch dtype."""
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    code = _DTYPES.get(dt)
+    code = _T.types.get(dt)
     if code is None:
         raise VaeError(-1, f"{name} must be float32, float16 or bfloat16, got {dt}")
     return code
@@ -473,11 +487,11 @@ class _On:
 
 def _call(index, stream, f, *args):
     """f(*args, raw stream) on the tensors' device and the given or current stream."""
-    from torch import _C
-    if stream is None and index == _C._cuda_getDevice():
-        return f(*args, _C._cuda_getCurrentRawStream(index))
+    T = _T or _torch()
+    if stream is None and index == T.device():
+        return f(*args, T.stream(index))
     with _On(index, stream):
-        return f(*args, _C._cuda_getCurrentRawStream(index))
+        return f(*args, T.stream(index))
 
 
 def _given(**tensors):
@@ -488,12 +502,13 @@ def _given(**tensors):
 
 def _tensor(t, name, dtype, shape):
     """Checks a tensor's type, shape and that it is contiguous."""
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
         raise VaeError(-1, f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise VaeError(-2, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise VaeError(-1, f"{name} must be contiguous")
+    raise VaeError(-1, f"{name} must be contiguous")
 
 
 def _work(workspace):
@@ -515,18 +530,17 @@ def layernorm(x, gamma=None, beta=None, eps: float = 1e-6, out_dtype=None, out=N
 
 
 def _layernorm(x, gamma, beta, eps, out_dtype, out, stream):
-    import torch
     if x.dim() != 2:
         raise VaeError(-2, f"x must have 2 dims, got {x.dim()}")
     shape = x.shape
     m, c = shape
     _tensor(x, "x", x.dtype, shape)
     if gamma is not None:
-        _tensor(gamma, "gamma", torch.float32, (c,))
+        _tensor(gamma, "gamma", _T.f32, (c,))
     if beta is not None:
-        _tensor(beta, "beta", torch.float32, (c,))
+        _tensor(beta, "beta", _T.f32, (c,))
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = _T.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
     else:
         _tensor(out, "out", out_dtype or out.dtype, shape)
     _check(lib().vae_layernorm(x.data_ptr(), _type(x.dtype, "x"), m, c, _ptr(gamma), _ptr(beta), eps, out.data_ptr(),
@@ -550,7 +564,6 @@ def layernorm_backward(dy, x, gamma=None, eps: float = 1e-6, weight_grads: bool 
 
 
 def _layernorm_backward(dy, x, gamma, eps, weight_grads, dx, dgamma, dbeta, workspace, stream):
-    import torch
     if x.dim() != 2:
         raise VaeError(-2, f"x must have 2 dims, got {x.dim()}")
     shape = x.shape
@@ -558,20 +571,22 @@ def _layernorm_backward(dy, x, gamma, eps, weight_grads, dx, dgamma, dbeta, work
     _tensor(x, "x", x.dtype, shape)
     _tensor(dy, "dy", dy.dtype, shape)
     if gamma is not None:
-        _tensor(gamma, "gamma", torch.float32, (c,))
+        _tensor(gamma, "gamma", _T.f32, (c,))
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = _T.torch.empty_like(x)
     else:
         _tensor(dx, "dx", x.dtype, shape)
     if weight_grads:
-        if dgamma is None and dbeta is None:
-            dgamma, dbeta = torch.empty((2, (c + 3) // 4 * 4), dtype=torch.float32, device=x.device)[:, :c]
-        dgamma = torch.empty((c,), dtype=torch.float32, device=x.device) if dgamma is None else dgamma
-        dbeta = torch.empty((c,), dtype=torch.float32, device=x.device) if dbeta is None else dbeta
-        _tensor(dgamma, "dgamma", torch.float32, (c,))
-        _tensor(dbeta, "dbeta", torch.float32, (c,))
+        if dgamma is None:
+            dgamma = _T.empty((c,), dtype=_T.f32, device=x.device)
+        else:
+            _tensor(dgamma, "dgamma", _T.f32, (c,))
+        if dbeta is None:
+            dbeta = _T.empty((c,), dtype=_T.f32, device=x.device)
+        else:
+            _tensor(dbeta, "dbeta", _T.f32, (c,))
         if workspace is None:
-            workspace = torch.empty(max(lib().vae_layernorm_backward_workspace_bytes(m, c), 16), dtype=torch.uint8,
+            workspace = _T.empty(max(lib().vae_layernorm_backward_workspace_bytes(m, c), 16), dtype=_T.u8,
                                     device=x.device)
     elif dgamma is not None or dbeta is not None:
         raise VaeError(-1, "dgamma and dbeta need weight_grads")
@@ -621,19 +636,18 @@ def rope(x, positions, plan: RopePlan, inverse: bool = False, out=None, stream=N
 
 
 def _rope(x, positions, plan, inverse, out, stream):
-    import torch
     if x.dim() != 4:
         raise VaeError(-2, f"x must have 4 dims, got {x.dim()}")
     shape = x.shape
     b, s, h, d = shape
-    ints = positions.dtype == torch.int32
-    if not ints and positions.dtype != torch.float32:
+    ints = positions.dtype == _T.i32
+    if not ints and positions.dtype != _T.f32:
         raise VaeError(-1, f"positions must be float32 or int32, got {positions.dtype}")
     pb = positions.shape[0] if positions.dim() == 3 else 1
     na = len(plan.axes)
     _tensor(positions, "positions", positions.dtype, (pb, s, na) if positions.dim() == 3 else (s, na))
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _T.empty(shape, dtype=x.dtype, device=x.device)
     elif out.shape != shape:
         raise VaeError(-2, f"out must be {tuple(shape)}, got {tuple(out.shape)}")
     elif out.dtype != x.dtype:
@@ -651,7 +665,6 @@ _NO_STRIDES = (0,) * 12
 
 def _attention_args(q, k, v, scale, q_len, k_len, block):
     """(the desc's fields up to v's strides, b, sq, hq) of a call; checks q, k, v and the lengths."""
-    import torch
     dtype = q.dtype
     for t, nm in ((q, "q"), (k, "k"), (v, "v")):
         if t.dim() != 4:
@@ -666,9 +679,9 @@ def _attention_args(q, k, v, scale, q_len, k_len, block):
     if v.shape != kshape:
         raise VaeError(-2, f"v must be {tuple(kshape)}, got {tuple(v.shape)}")
     if q_len is not None:
-        _tensor(q_len, "q_len", torch.int32, (b,))
+        _tensor(q_len, "q_len", _T.i32, (b,))
     if k_len is not None:
-        _tensor(k_len, "k_len", torch.int32, (b,))
+        _tensor(k_len, "k_len", _T.i32, (b,))
     return (_type(dtype, "q"), b, sq, sk, hq, hkv, d, 1.0 / d ** 0.5 if scale is None else scale, block,
             0 if q_len is None else q_len.data_ptr(), 0 if k_len is None else k_len.data_ptr(), *_strides3(q, "q"),
             *_strides3(k, "k"), *_strides3(v, "v"))
@@ -677,9 +690,8 @@ def _attention_args(q, k, v, scale, q_len, k_len, block):
 def _like(t, ref, name, lens):
     """``t`` checked against ``ref``'s shape and type, or a new dense tensor (zeros where ``lens`` leaves
     rows unwritten)."""
-    import torch
     if t is None:
-        return (torch.empty if lens is None else torch.zeros)(ref.shape, dtype=ref.dtype, device=ref.device)
+        return (_T.empty if lens is None else _T.zeros)(ref.shape, dtype=ref.dtype, device=ref.device)
     if t.shape != ref.shape:
         raise VaeError(-2, f"{name} must be {tuple(ref.shape)}, got {tuple(t.shape)}")
     if t.dtype != ref.dtype:
@@ -712,21 +724,20 @@ def attention(q, k, v, scale: Optional[float] = None, q_len=None, k_len=None, bl
 
 
 def _attention(q, k, v, scale, q_len, k_len, block, out, lse, workspace, stream):
-    import torch
     args = _attention_args(q, k, v, scale, q_len, k_len, block)
     b, sq, hq, _ = q.shape
     out = _like(out, q, "out", q_len)
     if lse is not None:
-        _tensor(lse, "lse", torch.float32, (b, hq, sq))
+        _tensor(lse, "lse", _T.f32, (b, hq, sq))
     elif q_len is None:
-        lse = torch.empty((b, hq, sq), dtype=torch.float32, device=q.device)
+        lse = _T.empty((b, hq, sq), dtype=_T.f32, device=q.device)
     else:
-        lse = torch.full((b, hq, sq), -float("inf"), dtype=torch.float32, device=q.device)
+        lse = _T.torch.full((b, hq, sq), -float("inf"), dtype=_T.f32, device=q.device)
     desc = _DESC.pack(*args, *_strides3(out, "out"), *_NO_STRIDES)
     L = lib()
     if workspace is None:
         nb = L.vae_attention_workspace_bytes(desc)
-        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+        workspace = _T.empty(nb, dtype=_T.u8, device=q.device) if nb else None
     _check(L.vae_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                            *_work(workspace), stream))
     return out, lse
@@ -751,19 +762,18 @@ def attention_backward(do, q, k, v, o, lse, scale: Optional[float] = None, q_len
 
 
 def _attention_backward(do, q, k, v, o, lse, scale, q_len, k_len, block, dq, dk, dv, workspace, stream):
-    import torch
     args = _attention_args(q, k, v, scale, q_len, k_len, block)
     b, sq, hq, _ = q.shape
     _like(do, q, "do", None)
     _like(o, q, "o", None)
-    _tensor(lse, "lse", torch.float32, (b, hq, sq))
+    _tensor(lse, "lse", _T.f32, (b, hq, sq))
     dq = _like(dq, q, "dq", q_len)
     dk, dv = _like(dk, k, "dk", k_len), _like(dv, k, "dv", k_len)
     desc = _DESC.pack(*args, *_strides3(o, "o"), *_strides3(do, "do"), *_strides3(dq, "dq"), *_strides3(dk, "dk"),
                       *_strides3(dv, "dv"))
     L = lib()
     if workspace is None:
-        workspace = torch.empty(max(L.vae_attention_backward_workspace_bytes(desc), 16), dtype=torch.uint8,
+        workspace = _T.empty(max(L.vae_attention_backward_workspace_bytes(desc), 16), dtype=_T.u8,
                                 device=q.device)
     _check(L.vae_attention_backward(desc, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                     lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *_work(workspace),
