@@ -36,6 +36,7 @@ enum : int {
     kWhereSelftest = 7,
     kWhereAttn = 8,
     kWhereFixer = 9,
+    kWhereNorm = 10,
 };
 
 // ───────────────────────────── PTX wrappers ─────────────────────────────

@@ -3,9 +3,15 @@
 // A row is read once into registers, so the two-pass statistics (mean, then
 // the mean square around it) and everything after them cost no further memory
 // traffic: both directions are bound by reading their inputs and writing their
-// output once. Rows of up to 1280 channels belong to one warp (shuffles only);
-// wider ones to a block. Rows whose length is a multiple of eight move in
-// 16-byte vectors, others element by element in the same registers.
+// output once.
+//
+// Ring form (many rows of a multiple of eight channels, up to 5120): one block
+// per SM stays; a row belongs to one, two or four warps, whose next rows are
+// already on the way into shared memory by bulk copies while they work on the
+// last one. Registers then hold one row only and the loads never pause.
+// Plain form (few rows, other lengths): rows of up to 1280 channels belong to
+// one warp, wider ones to a block, loaded straight into registers, in 16-byte
+// vectors where the length is a multiple of eight, else element by element.
 //
 // The gradients of gamma and beta are column sums over all rows: every thread
 // keeps the same columns on every row it meets, so it sums them in registers,
@@ -14,6 +20,7 @@
 // order is fixed, so the sums do not change from call to call.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "vae_types.cuh"
 
@@ -245,6 +252,288 @@ __global__ void __launch_bounds__(kWarp ? kLnBwdWarps * 32 : 512)
     }
 }
 
+// ───────────────────────────── ring form ─────────────────────────────
+
+constexpr int kRingFwdWarps = 16, kRingBwdWarps = 8;  // per block, one block per SM
+constexpr int kRingBlocks = 152;
+constexpr int kRingStages = 4;               // rows of a group in flight, at most
+constexpr size_t kRingSmem = 220 * 1024;
+
+struct LnRing {
+    int m, c, xt, yt, dyt;
+    int nv, wide;         // eights per thread, warps per row (a group)
+    int stages;
+    unsigned row_x, row_dy, stage;  // bytes of a row of x and dy, of a stage
+    unsigned bars;                  // offset of the barriers; gamma and beta lie before them
+    float eps;
+    const void *x, *dy;
+    const float *gamma, *beta;
+    void* out;            // y or dx
+    float* part;
+    DevStatus* status;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ void ln_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ float2 f2(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// Eights tid, tid + T, ... of a row (in shared memory, or gamma / beta there); 0 behind c.
+template <int T, int NV>
+__device__ __forceinline__ void row_in(const uint8_t* p, int c, int tid, int nt, float2 (&v)[NV][4]) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = (tid + k * nt) * 8;
+        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (i < c) load8<T>(reinterpret_cast<const typename Elem<T>::type*>(p) + i, t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = f2(t[2 * e], t[2 * e + 1]);
+    }
+}
+template <int NV>
+__device__ __forceinline__ void row_in(const uint8_t* p, int type, int c, int tid, int nt, float2 (&v)[NV][4]) {
+    if (type == VAE_F32) row_in<VAE_F32, NV>(p, c, tid, nt, v);
+    else if (type == VAE_F16) row_in<VAE_F16, NV>(p, c, tid, nt, v);
+    else row_in<VAE_BF16, NV>(p, c, tid, nt, v);
+}
+template <int T, int NV>
+__device__ __forceinline__ void row_out(void* p, size_t off, int c, int tid, int nt, const float2 (&v)[NV][4]) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = (tid + k * nt) * 8;
+        const float t[8] = {v[k][0].x, v[k][0].y, v[k][1].x, v[k][1].y, v[k][2].x, v[k][2].y, v[k][3].x, v[k][3].y};
+        if (i < c) store8<T>(static_cast<typename Elem<T>::type*>(p) + off + i, t);
+    }
+}
+template <int NV>
+__device__ __forceinline__ void row_out(void* p, int type, size_t off, int c, int tid, int nt, const float2 (&v)[NV][4]) {
+    if (type == VAE_F32) row_out<VAE_F32, NV>(p, off, c, tid, nt, v);
+    else if (type == VAE_F16) row_out<VAE_F16, NV>(p, off, c, tid, nt, v);
+    else row_out<VAE_BF16, NV>(p, off, c, tid, nt, v);
+}
+
+// The warps of a group meet (a barrier of the group's own).
+__device__ __forceinline__ void group_sync(int group, int wide) {
+    if (wide == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(wide * 32) : "memory");
+}
+// Two sums over the group's threads; `red`: [2][wide] floats of this group and call site.
+__device__ __forceinline__ float2 group_sum2(float2 v, float2* red, int group, int wide, int part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = add2(v, f2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+    if (wide > 1) {
+        if ((threadIdx.x & 31) == 0) red[part] = v;
+        group_sync(group, wide);
+        v = red[0];
+        for (int i = 1; i < wide; ++i) v = add2(v, red[i]);
+    }
+    return v;
+}
+__device__ __forceinline__ float group_sum(float x, float2* red, int group, int wide, int part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (wide > 1) {
+        if ((threadIdx.x & 31) == 0) red[part].x = x;
+        group_sync(group, wide);
+        x = red[0].x;
+        for (int i = 1; i < wide; ++i) x += red[i].x;
+    }
+    return x;
+}
+
+// Rows g, g + G, ... of all groups g < G of the grid. kBwd: the gradient.
+template <int NV, bool kBwd>
+__global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1) ln_ring_kernel(const LnRing p) {
+    constexpr int kWarps = kBwd ? kRingBwdWarps : kRingFwdWarps;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 red[3][kWarps];
+    __shared__ int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wide = p.wide, group = warp / wide, part = warp % wide, groups = kWarps / wide;
+    const int nt = wide * 32, tid = part * 32 + lane, c = p.c;
+    uint8_t* ring = smem + static_cast<size_t>(group) * p.stages * p.stage;
+    const float* gam = reinterpret_cast<const float*>(smem + static_cast<size_t>(groups) * p.stages * p.stage);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bars) + group * kRingStages;
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (tid == 0)
+        for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&full[i]), 1u);
+    fence_mbar_init();
+    pdl_wait();
+    const bool has_g = p.gamma != nullptr, has_b = !kBwd && p.beta != nullptr;
+    if (has_g || has_b) {
+        float* w = const_cast<float*>(gam);
+        for (int i = threadIdx.x; i < c; i += kWarps * 32) {
+            if (has_g) w[i] = p.gamma[i];
+            if (has_b) w[c + i] = p.beta[i];
+        }
+    }
+    __syncthreads();
+    const int all = static_cast<int>(gridDim.x) * groups, first = static_cast<int>(blockIdx.x) * groups + group;
+    const int n = first < p.m ? (p.m - 1 - first) / all + 1 : 0;  // this group's rows
+    auto fetch = [&](int k) {  // one lane of the group: the group's row k into stage k % stages
+        const size_t row = static_cast<size_t>(first) + static_cast<size_t>(k) * all;
+        const int st = k % p.stages;
+        const uint32_t bar = smem_u32(&full[st]), dst = smem_u32(ring + static_cast<size_t>(st) * p.stage);
+        mbar_arrive_expect_tx(bar, p.row_x + p.row_dy);
+        ln_bulk(dst, static_cast<const uint8_t*>(p.x) + row * p.row_x, p.row_x, bar);
+        if (kBwd) ln_bulk(dst + p.row_x, static_cast<const uint8_t*>(p.dy) + row * p.row_dy, p.row_dy, bar);
+    };
+    if (tid == 0)
+        for (int k = 0; k < n && k < p.stages; ++k) fetch(k);
+    float2 dg[NV][4], db[NV][4];
+    if constexpr (kBwd) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dg[k][e] = db[k][e] = f2(0.f, 0.f);
+    }
+    const float inv_c = 1.f / static_cast<float>(c);
+    bool ok = true;
+    int st = 0, late = 0;
+    uint32_t ph = 0;
+    for (int k = 0; k < n; ++k) {
+        // (a group whose wait ran out goes on through its barriers, but stores nothing)
+        if (ok && !warp_all(mbar_wait(smem_u32(&full[st]), ph, &abort_flag, p.timeout_ns, p.status, kWhereNorm))) {
+            ok = false;
+            late = k;
+        }
+        const uint8_t* src = ring + static_cast<size_t>(st) * p.stage;
+        float2 v[NV][4], g[NV][4];
+        row_in<NV>(src, p.xt, c, tid, nt, v);
+        if constexpr (kBwd) row_in<NV>(src + p.row_x, p.dyt, c, tid, nt, g);
+        float2 s = f2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s = add2(s, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
+        const float mean = group_sum(s.x + s.y, &red[0][group * wide], group, wide, part) * inv_c;
+        // every thread of the group has its part of the row in registers (wide > 1: the barrier in the sum)
+        if (wide == 1) __syncwarp();
+        if (tid == 0 && ok && k + p.stages < n) fetch(k + p.stages);
+        if (++st == p.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+        const float2 mm = f2(-mean, -mean);
+        s = f2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = (tid + i * nt) * 8 < c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[i][e] = in ? add2(v[i][e], mm) : f2(0.f, 0.f);
+                s = fma2(v[i][e], v[i][e], s);
+            }
+        }
+        const float rstd = 1.f / sqrtf(group_sum(s.x + s.y, &red[1][group * wide], group, wide, part) * inv_c + p.eps);
+        const float2 r2 = f2(rstd, rstd);
+        const size_t off = (static_cast<size_t>(first) + static_cast<size_t>(k) * all) * c;
+        if constexpr (!kBwd) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = mul2(v[i][e], r2);
+            if (has_g) {
+                row_in<VAE_F32, NV>(reinterpret_cast<const uint8_t*>(gam), c, tid, nt, g);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][e] = mul2(v[i][e], g[i][e]);
+            }
+            if (has_b) {
+                row_in<VAE_F32, NV>(reinterpret_cast<const uint8_t*>(gam + c), c, tid, nt, g);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][e] = add2(v[i][e], g[i][e]);
+            }
+            if (ok) row_out<NV>(p.out, p.yt, off, c, tid, nt, v);
+        } else {
+            float2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+                const int at = (tid + i * nt) * 8;
+                if (has_g && at < c) load8<VAE_F32>(gam + at, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dg[i][e] = fma2(mul2(g[i][e], r2), v[i][e], dg[i][e]);
+                    db[i][e] = add2(db[i][e], g[i][e]);
+                    g[i][e] = mul2(g[i][e], f2(w[2 * e], w[2 * e + 1]));
+                    s1 = add2(s1, g[i][e]);
+                    s2 = fma2(g[i][e], v[i][e], s2);
+                }
+            }
+            const float2 sums = group_sum2(f2(s1.x + s1.y, s2.x + s2.y), &red[2][group * wide], group, wide, part);
+            // dx = rstd (g - mean(g) - n mean(g n)), n = rstd v
+            const float k1 = -rstd * sums.x * inv_c, k2 = -rstd * rstd * rstd * sums.y * inv_c;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = fma2(g[i][e], r2, fma2(v[i][e], f2(k2, k2), f2(k1, k1)));
+            if (ok) row_out<NV>(p.out, p.xt, off, c, tid, nt, v);
+        }
+    }
+    // Every copy lands before the block may exit (after a time-out: the rows that were fetched and not met).
+    if (!ok && tid == 0) {
+        int never = 0;
+        for (int k = late; k < n && k < late + p.stages; ++k)
+            (void)mbar_wait(smem_u32(&full[k % p.stages]), static_cast<uint32_t>(k / p.stages) & 1u, &never, p.timeout_ns,
+                            p.status, kWhereDrain);
+    }
+    if constexpr (kBwd) {
+        if (p.part == nullptr) return;
+        // the groups' column sums, one group after another, over the ring
+        float* cols = reinterpret_cast<float*>(smem);
+        __syncthreads();
+        for (int u = 0; u < groups; ++u) {
+            if (group == u) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = (tid + i * nt) * 8 + 2 * e;
+                        if (at < c) {
+                            float2* a = reinterpret_cast<float2*>(cols + at);
+                            float2* b = reinterpret_cast<float2*>(cols + c + at);
+                            *a = u == 0 ? dg[i][e] : add2(*a, dg[i][e]);
+                            *b = u == 0 ? db[i][e] : add2(*b, db[i][e]);
+                        }
+                    }
+            }
+            __syncthreads();
+        }
+        float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * c;
+        for (int i = threadIdx.x; i < 2 * c; i += kWarps * 32) out[i] = cols[i];
+    }
+}
+
 // out[0 .. c) = sum over the blocks' partial rows, dgamma then dbeta: 32
 // columns x 8 slices of blocks per thread block, the slices joined in order.
 __global__ void __launch_bounds__(256) ln_cols_kernel(const float* __restrict__ part, int nblk, int c,
@@ -283,6 +572,65 @@ LnPlan ln_plan(int c) {
     }
     return p;
 }
+// The ring form's plan for rows of x (and dy: backward); false where the plain
+// form is used: lengths that are no multiple of eight or over 5120, or so few
+// rows that a group would not have two.
+bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, bool weights, LnRing* r) {
+    if (c % 8 != 0 || c > 5120) return false;
+    const int warps = backward ? kRingBwdWarps : kRingFwdWarps;
+    r->wide = c <= 1280 ? 1 : (c <= 2560 ? 2 : 4);
+    const int groups = warps / r->wide;
+    if (m < 2 * kRingBlocks * groups) return false;
+    r->nv = (c / 8 + r->wide * 32 - 1) / (r->wide * 32);
+    r->row_x = static_cast<unsigned>(c * type_size(xt));
+    r->row_dy = backward ? static_cast<unsigned>(c * type_size(dyt)) : 0u;
+    r->stage = r->row_x + r->row_dy;  // (multiples of 16 bytes)
+    const size_t consts = static_cast<size_t>(c) * (backward ? 4 : 8), bars = static_cast<size_t>(warps) * kRingStages * 8;
+    const size_t left = kRingSmem - consts - bars;
+    r->stages = static_cast<int>(std::min<size_t>(kRingStages, left / (static_cast<size_t>(groups) * r->stage)));
+    if (r->stages < 2) return false;
+    const size_t ring = static_cast<size_t>(groups) * r->stages * r->stage;
+    if (weights && ring < static_cast<size_t>(c) * 8) return false;  // (the column sums lie over the ring)
+    r->bars = static_cast<unsigned>(ring + consts);
+    r->m = m;
+    r->c = c;
+    r->xt = xt;
+    r->dyt = dyt;
+    return true;
+}
+size_t ln_ring_smem(const LnRing& r) { return r.bars + static_cast<size_t>(kRingFwdWarps) * kRingStages * 8; }
+
+template <bool kBwd>
+int ln_ring_run(LnRing& r, cudaStream_t st) {
+    r.status = device_status_ptr();
+    r.timeout_ns = wait_timeout_ns();
+    if (r.status == nullptr) return VAE_ERR_CUDA;
+    const auto go = [&](auto kernel, CtxOnce& once) -> int {
+        static std::mutex mu;
+        {
+            int dev;
+            VAE_CUDA_CHECK(cudaGetDevice(&dev));
+            std::lock_guard<std::mutex> lk(mu);
+            if (!once.done(dev)) {
+                VAE_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    static_cast<int>(kRingSmem + 1024)));
+                once.mark(dev);
+            }
+        }
+        VAE_CUDA_CHECK(launch_kernel(kernel, dim3(kRingBlocks), dim3((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32),
+                                     ln_ring_smem(r), st, static_cast<const LnRing&>(r)));
+        return VAE_OK;
+    };
+    static CtxOnce once[5];
+    switch (r.nv) {
+        case 1: return go(ln_ring_kernel<1, kBwd>, once[0]);
+        case 2: return go(ln_ring_kernel<2, kBwd>, once[1]);
+        case 3: return go(ln_ring_kernel<3, kBwd>, once[2]);
+        case 4: return go(ln_ring_kernel<4, kBwd>, once[3]);
+        default: return go(ln_ring_kernel<5, kBwd>, once[4]);
+    }
+}
+
 int ln_bwd_grid(int m, int c) {
     const LnPlan p = ln_plan(c);
     const int rows = p.warp ? (m - 1) / kLnBwdWarps + 1 : m;
@@ -333,6 +681,16 @@ int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamm
     if (!aligned16(x_dev) || !aligned16(y_dev) || !aligned16(gamma_dev) || !aligned16(beta_dev))
         return set_error(VAE_ERR_ALIGN, "layer norm: pointers must be 16-byte aligned");
     if ((rc = check_device()) != VAE_OK) return rc;
+    LnRing r{};
+    if (ln_ring_plan(m, c, x_type, x_type, false, false, &r)) {
+        r.x = x_dev;
+        r.gamma = gamma_dev;
+        r.beta = beta_dev;
+        r.eps = eps;
+        r.out = y_dev;
+        r.yt = y_type;
+        return ln_ring_run<false>(r, reinterpret_cast<cudaStream_t>(stream));
+    }
     const LnPlan p = ln_plan(c);
     const unsigned grid = p.warp ? (static_cast<unsigned>(m) - 1u) / kLnFwdWarps + 1u : static_cast<unsigned>(m);
     VAE_CUDA_CHECK(ln_dispatch(p, [&](auto nv, auto v8, auto warp) {
@@ -370,15 +728,27 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
                          vae_layernorm_backward_workspace_bytes(m, c));
     if ((rc = check_device()) != VAE_OK) return rc;
     const LnPlan p = ln_plan(c);
-    const int grid = ln_bwd_grid(m, c);
+    int grid = ln_bwd_grid(m, c);
     float* part = sums ? static_cast<float*>(workspace_dev) : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    VAE_CUDA_CHECK(ln_dispatch(p, [&](auto nv, auto v8, auto warp) {
+    LnRing r{};
+    if (ln_ring_plan(m, c, x_type, dy_type, true, sums, &r)) {
+        r.x = x_dev;
+        r.dy = dy_dev;
+        r.gamma = gamma_dev;
+        r.eps = eps;
+        r.out = dx_dev;
+        r.part = part;
+        grid = kRingBlocks;
+        if ((rc = ln_ring_run<true>(r, s)) != VAE_OK) return rc;
+    } else {
+        VAE_CUDA_CHECK(ln_dispatch(p, [&](auto nv, auto v8, auto warp) {
         return launch_kernel(ln_bwd_kernel<nv.value, v8.value, warp.value>, dim3(static_cast<unsigned>(grid)),
                              dim3(warp.value ? kLnBwdWarps * 32 : p.threads),
                              warp.value && sums ? 2 * static_cast<size_t>(c) * sizeof(float) : 0, s, dy_dev, dy_type,
                              x_dev, x_type, m, c, gamma_dev, eps, dx_dev, part);
-    }));
+        }));
+    }
     if (sums)
         VAE_CUDA_CHECK(launch_kernel(ln_cols_kernel, dim3((2u * static_cast<unsigned>(c) + 31u) / 32u), dim3(256), 0, s,
                                      static_cast<const float*>(part), grid, c, dgamma_dev, dbeta_dev));
