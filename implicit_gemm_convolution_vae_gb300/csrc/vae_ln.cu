@@ -382,32 +382,32 @@ __global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1
     uint8_t* ring = smem + static_cast<size_t>(group) * p.stages * p.stage;
     const float* gam = reinterpret_cast<const float*>(smem + static_cast<size_t>(groups) * p.stages * p.stage);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bars) + group * kRingStages;
-    if (threadIdx.x == 0) abort_flag = 0;
-    if (tid == 0)
-        for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&full[i]), 1u);
-    fence_mbar_init();
-    pdl_wait();
-    const bool has_g = p.gamma != nullptr, has_b = !kBwd && p.beta != nullptr;
-    if (has_g || has_b) {
-        float* w = const_cast<float*>(gam);
-        for (int i = threadIdx.x; i < c; i += kWarps * 32) {
-            if (has_g) w[i] = p.gamma[i];
-            if (has_b) w[c + i] = p.beta[i];
-        }
-    }
-    __syncthreads();
     const int all = static_cast<int>(gridDim.x) * groups, first = static_cast<int>(blockIdx.x) * groups + group;
     const int n = first < p.m ? (p.m - 1 - first) / all + 1 : 0;  // this group's rows
-    auto fetch = [&](int k) {  // one lane of the group: the group's row k into stage k % stages
+    auto fetch = [&](int k, int st) {  // one lane of the group: the group's row k into stage st = k % stages
         const size_t row = static_cast<size_t>(first) + static_cast<size_t>(k) * all;
-        const int st = k % p.stages;
         const uint32_t bar = smem_u32(&full[st]), dst = smem_u32(ring + static_cast<size_t>(st) * p.stage);
         mbar_arrive_expect_tx(bar, p.row_x + p.row_dy);
         ln_bulk(dst, static_cast<const uint8_t*>(p.x) + row * p.row_x, p.row_x, bar);
         if (kBwd) ln_bulk(dst + p.row_x, static_cast<const uint8_t*>(p.dy) + row * p.row_dy, p.row_dy, bar);
     };
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (tid == 0) {
+        for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&full[i]), 1u);
+        fence_mbar_init();
+    }
+    pdl_wait();
     if (tid == 0)
-        for (int k = 0; k < n && k < p.stages; ++k) fetch(k);
+        for (int k = 0; k < n && k < p.stages; ++k) fetch(k, k);
+    const bool has_g = p.gamma != nullptr, has_b = !kBwd && p.beta != nullptr;
+    if (has_g || has_b) {
+        float* w = const_cast<float*>(gam);
+        for (int i = threadIdx.x * 4; i < c; i += kWarps * 32 * 4) {
+            if (has_g) *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(p.gamma + i);
+            if (has_b) *reinterpret_cast<float4*>(w + c + i) = *reinterpret_cast<const float4*>(p.beta + i);
+        }
+    }
+    __syncthreads();
     float2 dg[NV][4], db[NV][4];
     if constexpr (kBwd) {
 #pragma unroll
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1
         const float mean = group_sum(s.x + s.y, &red[0][group * wide], group, wide, part) * inv_c;
         // every thread of the group has its part of the row in registers (wide > 1: the barrier in the sum)
         if (wide == 1) __syncwarp();
-        if (tid == 0 && ok && k + p.stages < n) fetch(k + p.stages);
+        if (tid == 0 && ok && k + p.stages < n) fetch(k + p.stages, st);
         if (++st == p.stages) {
             st = 0;
             ph ^= 1u;
@@ -509,48 +509,59 @@ __global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1
     }
     if constexpr (kBwd) {
         if (p.part == nullptr) return;
-        // the groups' column sums, one group after another, over the ring
+        // the groups' column sums side by side over the ring (64 c bytes at most; a ring holds as much), then joined in order
         float* cols = reinterpret_cast<float*>(smem);
         __syncthreads();
-        for (int u = 0; u < groups; ++u) {
-            if (group == u) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            const int at = (tid + i * nt) * 8;
+            if (at < c) {
+                float* w = cols + static_cast<size_t>(group) * 2 * c + at;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int at = (tid + i * nt) * 8 + 2 * e;
-                        if (at < c) {
-                            float2* a = reinterpret_cast<float2*>(cols + at);
-                            float2* b = reinterpret_cast<float2*>(cols + c + at);
-                            *a = u == 0 ? dg[i][e] : add2(*a, dg[i][e]);
-                            *b = u == 0 ? db[i][e] : add2(*b, db[i][e]);
-                        }
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    *reinterpret_cast<float2*>(w + 2 * e) = dg[i][e];
+                    *reinterpret_cast<float2*>(w + c + 2 * e) = db[i][e];
+                }
             }
-            __syncthreads();
         }
+        __syncthreads();
         float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * c;
-        for (int i = threadIdx.x; i < 2 * c; i += kWarps * 32) out[i] = cols[i];
+        for (int i = threadIdx.x; i < 2 * c; i += kWarps * 32) {
+            float a = cols[i];
+            for (int u = 1; u < groups; ++u) a += cols[static_cast<size_t>(u) * 2 * c + i];
+            out[i] = a;
+        }
     }
 }
 
 // out[0 .. c) = sum over the blocks' partial rows, dgamma then dbeta: 32
-// columns x 8 slices of blocks per thread block, the slices joined in order.
-__global__ void __launch_bounds__(256) ln_cols_kernel(const float* __restrict__ part, int nblk, int c,
-                                                      float* __restrict__ dgamma, float* __restrict__ dbeta) {
-    __shared__ float s[8][32];
+// columns x 32 slices of blocks per thread block, each slice's loads in flight
+// together, the slices joined in order.
+constexpr int kColSlices = 32;
+__global__ void __launch_bounds__(kColSlices * 32) ln_cols_kernel(const float* __restrict__ part, int nblk, int c,
+                                                                  float* __restrict__ dgamma, float* __restrict__ dbeta) {
+    __shared__ float s[kColSlices][33];
     pdl_wait();
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
+    constexpr int kMost = (2 * kLnBwdBlocks + kColSlices - 1) / kColSlices;
     float a = 0.f;
-    if (col < 2 * c)
-        for (int b = slice; b < nblk; b += 8) a += part[static_cast<size_t>(b) * 2 * c + col];
+    if (col < 2 * c) {
+        float v[kMost];
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int b = slice + k * kColSlices;
+            v[k] = b < nblk ? part[static_cast<size_t>(b) * 2 * c + col] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) a += v[k];
+    }
     s[slice][lane] = a;
     __syncthreads();
-    if (slice == 0 && col < 2 * c) {
-        for (int i = 1; i < 8; ++i) a += s[i][lane];
-        (col < c ? dgamma : dbeta - c)[col] = a;
-    }
+    // warp w joins column w's slices
+    a = warp_sum(s[lane][slice]);
+    const int out = blockIdx.x * 32 + slice;
+    if (lane == 0 && out < 2 * c) (out < c ? dgamma : dbeta - c)[out] = a;
 }
 
 // How a row is held: warp form or the block's threads, and eights per thread.
@@ -575,7 +586,7 @@ LnPlan ln_plan(int c) {
 // The ring form's plan for rows of x (and dy: backward); false where the plain
 // form is used: lengths that are no multiple of eight or over 5120, or so few
 // rows that a group would not have two.
-bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, bool weights, LnRing* r) {
+bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, LnRing* r) {
     if (c % 8 != 0 || c > 5120) return false;
     const int warps = backward ? kRingBwdWarps : kRingFwdWarps;
     r->wide = c <= 1280 ? 1 : (c <= 2560 ? 2 : 4);
@@ -590,7 +601,6 @@ bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, bool weights, Ln
     r->stages = static_cast<int>(std::min<size_t>(kRingStages, left / (static_cast<size_t>(groups) * r->stage)));
     if (r->stages < 2) return false;
     const size_t ring = static_cast<size_t>(groups) * r->stages * r->stage;
-    if (weights && ring < static_cast<size_t>(c) * 8) return false;  // (the column sums lie over the ring)
     r->bars = static_cast<unsigned>(ring + consts);
     r->m = m;
     r->c = c;
@@ -682,7 +692,7 @@ int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamm
         return set_error(VAE_ERR_ALIGN, "layer norm: pointers must be 16-byte aligned");
     if ((rc = check_device()) != VAE_OK) return rc;
     LnRing r{};
-    if (ln_ring_plan(m, c, x_type, x_type, false, false, &r)) {
+    if (ln_ring_plan(m, c, x_type, x_type, false, &r)) {
         r.x = x_dev;
         r.gamma = gamma_dev;
         r.beta = beta_dev;
@@ -732,7 +742,7 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
     float* part = sums ? static_cast<float*>(workspace_dev) : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     LnRing r{};
-    if (ln_ring_plan(m, c, x_type, dy_type, true, sums, &r)) {
+    if (ln_ring_plan(m, c, x_type, dy_type, true, &r)) {
         r.x = x_dev;
         r.dy = dy_dev;
         r.gamma = gamma_dev;
@@ -750,7 +760,8 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
         }));
     }
     if (sums)
-        VAE_CUDA_CHECK(launch_kernel(ln_cols_kernel, dim3((2u * static_cast<unsigned>(c) + 31u) / 32u), dim3(256), 0, s,
+        VAE_CUDA_CHECK(launch_kernel(ln_cols_kernel, dim3((2u * static_cast<unsigned>(c) + 31u) / 32u),
+                                     dim3(kColSlices * 32), 0, s,
                                      static_cast<const float*>(part), grid, c, dgamma_dev, dbeta_dev));
     return VAE_OK;
 }
