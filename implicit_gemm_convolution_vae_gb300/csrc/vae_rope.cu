@@ -9,6 +9,7 @@
 // of those tokens: one read and one write of the tensor, which bounds the call.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "vae_types.cuh"
 
@@ -18,13 +19,14 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxD = 256;
-constexpr int kRopeTokens = 8;  // tokens per block, at most
+constexpr int kRopeTokens = 32;  // tokens per block, at most
+constexpr int kRopePitch = VAE_ROPE_MAX_PAIRS + 2;  // of a token's (cos, sin) row: 16-byte aligned, few bank conflicts
 
 struct RopeParams {
     const void* x;
     void* y;
     const void* pos;
-    long long tokens;  // b * s
+    int tokens;        // b * s
     int s, h, d, tpb;  // tpb: tokens per block
     int pos_int, pos_batch, inverse;
     long long xs[3], ys[3];
@@ -37,86 +39,152 @@ __device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
     a = x;
 }
 
-// kV8: eights of channels in 16-byte accesses; else one pair (or one copied
-// channel) at a time. kInter: pairs (2p, 2p + 1), else (p, p + R/2).
-template <int T, bool kV8, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, const __grid_constant__ vae_rope_plan plan) {
+
+// A unit as it lies in memory: sixteen or eight elements, or one.
+template <int T, int kN>
+struct RopeUnit {
+    static constexpr bool kV8 = kN > 1;
+    static constexpr int kRegs = kV8 ? (T == VAE_F32 ? kN / 4 : kN / 8) : 1;
+    using Reg = std::conditional_t<kV8, uint4, typename Elem<T>::type>;
+    Reg r[kRegs];
+    __device__ __forceinline__ void load(const typename Elem<T>::type* p) {
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) r[i] = reinterpret_cast<const Reg*>(p)[i];
+    }
+    __device__ __forceinline__ void store(typename Elem<T>::type* p) const {
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) reinterpret_cast<Reg*>(p)[i] = r[i];
+    }
+    __device__ __forceinline__ void get(float (&v)[kN]) const {
+        if constexpr (kV8) {
+#pragma unroll
+            for (int i = 0; i < kN / 8; ++i) load8<T>(r + i * kRegs / (kN / 8), *reinterpret_cast<float(*)[8]>(v + 8 * i));
+        } else {
+            v[0] = to_f32<T>(r[0]);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[kN]) {
+        if constexpr (kV8) {
+#pragma unroll
+            for (int i = 0; i < kN / 8; ++i) store8<T>(r + i * kRegs / (kN / 8), *reinterpret_cast<const float(*)[8]>(v + 8 * i));
+        } else {
+            r[0] = from_f32<T>(v[0]);
+        }
+    }
+};
+
+// kN: channels of a unit, 16 (interleaved) or 8 in 16-byte accesses, or 1.
+// kInter: pairs (2p, 2p + 1), else (p, p + R/2).
+// A row is one head of one token. Its units (vectors of interleaved pairs, or
+// those of both halves, or both of a pair, together; then the copied ones: a
+// thread turns 16 or 32 bytes a row) go to threads side by side, and a thread keeps its unit on every row it
+// meets. The first rows are on their way while the angles are formed.
+template <int T, int kN, bool kInter>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p, const __grid_constant__ vae_rope_plan plan) {
     using E = typename Elem<T>::type;
-    __shared__ float2 cs[kRopeTokens][VAE_ROPE_MAX_PAIRS];
+    using Unit = RopeUnit<T, kN>;
+    constexpr bool kV8 = kN > 1;
+    constexpr bool kTwo = !(kV8 && kInter);  // two units turn together
+    // rows whose loads a thread has in flight together (64 registers leave room for 64 bytes twice over)
+    constexpr int kRopeBatch = kTwo && kV8 && T == VAE_F32 ? 2 : 4;
+    __shared__ __align__(16) float2 cs[kRopeTokens][kRopePitch];
     pdl_wait();
-    const long long t0 = static_cast<long long>(blockIdx.x) * p.tpb;
-    const int nt = static_cast<int>(p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb);
-    const int pairs = plan.pairs;
+    const int t0 = static_cast<int>(blockIdx.x) * p.tpb;
+    const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
+    const int b0 = t0 / p.s, s0 = t0 - b0 * p.s;
+    const int pairs = plan.pairs, rot = 2 * pairs;
+    const int nrot = kTwo ? pairs / kN : rot / kN;
+    const int units = nrot + (p.d - rot) / kN;  // (256 at most: d)
+    const int step = kRopeThreads / units;      // rows that the block takes at a time
+    const int u = threadIdx.x % units;
+    const bool copied = u >= nrot;
+    const int ia = copied ? rot + (u - nrot) * kN : (!kV8 && kInter ? 2 * u : u * kN);
+    const int ib = kV8 ? ia + pairs : (kInter ? ia + 1 : ia + pairs);
+    int hd = threadIdx.x / units, tk = hd < step ? 0 : nt;
+    auto settle = [&]() {
+        while (tk < nt && hd >= p.h) {
+            hd -= p.h;
+            ++tk;
+        }
+    };
+    settle();
+    auto offset = [&](int tok, int head, const long long (&st)[3]) {
+        int si = s0 + tok, bi = b0;
+        while (si >= p.s) {
+            si -= p.s;
+            ++bi;
+        }
+        return bi * st[0] + si * st[1] + head * st[2];
+    };
+    Unit a[kRopeBatch], b[kTwo ? kRopeBatch : 1];
+    int at[kRopeBatch];  // the rows: token << 20 | head
+    auto load = [&]() {
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k) {
+            at[k] = tk << 20 | hd;
+            if (tk < nt) {
+                const E* x = static_cast<const E*>(p.x) + offset(tk, hd, p.xs);
+                a[k].load(x + ia);
+                if constexpr (kTwo)
+                    if (!copied) b[k].load(x + ib);
+                hd += step;
+                settle();
+            }
+        }
+    };
+    load();
     for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
-        const int tk = i / pairs, pr = i - tk * pairs;
-        const long long tok = t0 + tk;
-        const long long prow = p.pos_batch > 1 ? tok : tok % p.s;
-        const long long at = prow * plan.naxes + plan.axis[pr];
-        const float pos = p.pos_int ? static_cast<float>(static_cast<const int*>(p.pos)[at])
-                                    : static_cast<const float*>(p.pos)[at];
+        // neighbours take the tokens of one pair: its entries of the plan are one address for them, and the constant
+        // bank serves one address at a time (a pair per lane took 3/4 of the call on few heads)
+        const int pr = i / nt, t = i - pr * nt;
+        const long long row = p.pos_batch > 1 ? t0 + t : (s0 + t) % p.s;
+        const long long i_pos = row * plan.naxes + plan.axis[pr];
+        const float pos = p.pos_int ? static_cast<float>(static_cast<const int*>(p.pos)[i_pos])
+                                    : static_cast<const float*>(p.pos)[i_pos];
         // whole turns + fraction of pos * hi (the fma's product is exact), then the rest
         const float hi = plan.turns_hi[pr];
         const float whole = rintf(pos * hi);
         const float frac = fmaf(pos, hi, -whole) + pos * plan.turns_lo[pr];
         float sn, c;
         sincospif(2.f * frac, &sn, &c);
-        cs[tk][pr] = make_float2(c, p.inverse ? -sn : sn);
+        cs[t][pr] = make_float2(c, p.inverse ? -sn : sn);
     }
     __syncthreads();
-    const int rot = 2 * pairs;
-    // units of one token and head: kV8 interleaved: d / 8 eights; kV8 halves: the
-    // eights of a pair of halves together, then the copied eights; scalar: pairs, then copied channels
-    const int nrot = kV8 ? (kInter ? rot / 8 : pairs / 8) : pairs;
-    const int units = nrot + (kV8 ? (p.d - rot) / 8 : p.d - rot);
-    const int per_tok = p.h * units;
-    for (int i = threadIdx.x; i < nt * per_tok; i += kRopeThreads) {
-        const int tk = i / per_tok, r = i - tk * per_tok;
-        const int hd = r / units, u = r - hd * units;
-        const long long tok = t0 + tk;
-        const long long bi = tok / p.s, si = tok - bi * p.s;
-        const E* x = static_cast<const E*>(p.x) + bi * p.xs[0] + si * p.xs[1] + hd * p.xs[2];
-        E* y = static_cast<E*>(p.y) + bi * p.ys[0] + si * p.ys[1] + hd * p.ys[2];
-        if constexpr (kV8) {
-            if (u >= nrot) {
-                float v[8];
-                const int at = rot + (u - nrot) * 8;
-                load8<T>(x + at, v);
-                store8<T>(y + at, v);
-            } else if constexpr (kInter) {
-                float v[8];
-                load8<T>(x + u * 8, v);
+    while (at[0] >> 20 < nt) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) turn(v[2 * e], v[2 * e + 1], cs[tk][u * 4 + e]);
-                store8<T>(y + u * 8, v);
-            } else {
-                float a[8], b[8];
-                load8<T>(x + u * 8, a);
-                load8<T>(x + pairs + u * 8, b);
+        for (int k = 0; k < kRopeBatch; ++k)
+            if (const int t = at[k] >> 20; t < nt) {
+                E* y = static_cast<E*>(p.y) + offset(t, at[k] & 0xfffff, p.ys);
+                if (!copied) {
+                    float v[kN];
+                    a[k].get(v);
+                    if constexpr (kTwo) {
+                        float w[kN];
+                        b[k].get(w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) turn(a[e], b[e], cs[tk][u * 8 + e]);
-                store8<T>(y + u * 8, a);
-                store8<T>(y + pairs + u * 8, b);
+                        for (int e = 0; e < kN; ++e) turn(v[e], w[e], cs[t][u * kN + e]);
+                        b[k].set(w);
+                        b[k].store(y + ib);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kN / 2; ++e) turn(v[2 * e], v[2 * e + 1], cs[t][u * (kN / 2) + e]);
+                    }
+                    a[k].set(v);
+                }
+                a[k].store(y + ia);
             }
-        } else {
-            if (u >= nrot) {
-                y[rot + u - nrot] = x[rot + u - nrot];
-            } else {
-                const int ia = kInter ? 2 * u : u, ib = kInter ? 2 * u + 1 : u + pairs;
-                float a = to_f32<T>(x[ia]), b = to_f32<T>(x[ib]);
-                turn(a, b, cs[tk][u]);
-                y[ia] = from_f32<T>(a);
-                y[ib] = from_f32<T>(b);
-            }
-        }
+        load();
     }
 }
 
 template <int T>
-cudaError_t rope_launch(bool v8, bool inter, unsigned grid, cudaStream_t s, const RopeParams& p,
+cudaError_t rope_launch(int unit, bool inter, unsigned grid, cudaStream_t s, const RopeParams& p,
                         const vae_rope_plan& plan) {
     const auto go = [&](auto k) { return launch_kernel(k, dim3(grid), dim3(kRopeThreads), 0, s, p, plan); };
-    if (v8) return inter ? go(rope_kernel<T, true, true>) : go(rope_kernel<T, true, false>);
-    return inter ? go(rope_kernel<T, false, true>) : go(rope_kernel<T, false, false>);
+    if constexpr (T != VAE_F32)
+        if (unit == 16) return go(rope_kernel<T, 16, true>);
+    if (unit == 8) return inter ? go(rope_kernel<T, 8, true>) : go(rope_kernel<T, 8, false>);
+    return inter ? go(rope_kernel<T, 1, true>) : go(rope_kernel<T, 1, false>);
 }
 
 }  // namespace
@@ -169,6 +237,8 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
     for (int i = 0; i < plan->pairs; ++i)
         if (plan->axis[i] >= plan->naxes) return set_error(VAE_ERR_ARG, "rope: the plan was not initialised");
     if (b < 1 || s < 1 || h < 1) return set_error(VAE_ERR_SHAPE, "rope: b, s, h >= 1 are needed");
+    if (static_cast<long long>(b) * s > 0x7fffff00LL || h >= (1 << 20))
+        return set_error(VAE_ERR_SHAPE, "rope: over 2^31 - 256 tokens or 2^20 - 1 heads");
     if (d > kRopeMaxD || 2 * plan->pairs > d)
         return set_error(VAE_ERR_SHAPE, "rope: the plan turns %d channels of a head of %d (at most %d)",
                          2 * plan->pairs, d, kRopeMaxD);
@@ -192,13 +262,15 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
     p.x = x_dev;
     p.y = y_dev;
     p.pos = pos_dev;
-    p.tokens = static_cast<long long>(b) * s;
+    p.tokens = b * s;
     p.s = s;
     p.h = h;
     p.d = d;
     p.pos_int = pos_int != 0;
     p.pos_batch = pos_batch;
     p.inverse = inverse != 0;
+    // Vectors where every row starts on 16 bytes and holds whole ones. Interleaved 16-bit pairs: sixteen channels a
+    // thread where they fit (340 MB: 74.6 us against 80.7 with eight; f32 measured 32.4 against 28.2 and keeps eight).
     bool v8 = aligned16(x_dev) && aligned16(y_dev) && d % 8 == 0 &&
               (plan->interleaved ? 2 * plan->pairs : plan->pairs) % 8 == 0;
     for (int i = 0; i < 3; ++i) {
@@ -208,16 +280,14 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
     }
     // Tokens per block: as many as share one (cos, sin) table, down to one when
     // there are too few tokens to give every SM a block.
-    p.tpb = static_cast<int>(std::min<long long>(kRopeTokens, std::max<long long>(1, p.tokens / 304)));
-    const long long grid = (p.tokens + p.tpb - 1) / p.tpb;
-    if (grid > 0x7fffffffLL || static_cast<long long>(h) * d > (1 << 24))
-        return set_error(VAE_ERR_SHAPE, "rope: too many tokens or heads");
+    p.tpb = std::min(kRopeTokens, std::max(1, p.tokens / 304));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned g = static_cast<unsigned>(grid);
+    const unsigned g = static_cast<unsigned>((p.tokens - 1) / p.tpb + 1);
     const bool in = plan->interleaved != 0;
-    VAE_CUDA_CHECK(type == VAE_F32   ? rope_launch<VAE_F32>(v8, in, g, st, p, *plan)
-                   : type == VAE_F16 ? rope_launch<VAE_F16>(v8, in, g, st, p, *plan)
-                                     : rope_launch<VAE_BF16>(v8, in, g, st, p, *plan));
+    const int unit = !v8 ? 1 : (in && type != VAE_F32 && d % 16 == 0 && plan->pairs % 8 == 0 ? 16 : 8);
+    VAE_CUDA_CHECK(type == VAE_F32   ? rope_launch<VAE_F32>(unit, in, g, st, p, *plan)
+                   : type == VAE_F16 ? rope_launch<VAE_F16>(unit, in, g, st, p, *plan)
+                                     : rope_launch<VAE_BF16>(unit, in, g, st, p, *plan));
     return VAE_OK;
 }
 

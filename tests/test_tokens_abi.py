@@ -81,6 +81,7 @@ def test_rope_refusals(L):
         assert rc(**{k: None}) == -1
     assert rc(t=3) == -1 and rc(plan=ctypes.byref(vg._RopePlan())) == -1
     assert rc(b=0) == -2 and rc(s=0) == -2 and rc(h=0) == -2 and rc(d=62) == -2 and rc(d=258) == -2
+    assert rc(b=1 << 16, s=1 << 15) == -2 and rc(h=1 << 20) == -2
     assert rc(pb=3) == -2 and rc(pb=0) == -2
     assert rc(xs=st(960, -192, 64)) == -2 and rc(ys=st(0, 192, 64)) == -2
     assert rc(y=FAKE, ys=st(960, 192, 128)) == -1
