@@ -45,9 +45,9 @@ int mha_check(const vae_attention_desc* a, bool backward, MhaShape* s) {
     s->g = a->hq / a->hkv;
     s->d = a->d;
     s->block = a->block;
-    // gp: the largest power of two in g, a tile's rows at most
+    // gp: the largest power of two in g, half a tile's rows at most
     s->gp_log2 = 0;
-    while (s->gp_log2 < 7 && s->g % (2 << s->gp_log2) == 0) ++s->gp_log2;
+    while (s->gp_log2 < 6 && s->g % (2 << s->gp_log2) == 0) ++s->gp_log2;
     s->nsub = s->g >> s->gp_log2;
     const long long rows = static_cast<long long>(a->sq) << s->gp_log2;
     s->ntile = static_cast<int>((rows + kMhaTile - 1) / kMhaTile);

@@ -4,7 +4,7 @@
 // with the contraction index outside (MN-major) and left operands in TMEM.
 //
 // Rows. The query heads that share a key head stand side by side as rows: with
-// gp the largest power of two that divides g = hq / hkv (128 at most), row
+// gp the largest power of two that divides g = hq / hkv (64 at most), row
 // r = token * gp + head of the group, so that one 128-row tile of q (a TMA box
 // of 128/gp tokens x gp heads) meets each key tile once for all of them. What
 // is left of g (sub = g / gp) are tiles of their own.
@@ -116,6 +116,35 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
     for (int k = 0; k < 8; ++k)
         umma_f16_ts(d_tmem, a_tmem + static_cast<uint32_t>((k >> 2) * kHalf + (k & 3) * 8), b + (2048u >> 4) * k, id,
                     k != 0 ? 1u : acc);
+}
+
+// D = A B^T with A's rows in TMEM (16 channels in eight columns), B K-major.
+template <int kSteps>
+__device__ __forceinline__ void mma_ts_k(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+        umma_f16_ts(d_tmem, a_tmem + 8u * k, b + static_cast<uint32_t>((k >> 2) * (kMhaChunkBytes >> 4) + (k & 3) * 2), id,
+                    k != 0 ? 1u : 0u);
+}
+
+// One arrival on the barrier at this offset in every CTA of `mask`, once the
+// MMAs issued so far are done.
+__device__ __forceinline__ void umma_commit_to(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
+}
+
+// A TMA box into the same place of every CTA of `mask`, counted on each one's
+// barrier at this offset.
+__device__ __forceinline__ void tma_load_4d_to(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                               int c3, uint16_t mask, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7, %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(mask), "l"(policy)
+        : "memory");
 }
 
 // 2^x, approximate (relative error near 2^-22); under 2^-126 it is 0.

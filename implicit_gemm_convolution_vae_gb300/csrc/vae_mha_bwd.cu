@@ -17,7 +17,20 @@
 // are read again with the rows as the contraction index. While the warps form
 // dS^T, the tensor cores run dV and the next S^T; while they form the next
 // P^T, dK and the next dP^T.
-// Query-tile kernel: the same with lanes as query rows; P stays in registers.
+// Query-tile kernel: the same with lanes as query rows; P stays in registers,
+// and the Q and dO rows lie in TMEM as the left operands of S and dP: M = N = 128
+// MMAs with both operands in shared memory ran at 90 cycles each, bound by the
+// 8 KB that each reads there, those with one in TMEM at 57 to 64.
+//
+// Both kernels read 64 KB of tiles per step, more than L2 gives every SM at the
+// rate the products run (28 bytes a cycle and SM were measured): where there is
+// work for every SM, clusters of two CTAs with neighbouring tiles of one head
+// take the same steps, each loads half of every tile and sends it to both.
+//
+// D = rowsum(dO * O) takes O as the forward rounded it. Rows that meet few keys
+// (kExactTiles tiles at most) feel that rounding in dS: the query-tile kernel
+// first runs over their keys once for D = rowsum(P * dP) itself, and hands it
+// to the key-tile kernel after it.
 //
 // 16 bits. P and dS are rounded to the tensors' type for the products, half a
 // step of 2^-8 or 2^-11 relative, as the forward's P. f16 would lose long rows'
@@ -44,24 +57,35 @@ constexpr int kPLog2 = 14;         // f16: P is held as P 2^14
 constexpr int kSideFloats = 256;   // of a row tile: 128 x (kPLog2 - lse log2(e)), 128 x D
 constexpr int kSideBytes = kSideFloats * 4;
 
-template <int kSteps>  // 16-channel steps of a row
+constexpr int kExactTiles = 8;     // key tiles up to which D is formed from P and dP
+
+// Shared memory of a kernel: kRes resident tiles, a ring of kN stages of two
+// tiles, kSideN side rows; the barriers behind them.
+template <int kSteps, int kRes, int kN, int kSideN>
 struct BwdCfg {
-    static constexpr int kCh = kSteps > 4 ? 2 : 1;  // 64-channel chunks
+    static constexpr int kCh = kSteps > 4 ? 2 : 1;  // 64-channel chunks of the kSteps x 16 channels
     static constexpr int kTileBytes = kCh * kMhaChunkBytes;
-    static constexpr int kStages = kCh == 2 ? 2 : 4;
-    static constexpr int kRing = 2 * kTileBytes;  // behind the two resident tiles
+    static constexpr int kStages = kN;
+    static constexpr int kRing = kRes * kTileBytes;
     static constexpr int kSide = kRing + kStages * 2 * kTileBytes;
-    static constexpr int kBars = kSide + kStages * kSideBytes;
-    static constexpr int kSmem = 1024 + kBars + 512;
+    static constexpr int kBars = kSide + kSideN * kSideBytes;
+    static constexpr int kSmem = kBars + 512;
+    static_assert(kSmem <= 232448, "attention shared memory over 227 KB");
 };
-static_assert(BwdCfg<8>::kSmem <= 232448 && BwdCfg<4>::kSmem <= 232448, "attention shared memory over 227 KB");
+template <int kSteps>
+using KvCfg = BwdCfg<kSteps, 2, (kSteps > 4 ? 2 : 5), (kSteps > 4 ? 2 : 5)>;
+template <int kSteps>
+using QCfg = BwdCfg<kSteps, 0, (kSteps > 4 ? 3 : 6), 1>;  // (the side row: 256 floats for the rows' sums)
 
 struct BwdParams {
     MhaShape s;
     float scale, scale_log2;
     int nsplit_q, nsplit_k;
-    const float* side;          // [b][hkv][nsub][ntile][256]
+    int csize_q, csize_k;       // CTAs per cluster
+    float* side;                // [b][hkv][nsub][ntile][256]
     const unsigned* maxima;     // f16: bits of max |dO|^2, max |V|^2
+    const void *q, *dout;
+    MhaStrides qs, gs;
     void *dq, *dk, *dv;
     MhaStrides dqs, dks, dvs;
     float *part_q, *part_kv;    // [nsplit_q][b][hq][sq][d], [nsplit_k][2][b][hkv][sk][d]
@@ -174,16 +198,16 @@ __global__ void __launch_bounds__(256) mha_prep_kernel(const PrepParams p) {
 struct BwdSmem {
     uint8_t *res, *ring, *side;
     uint64_t *a_full, *b_full, *empty;  // [kStages]: first tile (+ side), second tile, both free
-    uint64_t *res_full, *s_full, *x_full, *p_full, *ds_full, *done, *fix, *drain;
+    uint64_t* fix;                      // [kStages]: both tiles, before their rows behind the length are zeroed
+    uint64_t *res_full, *s_full, *x_full, *p_full, *ds_full, *done, *drain;
+    uint64_t* x_bar;  // [4 quadrants]
     uint32_t* tmem_slot;
     int* abort_flag;
 };
 
-template <int kSteps>
-__device__ __forceinline__ BwdSmem bwd_carve(uint8_t* raw) {
-    using C = BwdCfg<kSteps>;
+template <typename C>
+__device__ __forceinline__ BwdSmem bwd_carve(uint8_t* base) {
     BwdSmem s;
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.res = base;
     s.ring = base + C::kRing;
     s.side = base + C::kSide;
@@ -191,16 +215,17 @@ __device__ __forceinline__ BwdSmem bwd_carve(uint8_t* raw) {
     s.a_full = b;
     s.b_full = b + C::kStages;
     s.empty = b + 2 * C::kStages;
-    b += 3 * C::kStages;
+    s.fix = b + 3 * C::kStages;
+    b += 4 * C::kStages;
     s.res_full = b;
     s.s_full = b + 1;
     s.x_full = b + 2;  // dP has been formed
     s.p_full = b + 3;  // key-tile kernel: P^T is in TMEM; query-tile kernel: S has been read
     s.ds_full = b + 4;
     s.done = b + 5;
-    s.fix = b + 6;
-    s.drain = b + 7;
-    s.tmem_slot = reinterpret_cast<uint32_t*>(b + 8);
+    s.drain = b + 6;
+    s.x_bar = b + 7;
+    s.tmem_slot = reinterpret_cast<uint32_t*>(b + 11);
     s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
     return s;
 }
@@ -215,61 +240,81 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// A 128-row tile as two boxes of 64 rows per chunk, into this CTA; `half` is the
+// second box's distance in tokens.
 template <int kChunks>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int head, int token, int e,
-                                          uint64_t pol) {
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int head, int token, int half,
+                                          int e, uint64_t pol) {
     for (int c = 0; c < kChunks; ++c)
-        tma_load_4d(smem_u32(dst + c * kMhaChunkBytes), map, bar, c * 64, head, token, e, pol);
+        for (int r = 0; r < 2; ++r)
+            tma_load_4d(smem_u32(dst + c * kMhaChunkBytes + r * (kMhaChunkBytes / 2)), map, bar, c * 64, head,
+                        token + r * half, e, pol);
+}
+// The same into both CTAs of a cluster, each of which brings the half of its rank.
+template <int kChunks>
+__device__ __forceinline__ void load_tile_shared(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int head, int token,
+                                                 int half, int e, int rank, int csize, uint64_t pol) {
+    if (csize == 1) {
+        load_tile<kChunks>(dst, map, bar, head, token, half, e, pol);
+        return;
+    }
+    for (int c = 0; c < kChunks; ++c)
+        tma_load_4d_to(smem_u32(dst + c * kMhaChunkBytes + rank * (kMhaChunkBytes / 2)), map, bar, c * 64, head,
+                       token + rank * half, e, static_cast<uint16_t>(3), pol);
 }
 
-// Set-up and tear-down common to both kernels.
-template <int kSteps>
-__device__ __forceinline__ uint32_t bwd_begin(const BwdSmem& s, int warp) {
-    using C = BwdCfg<kSteps>;
+// Set-up and tear-down common to both kernels. No CTA of a cluster sends to
+// another before the other's barriers are there, or leaves before all is done.
+template <typename C>
+__device__ __forceinline__ void bwd_begin(const BwdSmem& s, int warp, int csize, uint32_t res_arrivals) {
     if (threadIdx.x == 0) {
         *s.abort_flag = 0;
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&s.a_full[i]), 1u);
             mbar_init(smem_u32(&s.b_full[i]), 1u);
-            mbar_init(smem_u32(&s.empty[i]), 1u);
+            mbar_init(smem_u32(&s.empty[i]), static_cast<uint32_t>(csize));
+            mbar_init(smem_u32(&s.fix[i]), 1u);
         }
-        mbar_init(smem_u32(s.res_full), 1u);
+        mbar_init(smem_u32(s.res_full), res_arrivals);
         mbar_init(smem_u32(s.s_full), 1u);
         mbar_init(smem_u32(s.x_full), 1u);
         mbar_init(smem_u32(s.p_full), kSoftWarps);
         mbar_init(smem_u32(s.ds_full), kSoftWarps);
         mbar_init(smem_u32(s.done), 1u);
-        mbar_init(smem_u32(s.fix), 1u);
-        mbar_init(smem_u32(s.drain), 1u);
+        mbar_init(smem_u32(s.drain), static_cast<uint32_t>(csize));
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.x_bar[i]), 2u);
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
+        tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);  // all 512 columns are this CTA's: they start at 0
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
+    if (csize > 1) cluster_sync();
     tc_fence_after();
-    return 0u;  // all 512 columns are this CTA's: they start at 0
 }
-__device__ __forceinline__ void bwd_end(uint32_t tmem, int warp) {
+__device__ __forceinline__ void bwd_end(int warp, int csize) {
     pdl_launch_dependents();
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (csize > 1) cluster_sync();
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(0u, kTmemCols);
     }
 }
 
 // The ring's producer state: what is in flight when a wait runs out has to
-// land before the CTA may exit.
+// land before the CTA may exit. A stage that has to be fixed completes on a
+// barrier of its own (per stage: the other CTA of a cluster may already send
+// the next one) and then on the stage's by hand.
 template <int kN>
 struct BwdRing {
     int stage = 0;
-    uint32_t phase = 0, armed = 0, arm_par = 0, fixes = 0;
+    uint32_t phase = 0, armed = 0, arm_par = 0, fixing = 0, fix_par = 0;
     __device__ __forceinline__ void arm() {
         armed |= 1u << stage;
         arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
@@ -280,23 +325,48 @@ struct BwdRing {
             phase ^= 1u;
         }
     }
-    __device__ __forceinline__ void drain(const BwdSmem& s, const BwdParams& p) const {
+    // Waits for the stage's copies (the whole warp), zeroes rows [from, 128) of both tiles and hands it over.
+    template <typename C>
+    __device__ __forceinline__ bool fix(const BwdSmem& s, const BwdParams& p, int from, int lane) {
+        armed &= ~(1u << stage);
+        fixing = 1u << stage;
+        const uint32_t par = (fix_par >> stage) & 1u;
+        __syncwarp();
+        if (!warp_all(bwait(&s.fix[stage], par, s, p))) return false;
+        fixing = 0u;
+        fix_par ^= 1u << stage;
+        uint8_t* dst = s.ring + stage * 2 * C::kTileBytes;
+        mha_zero_rows(dst, from, C::kCh, lane);
+        mha_zero_rows(dst + C::kTileBytes, from, C::kCh, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&s.a_full[stage]));
+            mbar_arrive(smem_u32(&s.b_full[stage]));
+        }
+        return true;
+    }
+    __device__ __forceinline__ void drain(const BwdSmem& s, const BwdParams& p, bool resident) const {
         int never = 0;
-        (void)mbar_wait(smem_u32(s.res_full), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
-        if (fixes > 0)
-            (void)mbar_wait(smem_u32(s.fix), (fixes - 1u) & 1u, &never, p.timeout_ns, p.status, kWhereDrain);
-        for (int i = 0; i < kN; ++i)
-            if (armed & (1u << i)) {
-                (void)mbar_wait(smem_u32(&s.a_full[i]), (arm_par >> i) & 1u, &never, p.timeout_ns, p.status, kWhereDrain);
-                (void)mbar_wait(smem_u32(&s.b_full[i]), (arm_par >> i) & 1u, &never, p.timeout_ns, p.status, kWhereDrain);
+        const auto wait = [&](uint64_t* bar, uint32_t par) {
+            (void)mbar_wait(smem_u32(bar), par, &never, p.timeout_ns, p.status, kWhereDrain);
+        };
+        if (resident) wait(s.res_full, 0u);
+        for (int i = 0; i < kN; ++i) {
+            if (fixing >> i & 1u) wait(&s.fix[i], (fix_par >> i) & 1u);
+            if (armed >> i & 1u) {
+                wait(&s.a_full[i], (arm_par >> i) & 1u);
+                wait(&s.b_full[i], (arm_par >> i) & 1u);
             }
+        }
     }
 };
 
-__device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p, bool ok) {
+// (Every CTA of a cluster waits for all of them: none leaves while another's MMAs still signal its barriers.)
+__device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p, bool ok, int csize) {
     if (elect_one()) {
         if (ok) umma_commit(smem_u32(s.done));
-        umma_commit(smem_u32(s.drain));
+        umma_commit_to(smem_u32(s.drain), static_cast<uint16_t>((1u << csize) - 1u));
         int never = 0;
         (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
     }
@@ -342,18 +412,22 @@ __device__ __forceinline__ void store_acc(uint32_t t, int d, bool live, bool any
 // ───────────────────────────── dK and dV, per key tile ─────────────────────────────
 
 struct KvWork {
-    int e, hk, kb, split;
+    int e, hk, kb, split, rank;
     int ql, kl;
-    int t0, nt;      // row tiles [t0, nt) of each part of the group see this key tile
+    int t0, nt;      // row tiles [t0, nt) of each part of the group see the cluster's key tiles
     int first, n;    // this split's share of the nsub * (nt - t0) tiles
 };
 
+// (A cluster's CTAs have key tiles kb, kb + 1 and the same row tiles.)
 __device__ __forceinline__ KvWork kv_work(const BwdParams& p) {
     const MhaShape& s = p.s;
     KvWork w;
-    int r = blockIdx.x;
-    w.kb = r % s.nkb;
-    r /= s.nkb;
+    const int nk = (s.nkb + p.csize_k - 1) / p.csize_k;
+    w.rank = static_cast<int>(blockIdx.x) % p.csize_k;
+    int r = blockIdx.x / p.csize_k;
+    const int kb0 = r % nk * p.csize_k;
+    w.kb = kb0 + w.rank;
+    r /= nk;
     w.split = r % p.nsplit_k;
     r /= p.nsplit_k;
     w.hk = r % s.hkv;
@@ -362,32 +436,31 @@ __device__ __forceinline__ KvWork kv_work(const BwdParams& p) {
     w.kl = mha_len(s.k_len, w.e, s.sk);
     const long long rows = static_cast<long long>(w.ql) << s.gp_log2;
     w.nt = static_cast<int>((rows + kMhaTile - 1) / kMhaTile);
-    int i0 = 0;  // the first query that sees a key of the tile
+    int i0 = 0;  // the first query that sees a key of the first tile
     if (s.block > 0) {
-        i0 = w.kb * kMhaTile / s.block * s.block - (w.kl - w.ql);
+        i0 = kb0 * kMhaTile / s.block * s.block - (w.kl - w.ql);
         if (i0 < 0) i0 = 0;
     }
     const long long t0 = (static_cast<long long>(i0) << s.gp_log2) / kMhaTile;
     w.t0 = t0 < w.nt ? static_cast<int>(t0) : w.nt;
-    const int all = w.kb * kMhaTile < w.kl ? s.nsub * (w.nt - w.t0) : 0;
+    const int all = kb0 * kMhaTile < w.kl ? s.nsub * (w.nt - w.t0) : 0;
     const int per = (all + p.nsplit_k - 1) / p.nsplit_k;
     w.first = w.split * per < all ? w.split * per : all;
     w.n = (w.first + per < all ? w.first + per : all) - w.first;
     return w;
 }
 
-template <int kSteps>
+template <typename C>
 __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& w, const CUtensorMap* mq,
                             const CUtensorMap* mg, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
-    using C = BwdCfg<kSteps>;
     const uint64_t pol = policy_evict_normal();
     const MhaShape& sh = p.s;
-    const int gp = 1 << sh.gp_log2;
+    const int gp = 1 << sh.gp_log2, half = 64 >> sh.gp_log2;
     if (lane == 0) {
         const uint32_t rb = smem_u32(s.res_full);
         mbar_arrive_expect_tx(rb, 2u * C::kTileBytes);
-        load_tile<C::kCh>(s.res, mk, rb, w.hk, w.kb * kMhaTile, w.e, pol);
-        load_tile<C::kCh>(s.res + C::kTileBytes, mv, rb, w.hk, w.kb * kMhaTile, w.e, pol);
+        load_tile<C::kCh>(s.res, mk, rb, w.hk, w.kb * kMhaTile, 64, w.e, pol);
+        load_tile<C::kCh>(s.res + C::kTileBytes, mv, rb, w.hk, w.kb * kMhaTile, 64, w.e, pol);
     }
     BwdRing<C::kStages> r;
     const int per = w.nt - w.t0;
@@ -401,7 +474,7 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
         // rows behind the length, inside the tensor, may hold anything: zeroed before the MMAs may read
         const long long valid = (static_cast<long long>(w.ql) << sh.gp_log2) - static_cast<long long>(tile) * kMhaTile;
         const bool fix = valid < kMhaTile && w.ql < sh.sq;
-        const uint32_t ab = smem_u32(fix ? s.fix : &s.a_full[r.stage]), bb = smem_u32(fix ? s.fix : &s.b_full[r.stage]);
+        const uint32_t ab = smem_u32(fix ? &s.fix[r.stage] : &s.a_full[r.stage]), bb = smem_u32(fix ? &s.fix[r.stage] : &s.b_full[r.stage]);
         if (lane == 0) {
             if (fix) {
                 mbar_arrive_expect_tx(ab, 2u * C::kTileBytes + kSideBytes);
@@ -409,41 +482,30 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
                 mbar_arrive_expect_tx(ab, C::kTileBytes + kSideBytes);
                 mbar_arrive_expect_tx(bb, C::kTileBytes);
             }
-            load_tile<C::kCh>(dst, mq, ab, head, token, w.e, pol);
+            load_tile_shared<C::kCh>(dst, mq, ab, head, token, half, w.e, w.rank, p.csize_k, pol);
             bulk_load(smem_u32(sd), src, kSideBytes, ab);
-            load_tile<C::kCh>(dst + C::kTileBytes, mg, bb, head, token, w.e, pol);
+            load_tile_shared<C::kCh>(dst + C::kTileBytes, mg, bb, head, token, half, w.e, w.rank, p.csize_k, pol);
         }
         if (fix) {
-            r.armed &= ~(1u << r.stage);  // (its copies complete on the fix barrier)
-            const uint32_t par = r.fixes & 1u;
-            ++r.fixes;
-            __syncwarp();
-            if (!warp_all(bwait(s.fix, par, s, p))) break;
-            mha_zero_rows(dst, static_cast<int>(valid), C::kCh, lane);
-            mha_zero_rows(dst + C::kTileBytes, static_cast<int>(valid), C::kCh, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&s.a_full[r.stage]));
-                mbar_arrive(smem_u32(&s.b_full[r.stage]));
-            }
+            if (!r.template fix<C>(s, p, static_cast<int>(valid), lane)) break;
         } else {
             r.arm();
         }
         r.next();
     }
-    if (lane == 0) r.drain(s, p);
+    if (lane == 0) r.drain(s, p, true);
     __syncwarp();
 }
 
 template <int T, int kSteps>
 __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
-    using C = BwdCfg<kSteps>;
+    using C = KvCfg<kSteps>;
     constexpr uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kSteps * 16, true);
     constexpr uint32_t tS = 0u, tX = 128u, tV = 256u, tK = 384u;
     constexpr uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
     const uint64_t kdesc = sw128_kmajor_desc(smem_u32(s.res)), vdesc = kdesc + second;
     const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
+    const uint16_t all = static_cast<uint16_t>((1u << p.csize_k) - 1u);
     auto wait = [&](uint64_t* bar, uint32_t par) { return warp_all(bwait(bar, par, s, p)); };
     auto score = [&](uint32_t st) {
         mma_ss<kSteps>(tS, kdesc, ring_k + st * stage_units, id_s);
@@ -484,7 +546,7 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
         tc_fence_after();
         if (elect_one()) {
             mma_ts<64>(tK, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
-            umma_commit(smem_u32(&s.empty[st]));
+            umma_commit_to(smem_u32(&s.empty[st]), all);
         }
         __syncwarp();
         if (more) {
@@ -496,17 +558,17 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
         st = st1;
         ph = ph1;
     }
-    mma_finish(s, p, ok);
+    mma_finish(s, p, ok, p.csize_k);
 }
 
 template <int T, int kSteps>
-__device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w, uint32_t tmem, int warp, int lane) {
-    using C = BwdCfg<kSteps>;
+__device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w, int warp, int lane) {
+    using C = KvCfg<kSteps>;
     const int quad = warp & 3, half = warp >> 2;
     const MhaShape& sh = p.s;
     const int j = w.kb * kMhaTile + quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
+    const uint32_t tS = lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
     const float c = ds_factor<T>(p.maxima);
     const float f = T == VAE_F16 ? c * (1.f / (1 << kPLog2)) : 1.f;  // dS c = (P 2^14) (dP - D) f
     // the first row of the group's packing that sees key j
@@ -606,7 +668,7 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
     const bool split = p.nsplit_k > 1;
     const MhaStrides os = half == 0 ? p.dvs : p.dks;
     const float g = half == 0 ? (T == VAE_F16 ? 1.f / (1 << kPLog2) : 1.f) : p.scale / c;
-    store_acc<T>(tmem + lane_off + 256u + static_cast<uint32_t>(half * 128), sh.d, j < w.kl, true, g,
+    store_acc<T>(lane_off + 256u + static_cast<uint32_t>(half * 128), sh.d, j < w.kl, true, g,
                  half == 0 ? p.dv : p.dk, w.e * os.b + j * os.s + w.hk * os.h, split ? p.part_kv : nullptr,
                  ((w.split * 2 + half) * rows + row) * sh.d);
 }
@@ -615,8 +677,9 @@ template <int T, int kSteps>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    const BwdSmem s = bwd_carve<kSteps>(smem_raw);
+    using C = KvCfg<kSteps>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];  // (the swizzled tiles lie on 1024-byte boundaries)
+    const BwdSmem s = bwd_carve<C>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const KvWork w = kv_work(p);
@@ -632,27 +695,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    const uint32_t tmem = bwd_begin<kSteps>(s, warp);
-    if (warp < kSoftWarps) kv_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
-    else if (warp == kTmaWarp) kv_producer<kSteps>(p, s, w, &mq, &mg, &mk, &mv, lane);
+    bwd_begin<C>(s, warp, p.csize_k, 1u);
+    if (warp < kSoftWarps) kv_softmax<T, kSteps>(p, s, w, warp, lane);
+    else if (warp == kTmaWarp) kv_producer<C>(p, s, w, &mq, &mg, &mk, &mv, lane);
     else kv_mma<T, kSteps>(p, s, w);
-    bwd_end(tmem, warp);
+    bwd_end(warp, p.csize_k);
 }
 
 // ───────────────────────────── dQ, per row tile ─────────────────────────────
 
 struct QWork {
-    int e, hk, sub, tile, split;
+    int e, hk, sub, tile, split, rank;
     int ql, kl;
-    int kb0, n;  // this split's key tiles
+    int kb0, n;  // this split's key tiles, the same for a cluster's CTAs
+    bool exact;  // D is formed here
 };
 
 __device__ __forceinline__ QWork q_work(const BwdParams& p) {
     const MhaShape& s = p.s;
     QWork w;
-    int r = blockIdx.x;
-    w.tile = s.ntile - 1 - r % s.ntile;  // the tiles that see the most keys first
-    r /= s.ntile;
+    const int nt = (s.ntile + p.csize_q - 1) / p.csize_q;
+    w.rank = static_cast<int>(blockIdx.x) % p.csize_q;
+    int r = blockIdx.x / p.csize_q;
+    const int t0 = (nt - 1 - r % nt) * p.csize_q;  // the tiles that see the most keys first
+    w.tile = t0 + w.rank;
+    r /= nt;
     w.split = r % p.nsplit_q;
     r /= p.nsplit_q;
     w.sub = r % s.nsub;
@@ -661,81 +728,67 @@ __device__ __forceinline__ QWork q_work(const BwdParams& p) {
     w.e = r / s.hkv;
     w.ql = mha_len(s.q_len, w.e, s.sq);
     w.kl = mha_len(s.k_len, w.e, s.sk);
-    const int i0 = (w.tile * kMhaTile) >> s.gp_log2;
-    int i1 = ((w.tile + 1) * kMhaTile - 1) >> s.gp_log2;
+    // the last row of the cluster's tiles sees the most keys
+    const int last = (t0 + p.csize_q < s.ntile ? t0 + p.csize_q : s.ntile) - 1;
+    const int i0 = (t0 * kMhaTile) >> s.gp_log2;
+    int i1 = ((last + 1) * kMhaTile - 1) >> s.gp_log2;
     if (i1 >= w.ql) i1 = w.ql - 1;
     const int lim = i0 < w.ql ? mha_key_limit(i1, w.ql, w.kl, s.block) : 0;
     const int all = (lim + kMhaTile - 1) / kMhaTile;
     const int per = (all + p.nsplit_q - 1) / p.nsplit_q;
     w.kb0 = w.split * per < all ? w.split * per : all;
     w.n = (w.kb0 + per < all ? w.kb0 + per : all) - w.kb0;
+    w.exact = p.nsplit_q == 1 && w.n <= kExactTiles;
     return w;
 }
 
-template <int kSteps>
-__device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w, const CUtensorMap* mq,
-                           const CUtensorMap* mg, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
-    using C = BwdCfg<kSteps>;
+template <typename C>
+__device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w, const CUtensorMap* mk,
+                           const CUtensorMap* mv, int lane) {
     const uint64_t pol = policy_evict_normal();
     const MhaShape& sh = p.s;
-    if (lane == 0) {
-        const uint32_t rb = smem_u32(s.res_full);
-        const int head = w.hk * sh.g + (w.sub << sh.gp_log2), token = (w.tile * kMhaTile) >> sh.gp_log2;
-        mbar_arrive_expect_tx(rb, 2u * C::kTileBytes);
-        load_tile<C::kCh>(s.res, mq, rb, head, token, w.e, pol);
-        load_tile<C::kCh>(s.res + C::kTileBytes, mg, rb, head, token, w.e, pol);
-    }
     BwdRing<C::kStages> r;
-    for (int x = 0; x < w.n; ++x) {
-        const int kb = w.kb0 + x;
+    const int steps = w.exact ? 2 * w.n : w.n;
+    for (int x = 0; x < steps; ++x) {
+        const int kb = w.kb0 + (x < w.n ? x : x - w.n);
         if (!warp_all(bwait(&s.empty[r.stage], r.phase ^ 1u, s, p))) break;
         uint8_t* dst = s.ring + r.stage * 2 * C::kTileBytes;
-        const bool fix = (kb + 1) * kMhaTile > w.kl && w.kl < sh.sk;  // the tile that the length ends in: the last
-        const uint32_t ab = smem_u32(fix ? s.fix : &s.a_full[r.stage]), bb = smem_u32(fix ? s.fix : &s.b_full[r.stage]);
+        const bool fix = (kb + 1) * kMhaTile > w.kl && w.kl < sh.sk;  // the tile that the length ends in
+        const uint32_t ab = smem_u32(fix ? &s.fix[r.stage] : &s.a_full[r.stage]), bb = smem_u32(fix ? &s.fix[r.stage] : &s.b_full[r.stage]);
         if (lane == 0) {
             mbar_arrive_expect_tx(ab, (fix ? 2u : 1u) * C::kTileBytes);
             if (!fix) mbar_arrive_expect_tx(bb, C::kTileBytes);
-            load_tile<C::kCh>(dst, mk, ab, w.hk, kb * kMhaTile, w.e, pol);
-            load_tile<C::kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, w.e, pol);
+            load_tile_shared<C::kCh>(dst, mk, ab, w.hk, kb * kMhaTile, 64, w.e, w.rank, p.csize_q, pol);
+            load_tile_shared<C::kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, 64, w.e, w.rank, p.csize_q, pol);
         }
         if (fix) {
-            r.armed &= ~(1u << r.stage);
-            const uint32_t par = r.fixes & 1u;
-            ++r.fixes;
-            __syncwarp();
-            if (!warp_all(bwait(s.fix, par, s, p))) break;
-            mha_zero_rows(dst, w.kl - kb * kMhaTile, C::kCh, lane);
-            mha_zero_rows(dst + C::kTileBytes, w.kl - kb * kMhaTile, C::kCh, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&s.a_full[r.stage]));
-                mbar_arrive(smem_u32(&s.b_full[r.stage]));
-            }
+            if (!r.template fix<C>(s, p, w.kl - kb * kMhaTile, lane)) break;
         } else {
             r.arm();
         }
         r.next();
     }
-    if (lane == 0) r.drain(s, p);
+    if (lane == 0) r.drain(s, p, false);
     __syncwarp();
 }
 
+constexpr uint32_t kTmemQ = 384u, kTmemG = 448u;  // the tile's Q and dO rows, 64 columns each
+
 template <int T, int kSteps>
 __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
-    using C = BwdCfg<kSteps>;
+    using C = QCfg<kSteps>;
     constexpr uint32_t id_s = mha_idesc(T, 128, 128, false), id_o = mha_idesc(T, 128, kSteps * 16, true);
     constexpr uint32_t tS = 0u, tX = 128u, tQ = 256u;
     constexpr uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
-    const uint64_t qdesc = sw128_kmajor_desc(smem_u32(s.res)), gdesc = qdesc + second;
     const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
+    const uint16_t all = static_cast<uint16_t>((1u << p.csize_q) - 1u);
     auto wait = [&](uint64_t* bar, uint32_t par) { return warp_all(bwait(bar, par, s, p)); };
     auto score = [&](uint32_t st) {
-        mma_ss<kSteps>(tS, qdesc, ring_k + st * stage_units, id_s);
+        mma_ts_k<kSteps>(tS, kTmemQ, ring_k + st * stage_units, id_s);
         umma_commit(smem_u32(s.s_full));
     };
     auto cross = [&](uint32_t st) {
-        mma_ss<kSteps>(tX, gdesc, ring_k + st * stage_units + second, id_s);
+        mma_ts_k<kSteps>(tX, kTmemG, ring_k + st * stage_units + second, id_s);
         umma_commit(smem_u32(s.x_full));
     };
     uint32_t st = 0, ph = 0;
@@ -748,9 +801,10 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
         }
         __syncwarp();
     }
-    for (int x = 0; ok && x < w.n; ++x) {
+    const int from = w.exact ? w.n : 0, steps = from + w.n;
+    for (int x = 0; ok && x < steps; ++x) {
         const uint32_t par = static_cast<uint32_t>(x) & 1u;
-        const bool more = x + 1 < w.n;
+        const bool more = x + 1 < steps;
         const bool wrap = st + 1 == C::kStages;
         const uint32_t st1 = wrap ? 0u : st + 1u, ph1 = wrap ? ph ^ 1u : ph;
         if (more) {  // S has been read
@@ -764,8 +818,8 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-            mma_ts<64>(tQ, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
-            umma_commit(smem_u32(&s.empty[st]));
+            if (x >= from) mma_ts<64>(tQ, tX, ring_m + st * stage_units, id_o, x != from ? 1u : 0u);
+            umma_commit_to(smem_u32(&s.empty[st]), all);
         }
         __syncwarp();
         if (more) {
@@ -777,28 +831,69 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
         st = st1;
         ph = ph1;
     }
-    mma_finish(s, p, ok);
+    mma_finish(s, p, ok, p.csize_q);
 }
 
 template <int T, int kSteps>
-__device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, uint32_t tmem, int warp, int lane) {
+__device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, int warp, int lane) {
     const int quad = warp & 3, half = warp >> 2;
     const MhaShape& sh = p.s;
     const int gp = 1 << sh.gp_log2;
     const int rr = quad * 32 + lane, r = w.tile * kMhaTile + rr;
     const int i = r >> sh.gp_log2, h = w.hk * sh.g + w.sub * gp + (r & (gp - 1));
-    const bool live = i < w.ql;
+    const bool here = w.tile < sh.ntile;  // (a cluster's last tile may be missing)
+    const bool live = here && i < w.ql;
     const int lim = live ? mha_key_limit(i, w.ql, w.kl, sh.block) : 0;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
-    const float* side = p.side + (((static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.nsub + w.sub) * sh.ntile + w.tile) * kSideFloats;
-    const float nl = side[rr], D = side[128 + rr];
+    const uint32_t tS = lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
+    // The row of Q (first four warps) or dO into TMEM, zeros behind the length and the channels.
+    {
+        const MhaStrides st = half == 0 ? p.qs : p.gs;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(half == 0 ? p.q : p.dout) +
+                                                          (live ? w.e * st.b + i * st.s + h * st.h : 0));
+#pragma unroll
+        for (int c = 0; c < kSteps / 2; ++c) {
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint4 x = live && (c * 4 + k) * 8 < sh.d ? src[c * 4 + k] : make_uint4(0u, 0u, 0u, 0u);
+                v[4 * k] = x.x;
+                v[4 * k + 1] = x.y;
+                v[4 * k + 2] = x.z;
+                v[4 * k + 3] = x.w;
+            }
+            __syncwarp();
+            tmem_st16((half == 0 ? kTmemQ : kTmemG) + lane_off + static_cast<uint32_t>(c * 16), v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(s.res_full));
+    }
+    float* side = p.side + (((static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.nsub + w.sub) * sh.ntile + (here ? w.tile : 0)) * kSideFloats;
+    const float nl = live ? side[rr] : -INFINITY;
+    float D = live ? side[128 + rr] : 0.f;
     const float c = ds_factor<T>(p.maxima);
     const float f = T == VAE_F16 ? c * (1.f / (1 << kPLog2)) : 1.f;
-    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl), D2 = make_float2(-D, -D);
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl);
+    float2 D2 = make_float2(-D, -D), sum = make_float2(0.f, 0.f);
+    const int from = w.exact ? w.n : 0, steps = from + w.n;
     bool ok = true;
-    for (int x = 0; x < w.n; ++x) {
+    for (int x = 0; x < steps; ++x) {
         const uint32_t par = static_cast<uint32_t>(x) & 1u;
+        if (w.exact && x == from) {
+            // D = rowsum(P dP): this half's sum and the other's, for the key-tile kernel too
+            float* trade = reinterpret_cast<float*>(s.side);
+            trade[half * kMhaTile + rr] = sum.x + sum.y;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.x_bar[quad]));
+            ok = warp_all(bwait(&s.x_bar[quad], 0u, s, p));
+            if (!ok) break;
+            const float all = *static_cast<volatile float*>(trade + rr) + *static_cast<volatile float*>(trade + kMhaTile + rr);
+            D = T == VAE_F16 ? all * (1.f / (1 << kPLog2)) : all;
+            if (half == 0 && live) side[128 + rr] = D;
+            D2 = make_float2(-D, -D);
+        }
         ok = warp_all(bwait(s.s_full, par, s, p));
         if (!ok) break;
         tc_fence_after();
@@ -815,7 +910,7 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
             pr[k] = mha_ex2(a.x);
             pr[k + 1] = mha_ex2(a.y);
         }
-        const int left = lim - (w.kb0 + x) * kMhaTile - half * 64;
+        const int left = lim - (w.kb0 + (x < w.n ? x : x - w.n)) * kMhaTile - half * 64;
         if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
             for (int k = 0; k < 64; ++k)
@@ -825,22 +920,30 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
         if (!ok) break;
         tc_fence_after();
         load64(tX, xr);
-        __syncwarp();
+        if (x < from) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t h2[16];
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const int at = k * 32 + 2 * u;
-                const uint32_t* y = xr[at >> 4] + (at & 15);
-                float2 a = add2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), D2);
-                a = mul2(a, make_float2(pr[at], pr[at + 1]));
-                if constexpr (T == VAE_F16) a = mul2(a, make_float2(f, f));
-                h2[u] = pack2<T>(a.x, a.y);
+            for (int k = 0; k < 64; k += 2) {
+                const uint32_t* y = xr[k >> 4] + (k & 15);
+                sum = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), make_float2(pr[k], pr[k + 1]), sum);
             }
-            tmem_st16(tX + static_cast<uint32_t>(k * 16), h2);
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t h2[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const int at = k * 32 + 2 * u;
+                    const uint32_t* y = xr[at >> 4] + (at & 15);
+                    float2 a = add2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), D2);
+                    a = mul2(a, make_float2(pr[at], pr[at + 1]));
+                    if constexpr (T == VAE_F16) a = mul2(a, make_float2(f, f));
+                    h2[u] = pack2<T>(a.x, a.y);
+                }
+                tmem_st16(tX + static_cast<uint32_t>(k * 16), h2);
+            }
+            tmem_st_wait();
         }
-        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(s.ds_full));
@@ -850,23 +953,23 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
     tc_fence_after();
     const long long rows = static_cast<long long>(sh.b) * sh.hq * sh.sq;
     const long long row = (static_cast<long long>(w.e) * sh.hq + h) * sh.sq + i;
-    store_acc<T>(tmem + lane_off + 256u, sh.d, live, true, p.scale / c, p.dq, w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h,
+    store_acc<T>(lane_off + 256u, sh.d, live, true, p.scale / c, p.dq, w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h,
                  p.nsplit_q > 1 ? p.part_q : nullptr, (w.split * rows + row) * sh.d);
 }
 
 template <int T, int kSteps>
 __global__ void __launch_bounds__(kThreads, 1)
-    mha_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
-                  const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    const BwdSmem s = bwd_carve<kSteps>(smem_raw);
+    mha_dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
+    using C = QCfg<kSteps>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];  // (the swizzled tiles lie on 1024-byte boundaries)
+    const BwdSmem s = bwd_carve<C>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const QWork w = q_work(p);
     if (w.n == 0) {  // no key: zeros within the length
         const int r = w.tile * kMhaTile + threadIdx.x;
         const int i = r >> p.s.gp_log2, h = w.hk * p.s.g + (w.sub << p.s.gp_log2) + (r & ((1 << p.s.gp_log2) - 1));
-        if (threadIdx.x < kMhaTile && i < w.ql) {
+        if (threadIdx.x < kMhaTile && w.tile < p.s.ntile && i < w.ql) {
             const long long rows = static_cast<long long>(p.s.b) * p.s.hq * p.s.sq;
             const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
             store_acc<T>(0u, p.s.d, true, false, 0.f, p.dq, w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h,
@@ -874,11 +977,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    const uint32_t tmem = bwd_begin<kSteps>(s, warp);
-    if (warp < kSoftWarps) q_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
-    else if (warp == kTmaWarp) q_producer<kSteps>(p, s, w, &mq, &mg, &mk, &mv, lane);
+    bwd_begin<C>(s, warp, p.csize_q, kSoftWarps);
+    if (warp < kSoftWarps) q_softmax<T, kSteps>(p, s, w, warp, lane);
+    else if (warp == kTmaWarp) q_producer<C>(p, s, w, &mk, &mv, lane);
     else q_mma<T, kSteps>(p, s, w);
-    bwd_end(tmem, warp);
+    bwd_end(warp, p.csize_q);
 }
 
 // ───────────────────────────── joining the splits ─────────────────────────────
@@ -910,9 +1013,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // Splits where tiles alone would leave SMs without work: two tiles of the other
-// side per CTA at least.
+// side per CTA at least. Clusters of two where every SM has work all the same.
 struct BwdPlan {
-    int nsplit_q, nsplit_k;
+    int nsplit_q, nsplit_k, csize_q, csize_k;
     long long q_items, k_items, row_tiles, key_tiles;
     size_t side, part_q, part_kv;  // floats
 };
@@ -922,12 +1025,15 @@ int splits(long long items, long long most) {
 }
 BwdPlan bwd_plan(const MhaShape& s) {
     BwdPlan f;
-    f.row_tiles = static_cast<long long>(s.b) * s.hkv * s.nsub * s.ntile;
-    f.key_tiles = static_cast<long long>(s.b) * s.hkv * s.nkb;
-    f.nsplit_q = splits(f.row_tiles, s.nkb);
+    const long long q_heads = static_cast<long long>(s.b) * s.hkv * s.nsub, k_heads = static_cast<long long>(s.b) * s.hkv;
+    f.row_tiles = q_heads * s.ntile;
+    f.key_tiles = k_heads * s.nkb;
+    f.csize_q = f.row_tiles >= kTargetCtas && s.ntile >= 2 ? 2 : 1;
+    f.csize_k = f.key_tiles >= kTargetCtas && s.nkb >= 2 ? 2 : 1;
+    f.nsplit_q = s.nkb <= kExactTiles ? 1 : splits(f.row_tiles, s.nkb);
     f.nsplit_k = splits(f.key_tiles, static_cast<long long>(s.nsub) * s.ntile);
-    f.q_items = f.row_tiles * f.nsplit_q;
-    f.k_items = f.key_tiles * f.nsplit_k;
+    f.q_items = q_heads * ((s.ntile + f.csize_q - 1) / f.csize_q * f.csize_q) * f.nsplit_q;
+    f.k_items = k_heads * ((s.nkb + f.csize_k - 1) / f.csize_k * f.csize_k) * f.nsplit_k;
     f.side = static_cast<size_t>(f.row_tiles) * kSideFloats;
     f.part_q = f.nsplit_q > 1 ? static_cast<size_t>(f.nsplit_q) * s.b * s.hq * s.sq * s.d : 0;
     f.part_kv = f.nsplit_k > 1 ? static_cast<size_t>(f.nsplit_k) * 2 * s.b * s.hkv * s.sk * s.d : 0;
@@ -935,29 +1041,46 @@ BwdPlan bwd_plan(const MhaShape& s) {
 }
 constexpr size_t kMaximaFloats = 64;  // two words used; keeps what follows aligned
 
+template <typename K, typename... Args>
+cudaError_t cluster_launch(K kernel, long long items, int csize, int smem, cudaStream_t st, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(csize);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 template <int T, int kSteps>
 int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap (&map)[4], const PrepParams& pp,
                const BwdParams& p, cudaStream_t st) {
     static CtxOnce once;
     static std::mutex mu;
-    using C = BwdCfg<kSteps>;
+    constexpr int kKvSmem = KvCfg<kSteps>::kSmem, kQSmem = QCfg<kSteps>::kSmem;
     {
         int dev;
         VAE_CUDA_CHECK(cudaGetDevice(&dev));
         std::lock_guard<std::mutex> lk(mu);
         if (!once.done(dev)) {
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dkv_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dq_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dkv_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem));
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dq_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem));
             once.mark(dev);
         }
     }
     if (T == VAE_F16) VAE_CUDA_CHECK(cudaMemsetAsync(pp.maxima, 0, 2 * sizeof(unsigned), st));
     const long long prep = f.row_tiles + (T == VAE_F16 ? f.key_tiles : 0);
     VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
-    VAE_CUDA_CHECK(launch_kernel(mha_dkv_kernel<T, kSteps>, dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), C::kSmem,
-                                 st, map[0], map[1], map[2], map[3], p));
-    VAE_CUDA_CHECK(launch_kernel(mha_dq_kernel<T, kSteps>, dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), C::kSmem,
-                                 st, map[0], map[1], map[2], map[3], p));
+    // (the query-tile kernel first: it may put its D into the side rows)
+    VAE_CUDA_CHECK(cluster_launch(mha_dq_kernel<T, kSteps>, f.q_items, f.csize_q, kQSmem, st, map[2], map[3], p));
+    VAE_CUDA_CHECK(cluster_launch(mha_dkv_kernel<T, kSteps>, f.k_items, f.csize_k, kKvSmem, st, map[0], map[1], map[2], map[3], p));
     const MhaShape& s = p.s;
     if (f.nsplit_k > 1) {
         const long long rows = static_cast<long long>(s.b) * s.hkv * s.sk;
@@ -991,10 +1114,10 @@ int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout
         return set_error(VAE_ERR_SHAPE, "attention: too many tiles");
     const int gp = 1 << s.gp_log2;
     CUtensorMap map[4];
-    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, kMhaTile / gp);
-    if (rc == VAE_OK) rc = mha_map(&map[1], a, dout, a->do_stride, s.sq, s.hq, gp, kMhaTile / gp);
-    if (rc == VAE_OK) rc = mha_map(&map[2], a, k, a->k_stride, s.sk, s.hkv, 1, kMhaTile);
-    if (rc == VAE_OK) rc = mha_map(&map[3], a, v, a->v_stride, s.sk, s.hkv, 1, kMhaTile);
+    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, 64 / gp);
+    if (rc == VAE_OK) rc = mha_map(&map[1], a, dout, a->do_stride, s.sq, s.hq, gp, 64 / gp);
+    if (rc == VAE_OK) rc = mha_map(&map[2], a, k, a->k_stride, s.sk, s.hkv, 1, 64);
+    if (rc == VAE_OK) rc = mha_map(&map[3], a, v, a->v_stride, s.sk, s.hkv, 1, 64);
     if (rc != VAE_OK) return rc;
     float* w = static_cast<float*>(ws);
     PrepParams pp{};
@@ -1015,6 +1138,12 @@ int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout
     p.scale_log2 = a->scale * 1.4426950408889634074f;
     p.nsplit_q = f.nsplit_q;
     p.nsplit_k = f.nsplit_k;
+    p.csize_q = f.csize_q;
+    p.csize_k = f.csize_k;
+    p.q = q;
+    p.dout = dout;
+    p.qs = mha_strides(a->q_stride);
+    p.gs = mha_strides(a->do_stride);
     p.side = pp.side;
     p.maxima = pp.maxima;
     p.dq = dq;

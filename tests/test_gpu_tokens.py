@@ -240,7 +240,11 @@ ATT = [(1, 1, 1, 1, 1, 8, "f16", 0, None, None), (1, 1, 130, 2, 1, 64, "bf16", 0
        (4, 1, 2000, 16, 4, 128, "bf16", 0, None, [2000, 1, 0, 777]), (4, 1, 999, 8, 1, 64, "f16", 7, None, [5, 999, 128, 129]),
        (3, 150, 160, 4, 2, 80, "f16", 0, [150, 0, 1], [160, 33, 0]), (3, 310, 310, 4, 4, 128, "bf16", 100, [310, 7, 131], [310, 9, 256]),
        (2, 64, 64, 12, 4, 16, "bf16", 3, [60, 64], [64, 20]), (1, 1100, 1100, 2, 1, 120, "f16", 0, None, None),
-       (1, 3, 5000, 32, 2, 128, "f16", 1, None, None), (2, 513, 640, 5, 5, 24, "bf16", 50, [400, 513], [640, 100])]
+       (1, 3, 5000, 32, 2, 128, "f16", 1, None, None), (2, 513, 640, 5, 5, 24, "bf16", 50, [400, 513], [640, 100]),
+       # enough tiles for every SM: tiles in pairs, an odd one left over
+       (4, 300, 310, 40, 40, 32, "f16", 0, [300, 0, 129, 1], [310, 128, 7, 300]),
+       (2, 1200, 1200, 16, 8, 64, "bf16", 70, [1200, 1030], [1200, 1100]), (1, 1300, 1300, 16, 16, 128, "f16", 1, None, None),
+       (1, 640, 1290, 40, 40, 128, "bf16", 0, None, [1290]), (3, 130, 258, 64, 64, 96, "f16", 33, [130, 128, 64], [258, 200, 129])]
 
 
 def _att_inputs(case, seed=11):
