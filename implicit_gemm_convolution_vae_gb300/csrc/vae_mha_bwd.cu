@@ -1012,28 +1012,44 @@ __global__ void __launch_bounds__(256)
         make_uint2(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w));
 }
 
-// Splits where tiles alone would leave SMs without work: two tiles of the other
-// side per CTA at least. Clusters of two where every SM has work all the same.
+// Clusters of two where every SM has work all the same, and the number of splits
+// of the other side whose waves of CTAs take the shortest time, by what the
+// parts measured on GB300 (microseconds): a tile of the other side 1.4 (query
+// tiles) and 1.8 (key tiles), a CTA's set-up and end 5, the joining kernel 3 and
+// its traffic at 6 TB/s.
 struct BwdPlan {
     int nsplit_q, nsplit_k, csize_q, csize_k;
     long long q_items, k_items, row_tiles, key_tiles;
     size_t side, part_q, part_kv;  // floats
 };
-int splits(long long items, long long most) {
-    const long long want = items < kTargetCtas ? kTargetCtas / items : 1;
-    return static_cast<int>(std::max<long long>(1, std::min(want, most / 2)));
+// heads x tiles CTAs against `other` tiles; `sum`: elements that a split writes and the join reads.
+void split_plan(long long heads, int tiles, long long other, double tile_us, double sum, int most, int* nsplit, int* csize,
+                long long* items) {
+    *csize = heads * tiles >= kTargetCtas && tiles >= 2 ? 2 : 1;
+    const long long each = heads * ((tiles + *csize - 1) / *csize * *csize);
+    double least = 0.0;
+    for (int n = 1; n == 1 || (n <= most && each * n <= 8 * kTargetCtas); ++n) {
+        const double waves = static_cast<double>((each * n - 1) / kTargetCtas + 1);
+        double t = waves * (static_cast<double>((other - 1) / n + 1) * tile_us + 5.0);
+        if (n > 1) t += 3.0 + 8.0 * n * sum / 6e6;
+        if (n == 1 || t < least) {
+            least = t;
+            *nsplit = n;
+        }
+    }
+    *items = each * *nsplit;
 }
 BwdPlan bwd_plan(const MhaShape& s) {
     BwdPlan f;
     const long long q_heads = static_cast<long long>(s.b) * s.hkv * s.nsub, k_heads = static_cast<long long>(s.b) * s.hkv;
+    const long long row_tiles = static_cast<long long>(s.nsub) * s.ntile;
     f.row_tiles = q_heads * s.ntile;
     f.key_tiles = k_heads * s.nkb;
-    f.csize_q = f.row_tiles >= kTargetCtas && s.ntile >= 2 ? 2 : 1;
-    f.csize_k = f.key_tiles >= kTargetCtas && s.nkb >= 2 ? 2 : 1;
-    f.nsplit_q = s.nkb <= kExactTiles ? 1 : splits(f.row_tiles, s.nkb);
-    f.nsplit_k = splits(f.key_tiles, static_cast<long long>(s.nsub) * s.ntile);
-    f.q_items = q_heads * ((s.ntile + f.csize_q - 1) / f.csize_q * f.csize_q) * f.nsplit_q;
-    f.k_items = k_heads * ((s.nkb + f.csize_k - 1) / f.csize_k * f.csize_k) * f.nsplit_k;
+    // (two tiles of the other side a CTA at least; rows that meet few keys are not split: they form their D)
+    split_plan(q_heads, s.ntile, s.nkb, 1.4, static_cast<double>(s.b) * s.hq * s.sq * s.d,
+               s.nkb <= kExactTiles ? 1 : s.nkb / 2, &f.nsplit_q, &f.csize_q, &f.q_items);
+    split_plan(k_heads, s.nkb, row_tiles, 1.8, 2.0 * s.b * s.hkv * s.sk * s.d,
+               static_cast<int>(std::min<long long>(row_tiles / 2, 1 << 20)), &f.nsplit_k, &f.csize_k, &f.k_items);
     f.side = static_cast<size_t>(f.row_tiles) * kSideFloats;
     f.part_q = f.nsplit_q > 1 ? static_cast<size_t>(f.nsplit_q) * s.b * s.hq * s.sq * s.d : 0;
     f.part_kv = f.nsplit_k > 1 ? static_cast<size_t>(f.nsplit_k) * 2 * s.b * s.hkv * s.sk * s.d : 0;

@@ -13,8 +13,10 @@
 //   read once for 256 rows.
 //   One query tile (alt, where there are too few tiles to fill the GPU): the
 //   streams take every other key tile and their (m, l, O) join at the end
-//   through shared memory; the keys are further split over CTAs, whose f32
-//   partial rows a second kernel joins in a fixed order.
+//   through shared memory.
+// In either form the keys may be split over CTAs, whose f32 partial rows a
+// second kernel joins in a fixed order: for single tokens over a long cache, and
+// where a last wave of CTAs would leave most SMs without work.
 //
 // P is held as 2^(S - m + kBias) with m moved only when the new maximum is 2^8
 // over it: at most 2^14, exact scaling, and f16 keeps P down to 2^-20 of the
@@ -50,12 +52,12 @@ static_assert(FwdCfg<8>::kSmem <= 232448 && FwdCfg<4>::kSmem <= 232448, "attenti
 
 struct FwdParams {
     MhaShape s;
-    int alt, nsplit, bps;  // key tiles per split
+    int alt, nsplit;  // with nsplit > 1: nsplit * b pieces of key tiles, shared out by the entries' lengths
     float scale_log2;
     void* o;
     MhaStrides os;
     float* lse;
-    float *po, *plse;  // partials of the splits: [nsplit][b * hq * sq][d], [nsplit][b * hq * sq] (log2)
+    float *po, *plse;  // the pieces' partial rows: [nsplit * b][hq * sq][d], [nsplit * b][hq * sq] (log2)
     DevStatus* status;
     unsigned long long timeout_ns;
 };
@@ -100,7 +102,7 @@ __device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, const FwdS
 struct FwdWork {
     int e, hk, sub;   // batch entry, key head, part of the group
     int tile[2];      // the streams' 128-row tiles (alt: the same)
-    int split;
+    int piece;        // which partial rows (nsplit > 1)
     int ql, kl;
     int kb0, n;       // key tiles [kb0, kb0 + n)
     int streams;
@@ -114,6 +116,57 @@ __device__ __forceinline__ int tile_limit(const MhaShape& s, int tile, int ql, i
     return mha_key_limit(i1, ql, kl, s.block);
 }
 
+// How nsplit * b pieces are shared out: each entry's key tiles in runs of
+// `run`, the shortest for which the runs of all entries are no more than the
+// pieces. Long caches beside short ones then give every CTA about as much.
+// (The whole warp, converged; `first` of an entry is the number of runs before it.)
+struct Pieces {
+    int run, first, count, e;
+};
+__device__ __forceinline__ int key_tiles(const MhaShape& s, int e) {
+    return (mha_len(s.k_len, e, s.sk) + kMhaTile - 1) / kMhaTile;
+}
+__device__ __forceinline__ int piece_run(const MhaShape& s, int pieces) {
+    const int lane = threadIdx.x & 31;
+    int all = 0;
+    for (int e = lane; e < s.b; e += 32) all += key_tiles(s, e);
+    all = __reduce_add_sync(0xffffffffu, all);
+    for (int run = all > pieces ? (all - 1) / pieces + 1 : 1;; ++run) {  // (ends: one run an entry is enough at last)
+        int n = 0;
+        for (int e = lane; e < s.b; e += 32) n += (key_tiles(s, e) + run - 1) / run;
+        if (__reduce_add_sync(0xffffffffu, n) <= pieces) return run;
+    }
+}
+// The entry that piece `at` belongs to (e = b: none), or the runs of entry `of` (at < 0).
+__device__ __forceinline__ Pieces find_piece(const MhaShape& s, int pieces, int at, int of) {
+    const int lane = threadIdx.x & 31;
+    Pieces r;
+    r.run = piece_run(s, pieces);
+    r.e = s.b;
+    r.first = r.count = 0;
+    int before = 0;
+    for (int e0 = 0; e0 < s.b; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < s.b ? (key_tiles(s, e) + r.run - 1) / r.run : 0;
+        int upto = n;  // inclusive scan
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int first = before + upto - n;
+        const unsigned hit = __ballot_sync(0xffffffffu, at < 0 ? e == of : (at >= first && at < first + n));
+        if (hit != 0u) {
+            const int l = __ffs(static_cast<int>(hit)) - 1;
+            r.first = __shfl_sync(0xffffffffu, first, l);
+            r.count = __shfl_sync(0xffffffffu, n, l);
+            r.e = e0 + l;
+            return r;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return r;
+}
+
 __device__ __forceinline__ FwdWork fwd_work(const FwdParams& p) {
     const MhaShape& s = p.s;
     FwdWork w;
@@ -121,20 +174,29 @@ __device__ __forceinline__ FwdWork fwd_work(const FwdParams& p) {
     int r = blockIdx.x;
     const int t = nt - 1 - r % nt;  // the last tiles see the most keys where blocks limit them: first
     r /= nt;
-    w.split = r % p.nsplit;
-    r /= p.nsplit;
+    w.piece = r % (p.nsplit * s.b);
+    r /= p.nsplit * s.b;
     w.sub = r % s.nsub;
-    r /= s.nsub;
-    w.hk = r % s.hkv;
-    w.e = r / s.hkv;
+    w.hk = r / s.nsub;
+    int run = s.nkb, at = 0;
+    w.e = w.piece;
+    w.n = 0;
+    w.streams = 0;
     w.tile[0] = p.alt ? t : 2 * t;
     w.tile[1] = p.alt ? t : 2 * t + 1;
+    if (p.nsplit > 1) {
+        const Pieces x = find_piece(s, p.nsplit * s.b, w.piece, 0);
+        w.e = x.e;
+        run = x.run;
+        at = w.piece - x.first;
+        if (w.e == s.b) return w;  // no piece left
+    }
     w.ql = mha_len(s.q_len, w.e, s.sq);
     w.kl = mha_len(s.k_len, w.e, s.sk);
     const int l0 = tile_limit(s, w.tile[0], w.ql, w.kl), l1 = p.alt ? 0 : tile_limit(s, w.tile[1], w.ql, w.kl);
     const int nb = ((l0 > l1 ? l0 : l1) + kMhaTile - 1) / kMhaTile;
-    w.kb0 = w.split * p.bps;
-    const int end = w.kb0 + p.bps < nb ? w.kb0 + p.bps : nb;
+    w.kb0 = at * run;
+    const int end = w.kb0 + run < nb ? w.kb0 + run : nb;
     w.n = end > w.kb0 ? end - w.kb0 : 0;
     w.streams = p.alt ? (w.n >= 2 ? 2 : 1) : ((w.tile[1] * kMhaTile) >> s.gp_log2) < w.ql && w.tile[1] < s.ntile ? 2 : 1;
     return w;
@@ -296,6 +358,7 @@ __device__ void fwd_store(const FwdParams& p, const FwdWork& w, uint32_t tO, int
                           const float* o1, float w1, float inv, float lse2) {
     const int d = p.s.d;
     const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
+    const long long prow = (static_cast<long long>(w.piece) * p.s.hq + h) * p.s.sq + i;
     for (int c = 0; c < d; c += 16) {
         uint32_t r[16];
         __syncwarp();
@@ -313,13 +376,13 @@ __device__ void fwd_store(const FwdParams& p, const FwdWork& w, uint32_t tO, int
                 v[k] *= inv;
             }
             if (p.nsplit > 1)
-                store8<VAE_F32>(p.po + (static_cast<long long>(w.split) * p.s.b * p.s.hq * p.s.sq + row) * d + c + u, v);
+                store8<VAE_F32>(p.po + prow * d + c + u, v);
             else
                 store8<T>(static_cast<typename Elem<T>::type*>(p.o) + w.e * p.os.b + i * p.os.s + h * p.os.h + c + u, v);
         }
     }
     if (!live) return;
-    if (p.nsplit > 1) p.plse[static_cast<long long>(w.split) * p.s.b * p.s.hq * p.s.sq + row] = lse2;
+    if (p.nsplit > 1) p.plse[prow] = lse2;
     else p.lse[row] = lse2 * 0.69314718055994530942f;
 }
 
@@ -461,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const FwdWork w = fwd_work(p);
+    if (w.e == p.s.b) return;  // more pieces than runs of key tiles
     if (w.n == 0) {  // no key: rows within the length give 0 and -infinity
         const int gp = 1 << p.s.gp_log2;
         for (int t = 0; t < (p.alt ? 1 : 2); ++t) {
@@ -469,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (threadIdx.x >= kMhaTile || w.tile[t] >= p.s.ntile || i >= w.ql) continue;
             const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
             if (p.nsplit > 1) {
-                p.plse[static_cast<long long>(w.split) * p.s.b * p.s.hq * p.s.sq + row] = -INFINITY;
+                p.plse[(static_cast<long long>(w.piece) * p.s.hq + h) * p.s.sq + i] = -INFINITY;
             } else {
                 const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                 for (int c = 0; c < p.s.d; c += 8)
@@ -521,31 +585,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the splits' partial rows: a warp per row, splits in order.
+// Joins the pieces' partial rows: a warp per row, pieces in order.
 template <int T>
 __global__ void __launch_bounds__(128) mha_join_kernel(const FwdParams p) {
     pdl_wait();
     const MhaShape& s = p.s;
-    const long long rows = static_cast<long long>(s.b) * s.hq * s.sq;
+    const long long rows = static_cast<long long>(s.b) * s.hq * s.sq, per = static_cast<long long>(s.hq) * s.sq;
     const long long row = static_cast<long long>(blockIdx.x) * 4 + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     if (row >= rows) return;
     const int i = static_cast<int>(row % s.sq), h = static_cast<int>(row / s.sq % s.hq);
-    const int e = static_cast<int>(row / s.sq / s.hq);
+    const int e = static_cast<int>(row / per);
     if (i >= mha_len(s.q_len, e, s.sq)) return;
+    const Pieces x = find_piece(s, p.nsplit * s.b, -1, e);
+    const long long row0 = x.first * per + (row - e * per);  // its place in the entry's first piece
     float mm = -INFINITY;
-    for (int k = lane; k < p.nsplit; k += 32) mm = fmaxf(mm, p.plse[k * rows + row]);
+    for (int k = lane; k < x.count; k += 32) mm = fmaxf(mm, p.plse[k * per + row0]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     float ll = 0.f;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < p.nsplit; ++k) {
-        const float x = p.plse[k * rows + row];
-        if (x == -INFINITY) continue;
-        const float wt = mha_ex2(x - mm);
+#pragma unroll 4
+    for (int k = 0; k < x.count; ++k) {
+        const float y = p.plse[k * per + row0];
+        const bool some = y != -INFINITY;  // (a piece that the row sees nothing of has written nothing else)
+        const float wt = some ? mha_ex2(y - mm) : 0.f;
         ll += wt;
-        if (lane * 4 < s.d) {
-            const float4 f = *reinterpret_cast<const float4*>(p.po + (k * rows + row) * s.d + lane * 4);
+        if (some && lane * 4 < s.d) {
+            const float4 f = *reinterpret_cast<const float4*>(p.po + (k * per + row0) * s.d + lane * 4);
             v[0] += f.x * wt;
             v[1] += f.y * wt;
             v[2] += f.z * wt;
@@ -561,31 +628,32 @@ __global__ void __launch_bounds__(128) mha_join_kernel(const FwdParams p) {
     if (lane == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
 }
 
-// Pair form where 256-row work items give every SM one; else one tile per CTA
-// with the keys split so that about every SM has work, two key tiles (one per
-// stream) per CTA at least.
+// The form and the number of splits whose waves of CTAs take the shortest time,
+// by what the parts measured on GB300 (microseconds): a key tile 1.65 in the
+// pair form (two row tiles) and 1.2 in the other, a CTA's set-up and end 4, the
+// joining kernel 3 and its traffic at 6 TB/s.
 struct FwdPlan {
-    int alt, nsplit, bps;
+    int alt, nsplit;
     long long items;
 };
 FwdPlan fwd_plan(const MhaShape& s) {
-    FwdPlan f;
-    const long long heads = static_cast<long long>(s.b) * s.hkv * s.nsub;
-    const long long pairs = heads * ((s.ntile + 1) / 2);
-    f.alt = pairs < kTargetCtas;
-    f.nsplit = 1;
-    f.bps = s.nkb;
-    f.items = pairs;
-    if (f.alt) {
-        f.items = heads * s.ntile;
-        const long long want = kTargetCtas / f.items, most = s.nkb / 2;
-        long long n = want < most ? want : most;
-        if (n < 1) n = 1;
-        f.bps = static_cast<int>((s.nkb + n - 1) / n);
-        f.nsplit = (s.nkb + f.bps - 1) / f.bps;
+    FwdPlan best{};
+    double least = 0.0;
+    const long long heads = static_cast<long long>(s.hkv) * s.nsub;
+    for (int alt = 0; alt < 2; ++alt) {
+        const long long items = heads * s.b * (alt ? s.ntile : (s.ntile + 1) / 2);
+        const int most = s.nkb / 2;  // two key tiles a CTA at least
+        for (int n = 1; n == 1 || (n <= most && items * n <= 8 * kTargetCtas); ++n) {
+            const double waves = static_cast<double>((items * n - 1) / kTargetCtas + 1);
+            double t = waves * (((s.nkb - 1) / n + 1) * (alt ? 1.2 : 1.65) + 4.0);
+            if (n > 1) t += 3.0 + 8.0 * n * s.b * s.hq * s.sq * s.d / 6e6;
+            if (best.items == 0 || t < least) {
+                least = t;
+                best = {alt, n, items * n};
+            }
+        }
     }
-    f.items *= f.nsplit;
-    return f;
+    return best;
 }
 
 template <int T, int kSteps>
@@ -636,7 +704,6 @@ int mha_fwd_run(const vae_attention_desc* a, const MhaShape& s, const void* q, c
     p.s = s;
     p.alt = f.alt;
     p.nsplit = f.nsplit;
-    p.bps = f.bps;
     p.scale_log2 = a->scale * 1.4426950408889634074f;
     p.o = o;
     p.os = mha_strides(a->o_stride);
