@@ -14,6 +14,10 @@
 //   One query tile (alt, where there are too few tiles to fill the GPU): the
 //   streams take every other key tile and their (m, l, O) join at the end
 //   through shared memory.
+//   Few rows (narrow: 32 at most, as for single tokens): one tile holds its rows
+//   four times, once per TMEM lane quadrant, and each quadrant's warp takes a
+//   quarter of the keys, so that the softmax of a few rows is not one warp's
+//   chain of 128 keys; eight partial (m, l, O) join at the end.
 // In either form the keys may be split over CTAs, whose f32 partial rows a
 // second kernel joins in a fixed order: for single tokens over a long cache, and
 // where a last wave of CTAs would leave most SMs without work.
@@ -52,7 +56,8 @@ static_assert(FwdCfg<8>::kSmem <= 232448 && FwdCfg<4>::kSmem <= 232448, "attenti
 
 struct FwdParams {
     MhaShape s;
-    int alt, nsplit;  // with nsplit > 1: nsplit * b pieces of key tiles, shared out by the entries' lengths
+    int alt, narrow;  // narrow: alt with the rows in every quadrant
+    int nsplit;       // with nsplit > 1: nsplit * b pieces of key tiles, shared out by the entries' lengths
     float scale_log2;
     void* o;
     MhaStrides os;
@@ -215,8 +220,9 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
         mbar_arrive_expect_tx(smem_u32(s.q_full), static_cast<uint32_t>(nq * C::kTileBytes));
         for (int t = 0; t < nq; ++t)
             for (int c = 0; c < C::kCh; ++c)
-                tma_load_4d(smem_u32(s.q + t * C::kTileBytes + c * kMhaChunkBytes), mq, smem_u32(s.q_full), c * 64, h0,
-                            (w.tile[t] * kMhaTile) >> p.s.gp_log2, w.e, pol);
+                for (int r = 0; r < (p.narrow ? 4 : 1); ++r)  // (narrow: the map's boxes are 32 rows)
+                    tma_load_4d(smem_u32(s.q + t * C::kTileBytes + c * kMhaChunkBytes + r * (kMhaChunkBytes / 4)), mq,
+                                smem_u32(s.q_full), c * 64, h0, (w.tile[t] * kMhaTile) >> p.s.gp_log2, w.e, pol);
     }
     const int ahead = p.alt ? 2 : 1;
     int stage = 0;
@@ -514,6 +520,149 @@ __device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork&
     }
 }
 
+// The narrow form's softmax: every quadrant holds the same 32 rows; its warp
+// takes 32 of a tile's 128 keys.
+template <int T, int kSteps>
+__device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const FwdWork& w, int warp, int lane) {
+    constexpr float kBias = T == VAE_F16 ? 6.f : 0.f;
+    const int t = warp >> 2, quad = warp & 3;
+    const int gp = 1 << p.s.gp_log2;
+    const auto row_of = [&](int r, int* i, int* h) {
+        *i = r >> p.s.gp_log2;
+        *h = w.hk * p.s.g + w.sub * gp + (r & (gp - 1));
+    };
+    int i, h;
+    row_of(lane, &i, &h);
+    const bool live = i < w.ql;
+    const int lim = live ? mha_key_limit(i, w.ql, w.kl, p.s.block) : 0;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = lane_off + static_cast<uint32_t>(t * 128), tO = tS + 256u;
+    const int dn = (p.s.d + 15) / 16 * 16;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    uint32_t par = 0;
+    for (int j = t; j < w.n; j += 2, par ^= 1u) {
+        ok = warp_all(fwait(&s.s_full[t], par, s, p));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[2][16];
+        __syncwarp();
+        tmem_ld16(tS + static_cast<uint32_t>(quad * 32), x[0]);
+        tmem_ld16(tS + static_cast<uint32_t>(quad * 32 + 16), x[1]);
+        tmem_ld_wait_regs(x[0]);
+        tmem_ld_wait_regs(x[1]);
+        const int left = lim - (w.kb0 + j) * kMhaTile - quad * 32;
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if (k >= left) x[0][k] = 0xff800000u;  // -infinity
+            if (16 + k >= left) x[1][k] = 0xff800000u;
+            mx[0] = fmaxf(mx[0], __uint_as_float(x[0][k]));
+            mx[1] = fmaxf(mx[1], __uint_as_float(x[1][k]));
+        }
+        const float top = fmaxf(mx[0], mx[1]) * p.scale_log2;
+        if (j < 2) {
+            m = top;
+        } else {
+            const bool up = top > m + 8.f;
+            if (__any_sync(0xffffffffu, up)) {
+                const float alpha = up ? mha_ex2(m - top) : 1.f;
+                if (up) m = top;
+                l *= alpha;
+                for (int c = 0; c < dn; c += 16) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    tmem_ld16(tO + static_cast<uint32_t>(c), o);
+                    tmem_ld_wait_regs(o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                    tmem_st16(tO + static_cast<uint32_t>(c), o);
+                }
+            }
+        }
+        const float sub = m == -INFINITY ? 0.f : kBias - m;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), sub2 = make_float2(sub, sub);
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t h2[16], zero[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const uint32_t* y = x[k >> 3] + 2 * (k & 7);
+            float2 f = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, sub2);
+            f.x = mha_ex2(f.x);
+            f.y = mha_ex2(f.y);
+            sum = add2(sum, f);
+            h2[k] = pack2<T>(f.x, f.y);
+            zero[k] = 0u;
+        }
+        l += sum.x + sum.y;
+        __syncwarp();
+        // the other quadrants' keys count as 0 in these lanes
+        tmem_st16(tS + static_cast<uint32_t>(quad * 16), h2);
+        tmem_st16(tS + static_cast<uint32_t>((quad ^ 1) * 16), zero);
+        tmem_st16(tS + static_cast<uint32_t>((quad ^ 2) * 16), zero);
+        tmem_st16(tS + static_cast<uint32_t>((quad ^ 3) * 16), zero);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.p_full[t]));
+    }
+    // The parts pass through the ring, which every MMA has read once both streams are done: [part][channel][32 rows].
+    const int parts = w.streams * 4;
+    const bool runs = t < w.streams;
+    if (ok) ok = warp_all(fwait(&s.o_full[0], 0u, s, p) && (w.streams == 1 || fwait(&s.o_full[1], 0u, s, p)));
+    float* o = reinterpret_cast<float*>(s.ring);
+    float* ml = o + 8 * dn * 32;  // [2][8 parts][32 rows]
+    if (ok && runs) {
+        tc_fence_after();
+        for (int c = 0; c < dn; c += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tmem_ld16(tO + static_cast<uint32_t>(c), v);
+            tmem_ld_wait_regs(v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[(warp * dn + c + k) * 32 + lane] = __uint_as_float(v[k]);
+        }
+        ml[warp * 32 + lane] = m;
+        ml[256 + warp * 32 + lane] = l;
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");  // (every softmax warp comes here, timed out or not)
+    if (!ok || *static_cast<volatile int*>(s.abort_flag) != 0) return;
+    // a row per lane, a slice of the channels per warp
+    float mm = -INFINITY;
+    for (int k = 0; k < parts; ++k) mm = fmaxf(mm, ml[k * 32 + lane]);
+    float wt[8], ll = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float mk = k < parts ? ml[k * 32 + lane] : -INFINITY;
+        wt[k] = mk == -INFINITY ? 0.f : mha_ex2(mk - mm);
+        if (k < parts) ll += wt[k] * ml[256 + k * 32 + lane];
+    }
+    if (!live) return;
+    const float inv = mm == -INFINITY ? 0.f : 1.f / ll;
+    const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
+    const long long prow = (static_cast<long long>(w.piece) * p.s.hq + h) * p.s.sq + i;
+    for (int c = warp * 8; c < p.s.d; c += 64) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < parts) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] += wt[k] * o[(k * dn + c + u) * 32 + lane];
+            }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] *= inv;
+        if (p.nsplit > 1)
+            store8<VAE_F32>(p.po + prow * p.s.d + c, v);
+        else
+            store8<T>(static_cast<typename Elem<T>::type*>(p.o) + w.e * p.os.b + i * p.os.s + h * p.os.h + c, v);
+    }
+    if (warp == 0) {
+        const float lse2 = mm == -INFINITY ? -INFINITY : mm - kBias + log2f(ll);
+        if (p.nsplit > 1) p.plse[prow] = lse2;
+        else p.lse[row] = lse2 * 0.69314718055994530942f;
+    }
+}
+
 template <int T, int kSteps>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -568,7 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     constexpr uint32_t tmem = 0u;  // all 512 columns are this CTA's: they start at 0
     if (warp < kSoftWarps) {
-        fwd_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
+        if (p.narrow) fwd_softmax_narrow<T, kSteps>(p, s, w, warp, lane);
+        else fwd_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
     } else if (warp == kTmaWarp) {
         fwd_producer<kSteps>(p, s, w, &mq, &mk, &mv, lane);
     } else {
@@ -633,14 +783,14 @@ __global__ void __launch_bounds__(128) mha_join_kernel(const FwdParams p) {
 // pair form (two row tiles) and 1.2 in the other, a CTA's set-up and end 4, the
 // joining kernel 3 and its traffic at 6 TB/s.
 struct FwdPlan {
-    int alt, nsplit;
+    int alt, narrow, nsplit;
     long long items;
 };
 FwdPlan fwd_plan(const MhaShape& s) {
     FwdPlan best{};
     double least = 0.0;
     const long long heads = static_cast<long long>(s.hkv) * s.nsub;
-    for (int alt = 0; alt < 2; ++alt) {
+    for (int alt = s.ntile == 1; alt < 2; ++alt) {
         const long long items = heads * s.b * (alt ? s.ntile : (s.ntile + 1) / 2);
         const int most = s.nkb / 2;  // two key tiles a CTA at least
         for (int n = 1; n == 1 || (n <= most && items * n <= 8 * kTargetCtas); ++n) {
@@ -649,7 +799,7 @@ FwdPlan fwd_plan(const MhaShape& s) {
             if (n > 1) t += 3.0 + 8.0 * n * s.b * s.hq * s.sq * s.d / 6e6;
             if (best.items == 0 || t < least) {
                 least = t;
-                best = {alt, n, items * n};
+                best = {alt, alt && s.sq << s.gp_log2 <= 32, n, items * n};
             }
         }
     }
@@ -696,13 +846,14 @@ int mha_fwd_run(const vae_attention_desc* a, const MhaShape& s, const void* q, c
     if (f.items > 0x7fffffffLL) return set_error(VAE_ERR_SHAPE, "attention: too many tiles");
     const int gp = 1 << s.gp_log2;
     CUtensorMap map[3];
-    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, kMhaTile / gp);
+    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, (f.narrow ? 32 : kMhaTile) / gp);
     if (rc == VAE_OK) rc = mha_map(&map[1], a, k, a->k_stride, s.sk, s.hkv, 1, kMhaTile);
     if (rc == VAE_OK) rc = mha_map(&map[2], a, v, a->v_stride, s.sk, s.hkv, 1, kMhaTile);
     if (rc != VAE_OK) return rc;
     FwdParams p{};
     p.s = s;
     p.alt = f.alt;
+    p.narrow = f.narrow;
     p.nsplit = f.nsplit;
     p.scale_log2 = a->scale * 1.4426950408889634074f;
     p.o = o;
