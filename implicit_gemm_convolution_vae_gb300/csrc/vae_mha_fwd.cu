@@ -753,20 +753,28 @@ __global__ void __launch_bounds__(128) mha_join_kernel(const FwdParams p) {
     for (int k = lane; k < x.count; k += 32) mm = fmaxf(mm, p.plse[k * per + row0]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    // Eight pieces' loads in flight together; a piece that the row sees nothing of has written nothing but its -infinity.
     float ll = 0.f;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = 0; k < x.count; ++k) {
-        const float y = p.plse[k * per + row0];
-        const bool some = y != -INFINITY;  // (a piece that the row sees nothing of has written nothing else)
-        const float wt = some ? mha_ex2(y - mm) : 0.f;
-        ll += wt;
-        if (some && lane * 4 < s.d) {
-            const float4 f = *reinterpret_cast<const float4*>(p.po + (k * per + row0) * s.d + lane * 4);
-            v[0] += f.x * wt;
-            v[1] += f.y * wt;
-            v[2] += f.z * wt;
-            v[3] += f.w * wt;
+    const int c = lane * 4 < s.d ? lane * 4 : 0;
+    for (int k0 = 0; k0 < x.count; k0 += 8) {
+        float y[8];
+        float4 f[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int k = k0 + u < x.count ? k0 + u : x.count - 1;
+            y[u] = p.plse[k * per + row0];
+            f[u] = *reinterpret_cast<const float4*>(p.po + (k * per + row0) * s.d + c);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (k0 + u >= x.count || y[u] == -INFINITY) continue;
+            const float wt = mha_ex2(y[u] - mm);
+            ll += wt;
+            v[0] += f[u].x * wt;
+            v[1] += f[u].y * wt;
+            v[2] += f[u].z * wt;
+            v[3] += f[u].w * wt;
         }
     }
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
