@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kWarp ? kLnBwdWarps * 32 : 512)
     ln_bwd_kernel(const void* __restrict__ dy, int dyt, const void* x, int xt, int m, int c,
                   const float* __restrict__ gamma, float eps, void* dx, float* __restrict__ part) {
     __shared__ float red[4][32];
-    extern __shared__ float cols[];  // (one-warp form) the warps' column sums, [2][c]
+    extern __shared__ float cols[];  // (one-warp form) the warps' column sums, [warps][2][c]
     pdl_wait();
     const int nt = kWarp ? 32 : blockDim.x;
     const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x;
@@ -222,22 +222,24 @@ __global__ void __launch_bounds__(kWarp ? kLnBwdWarps * 32 : 512)
     if (part == nullptr) return;
     float* out = part + static_cast<size_t>(blockIdx.x) * 2 * c;
     if constexpr (kWarp) {
-        for (int u = 0; u < kLnBwdWarps; ++u) {
-            if (warp == u) {
+        // the warps' sums side by side, then joined in order
 #pragma unroll
-                for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = elem_at<kV8>(k, e, tid, nt);
-                        if (i < c) {
-                            cols[i] = u == 0 ? dg[k][e] : cols[i] + dg[k][e];
-                            cols[c + i] = u == 0 ? db[k][e] : cols[c + i] + db[k][e];
-                        }
-                    }
+            for (int e = 0; e < 8; ++e) {
+                const int i = elem_at<kV8>(k, e, tid, nt);
+                if (i < c) {
+                    cols[warp * 2 * c + i] = dg[k][e];
+                    cols[warp * 2 * c + c + i] = db[k][e];
+                }
             }
-            __syncthreads();
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * c; i += blockDim.x) {
+            float a = cols[i];
+#pragma unroll
+            for (int u = 1; u < kLnBwdWarps; ++u) a += cols[u * 2 * c + i];
+            out[i] = a;
         }
-        for (int i = threadIdx.x; i < 2 * c; i += blockDim.x) out[i] = cols[i];
     } else {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(kWarp ? kLnBwdWarps * 32 : 512)
                 }
             }
     }
+    pdl_launch_dependents();
 }
 
 // ───────────────────────────── ring form ─────────────────────────────
@@ -531,6 +534,7 @@ __global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1
             for (int u = 1; u < groups; ++u) a += cols[static_cast<size_t>(u) * 2 * c + i];
             out[i] = a;
         }
+        pdl_launch_dependents();
     }
 }
 
@@ -753,14 +757,19 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
         if ((rc = ln_ring_run<true>(r, s)) != VAE_OK) return rc;
     } else {
         VAE_CUDA_CHECK(ln_dispatch(p, [&](auto nv, auto v8, auto warp) {
-        return launch_kernel(ln_bwd_kernel<nv.value, v8.value, warp.value>, dim3(static_cast<unsigned>(grid)),
-                             dim3(warp.value ? kLnBwdWarps * 32 : p.threads),
-                             warp.value && sums ? 2 * static_cast<size_t>(c) * sizeof(float) : 0, s, dy_dev, dy_type,
-                             x_dev, x_type, m, c, gamma_dev, eps, dx_dev, part);
+            const auto kernel = ln_bwd_kernel<nv.value, v8.value, warp.value>;
+            const size_t cols = warp.value && sums ? kLnBwdWarps * 2 * static_cast<size_t>(c) * sizeof(float) : 0;
+            if (cols > 48 * 1024) {
+                const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                           static_cast<int>(cols));
+                if (e != cudaSuccess) return e;
+            }
+            return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(warp.value ? kLnBwdWarps * 32 : p.threads),
+                                 cols, s, dy_dev, dy_type, x_dev, x_type, m, c, gamma_dev, eps, dx_dev, part);
         }));
     }
     if (sums)
-        VAE_CUDA_CHECK(launch_kernel(ln_cols_kernel, dim3((2u * static_cast<unsigned>(c) + 31u) / 32u),
+        VAE_CUDA_CHECK(launch_next(ln_cols_kernel, dim3((2u * static_cast<unsigned>(c) + 31u) / 32u),
                                      dim3(kColSlices * 32), 0, s,
                                      static_cast<const float*>(part), grid, c, dgamma_dev, dbeta_dev));
     return VAE_OK;

@@ -127,12 +127,16 @@ __device__ __forceinline__ void mma_ts_k(uint32_t d_tmem, uint32_t a_tmem, uint6
                     k != 0 ? 1u : 0u);
 }
 
-// One arrival on the barrier at this offset in every CTA of `mask`, once the
-// MMAs issued so far are done.
-__device__ __forceinline__ void umma_commit_to(uint32_t bar, uint16_t mask) {
+// One arrival on the barrier at this offset in every CTA of a cluster of
+// `csize` (1 or 2), once the MMAs issued so far are done.
+__device__ __forceinline__ void umma_commit_all(uint32_t bar, int csize) {
+    if (csize == 1) {
+        umma_commit(bar);
+        return;
+    }
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(mask)
+        "h"(static_cast<uint16_t>(3))
         : "memory");
 }
 

@@ -366,7 +366,7 @@ struct BwdRing {
 __device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p, bool ok, int csize) {
     if (elect_one()) {
         if (ok) umma_commit(smem_u32(s.done));
-        umma_commit_to(smem_u32(s.drain), static_cast<uint16_t>((1u << csize) - 1u));
+        umma_commit_all(smem_u32(s.drain), csize);
         int never = 0;
         (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
     }
@@ -505,7 +505,6 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
     constexpr uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
     const uint64_t kdesc = sw128_kmajor_desc(smem_u32(s.res)), vdesc = kdesc + second;
     const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
-    const uint16_t all = static_cast<uint16_t>((1u << p.csize_k) - 1u);
     auto wait = [&](uint64_t* bar, uint32_t par) { return warp_all(bwait(bar, par, s, p)); };
     auto score = [&](uint32_t st) {
         mma_ss<kSteps>(tS, kdesc, ring_k + st * stage_units, id_s);
@@ -546,7 +545,7 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
         tc_fence_after();
         if (elect_one()) {
             mma_ts<64>(tK, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
-            umma_commit_to(smem_u32(&s.empty[st]), all);
+            umma_commit_all(smem_u32(&s.empty[st]), p.csize_k);
         }
         __syncwarp();
         if (more) {
@@ -781,7 +780,6 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
     constexpr uint32_t tS = 0u, tX = 128u, tQ = 256u;
     constexpr uint32_t stage_units = 2u * C::kTileBytes >> 4, second = C::kTileBytes >> 4;
     const uint64_t ring_k = sw128_kmajor_desc(smem_u32(s.ring)), ring_m = sw128_mnmajor_desc(smem_u32(s.ring));
-    const uint16_t all = static_cast<uint16_t>((1u << p.csize_q) - 1u);
     auto wait = [&](uint64_t* bar, uint32_t par) { return warp_all(bwait(bar, par, s, p)); };
     auto score = [&](uint32_t st) {
         mma_ts_k<kSteps>(tS, kTmemQ, ring_k + st * stage_units, id_s);
@@ -819,7 +817,7 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
         tc_fence_after();
         if (elect_one()) {
             if (x >= from) mma_ts<64>(tQ, tX, ring_m + st * stage_units, id_o, x != from ? 1u : 0u);
-            umma_commit_to(smem_u32(&s.empty[st]), all);
+            umma_commit_all(smem_u32(&s.empty[st]), p.csize_q);
         }
         __syncwarp();
         if (more) {
@@ -1057,24 +1055,6 @@ BwdPlan bwd_plan(const MhaShape& s) {
 }
 constexpr size_t kMaximaFloats = 64;  // two words used; keeps what follows aligned
 
-template <typename K, typename... Args>
-cudaError_t cluster_launch(K kernel, long long items, int csize, int smem, cudaStream_t st, Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(items));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(csize);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 template <int T, int kSteps>
 int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap (&map)[4], const PrepParams& pp,
                const BwdParams& p, cudaStream_t st) {
@@ -1095,8 +1075,11 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
     const long long prep = f.row_tiles + (T == VAE_F16 ? f.key_tiles : 0);
     VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
     // (the query-tile kernel first: it may put its D into the side rows)
-    VAE_CUDA_CHECK(cluster_launch(mha_dq_kernel<T, kSteps>, f.q_items, f.csize_q, kQSmem, st, map[2], map[3], p));
-    VAE_CUDA_CHECK(cluster_launch(mha_dkv_kernel<T, kSteps>, f.k_items, f.csize_k, kKvSmem, st, map[0], map[1], map[2], map[3], p));
+    VAE_CUDA_CHECK(launch_kernel_as(pdl_enabled(), static_cast<unsigned>(f.csize_q), mha_dq_kernel<T, kSteps>,
+                                    dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), kQSmem, st, map[2], map[3], p));
+    VAE_CUDA_CHECK(launch_kernel_as(pdl_enabled(), static_cast<unsigned>(f.csize_k), mha_dkv_kernel<T, kSteps>,
+                                    dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), kKvSmem, st, map[0], map[1], map[2],
+                                    map[3], p));
     const MhaShape& s = p.s;
     if (f.nsplit_k > 1) {
         const long long rows = static_cast<long long>(s.b) * s.hkv * s.sk;

@@ -261,6 +261,7 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
         return true;
     };
     for (int j = 0; ok && j < ahead && j < w.n; ++j) ok = load(false, j);
+    __syncthreads();  // the first tiles are on their way while the CTA is set up
     for (int j = 0; ok && j < w.n; ++j) {
         ok = load(true, j);
         if (ok && j + ahead < w.n) ok = load(false, j + ahead);
@@ -671,6 +672,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const FwdSmem s = fwd_carve<kSteps>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (warp == kTmaWarp && lane == 0) {
+        tma_prefetch_desc(&mq);
+        tma_prefetch_desc(&mk);
+        tma_prefetch_desc(&mv);
+    }
     pdl_wait();
     const FwdWork w = fwd_work(p);
     if (w.e == p.s.b) return;  // more pieces than runs of key tiles
@@ -692,37 +698,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    if (threadIdx.x == 0) {
-        *s.abort_flag = 0;
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(smem_u32(&s.full[i]), 1u);
-            mbar_init(smem_u32(&s.empty[i]), 1u);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&s.s_full[i]), 1u);
-            mbar_init(smem_u32(&s.p_full[i]), 4u);
-            mbar_init(smem_u32(&s.o_full[i]), 1u);
-        }
-        mbar_init(smem_u32(s.q_full), 1u);
-        mbar_init(smem_u32(s.fix), 1u);
-        mbar_init(smem_u32(s.drain), 1u);
-        fence_mbar_init();
-    }
-    if (warp == kMmaWarp) {
-        tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     constexpr uint32_t tmem = 0u;  // all 512 columns are this CTA's: they start at 0
-    if (warp < kSoftWarps) {
-        if (p.narrow) fwd_softmax_narrow<T, kSteps>(p, s, w, warp, lane);
-        else fwd_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
-    } else if (warp == kTmaWarp) {
-        fwd_producer<kSteps>(p, s, w, &mq, &mk, &mv, lane);
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            *s.abort_flag = 0;
+            for (int i = 0; i < C::kStages; ++i) {
+                mbar_init(smem_u32(&s.full[i]), 1u);
+                mbar_init(smem_u32(&s.empty[i]), 1u);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&s.s_full[i]), 1u);
+                mbar_init(smem_u32(&s.p_full[i]), 4u);
+                mbar_init(smem_u32(&s.o_full[i]), 1u);
+            }
+            mbar_init(smem_u32(s.q_full), 1u);
+            mbar_init(smem_u32(s.fix), 1u);
+            mbar_init(smem_u32(s.drain), 1u);
+            fence_mbar_init();
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        fwd_producer<kSteps>(p, s, w, &mq, &mk, &mv, lane);  // (meets the others' __syncthreads)
     } else {
-        fwd_mma<T, kSteps>(p, s, w);
+        if (warp == kMmaWarp) {
+            tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == kMmaWarp) fwd_mma<T, kSteps>(p, s, w);
+        else if (p.narrow) fwd_softmax_narrow<T, kSteps>(p, s, w, warp, lane);
+        else fwd_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
     }
     pdl_launch_dependents();
     __syncwarp();
@@ -834,7 +841,7 @@ int fwd_launch(const vae_attention_desc* a, const FwdPlan& f, const CUtensorMap 
                                  st, map[0], map[1], map[2], p));
     if (f.nsplit > 1) {
         const long long rows = static_cast<long long>(a->b) * a->hq * a->sq;
-        VAE_CUDA_CHECK(launch_kernel(mha_join_kernel<T>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p));
+        VAE_CUDA_CHECK(launch_next(mha_join_kernel<T>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p));
     }
     return VAE_OK;
 }
