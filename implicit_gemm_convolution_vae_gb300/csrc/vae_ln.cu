@@ -573,11 +573,12 @@ struct LnPlan {
     bool v8, warp;
     int nv, threads;
 };
-LnPlan ln_plan(int c) {
+LnPlan ln_plan(int c, bool backward) {
     LnPlan p;
     p.v8 = c % 8 == 0;
     const int nvec = (c + 7) / 8;
-    p.warp = nvec <= 32 * kLnWarpVec;
+    // (the gradient element by element: over 512 channels a warp's registers would leave one block an SM)
+    p.warp = nvec <= (backward && !p.v8 ? 64 : 32 * kLnWarpVec);
     if (p.warp) {
         p.nv = (nvec + 31) / 32;
         p.threads = 32;
@@ -646,7 +647,7 @@ int ln_ring_run(LnRing& r, cudaStream_t st) {
 }
 
 int ln_bwd_grid(int m, int c) {
-    const LnPlan p = ln_plan(c);
+    const LnPlan p = ln_plan(c, true);
     const int rows = p.warp ? (m - 1) / kLnBwdWarps + 1 : m;
     return std::min(rows, p.warp ? kLnBwdBlocks : 2 * kLnBwdBlocks);
 }
@@ -705,7 +706,7 @@ int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamm
         r.yt = y_type;
         return ln_ring_run<false>(r, reinterpret_cast<cudaStream_t>(stream));
     }
-    const LnPlan p = ln_plan(c);
+    const LnPlan p = ln_plan(c, false);
     const unsigned grid = p.warp ? (static_cast<unsigned>(m) - 1u) / kLnFwdWarps + 1u : static_cast<unsigned>(m);
     VAE_CUDA_CHECK(ln_dispatch(p, [&](auto nv, auto v8, auto warp) {
         return launch_kernel(ln_fwd_kernel<nv.value, v8.value, warp.value>, dim3(grid),
@@ -741,7 +742,7 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
         return set_error(VAE_ERR_NOMEM, "layer norm: workspace of %zu bytes, %zu needed", workspace_bytes,
                          vae_layernorm_backward_workspace_bytes(m, c));
     if ((rc = check_device()) != VAE_OK) return rc;
-    const LnPlan p = ln_plan(c);
+    const LnPlan p = ln_plan(c, true);
     int grid = ln_bwd_grid(m, c);
     float* part = sums ? static_cast<float*>(workspace_dev) : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -57,7 +57,7 @@ constexpr int kPLog2 = 14;         // f16: P is held as P 2^14
 constexpr int kSideFloats = 256;   // of a row tile: 128 x (kPLog2 - lse log2(e)), 128 x D
 constexpr int kSideBytes = kSideFloats * 4;
 
-constexpr int kExactTiles = 8;     // key tiles up to which D is formed from P and dP
+constexpr int kExactTiles = 2;     // key tiles up to which D is formed from P and dP
 
 // Shared memory of a kernel: kRes resident tiles, a ring of kN stages of two
 // tiles, kSideN side rows; the barriers behind them.
