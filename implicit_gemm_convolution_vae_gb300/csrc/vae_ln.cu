@@ -6,7 +6,7 @@
 // output once.
 //
 // Ring form (many rows of a multiple of eight channels, up to 5120): one block
-// per SM stays; a row belongs to one, two or four warps, whose next rows are
+// per SM stays; rows belong to groups of one to eight warps, whose next rows are
 // already on the way into shared memory by bulk copies while they work on the
 // last one. Registers then hold one row only and the loads never pause.
 // Plain form (few rows, other lengths): rows of up to 1280 channels belong to
@@ -257,17 +257,23 @@ __global__ void __launch_bounds__(kWarp ? kLnBwdWarps * 32 : 512)
 
 // ───────────────────────────── ring form ─────────────────────────────
 
-constexpr int kRingFwdWarps = 16, kRingBwdWarps = 8;  // per block, one block per SM
-constexpr int kRingBlocks = 152;
-constexpr int kRingStages = 4;               // rows of a group in flight, at most
+constexpr int kRingBlocks = 152;  // one per SM
+constexpr int kRingStages = 4;    // chunks of a group in flight, at most
 constexpr size_t kRingSmem = 220 * 1024;
+
+// Rows that a group takes together (a chunk: they lie side by side in memory),
+// as many as its registers hold: the sums of a chunk's rows cross the warp
+// together, and gamma and beta are read once for them.
+__host__ __device__ constexpr int ring_rows(int nq) { return nq <= 2 ? 4 : 2; }
+// Warps per block, at most: what leaves each thread its registers.
+__host__ __device__ constexpr int ring_warps(int nq, bool backward) { return backward || nq > 5 ? 12 : 16; }
 
 struct LnRing {
     int m, c, xt, yt, dyt;
-    int nv, wide;         // eights per thread, warps per row (a group)
+    int nq, wide, warps;  // fours per thread, warps per row (a group), warps per block
     int stages;
     unsigned row_x, row_dy, stage;  // bytes of a row of x and dy, of a stage
-    unsigned bars;                  // offset of the barriers; gamma and beta lie before them
+    unsigned consts, bars;          // offsets of gamma and beta, and of the barriers
     float eps;
     const void *x, *dy;
     const float *gamma, *beta;
@@ -283,64 +289,54 @@ __device__ __forceinline__ void ln_bulk(uint32_t dst, const void* src, uint32_t 
                  : "memory");
 }
 
-__device__ __forceinline__ float2 f2(float a, float b) { return make_float2(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-
-// Eights tid, tid + T, ... of a row (in shared memory, or gamma / beta there); 0 behind c.
-template <int T, int NV>
-__device__ __forceinline__ void row_in(const uint8_t* p, int c, int tid, int nt, float2 (&v)[NV][4]) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int i = (tid + k * nt) * 8;
-        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (i < c) load8<T>(reinterpret_cast<const typename Elem<T>::type*>(p) + i, t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[k][e] = f2(t[2 * e], t[2 * e + 1]);
+// Four elements, as two pairs. (Fours of neighbouring lanes touch every bank of
+// shared memory once; eights of f32 would meet in half of them.)
+struct Four {
+    float2 a, b;
+};
+template <int T>
+__device__ __forceinline__ Four four_in(const uint8_t* p, int i) {
+    if constexpr (T == VAE_F32) {
+        const float4 v = reinterpret_cast<const float4*>(p)[i];
+        return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
+    } else {
+        const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+        return {unpack2<T>(v.x), unpack2<T>(v.y)};
     }
 }
-template <int NV>
-__device__ __forceinline__ void row_in(const uint8_t* p, int type, int c, int tid, int nt, float2 (&v)[NV][4]) {
-    if (type == VAE_F32) row_in<VAE_F32, NV>(p, c, tid, nt, v);
-    else if (type == VAE_F16) row_in<VAE_F16, NV>(p, c, tid, nt, v);
-    else row_in<VAE_BF16, NV>(p, c, tid, nt, v);
+template <int T>
+__device__ __forceinline__ void four_out(uint8_t* p, int i, Four v) {
+    if constexpr (T == VAE_F32) reinterpret_cast<float4*>(p)[i] = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
+    else reinterpret_cast<uint2*>(p)[i] = make_uint2(pack2<T>(v.a.x, v.a.y), pack2<T>(v.b.x, v.b.y));
 }
-template <int T, int NV>
-__device__ __forceinline__ void row_out(void* p, size_t off, int c, int tid, int nt, const float2 (&v)[NV][4]) {
+// Fours tid, tid + nt, ... of a row; 0 behind its n fours.
+template <int T, int NQ>
+__device__ __forceinline__ void row_in_t(const uint8_t* p, int n, int tid, int nt, Four (&v)[NQ]) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int i = (tid + k * nt) * 8;
-        const float t[8] = {v[k][0].x, v[k][0].y, v[k][1].x, v[k][1].y, v[k][2].x, v[k][2].y, v[k][3].x, v[k][3].y};
-        if (i < c) store8<T>(static_cast<typename Elem<T>::type*>(p) + off + i, t);
+    for (int k = 0; k < NQ; ++k) {
+        const int i = tid + k * nt;
+        v[k] = i < n ? four_in<T>(p, i) : Four{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     }
 }
-template <int NV>
-__device__ __forceinline__ void row_out(void* p, int type, size_t off, int c, int tid, int nt, const float2 (&v)[NV][4]) {
-    if (type == VAE_F32) row_out<VAE_F32, NV>(p, off, c, tid, nt, v);
-    else if (type == VAE_F16) row_out<VAE_F16, NV>(p, off, c, tid, nt, v);
-    else row_out<VAE_BF16, NV>(p, off, c, tid, nt, v);
+template <int NQ>
+__device__ __forceinline__ void row_in(const uint8_t* p, int type, int n, int tid, int nt, Four (&v)[NQ]) {
+    if (type == VAE_F32) row_in_t<VAE_F32, NQ>(p, n, tid, nt, v);
+    else if (type == VAE_F16) row_in_t<VAE_F16, NQ>(p, n, tid, nt, v);
+    else row_in_t<VAE_BF16, NQ>(p, n, tid, nt, v);
+}
+template <int T, int NQ>
+__device__ __forceinline__ void row_out_t(uint8_t* p, int n, int tid, int nt, const Four (&v)[NQ]) {
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) {
+        const int i = tid + k * nt;
+        if (i < n) four_out<T>(p, i, v[k]);
+    }
+}
+template <int NQ>
+__device__ __forceinline__ void row_out(uint8_t* p, int type, int n, int tid, int nt, const Four (&v)[NQ]) {
+    if (type == VAE_F32) row_out_t<VAE_F32, NQ>(p, n, tid, nt, v);
+    else if (type == VAE_F16) row_out_t<VAE_F16, NQ>(p, n, tid, nt, v);
+    else row_out_t<VAE_BF16, NQ>(p, n, tid, nt, v);
 }
 
 // The warps of a group meet (a barrier of the group's own).
@@ -348,51 +344,51 @@ __device__ __forceinline__ void group_sync(int group, int wide) {
     if (wide == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(wide * 32) : "memory");
 }
-// Two sums over the group's threads; `red`: [2][wide] floats of this group and call site.
-__device__ __forceinline__ float2 group_sum2(float2 v, float2* red, int group, int wide, int part) {
+// N sums over the group's threads, the same bits in each; `red`: [wide][N] floats of this group and call site.
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float* red, int group, int wide, int part) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = add2(v, f2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-    if (wide > 1) {
-        if ((threadIdx.x & 31) == 0) red[part] = v;
-        group_sync(group, wide);
-        v = red[0];
-        for (int i = 1; i < wide; ++i) v = add2(v, red[i]);
-    }
-    return v;
-}
-__device__ __forceinline__ float group_sum(float x, float2* red, int group, int wide, int part) {
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     if (wide > 1) {
-        if ((threadIdx.x & 31) == 0) red[part].x = x;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[part * N + i] = v[i];
         group_sync(group, wide);
-        x = red[0].x;
-        for (int i = 1; i < wide; ++i) x += red[i].x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = red[i];
+        for (int k = 1; k < wide; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += red[k * N + i];
     }
-    return x;
 }
 
-// Rows g, g + G, ... of all groups g < G of the grid. kBwd: the gradient.
-template <int NV, bool kBwd>
-__global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1) ln_ring_kernel(const LnRing p) {
-    constexpr int kWarps = kBwd ? kRingBwdWarps : kRingFwdWarps;
+// Chunks g, g + G, ... of all groups g < G of the grid. kBwd: the gradient.
+template <int NQ, bool kBwd>
+__global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(const LnRing p) {
+    constexpr int R = ring_rows(NQ);
+    constexpr int kMaxWarps = ring_warps(NQ, kBwd);
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 red[3][kWarps];
+    __shared__ float red[3][kMaxWarps * 2 * R];
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wide = p.wide, group = warp / wide, part = warp % wide, groups = kWarps / wide;
-    const int nt = wide * 32, tid = part * 32 + lane, c = p.c;
+    const int wide = p.wide, group = warp / wide, part = warp % wide, groups = p.warps / wide;
+    const int nt = wide * 32, tid = part * 32 + lane, c = p.c, n4 = c / 4;
     uint8_t* ring = smem + static_cast<size_t>(group) * p.stages * p.stage;
-    const float* gam = reinterpret_cast<const float*>(smem + static_cast<size_t>(groups) * p.stages * p.stage);
+    const uint8_t* gam = smem + p.consts;
+    const uint8_t* bet = gam + static_cast<size_t>(c) * 4;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bars) + group * kRingStages;
     const int all = static_cast<int>(gridDim.x) * groups, first = static_cast<int>(blockIdx.x) * groups + group;
-    const int n = first < p.m ? (p.m - 1 - first) / all + 1 : 0;  // this group's rows
-    auto fetch = [&](int k, int st) {  // one lane of the group: the group's row k into stage st = k % stages
-        const size_t row = static_cast<size_t>(first) + static_cast<size_t>(k) * all;
+    const int chunks = (p.m - 1) / R + 1;
+    const int n = first < chunks ? (chunks - 1 - first) / all + 1 : 0;  // this group's chunks
+    auto fetch = [&](int k, int st) {  // one lane of the group: the group's chunk k into stage st = k % stages
+        const size_t row = (static_cast<size_t>(first) + static_cast<size_t>(k) * all) * R;
+        const unsigned rows = p.m - row < static_cast<size_t>(R) ? static_cast<unsigned>(p.m - row) : R;
         const uint32_t bar = smem_u32(&full[st]), dst = smem_u32(ring + static_cast<size_t>(st) * p.stage);
-        mbar_arrive_expect_tx(bar, p.row_x + p.row_dy);
-        ln_bulk(dst, static_cast<const uint8_t*>(p.x) + row * p.row_x, p.row_x, bar);
-        if (kBwd) ln_bulk(dst + p.row_x, static_cast<const uint8_t*>(p.dy) + row * p.row_dy, p.row_dy, bar);
+        mbar_arrive_expect_tx(bar, rows * (p.row_x + p.row_dy));
+        ln_bulk(dst, static_cast<const uint8_t*>(p.x) + row * p.row_x, rows * p.row_x, bar);
+        if (kBwd) ln_bulk(dst + R * p.row_x, static_cast<const uint8_t*>(p.dy) + row * p.row_dy, rows * p.row_dy, bar);
     };
     if (threadIdx.x == 0) abort_flag = 0;
     if (tid == 0) {
@@ -403,20 +399,17 @@ __global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1
     if (tid == 0)
         for (int k = 0; k < n && k < p.stages; ++k) fetch(k, k);
     const bool has_g = p.gamma != nullptr, has_b = !kBwd && p.beta != nullptr;
-    if (has_g || has_b) {
-        float* w = const_cast<float*>(gam);
-        for (int i = threadIdx.x * 4; i < c; i += kWarps * 32 * 4) {
-            if (has_g) *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(p.gamma + i);
-            if (has_b) *reinterpret_cast<float4*>(w + c + i) = *reinterpret_cast<const float4*>(p.beta + i);
+    if (has_g || has_b)
+        for (int i = threadIdx.x; i < n4; i += blockDim.x) {
+            if (has_g) reinterpret_cast<float4*>(smem + p.consts)[i] = reinterpret_cast<const float4*>(p.gamma)[i];
+            if (has_b) reinterpret_cast<float4*>(smem + p.consts + c * 4)[i] = reinterpret_cast<const float4*>(p.beta)[i];
         }
-    }
     __syncthreads();
-    float2 dg[NV][4], db[NV][4];
+    const Four zero{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    Four dg[kBwd ? NQ : 1], db[kBwd ? NQ : 1];
     if constexpr (kBwd) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dg[k][e] = db[k][e] = f2(0.f, 0.f);
+        for (int k = 0; k < NQ; ++k) dg[k] = db[k] = zero;
     }
     const float inv_c = 1.f / static_cast<float>(c);
     bool ok = true;
@@ -428,82 +421,100 @@ __global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1
             ok = false;
             late = k;
         }
+        const size_t row0 = (static_cast<size_t>(first) + static_cast<size_t>(k) * all) * R;
+        const int rows = p.m - row0 < static_cast<size_t>(R) ? static_cast<int>(p.m - row0) : R;
         const uint8_t* src = ring + static_cast<size_t>(st) * p.stage;
-        float2 v[NV][4], g[NV][4];
-        row_in<NV>(src, p.xt, c, tid, nt, v);
-        if constexpr (kBwd) row_in<NV>(src + p.row_x, p.dyt, c, tid, nt, g);
-        float2 s = f2(0.f, 0.f);
+        Four v[R][NQ], g[kBwd ? R : 1][NQ];
+        float s[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s = add2(s, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
-        const float mean = group_sum(s.x + s.y, &red[0][group * wide], group, wide, part) * inv_c;
-        // every thread of the group has its part of the row in registers (wide > 1: the barrier in the sum)
+        for (int r = 0; r < R; ++r) {
+            row_in<NQ>(src + r * p.row_x, p.xt, r < rows ? n4 : 0, tid, nt, v[r]);
+            if constexpr (kBwd) row_in<NQ>(src + R * p.row_x + r * p.row_dy, p.dyt, r < rows ? n4 : 0, tid, nt, g[r]);
+            float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) t = add2(t, add2(v[r][i].a, v[r][i].b));
+            s[r] = t.x + t.y;
+        }
+        group_sums<R>(s, &red[0][group * wide * R], group, wide, part);
+        // every thread of the group has its part of the chunk in registers (wide > 1: the barrier in the sums)
         if (wide == 1) __syncwarp();
         if (tid == 0 && ok && k + p.stages < n) fetch(k + p.stages, st);
         if (++st == p.stages) {
             st = 0;
             ph ^= 1u;
         }
-        const float2 mm = f2(-mean, -mean);
-        s = f2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool in = (tid + i * nt) * 8 < c;
+        for (int r = 0; r < R; ++r) {
+            const float2 mm = make_float2(-s[r] * inv_c, -s[r] * inv_c);
+            float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[i][e] = in ? add2(v[i][e], mm) : f2(0.f, 0.f);
-                s = fma2(v[i][e], v[i][e], s);
+            for (int i = 0; i < NQ; ++i) {
+                const bool in = tid + i * nt < n4;
+                v[r][i] = in ? Four{add2(v[r][i].a, mm), add2(v[r][i].b, mm)} : zero;
+                t = fma2(v[r][i].a, v[r][i].a, fma2(v[r][i].b, v[r][i].b, t));
             }
+            s[r] = t.x + t.y;
         }
-        const float rstd = 1.f / sqrtf(group_sum(s.x + s.y, &red[1][group * wide], group, wide, part) * inv_c + p.eps);
-        const float2 r2 = f2(rstd, rstd);
-        const size_t off = (static_cast<size_t>(first) + static_cast<size_t>(k) * all) * c;
+        group_sums<R>(s, &red[1][group * wide * R], group, wide, part);
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r] = 1.f / sqrtf(s[r] * inv_c + p.eps);
+        uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * c * (((kBwd ? p.xt : p.yt) == VAE_F32) ? 4 : 2);
+        const size_t out_row = static_cast<size_t>(c) * (((kBwd ? p.xt : p.yt) == VAE_F32) ? 4 : 2);
         if constexpr (!kBwd) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NQ; ++i) {
+                const int at = tid + i * nt;
+                const Four w = has_g && at < n4 ? four_in<VAE_F32>(gam, at) : Four{make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+                const Four b = has_b && at < n4 ? four_in<VAE_F32>(bet, at) : zero;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i][e] = mul2(v[i][e], r2);
-            if (has_g) {
-                row_in<VAE_F32, NV>(reinterpret_cast<const uint8_t*>(gam), c, tid, nt, g);
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[i][e] = mul2(v[i][e], g[i][e]);
-            }
-            if (has_b) {
-                row_in<VAE_F32, NV>(reinterpret_cast<const uint8_t*>(gam + c), c, tid, nt, g);
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[i][e] = add2(v[i][e], g[i][e]);
-            }
-            if (ok) row_out<NV>(p.out, p.yt, off, c, tid, nt, v);
-        } else {
-            float2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-                const int at = (tid + i * nt) * 8;
-                if (has_g && at < c) load8<VAE_F32>(gam + at, w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    dg[i][e] = fma2(mul2(g[i][e], r2), v[i][e], dg[i][e]);
-                    db[i][e] = add2(db[i][e], g[i][e]);
-                    g[i][e] = mul2(g[i][e], f2(w[2 * e], w[2 * e + 1]));
-                    s1 = add2(s1, g[i][e]);
-                    s2 = fma2(g[i][e], v[i][e], s2);
+                for (int r = 0; r < R; ++r) {
+                    const float2 q = make_float2(s[r], s[r]);
+                    v[r][i] = {fma2(mul2(v[r][i].a, q), w.a, b.a), fma2(mul2(v[r][i].b, q), w.b, b.b)};
                 }
             }
-            const float2 sums = group_sum2(f2(s1.x + s1.y, s2.x + s2.y), &red[2][group * wide], group, wide, part);
-            // dx = rstd (g - mean(g) - n mean(g n)), n = rstd v
-            const float k1 = -rstd * sums.x * inv_c, k2 = -rstd * rstd * rstd * sums.y * inv_c;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int r = 0; r < R; ++r)
+                if (ok && r < rows) row_out<NQ>(out + r * out_row, p.yt, n4, tid, nt, v[r]);
+        } else {
+            float2 s1[R], s2[R];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i][e] = fma2(g[i][e], r2, fma2(v[i][e], f2(k2, k2), f2(k1, k1)));
-            if (ok) row_out<NV>(p.out, p.xt, off, c, tid, nt, v);
+            for (int r = 0; r < R; ++r) s1[r] = s2[r] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int at = tid + i * nt;
+                const Four w = has_g && at < n4 ? four_in<VAE_F32>(gam, at) : Four{make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float2 q = make_float2(s[r], s[r]);
+                    Four& y = g[r][i];
+                    const Four& d = v[r][i];
+                    dg[i] = {fma2(mul2(y.a, q), d.a, dg[i].a), fma2(mul2(y.b, q), d.b, dg[i].b)};
+                    db[i] = {add2(db[i].a, y.a), add2(db[i].b, y.b)};
+                    y = {mul2(y.a, w.a), mul2(y.b, w.b)};
+                    s1[r] = add2(s1[r], add2(y.a, y.b));
+                    s2[r] = fma2(y.a, d.a, fma2(y.b, d.b, s2[r]));
+                }
+            }
+            float sums[2 * R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                sums[r] = s1[r].x + s1[r].y;
+                sums[R + r] = s2[r].x + s2[r].y;
+            }
+            group_sums<2 * R>(sums, &red[2][group * wide * 2 * R], group, wide, part);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                // dx = rstd (g - mean(g) - n mean(g n)), n = rstd v
+                const float rstd = s[r], k1 = -rstd * sums[r] * inv_c, k2 = -rstd * rstd * rstd * sums[R + r] * inv_c;
+                const float2 q = make_float2(rstd, rstd), q1 = make_float2(k1, k1), q2 = make_float2(k2, k2);
+#pragma unroll
+                for (int i = 0; i < NQ; ++i)
+                    v[r][i] = {fma2(g[r][i].a, q, fma2(v[r][i].a, q2, q1)), fma2(g[r][i].b, q, fma2(v[r][i].b, q2, q1))};
+                if (ok && r < rows) row_out<NQ>(out + r * out_row, p.xt, n4, tid, nt, v[r]);
+            }
         }
     }
-    // Every copy lands before the block may exit (after a time-out: the rows that were fetched and not met).
+    // Every copy lands before the block may exit (after a time-out: the chunks that were fetched and not met).
     if (!ok && tid == 0) {
         int never = 0;
         for (int k = late; k < n && k < late + p.stages; ++k)
@@ -512,24 +523,21 @@ __global__ void __launch_bounds__((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32, 1
     }
     if constexpr (kBwd) {
         if (p.part == nullptr) return;
-        // the groups' column sums side by side over the ring (64 c bytes at most; a ring holds as much), then joined in order
+        // the groups' column sums side by side over the ring (8 c bytes a group: less than its two stages), then joined in order
         float* cols = reinterpret_cast<float*>(smem);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int at = (tid + i * nt) * 8;
-            if (at < c) {
-                float* w = cols + static_cast<size_t>(group) * 2 * c + at;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    *reinterpret_cast<float2*>(w + 2 * e) = dg[i][e];
-                    *reinterpret_cast<float2*>(w + c + 2 * e) = db[i][e];
-                }
+        for (int i = 0; i < NQ; ++i) {
+            const int at = tid + i * nt;
+            if (at < n4) {
+                uint8_t* w = reinterpret_cast<uint8_t*>(cols + static_cast<size_t>(group) * 2 * c);
+                four_out<VAE_F32>(w, at, dg[i]);
+                four_out<VAE_F32>(w + static_cast<size_t>(c) * 4, at, db[i]);
             }
         }
         __syncthreads();
         float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * c;
-        for (int i = threadIdx.x; i < 2 * c; i += kWarps * 32) {
+        for (int i = threadIdx.x; i < 2 * c; i += blockDim.x) {
             float a = cols[i];
             for (int u = 1; u < groups; ++u) a += cols[static_cast<size_t>(u) * 2 * c + i];
             out[i] = a;
@@ -590,60 +598,73 @@ LnPlan ln_plan(int c, bool backward) {
 }
 // The ring form's plan for rows of x (and dy: backward); false where the plain
 // form is used: lengths that are no multiple of eight or over 5120, or so few
-// rows that a group would not have two.
+// rows that a group would not have two chunks.
 bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, LnRing* r) {
     if (c % 8 != 0 || c > 5120) return false;
-    const int warps = backward ? kRingBwdWarps : kRingFwdWarps;
-    r->wide = c <= 1280 ? 1 : (c <= 2560 ? 2 : 4);
-    const int groups = warps / r->wide;
-    if (m < 2 * kRingBlocks * groups) return false;
-    r->nv = (c / 8 + r->wide * 32 - 1) / (r->wide * 32);
+    const int most = backward ? 640 : 1280;  // channels of one warp's share of a row
+    r->wide = c <= most ? 1 : (c <= 2 * most ? 2 : (c <= 4 * most ? 4 : 8));
+    r->nq = (c / 4 + r->wide * 32 - 1) / (r->wide * 32);
+    const int rows = ring_rows(r->nq);
     r->row_x = static_cast<unsigned>(c * type_size(xt));
     r->row_dy = backward ? static_cast<unsigned>(c * type_size(dyt)) : 0u;
-    r->stage = r->row_x + r->row_dy;  // (multiples of 16 bytes)
-    const size_t consts = static_cast<size_t>(c) * (backward ? 4 : 8), bars = static_cast<size_t>(warps) * kRingStages * 8;
+    r->stage = rows * (r->row_x + r->row_dy);  // (multiples of 16 bytes)
+    const int max_warps = ring_warps(r->nq, backward);
+    const size_t consts = static_cast<size_t>(c) * (backward ? 4 : 8), bars = static_cast<size_t>(max_warps) * kRingStages * 8;
     const size_t left = kRingSmem - consts - bars;
+    // as many groups as fit with two stages each, then as many stages as fit
+    const size_t fit = left / (2 * static_cast<size_t>(r->stage));
+    const int groups = static_cast<int>(std::min<size_t>(fit, max_warps / r->wide));
+    if (groups < 1 || m < 2 * kRingBlocks * groups * rows) return false;
+    r->warps = groups * r->wide;
     r->stages = static_cast<int>(std::min<size_t>(kRingStages, left / (static_cast<size_t>(groups) * r->stage)));
-    if (r->stages < 2) return false;
-    const size_t ring = static_cast<size_t>(groups) * r->stages * r->stage;
-    r->bars = static_cast<unsigned>(ring + consts);
+    r->consts = static_cast<unsigned>(static_cast<size_t>(groups) * r->stages * r->stage);
+    r->bars = static_cast<unsigned>(r->consts + consts);
     r->m = m;
     r->c = c;
     r->xt = xt;
     r->dyt = dyt;
     return true;
 }
-size_t ln_ring_smem(const LnRing& r) { return r.bars + static_cast<size_t>(kRingFwdWarps) * kRingStages * 8; }
+size_t ln_ring_smem(const LnRing& r) { return r.bars + static_cast<size_t>(r.warps) * kRingStages * 8; }
 
+template <int NQ, bool kBwd>
+int ln_ring_launch(const LnRing& r, cudaStream_t st) {
+    static CtxOnce once;
+    static std::mutex mu;
+    {
+        int dev;
+        VAE_CUDA_CHECK(cudaGetDevice(&dev));
+        std::lock_guard<std::mutex> lk(mu);
+        if (!once.done(dev)) {
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(ln_ring_kernel<NQ, kBwd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                static_cast<int>(kRingSmem)));
+            once.mark(dev);
+        }
+    }
+    VAE_CUDA_CHECK(launch_kernel(ln_ring_kernel<NQ, kBwd>, dim3(kRingBlocks), dim3(r.warps * 32), ln_ring_smem(r), st, r));
+    return VAE_OK;
+}
 template <bool kBwd>
 int ln_ring_run(LnRing& r, cudaStream_t st) {
     r.status = device_status_ptr();
     r.timeout_ns = wait_timeout_ns();
     if (r.status == nullptr) return VAE_ERR_CUDA;
-    const auto go = [&](auto kernel, CtxOnce& once) -> int {
-        static std::mutex mu;
-        {
-            int dev;
-            VAE_CUDA_CHECK(cudaGetDevice(&dev));
-            std::lock_guard<std::mutex> lk(mu);
-            if (!once.done(dev)) {
-                VAE_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    static_cast<int>(kRingSmem + 1024)));
-                once.mark(dev);
-            }
-        }
-        VAE_CUDA_CHECK(launch_kernel(kernel, dim3(kRingBlocks), dim3((kBwd ? kRingBwdWarps : kRingFwdWarps) * 32),
-                                     ln_ring_smem(r), st, static_cast<const LnRing&>(r)));
-        return VAE_OK;
-    };
-    static CtxOnce once[5];
-    switch (r.nv) {
-        case 1: return go(ln_ring_kernel<1, kBwd>, once[0]);
-        case 2: return go(ln_ring_kernel<2, kBwd>, once[1]);
-        case 3: return go(ln_ring_kernel<3, kBwd>, once[2]);
-        case 4: return go(ln_ring_kernel<4, kBwd>, once[3]);
-        default: return go(ln_ring_kernel<5, kBwd>, once[4]);
+    switch (r.nq) {
+        case 1: return ln_ring_launch<1, kBwd>(r, st);
+        case 2: return ln_ring_launch<2, kBwd>(r, st);
+        case 3: return ln_ring_launch<3, kBwd>(r, st);
+        case 4: return ln_ring_launch<4, kBwd>(r, st);
+        case 5: return ln_ring_launch<5, kBwd>(r, st);
+        default: break;
     }
+    if constexpr (!kBwd) switch (r.nq) {
+            case 6: return ln_ring_launch<6, kBwd>(r, st);
+            case 7: return ln_ring_launch<7, kBwd>(r, st);
+            case 8: return ln_ring_launch<8, kBwd>(r, st);
+            case 9: return ln_ring_launch<9, kBwd>(r, st);
+            default: return ln_ring_launch<10, kBwd>(r, st);
+        }
+    return set_error(VAE_ERR_SHAPE, "layer norm: no ring form for %d channels", r.c);
 }
 
 int ln_bwd_grid(int m, int c) {

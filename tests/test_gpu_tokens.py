@@ -53,7 +53,8 @@ def _within(got, ref, tol):
 
 LN_SHAPES = [(1, 1), (1, 8), (3, 7), (5, 33), (129, 144), (64, 256), (77, 257), (33, 576), (19, 1152), (18, 1280),
              (9, 1281), (7, 1288), (10, 2304), (6, 4096), (5, 5001), (4, 8192), (3, 16383), (3, 16384), (2500, 64),
-             (5001, 144), (4900, 1152), (5000, 1280), (2600, 1288), (2500, 2560), (1300, 2568), (1400, 5120), (1300, 5128)]
+             (5001, 144), (4900, 1152), (5000, 1280), (2600, 1288), (2500, 2560), (1300, 2568), (1400, 5120), (1300, 5128),
+             (20003, 40), (20001, 200), (7300, 640), (4000, 648)]
 
 
 def _ln_terms(x, eps):
