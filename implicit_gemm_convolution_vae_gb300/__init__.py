@@ -678,6 +678,8 @@ def _attention_args(q, k, v, scale, q_len, k_len, block):
         raise VaeError(-2, f"k must be {(b, sk, hkv, d)}, got {tuple(kshape)}")
     if v.shape != kshape:
         raise VaeError(-2, f"v must be {tuple(kshape)}, got {tuple(v.shape)}")
+    if not 0 <= block < 1 << 31:
+        raise VaeError(-1, f"block must be >= 0 and fit 31 bits, got {block}")
     if q_len is not None:
         _tensor(q_len, "q_len", _T.i32, (b,))
     if k_len is not None:

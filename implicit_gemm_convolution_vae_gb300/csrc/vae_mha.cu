@@ -32,10 +32,11 @@ int mha_check(const vae_attention_desc* a, bool backward, MhaShape* s) {
               {"dk", a->dk_stride, a->sk, a->hkv}, {"dv", a->dv_stride, a->sk, a->hkv}};
     for (int i = 0; i < (backward ? 8 : 4); ++i) {
         const int dim[3] = {a->b, t[i].n, t[i].h};
+        const bool written = i == 3 || i > 4;  // rows of o, dq, dk, dv must not lie in one another
         for (int k = 0; k < 3; ++k)
-            if (dim[k] > 1 && (t[i].st[k] < 8 || t[i].st[k] % 8 != 0 || t[i].st[k] >= (1LL << 38)))
-                return set_error(VAE_ERR_SHAPE, "attention: %s's strides must be positive multiples of 8 (stride %d: %lld)",
-                                 t[i].name, k, t[i].st[k]);
+            if (dim[k] > 1 && (t[i].st[k] < (written ? a->d : 8) || t[i].st[k] % 8 != 0 || t[i].st[k] >= (1LL << 38)))
+                return set_error(VAE_ERR_SHAPE, "attention: %s's strides must be positive multiples of 8, and d at least where it is written "
+                                 "(stride %d: %lld)", t[i].name, k, t[i].st[k]);
     }
     s->b = a->b;
     s->sq = a->sq;
@@ -93,6 +94,8 @@ int vae_attention(const vae_attention_desc* desc, const void* q_dev, const void*
     if (!aligned16(q_dev) || !aligned16(k_dev) || !aligned16(v_dev) || !aligned16(o_dev) || !aligned16(lse_dev) ||
         !aligned16(workspace_dev))
         return set_error(VAE_ERR_ALIGN, "attention: pointers must be 16-byte aligned");
+    if (o_dev == q_dev || o_dev == k_dev || o_dev == v_dev)
+        return set_error(VAE_ERR_ARG, "attention: o may not be q, k or v");
     const size_t need = mha_fwd_bytes(s);
     if (need > 0 && (workspace_dev == nullptr || workspace_bytes < need))
         return set_error(VAE_ERR_NOMEM, "attention: workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -119,6 +122,12 @@ int vae_attention_backward(const vae_attention_desc* desc, const void* do_dev, c
         if (p == nullptr) return set_error(VAE_ERR_ARG, "attention: NULL tensor or workspace");
     for (const void* p : all)
         if (!aligned16(p)) return set_error(VAE_ERR_ALIGN, "attention: pointers must be 16-byte aligned");
+    const void* in[5] = {do_dev, q_dev, k_dev, v_dev, o_dev};
+    for (const void* p : in)
+        if (p == dq_dev || p == dk_dev || p == dv_dev)
+            return set_error(VAE_ERR_ARG, "attention: a gradient may not be written over an input");
+    if (dq_dev == dk_dev || dq_dev == dv_dev || dk_dev == dv_dev)
+        return set_error(VAE_ERR_ARG, "attention: dq, dk and dv must be tensors of their own");
     if (workspace_bytes < mha_bwd_bytes(s))
         return set_error(VAE_ERR_NOMEM, "attention: workspace of %zu bytes, %zu needed", workspace_bytes, mha_bwd_bytes(s));
     if ((rc = check_device()) != VAE_OK) return rc;

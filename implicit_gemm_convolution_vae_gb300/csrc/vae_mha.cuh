@@ -36,7 +36,7 @@ __device__ __forceinline__ int mha_len(const int* lens, int e, int n) {
 // the block that its position i + kl - ql lies in.
 __device__ __forceinline__ int mha_key_limit(int i, int ql, int kl, int block) {
     if (block <= 0) return kl;
-    const int at = i + kl - ql;
+    const int at = i - ql + kl;  // (in this order no sum passes 31 bits)
     if (at < 0) return 0;
     const long long end = (static_cast<long long>(at) / block + 1) * block;
     return end < kl ? static_cast<int>(end) : kl;

@@ -436,12 +436,12 @@ __device__ __forceinline__ KvWork kv_work(const BwdParams& p) {
     w.kl = mha_len(s.k_len, w.e, s.sk);
     const long long rows = static_cast<long long>(w.ql) << s.gp_log2;
     w.nt = static_cast<int>((rows + kMhaTile - 1) / kMhaTile);
-    int i0 = 0;  // the first query that sees a key of the first tile
+    long long i0 = 0;  // the first query that sees a key of the first tile
     if (s.block > 0) {
-        i0 = kb0 * kMhaTile / s.block * s.block - (w.kl - w.ql);
+        i0 = static_cast<long long>(kb0 * kMhaTile / s.block * s.block) - (w.kl - w.ql);
         if (i0 < 0) i0 = 0;
     }
-    const long long t0 = (static_cast<long long>(i0) << s.gp_log2) / kMhaTile;
+    const long long t0 = (i0 << s.gp_log2) / kMhaTile;
     w.t0 = t0 < w.nt ? static_cast<int>(t0) : w.nt;
     const int all = kb0 * kMhaTile < w.kl ? s.nsub * (w.nt - w.t0) : 0;
     const int per = (all + p.nsplit_k - 1) / p.nsplit_k;
@@ -572,7 +572,7 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
     const float f = T == VAE_F16 ? c * (1.f / (1 << kPLog2)) : 1.f;  // dS c = (P 2^14) (dP - D) f
     // the first row of the group's packing that sees key j
     long long see = 0;
-    if (sh.block > 0) see = static_cast<long long>(j / sh.block * sh.block - (w.kl - w.ql)) * (1 << sh.gp_log2);
+    if (sh.block > 0) see = (static_cast<long long>(j / sh.block * sh.block) - (w.kl - w.ql)) * (1 << sh.gp_log2);
     const int per = w.nt - w.t0;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
@@ -1026,7 +1026,7 @@ void split_plan(long long heads, int tiles, long long other, double tile_us, dou
     *csize = heads * tiles >= kTargetCtas && tiles >= 2 ? 2 : 1;
     const long long each = heads * ((tiles + *csize - 1) / *csize * *csize);
     double least = 0.0;
-    for (int n = 1; n == 1 || (n <= most && each * n <= 8 * kTargetCtas); ++n) {
+    for (int n = 1; n == 1 || (n <= most && each * n <= 4 * kTargetCtas); ++n) {
         const double waves = static_cast<double>((each * n - 1) / kTargetCtas + 1);
         double t = waves * (static_cast<double>((other - 1) / n + 1) * tile_us + 5.0);
         if (n > 1) t += 3.0 + 8.0 * n * sum / 6e6;
@@ -1074,10 +1074,11 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
     if (T == VAE_F16) VAE_CUDA_CHECK(cudaMemsetAsync(pp.maxima, 0, 2 * sizeof(unsigned), st));
     const long long prep = f.row_tiles + (T == VAE_F16 ? f.key_tiles : 0);
     VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
-    // (the query-tile kernel first: it may put its D into the side rows)
-    VAE_CUDA_CHECK(launch_kernel_as(pdl_enabled(), static_cast<unsigned>(f.csize_q), mha_dq_kernel<T, kSteps>,
+    // (The query-tile kernel first: it may put its D into the side rows. Always launched as clusters, of one CTA at least:
+    // a commit or copy with a cluster mask is an illegal instruction in a grid that was launched without.)
+    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_q), mha_dq_kernel<T, kSteps>,
                                     dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), kQSmem, st, map[2], map[3], p));
-    VAE_CUDA_CHECK(launch_kernel_as(pdl_enabled(), static_cast<unsigned>(f.csize_k), mha_dkv_kernel<T, kSteps>,
+    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_k), mha_dkv_kernel<T, kSteps>,
                                     dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), kKvSmem, st, map[0], map[1], map[2],
                                     map[3], p));
     const MhaShape& s = p.s;

@@ -808,7 +808,7 @@ FwdPlan fwd_plan(const MhaShape& s) {
     for (int alt = s.ntile == 1; alt < 2; ++alt) {
         const long long items = heads * s.b * (alt ? s.ntile : (s.ntile + 1) / 2);
         const int most = s.nkb / 2;  // two key tiles a CTA at least
-        for (int n = 1; n == 1 || (n <= most && items * n <= 8 * kTargetCtas); ++n) {
+        for (int n = 1; n == 1 || (n <= most && items * n <= 4 * kTargetCtas); ++n) {
             const double waves = static_cast<double>((items * n - 1) / kTargetCtas + 1);
             double t = waves * (((s.nkb - 1) / n + 1) * (alt ? 1.2 : 1.65) + 4.0);
             if (n > 1) t += 3.0 + 8.0 * n * s.b * s.hq * s.sq * s.d / 6e6;

@@ -440,11 +440,15 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
  *   same bits. dq rows from ql on and dk, dv rows from kl on are not written.
  * Requirements: b, sq, sk >= 1; hq % hkv == 0; d % 8 == 0, 8 <= d <= 128;
  * scale > 0 and finite; pointers 16-byte aligned; strides multiples of 8,
- * positive where the dimension is over 1 (a broadcast is not taken: give k and
- * v their hkv heads). b * hq * sq and b * hkv * sk at most 2^31 - 256.
+ * positive where the dimension is over 1, at least d in o, dq, dk and dv (a
+ * broadcast is not taken: give k and v their hkv heads). What is written lies
+ * apart from what is read, and dq, dk and dv from one another. b * hq * sq and b * hkv * sk at most 2^31 - 256.
  * workspace_dev: vae_attention_workspace_bytes(desc) /
  * vae_attention_backward_workspace_bytes(desc) bytes, 16-byte aligned, contents
  * ignored on entry, NULL where that is 0. Both depend on the desc's sizes alone.
+ * Before a call is captured into a graph, make one like it eagerly (the first
+ * call of a kernel sets it up on its device). The same holds for the operators
+ * above.
  */
 typedef struct {
     int type;

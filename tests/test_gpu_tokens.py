@@ -450,6 +450,19 @@ def test_attention_streams_and_captured_graphs():
     assert torch.equal(go, o2) and torch.equal(gl, l2)
 
 
+def test_operators_launched_ahead():
+    """With every kernel launched while the one before it still runs (VAE_PDL=1, read once per process): the same
+    results, as each waits for the grid before it."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", os.path.abspath(__file__),
+                        "-k", "strided_views or together or test_token_block or peaked or joint or in_place"],
+                       cwd=root, env=dict(os.environ, VAE_PDL="1"), capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
+
+
 # ───────────────────────────── together ─────────────────────────────
 
 def test_token_block_forward_and_backward():

@@ -118,43 +118,55 @@ def _desc(**kw):
     return a
 
 
+P5 = [FAKE + i * 65536 for i in range(5)]
+P10 = [FAKE + i * 65536 for i in range(10)]
 BAD = [(dict(type=F32), -1), (dict(type=9), -1), (dict(b=0), -2), (dict(sq=0), -2), (dict(sk=0), -2), (dict(hq=0), -2),
        (dict(hkv=0), -2), (dict(hq=7), -2), (dict(d=0), -2), (dict(d=12), -2), (dict(d=136), -2), (dict(scale=0.0), -1),
        (dict(scale=-1.0), -1), (dict(scale=NAN), -1), (dict(scale=INF), -1), (dict(block=-1), -1),
        (dict(q_stride=(15360, 384, 60)), -2), (dict(k_stride=(9600, 192, 0)), -2), (dict(v_stride=(9600, -192, 64)), -2),
-       (dict(o_stride=(0, 384, 64)), -2), (dict(b=1 << 12, sq=1 << 20), -2)]
+       (dict(o_stride=(0, 384, 64)), -2), (dict(o_stride=(15360, 384, 56)), -2), (dict(b=1 << 12, sq=1 << 20), -2)]
 
 
 @pytest.mark.parametrize("bad,code", BAD)
 def test_attention_refuses_bad_descs(L, bad, code):
     a = ctypes.byref(_desc(**bad))
     assert L.vae_attention_backward_workspace_bytes(a) == 0
-    assert L.vae_attention(a, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == code
-    assert L.vae_attention_backward(a, *[FAKE] * 10, 1 << 40, None) == code
+    assert L.vae_attention(a, *P5, FAKE, 1 << 40, None) == code
+    assert L.vae_attention_backward(a, *P10, 1 << 40, None) == code
 
 
 def test_attention_refuses_bad_pointers_and_workspaces(L):
     a = ctypes.byref(_desc())
-    assert L.vae_attention(None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == -1
+    assert L.vae_attention(None, *P5, FAKE, 1 << 40, None) == -1
     for i in range(5):
-        p = [FAKE] * 5
+        p = list(P5)
         p[i] = None
         assert L.vae_attention(a, *p, FAKE, 1 << 40, None) == -1
         p[i] = FAKE + 8
         assert L.vae_attention(a, *p, FAKE, 1 << 40, None) == -3
-    assert L.vae_attention_backward(None, *[FAKE] * 10, 1 << 40, None) == -1
+    for i in range(3):  # o over q, k or v
+        p = list(P5)
+        p[3] = p[i]
+        assert L.vae_attention(a, *p, FAKE, 1 << 40, None) == -1
+        assert "may not be" in vg.last_error()
+    assert L.vae_attention_backward(None, *P10, 1 << 40, None) == -1
     for i in range(10):
-        p = [FAKE] * 10
+        p = list(P10)
         p[i] = None
         assert L.vae_attention_backward(a, *p, 1 << 40, None) == -1
         p[i] = FAKE + 8
         assert L.vae_attention_backward(a, *p, 1 << 40, None) == -3
+    for i in (6, 7, 8):  # a gradient over an input, or over another
+        for j in (0, 1, 2, 3, 4, 6 + (i - 5) % 3):
+            p = list(P10)
+            p[i] = p[j]
+            assert L.vae_attention_backward(a, *p, 1 << 40, None) == -1
     n = L.vae_attention_backward_workspace_bytes(a)
     assert n > 0 and n % 16 == 0
-    assert L.vae_attention_backward(a, *[FAKE] * 10, n - 1, None) == -4
+    assert L.vae_attention_backward(a, *P10, n - 1, None) == -4
     for bad in (dict(do_stride=(15360, 384, 4)), dict(dq_stride=(15360, 0, 64)), dict(dk_stride=(1, 192, 64)),
-                dict(dv_stride=(9600, 192, -64))):
-        assert L.vae_attention_backward(ctypes.byref(_desc(**bad)), *[FAKE] * 10, 1 << 40, None) == -2
+                dict(dv_stride=(9600, 192, -64)), dict(dq_stride=(15360, 384, 32))):
+        assert L.vae_attention_backward(ctypes.byref(_desc(**bad)), *P10, 1 << 40, None) == -2
 
 
 def test_workspace_sizes_follow_the_shape(L):
@@ -189,5 +201,5 @@ def test_no_cpu_fallback_without_a_gpu(L):
         pytest.skip("a GPU is present")
     assert L.vae_layernorm(FAKE, F32, 4, 64, None, None, 1e-6, FAKE, F32, None) in (-5, -7)
     n = 1 << 40
-    assert L.vae_attention(ctypes.byref(_desc()), *[FAKE] * 6, n, None) in (-5, -7)
-    assert L.vae_attention_backward(ctypes.byref(_desc()), *[FAKE] * 10, n, None) in (-5, -7)
+    assert L.vae_attention(ctypes.byref(_desc()), *P5, FAKE, n, None) in (-5, -7)
+    assert L.vae_attention_backward(ctypes.byref(_desc()), *P10, n, None) in (-5, -7)
