@@ -437,7 +437,8 @@ __device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork&
 #pragma unroll
             for (int c = 0; c < 8; ++c)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[c][k]));
+                for (int k = 0; k < 16; k += 2)
+                    mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
             if (j < step) {  // the stream's first tile
                 m = top;
