@@ -7,6 +7,11 @@
 // digits and no 64-bit arithmetic runs on the device. A block computes the
 // (cos, sin) of its tokens' pairs once in shared memory, then turns every head
 // of those tokens: one read and one write of the tensor, which bounds the call.
+// Measured on GB300 at 36864 tokens x 18 heads x 128 in f16 (340 MB): 70 us
+// interleaved (4.9 TB/s), 60 us in halves (5.7 TB/s). Small blocks, so that the
+// angles of some are formed while others move rows: 8 tokens, 128 threads, 12
+// blocks an SM and two rows a thread in flight; 32 tokens and four blocks of 256
+// threads with four rows in flight took 75 and 66 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -17,9 +22,10 @@ namespace vae {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxD = 256;
-constexpr int kRopeTokens = 32;  // tokens per block, at most
+constexpr int kRopeTokens = 8;  // tokens per block, at most
+// Threads of a block: a row's units (up to 255 one by one, 32 in vectors) have to fit.
+__host__ __device__ constexpr int rope_threads(int unit) { return unit > 1 ? 128 : 256; }
 constexpr int kRopePitch = VAE_ROPE_MAX_PAIRS + 2;  // of a token's (cos, sin) row: 16-byte aligned, few bank conflicts
 
 struct RopeParams {
@@ -80,13 +86,13 @@ struct RopeUnit {
 // thread turns 16 or 32 bytes a row) go to threads side by side, and a thread keeps its unit on every row it
 // meets. The first rows are on their way while the angles are formed.
 template <int T, int kN, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p, const __grid_constant__ vae_rope_plan plan) {
+__global__ void __launch_bounds__(rope_threads(kN), 1536 / rope_threads(kN)) rope_kernel(const RopeParams p, const __grid_constant__ vae_rope_plan plan) {
     using E = typename Elem<T>::type;
     using Unit = RopeUnit<T, kN>;
+    constexpr int kThreads = rope_threads(kN);
     constexpr bool kV8 = kN > 1;
     constexpr bool kTwo = !(kV8 && kInter);  // two units turn together
-    // rows whose loads a thread has in flight together (64 registers leave room for 64 bytes twice over)
-    constexpr int kRopeBatch = kTwo && kV8 && T == VAE_F32 ? 2 : 4;
+    constexpr int kRopeBatch = 2;  // rows whose loads a thread has in flight together
     __shared__ __align__(16) float2 cs[kRopeTokens][kRopePitch];
     pdl_wait();
     const int t0 = static_cast<int>(blockIdx.x) * p.tpb;
@@ -94,8 +100,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
     const int b0 = t0 / p.s, s0 = t0 - b0 * p.s;
     const int pairs = plan.pairs, rot = 2 * pairs;
     const int nrot = kTwo ? pairs / kN : rot / kN;
-    const int units = nrot + (p.d - rot) / kN;  // (256 at most: d)
-    const int step = kRopeThreads / units;      // rows that the block takes at a time
+    const int units = nrot + (p.d - rot) / kN;  // (kThreads at most)
+    const int step = kThreads / units;          // rows that the block takes at a time
     const int u = threadIdx.x % units;
     const bool copied = u >= nrot;
     const int ia = copied ? rot + (u - nrot) * kN : (!kV8 && kInter ? 2 * u : u * kN);
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
         }
     };
     load();
-    for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
         // neighbours take the tokens of one pair: its entries of the plan are one address for them, and the constant
         // bank serves one address at a time (a pair per lane took 3/4 of the call on few heads)
         const int pr = i / nt, t = i - pr * nt;
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
 template <int T>
 cudaError_t rope_launch(int unit, bool inter, unsigned grid, cudaStream_t s, const RopeParams& p,
                         const vae_rope_plan& plan) {
-    const auto go = [&](auto k) { return launch_kernel(k, dim3(grid), dim3(kRopeThreads), 0, s, p, plan); };
+    const auto go = [&](auto k) { return launch_kernel(k, dim3(grid), dim3(rope_threads(unit)), 0, s, p, plan); };
     if constexpr (T != VAE_F32)
         if (unit == 16) return go(rope_kernel<T, 16, true>);
     if (unit == 8) return inter ? go(rope_kernel<T, 8, true>) : go(rope_kernel<T, 8, false>);
@@ -270,7 +276,8 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
     p.pos_batch = pos_batch;
     p.inverse = inverse != 0;
     // Vectors where every row starts on 16 bytes and holds whole ones. Interleaved 16-bit pairs: sixteen channels a
-    // thread where they fit (340 MB: 74.6 us against 80.7 with eight; f32 measured 32.4 against 28.2 and keeps eight).
+    // thread where they fit (340 MB with blocks of 256: 74.6 us against 80.7 with eight; f32, 57 MB: 32.4 against 28.2,
+    // and keeps eight).
     bool v8 = aligned16(x_dev) && aligned16(y_dev) && d % 8 == 0 &&
               (plan->interleaved ? 2 * plan->pairs : plan->pairs) % 8 == 0;
     for (int i = 0; i < 3; ++i) {

@@ -176,7 +176,8 @@ ROPE = [(1, 1, 1, 2, (2,), "f32", True, True, False), (2, 5, 3, 10, (2, 6), "f16
         (1, 256, 8, 64, (32, 32), "bf16", True, True, False), (2, 33, 6, 128, (16, 56, 56), "f16", True, False, True),
         (2, 33, 6, 128, (16, 56, 56), "bf16", False, True, False), (1, 700, 5, 96, (0, 32, 32), "f16", False, True, True),
         (3, 19, 2, 256, (64, 64, 64, 64), "f32", True, False, True), (1, 50, 4, 72, (8, 24, 24), "f32", False, True, False),
-        (1, 50, 4, 66, (2, 32, 32), "f16", True, True, False), (2, 1000, 40, 40, (8, 16, 16), "bf16", True, False, True)]
+        (1, 50, 4, 66, (2, 32, 32), "f16", True, True, False), (2, 1000, 40, 40, (8, 16, 16), "bf16", True, False, True),
+        (1, 9, 2, 256, (2,), "f16", True, True, False), (1, 700, 3, 255, (2,), "bf16", False, False, False), (2, 5, 2, 253, (100, 2, 0, 8), "f32", False, True, True)]
 
 
 @pytest.mark.parametrize("case", ROPE)
