@@ -658,13 +658,13 @@ def _rope(x, positions, plan, inverse, out, stream):
     return out
 
 
-# struct vae_attention_desc: type .. d, scale, block (and its padding), the two lengths, eight times three strides
-_DESC = struct.Struct("=7ifi4x2Q24q")
+# struct vae_attention_desc: type .. d, scale, block, fill, the two lengths, eight times three strides
+_DESC = struct.Struct("=7if2i2Q24q")
 _NO_STRIDES = (0,) * 12
 
 
-def _attention_args(q, k, v, scale, q_len, k_len, block):
-    """(the desc's fields up to v's strides, b, sq, hq) of a call; checks q, k, v and the lengths."""
+def _attention_args(q, k, v, scale, q_len, k_len, block, fill):
+    """The desc's fields up to v's strides; checks q, k, v and the lengths."""
     dtype = q.dtype
     for t, nm in ((q, "q"), (k, "k"), (v, "v")):
         if t.dim() != 4:
@@ -684,7 +684,7 @@ def _attention_args(q, k, v, scale, q_len, k_len, block):
         _tensor(q_len, "q_len", _T.i32, (b,))
     if k_len is not None:
         _tensor(k_len, "k_len", _T.i32, (b,))
-    return (_type(dtype, "q"), b, sq, sk, hq, hkv, d, 1.0 / d ** 0.5 if scale is None else scale, block,
+    return (_type(dtype, "q"), b, sq, sk, hq, hkv, d, 1.0 / d ** 0.5 if scale is None else scale, block, fill,
             0 if q_len is None else q_len.data_ptr(), 0 if k_len is None else k_len.data_ptr(), *_strides3(q, "q"),
             *_strides3(k, "k"), *_strides3(v, "v"))
 
@@ -707,7 +707,7 @@ def _dense(n, h, d):
 
 def attention_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
     q, k = _dense(sq, hq, d), _dense(sk, hkv, d)
-    return int(lib().vae_attention_workspace_bytes(_DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, *q, *k, *k, *q,
+    return int(lib().vae_attention_workspace_bytes(_DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, 0, *q, *k, *k, *q,
                                                               *_NO_STRIDES)))
 
 
@@ -726,12 +726,14 @@ def attention(q, k, v, scale: Optional[float] = None, q_len=None, k_len=None, bl
 
 
 def _attention(q, k, v, scale, q_len, k_len, block, out, lse, workspace, stream):
-    args = _attention_args(q, k, v, scale, q_len, k_len, block)
+    # new tensors are filled behind the lengths by the kernels; beside one that the caller gave, beforehand
+    fill = out is None and lse is None
+    args = _attention_args(q, k, v, scale, q_len, k_len, block, fill)
     b, sq, hq, _ = q.shape
-    out = _like(out, q, "out", q_len)
+    out = _like(out, q, "out", None if fill else q_len)
     if lse is not None:
         _tensor(lse, "lse", _T.f32, (b, hq, sq))
-    elif q_len is None:
+    elif fill or q_len is None:
         lse = _T.empty((b, hq, sq), dtype=_T.f32, device=q.device)
     else:
         lse = _T.torch.full((b, hq, sq), -float("inf"), dtype=_T.f32, device=q.device)
@@ -748,7 +750,7 @@ def _attention(q, k, v, scale, q_len, k_len, block, out, lse, workspace, stream)
 def attention_backward_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
     q, k = _dense(sq, hq, d), _dense(sk, hkv, d)
     return int(lib().vae_attention_backward_workspace_bytes(
-        _DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, *q, *k, *k, *q, *q, *q, *k, *k)))
+        _DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, 0, *q, *k, *k, *q, *q, *q, *k, *k)))
 
 
 def attention_backward(do, q, k, v, o, lse, scale: Optional[float] = None, q_len=None, k_len=None, block: int = 0,
@@ -764,13 +766,15 @@ def attention_backward(do, q, k, v, o, lse, scale: Optional[float] = None, q_len
 
 
 def _attention_backward(do, q, k, v, o, lse, scale, q_len, k_len, block, dq, dk, dv, workspace, stream):
-    args = _attention_args(q, k, v, scale, q_len, k_len, block)
+    fill = dq is None and dk is None and dv is None
+    args = _attention_args(q, k, v, scale, q_len, k_len, block, fill)
     b, sq, hq, _ = q.shape
     _like(do, q, "do", None)
     _like(o, q, "o", None)
     _tensor(lse, "lse", _T.f32, (b, hq, sq))
-    dq = _like(dq, q, "dq", q_len)
-    dk, dv = _like(dk, k, "dk", k_len), _like(dv, k, "dv", k_len)
+    q_fill, k_fill = (None, None) if fill else (q_len, k_len)
+    dq = _like(dq, q, "dq", q_fill)
+    dk, dv = _like(dk, k, "dk", k_fill), _like(dv, k, "dv", k_fill)
     desc = _DESC.pack(*args, *_strides3(o, "o"), *_strides3(do, "do"), *_strides3(dq, "dq"), *_strides3(dk, "dk"),
                       *_strides3(dv, "dv"))
     L = lib()

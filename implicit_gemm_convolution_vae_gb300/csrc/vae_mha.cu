@@ -46,6 +46,7 @@ int mha_check(const vae_attention_desc* a, bool backward, MhaShape* s) {
     s->g = a->hq / a->hkv;
     s->d = a->d;
     s->block = a->block;
+    s->fill = a->fill != 0;
     // gp: the largest power of two in g, half a tile's rows at most
     s->gp_log2 = 0;
     while (s->gp_log2 < 6 && s->g % (2 << s->gp_log2) == 0) ++s->gp_log2;

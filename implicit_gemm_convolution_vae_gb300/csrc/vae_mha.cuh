@@ -16,6 +16,7 @@ namespace vae {
 
 struct MhaShape {
     int b, sq, sk, hq, hkv, g, d, block;
+    int fill;           // rows behind the lengths are written as 0
     int gp_log2, nsub;  // gp = 1 << gp_log2, nsub = g / gp
     int ntile;          // 128-row tiles of sq * gp rows
     int nkb;            // 128-key tiles of sk
@@ -162,6 +163,32 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// Writes 0 to the rows of a 128-row query tile of key head hk that lie behind
+// ql (and -infinity to their lse, where there is one), or to the rows from kl
+// on of a key tile; every thread of the block.
+__device__ __forceinline__ void mha_fill_row(void* x, long long off, int d, int part) {
+    for (int c = part * 8; c < d; c += 32)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + off + c) = make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void mha_fill_queries(const MhaShape& s, int e, int hk, int sub, int tile, int ql, void* x,
+                                                 long long sb, long long ss, long long sh, float* lse) {
+    const int gp = 1 << s.gp_log2;
+    if (ql == s.sq || tile >= s.ntile || ((tile + 1) * static_cast<long long>(kMhaTile) - 1) >> s.gp_log2 < ql) return;
+    for (int k = threadIdx.x; k < kMhaTile * 4; k += blockDim.x) {
+        const int r = tile * kMhaTile + k / 4, i = r >> s.gp_log2, h = hk * s.g + sub * gp + (r & (gp - 1));
+        if (i < ql || i >= s.sq) continue;
+        mha_fill_row(x, e * sb + i * ss + h * sh, s.d, k & 3);
+        if (lse != nullptr && (k & 3) == 0) lse[(static_cast<long long>(e) * s.hq + h) * s.sq + i] = -INFINITY;
+    }
+}
+__device__ __forceinline__ void mha_fill_keys(const MhaShape& s, int e, int hk, int kb, int kl, void* x, long long sb,
+                                              long long ss, long long sh) {
+    for (int k = threadIdx.x; k < kMhaTile * 4; k += blockDim.x) {
+        const int j = kb * kMhaTile + k / 4;
+        if (j >= kl && j < s.sk) mha_fill_row(x, e * sb + j * ss + hk * sh, s.d, k & 3);
+    }
 }
 
 // Zeroes rows [from, 128) of a tile of `chunks` chunks in shared memory; the

@@ -682,6 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const KvWork w = kv_work(p);
+    if (p.s.fill && p.nsplit_k == 1) {  // (else the joining kernel does)
+        mha_fill_keys(p.s, w.e, w.hk, w.kb, w.kl, p.dk, p.dks.b, p.dks.s, p.dks.h);
+        mha_fill_keys(p.s, w.e, w.hk, w.kb, w.kl, p.dv, p.dvs.b, p.dvs.s, p.dvs.h);
+    }
     if (w.n == 0) {  // no query: zeros within the length
         const int j = w.kb * kMhaTile + (threadIdx.x & 127);
         if (threadIdx.x < 2 * kMhaTile && j < w.kl) {
@@ -964,6 +968,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     pdl_wait();
     const QWork w = q_work(p);
+    if (p.s.fill && p.nsplit_q == 1)  // (else the joining kernel does)
+        mha_fill_queries(p.s, w.e, w.hk, w.sub, w.tile, w.ql, p.dq, p.dqs.b, p.dqs.s, p.dqs.h, nullptr);
     if (w.n == 0) {  // no key: zeros within the length
         const int r = w.tile * kMhaTile + threadIdx.x;
         const int i = r >> p.s.gp_log2, h = w.hk * p.s.g + (w.sub << p.s.gp_log2) + (r & ((1 << p.s.gp_log2) - 1));
@@ -989,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int T>
 __global__ void __launch_bounds__(256)
     mha_sum_kernel(const float* __restrict__ part, long long split_stride, int nsplit, int b, int h, int n, int d,
-                   const int* len, void* out, MhaStrides os) {
+                   const int* len, int fill, void* out, MhaStrides os) {
     pdl_wait();
     const long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const int d4 = d / 4;
@@ -997,7 +1003,11 @@ __global__ void __launch_bounds__(256)
     if (row >= static_cast<long long>(b) * h * n) return;
     const int c = static_cast<int>(x - row * d4) * 4;
     const int i = static_cast<int>(row % n), hh = static_cast<int>(row / n % h), e = static_cast<int>(row / n / h);
-    if (i >= mha_len(len, e, n)) return;
+    if (i >= mha_len(len, e, n)) {
+        if (fill)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + e * os.b + i * os.s + hh * os.h + c) = make_uint2(0u, 0u);
+        return;
+    }
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < nsplit; ++k) {
         const float4 v = *reinterpret_cast<const float4*>(part + k * split_stride + row * d + c);
@@ -1088,13 +1098,13 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
         for (int k = 0; k < 2; ++k)
             VAE_CUDA_CHECK(launch_kernel(mha_sum_kernel<T>, dim3(grid), dim3(256), 0, st,
                                          static_cast<const float*>(p.part_kv) + k * rows * s.d, 2 * rows * s.d, f.nsplit_k,
-                                         s.b, s.hkv, s.sk, s.d, s.k_len, k == 0 ? p.dv : p.dk, k == 0 ? p.dvs : p.dks));
+                                         s.b, s.hkv, s.sk, s.d, s.k_len, s.fill, k == 0 ? p.dv : p.dk, k == 0 ? p.dvs : p.dks));
     }
     if (f.nsplit_q > 1) {
         const long long rows = static_cast<long long>(s.b) * s.hq * s.sq;
         const unsigned grid = static_cast<unsigned>((rows * (s.d / 4) + 255) / 256);
         VAE_CUDA_CHECK(launch_kernel(mha_sum_kernel<T>, dim3(grid), dim3(256), 0, st, static_cast<const float*>(p.part_q),
-                                     rows * s.d, f.nsplit_q, s.b, s.hq, s.sq, s.d, s.q_len, p.dq, p.dqs));
+                                     rows * s.d, f.nsplit_q, s.b, s.hq, s.sq, s.d, s.q_len, s.fill, p.dq, p.dqs));
     }
     return VAE_OK;
 }

@@ -681,6 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     const FwdWork w = fwd_work(p);
     if (w.e == p.s.b) return;  // more pieces than runs of key tiles
+    if (p.s.fill && p.nsplit == 1)  // (else the joining kernel does)
+        for (int t = 0; t < (p.alt ? 1 : 2); ++t)
+            mha_fill_queries(p.s, w.e, w.hk, w.sub, w.tile[t], w.ql, p.o, p.os.b, p.os.s, p.os.h, p.lse);
     if (w.n == 0) {  // no key: rows within the length give 0 and -infinity
         const int gp = 1 << p.s.gp_log2;
         for (int t = 0; t < (p.alt ? 1 : 2); ++t) {
@@ -754,7 +757,13 @@ __global__ void __launch_bounds__(128) mha_join_kernel(const FwdParams p) {
     if (row >= rows) return;
     const int i = static_cast<int>(row % s.sq), h = static_cast<int>(row / s.sq % s.hq);
     const int e = static_cast<int>(row / per);
-    if (i >= mha_len(s.q_len, e, s.sq)) return;
+    if (i >= mha_len(s.q_len, e, s.sq)) {
+        if (s.fill) {
+            if (lane < 4) mha_fill_row(p.o, e * p.os.b + i * p.os.s + h * p.os.h, s.d, lane);
+            if (lane == 0) p.lse[row] = -INFINITY;
+        }
+        return;
+    }
     const Pieces x = find_piece(s, p.nsplit * s.b, -1, e);
     const long long row0 = x.first * per + (row - e * per);  // its place in the entry's first piece
     float mm = -INFINITY;

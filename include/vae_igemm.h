@@ -430,14 +430,15 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
  *   position i + kl - ql and sees the keys of its own block and the earlier
  *   ones, j < (floor(position / block) + 1) * block; at a negative position none.
  * A row that sees no key gives o = 0, lse = -infinity. Rows from ql on are not
- * written. Keys and values from kl on, and queries from ql on, may hold
+ * written (with fill: 0, lse = -infinity). Keys and values from kl on, and queries from ql on, may hold
  * anything; a key within kl that a row does not see must be finite.
  * vae_attention_backward: with P = exp(scale q k^T - lse), D = sum(do * o),
  *   dv = P^T do, dS = P * (do v^T - D) * scale, dq = dS k, dk = dS^T q,
  *   summed over the query heads that share a key head; o and lse from
  *   vae_attention of the same inputs. P is recomputed; dk and dv are formed per
  *   key tile and dq per query tile, in a fixed order: the same inputs give the
- *   same bits. dq rows from ql on and dk, dv rows from kl on are not written.
+ *   same bits. dq rows from ql on and dk, dv rows from kl on are not written
+ *   (with fill: 0).
  * Requirements: b, sq, sk >= 1; hq % hkv == 0; d % 8 == 0, 8 <= d <= 128;
  * scale > 0 and finite; pointers 16-byte aligned; strides multiples of 8,
  * positive where the dimension is over 1, at least d in o, dq, dk and dv (a
@@ -455,6 +456,7 @@ typedef struct {
     int b, sq, sk, hq, hkv, d;
     float scale;
     int block;
+    int fill;  /* 0: rows behind the lengths are left as they were; else written: 0, and lse -infinity */
     const int* q_len_dev;
     const int* k_len_dev;
     long long q_stride[3], k_stride[3], v_stride[3], o_stride[3];

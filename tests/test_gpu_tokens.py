@@ -399,6 +399,23 @@ def test_attention_scale_and_lengths_out_of_range_are_clamped():
     _within(ref, ro, U["f16"] * np.abs(ro) + FLOOR["f16"] + (U["f16"] + SUM * (4 + 2 * qk.max())) * pv * 1.01 + 2.0 ** -24 * pv.max())
 
 
+def test_attention_new_tensors_beside_given_ones():
+    """Rows behind the lengths: left in a tensor that the caller gave, 0 (lse -inf) in new ones, whichever are given."""
+    torch = torch_mod()
+    case = (3, 150, 160, 4, 2, 80, "f16", 0, [150, 0, 1], [160, 33, 0])
+    (q, k, v, do), _, kw, _ = _att_inputs(case)
+    rows, keys = (torch.from_numpy(m).cuda() for m in _rows_behind(case))
+    o, lse = vg.attention(q, k, v, **kw)
+    o1, l1 = vg.attention(q, k, v, out=torch.full_like(q, 7.0), **kw)
+    assert torch.equal(l1, lse) and (o1[rows] == 7.0).all() and torch.equal(o1[~rows], o[~rows]) and not o[rows].any()
+    o2, l2 = vg.attention(q, k, v, lse=torch.full_like(lse, 7.0), **kw)
+    assert torch.equal(o2, o) and (l2.transpose(1, 2)[rows] == 7.0).all()
+    dq, dk, dv = vg.attention_backward(do, q, k, v, o, lse, **kw)
+    dq1, dk1, dv1 = vg.attention_backward(do, q, k, v, o, lse, dk=torch.full_like(k, 7.0), **kw)
+    assert torch.equal(dq1, dq) and torch.equal(dv1, dv) and (dk1[keys] == 7.0).all() and torch.equal(dk1[~keys], dk[~keys])
+    assert not dq[rows].any() and not dk[keys].any() and not dv[keys].any()
+
+
 def test_attention_offsets_past_32_bits():
     """The second batch entry's keys lie over 2^31 elements behind the first's."""
     torch = torch_mod()

@@ -91,15 +91,15 @@ def test_rope_refusals(L):
 class AttentionDesc(ctypes.Structure):
     """vae_attention_desc as the header declares it."""
     _fields_ = [(n, ctypes.c_int) for n in ("type", "b", "sq", "sk", "hq", "hkv", "d")] + \
-        [("scale", ctypes.c_float), ("block", ctypes.c_int), ("q_len", ctypes.c_void_p), ("k_len", ctypes.c_void_p)] + \
+        [("scale", ctypes.c_float), ("block", ctypes.c_int), ("fill", ctypes.c_int), ("q_len", ctypes.c_void_p), ("k_len", ctypes.c_void_p)] + \
         [(n + "_stride", ctypes.c_longlong * 3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")]
 
 
 def test_binding_packs_the_desc_as_declared(L):
-    a = AttentionDesc(2, 3, 4, 5, 6, 7, 8, 0.5, 9, 1 << 40, 1 << 41)
+    a = AttentionDesc(2, 3, 4, 5, 6, 7, 8, 0.5, 9, 1, 1 << 40, 1 << 41)
     for i, n in enumerate(("q", "k", "v", "o", "do", "dq", "dk", "dv")):
         setattr(a, n + "_stride", (ctypes.c_longlong * 3)(*[(i * 3 + j + 1) << 33 for j in range(3)]))
-    assert bytes(a) == vg._DESC.pack(2, 3, 4, 5, 6, 7, 8, 0.5, 9, 1 << 40, 1 << 41, *[(i + 1) << 33 for i in range(24)])
+    assert bytes(a) == vg._DESC.pack(2, 3, 4, 5, 6, 7, 8, 0.5, 9, True, 1 << 40, 1 << 41, *[(i + 1) << 33 for i in range(24)])
 
 
 def _dense(b, n, h, d):
