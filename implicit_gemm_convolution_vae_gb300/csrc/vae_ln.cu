@@ -12,6 +12,8 @@
 // Plain form (few rows, other lengths): rows of up to 1280 channels belong to
 // one warp, wider ones to a block, loaded straight into registers, in 16-byte
 // vectors where the length is a multiple of eight, else element by element.
+// Measured on GB300: 16384x1152 f32 to f16 (113 MB) 20.4 us in the ring form, 24.9
+// in the plain one; its gradient over 65536 rows (755 MB) 123 us (6.1 TB/s) and 192.
 //
 // The gradients of gamma and beta are column sums over all rows: every thread
 // keeps the same columns on every row it meets, so it sums them in registers,

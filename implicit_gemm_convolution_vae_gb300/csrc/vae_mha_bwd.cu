@@ -32,6 +32,12 @@
 // first runs over their keys once for D = rowsum(P * dP) itself, and hands it
 // to the key-tile kernel after it.
 //
+// Measured on GB300: 16384 tokens x 9 heads x 128 in f16 2650 to 2900 us (1070 to
+// 1170 TFLOP/s of the five products' flops). A step takes 2590 cycles in the
+// query-tile kernel (2090 with no hand-over between warps, 1536 at the tensor
+// rate) and 3390 in the key-tile kernel (2600, 2048): bound by the MMAs under
+// shared-memory bandwidth, then by the hand-overs.
+//
 // 16 bits. P and dS are rounded to the tensors' type for the products, half a
 // step of 2^-8 or 2^-11 relative, as the forward's P. f16 would lose long rows'
 // P ~ 1/n below 2^-14, so it holds P 2^14 and dS c, with c the power of two
