@@ -5,11 +5,11 @@
 // traffic: both directions are bound by reading their inputs and writing their
 // output once.
 //
-// Ring form (many rows of a multiple of eight channels, up to 5120): one block
-// per SM stays; rows belong to groups of one to eight warps, whose next rows are
-// already on the way into shared memory by bulk copies while they work on the
-// last one. Registers then hold one row only and the loads never pause.
-// Plain form (few rows, other lengths): rows of up to 1280 channels belong to
+// Ring form (many rows of up to 5120 channels; forward: of a multiple of eight):
+// one block per SM stays; rows belong to groups of one to eight warps, whose next
+// rows are already on the way into shared memory by bulk copies while they work
+// on the last ones. Registers hold those only and the loads never pause.
+// Plain form (few rows, or longer ones): rows of up to 1280 channels belong to
 // one warp, wider ones to a block, loaded straight into registers, in 16-byte
 // vectors where the length is a multiple of eight, else element by element.
 // Measured on GB300: 16384x1152 f32 to f16 (113 MB) 20.4 us in the ring form, 24.9
@@ -17,12 +17,13 @@
 //
 // The gradients of gamma and beta are column sums over all rows: every thread
 // keeps the same columns on every row it meets, so it sums them in registers,
-// the warps of a block add up in shared memory one after another, each block
-// writes one partial row, and a second kernel adds the blocks' rows. Every
+// the warps of a block join in shared memory in a fixed order, each block writes
+// one partial row, and a second kernel adds the blocks' rows. Every
 // order is fixed, so the sums do not change from call to call.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "vae_types.cuh"
 
@@ -274,7 +275,8 @@ struct LnRing {
     int m, c, xt, yt, dyt;
     int nq, wide, warps;  // fours per thread, warps per row (a group), warps per block
     int stages;
-    unsigned row_x, row_dy, stage;  // bytes of a row of x and dy, of a stage
+    unsigned row_x, row_dy;         // bytes of a row of x and dy
+    unsigned second, stage;         // offset of dy in a stage, bytes of a stage
     unsigned consts, bars;          // offsets of gamma and beta, and of the barriers
     float eps;
     const void *x, *dy;
@@ -311,34 +313,81 @@ __device__ __forceinline__ void four_out(uint8_t* p, int i, Four v) {
     if constexpr (T == VAE_F32) reinterpret_cast<float4*>(p)[i] = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
     else reinterpret_cast<uint2*>(p)[i] = make_uint2(pack2<T>(v.a.x, v.a.y), pack2<T>(v.b.x, v.b.y));
 }
-// Fours tid, tid + nt, ... of a row; 0 behind its n fours.
-template <int T, int NQ>
+// A thread's four number k of a row of n fours: four tid + k nt, or in rows whose
+// length is no multiple of eight (kOdd, n elements) the single elements
+// tid + (4 k + e) nt; `other` behind the row's end.
+__device__ __forceinline__ int odd_at(int k, int e, int tid, int nt) { return tid + (4 * k + e) * nt; }
+template <int T, bool kOdd>
+__device__ __forceinline__ Four get4(const uint8_t* p, int n, int k, int tid, int nt, float other) {
+    if constexpr (!kOdd) {
+        const int i = tid + k * nt;
+        return i < n ? four_in<T>(p, i) : Four{make_float2(other, other), make_float2(other, other)};
+    } else {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = odd_at(k, e, tid, nt);
+            v[e] = i < n ? to_f32<T>(reinterpret_cast<const typename Elem<T>::type*>(p)[i]) : other;
+        }
+        return {make_float2(v[0], v[1]), make_float2(v[2], v[3])};
+    }
+}
+template <int T, bool kOdd>
+__device__ __forceinline__ void put4(uint8_t* p, int n, int k, int tid, int nt, Four v) {
+    if constexpr (!kOdd) {
+        const int i = tid + k * nt;
+        if (i < n) four_out<T>(p, i, v);
+    } else {
+        const float f[4] = {v.a.x, v.a.y, v.b.x, v.b.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = odd_at(k, e, tid, nt);
+            if (i < n) reinterpret_cast<typename Elem<T>::type*>(p)[i] = from_f32<T>(f[e]);
+        }
+    }
+}
+template <int T, int NQ, bool kOdd>
 __device__ __forceinline__ void row_in_t(const uint8_t* p, int n, int tid, int nt, Four (&v)[NQ]) {
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-        const int i = tid + k * nt;
-        v[k] = i < n ? four_in<T>(p, i) : Four{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    }
+    for (int k = 0; k < NQ; ++k) v[k] = get4<T, kOdd>(p, n, k, tid, nt, 0.f);
 }
-template <int NQ>
+template <int NQ, bool kOdd>
 __device__ __forceinline__ void row_in(const uint8_t* p, int type, int n, int tid, int nt, Four (&v)[NQ]) {
-    if (type == VAE_F32) row_in_t<VAE_F32, NQ>(p, n, tid, nt, v);
-    else if (type == VAE_F16) row_in_t<VAE_F16, NQ>(p, n, tid, nt, v);
-    else row_in_t<VAE_BF16, NQ>(p, n, tid, nt, v);
+    if (type == VAE_F32) row_in_t<VAE_F32, NQ, kOdd>(p, n, tid, nt, v);
+    else if (type == VAE_F16) row_in_t<VAE_F16, NQ, kOdd>(p, n, tid, nt, v);
+    else row_in_t<VAE_BF16, NQ, kOdd>(p, n, tid, nt, v);
 }
-template <int T, int NQ>
+template <int T, int NQ, bool kOdd>
 __device__ __forceinline__ void row_out_t(uint8_t* p, int n, int tid, int nt, const Four (&v)[NQ]) {
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-        const int i = tid + k * nt;
-        if (i < n) four_out<T>(p, i, v[k]);
-    }
+    for (int k = 0; k < NQ; ++k) put4<T, kOdd>(p, n, k, tid, nt, v[k]);
 }
-template <int NQ>
+template <int NQ, bool kOdd>
 __device__ __forceinline__ void row_out(uint8_t* p, int type, int n, int tid, int nt, const Four (&v)[NQ]) {
-    if (type == VAE_F32) row_out_t<VAE_F32, NQ>(p, n, tid, nt, v);
-    else if (type == VAE_F16) row_out_t<VAE_F16, NQ>(p, n, tid, nt, v);
-    else row_out_t<VAE_BF16, NQ>(p, n, tid, nt, v);
+    if (type == VAE_F32) row_out_t<VAE_F32, NQ, kOdd>(p, n, tid, nt, v);
+    else if (type == VAE_F16) row_out_t<VAE_F16, NQ, kOdd>(p, n, tid, nt, v);
+    else row_out_t<VAE_BF16, NQ, kOdd>(p, n, tid, nt, v);
+}
+
+// A run of `bytes` at base + at into dst by a bulk copy, which takes whole
+// 16-byte units: from the unit that it starts in to the one that it ends in,
+// but not past `end`, the tensor's; what a last, partial unit holds comes by
+// hand (before the arrival on the barrier, which the readers acquire). The run
+// starts at dst + at % 16. Returns the bytes that the copy brings.
+template <bool kOdd>
+__device__ __forceinline__ uint32_t run_bytes(size_t at, size_t bytes, size_t end) {
+    if constexpr (!kOdd) return static_cast<uint32_t>(bytes);
+    const size_t from = at & ~size_t(15), to = (at + bytes + 15) & ~size_t(15);
+    return static_cast<uint32_t>((to <= end ? to : end & ~size_t(15)) - from);
+}
+template <bool kOdd>
+__device__ __forceinline__ void run_tail(uint8_t* dst, const void* base, size_t at, size_t bytes, size_t end) {
+    if constexpr (kOdd) {
+        const size_t from = at & ~size_t(15), to = (at + bytes + 15) & ~size_t(15);
+        if (to <= end) return;
+        for (size_t b = end & ~size_t(15); b < end; b += 2)
+            *reinterpret_cast<uint16_t*>(dst + (b - from)) = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(base) + b);
+    }
 }
 
 // The warps of a group meet (a barrier of the group's own).
@@ -367,7 +416,7 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int group,
 }
 
 // Chunks g, g + G, ... of all groups g < G of the grid. kBwd: the gradient.
-template <int NQ, bool kBwd>
+template <int NQ, bool kBwd, bool kOdd>
 __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(const LnRing p) {
     constexpr int R = ring_rows(NQ);
     constexpr int kMaxWarps = ring_warps(NQ, kBwd);
@@ -376,7 +425,8 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wide = p.wide, group = warp / wide, part = warp % wide, groups = p.warps / wide;
-    const int nt = wide * 32, tid = part * 32 + lane, c = p.c, n4 = c / 4;
+    const int nt = wide * 32, tid = part * 32 + lane, c = p.c;
+    const int nr = kOdd ? c : c / 4;  // of a row: elements, or fours
     uint8_t* ring = smem + static_cast<size_t>(group) * p.stages * p.stage;
     const uint8_t* gam = smem + p.consts;
     const uint8_t* bet = gam + static_cast<size_t>(c) * 4;
@@ -387,10 +437,16 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
     auto fetch = [&](int k, int st) {  // one lane of the group: the group's chunk k into stage st = k % stages
         const size_t row = (static_cast<size_t>(first) + static_cast<size_t>(k) * all) * R;
         const unsigned rows = p.m - row < static_cast<size_t>(R) ? static_cast<unsigned>(p.m - row) : R;
-        const uint32_t bar = smem_u32(&full[st]), dst = smem_u32(ring + static_cast<size_t>(st) * p.stage);
-        mbar_arrive_expect_tx(bar, rows * (p.row_x + p.row_dy));
-        ln_bulk(dst, static_cast<const uint8_t*>(p.x) + row * p.row_x, rows * p.row_x, bar);
-        if (kBwd) ln_bulk(dst + R * p.row_x, static_cast<const uint8_t*>(p.dy) + row * p.row_dy, rows * p.row_dy, bar);
+        const uint32_t bar = smem_u32(&full[st]);
+        uint8_t* dst = ring + static_cast<size_t>(st) * p.stage;
+        const size_t ax = row * p.row_x, nx = static_cast<size_t>(rows) * p.row_x, ex = static_cast<size_t>(p.m) * p.row_x;
+        const size_t ay = row * p.row_dy, ny = static_cast<size_t>(rows) * p.row_dy, ey = static_cast<size_t>(p.m) * p.row_dy;
+        const uint32_t bx = run_bytes<kOdd>(ax, nx, ex), by = kBwd ? run_bytes<kOdd>(ay, ny, ey) : 0u;
+        run_tail<kOdd>(dst, p.x, ax, nx, ex);
+        if (kBwd) run_tail<kOdd>(dst + p.second, p.dy, ay, ny, ey);
+        mbar_arrive_expect_tx(bar, bx + by);
+        if (bx > 0) ln_bulk(smem_u32(dst), static_cast<const uint8_t*>(p.x) + (kOdd ? ax & ~size_t(15) : ax), bx, bar);
+        if (by > 0) ln_bulk(smem_u32(dst + p.second), static_cast<const uint8_t*>(p.dy) + (kOdd ? ay & ~size_t(15) : ay), by, bar);
     };
     if (threadIdx.x == 0) abort_flag = 0;
     if (tid == 0) {
@@ -401,10 +457,11 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
     if (tid == 0)
         for (int k = 0; k < n && k < p.stages; ++k) fetch(k, k);
     const bool has_g = p.gamma != nullptr, has_b = !kBwd && p.beta != nullptr;
+    using Const = std::conditional_t<kOdd, float, float4>;
     if (has_g || has_b)
-        for (int i = threadIdx.x; i < n4; i += blockDim.x) {
-            if (has_g) reinterpret_cast<float4*>(smem + p.consts)[i] = reinterpret_cast<const float4*>(p.gamma)[i];
-            if (has_b) reinterpret_cast<float4*>(smem + p.consts + c * 4)[i] = reinterpret_cast<const float4*>(p.beta)[i];
+        for (int i = threadIdx.x; i < nr; i += blockDim.x) {
+            if (has_g) reinterpret_cast<Const*>(smem + p.consts)[i] = reinterpret_cast<const Const*>(p.gamma)[i];
+            if (has_b) reinterpret_cast<Const*>(smem + p.consts)[nr + i] = reinterpret_cast<const Const*>(p.beta)[i];
         }
     __syncthreads();
     const Four zero{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -430,8 +487,10 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
         float s[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            row_in<NQ>(src + r * p.row_x, p.xt, r < rows ? n4 : 0, tid, nt, v[r]);
-            if constexpr (kBwd) row_in<NQ>(src + R * p.row_x + r * p.row_dy, p.dyt, r < rows ? n4 : 0, tid, nt, g[r]);
+            row_in<NQ, kOdd>(src + (kOdd ? row0 * p.row_x & 15 : 0) + r * p.row_x, p.xt, r < rows ? nr : 0, tid, nt, v[r]);
+            if constexpr (kBwd)
+                row_in<NQ, kOdd>(src + p.second + (kOdd ? row0 * p.row_dy & 15 : 0) + r * p.row_dy, p.dyt, r < rows ? nr : 0, tid,
+                                 nt, g[r]);
             float2 t = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NQ; ++i) t = add2(t, add2(v[r][i].a, v[r][i].b));
@@ -451,8 +510,15 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
             float2 t = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                const bool in = tid + i * nt < n4;
-                v[r][i] = in ? Four{add2(v[r][i].a, mm), add2(v[r][i].b, mm)} : zero;
+                if constexpr (!kOdd) {
+                    v[r][i] = tid + i * nt < nr ? Four{add2(v[r][i].a, mm), add2(v[r][i].b, mm)} : zero;
+                } else {
+                    v[r][i] = {add2(v[r][i].a, mm), add2(v[r][i].b, mm)};
+                    if (odd_at(i, 0, tid, nt) >= nr) v[r][i].a.x = 0.f;
+                    if (odd_at(i, 1, tid, nt) >= nr) v[r][i].a.y = 0.f;
+                    if (odd_at(i, 2, tid, nt) >= nr) v[r][i].b.x = 0.f;
+                    if (odd_at(i, 3, tid, nt) >= nr) v[r][i].b.y = 0.f;
+                }
                 t = fma2(v[r][i].a, v[r][i].a, fma2(v[r][i].b, v[r][i].b, t));
             }
             s[r] = t.x + t.y;
@@ -465,9 +531,8 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
         if constexpr (!kBwd) {
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                const int at = tid + i * nt;
-                const Four w = has_g && at < n4 ? four_in<VAE_F32>(gam, at) : Four{make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
-                const Four b = has_b && at < n4 ? four_in<VAE_F32>(bet, at) : zero;
+                const Four w = get4<VAE_F32, kOdd>(gam, has_g ? nr : 0, i, tid, nt, 1.f);
+                const Four b = get4<VAE_F32, kOdd>(bet, has_b ? nr : 0, i, tid, nt, 0.f);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float2 q = make_float2(s[r], s[r]);
@@ -476,15 +541,14 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
             }
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (ok && r < rows) row_out<NQ>(out + r * out_row, p.yt, n4, tid, nt, v[r]);
+                if (ok && r < rows) row_out<NQ, kOdd>(out + r * out_row, p.yt, nr, tid, nt, v[r]);
         } else {
             float2 s1[R], s2[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) s1[r] = s2[r] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                const int at = tid + i * nt;
-                const Four w = has_g && at < n4 ? four_in<VAE_F32>(gam, at) : Four{make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+                const Four w = get4<VAE_F32, kOdd>(gam, has_g ? nr : 0, i, tid, nt, 1.f);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float2 q = make_float2(s[r], s[r]);
@@ -512,7 +576,7 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
 #pragma unroll
                 for (int i = 0; i < NQ; ++i)
                     v[r][i] = {fma2(g[r][i].a, q, fma2(v[r][i].a, q2, q1)), fma2(g[r][i].b, q, fma2(v[r][i].b, q2, q1))};
-                if (ok && r < rows) row_out<NQ>(out + r * out_row, p.xt, n4, tid, nt, v[r]);
+                if (ok && r < rows) row_out<NQ, kOdd>(out + r * out_row, p.xt, nr, tid, nt, v[r]);
             }
         }
     }
@@ -530,12 +594,9 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            const int at = tid + i * nt;
-            if (at < n4) {
-                uint8_t* w = reinterpret_cast<uint8_t*>(cols + static_cast<size_t>(group) * 2 * c);
-                four_out<VAE_F32>(w, at, dg[i]);
-                four_out<VAE_F32>(w + static_cast<size_t>(c) * 4, at, db[i]);
-            }
+            uint8_t* w = reinterpret_cast<uint8_t*>(cols + static_cast<size_t>(group) * 2 * c);
+            put4<VAE_F32, kOdd>(w, nr, i, tid, nt, dg[i]);
+            put4<VAE_F32, kOdd>(w + static_cast<size_t>(c) * 4, nr, i, tid, nt, db[i]);
         }
         __syncthreads();
         float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * c;
@@ -599,19 +660,25 @@ LnPlan ln_plan(int c, bool backward) {
     return p;
 }
 // The ring form's plan for rows of x (and dy: backward); false where the plain
-// form is used: lengths that are no multiple of eight or over 5120, or so few
-// rows that a group would not have two chunks.
-bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, LnRing* r) {
-    if (c % 8 != 0 || c > 5120) return false;
+// form is used: rows over 5120 channels, so few of them that a group would not
+// have two chunks, tensors off the 16-byte boundaries that the copies need, and
+// forward rows of a length that is no multiple of eight (16384x1155: 39 us in
+// the ring against 27 in the plain form; their gradient 66 against 107).
+bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, bool aligned, LnRing* r) {
+    const bool odd = c % 8 != 0;
+    if (c > 5120 || c < 8 || !aligned || (odd && !backward)) return false;
     const int most = backward ? 640 : 1280;  // channels of one warp's share of a row
     r->wide = c <= most ? 1 : (c <= 2 * most ? 2 : (c <= 4 * most ? 4 : 8));
-    r->nq = (c / 4 + r->wide * 32 - 1) / (r->wide * 32);
+    r->nq = ((c + 3) / 4 + r->wide * 32 - 1) / (r->wide * 32);
     const int rows = ring_rows(r->nq);
     r->row_x = static_cast<unsigned>(c * type_size(xt));
     r->row_dy = backward ? static_cast<unsigned>(c * type_size(dyt)) : 0u;
-    r->stage = rows * (r->row_x + r->row_dy);  // (multiples of 16 bytes)
+    // (odd lengths: up to two partial units more)
+    r->second = odd ? (rows * r->row_x + 32 + 15) / 16 * 16 : rows * r->row_x;
+    r->stage = r->second + (backward ? (odd ? (rows * r->row_dy + 32 + 15) / 16 * 16 : rows * r->row_dy) : 0);
     const int max_warps = ring_warps(r->nq, backward);
-    const size_t consts = static_cast<size_t>(c) * (backward ? 4 : 8), bars = static_cast<size_t>(max_warps) * kRingStages * 8;
+    const size_t consts = (static_cast<size_t>(c) * (backward ? 4 : 8) + 15) / 16 * 16;
+    const size_t bars = static_cast<size_t>(max_warps) * kRingStages * 8;
     const size_t left = kRingSmem - consts - bars;
     // As many groups as fit with two stages each (the gradient: three, where that leaves one; 65536x1152 in f32 and f16
     // 125 us against 136), then as many stages as fit.
@@ -631,8 +698,8 @@ bool ln_ring_plan(int m, int c, int xt, int dyt, bool backward, LnRing* r) {
 }
 size_t ln_ring_smem(const LnRing& r) { return r.bars + static_cast<size_t>(r.warps) * kRingStages * 8; }
 
-template <int NQ, bool kBwd>
-int ln_ring_launch(const LnRing& r, cudaStream_t st) {
+template <int NQ, bool kBwd, bool kOdd>
+int ln_ring_launch_as(const LnRing& r, cudaStream_t st) {
     static CtxOnce once;
     static std::mutex mu;
     {
@@ -640,13 +707,19 @@ int ln_ring_launch(const LnRing& r, cudaStream_t st) {
         VAE_CUDA_CHECK(cudaGetDevice(&dev));
         std::lock_guard<std::mutex> lk(mu);
         if (!once.done(dev)) {
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(ln_ring_kernel<NQ, kBwd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(ln_ring_kernel<NQ, kBwd, kOdd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                 static_cast<int>(kRingSmem)));
             once.mark(dev);
         }
     }
-    VAE_CUDA_CHECK(launch_kernel(ln_ring_kernel<NQ, kBwd>, dim3(kRingBlocks), dim3(r.warps * 32), ln_ring_smem(r), st, r));
+    VAE_CUDA_CHECK(launch_kernel(ln_ring_kernel<NQ, kBwd, kOdd>, dim3(kRingBlocks), dim3(r.warps * 32), ln_ring_smem(r), st, r));
     return VAE_OK;
+}
+template <int NQ, bool kBwd>
+int ln_ring_launch(const LnRing& r, cudaStream_t st) {
+    if constexpr (kBwd)
+        if (r.c % 8 != 0) return ln_ring_launch_as<NQ, kBwd, true>(r, st);
+    return ln_ring_launch_as<NQ, kBwd, false>(r, st);
 }
 template <bool kBwd>
 int ln_ring_run(LnRing& r, cudaStream_t st) {
@@ -695,6 +768,11 @@ cudaError_t ln_dispatch(const LnPlan& p, F&& f) {
     return cudaErrorInvalidValue;
 }
 
+// Rows of a multiple of eight channels move in 16-byte vectors; others by the element.
+bool ln_aligned(const void* p, size_t element, int c) {
+    return reinterpret_cast<uintptr_t>(p) % (c % 8 == 0 ? 16 : element) == 0;
+}
+
 int ln_check(const void* x, int xt, int m, int c, float eps, const void* y, int yt) {
     if (x == nullptr || y == nullptr) return set_error(VAE_ERR_ARG, "layer norm: NULL tensor");
     if (!type_ok(xt) || !type_ok(yt)) return set_error(VAE_ERR_ARG, "layer norm: unknown element type");
@@ -718,11 +796,12 @@ int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamm
     if (rc != VAE_OK) return rc;
     if (x_dev == y_dev && x_type != y_type)
         return set_error(VAE_ERR_ARG, "layer norm: in place needs x and y of one type");
-    if (!aligned16(x_dev) || !aligned16(y_dev) || !aligned16(gamma_dev) || !aligned16(beta_dev))
-        return set_error(VAE_ERR_ALIGN, "layer norm: pointers must be 16-byte aligned");
+    if (!ln_aligned(x_dev, type_size(x_type), c) || !ln_aligned(y_dev, type_size(y_type), c) ||
+        !ln_aligned(gamma_dev, 4, c) || !ln_aligned(beta_dev, 4, c))
+        return set_error(VAE_ERR_ALIGN, "layer norm: pointers must be 16-byte aligned (to their elements where c %% 8 != 0)");
     if ((rc = check_device()) != VAE_OK) return rc;
     LnRing r{};
-    if (ln_ring_plan(m, c, x_type, x_type, false, &r)) {
+    if (ln_ring_plan(m, c, x_type, x_type, false, aligned16(x_dev), &r)) {
         r.x = x_dev;
         r.gamma = gamma_dev;
         r.beta = beta_dev;
@@ -760,9 +839,10 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
         return set_error(VAE_ERR_ARG, "layer norm: dx over dy needs one type");
     const bool sums = dgamma_dev != nullptr;
     if (sums && workspace_dev == nullptr) return set_error(VAE_ERR_ARG, "layer norm: NULL workspace");
-    if (!aligned16(x_dev) || !aligned16(dy_dev) || !aligned16(dx_dev) || !aligned16(gamma_dev) ||
-        !aligned16(dgamma_dev) || !aligned16(dbeta_dev) || !aligned16(workspace_dev))
-        return set_error(VAE_ERR_ALIGN, "layer norm: pointers must be 16-byte aligned");
+    if (!ln_aligned(x_dev, type_size(x_type), c) || !ln_aligned(dy_dev, type_size(dy_type), c) ||
+        !ln_aligned(dx_dev, type_size(x_type), c) || !ln_aligned(gamma_dev, 4, c) || !ln_aligned(dgamma_dev, 4, c) ||
+        !ln_aligned(dbeta_dev, 4, c) || !aligned16(workspace_dev))
+        return set_error(VAE_ERR_ALIGN, "layer norm: pointers must be 16-byte aligned (to their elements where c %% 8 != 0)");
     if (sums && workspace_bytes < vae_layernorm_backward_workspace_bytes(m, c))
         return set_error(VAE_ERR_NOMEM, "layer norm: workspace of %zu bytes, %zu needed", workspace_bytes,
                          vae_layernorm_backward_workspace_bytes(m, c));
@@ -772,7 +852,7 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
     float* part = sums ? static_cast<float*>(workspace_dev) : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     LnRing r{};
-    if (ln_ring_plan(m, c, x_type, dy_type, true, &r)) {
+    if (ln_ring_plan(m, c, x_type, dy_type, true, aligned16(x_dev) && aligned16(dy_dev), &r)) {
         r.x = x_dev;
         r.dy = dy_dev;
         r.gamma = gamma_dev;

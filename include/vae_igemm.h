@@ -357,7 +357,8 @@ enum { VAE_F32 = 0, VAE_F16 = 1, VAE_BF16 = 2 };
  *   types are the same); gamma_dev, beta_dev f32 [c], each or both NULL
  *   (1 and 0).
  * Requirements: m >= 1, 1 <= c <= 16384, eps >= 0 and finite; pointers
- * 16-byte aligned. Rows of c % 8 == 0 take 16-byte loads, others scalar ones.
+ * 16-byte aligned, or where c % 8 != 0 aligned to their elements (those rows
+ * move element by element).
  */
 int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamma_dev, const float* beta_dev,
                   float eps, void* y_dev, int y_type, vae_stream_t stream);

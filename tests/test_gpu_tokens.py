@@ -54,7 +54,8 @@ def _within(got, ref, tol):
 LN_SHAPES = [(1, 1), (1, 8), (3, 7), (5, 33), (129, 144), (64, 256), (77, 257), (33, 576), (19, 1152), (18, 1280),
              (9, 1281), (7, 1288), (10, 2304), (6, 4096), (5, 5001), (4, 8192), (3, 16383), (3, 16384), (2500, 64),
              (5001, 144), (4900, 1152), (5000, 1280), (2600, 1288), (2500, 2560), (1300, 2568), (1400, 5120), (1300, 5128),
-             (20003, 40), (20001, 200), (7300, 640), (4000, 648)]
+             (20003, 40), (20001, 200), (7300, 640), (4000, 648),
+             (20011, 9), (20003, 35), (10001, 214), (5003, 1155), (3001, 2301), (1301, 5119)]
 
 
 def _ln_terms(x, eps):
@@ -93,6 +94,21 @@ def test_layernorm_in_place_constant_rows_and_one_operand():
     assert torch.equal(z, torch.arange(40.0, device="cuda").expand(3, 40))
     g = torch.full((72,), 2.0, device="cuda")
     assert torch.equal(vg.layernorm(x, gamma=g, out_dtype=torch.float32), 2.0 * vg.layernorm(x, out_dtype=torch.float32))
+
+
+def test_layernorm_odd_rows_off_the_boundaries():
+    """Rows of an odd length from the second row of a tensor on: element by element, both directions."""
+    torch = torch_mod()
+    for m in (7, 20000):
+        x, _ = _draw(2, f"ln.off.{m}", (m + 1, 33), "f16")
+        dy, _ = _draw(2, f"ln.off.dy.{m}", (m + 1, 33), "f16")
+        # (aligned and unaligned rows may take different forms: sums in another order, one more step of f16 at most)
+        near = lambda a, b: (a.float() - b.float()).abs().max() <= 2.0 ** -9 * b.float().abs().max()  # noqa: E731
+        assert near(vg.layernorm(x[1:]), vg.layernorm(x[1:].clone()))
+        got, ref = vg.layernorm_backward(dy[1:], x[1:]), vg.layernorm_backward(dy[1:].clone(), x[1:].clone())
+        assert near(got[0], ref[0])
+        for a, b in zip(got[1:], ref[1:]):
+            assert (a - b).abs().max() <= SUM * dy.float().abs().sum(0).max() * x.float().abs().max()
 
 
 def test_layernorm_spikes_and_offsets():

@@ -32,6 +32,7 @@ def test_layernorm_refusals(L):
     assert rc(eps=-1.0) == -1 and rc(eps=NAN) == -1 and rc(eps=INF) == -1
     assert rc(y=FAKE) == -1 and "in place" in vg.last_error()
     assert rc(x=FAKE + 4) == -3 and rc(y=FAKE + 2) == -3 and rc(g=FAKE + 4) == -3
+    assert rc(c=63, x=FAKE + 2) == -3 and rc(c=63, y=FAKE + 65537) == -3 and rc(c=63, b=FAKE + 2) == -3
 
 
 def test_layernorm_backward_refusals(L):
