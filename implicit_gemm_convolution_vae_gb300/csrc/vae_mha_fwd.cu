@@ -538,12 +538,7 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
     constexpr float kBias = T == VAE_F16 ? 6.f : 0.f;
     const int t = warp >> 2, quad = warp & 3;
     const int gp = 1 << p.s.gp_log2;
-    const auto row_of = [&](int r, int* i, int* h) {
-        *i = r >> p.s.gp_log2;
-        *h = w.hk * p.s.g + w.sub * gp + (r & (gp - 1));
-    };
-    int i, h;
-    row_of(lane, &i, &h);
+    const int i = lane >> p.s.gp_log2, h = w.hk * p.s.g + w.sub * gp + (lane & (gp - 1));
     const bool live = i < w.ql;
     const int lim = live ? mha_key_limit(i, w.ql, w.kl, p.s.block) : 0;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
