@@ -35,7 +35,9 @@
 // 717). Bound by the MMAs: S reads both operands from shared memory, 8 KB in 64
 // cycles, which is all that it gives, and a step of both streams takes 2970
 // cycles of which the products alone take 2400. Eight softmax warps and not
-// sixteen (half a row each, maxima traded: 1282 us). One token over four caches
+// sixteen (half a row each, maxima traded: 1282 us); a tile's PV whole and not
+// from its first half of P on (918 against 876 us), a tile whole and not S and
+// P in halves of 64 keys (1193 against 882 us). One token over four caches
 // of up to 32760 keys (201 MB): 45 us a call in a graph, 6.3 TB/s while it
 // streams.
 #include <cmath>
@@ -47,8 +49,14 @@ namespace vae {
 namespace {
 
 constexpr int kSoftWarps = 8;
-constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kThreads = (kSoftWarps + 4) * 32;  // whole warpgroups; the last two warps wait at the end
 constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+// A softmax thread holds a row's 128 scores, which 168 registers (65536 over
+// three warpgroups) do not fit without spilling: the other warpgroup gives some
+// of its own up (16384 tokens, 9 heads of 128: 876 to 846 us; of 64: 738 to
+// 700). 224 + 56 make the MMA warp's group spill: 900 us.
+constexpr int kLaunchRegs = 168, kSoftRegs = 216, kOtherRegs = 72;
+static_assert(kSoftWarps * kSoftRegs + 4 * kOtherRegs <= (kSoftWarps + 4) * kLaunchRegs, "more registers than the launch has");
 constexpr uint32_t kTmemCols = 512;  // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kTargetCtas = 152;     // one CTA per SM
 
@@ -669,6 +677,43 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
     }
 }
 
+// The third warpgroup: it sets up the barriers and TMEM, loads and issues the products.
+template <int T, int kSteps>
+__device__ __forceinline__ void fwd_feed(const FwdParams& p, const FwdSmem& s, const FwdWork& w, const CUtensorMap& mq,
+                                         const CUtensorMap& mk, const CUtensorMap& mv, int warp, int lane) {
+    using C = FwdCfg<kSteps>;
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            *s.abort_flag = 0;
+            for (int i = 0; i < C::kStages; ++i) {
+                mbar_init(smem_u32(&s.full[i]), 1u);
+                mbar_init(smem_u32(&s.empty[i]), 1u);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&s.s_full[i]), 1u);
+                mbar_init(smem_u32(&s.p_full[i]), 4u);
+                mbar_init(smem_u32(&s.o_full[i]), 1u);
+            }
+            mbar_init(smem_u32(s.q_full), 1u);
+            mbar_init(smem_u32(s.fix), 1u);
+            mbar_init(smem_u32(s.drain), 1u);
+            fence_mbar_init();
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        fwd_producer<kSteps>(p, s, w, &mq, &mk, &mv, lane);  // (meets the others' __syncthreads)
+    } else {
+        if (warp == kMmaWarp) {
+            tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == kMmaWarp) fwd_mma<T, kSteps>(p, s, w);
+    }
+}
+
 template <int T, int kSteps>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -707,37 +752,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     constexpr uint32_t tmem = 0u;  // all 512 columns are this CTA's: they start at 0
-    if (warp == kTmaWarp) {
-        if (lane == 0) {
-            *s.abort_flag = 0;
-            for (int i = 0; i < C::kStages; ++i) {
-                mbar_init(smem_u32(&s.full[i]), 1u);
-                mbar_init(smem_u32(&s.empty[i]), 1u);
-            }
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_u32(&s.s_full[i]), 1u);
-                mbar_init(smem_u32(&s.p_full[i]), 4u);
-                mbar_init(smem_u32(&s.o_full[i]), 1u);
-            }
-            mbar_init(smem_u32(s.q_full), 1u);
-            mbar_init(smem_u32(s.fix), 1u);
-            mbar_init(smem_u32(s.drain), 1u);
-            fence_mbar_init();
-            fence_proxy_async_smem();
-        }
-        __syncwarp();
-        fwd_producer<kSteps>(p, s, w, &mq, &mk, &mv, lane);  // (meets the others' __syncthreads)
-    } else {
-        if (warp == kMmaWarp) {
-            tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
-            tmem_relinquish();
-        }
+    if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (warp == kMmaWarp) fwd_mma<T, kSteps>(p, s, w);
-        else if (p.narrow) fwd_softmax_narrow<T, kSteps>(p, s, w, warp, lane);
+        if (p.narrow) fwd_softmax_narrow<T, kSteps>(p, s, w, warp, lane);
         else fwd_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        fwd_feed<T, kSteps>(p, s, w, mq, mk, mv, warp, lane);
     }
     pdl_launch_dependents();
     __syncwarp();
@@ -848,6 +872,11 @@ int fwd_launch(const vae_attention_desc* a, const FwdPlan& f, const CUtensorMap 
         if (!once.done(dev)) {
             VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_fwd_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                 C::kSmem));
+            cudaFuncAttributes at;
+            VAE_CUDA_CHECK(cudaFuncGetAttributes(&at, mha_fwd_kernel<T, kSteps>));
+            if (at.numRegs < kLaunchRegs)  // the softmax warps would wait for registers that the block does not have
+                return set_error(VAE_ERR_CUDA, "attention: compiled to %d registers a thread, its split needs %d",
+                                 at.numRegs, kLaunchRegs);
             once.mark(dev);
         }
     }
