@@ -152,6 +152,17 @@ __device__ __forceinline__ void tma_load_4d_to(uint32_t dst, const CUtensorMap* 
         : "memory");
 }
 
+// What packing a and b to 16 bits leaves of them, packed. Where a tile has room
+// for its rows twice, the second copies take this part of P and dS: the products
+// with the two are added. One rounding of P or dS is as large as the result's
+// own. Over many rows and keys both add up to 1.4 times the latter's error, but
+// over few they may fall together (2.2 times in bf16 for one row over 16 keys).
+template <int T>
+__device__ __forceinline__ uint32_t pack2_rest(float a, float b) {
+    const float2 h = unpack2<T>(pack2<T>(a, b));
+    return pack2<T>(a - h.x, b - h.y);
+}
+
 // 2^x, approximate (relative error near 2^-22); under 2^-126 it is 0.
 __device__ __forceinline__ float mha_ex2(float x) {
     float y;
@@ -193,9 +204,9 @@ __device__ __forceinline__ void mha_fill_keys(const MhaShape& s, int e, int hk, 
 
 // Zeroes rows [from, 128) of a tile of `chunks` chunks in shared memory; the
 // whole warp. The caller fences towards the async proxy.
-__device__ __forceinline__ void mha_zero_rows(uint8_t* tile, int from, int chunks, int lane) {
+__device__ __forceinline__ void mha_zero_rows(uint8_t* tile, int from, int to, int chunks, int lane) {
     for (int c = 0; c < chunks; ++c)
-        for (int i = from * 8 + lane; i < kMhaTile * 8; i += 32)
+        for (int i = from * 8 + lane; i < to * 8; i += 32)
             *reinterpret_cast<uint4*>(tile + c * kMhaChunkBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 

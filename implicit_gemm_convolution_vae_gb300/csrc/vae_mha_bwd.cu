@@ -43,7 +43,9 @@
 // P ~ 1/n below 2^-14, so it holds P 2^14 and dS c, with c the power of two
 // that brings 2 max|dO| max|V| (a bound on |dP - D| by Cauchy-Schwarz, from a
 // first kernel) to 2^14 .. 2^15; both factors leave in the epilogue. The
-// maximum is taken by an atomic maximum, which has no order.
+// maximum is taken by an atomic maximum, which has no order. Up to 64 rows of a
+// head lie twice in their tile: the second copies' P and dS are what the first's
+// rounding left of them.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -88,6 +90,7 @@ struct BwdParams {
     float scale, scale_log2;
     int nsplit_q, nsplit_k;
     int csize_q, csize_k;       // CTAs per cluster
+    int twice;                  // at most 64 rows to a head: each lies twice in its tile, P and dS in two parts
     float* side;                // [b][hkv][nsub][ntile][256]
     const unsigned* maxima;     // f16: bits of max |dO|^2, max |V|^2
     const void *q, *dout;
@@ -331,9 +334,10 @@ struct BwdRing {
             phase ^= 1u;
         }
     }
-    // Waits for the stage's copies (the whole warp), zeroes rows [from, 128) of both tiles and hands it over.
+    // Waits for the stage's copies (the whole warp), zeroes the rows behind the first `from` of both tiles (of each
+    // half: twice) and hands it over.
     template <typename C>
-    __device__ __forceinline__ bool fix(const BwdSmem& s, const BwdParams& p, int from, int lane) {
+    __device__ __forceinline__ bool fix(const BwdSmem& s, const BwdParams& p, int from, bool twice, int lane) {
         armed &= ~(1u << stage);
         fixing = 1u << stage;
         const uint32_t par = (fix_par >> stage) & 1u;
@@ -342,8 +346,10 @@ struct BwdRing {
         fixing = 0u;
         fix_par ^= 1u << stage;
         uint8_t* dst = s.ring + stage * 2 * C::kTileBytes;
-        mha_zero_rows(dst, from, C::kCh, lane);
-        mha_zero_rows(dst + C::kTileBytes, from, C::kCh, lane);
+        for (int k = 0; k < 2; ++k, dst += C::kTileBytes) {
+            mha_zero_rows(dst, from, twice ? kMhaTile / 2 : kMhaTile, C::kCh, lane);
+            if (twice) mha_zero_rows(dst, kMhaTile / 2 + from, kMhaTile, C::kCh, lane);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -388,10 +394,11 @@ __device__ __forceinline__ void load64(uint32_t t, uint32_t (&x)[4][16]) {
     for (int c = 0; c < 4; ++c) tmem_ld_wait_regs(x[c]);
 }
 
-// A row of an accumulator, times `f`, to the 16-bit tensor or an f32 partial.
+// A row of an accumulator (and of its second part, in shared memory), times `f`,
+// to the 16-bit tensor or an f32 partial.
 template <int T>
 __device__ __forceinline__ void store_acc(uint32_t t, int d, bool live, bool any, float f, void* out, long long off, float* part,
-                                          long long poff) {
+                                          long long poff, const float* more = nullptr) {
     for (int c = 0; c < d; c += 16) {
         uint32_t r[16];
         if (any) {
@@ -408,7 +415,8 @@ __device__ __forceinline__ void store_acc(uint32_t t, int d, bool live, bool any
             if (c + u >= d) continue;
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[u + k]) * f;
+            for (int k = 0; k < 8; ++k)
+                v[k] = (more != nullptr ? __uint_as_float(r[u + k]) + more[(c + u + k) * 64] : __uint_as_float(r[u + k])) * f;
             if (part != nullptr) store8<VAE_F32>(part + poff + c + u, v);
             else store8<T>(static_cast<typename Elem<T>::type*>(out) + off + c + u, v);
         }
@@ -461,7 +469,7 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
                             const CUtensorMap* mg, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
     const uint64_t pol = policy_evict_normal();
     const MhaShape& sh = p.s;
-    const int gp = 1 << sh.gp_log2, half = 64 >> sh.gp_log2;
+    const int gp = 1 << sh.gp_log2, half = p.twice ? 0 : 64 >> sh.gp_log2;
     if (lane == 0) {
         const uint32_t rb = smem_u32(s.res_full);
         mbar_arrive_expect_tx(rb, 2u * C::kTileBytes);
@@ -493,7 +501,7 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
             load_tile_shared<C::kCh>(dst + C::kTileBytes, mg, bb, head, token, half, w.e, w.rank, p.csize_k, pol);
         }
         if (fix) {
-            if (!r.template fix<C>(s, p, static_cast<int>(valid), lane)) break;
+            if (!r.template fix<C>(s, p, static_cast<int>(valid), p.twice != 0, lane)) break;
         } else {
             r.arm();
         }
@@ -566,7 +574,25 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
     mma_finish(s, p, ok, p.csize_k);
 }
 
-template <int T, int kSteps>
+// 64 values as 16-bit pairs in 32 columns, or what that rounding leaves of them.
+template <int T>
+__device__ __forceinline__ void store64(uint32_t t, const float (&v)[64], bool rest) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t h2[16];
+        if (rest) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u) h2[u] = pack2_rest<T>(v[k * 32 + 2 * u], v[k * 32 + 2 * u + 1]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 16; ++u) h2[u] = pack2<T>(v[k * 32 + 2 * u], v[k * 32 + 2 * u + 1]);
+        }
+        tmem_st16(t + static_cast<uint32_t>(k * 16), h2);
+    }
+}
+
+template <int T, int kSteps, bool kTwice>
 __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w, int warp, int lane) {
     using C = KvCfg<kSteps>;
     const int quad = warp & 3, half = warp >> 2;
@@ -580,6 +606,8 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
     long long see = 0;
     if (sh.block > 0) see = (static_cast<long long>(j / sh.block * sh.block) - (w.kl - w.ql)) * (1 << sh.gp_log2);
     const int per = w.nt - w.t0;
+    const bool rest = kTwice && half == 1;  // these columns hold the other half's rows again
+    const int col0 = rest ? 0 : half * 64;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
     int st = 0;
@@ -589,7 +617,7 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
         const int tile = w.t0 + (w.first + x) % per;
         ok = warp_all(bwait(&s.a_full[st], ph, s, p));  // the side rows
         if (!ok) break;
-        const float* side = reinterpret_cast<const float*>(s.side + st * kSideBytes) + half * 64;
+        const float* side = reinterpret_cast<const float*>(s.side + st * kSideBytes) + col0;
         ok = warp_all(bwait(s.s_full, par, s, p));
         if (!ok) break;
         tc_fence_after();
@@ -607,21 +635,14 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
             pr[k + 2] = mha_ex2(b.x);
             pr[k + 3] = mha_ex2(b.y);
         }
-        const long long before = see - static_cast<long long>(tile) * kMhaTile - half * 64;
+        const long long before = see - static_cast<long long>(tile) * kMhaTile - col0;
         const int hide = before > 64 ? 64 : (before < 0 ? 0 : static_cast<int>(before));  // columns that do not see the key
         if (__any_sync(0xffffffffu, hide > 0)) {
 #pragma unroll
             for (int k = 0; k < 64; ++k)
                 if (k < hide) pr[k] = 0.f;
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t h2[16];
-#pragma unroll
-            for (int u = 0; u < 16; ++u) h2[u] = pack2<T>(pr[k * 32 + 2 * u], pr[k * 32 + 2 * u + 1]);
-            tmem_st16(tS + static_cast<uint32_t>(k * 16), h2);
-        }
+        store64<T>(tS, pr, rest);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -647,14 +668,7 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
             pr[k + 2] = b.x;
             pr[k + 3] = b.y;
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t h2[16];
-#pragma unroll
-            for (int u = 0; u < 16; ++u) h2[u] = pack2<T>(pr[k * 32 + 2 * u], pr[k * 32 + 2 * u + 1]);
-            tmem_st16(tX + static_cast<uint32_t>(k * 16), h2);
-        }
+        store64<T>(tX, pr, rest);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -672,13 +686,14 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
     const long long row = (static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.sk + j;
     const bool split = p.nsplit_k > 1;
     const MhaStrides os = half == 0 ? p.dvs : p.dks;
-    const float g = half == 0 ? (T == VAE_F16 ? 1.f / (1 << kPLog2) : 1.f) : p.scale / c;
+    // (softmax over a single key is 1 whatever its score: that gradient is 0)
+    const float g = half == 0 ? (T == VAE_F16 ? 1.f / (1 << kPLog2) : 1.f) : w.kl == 1 ? 0.f : p.scale / c;
     store_acc<T>(lane_off + 256u + static_cast<uint32_t>(half * 128), sh.d, j < w.kl, true, g,
                  half == 0 ? p.dv : p.dk, w.e * os.b + j * os.s + w.hk * os.h, split ? p.part_kv : nullptr,
                  ((w.split * 2 + half) * rows + row) * sh.d);
 }
 
-template <int T, int kSteps>
+template <int T, int kSteps, bool kTwice>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
@@ -705,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     bwd_begin<C>(s, warp, p.csize_k, 1u);
-    if (warp < kSoftWarps) kv_softmax<T, kSteps>(p, s, w, warp, lane);
+    if (warp < kSoftWarps) kv_softmax<T, kSteps, kTwice>(p, s, w, warp, lane);
     else if (warp == kTmaWarp) kv_producer<C>(p, s, w, &mq, &mg, &mk, &mv, lane);
     else kv_mma<T, kSteps>(p, s, w);
     bwd_end(warp, p.csize_k);
@@ -771,7 +786,7 @@ __device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w,
             load_tile_shared<C::kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, 64, w.e, w.rank, p.csize_q, pol);
         }
         if (fix) {
-            if (!r.template fix<C>(s, p, w.kl - kb * kMhaTile, lane)) break;
+            if (!r.template fix<C>(s, p, w.kl - kb * kMhaTile, false, lane)) break;
         } else {
             r.arm();
         }
@@ -842,12 +857,13 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
     mma_finish(s, p, ok, p.csize_q);
 }
 
-template <int T, int kSteps>
+template <int T, int kSteps, bool kTwice>
 __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, int warp, int lane) {
     const int quad = warp & 3, half = warp >> 2;
     const MhaShape& sh = p.s;
     const int gp = 1 << sh.gp_log2;
-    const int rr = quad * 32 + lane, r = w.tile * kMhaTile + rr;
+    const int at = quad * 32 + lane, rr = kTwice ? at & 63 : at, r = w.tile * kMhaTile + rr;
+    const bool rest = kTwice && rr != at;  // these lanes hold the other half's rows again
     const int i = r >> sh.gp_log2, h = w.hk * sh.g + w.sub * gp + (r & (gp - 1));
     const bool here = w.tile < sh.ntile;  // (a cluster's last tile may be missing)
     const bool live = here && i < w.ql;
@@ -892,14 +908,14 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
         if (w.exact && x == from) {
             // D = rowsum(P dP): this half's sum and the other's, for the key-tile kernel too
             float* trade = reinterpret_cast<float*>(s.side);
-            trade[half * kMhaTile + rr] = sum.x + sum.y;
+            trade[half * kMhaTile + at] = sum.x + sum.y;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.x_bar[quad]));
             ok = warp_all(bwait(&s.x_bar[quad], 0u, s, p));
             if (!ok) break;
-            const float all = *static_cast<volatile float*>(trade + rr) + *static_cast<volatile float*>(trade + kMhaTile + rr);
+            const float all = *static_cast<volatile float*>(trade + at) + *static_cast<volatile float*>(trade + kMhaTile + at);
             D = T == VAE_F16 ? all * (1.f / (1 << kPLog2)) : all;
-            if (half == 0 && live) side[128 + rr] = D;
+            if (half == 0 && live && !rest) side[128 + rr] = D;
             D2 = make_float2(-D, -D);
         }
         ok = warp_all(bwait(s.s_full, par, s, p));
@@ -941,12 +957,13 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
                 uint32_t h2[16];
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
-                    const int at = k * 32 + 2 * u;
-                    const uint32_t* y = xr[at >> 4] + (at & 15);
+                    const int n = k * 32 + 2 * u;
+                    const uint32_t* y = xr[n >> 4] + (n & 15);
                     float2 a = add2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), D2);
-                    a = mul2(a, make_float2(pr[at], pr[at + 1]));
+                    a = mul2(a, make_float2(pr[n], pr[n + 1]));
                     if constexpr (T == VAE_F16) a = mul2(a, make_float2(f, f));
                     h2[u] = pack2<T>(a.x, a.y);
+                    if (kTwice && rest) h2[u] = pack2_rest<T>(a.x, a.y);
                 }
                 tmem_st16(tX + static_cast<uint32_t>(k * 16), h2);
             }
@@ -957,15 +974,35 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
         if (lane == 0) mbar_arrive(smem_u32(s.ds_full));
     }
     if (ok) ok = warp_all(bwait(s.done, 0u, s, p));
-    if (!ok || half != 0) return;
+    if (half != 0) return;
+    // the second copies' rows pass through the ring, which every MMA has read: [channel][64 rows]
+    float* more = kTwice ? reinterpret_cast<float*>(s.ring) : nullptr;
+    if constexpr (kTwice) {
+        if (ok && quad >= 2) {
+            tc_fence_after();
+            for (int c0 = 0; c0 < sh.d; c0 += 16) {
+                uint32_t v[16];
+                __syncwarp();
+                tmem_ld16(lane_off + 256u + static_cast<uint32_t>(c0), v);
+                tmem_ld_wait_regs(v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) more[(c0 + k) * 64 + rr] = __uint_as_float(v[k]);
+            }
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // (the first four warps all come here, timed out or not)
+        if (quad >= 2) return;
+    }
+    if (!ok) return;
     tc_fence_after();
     const long long rows = static_cast<long long>(sh.b) * sh.hq * sh.sq;
     const long long row = (static_cast<long long>(w.e) * sh.hq + h) * sh.sq + i;
-    store_acc<T>(lane_off + 256u, sh.d, live, true, p.scale / c, p.dq, w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h,
-                 p.nsplit_q > 1 ? p.part_q : nullptr, (w.split * rows + row) * sh.d);
+    // (a row that sees a single key: P is 1 whatever the score, and dq 0)
+    store_acc<T>(lane_off + 256u, sh.d, live, true, lim == 1 ? 0.f : p.scale / c, p.dq,
+                 w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h, p.nsplit_q > 1 ? p.part_q : nullptr,
+                 (w.split * rows + row) * sh.d, kTwice ? more + rr : nullptr);
 }
 
-template <int T, int kSteps>
+template <int T, int kSteps, bool kTwice>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdParams p) {
     using C = QCfg<kSteps>;
@@ -988,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     bwd_begin<C>(s, warp, p.csize_q, kSoftWarps);
-    if (warp < kSoftWarps) q_softmax<T, kSteps>(p, s, w, warp, lane);
+    if (warp < kSoftWarps) q_softmax<T, kSteps, kTwice>(p, s, w, warp, lane);
     else if (warp == kTmaWarp) q_producer<C>(p, s, w, &mk, &mv, lane);
     else q_mma<T, kSteps>(p, s, w);
     bwd_end(warp, p.csize_q);
@@ -1071,7 +1108,7 @@ BwdPlan bwd_plan(const MhaShape& s) {
 }
 constexpr size_t kMaximaFloats = 64;  // two words used; keeps what follows aligned
 
-template <int T, int kSteps>
+template <int T, int kSteps, bool kTwice>
 int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap (&map)[4], const PrepParams& pp,
                const BwdParams& p, cudaStream_t st) {
     static CtxOnce once;
@@ -1082,8 +1119,8 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
         VAE_CUDA_CHECK(cudaGetDevice(&dev));
         std::lock_guard<std::mutex> lk(mu);
         if (!once.done(dev)) {
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dkv_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem));
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dq_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem));
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dkv_kernel<T, kSteps, kTwice>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem));
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_dq_kernel<T, kSteps, kTwice>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem));
             once.mark(dev);
         }
     }
@@ -1092,9 +1129,9 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
     VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
     // (The query-tile kernel first: it may put its D into the side rows. Always launched as clusters, of one CTA at least:
     // a commit or copy with a cluster mask is an illegal instruction in a grid that was launched without.)
-    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_q), mha_dq_kernel<T, kSteps>,
+    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_q), mha_dq_kernel<T, kSteps, kTwice>,
                                     dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), kQSmem, st, map[2], map[3], p));
-    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_k), mha_dkv_kernel<T, kSteps>,
+    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_k), mha_dkv_kernel<T, kSteps, kTwice>,
                                     dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), kKvSmem, st, map[0], map[1], map[2],
                                     map[3], p));
     const MhaShape& s = p.s;
@@ -1113,6 +1150,19 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
                                      rows * s.d, f.nsplit_q, s.b, s.hq, s.sq, s.d, s.q_len, s.fill, p.dq, p.dqs));
     }
     return VAE_OK;
+}
+
+template <bool kTwice>
+int bwd_by_type(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap (&map)[4], const PrepParams& pp,
+                const BwdParams& p, cudaStream_t st) {
+    const int d = p.s.d;
+    if (a->type == VAE_F16)
+        return d <= 64   ? bwd_launch<VAE_F16, 4, kTwice>(a, f, map, pp, p, st)
+               : d <= 96 ? bwd_launch<VAE_F16, 6, kTwice>(a, f, map, pp, p, st)
+                         : bwd_launch<VAE_F16, 8, kTwice>(a, f, map, pp, p, st);
+    return d <= 64   ? bwd_launch<VAE_BF16, 4, kTwice>(a, f, map, pp, p, st)
+           : d <= 96 ? bwd_launch<VAE_BF16, 6, kTwice>(a, f, map, pp, p, st)
+                     : bwd_launch<VAE_BF16, 8, kTwice>(a, f, map, pp, p, st);
 }
 
 }  // namespace
@@ -1156,6 +1206,7 @@ int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout
     p.nsplit_k = f.nsplit_k;
     p.csize_q = f.csize_q;
     p.csize_k = f.csize_k;
+    p.twice = static_cast<long long>(s.sq) * gp <= kMhaTile / 2;
     p.q = q;
     p.dout = dout;
     p.qs = mha_strides(a->q_stride);
@@ -1173,10 +1224,7 @@ int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout
     p.status = device_status_ptr();
     p.timeout_ns = wait_timeout_ns();
     if (p.status == nullptr) return VAE_ERR_CUDA;
-    const bool h = a->type == VAE_F16;
-    if (s.d <= 64) return h ? bwd_launch<VAE_F16, 4>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 4>(a, f, map, pp, p, st);
-    if (s.d <= 96) return h ? bwd_launch<VAE_F16, 6>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 6>(a, f, map, pp, p, st);
-    return h ? bwd_launch<VAE_F16, 8>(a, f, map, pp, p, st) : bwd_launch<VAE_BF16, 8>(a, f, map, pp, p, st);
+    return p.twice ? bwd_by_type<true>(a, f, map, pp, p, st) : bwd_by_type<false>(a, f, map, pp, p, st);
 }
 
 }  // namespace vae

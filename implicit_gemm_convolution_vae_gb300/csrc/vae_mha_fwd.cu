@@ -17,7 +17,8 @@
 //   Few rows (narrow: 32 at most, as for single tokens): one tile holds its rows
 //   four times, once per TMEM lane quadrant, and each quadrant's warp takes a
 //   quarter of the keys, so that the softmax of a few rows is not one warp's
-//   chain of 128 keys; eight partial (m, l, O) join at the end.
+//   chain of 128 keys; eight partial (m, l, O) join at the end. Up to 16 rows lie
+//   twice in each quadrant, for P in two 16-bit parts.
 // In either form the keys may be split over CTAs, whose f32 partial rows a
 // second kernel joins in a fixed order: for single tokens over a long cache, and
 // where a last wave of CTAs would leave most SMs without work.
@@ -53,10 +54,15 @@ constexpr int kThreads = (kSoftWarps + 4) * 32;  // whole warpgroups; the last t
 constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 // A softmax thread holds a row's 128 scores, which 168 registers (65536 over
 // three warpgroups) do not fit without spilling: the other warpgroup gives some
-// of its own up (16384 tokens, 9 heads of 128: 876 to 846 us; of 64: 738 to
-// 700). 224 + 56 make the MMA warp's group spill: 900 us.
-constexpr int kLaunchRegs = 168, kSoftRegs = 216, kOtherRegs = 72;
-static_assert(kSoftWarps * kSoftRegs + 4 * kOtherRegs <= (kSoftWarps + 4) * kLaunchRegs, "more registers than the launch has");
+// of its own up. 16384 tokens, 9 heads of 128: 876 us without, 216 + 72 841,
+// 208 + 88 875, 224 + 56 902 (the MMA warp's group spills); of 64, whose ring has
+// more stages: 738, 698, 677, 693. (Narrow, a thread holds 32 scores: not needed.)
+constexpr int kLaunchRegs = 168;
+template <int kSteps>
+struct FwdRegs {
+    static constexpr int kSoft = kSteps > 4 ? 216 : 208, kOther = kSteps > 4 ? 72 : 88;
+    static_assert(kSoftWarps * kSoft + 4 * kOther <= (kSoftWarps + 4) * kLaunchRegs, "more registers than the launch has");
+};
 constexpr uint32_t kTmemCols = 512;  // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kTargetCtas = 152;     // one CTA per SM
 
@@ -73,7 +79,8 @@ static_assert(FwdCfg<8>::kSmem <= 232448 && FwdCfg<4>::kSmem <= 232448, "attenti
 
 struct FwdParams {
     MhaShape s;
-    int alt, narrow;  // narrow: alt with the rows in every quadrant
+    int alt;
+    int twice;        // narrow, the rows twice in each quadrant: the second copies' P is what the first rounded off
     int nsplit;       // with nsplit > 1: nsplit * b pieces of key tiles, shared out by the entries' lengths
     float scale_log2;
     void* o;
@@ -224,7 +231,7 @@ __device__ __forceinline__ FwdWork fwd_work(const FwdParams& p) {
     return w;
 }
 
-template <int kSteps>
+template <int kSteps, bool kNarrow>
 __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork& w, const CUtensorMap* mq,
                              const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
     using C = FwdCfg<kSteps>;
@@ -237,8 +244,8 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
         mbar_arrive_expect_tx(smem_u32(s.q_full), static_cast<uint32_t>(nq * C::kTileBytes));
         for (int t = 0; t < nq; ++t)
             for (int c = 0; c < C::kCh; ++c)
-                for (int r = 0; r < (p.narrow ? 4 : 1); ++r)  // (narrow: the map's boxes are 32 rows)
-                    tma_load_4d(smem_u32(s.q + t * C::kTileBytes + c * kMhaChunkBytes + r * (kMhaChunkBytes / 4)), mq,
+                for (int r = 0; r < (!kNarrow ? 1 : p.twice ? 8 : 4); ++r)  // (the map's boxes are 128, 16 or 32 rows)
+                    tma_load_4d(smem_u32(s.q + t * C::kTileBytes + c * kMhaChunkBytes + r * (kMhaChunkBytes / (p.twice ? 8 : 4))), mq,
                                 smem_u32(s.q_full), c * 64, h0, (w.tile[t] * kMhaTile) >> p.s.gp_log2, w.e, pol);
     }
     const int ahead = p.alt ? 2 : 1;
@@ -263,7 +270,7 @@ __device__ void fwd_producer(const FwdParams& p, const FwdSmem& s, const FwdWork
             fixed = true;
             __syncwarp();
             if (!warp_all(fwait(s.fix, 0u, s, p))) return false;
-            mha_zero_rows(dst, w.kl - kb * kMhaTile, C::kCh, lane);
+            mha_zero_rows(dst, w.kl - kb * kMhaTile, kMhaTile, C::kCh, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.full[stage]));
@@ -546,7 +553,8 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
     constexpr float kBias = T == VAE_F16 ? 6.f : 0.f;
     const int t = warp >> 2, quad = warp & 3;
     const int gp = 1 << p.s.gp_log2;
-    const int i = lane >> p.s.gp_log2, h = w.hk * p.s.g + w.sub * gp + (lane & (gp - 1));
+    const int rr = p.twice ? lane & 15 : lane;
+    const int i = rr >> p.s.gp_log2, h = w.hk * p.s.g + w.sub * gp + (rr & (gp - 1));
     const bool live = i < w.ql;
     const int lim = live ? mha_key_limit(i, w.ql, w.kl, p.s.block) : 0;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -605,7 +613,7 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
             f.x = mha_ex2(f.x);
             f.y = mha_ex2(f.y);
             sum = add2(sum, f);
-            h2[k] = pack2<T>(f.x, f.y);
+            h2[k] = rr == lane ? pack2<T>(f.x, f.y) : pack2_rest<T>(f.x, f.y);
             zero[k] = 0u;
         }
         l += sum.x + sum.y;
@@ -651,7 +659,7 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
         wt[k] = mk == -INFINITY ? 0.f : mha_ex2(mk - mm);
         if (k < parts) ll += wt[k] * ml[256 + k * 32 + lane];
     }
-    if (!live) return;
+    if (!live || rr != lane) return;
     const float inv = mm == -INFINITY ? 0.f : 1.f / ll;
     const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
     const long long prow = (static_cast<long long>(w.piece) * p.s.hq + h) * p.s.sq + i;
@@ -661,7 +669,10 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
         for (int k = 0; k < 8; ++k)
             if (k < parts) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] += wt[k] * o[(k * dn + c + u) * 32 + lane];
+                for (int u = 0; u < 8; ++u) {
+                    const float* x = o + (k * dn + c + u) * 32 + lane;
+                    v[u] += wt[k] * (p.twice ? x[0] + x[16] : x[0]);
+                }
             }
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] *= inv;
@@ -678,7 +689,7 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
 }
 
 // The third warpgroup: it sets up the barriers and TMEM, loads and issues the products.
-template <int T, int kSteps>
+template <int T, int kSteps, bool kNarrow>
 __device__ __forceinline__ void fwd_feed(const FwdParams& p, const FwdSmem& s, const FwdWork& w, const CUtensorMap& mq,
                                          const CUtensorMap& mk, const CUtensorMap& mv, int warp, int lane) {
     using C = FwdCfg<kSteps>;
@@ -701,7 +712,7 @@ __device__ __forceinline__ void fwd_feed(const FwdParams& p, const FwdSmem& s, c
             fence_proxy_async_smem();
         }
         __syncwarp();
-        fwd_producer<kSteps>(p, s, w, &mq, &mk, &mv, lane);  // (meets the others' __syncthreads)
+        fwd_producer<kSteps, kNarrow>(p, s, w, &mq, &mk, &mv, lane);  // (meets the others' __syncthreads)
     } else {
         if (warp == kMmaWarp) {
             tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
@@ -714,7 +725,7 @@ __device__ __forceinline__ void fwd_feed(const FwdParams& p, const FwdSmem& s, c
     }
 }
 
-template <int T, int kSteps>
+template <int T, int kSteps, bool kNarrow>
 __global__ void __launch_bounds__(kThreads, 1)
     mha_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const FwdParams p) {
@@ -753,15 +764,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     constexpr uint32_t tmem = 0u;  // all 512 columns are this CTA's: they start at 0
     if (warp < kSoftWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        if constexpr (!kNarrow) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FwdRegs<kSteps>::kSoft));
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (p.narrow) fwd_softmax_narrow<T, kSteps>(p, s, w, warp, lane);
+        if constexpr (kNarrow) fwd_softmax_narrow<T, kSteps>(p, s, w, warp, lane);
         else fwd_softmax<T, kSteps>(p, s, w, tmem, warp, lane);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        fwd_feed<T, kSteps>(p, s, w, mq, mk, mv, warp, lane);
+        if constexpr (!kNarrow) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FwdRegs<kSteps>::kOther));
+        fwd_feed<T, kSteps, kNarrow>(p, s, w, mq, mk, mv, warp, lane);
     }
     pdl_launch_dependents();
     __syncwarp();
@@ -859,7 +870,7 @@ FwdPlan fwd_plan(const MhaShape& s) {
     return best;
 }
 
-template <int T, int kSteps>
+template <int T, int kSteps, bool kNarrow>
 int fwd_launch(const vae_attention_desc* a, const FwdPlan& f, const CUtensorMap (&map)[3], const FwdParams& p,
                cudaStream_t st) {
     static CtxOnce once;
@@ -870,23 +881,35 @@ int fwd_launch(const vae_attention_desc* a, const FwdPlan& f, const CUtensorMap 
         VAE_CUDA_CHECK(cudaGetDevice(&dev));
         std::lock_guard<std::mutex> lk(mu);
         if (!once.done(dev)) {
-            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_fwd_kernel<T, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            VAE_CUDA_CHECK(cudaFuncSetAttribute(mha_fwd_kernel<T, kSteps, kNarrow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                 C::kSmem));
             cudaFuncAttributes at;
-            VAE_CUDA_CHECK(cudaFuncGetAttributes(&at, mha_fwd_kernel<T, kSteps>));
-            if (at.numRegs < kLaunchRegs)  // the softmax warps would wait for registers that the block does not have
+            VAE_CUDA_CHECK(cudaFuncGetAttributes(&at, mha_fwd_kernel<T, kSteps, kNarrow>));
+            if (!kNarrow && at.numRegs < kLaunchRegs)  // the softmax warps would wait for registers that the block does not have
                 return set_error(VAE_ERR_CUDA, "attention: compiled to %d registers a thread, its split needs %d",
                                  at.numRegs, kLaunchRegs);
             once.mark(dev);
         }
     }
-    VAE_CUDA_CHECK(launch_kernel(mha_fwd_kernel<T, kSteps>, dim3(static_cast<unsigned>(f.items)), dim3(kThreads), C::kSmem,
+    VAE_CUDA_CHECK(launch_kernel(mha_fwd_kernel<T, kSteps, kNarrow>, dim3(static_cast<unsigned>(f.items)), dim3(kThreads), C::kSmem,
                                  st, map[0], map[1], map[2], p));
     if (f.nsplit > 1) {
         const long long rows = static_cast<long long>(a->b) * a->hq * a->sq;
         VAE_CUDA_CHECK(launch_next(mha_join_kernel<T>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p));
     }
     return VAE_OK;
+}
+
+template <bool kNarrow>
+int fwd_by_type(const vae_attention_desc* a, const FwdPlan& f, const CUtensorMap (&map)[3], const FwdParams& p, cudaStream_t st) {
+    const int d = p.s.d;
+    if (a->type == VAE_F16)
+        return d <= 64   ? fwd_launch<VAE_F16, 4, kNarrow>(a, f, map, p, st)
+               : d <= 96 ? fwd_launch<VAE_F16, 6, kNarrow>(a, f, map, p, st)
+                         : fwd_launch<VAE_F16, 8, kNarrow>(a, f, map, p, st);
+    return d <= 64   ? fwd_launch<VAE_BF16, 4, kNarrow>(a, f, map, p, st)
+           : d <= 96 ? fwd_launch<VAE_BF16, 6, kNarrow>(a, f, map, p, st)
+                     : fwd_launch<VAE_BF16, 8, kNarrow>(a, f, map, p, st);
 }
 
 }  // namespace
@@ -904,14 +927,15 @@ int mha_fwd_run(const vae_attention_desc* a, const MhaShape& s, const void* q, c
     if (f.items > 0x7fffffffLL) return set_error(VAE_ERR_SHAPE, "attention: too many tiles");
     const int gp = 1 << s.gp_log2;
     CUtensorMap map[3];
-    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, (f.narrow ? 32 : kMhaTile) / gp);
+    const bool twice = f.narrow && static_cast<long long>(s.sq) * gp <= 16;
+    int rc = mha_map(&map[0], a, q, a->q_stride, s.sq, s.hq, gp, (twice ? 16 : f.narrow ? 32 : kMhaTile) / gp);
     if (rc == VAE_OK) rc = mha_map(&map[1], a, k, a->k_stride, s.sk, s.hkv, 1, kMhaTile);
     if (rc == VAE_OK) rc = mha_map(&map[2], a, v, a->v_stride, s.sk, s.hkv, 1, kMhaTile);
     if (rc != VAE_OK) return rc;
     FwdParams p{};
     p.s = s;
     p.alt = f.alt;
-    p.narrow = f.narrow;
+    p.twice = twice;
     p.nsplit = f.nsplit;
     p.scale_log2 = a->scale * 1.4426950408889634074f;
     p.o = o;
@@ -922,10 +946,8 @@ int mha_fwd_run(const vae_attention_desc* a, const MhaShape& s, const void* q, c
     p.status = device_status_ptr();
     p.timeout_ns = wait_timeout_ns();
     if (p.status == nullptr) return VAE_ERR_CUDA;
-    const bool h = a->type == VAE_F16;
-    if (s.d <= 64) return h ? fwd_launch<VAE_F16, 4>(a, f, map, p, st) : fwd_launch<VAE_BF16, 4>(a, f, map, p, st);
-    if (s.d <= 96) return h ? fwd_launch<VAE_F16, 6>(a, f, map, p, st) : fwd_launch<VAE_BF16, 6>(a, f, map, p, st);
-    return h ? fwd_launch<VAE_F16, 8>(a, f, map, p, st) : fwd_launch<VAE_BF16, 8>(a, f, map, p, st);
+    if (f.narrow) return fwd_by_type<true>(a, f, map, p, st);
+    return fwd_by_type<false>(a, f, map, p, st);
 }
 
 }  // namespace vae

@@ -381,6 +381,63 @@ def test_attention_peaked_scores(t):
         _within(g, r, 1.01 * e + U[t] * np.abs(r) * 1.001 + FLOOR[t])
 
 
+FEW = [
+    # b, sq, sk, hq, hkv, d, type, block, q_len, k_len: at most 64 rows of a key head (the output: 16)
+    (2, 1, 16, 4, 2, 64, "bf16", 0, None, None),
+    (1, 5, 20, 3, 3, 64, "f16", 0, None, None),
+    (1, 30, 30, 2, 2, 128, "bf16", 1, None, None),
+    (1, 30, 200, 2, 1, 72, "f16", 0, None, None),
+    (2, 16, 200, 2, 2, 96, "f16", 0, (7, 16), (200, 90)),
+    (2, 64, 256, 2, 2, 64, "bf16", 16, (64, 41), None),
+    (2, 1, 3001, 8, 2, 128, "f16", 0, None, (3001, 17)),
+    (1, 3, 1500, 4, 4, 64, "bf16", 0, None, None),
+    (1, 4, 700, 24, 2, 40, "bf16", 0, None, None),  # 12 heads to a key head: three parts of four
+]
+
+
+@pytest.mark.parametrize("case", FEW)
+def test_attention_few_rows_in_two_parts(case):
+    """Few rows lie twice in a tile, and P and dS are held in two 16-bit parts: what the second rounds off is at most U of the
+    first's U, so that the results are off by their own rounding and U U of the sums only (gradients of
+    scores where D is formed from f32, up to 256 keys; f16's second part, 2^-14 of the first's scale at
+    the least, ends at 2^-25 2^-14, under the bound's tiny term)."""
+    t = case[6]
+    (q, k, v, do), (q64, k64, v64, do64), kw, okw = _att_inputs(case)
+    o, lse = vg.attention(q, k, v, **kw)
+    got = vg.attention_backward(do, q, k, v, o, lse, **kw)
+    vg.sync_status()
+    rows, keys = _rows_behind(case)
+    ro, rl, pv, qk = ot.attention(q64, k64, v64, bounds=True, **okw)
+    es = SUM * (1.0 + qk + np.where(np.isinf(rl), 0.0, np.abs(rl))).transpose(0, 2, 1)[..., None]
+    tol = U[t] * np.abs(ro) * 1.001 + FLOOR[t] + (U[t] ** 2 + 2 * es + SUM) * pv + 2.0 ** -38 * pv.max()
+    gp = np.gcd(case[3] // case[4], 64)
+    if case[1] * gp <= 16:
+        _within(_np(o)[~rows], ro[~rows], tol[~rows])
+    ref = ot.attention_backward(do64, q64, k64, v64, **okw)
+    tol = ot.attention_backward_bounds(do64, q64, k64, v64, U[t] ** 2, SUM, tiny=2.0 ** -38 if t == "f16" else 2.0 ** -100, **okw)
+    for n, (g, r, e, behind) in enumerate(zip(got, ref, tol, (rows, keys, keys))):
+        if n == 2 or case[2] <= 256:
+            _within(_np(g)[~behind], r[~behind], 1.01 * e[~behind] + U[t] * np.abs(r[~behind]) * 1.001 + FLOOR[t])
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("case", [(2, 1, 1, 4, 2, 64, 1, None), (1, 300, 1, 3, 3, 128, 0, None), (2, 140, 50, 4, 1, 96, 0, (1, 1)),
+                                  (1, 1, 1, 1, 1, 40, 0, None)])
+def test_attention_single_key(case, t):
+    """Softmax over one key is 1 whatever its score: o is the value, dq and dk are exactly 0."""
+    torch = torch_mod()
+    b, sq, sk, hq, hkv, d, block, k_len = case
+    (q, k, v, do), (_, _, _, do64), kw, _ = _att_inputs((b, sq, sk, hq, hkv, d, t, block, None, k_len))
+    o, lse = vg.attention(q, k, v, **kw)
+    dq, dk, dv = vg.attention_backward(do, q, k, v, o, lse, **kw)
+    vg.sync_status()
+    assert torch.equal(o, v[:, :1].repeat_interleave(hq // hkv, 2).expand_as(o))
+    assert not dq.any() and not dk.any()
+    ref = do64.reshape(b, sq, hkv, hq // hkv, d)
+    tol = (U[t] ** 2 + 2 * SUM) * np.abs(ref).sum((1, 3))
+    _within(dv[:, 0], ref.sum((1, 3)), tol * 1.01 + U[t] * np.abs(ref.sum((1, 3))) * 1.001 + FLOOR[t])
+
+
 def test_attention_strided_views_and_other_token_orders():
     """q, k, v as views of one projection, outputs and gradients into views, batch and token dims swapped
     in memory: the same bits as with dense tensors."""
