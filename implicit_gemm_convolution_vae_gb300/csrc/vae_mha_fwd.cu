@@ -31,16 +31,16 @@
 // masked scores are replaced before the maximum, and V's rows are zeroed in
 // shared memory on the one tile that the length ends in.
 //
-// Measured on GB300: 16384 tokens x 9 heads x 128 in f16 865 to 947 us (1300 to
-// 1430 TFLOP/s; with the softmax left out 786, with no hand-over between warps
+// Measured on GB300: 16384 tokens x 9 heads x 128 in f16 840 to 920 us (1340 to
+// 1470 TFLOP/s; with the softmax left out 786, with no hand-over between warps
 // 717). Bound by the MMAs: S reads both operands from shared memory, 8 KB in 64
-// cycles, which is all that it gives, and a step of both streams takes 2970
-// cycles of which the products alone take 2400. Eight softmax warps and not
-// sixteen (half a row each, maxima traded: 1282 us); a tile's PV whole and not
-// from its first half of P on (918 against 876 us), a tile whole and not S and
-// P in halves of 64 keys (1193 against 882 us). One token over four caches
-// of up to 32760 keys (201 MB): 45 us a call in a graph, 6.3 TB/s while it
-// streams.
+// cycles, which is all that it gives; the products alone take 2400 cycles of a
+// step of both streams, which took 2970 before the registers were moved (below).
+// Eight softmax warps and not sixteen (half a row each, maxima traded: 1282 us);
+// a tile's PV whole and not from its first half of P on (918 against 876 us), a
+// tile whole and not S and P in halves of 64 keys (1193 against 882 us). One
+// token over four caches of up to 32760 keys (201 MB): 45 us a call in a graph,
+// 6.3 TB/s while it streams.
 #include <cmath>
 
 #include "vae_mha_fwd.h"
