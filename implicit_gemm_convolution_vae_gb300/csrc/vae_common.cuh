@@ -540,30 +540,26 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // the 1024^2 decode measured 14.8 ms with it against 14.3 ms without on GB300.
 bool pdl_enabled();
 
-// overlap: launched while the grid before it on the stream still runs. csize: CTAs per cluster; 0: no cluster launch
-// (a kernel whose code signals over its cluster is launched as one of a single CTA at least).
+// overlap: launched while the grid before it on the stream still runs.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel_as(bool overlap, unsigned csize, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                             cudaStream_t stream, Args&&... args) {
+cudaError_t launch_kernel_as(bool overlap, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = overlap ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = csize;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = csize > 0 ? 2 : 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                           Args&&... args) {
-    return launch_kernel_as(pdl_enabled(), 0u, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
+    return launch_kernel_as(pdl_enabled(), kernel, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 // The second and later kernels of one call: always launched ahead (they wait in
 // pdl_wait, and every kernel before them in the call lets them go with
@@ -571,7 +567,7 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
 template <typename... KArgs, typename... Args>
 cudaError_t launch_next(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                         Args&&... args) {
-    return launch_kernel_as(true, 0u, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
+    return launch_kernel_as(true, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 #define VAE_CUDA_CHECK(expr)                                                                   \

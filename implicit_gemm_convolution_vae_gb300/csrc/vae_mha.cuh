@@ -128,30 +128,6 @@ __device__ __forceinline__ void mma_ts_k(uint32_t d_tmem, uint32_t a_tmem, uint6
                     k != 0 ? 1u : 0u);
 }
 
-// One arrival on the barrier at this offset in every CTA of a cluster of
-// `csize` (1 or 2), once the MMAs issued so far are done.
-__device__ __forceinline__ void umma_commit_all(uint32_t bar, int csize) {
-    if (csize == 1) {
-        umma_commit(bar);
-        return;
-    }
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
-// A TMA box into the same place of every CTA of `mask`, counted on each one's
-// barrier at this offset.
-__device__ __forceinline__ void tma_load_4d_to(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
-                                               int c3, uint16_t mask, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7, %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(mask), "l"(policy)
-        : "memory");
-}
-
 // What packing a and b to 16 bits leaves of them, packed. Where a tile has room
 // for its rows twice, the second copies take this part of P and dS: the products
 // with the two are added. One rounding of P or dS is as large as the result's

@@ -22,10 +22,8 @@
 // MMAs with both operands in shared memory ran at 90 cycles each, bound by the
 // 8 KB that each reads there, those with one in TMEM at 57 to 64.
 //
-// Both kernels read 64 KB of tiles per step, more than L2 gives every SM at the
-// rate the products run (28 bytes a cycle and SM were measured): where there is
-// work for every SM, clusters of two CTAs with neighbouring tiles of one head
-// take the same steps, each loads half of every tile and sends it to both.
+// Both kernels read 64 KB of tiles per step, and L2 gives every SM 26 to 29 bytes
+// a cycle (measured): 2280 to 2510 cycles of each step's time are the tiles' way.
 //
 // D = rowsum(dO * O) takes O as the forward rounded it. Rows that meet few keys
 // (kExactTiles tiles at most) feel that rounding in dS: the query-tile kernel
@@ -89,7 +87,6 @@ struct BwdParams {
     MhaShape s;
     float scale, scale_log2;
     int nsplit_q, nsplit_k;
-    int csize_q, csize_k;       // CTAs per cluster
     int twice;                  // at most 64 rows to a head: each lies twice in its tile, P and dS in two parts
     float* side;                // [b][hkv][nsub][ntile][256]
     const unsigned* maxima;     // f16: bits of max |dO|^2, max |V|^2
@@ -259,29 +256,15 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
             tma_load_4d(smem_u32(dst + c * kMhaChunkBytes + r * (kMhaChunkBytes / 2)), map, bar, c * 64, head,
                         token + r * half, e, pol);
 }
-// The same into both CTAs of a cluster, each of which brings the half of its rank.
-template <int kChunks>
-__device__ __forceinline__ void load_tile_shared(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int head, int token,
-                                                 int half, int e, int rank, int csize, uint64_t pol) {
-    if (csize == 1) {
-        load_tile<kChunks>(dst, map, bar, head, token, half, e, pol);
-        return;
-    }
-    for (int c = 0; c < kChunks; ++c)
-        tma_load_4d_to(smem_u32(dst + c * kMhaChunkBytes + rank * (kMhaChunkBytes / 2)), map, bar, c * 64, head,
-                       token + rank * half, e, static_cast<uint16_t>(3), pol);
-}
-
-// Set-up and tear-down common to both kernels. No CTA of a cluster sends to
-// another before the other's barriers are there, or leaves before all is done.
+// Set-up and tear-down common to both kernels.
 template <typename C>
-__device__ __forceinline__ void bwd_begin(const BwdSmem& s, int warp, int csize, uint32_t res_arrivals) {
+__device__ __forceinline__ void bwd_begin(const BwdSmem& s, int warp, uint32_t res_arrivals) {
     if (threadIdx.x == 0) {
         *s.abort_flag = 0;
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&s.a_full[i]), 1u);
             mbar_init(smem_u32(&s.b_full[i]), 1u);
-            mbar_init(smem_u32(&s.empty[i]), static_cast<uint32_t>(csize));
+            mbar_init(smem_u32(&s.empty[i]), 1u);
             mbar_init(smem_u32(&s.fix[i]), 1u);
         }
         mbar_init(smem_u32(s.res_full), res_arrivals);
@@ -290,7 +273,7 @@ __device__ __forceinline__ void bwd_begin(const BwdSmem& s, int warp, int csize,
         mbar_init(smem_u32(s.p_full), kSoftWarps);
         mbar_init(smem_u32(s.ds_full), kSoftWarps);
         mbar_init(smem_u32(s.done), 1u);
-        mbar_init(smem_u32(s.drain), static_cast<uint32_t>(csize));
+        mbar_init(smem_u32(s.drain), 1u);
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.x_bar[i]), 2u);
         fence_mbar_init();
     }
@@ -300,15 +283,13 @@ __device__ __forceinline__ void bwd_begin(const BwdSmem& s, int warp, int csize,
     }
     tc_fence_before();
     __syncthreads();
-    if (csize > 1) cluster_sync();
     tc_fence_after();
 }
-__device__ __forceinline__ void bwd_end(int warp, int csize) {
+__device__ __forceinline__ void bwd_end(int warp) {
     pdl_launch_dependents();
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (csize > 1) cluster_sync();
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
@@ -318,8 +299,7 @@ __device__ __forceinline__ void bwd_end(int warp, int csize) {
 
 // The ring's producer state: what is in flight when a wait runs out has to
 // land before the CTA may exit. A stage that has to be fixed completes on a
-// barrier of its own (per stage: the other CTA of a cluster may already send
-// the next one) and then on the stage's by hand.
+// barrier of its own and then on the stage's by hand.
 template <int kN>
 struct BwdRing {
     int stage = 0;
@@ -374,11 +354,11 @@ struct BwdRing {
     }
 };
 
-// (Every CTA of a cluster waits for all of them: none leaves while another's MMAs still signal its barriers.)
-__device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p, bool ok, int csize) {
+// (No CTA leaves while its MMAs still run.)
+__device__ __forceinline__ void mma_finish(const BwdSmem& s, const BwdParams& p, bool ok) {
     if (elect_one()) {
         if (ok) umma_commit(smem_u32(s.done));
-        umma_commit_all(smem_u32(s.drain), csize);
+        umma_commit(smem_u32(s.drain));
         int never = 0;
         (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
     }
@@ -426,22 +406,18 @@ __device__ __forceinline__ void store_acc(uint32_t t, int d, bool live, bool any
 // ───────────────────────────── dK and dV, per key tile ─────────────────────────────
 
 struct KvWork {
-    int e, hk, kb, split, rank;
+    int e, hk, kb, split;
     int ql, kl;
-    int t0, nt;      // row tiles [t0, nt) of each part of the group see the cluster's key tiles
+    int t0, nt;      // row tiles [t0, nt) of each part of the group see the key tile
     int first, n;    // this split's share of the nsub * (nt - t0) tiles
 };
 
-// (A cluster's CTAs have key tiles kb, kb + 1 and the same row tiles.)
 __device__ __forceinline__ KvWork kv_work(const BwdParams& p) {
     const MhaShape& s = p.s;
     KvWork w;
-    const int nk = (s.nkb + p.csize_k - 1) / p.csize_k;
-    w.rank = static_cast<int>(blockIdx.x) % p.csize_k;
-    int r = blockIdx.x / p.csize_k;
-    const int kb0 = r % nk * p.csize_k;
-    w.kb = kb0 + w.rank;
-    r /= nk;
+    int r = blockIdx.x;
+    w.kb = r % s.nkb;
+    r /= s.nkb;
     w.split = r % p.nsplit_k;
     r /= p.nsplit_k;
     w.hk = r % s.hkv;
@@ -450,14 +426,14 @@ __device__ __forceinline__ KvWork kv_work(const BwdParams& p) {
     w.kl = mha_len(s.k_len, w.e, s.sk);
     const long long rows = static_cast<long long>(w.ql) << s.gp_log2;
     w.nt = static_cast<int>((rows + kMhaTile - 1) / kMhaTile);
-    long long i0 = 0;  // the first query that sees a key of the first tile
+    long long i0 = 0;  // the first query that sees a key of the tile
     if (s.block > 0) {
-        i0 = static_cast<long long>(kb0 * kMhaTile / s.block * s.block) - (w.kl - w.ql);
+        i0 = static_cast<long long>(w.kb * kMhaTile / s.block * s.block) - (w.kl - w.ql);
         if (i0 < 0) i0 = 0;
     }
     const long long t0 = (i0 << s.gp_log2) / kMhaTile;
     w.t0 = t0 < w.nt ? static_cast<int>(t0) : w.nt;
-    const int all = kb0 * kMhaTile < w.kl ? s.nsub * (w.nt - w.t0) : 0;
+    const int all = w.kb * kMhaTile < w.kl ? s.nsub * (w.nt - w.t0) : 0;
     const int per = (all + p.nsplit_k - 1) / p.nsplit_k;
     w.first = w.split * per < all ? w.split * per : all;
     w.n = (w.first + per < all ? w.first + per : all) - w.first;
@@ -496,9 +472,9 @@ __device__ void kv_producer(const BwdParams& p, const BwdSmem& s, const KvWork& 
                 mbar_arrive_expect_tx(ab, C::kTileBytes + kSideBytes);
                 mbar_arrive_expect_tx(bb, C::kTileBytes);
             }
-            load_tile_shared<C::kCh>(dst, mq, ab, head, token, half, w.e, w.rank, p.csize_k, pol);
+            load_tile<C::kCh>(dst, mq, ab, head, token, half, w.e, pol);
             bulk_load(smem_u32(sd), src, kSideBytes, ab);
-            load_tile_shared<C::kCh>(dst + C::kTileBytes, mg, bb, head, token, half, w.e, w.rank, p.csize_k, pol);
+            load_tile<C::kCh>(dst + C::kTileBytes, mg, bb, head, token, half, w.e, pol);
         }
         if (fix) {
             if (!r.template fix<C>(s, p, static_cast<int>(valid), p.twice != 0, lane)) break;
@@ -559,7 +535,7 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
         tc_fence_after();
         if (elect_one()) {
             mma_ts<64>(tK, tX, ring_m + st * stage_units, id_o, x != 0 ? 1u : 0u);
-            umma_commit_all(smem_u32(&s.empty[st]), p.csize_k);
+            umma_commit(smem_u32(&s.empty[st]));
         }
         __syncwarp();
         if (more) {
@@ -571,7 +547,7 @@ __device__ void kv_mma(const BwdParams& p, const BwdSmem& s, const KvWork& w) {
         st = st1;
         ph = ph1;
     }
-    mma_finish(s, p, ok, p.csize_k);
+    mma_finish(s, p, ok);
 }
 
 // 64 values as 16-bit pairs in 32 columns, or what that rounding leaves of them.
@@ -719,31 +695,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    bwd_begin<C>(s, warp, p.csize_k, 1u);
+    bwd_begin<C>(s, warp, 1u);
     if (warp < kSoftWarps) kv_softmax<T, kSteps, kTwice>(p, s, w, warp, lane);
     else if (warp == kTmaWarp) kv_producer<C>(p, s, w, &mq, &mg, &mk, &mv, lane);
     else kv_mma<T, kSteps>(p, s, w);
-    bwd_end(warp, p.csize_k);
+    bwd_end(warp);
 }
 
 // ───────────────────────────── dQ, per row tile ─────────────────────────────
 
 struct QWork {
-    int e, hk, sub, tile, split, rank;
+    int e, hk, sub, tile, split;
     int ql, kl;
-    int kb0, n;  // this split's key tiles, the same for a cluster's CTAs
+    int kb0, n;  // this split's key tiles
     bool exact;  // D is formed here
 };
 
 __device__ __forceinline__ QWork q_work(const BwdParams& p) {
     const MhaShape& s = p.s;
     QWork w;
-    const int nt = (s.ntile + p.csize_q - 1) / p.csize_q;
-    w.rank = static_cast<int>(blockIdx.x) % p.csize_q;
-    int r = blockIdx.x / p.csize_q;
-    const int t0 = (nt - 1 - r % nt) * p.csize_q;  // the tiles that see the most keys first
-    w.tile = t0 + w.rank;
-    r /= nt;
+    int r = blockIdx.x;
+    w.tile = s.ntile - 1 - r % s.ntile;  // the tiles that see the most keys first
+    r /= s.ntile;
     w.split = r % p.nsplit_q;
     r /= p.nsplit_q;
     w.sub = r % s.nsub;
@@ -752,10 +725,9 @@ __device__ __forceinline__ QWork q_work(const BwdParams& p) {
     w.e = r / s.hkv;
     w.ql = mha_len(s.q_len, w.e, s.sq);
     w.kl = mha_len(s.k_len, w.e, s.sk);
-    // the last row of the cluster's tiles sees the most keys
-    const int last = (t0 + p.csize_q < s.ntile ? t0 + p.csize_q : s.ntile) - 1;
-    const int i0 = (t0 * kMhaTile) >> s.gp_log2;
-    int i1 = ((last + 1) * kMhaTile - 1) >> s.gp_log2;
+    // the tile's last row sees the most keys
+    const int i0 = (w.tile * kMhaTile) >> s.gp_log2;
+    int i1 = ((w.tile + 1) * kMhaTile - 1) >> s.gp_log2;
     if (i1 >= w.ql) i1 = w.ql - 1;
     const int lim = i0 < w.ql ? mha_key_limit(i1, w.ql, w.kl, s.block) : 0;
     const int all = (lim + kMhaTile - 1) / kMhaTile;
@@ -782,8 +754,8 @@ __device__ void q_producer(const BwdParams& p, const BwdSmem& s, const QWork& w,
         if (lane == 0) {
             mbar_arrive_expect_tx(ab, (fix ? 2u : 1u) * C::kTileBytes);
             if (!fix) mbar_arrive_expect_tx(bb, C::kTileBytes);
-            load_tile_shared<C::kCh>(dst, mk, ab, w.hk, kb * kMhaTile, 64, w.e, w.rank, p.csize_q, pol);
-            load_tile_shared<C::kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, 64, w.e, w.rank, p.csize_q, pol);
+            load_tile<C::kCh>(dst, mk, ab, w.hk, kb * kMhaTile, 64, w.e, pol);
+            load_tile<C::kCh>(dst + C::kTileBytes, mv, bb, w.hk, kb * kMhaTile, 64, w.e, pol);
         }
         if (fix) {
             if (!r.template fix<C>(s, p, w.kl - kb * kMhaTile, false, lane)) break;
@@ -842,7 +814,7 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
         tc_fence_after();
         if (elect_one()) {
             if (x >= from) mma_ts<64>(tQ, tX, ring_m + st * stage_units, id_o, x != from ? 1u : 0u);
-            umma_commit_all(smem_u32(&s.empty[st]), p.csize_q);
+            umma_commit(smem_u32(&s.empty[st]));
         }
         __syncwarp();
         if (more) {
@@ -854,7 +826,7 @@ __device__ void q_mma(const BwdParams& p, const BwdSmem& s, const QWork& w) {
         st = st1;
         ph = ph1;
     }
-    mma_finish(s, p, ok, p.csize_q);
+    mma_finish(s, p, ok);
 }
 
 template <int T, int kSteps, bool kTwice>
@@ -865,8 +837,7 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
     const int at = quad * 32 + lane, rr = kTwice ? at & 63 : at, r = w.tile * kMhaTile + rr;
     const bool rest = kTwice && rr != at;  // these lanes hold the other half's rows again
     const int i = r >> sh.gp_log2, h = w.hk * sh.g + w.sub * gp + (r & (gp - 1));
-    const bool here = w.tile < sh.ntile;  // (a cluster's last tile may be missing)
-    const bool live = here && i < w.ql;
+    const bool live = i < w.ql;
     const int lim = live ? mha_key_limit(i, w.ql, w.kl, sh.block) : 0;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
@@ -894,7 +865,7 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(s.res_full));
     }
-    float* side = p.side + (((static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.nsub + w.sub) * sh.ntile + (here ? w.tile : 0)) * kSideFloats;
+    float* side = p.side + (((static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.nsub + w.sub) * sh.ntile + w.tile) * kSideFloats;
     const float nl = live ? side[rr] : -INFINITY;
     float D = live ? side[128 + rr] : 0.f;
     const float c = ds_factor<T>(p.maxima);
@@ -1016,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w.n == 0) {  // no key: zeros within the length
         const int r = w.tile * kMhaTile + threadIdx.x;
         const int i = r >> p.s.gp_log2, h = w.hk * p.s.g + (w.sub << p.s.gp_log2) + (r & ((1 << p.s.gp_log2) - 1));
-        if (threadIdx.x < kMhaTile && w.tile < p.s.ntile && i < w.ql) {
+        if (threadIdx.x < kMhaTile && i < w.ql) {
             const long long rows = static_cast<long long>(p.s.b) * p.s.hq * p.s.sq;
             const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
             store_acc<T>(0u, p.s.d, true, false, 0.f, p.dq, w.e * p.dqs.b + i * p.dqs.s + h * p.dqs.h,
@@ -1024,11 +995,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    bwd_begin<C>(s, warp, p.csize_q, kSoftWarps);
+    bwd_begin<C>(s, warp, kSoftWarps);
     if (warp < kSoftWarps) q_softmax<T, kSteps, kTwice>(p, s, w, warp, lane);
     else if (warp == kTmaWarp) q_producer<C>(p, s, w, &mk, &mv, lane);
     else q_mma<T, kSteps>(p, s, w);
-    bwd_end(warp, p.csize_q);
+    bwd_end(warp);
 }
 
 // ───────────────────────────── joining the splits ─────────────────────────────
@@ -1063,21 +1034,18 @@ __global__ void __launch_bounds__(256)
         make_uint2(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w));
 }
 
-// Clusters of two where every SM has work all the same, and the number of splits
-// of the other side whose waves of CTAs take the shortest time, by what the
-// parts measured on GB300 (microseconds): a tile of the other side 1.4 (query
+// The number of splits of the other side whose waves of CTAs take the shortest
+// time, by what the parts measured on GB300 (microseconds): a tile of the other side 1.4 (query
 // tiles) and 1.8 (key tiles), a CTA's set-up and end 5, the joining kernel 3 and
 // its traffic at 6 TB/s.
 struct BwdPlan {
-    int nsplit_q, nsplit_k, csize_q, csize_k;
+    int nsplit_q, nsplit_k;
     long long q_items, k_items, row_tiles, key_tiles;
     size_t side, part_q, part_kv;  // floats
 };
 // heads x tiles CTAs against `other` tiles; `sum`: elements that a split writes and the join reads.
-void split_plan(long long heads, int tiles, long long other, double tile_us, double sum, int most, int* nsplit, int* csize,
-                long long* items) {
-    *csize = heads * tiles >= kTargetCtas && tiles >= 2 ? 2 : 1;
-    const long long each = heads * ((tiles + *csize - 1) / *csize * *csize);
+void split_plan(long long heads, int tiles, long long other, double tile_us, double sum, int most, int* nsplit, long long* items) {
+    const long long each = heads * tiles;
     double least = 0.0;
     for (int n = 1; n == 1 || (n <= most && each * n <= 4 * kTargetCtas); ++n) {
         const double waves = static_cast<double>((each * n - 1) / kTargetCtas + 1);
@@ -1098,9 +1066,9 @@ BwdPlan bwd_plan(const MhaShape& s) {
     f.key_tiles = k_heads * s.nkb;
     // (two tiles of the other side a CTA at least; rows that meet few keys are not split: they form their D)
     split_plan(q_heads, s.ntile, s.nkb, 1.4, static_cast<double>(s.b) * s.hq * s.sq * s.d,
-               s.nkb <= kExactTiles ? 1 : s.nkb / 2, &f.nsplit_q, &f.csize_q, &f.q_items);
+               s.nkb <= kExactTiles ? 1 : s.nkb / 2, &f.nsplit_q, &f.q_items);
     split_plan(k_heads, s.nkb, row_tiles, 1.8, 2.0 * s.b * s.hkv * s.sk * s.d,
-               static_cast<int>(std::min<long long>(row_tiles / 2, 1 << 20)), &f.nsplit_k, &f.csize_k, &f.k_items);
+               static_cast<int>(std::min<long long>(row_tiles / 2, 1 << 20)), &f.nsplit_k, &f.k_items);
     f.side = static_cast<size_t>(f.row_tiles) * kSideFloats;
     f.part_q = f.nsplit_q > 1 ? static_cast<size_t>(f.nsplit_q) * s.b * s.hq * s.sq * s.d : 0;
     f.part_kv = f.nsplit_k > 1 ? static_cast<size_t>(f.nsplit_k) * 2 * s.b * s.hkv * s.sk * s.d : 0;
@@ -1127,13 +1095,11 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
     if (T == VAE_F16) VAE_CUDA_CHECK(cudaMemsetAsync(pp.maxima, 0, 2 * sizeof(unsigned), st));
     const long long prep = f.row_tiles + (T == VAE_F16 ? f.key_tiles : 0);
     VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
-    // (The query-tile kernel first: it may put its D into the side rows. Always launched as clusters, of one CTA at least:
-    // a commit or copy with a cluster mask is an illegal instruction in a grid that was launched without.)
-    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_q), mha_dq_kernel<T, kSteps, kTwice>,
-                                    dim3(static_cast<unsigned>(f.q_items)), dim3(kThreads), kQSmem, st, map[2], map[3], p));
-    VAE_CUDA_CHECK(launch_kernel_as(false, static_cast<unsigned>(f.csize_k), mha_dkv_kernel<T, kSteps, kTwice>,
-                                    dim3(static_cast<unsigned>(f.k_items)), dim3(kThreads), kKvSmem, st, map[0], map[1], map[2],
-                                    map[3], p));
+    // (The query-tile kernel first: it may put its D into the side rows.)
+    VAE_CUDA_CHECK(launch_kernel_as(false, mha_dq_kernel<T, kSteps, kTwice>, dim3(static_cast<unsigned>(f.q_items)),
+                                    dim3(kThreads), kQSmem, st, map[2], map[3], p));
+    VAE_CUDA_CHECK(launch_kernel_as(false, mha_dkv_kernel<T, kSteps, kTwice>, dim3(static_cast<unsigned>(f.k_items)),
+                                    dim3(kThreads), kKvSmem, st, map[0], map[1], map[2], map[3], p));
     const MhaShape& s = p.s;
     if (f.nsplit_k > 1) {
         const long long rows = static_cast<long long>(s.b) * s.hkv * s.sk;
@@ -1204,8 +1170,6 @@ int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout
     p.scale_log2 = a->scale * 1.4426950408889634074f;
     p.nsplit_q = f.nsplit_q;
     p.nsplit_k = f.nsplit_k;
-    p.csize_q = f.csize_q;
-    p.csize_k = f.csize_k;
     p.twice = static_cast<long long>(s.sq) * gp <= kMhaTile / 2;
     p.q = q;
     p.dout = dout;
