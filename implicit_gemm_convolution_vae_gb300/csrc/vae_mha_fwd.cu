@@ -31,6 +31,11 @@
 // masked scores are replaced before the maximum, and V's rows are zeroed in
 // shared memory on the one tile that the length ends in.
 //
+// A row sees no key exactly where its sum l is 0: the key of a row's first maximum
+// adds 2^kBias to it, and l is scaled down only when a new one does. (The maximum
+// does not tell: it passes over NaN. A NaN score leaves l, O and so o and lse NaN,
+// through every join.)
+//
 // Measured on GB300: 16384 tokens x 9 heads x 128 in f16 840 to 920 us (1340 to
 // 1470 TFLOP/s; with the softmax left out 786, with no hand-over between warps
 // 717). Bound by the MMAs: S reads both operands from shared memory, 8 KB in 64
@@ -417,6 +422,12 @@ __device__ void fwd_store(const FwdParams& p, const FwdWork& w, uint32_t tO, int
     else p.lse[row] = lse2 * 0.69314718055994530942f;
 }
 
+// The weight of a part whose maximum is m and sum l beside the maximum mm of all parts: 0 where it saw no key. (m and mm
+// are -infinity where every score that a part saw is NaN, and l is NaN then.)
+__device__ __forceinline__ float part_weight(float m, float l, float mm) {
+    return l == 0.f ? 0.f : m == mm ? 1.f : mha_ex2(m - mm);
+}
+
 template <int T, int kSteps>
 __device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork& w, uint32_t tmem, int warp, int lane) {
     // f16 holds P 2^kBias high (the sum l too): 2^(8 + 6) at most
@@ -533,14 +544,14 @@ __device__ void fwd_softmax(const FwdParams& p, const FwdSmem& s, const FwdWork&
             tc_fence_after();
             const float m1 = s.ml[rr], l1 = s.ml[128 + rr];
             const float mm = fmaxf(m, m1);
-            const float w0 = m == -INFINITY ? 0.f : mha_ex2(m - mm), w1 = m1 == -INFINITY ? 0.f : mha_ex2(m1 - mm);
+            const float w0 = part_weight(m, l, mm), w1 = part_weight(m1, l1, mm);
             const float ll = w0 * l + w1 * l1;
-            fwd_store<T, kSteps>(p, w, tO, i, h, live, w0, o1 + rr, w1, mm == -INFINITY ? 0.f : 1.f / ll,
-                              mm == -INFINITY ? -INFINITY : mm - kBias + log2f(ll));
+            fwd_store<T, kSteps>(p, w, tO, i, h, live, w0, o1 + rr, w1, ll == 0.f ? 0.f : 1.f / ll,
+                              ll == 0.f ? -INFINITY : mm - kBias + log2f(ll));
         }
     } else if (runs && ok && any_live) {
         tc_fence_after();
-        const bool none = m == -INFINITY;
+        const bool none = l == 0.f;
         fwd_store<T, kSteps>(p, w, tO, i, h, live, 1.f, nullptr, 0.f, none ? 0.f : 1.f / l,
                           none ? -INFINITY : m - kBias + log2f(l));
     }
@@ -655,12 +666,12 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
     float wt[8], ll = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float mk = k < parts ? ml[k * 32 + lane] : -INFINITY;
-        wt[k] = mk == -INFINITY ? 0.f : mha_ex2(mk - mm);
-        if (k < parts) ll += wt[k] * ml[256 + k * 32 + lane];
+        const float lk = k < parts ? ml[256 + k * 32 + lane] : 0.f;
+        wt[k] = k < parts ? part_weight(ml[k * 32 + lane], lk, mm) : 0.f;
+        ll += wt[k] * lk;
     }
     if (!live || rr != lane) return;
-    const float inv = mm == -INFINITY ? 0.f : 1.f / ll;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const long long row = (static_cast<long long>(w.e) * p.s.hq + h) * p.s.sq + i;
     const long long prow = (static_cast<long long>(w.piece) * p.s.hq + h) * p.s.sq + i;
     for (int c = warp * 8; c < p.s.d; c += 64) {
@@ -682,7 +693,7 @@ __device__ void fwd_softmax_narrow(const FwdParams& p, const FwdSmem& s, const F
             store8<T>(static_cast<typename Elem<T>::type*>(p.o) + w.e * p.os.b + i * p.os.s + h * p.os.h + c, v);
     }
     if (warp == 0) {
-        const float lse2 = mm == -INFINITY ? -INFINITY : mm - kBias + log2f(ll);
+        const float lse2 = ll == 0.f ? -INFINITY : mm - kBias + log2f(ll);
         if (p.nsplit > 1) p.plse[prow] = lse2;
         else p.lse[row] = lse2 * 0.69314718055994530942f;
     }
@@ -833,13 +844,13 @@ __global__ void __launch_bounds__(128) mha_join_kernel(const FwdParams p) {
             v[3] += f[u].w * wt;
         }
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;  // (a piece's NaN passes through its weight)
     if (lane * 4 < s.d) {
         uint2* dst = reinterpret_cast<uint2*>(static_cast<typename Elem<T>::type*>(p.o) + e * p.os.b + i * p.os.s +
                                               h * p.os.h + lane * 4);
         *dst = make_uint2(pack2<T>(v[0] * inv, v[1] * inv), pack2<T>(v[2] * inv, v[3] * inv));
     }
-    if (lane == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+    if (lane == 0) p.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
 }
 
 // The form and the number of splits whose waves of CTAs take the shortest time,

@@ -430,7 +430,8 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
  *   tokens; 1: causal): with ql, kl the valid lengths, query i stands at
  *   position i + kl - ql and sees the keys of its own block and the earlier
  *   ones, j < (floor(position / block) + 1) * block; at a negative position none.
- * A row that sees no key gives o = 0, lse = -infinity. Rows from ql on are not
+ * A row that sees no key gives o = 0, lse = -infinity; one that holds NaN or
+ * sees a key that does gives NaN in both. Rows from ql on are not
  * written (with fill: 0, lse = -infinity). Keys and values from kl on, and queries from ql on, may hold
  * anything; a key within kl that a row does not see must be finite.
  * vae_attention_backward: with P = exp(scale q k^T - lse), D = sum(do * o),

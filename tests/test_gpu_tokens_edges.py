@@ -1,0 +1,94 @@
+"""GPU parity of the token operators where the values or the shapes are unusual.
+Oracle, tolerances and inputs as in test_gpu_tokens.py."""
+import numpy as np
+import pytest
+
+import implicit_gemm_convolution_vae_gb300 as vg
+from gpu_common import torch_mod
+from oracle import tokens as ot
+from test_gpu_tokens import _att_inputs, _np
+
+pytestmark = pytest.mark.gpu
+
+# ───────────────────────────── NaN that counts ─────────────────────────────
+
+# the forms of the forward: b, sq, sk, hq, hkv, d, type, block, q_len, k_len
+NAN_FORMS = [
+    (1, 4, 100, 4, 4, 64, "f16", 0, None, None),                  # at most 32 rows, one key tile
+    (2, 1, 300, 8, 2, 128, "bf16", 0, None, None),                # at most 32 rows, both streams
+    (2, 1, 3000, 8, 2, 128, "bf16", 0, None, [2945, 700]),        # at most 32 rows, keys over CTAs
+    (1, 24, 2000, 1, 1, 96, "f16", 0, None, None),                # the same, rows once a quadrant
+    (1, 100, 100, 2, 2, 64, "f16", 0, None, None),                # one row tile, one stream
+    (1, 100, 300, 2, 2, 128, "bf16", 1, None, None),              # one row tile, both streams
+    (1, 100, 3000, 3, 1, 64, "f16", 0, None, [2945]),             # one row tile, keys over CTAs
+    (4, 300, 310, 40, 40, 32, "f16", 0, [300, 0, 129, 1], [310, 128, 7, 300]),  # row tiles in pairs
+]
+
+
+def _nan_call(case, q, k, v, kw, okw):
+    """(o, lse, the oracle's o and lse) of a call, and the check that NaN stands where the oracle's does."""
+    o, lse = vg.attention(q, k, v, **kw)
+    vg.sync_status()
+    with np.errstate(invalid="ignore"):
+        ro, rl = ot.attention(_np(q), _np(k), _np(v), **okw)
+    assert (np.isnan(_np(o)) == np.isnan(ro)).all()
+    assert (np.isnan(_np(lse)) == np.isnan(rl)).all() and (np.isneginf(_np(lse)) == np.isneginf(rl)).all()
+    return o, lse, ro, rl
+
+
+@pytest.mark.parametrize("case", NAN_FORMS)
+@pytest.mark.parametrize("where", ["query", "key", "last key"])
+def test_attention_nan_in_rows_and_keys_that_count(case, where):
+    """NaN in a valid query row is NaN in its output and log-sum-exp, NaN in a key is NaN for the rows that see it,
+    and the rows that meet neither keep their bits."""
+    torch = torch_mod()
+    b, sq, sk, hq, hkv, _, _, _, q_len, k_len = case
+    (q, k, v, _), _, kw, okw = _att_inputs(case)
+    clean, clean_lse = vg.attention(q, k, v, **kw)
+    kl = sk if k_len is None else k_len[0]
+    q, k = q.clone(), k.clone()
+    if where == "query":
+        i = (sq if q_len is None else q_len[0]) - 1
+        q[0, i, hq - 1, 3] = float("nan")
+        q[0, i // 2, 0] = float("nan")
+    else:
+        k[0, kl - 1 if where == "last key" else kl // 3, hkv - 1, 5] = float("nan")
+    o, lse, ro, rl = _nan_call(case, q, k, v, kw, okw)
+    met = torch.from_numpy(np.isnan(rl)).cuda()
+    assert met.any() and torch.equal(lse[~met], clean_lse[~met])
+    met = met.transpose(1, 2)
+    assert torch.equal(o[~met], clean[~met])
+
+
+def test_attention_nan_piece_of_one_key():
+    """A split whose only key holds NaN: its part joins as NaN."""
+    case = (1, 1, 1300, 4, 1, 64, "f16", 0, None, None)
+    (q, k, v, _), _, _, _ = _att_inputs(case)
+    torch = torch_mod()
+    for kl in (1, 129, 257, 1025, 1281):
+        n = torch.tensor([kl], dtype=torch.int32, device="cuda")
+        kk = k.clone()
+        kk[0, kl - 1, 0, 0] = float("nan")
+        o, lse = vg.attention(q, kk, v, k_len=n)
+        assert torch.isnan(o).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("case", [(1, 4, 100, 4, 4, 64, "f16", 0, None, None), (1, 140, 600, 4, 2, 128, "bf16", 0, None, None)])
+def test_attention_backward_nan_row(case):
+    """The gradient of a query row with NaN is NaN in its dq and, as every key meets the row, in its head's dk and dv;
+    the other rows' dq keep their bits."""
+    torch = torch_mod()
+    hq, hkv = case[3], case[4]
+    (q, k, v, do), _, kw, _ = _att_inputs(case)
+    o, lse = vg.attention(q, k, v, **kw)
+    ref = vg.attention_backward(do, q, k, v, o, lse, **kw)
+    q = q.clone()
+    q[0, 2, hq - 1, 7] = float("nan")
+    o, lse = vg.attention(q, k, v, **kw)
+    dq, dk, dv = vg.attention_backward(do, q, k, v, o, lse, **kw)
+    vg.sync_status()
+    assert torch.isnan(dq[0, 2, hq - 1]).all()
+    dq[0, 2, hq - 1] = ref[0][0, 2, hq - 1]
+    assert torch.equal(dq, ref[0])
+    for a, r in ((dk, ref[1]), (dv, ref[2])):
+        assert torch.isnan(a[:, :, hkv - 1]).all() and torch.equal(a[:, :, :hkv - 1], r[:, :, :hkv - 1])
