@@ -6,7 +6,7 @@ import pytest
 import implicit_gemm_convolution_vae_gb300 as vg
 from gpu_common import torch_mod
 from oracle import tokens as ot
-from test_gpu_tokens import _att_inputs, _np
+from test_gpu_tokens import SUM, U, _att_inputs, _draw, _ln_terms, _np, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,22 @@ def test_attention_backward_nan_row(case):
     assert torch.equal(dq, ref[0])
     for a, r in ((dk, ref[1]), (dv, ref[2])):
         assert torch.isnan(a[:, :, hkv - 1]).all() and torch.equal(a[:, :, :hkv - 1], r[:, :, :hkv - 1])
+
+
+# ───────────────────────────── layer norm ─────────────────────────────
+
+@pytest.mark.parametrize("m,c", [(1, 64), (64, 256), (15001, 144), (15002, 144), (4901, 1152), (20003, 35), (20001, 200), (1401, 5120)])
+def test_layernorm_backward_without_eps(m, c):
+    """eps 0, which is allowed, and row counts that end inside a chunk: the rows that are not there count nothing."""
+    x, x64 = _draw(29, f"ln.eps0.{m}.{c}", (m, c), "f32", 1.0, 0.25)
+    dy, dy64 = _draw(29, f"ln.eps0.dy.{m}.{c}", (m, c), "f16")
+    n, rstd, en = _ln_terms(x64, 0.0)
+    dx, dg, db = vg.layernorm_backward(dy, x, eps=0.0)
+    rx, rg, rb = ot.layernorm_backward(dy64, x64, None, 0.0)
+    gr = np.abs(dy64)
+    mean = lambda a: a.mean(1, keepdims=True)  # noqa: E731
+    m2 = np.abs(mean(dy64 * n))
+    _within(dx, rx, U["f32"] * np.abs(rx) * 1.001 + 2 * SUM * np.abs(rx) + 1.01 * rstd * (
+        SUM * (2.0 ** -5 * gr + mean(gr) + 2 * np.abs(n) * mean(gr * np.abs(n))) + en * m2 + np.abs(n) * mean(gr * en)))
+    _within(dg, rg, (gr * (1.01 * en + SUM * np.abs(n))).sum(0))
+    _within(db, rb, SUM * gr.sum(0))
