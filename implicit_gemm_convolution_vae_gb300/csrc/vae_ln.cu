@@ -571,8 +571,9 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
             group_sums<2 * R>(sums, &red[2][group * wide * 2 * R], group, wide, part);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                // dx = rstd (g - mean(g) - n mean(g n)), n = rstd v
-                const float rstd = s[r], k1 = -rstd * sums[r] * inv_c, k2 = -rstd * rstd * rstd * sums[R + r] * inv_c;
+                // dx = rstd (g - mean(g) - n mean(g n)), n = rstd v; rstd^3 by itself would leave f32 for rows far from
+                // one (from about 2^42 and 2^-42 on), rstd times the sum over g v first stays near the size of g
+                const float rstd = s[r], k1 = -rstd * sums[r] * inv_c, k2 = -rstd * (rstd * (rstd * sums[R + r] * inv_c));
                 const float2 q = make_float2(rstd, rstd), q1 = make_float2(k1, k1), q2 = make_float2(k2, k2);
 #pragma unroll
                 for (int i = 0; i < NQ; ++i)

@@ -111,3 +111,26 @@ def test_layernorm_backward_without_eps(m, c):
         SUM * (2.0 ** -5 * gr + mean(gr) + 2 * np.abs(n) * mean(gr * np.abs(n))) + en * m2 + np.abs(n) * mean(gr * en)))
     _within(dg, rg, (gr * (1.01 * en + SUM * np.abs(n))).sum(0))
     _within(db, rb, SUM * gr.sum(0))
+
+
+@pytest.mark.parametrize("m,c", [(64, 256), (5001, 144), (4900, 1152), (20003, 35), (1400, 5120)])
+@pytest.mark.parametrize("log2", [-52, 52])
+def test_layernorm_of_values_far_from_one(m, c, log2):
+    """Rows 2^52 and 2^-52 large: the statistics' squares stay within f32, and so does everything formed
+    from them. The bounds are those of values near one, which scale with the rows."""
+    x, x64 = _draw(30, f"ln.far.{m}.{c}.{log2}", (m, c), "f32", 2.0 ** log2, 2.0 ** (log2 - 2))
+    dy, dy64 = _draw(30, f"ln.far.dy.{m}.{c}", (m, c), "f32")
+    g, g64 = _draw(30, f"ln.far.g.{c}", (c,), "f32", 0.2, 1.0)
+    n, rstd, en = _ln_terms(x64, 0.0)
+    ref = ot.layernorm(x64, g64, None, 0.0)
+    _within(vg.layernorm(x, g, eps=0.0), ref, 1.01 * np.abs(g64) * en + 8 * U["f32"] * np.abs(ref))
+    dx, dg, db = vg.layernorm_backward(dy, x, g, eps=0.0)
+    rx, rg, rb = ot.layernorm_backward(dy64, x64, g64, 0.0)
+    gr = np.abs(dy64 * g64)
+    mean = lambda a: a.mean(1, keepdims=True)  # noqa: E731
+    m2 = np.abs(mean(dy64 * g64 * n))
+    tol = U["f32"] * np.abs(rx) * 1.001 + 2 * SUM * np.abs(rx) + 1.01 * rstd * (
+        SUM * (2.0 ** -5 * gr + mean(gr) + 2 * np.abs(n) * mean(gr * np.abs(n))) + en * m2 + np.abs(n) * mean(gr * en))
+    _within(dx, rx, tol)
+    _within(dg, rg, (np.abs(dy64) * (1.01 * en + SUM * np.abs(n))).sum(0))
+    _within(db, rb, SUM * np.abs(dy64).sum(0))
