@@ -525,8 +525,11 @@ __global__ void __launch_bounds__(ring_warps(NQ, kBwd) * 32, 1) ln_ring_kernel(c
         }
         group_sums<R>(s, &red[1][group * wide * R], group, wide, part);
 #pragma unroll
-        for (int r = 0; r < R; ++r)  // (0 for the rows that the last chunk lacks: with eps 0 theirs would be infinite)
-            s[r] = r < rows ? 1.f / sqrtf(s[r] * inv_c + p.eps) : 0.f;
+        for (int r = 0; r < R; ++r) s[r] = 1.f / sqrtf(s[r] * inv_c + p.eps);
+        if (rows < R)  // (0 for the rows that the last chunk lacks: with eps 0 theirs would be infinite)
+#pragma unroll
+            for (int r = 1; r < R; ++r)
+                if (r >= rows) s[r] = 0.f;
         uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * c * (((kBwd ? p.xt : p.yt) == VAE_F32) ? 4 : 2);
         const size_t out_row = static_cast<size_t>(c) * (((kBwd ? p.xt : p.yt) == VAE_F32) ? 4 : 2);
         if constexpr (!kBwd) {
