@@ -40,8 +40,9 @@
 // step of 2^-8 or 2^-11 relative, as the forward's P. f16 would lose long rows'
 // P ~ 1/n below 2^-14, so it holds P 2^14 and dS c, with c the power of two
 // that brings 2 max|dO| max|V| (a bound on |dP - D| by Cauchy-Schwarz, from a
-// first kernel) to 2^14 .. 2^15; both factors leave in the epilogue. The
-// maximum is taken by an atomic maximum, which has no order. Up to 64 rows of a
+// first kernel) to 2^14 .. 2^15; both factors leave in the epilogue. Every
+// batch entry and key head has a c of its own: no gradient's digits hang on how
+// large another's are. The maximum is taken by an atomic maximum, which has no order. Up to 64 rows of a
 // head lie twice in their tile: the second copies' P and dS are what the first's
 // rounding left of them.
 #include <algorithm>
@@ -89,7 +90,7 @@ struct BwdParams {
     int nsplit_q, nsplit_k;
     int twice;                  // at most 64 rows to a head: each lies twice in its tile, P and dS in two parts
     float* side;                // [b][hkv][nsub][ntile][256]
-    const unsigned* maxima;     // f16: bits of max |dO|^2, max |V|^2
+    const unsigned* maxima;     // f16: [b][hkv] x bits of max |dO|^2, max |V|^2
     const void *q, *dout;
     MhaStrides qs, gs;
     void *dq, *dk, *dv;
@@ -99,7 +100,11 @@ struct BwdParams {
     unsigned long long timeout_ns;
 };
 
-// c of the file comment.
+// Where the maxima of entry e and key head hk lie.
+__host__ __device__ __forceinline__ size_t maxima_at(const MhaShape& s, int e, int hk) {
+    return 2 * (static_cast<size_t>(e) * s.hkv + hk);
+}
+// c of the file comment, from an entry's and key head's maxima.
 template <int T>
 __device__ __forceinline__ float ds_factor(const unsigned* maxima) {
     if constexpr (T == VAE_BF16) {
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(256) mha_prep_kernel(const PrepParams p) {
     const MhaShape& s = p.s;
     const int part = threadIdx.x & 15, r0 = threadIdx.x >> 4;
     float big = 0.f;
-    unsigned* maximum = p.maxima;
+    unsigned* maximum;
     if (static_cast<int>(blockIdx.x) < p.row_tiles) {
         int x = blockIdx.x;
         const int tile = x % s.ntile;
@@ -139,6 +144,7 @@ __global__ void __launch_bounds__(256) mha_prep_kernel(const PrepParams p) {
         const int sub = x % s.nsub;
         x /= s.nsub;
         const int hk = x % s.hkv, e = x / s.hkv;
+        maximum = p.maxima + maxima_at(s, e, hk);
         const int ql = mha_len(s.q_len, e, s.sq);
         const int gp = 1 << s.gp_log2;
         float* side = p.side + static_cast<long long>(blockIdx.x) * kSideFloats;
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(256) mha_prep_kernel(const PrepParams p) {
         x /= s.nkb;
         const int hk = x % s.hkv, e = x / s.hkv;
         const int kl = mha_len(s.k_len, e, s.sk);
-        maximum = p.maxima + 1;
+        maximum = p.maxima + maxima_at(s, e, hk) + 1;
 #pragma unroll 4
         for (int k = 0; k < kMhaTile / 16; ++k) {
             const int j = kb * kMhaTile + r0 + k * 16;
@@ -576,7 +582,7 @@ __device__ void kv_softmax(const BwdParams& p, const BwdSmem& s, const KvWork& w
     const int j = w.kb * kMhaTile + quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = lane_off + static_cast<uint32_t>(half * 64), tX = tS + 128u;
-    const float c = ds_factor<T>(p.maxima);
+    const float c = ds_factor<T>(p.maxima + maxima_at(sh, w.e, w.hk));
     const float f = T == VAE_F16 ? c * (1.f / (1 << kPLog2)) : 1.f;  // dS c = (P 2^14) (dP - D) f
     // the first row of the group's packing that sees key j
     long long see = 0;
@@ -868,7 +874,7 @@ __device__ void q_softmax(const BwdParams& p, const BwdSmem& s, const QWork& w, 
     float* side = p.side + (((static_cast<long long>(w.e) * sh.hkv + w.hk) * sh.nsub + w.sub) * sh.ntile + w.tile) * kSideFloats;
     const float nl = live ? side[rr] : -INFINITY;
     float D = live ? side[128 + rr] : 0.f;
-    const float c = ds_factor<T>(p.maxima);
+    const float c = ds_factor<T>(p.maxima + maxima_at(sh, w.e, w.hk));
     const float f = T == VAE_F16 ? c * (1.f / (1 << kPLog2)) : 1.f;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl);
     float2 D2 = make_float2(-D, -D), sum = make_float2(0.f, 0.f);
@@ -1074,7 +1080,8 @@ BwdPlan bwd_plan(const MhaShape& s) {
     f.part_kv = f.nsplit_k > 1 ? static_cast<size_t>(f.nsplit_k) * 2 * s.b * s.hkv * s.sk * s.d : 0;
     return f;
 }
-constexpr size_t kMaximaFloats = 64;  // two words used; keeps what follows aligned
+// Words for the maxima; whole 256 bytes keep what follows aligned.
+size_t maxima_floats(const MhaShape& s) { return (maxima_at(s, s.b, 0) + 63) / 64 * 64; }
 
 template <int T, int kSteps, bool kTwice>
 int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap (&map)[4], const PrepParams& pp,
@@ -1092,7 +1099,7 @@ int bwd_launch(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap 
             once.mark(dev);
         }
     }
-    if (T == VAE_F16) VAE_CUDA_CHECK(cudaMemsetAsync(pp.maxima, 0, 2 * sizeof(unsigned), st));
+    if (T == VAE_F16) VAE_CUDA_CHECK(cudaMemsetAsync(pp.maxima, 0, maxima_at(p.s, p.s.b, 0) * sizeof(unsigned), st));
     const long long prep = f.row_tiles + (T == VAE_F16 ? f.key_tiles : 0);
     VAE_CUDA_CHECK(launch_kernel(mha_prep_kernel<T>, dim3(static_cast<unsigned>(prep)), dim3(256), 0, st, pp));
     // (The query-tile kernel first: it may put its D into the side rows.)
@@ -1135,7 +1142,7 @@ int bwd_by_type(const vae_attention_desc* a, const BwdPlan& f, const CUtensorMap
 
 size_t mha_bwd_bytes(const MhaShape& s) {
     const BwdPlan f = bwd_plan(s);
-    return ((kMaximaFloats + f.side + f.part_q + f.part_kv) * sizeof(float) + 15) / 16 * 16;
+    return ((maxima_floats(s) + f.side + f.part_q + f.part_kv) * sizeof(float) + 15) / 16 * 16;
 }
 
 int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout, const void* q, const void* k,
@@ -1162,7 +1169,7 @@ int mha_bwd_run(const vae_attention_desc* a, const MhaShape& s, const void* dout
     pp.vs = mha_strides(a->v_stride);
     pp.lse = lse;
     pp.maxima = static_cast<unsigned*>(ws);
-    pp.side = w + kMaximaFloats;
+    pp.side = w + maxima_floats(s);
     pp.row_tiles = static_cast<int>(f.row_tiles);
     BwdParams p{};
     p.s = s;

@@ -437,7 +437,10 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
  * vae_attention_backward: with P = exp(scale q k^T - lse), D = sum(do * o),
  *   dv = P^T do, dS = P * (do v^T - D) * scale, dq = dS k, dk = dS^T q,
  *   summed over the query heads that share a key head; o and lse from
- *   vae_attention of the same inputs. P is recomputed; dk and dv are formed per
+ *   vae_attention of the same inputs. In f16 dS is held against the largest
+ *   |do| |v| of its batch entry and key head, to 2^-39 of it: rows of do more
+ *   than 2^9 below the largest of their head begin to lose digits over 16384
+ *   keys, shorter rows later. P is recomputed; dk and dv are formed per
  *   key tile and dq per query tile, in a fixed order: the same inputs give the
  *   same bits. dq rows from ql on and dk, dv rows from kl on are not written
  *   (with fill: 0).

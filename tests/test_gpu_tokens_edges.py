@@ -6,7 +6,7 @@ import pytest
 import implicit_gemm_convolution_vae_gb300 as vg
 from gpu_common import torch_mod
 from oracle import tokens as ot
-from test_gpu_tokens import SUM, U, _att_inputs, _draw, _ln_terms, _np, _within
+from test_gpu_tokens import FLOOR, SUM, U, _att_inputs, _draw, _ln_terms, _np, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,39 @@ def test_layernorm_of_values_far_from_one(m, c, log2):
     _within(dx, rx, tol)
     _within(dg, rg, (np.abs(dy64) * (1.01 * en + SUM * np.abs(n))).sum(0))
     _within(db, rb, SUM * np.abs(dy64).sum(0))
+
+
+# ───────────────────────────── gradients far apart ─────────────────────────────
+
+@pytest.mark.parametrize("case", [(2, 300, 333, 2, 2, 64, "f16", 0, None, None), (2, 20, 200, 4, 2, 64, "f16", 0, None, None)])
+@pytest.mark.parametrize("small", ["entry", "head"])
+def test_attention_backward_f16_sizes_apart(case, small):
+    """One entry's (or key head's) do and v 2^24 under the other's, in f16: its gradients keep their digits, as if it
+    were alone in the call. Bounds: those of a call of its own (the tiny term is relative to its own
+    largest |do| |v|); keys times eight put its dq over f16's smallest steps."""
+    (q, k, v, do), _, _, _ = _att_inputs(case)
+    k = (k.float() * 8).half()
+    q = (q.float() / 8).half()
+    g = case[3] // case[4]
+    big = (slice(0, 1), slice(None)) if small == "entry" else (slice(None), slice(0, 1))
+    tiny = (slice(1, 2), slice(None)) if small == "entry" else (slice(None), slice(1, 2))
+    wide = lambda s: slice(s.start * g, s.stop * g) if s.start is not None else s  # noqa: E731
+    for part, fd, fv in ((big, 2.0 ** 8, 2.0 ** 6), (tiny, 2.0 ** -8, 2.0 ** -2)):
+        do[part[0], :, wide(part[1])] *= fd
+        v[part[0], :, part[1]] *= fv
+    o, lse = vg.attention(q, k, v)
+    got = vg.attention_backward(do, q, k, v, o, lse)
+    vg.sync_status()
+    for part in (big, tiny):
+        rows = lambda a: _np(a[part[0], :, wide(part[1])])  # noqa: E731
+        keys = lambda a: _np(a[part[0], :, part[1]])  # noqa: E731
+        args = rows(do), rows(q), keys(k), keys(v)
+        ref = ot.attention_backward(*args)
+        tol = ot.attention_backward_bounds(*args, U["f16"], SUM, tiny=2.0 ** -38)
+        for a, r, e in zip((rows(got[0]), keys(got[1]), keys(got[2])), ref, tol):
+            e = 1.01 * e + U["f16"] * np.abs(r) * 1.001 + FLOOR["f16"]
+            # f16 ends at 65504, and from 65520 on (half a step of 32 further) a value rounds to infinity: some of the
+            # large part's dq lie there. An infinity of the right sign is right where the bound reaches that far.
+            over = np.isinf(a) & (np.sign(a) == np.sign(r)) & (np.abs(r) + e >= 65520.0)
+            assert part is big or not over.any()
+            _within(np.where(over, r, a), r, e)
