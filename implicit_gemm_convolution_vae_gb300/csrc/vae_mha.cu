@@ -4,8 +4,28 @@
 
 #include "vae_mha_bwd.h"
 #include "vae_mha_fwd.h"
+#include "vae_overlap.h"
 
 namespace vae {
+
+namespace {
+
+// A tensor of a call, for the check that what is written shares no memory with anything else.
+struct MhaPart {
+    const char* name;
+    Extent at;
+    bool written;
+};
+int mha_apart(const MhaPart* t, int count) {
+    for (int i = 0; i < count; ++i)
+        for (int j = 0; j < i; ++j)
+            if ((t[i].written || t[j].written) && extents_meet(t[i].at, t[j].at))
+                return set_error(VAE_ERR_ARG, "attention: %s may not overlap %s", t[i].name, t[j].name);
+    return VAE_OK;
+}
+Extent lens_extent(const int* lens, int b) { return extent_dense(lens, lens != nullptr ? static_cast<size_t>(b) * sizeof(int) : 0); }
+
+}  // namespace
 
 int mha_check(const vae_attention_desc* a, bool backward, MhaShape* s) {
     if (a == nullptr) return set_error(VAE_ERR_ARG, "attention: NULL desc");
@@ -37,6 +57,8 @@ int mha_check(const vae_attention_desc* a, bool backward, MhaShape* s) {
             if (dim[k] > 1 && (t[i].st[k] < (written ? a->d : 8) || t[i].st[k] % 8 != 0 || t[i].st[k] >= (1LL << 38)))
                 return set_error(VAE_ERR_SHAPE, "attention: %s's strides must be positive multiples of 8, and d at least where it is written "
                                  "(stride %d: %lld)", t[i].name, k, t[i].st[k]);
+        if (written && extent_folds(extent_tokens(nullptr, t[i].st, a->b, t[i].n, t[i].h, a->d, 2)))
+            return set_error(VAE_ERR_SHAPE, "attention: rows of %s lie in one another", t[i].name);
     }
     s->b = a->b;
     s->sq = a->sq;
@@ -100,6 +122,16 @@ int vae_attention(const vae_attention_desc* desc, const void* q_dev, const void*
     const size_t need = mha_fwd_bytes(s);
     if (need > 0 && (workspace_dev == nullptr || workspace_bytes < need))
         return set_error(VAE_ERR_NOMEM, "attention: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    const auto tokens = [&](const void* p, const long long* st, int n, int h) { return extent_tokens(p, st, s.b, n, h, s.d, 2); };
+    const MhaPart parts[] = {{"q", tokens(q_dev, desc->q_stride, s.sq, s.hq), false},
+                             {"k", tokens(k_dev, desc->k_stride, s.sk, s.hkv), false},
+                             {"v", tokens(v_dev, desc->v_stride, s.sk, s.hkv), false},
+                             {"q_len", lens_extent(s.q_len, s.b), false},
+                             {"k_len", lens_extent(s.k_len, s.b), false},
+                             {"o", tokens(o_dev, desc->o_stride, s.sq, s.hq), true},
+                             {"lse", extent_dense(lse_dev, static_cast<size_t>(s.b) * s.hq * s.sq * sizeof(float)), true},
+                             {"the workspace", extent_dense(workspace_dev, need), need > 0}};
+    if ((rc = mha_apart(parts, need > 0 ? 8 : 7)) != VAE_OK) return rc;
     if ((rc = check_device()) != VAE_OK) return rc;
     return mha_fwd_run(desc, s, q_dev, k_dev, v_dev, o_dev, lse_dev, workspace_dev,
                        reinterpret_cast<cudaStream_t>(stream));
@@ -129,8 +161,23 @@ int vae_attention_backward(const vae_attention_desc* desc, const void* do_dev, c
             return set_error(VAE_ERR_ARG, "attention: a gradient may not be written over an input");
     if (dq_dev == dk_dev || dq_dev == dv_dev || dk_dev == dv_dev)
         return set_error(VAE_ERR_ARG, "attention: dq, dk and dv must be tensors of their own");
-    if (workspace_bytes < mha_bwd_bytes(s))
-        return set_error(VAE_ERR_NOMEM, "attention: workspace of %zu bytes, %zu needed", workspace_bytes, mha_bwd_bytes(s));
+    const size_t need = mha_bwd_bytes(s);
+    if (workspace_bytes < need)
+        return set_error(VAE_ERR_NOMEM, "attention: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    const auto tokens = [&](const void* p, const long long* st, int n, int h) { return extent_tokens(p, st, s.b, n, h, s.d, 2); };
+    const MhaPart parts[] = {{"do", tokens(do_dev, desc->do_stride, s.sq, s.hq), false},
+                             {"q", tokens(q_dev, desc->q_stride, s.sq, s.hq), false},
+                             {"k", tokens(k_dev, desc->k_stride, s.sk, s.hkv), false},
+                             {"v", tokens(v_dev, desc->v_stride, s.sk, s.hkv), false},
+                             {"o", tokens(o_dev, desc->o_stride, s.sq, s.hq), false},
+                             {"lse", extent_dense(lse_dev, static_cast<size_t>(s.b) * s.hq * s.sq * sizeof(float)), false},
+                             {"q_len", lens_extent(s.q_len, s.b), false},
+                             {"k_len", lens_extent(s.k_len, s.b), false},
+                             {"dq", tokens(dq_dev, desc->dq_stride, s.sq, s.hq), true},
+                             {"dk", tokens(dk_dev, desc->dk_stride, s.sk, s.hkv), true},
+                             {"dv", tokens(dv_dev, desc->dv_stride, s.sk, s.hkv), true},
+                             {"the workspace", extent_dense(workspace_dev, need), true}};
+    if ((rc = mha_apart(parts, 12)) != VAE_OK) return rc;
     if ((rc = check_device()) != VAE_OK) return rc;
     return mha_bwd_run(desc, s, do_dev, q_dev, k_dev, v_dev, o_dev, lse_dev, dq_dev, dk_dev, dv_dev, workspace_dev,
                        reinterpret_cast<cudaStream_t>(stream));

@@ -447,8 +447,10 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
  * Requirements: b, sq, sk >= 1; hq % hkv == 0; d % 8 == 0, 8 <= d <= 128;
  * scale > 0 and finite; pointers 16-byte aligned; strides multiples of 8,
  * positive where the dimension is over 1, at least d in o, dq, dk and dv (a
- * broadcast is not taken: give k and v their hkv heads). What is written lies
- * apart from what is read, and dq, dk and dv from one another. b * hq * sq and b * hkv * sk at most 2^31 - 256.
+ * broadcast is not taken: give k and v their hkv heads). What is written, the
+ * workspace too, lies apart from what is read and from one another, and so do its
+ * rows; views that lie in one another without meeting (heads of one tensor) are
+ * taken, calls whose tensors meet refused. b * hq * sq and b * hkv * sk at most 2^31 - 256.
  * workspace_dev: vae_attention_workspace_bytes(desc) /
  * vae_attention_backward_workspace_bytes(desc) bytes, 16-byte aligned, contents
  * ignored on entry, NULL where that is 0. Both depend on the desc's sizes alone.
