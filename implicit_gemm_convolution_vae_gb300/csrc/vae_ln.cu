@@ -22,9 +22,11 @@
 // order is fixed, so the sums do not change from call to call.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
+#include "vae_overlap.h"
 #include "vae_types.cuh"
 
 namespace vae {
@@ -787,6 +789,20 @@ int ln_check(const void* x, int xt, int m, int c, float eps, const void* y, int 
     return VAE_OK;
 }
 
+// `what` is written over none of the rest.
+struct LnPart {
+    const char* name;
+    const void* p;
+    size_t bytes;
+};
+int ln_apart(const LnPart& what, std::initializer_list<LnPart> rest) {
+    if (what.p == nullptr) return VAE_OK;
+    for (const LnPart& r : rest)
+        if (r.p != nullptr && extents_meet(extent_dense(what.p, what.bytes), extent_dense(r.p, r.bytes)))
+            return set_error(VAE_ERR_ARG, "layer norm: %s may not overlap %s", what.name, r.name);
+    return VAE_OK;
+}
+
 }  // namespace
 }  // namespace vae
 
@@ -804,6 +820,10 @@ int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamm
     if (!ln_aligned(x_dev, type_size(x_type), c) || !ln_aligned(y_dev, type_size(y_type), c) ||
         !ln_aligned(gamma_dev, 4, c) || !ln_aligned(beta_dev, 4, c))
         return set_error(VAE_ERR_ALIGN, "layer norm: pointers must be 16-byte aligned (to their elements where c %% 8 != 0)");
+    const size_t n = static_cast<size_t>(m) * c, row = static_cast<size_t>(c) * sizeof(float);
+    if ((rc = ln_apart({"y", y_dev, n * type_size(y_type)}, {{"x", x_dev == y_dev ? nullptr : x_dev, n * type_size(x_type)},
+                                                             {"gamma", gamma_dev, row}, {"beta", beta_dev, row}})) != VAE_OK)
+        return rc;
     if ((rc = check_device()) != VAE_OK) return rc;
     LnRing r{};
     if (ln_ring_plan(m, c, x_type, x_type, false, aligned16(x_dev), &r)) {
@@ -851,6 +871,16 @@ int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, i
     if (sums && workspace_bytes < vae_layernorm_backward_workspace_bytes(m, c))
         return set_error(VAE_ERR_NOMEM, "layer norm: workspace of %zu bytes, %zu needed", workspace_bytes,
                          vae_layernorm_backward_workspace_bytes(m, c));
+    const size_t n = static_cast<size_t>(m) * c, row = static_cast<size_t>(c) * sizeof(float);
+    const LnPart x{"x", x_dev, n * type_size(x_type)}, dy{"dy", dy_dev, n * type_size(dy_type)}, dx{"dx", dx_dev, x.bytes};
+    const LnPart gamma{"gamma", gamma_dev, row}, dgamma{"dgamma", dgamma_dev, row}, dbeta{"dbeta", dbeta_dev, row};
+    const LnPart none{"", nullptr, 0};
+    // (dgamma and dbeta are written once x, dy and gamma have been read)
+    if ((rc = ln_apart(dx, {dx_dev == x_dev ? none : x, dx_dev == dy_dev ? none : dy, gamma, dgamma, dbeta})) != VAE_OK ||
+        (rc = ln_apart(dgamma, {dbeta})) != VAE_OK ||
+        (sums && (rc = ln_apart({"the workspace", workspace_dev, vae_layernorm_backward_workspace_bytes(m, c)},
+                                {x, dy, dx, gamma, dgamma, dbeta})) != VAE_OK))
+        return rc;
     if ((rc = check_device()) != VAE_OK) return rc;
     const LnPlan p = ln_plan(c, true);
     int grid = ln_bwd_grid(m, c);

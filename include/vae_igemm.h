@@ -358,7 +358,8 @@ enum { VAE_F32 = 0, VAE_F16 = 1, VAE_BF16 = 2 };
  *   (1 and 0).
  * Requirements: m >= 1, 1 <= c <= 16384, eps >= 0 and finite; pointers
  * 16-byte aligned, or where c % 8 != 0 aligned to their elements (those rows
- * move element by element).
+ * move element by element). y overlaps neither gamma, beta nor, unless it is x
+ * itself, x.
  */
 int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamma_dev, const float* beta_dev,
                   float eps, void* y_dev, int y_type, vae_stream_t stream);
@@ -374,7 +375,8 @@ int vae_layernorm(const void* x_dev, int x_type, int m, int c, const float* gamm
  *   workspace_dev of vae_layernorm_backward_workspace_bytes(m, c) bytes,
  *   16-byte aligned, contents ignored on entry; NULL is fine when dgamma_dev
  *   is NULL. The row sums are taken in a fixed order: the same inputs give the
- *   same bits.
+ *   same bits. dx may be x or dy (of one type) and overlaps nothing else; nor do
+ *   dgamma and dbeta one another, or the workspace anything.
  */
 size_t vae_layernorm_backward_workspace_bytes(int m, int c);
 int vae_layernorm_backward(const void* dy_dev, int dy_type, const void* x_dev, int x_type, int m, int c,

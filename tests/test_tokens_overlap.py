@@ -10,7 +10,7 @@ import pytest
 
 import implicit_gemm_convolution_vae_gb300 as vg
 from implicit_gemm_convolution_vae_gb300.build import CSRC, build
-from test_tokens_abi import BF16, FAKE, AttentionDesc
+from test_tokens_abi import BF16, F16, F32, FAKE, AttentionDesc
 
 X = FAKE * 16  # where the tensors lie
 NO_GPU = (-5, -7)  # the arguments were taken, and no device was found
@@ -117,6 +117,52 @@ def test_search_of_large_layouts(search):
     answers = search(pairs)
     assert [m for m, _ in answers] == [False, False, True, False, True, True, False, True, True]
     assert [f for _, f in answers] == [False] * 8 + [True]
+
+
+# ───────────────────────────── layer norm ─────────────────────────────
+
+M, C = 100, 64
+
+
+def test_layernorm_refuses_shared_memory(L):
+    nb = M * C * 4
+
+    def rc(y, x=X, g=X + 10 * nb, b=X + 11 * nb):
+        return L.vae_layernorm(x, F32, M, C, g, b, 1e-6, y, F32, None)
+
+    for y in (X + 16, X - 16, X + nb - 16, X - nb + 16, X + C * 4, X + 10 * nb, X + 10 * nb - nb + 16, X + 11 * nb + 16):
+        assert rc(y) == -1 and "overlap" in vg.last_error(), y
+    half = L.vae_layernorm(X, F32, M, C, None, None, 1e-6, X + 16, F16, None)
+    assert half == -1 and "overlap" in vg.last_error()
+
+
+def test_layernorm_takes_neighbours_and_in_place(L, no_gpu):
+    nb = M * C * 4
+    for y in (X, X + nb, X - nb, X + 10 * nb - nb, X + 11 * nb + C * 4):
+        assert L.vae_layernorm(X, F32, M, C, X + 10 * nb, X + 11 * nb, 1e-6, y, F32, None) in NO_GPU
+
+
+def _ln_backward(L, **kw):
+    nb, ws = M * C * 4, L.vae_layernorm_backward_workspace_bytes(M, C)
+    a = {**dict(dy=X, x=X + nb, g=X + 2 * nb, dx=X + 3 * nb, dg=X + 4 * nb, db=X + 5 * nb, w=X + 16 * nb), **kw}
+    return L.vae_layernorm_backward(a["dy"], F32, a["x"], F32, M, C, a["g"], 1e-6, a["dx"], a["dg"], a["db"], a["w"], ws, None)
+
+
+def test_layernorm_backward_refuses_shared_memory(L):
+    nb, ws = M * C * 4, L.vae_layernorm_backward_workspace_bytes(M, C)
+    bad = [dict(dx=X + 16), dict(dx=X + nb + 16), dict(dx=X + 2 * nb - 16), dict(dx=X + 2 * nb), dict(dg=X + 3 * nb),
+           dict(db=X + 4 * nb - 16), dict(dg=X + 5 * nb + 240), dict(db=X + 4 * nb), dict(w=X + 3 * nb + 32), dict(w=X - ws + 16),
+           dict(w=X + 4 * nb), dict(w=X + 5 * nb - ws + 16), dict(w=X + 2 * nb + 128), dict(w=X + nb)]
+    for kw in bad:
+        assert _ln_backward(L, **kw) == -1 and "overlap" in vg.last_error(), kw
+
+
+def test_layernorm_backward_takes_neighbours_and_in_place(L, no_gpu):
+    nb, ws = M * C * 4, L.vae_layernorm_backward_workspace_bytes(M, C)
+    good = [{}, dict(dx=X), dict(dx=X + nb), dict(w=X - ws), dict(dg=X + 4 * nb, db=X + 4 * nb + C * 4), dict(dg=X + 2 * nb),
+            dict(dy=X, x=X), dict(dx=X, x=X), dict(dg=None, db=None, w=None)]
+    for kw in good:
+        assert _ln_backward(L, **kw) in NO_GPU, (kw, vg.last_error())
 
 
 # ───────────────────────────── attention ─────────────────────────────
