@@ -16,6 +16,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "vae_overlap.h"
 #include "vae_types.cuh"
 
 namespace vae {
@@ -262,6 +263,12 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
     if (reinterpret_cast<uintptr_t>(x_dev) % es || reinterpret_cast<uintptr_t>(y_dev) % es ||
         reinterpret_cast<uintptr_t>(pos_dev) % 4)
         return set_error(VAE_ERR_ALIGN, "rope: a pointer is not aligned to its elements");
+    const Extent y_at = extent_tokens(y_dev, y_stride, b, s, h, d, es);
+    if (extent_folds(y_at)) return set_error(VAE_ERR_SHAPE, "rope: rows of y lie in one another");
+    if (x_dev != y_dev && extents_meet(extent_tokens(x_dev, x_stride, b, s, h, d, es), y_at))
+        return set_error(VAE_ERR_ARG, "rope: y may not overlap x (but may be x)");
+    if (extents_meet(extent_dense(pos_dev, static_cast<size_t>(pos_batch) * s * plan->naxes * 4), y_at))
+        return set_error(VAE_ERR_ARG, "rope: y may not overlap the positions");
     int rc = check_device();
     if (rc != VAE_OK) return rc;
     RopeParams p{};

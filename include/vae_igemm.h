@@ -413,7 +413,8 @@ int vae_rope_plan_init(vae_rope_plan* plan, int naxes, const int* dims, double t
  *   pos_dev [pos_batch][s][naxes], f32 or int32 (pos_int != 0), pos_batch = 1
  *   (shared by the batch) or b.
  * Requirements: b, s, h >= 1, b * s <= 2^31 - 256, h < 2^20, 2 * plan pairs <= d
- * <= 256, strides >= 0 (y's > 0 where the dimension is over 1).
+ * <= 256, strides >= 0; y's > 0 where the dimension is over 1, no two of its rows
+ * over one another, and none over the positions.
  */
 int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long long x_stride[3],
              const void* pos_dev, int pos_int, int pos_batch, const vae_rope_plan* plan, int inverse,

@@ -10,7 +10,7 @@ import pytest
 
 import implicit_gemm_convolution_vae_gb300 as vg
 from implicit_gemm_convolution_vae_gb300.build import CSRC, build
-from test_tokens_abi import BF16, F16, F32, FAKE, AttentionDesc
+from test_tokens_abi import BF16, F16, F32, FAKE, AttentionDesc, _plan
 
 X = FAKE * 16  # where the tensors lie
 NO_GPU = (-5, -7)  # the arguments were taken, and no device was found
@@ -163,6 +163,34 @@ def test_layernorm_backward_takes_neighbours_and_in_place(L, no_gpu):
             dict(dy=X, x=X), dict(dx=X, x=X), dict(dg=None, db=None, w=None)]
     for kw in good:
         assert _ln_backward(L, **kw) in NO_GPU, (kw, vg.last_error())
+
+
+# ───────────────────────────── rotary positions ─────────────────────────────
+
+def _rope(L, x, xs, y, ys, pos=X * 8, b=2, s=5, h=3, d=64):
+    st = lambda v: (ctypes.c_longlong * 3)(*v)  # noqa: E731
+    return L.vae_rope(x, F16, b, s, h, d, st(xs), pos, 0, 1, ctypes.byref(_plan(L)[1]), 0, y, st(ys), None)
+
+
+ROW = (5 * 8 * 64, 8 * 64, 64)  # heads 0 .. 2 of eight
+
+
+def test_rope_refuses_shared_memory(L):
+    for y, ys in ((X + 2, ROW), (X - 2, ROW), (X + 2 * 128, ROW), (X + 2 * 8 * 64, ROW), (X, (ROW[0], ROW[1], 128)),
+                  (X + 2 * 64, (960, 192, 64))):
+        assert _rope(L, X, ROW, y, ys) == -1, (y, ys)
+    assert _rope(L, X, ROW, X * 8 + 32, ROW) == -1 and "overlap" in vg.last_error()
+    # rows of y in one another
+    for ys in ((960, 192, 32), (960, 64, 64), (192, 192, 64), (960, 100, 64)):
+        assert _rope(L, X, ROW, X * 2, ys) == -2 and "row" in vg.last_error(), ys
+
+
+def test_rope_takes_parts_of_a_projection_and_broadcasts(L, no_gpu):
+    assert _rope(L, X, ROW, X, ROW) in NO_GPU
+    for k in (3, 4, 5):  # the heads behind
+        assert _rope(L, X, ROW, X + 2 * 64 * k, ROW) in NO_GPU
+    assert _rope(L, X, (0, 192, 64), X * 2, (960, 192, 64)) in NO_GPU
+    assert _rope(L, X, ROW, X * 2, (64, 128, 640)) in NO_GPU  # batch inside tokens inside heads
 
 
 # ───────────────────────────── attention ─────────────────────────────
