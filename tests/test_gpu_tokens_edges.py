@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import implicit_gemm_convolution_vae_gb300 as vg
+import test_gpu_tokens as base
 from gpu_common import torch_mod
 from oracle import tokens as ot
 from test_gpu_tokens import FLOOR, SUM, U, _att_inputs, _draw, _ln_terms, _np, _within
@@ -170,3 +171,27 @@ def test_attention_backward_f16_sizes_apart(case, small):
             over = np.isinf(a) & (np.sign(a) == np.sign(r)) & (np.abs(r) + e >= 65520.0)
             assert part is big or not over.any()
             _within(np.where(over, r, a), r, e)
+
+
+# ───────────────────────────── shapes ─────────────────────────────
+
+SHAPES = [
+    # more entries than a warp has lanes, the keys over CTAs; lengths of 0 and 1 among them
+    (40, 1, 700, 4, 1, 64, "bf16", 0, None, [(e * 97) % 701 for e in range(40)]),
+    (33, 2, 1500, 1, 1, 128, "f16", 1, None, [0] * 5 + [1500, 1] + [1500 - 40 * e for e in range(26)]),
+    (70, 1, 300, 2, 1, 40, "f16", 0, None, None),
+    # groups of 3, 5, 6, 7 and 15 heads to a key head, keys over CTAs and not
+    (2, 1, 3000, 12, 4, 128, "bf16", 0, None, [3000, 1111]), (2, 1, 2000, 5, 1, 64, "f16", 0, None, None),
+    (1, 2, 1500, 14, 2, 96, "bf16", 5, None, None), (2, 3, 900, 12, 2, 64, "f16", 0, None, [900, 1]),
+    (1, 1, 200, 15, 1, 72, "f16", 0, None, None), (1, 150, 150, 7, 1, 64, "bf16", 32, None, None),
+]
+
+
+@pytest.mark.parametrize("case", SHAPES)
+def test_attention_many_entries_and_odd_groups(case):
+    base.test_attention(case)
+
+
+@pytest.mark.parametrize("case", SHAPES)
+def test_attention_backward_many_entries_and_odd_groups(case):
+    base.test_attention_backward(case)
