@@ -737,10 +737,11 @@ __device__ __forceinline__ QWork q_work(const BwdParams& p) {
     if (i1 >= w.ql) i1 = w.ql - 1;
     const int lim = i0 < w.ql ? mha_key_limit(i1, w.ql, w.kl, s.block) : 0;
     const int all = (lim + kMhaTile - 1) / kMhaTile;
-    const int per = (all + p.nsplit_q - 1) / p.nsplit_q;
+    // (few key tiles are one split's: it forms D over all of them)
+    w.exact = all <= kExactTiles;
+    const int per = w.exact ? all : (all + p.nsplit_q - 1) / p.nsplit_q;
     w.kb0 = w.split * per < all ? w.split * per : all;
     w.n = (w.kb0 + per < all ? w.kb0 + per : all) - w.kb0;
-    w.exact = p.nsplit_q == 1 && w.n <= kExactTiles;
     return w;
 }
 

@@ -121,10 +121,12 @@ def attention_backward(do, q, k, v, scale=None, q_len=None, k_len=None, block: i
     return dq, dk, dv
 
 
-def attention_backward_bounds(do, q, k, v, u, c, scale=None, q_len=None, k_len=None, block: int = 0, tiny=0.0):
+def attention_backward_bounds(do, q, k, v, u, c, scale=None, q_len=None, k_len=None, block: int = 0, tiny=0.0,
+                              exact_d: bool = False):
     """How far (dq, dk, dv) may be off, element by element, when probabilities and dS are rounded by u
     relative (and ``tiny`` absolute, times the largest |do| |v|), o carries 2 u of sum p |v|, and every
-    sum in f32 carries c of its absolute values; without the outputs' own rounding."""
+    sum in f32 carries c of its absolute values; without the outputs' own rounding. exact_d: rowsum(p dp)
+    is formed from p and dp in f32 and not from the rounded o."""
     scale = 1.0 / np.sqrt(q.shape[-1]) if scale is None else scale
     hq = q.shape[2]
     g = hq // k.shape[2]
@@ -142,7 +144,9 @@ def attention_backward_bounds(do, q, k, v, u, c, scale=None, q_len=None, k_len=N
             x = np.abs(qq) @ np.abs(kk).T * scale
             ep = c * (1.0 + x + np.where(np.isinf(lse), 0.0, np.abs(lse))[:, None])  # of p, relative: exp of an f32 argument
             edp = c * (ad @ av.T)
-            eD = 2.0 * u * (ad * (p @ av)).sum(1, keepdims=True) + c * (ad * (p @ av)).sum(1, keepdims=True)
+            eD = (0.0 if exact_d else 2.0 * u) * (ad * (p @ av)).sum(1, keepdims=True) + c * (ad * (p @ av)).sum(1, keepdims=True)
+            if exact_d:
+                eD = eD + (p * (edp + ep * np.abs(dp))).sum(1, keepdims=True)
             ds = np.abs(p * (dp - D))
             eds = (u + 2 * c) * ds + p * (edp + eD + ep * np.abs(dp - D))
             eds = np.where(m, eds + tiny * norm(do) * norm(v), 0.0)

@@ -195,3 +195,28 @@ def test_attention_many_entries_and_odd_groups(case):
 @pytest.mark.parametrize("case", SHAPES)
 def test_attention_backward_many_entries_and_odd_groups(case):
     base.test_attention_backward(case)
+
+
+# ───────────────────────────── rows of few keys ─────────────────────────────
+
+@pytest.mark.parametrize("case", [(1, 1024, 1024, 8, 8, 64, "bf16", 1, None, None), (1, 1000, 1000, 2, 1, 40, "f16", 1, None, None),
+                                  (3, 200, 1024, 2, 2, 128, "bf16", 0, None, [1024, 256, 129])])
+def test_attention_backward_rows_of_few_keys(case):
+    """Rows whose tile of 128 rows meets at most 256 keys take D from p and dp, whether or not the other rows' keys are
+    split over CTAs: where p and dp leave little of dS, D from the rounded output would show."""
+    b, sq, sk, hq, hkv, d, t, block, _, k_len = case
+    (q, k, v, do), (q64, k64, v64, do64), kw, okw = _att_inputs(case)
+    o, lse = vg.attention(q, k, v, **kw)
+    dq, _, _ = vg.attention_backward(do, q, k, v, o, lse, **kw)
+    vg.sync_status()
+    ref = ot.attention_backward(do64, q64, k64, v64, **okw)[0]
+    tol = ot.attention_backward_bounds(do64, q64, k64, v64, U[t], SUM, tiny=2.0 ** -38 if t == "f16" else 2.0 ** -100,
+                                       exact_d=True, **okw)[0]
+    tol = 1.01 * tol + U[t] * np.abs(ref) * 1.001 + FLOOR[t]
+    got = _np(dq)
+    kl = [sk] * b if k_len is None else k_len
+    for e in range(b):
+        if block == 0 and kl[e] > 256:
+            continue
+        rows = sq if block == 0 else 256 // (hq // hkv)  # (causal from position 0, heads of a group side by side)
+        _within(got[e, :rows], ref[e, :rows], tol[e, :rows])
