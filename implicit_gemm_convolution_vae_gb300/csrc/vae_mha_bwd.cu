@@ -22,19 +22,21 @@
 // MMAs with both operands in shared memory ran at 90 cycles each, bound by the
 // 8 KB that each reads there, those with one in TMEM at 57 to 64.
 //
-// Both kernels read 64 KB of tiles per step, and L2 gives every SM 26 to 29 bytes
-// a cycle (measured): 2280 to 2510 cycles of each step's time are the tiles' way.
+// Both kernels read 64 KB of tiles per step of 128 channels, and L2 gives every SM
+// 26 to 29 bytes a cycle (measured): the loads alone take 2280 to 2510 cycles.
 //
 // D = rowsum(dO * O) takes O as the forward rounded it. Rows that meet few keys
 // (kExactTiles tiles at most) feel that rounding in dS: the query-tile kernel
 // first runs over their keys once for D = rowsum(P * dP) itself, and hands it
-// to the key-tile kernel after it.
+// to the key-tile kernel after it. Over more keys the rounded O costs dq 1.44 to
+// 1.46 times its own rounding at 96 and 128 channels instead of the 1.41 that one
+// rounding of dS costs, up to 1.55 at 40 and 2.0 at 8; the pass over all keys would
+// take two products more of seven.
 //
-// Measured on GB300: 16384 tokens x 9 heads x 128 in f16 2650 to 2900 us (1070 to
-// 1170 TFLOP/s of the five products' flops). A step takes 2590 cycles in the
-// query-tile kernel (2090 with no hand-over between warps, 1536 at the tensor
-// rate) and 3390 in the key-tile kernel (2600, 2048): bound by the MMAs under
-// shared-memory bandwidth, then by the hand-overs.
+// Measured on GB300: 16384 tokens x 9 heads x 128 in f16 2800 to 2980 us (1040 to
+// 1100 TFLOP/s of the five products' flops). A step takes 2520 cycles in the
+// query-tile kernel, as long as its loads (1536 at the tensor rate), and 3480 in
+// the key-tile kernel (2600 with no hand-over between warps, 2048 at the tensor rate).
 //
 // 16 bits. P and dS are rounded to the tensors' type for the products, half a
 // step of 2^-8 or 2^-11 relative, as the forward's P. f16 would lose long rows'
