@@ -500,6 +500,15 @@ def _given(**tensors):
             raise VaeError(-1, f"{name} is needed")
 
 
+_INT = (1 << 31) - 1  # the C ABI's sizes; ctypes would cut a larger one off without a word
+
+
+def _sizes(**sizes):
+    for name, n in sizes.items():
+        if n > _INT:
+            raise VaeError(-2, f"{name} must be below 2^31, got {n}")
+
+
 def _tensor(t, name, dtype, shape):
     """Checks a tensor's type, shape and that it is contiguous."""
     if t.dtype is dtype and t.shape == shape and t.is_contiguous():
@@ -534,6 +543,8 @@ def _layernorm(x, gamma, beta, eps, out_dtype, out, stream):
         raise VaeError(-2, f"x must have 2 dims, got {x.dim()}")
     shape = x.shape
     m, c = shape
+    if m > _INT or c > _INT:
+        _sizes(m=m, c=c)
     _tensor(x, "x", x.dtype, shape)
     if gamma is not None:
         _tensor(gamma, "gamma", _T.f32, (c,))
@@ -549,6 +560,7 @@ def _layernorm(x, gamma, beta, eps, out_dtype, out, stream):
 
 
 def layernorm_backward_workspace_bytes(m: int, c: int) -> int:
+    _sizes(m=m, c=c)
     return int(lib().vae_layernorm_backward_workspace_bytes(m, c))
 
 
@@ -568,6 +580,8 @@ def _layernorm_backward(dy, x, gamma, eps, weight_grads, dx, dgamma, dbeta, work
         raise VaeError(-2, f"x must have 2 dims, got {x.dim()}")
     shape = x.shape
     m, c = shape
+    if m > _INT or c > _INT:
+        _sizes(m=m, c=c)
     _tensor(x, "x", x.dtype, shape)
     _tensor(dy, "dy", dy.dtype, shape)
     if gamma is not None:
@@ -607,6 +621,7 @@ class RopePlan:
 
     def __init__(self, axes, theta: float = 10000.0, interleaved: bool = True):
         self.axes = tuple(int(a) for a in axes)
+        _sizes(axes=max((abs(a) for a in self.axes), default=0))
         self._plan = _RopePlan()
         dims = (_I * max(1, len(self.axes)))(*self.axes)
         _check(lib().vae_rope_plan_init(ctypes.byref(self._plan), len(self.axes), dims, float(theta),
@@ -640,6 +655,8 @@ def _rope(x, positions, plan, inverse, out, stream):
         raise VaeError(-2, f"x must have 4 dims, got {x.dim()}")
     shape = x.shape
     b, s, h, d = shape
+    if b > _INT or s > _INT or h > _INT or d > _INT:
+        _sizes(b=b, s=s, h=h, d=d)
     ints = positions.dtype == _T.i32
     if not ints and positions.dtype != _T.f32:
         raise VaeError(-1, f"positions must be float32 or int32, got {positions.dtype}")
@@ -674,6 +691,8 @@ def _attention_args(q, k, v, scale, q_len, k_len, block, fill):
     b, sq, hq, d = q.shape
     kshape = k.shape
     _, sk, hkv, _ = kshape
+    if b > _INT or sq > _INT or sk > _INT or hq > _INT or hkv > _INT or d > _INT:
+        _sizes(b=b, sq=sq, sk=sk, hq=hq, hkv=hkv, d=d)
     if kshape[0] != b or kshape[3] != d:
         raise VaeError(-2, f"k must be {(b, sk, hkv, d)}, got {tuple(kshape)}")
     if v.shape != kshape:
@@ -706,6 +725,7 @@ def _dense(n, h, d):
 
 
 def attention_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
+    _sizes(b=b, sq=sq, sk=sk, hq=hq, hkv=hkv, d=d, block=block)
     q, k = _dense(sq, hq, d), _dense(sk, hkv, d)
     return int(lib().vae_attention_workspace_bytes(_DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, 0, *q, *k, *k, *q,
                                                               *_NO_STRIDES)))
@@ -748,6 +768,7 @@ def _attention(q, k, v, scale, q_len, k_len, block, out, lse, workspace, stream)
 
 
 def attention_backward_workspace_bytes(b: int, sq: int, sk: int, hq: int, hkv: int, d: int, block: int = 0) -> int:
+    _sizes(b=b, sq=sq, sk=sk, hq=hq, hkv=hkv, d=d, block=block)
     q, k = _dense(sq, hq, d), _dense(sk, hkv, d)
     return int(lib().vae_attention_backward_workspace_bytes(
         _DESC.pack(1, b, sq, sk, hq, hkv, d, 1.0, block, 0, 0, 0, *q, *k, *k, *q, *q, *q, *k, *k)))
