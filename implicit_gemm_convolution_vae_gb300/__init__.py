@@ -26,6 +26,7 @@ __all__ = [
     "conv1x1", "rmsnorm_silu", "groupnorm_silu",
     "groupnorm_workspace_bytes", "cast_f16", "mid_attention", "mid_attention_workspace_bytes",
     "layernorm", "layernorm_backward", "layernorm_backward_workspace_bytes", "RopePlan", "rope",
+    "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_bytes",
     "attention", "attention_workspace_bytes", "attention_backward", "attention_backward_workspace_bytes",
     "Decoder", "DecodeGraph", "pack_conv3x3", "pack_conv1x1",
     "UPSAMPLE2X", "PAD_REPLICATE", "PAD_REFLECT", "DOWNSAMPLE2X", "EPI_SILU", "OUT_F16", "FAMILY_GN", "FAMILY_RMS",
@@ -81,6 +82,9 @@ SIGNATURES = {
     "vae_layernorm_backward": ([_P, _I, _P, _I, _I, _I, _P, _F, _P, _P, _P, _P, _SZ, _P], _I),
     "vae_rope_plan_init": ([_P, _I, _P, ctypes.c_double, _I], _I),
     "vae_rope": ([_P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P], _I),
+    "vae_qk_norm_rope": ([_P] * 9 + [_P], _I),
+    "vae_qk_norm_rope_backward_workspace_bytes": ([_P], _SZ),
+    "vae_qk_norm_rope_backward": ([_P] * 14 + [_SZ, _P], _I),
     "vae_attention_workspace_bytes": ([_P], _SZ),
     "vae_attention": ([_P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
     "vae_attention_backward_workspace_bytes": ([_P], _SZ),
@@ -806,6 +810,120 @@ def _attention_backward(do, q, k, v, o, lse, scale, q_len, k_len, block, dq, dk,
                                     lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *_work(workspace),
                                     stream))
     return dq, dk, dv
+
+
+# struct vae_qk_norm_rope_desc: type .. d, eps, pos_int, pos_batch, six times three strides
+_QK_DESC = struct.Struct("=6if2i4x18q")
+
+
+def _qk_desc(q, k, gamma_q, gamma_k, positions, plan, eps, q_out, k_out, dq_out=None, dk_out=None):
+    """The desc of the call (with new outputs where q_out, k_out are None) and the outputs; checks the tensors."""
+    dtype = q.dtype
+    code = _type(dtype, "q")
+    if k.dtype != dtype:
+        raise VaeError(-1, f"k must be {dtype}, got {k.dtype}")
+    if q.dim() != 4 or k.dim() != 4:
+        raise VaeError(-2, f"q and k must have 4 dims, got {q.dim()} and {k.dim()}")
+    b, s, hq, d = q.shape
+    hk = k.shape[2]
+    if b > _INT or s > _INT or hq > _INT or hk > _INT or d > _INT:
+        _sizes(b=b, s=s, hq=hq, hk=hk, d=d)
+    if k.shape != (b, s, hk, d):
+        raise VaeError(-2, f"k must be {(b, s, hk, d)}, got {tuple(k.shape)}")
+    if gamma_q is not None:
+        _tensor(gamma_q, "gamma_q", _T.f32, (d,))
+    if gamma_k is not None:
+        _tensor(gamma_k, "gamma_k", _T.f32, (d,))
+    if (positions is None) != (plan is None):
+        raise VaeError(-1, "positions and plan come together")
+    ints, pb = False, 1
+    if positions is not None:
+        ints = positions.dtype == _T.i32
+        if not ints and positions.dtype != _T.f32:
+            raise VaeError(-1, f"positions must be float32 or int32, got {positions.dtype}")
+        pb = positions.shape[0] if positions.dim() == 3 else 1
+        na = len(plan.axes)
+        _tensor(positions, "positions", positions.dtype, (pb, s, na) if positions.dim() == 3 else (s, na))
+    if q_out is None:
+        q_out = _T.empty(q.shape, dtype=dtype, device=q.device)
+    else:
+        _like(q_out, q, "q's output", None)
+    if k_out is None:
+        k_out = _T.empty(k.shape, dtype=dtype, device=q.device)
+    else:
+        _like(k_out, k, "k's output", None)
+    more = _NO_STRIDES[:6]
+    if dq_out is not None:
+        _like(dq_out, q, "dq_out", None)
+        _like(dk_out, k, "dk_out", None)
+        more = (*_strides3(dq_out, "dq_out"), *_strides3(dk_out, "dk_out"))
+    return _QK_DESC.pack(code, b, s, hq, hk, d, eps, ints, pb, *_strides3(q, "q"), *_strides3(k, "k"),
+                         *_strides3(q_out, "q's output"), *_strides3(k_out, "k's output"), *more), q_out, k_out
+
+
+def qk_norm_rope(q, k, gamma_q=None, gamma_k=None, positions=None, plan: Optional[RopePlan] = None, eps: float = 1e-6,
+                 q_out=None, k_out=None, stream=None):
+    """The RMS norm of every head of q [b][s][hq][d] and k [b][s][hk][d] (one type, strides free, channels
+    contiguous) with the weights gamma_q, gamma_k f32 [d], then the rotary positions of ``rope`` (or, without
+    positions and plan, the norm alone), in one pass. Returns (q, k); the outputs may be the inputs, or k's
+    places in a cache."""
+    if q is None or k is None:
+        _given(q=q, k=k)
+    index = _device_of((("q", q), ("k", k), ("gamma_q", gamma_q), ("gamma_k", gamma_k), ("positions", positions),
+                        ("q_out", q_out), ("k_out", k_out)))
+    return _call(index, stream, _qk_norm_rope, q, k, gamma_q, gamma_k, positions, plan, eps, q_out, k_out)
+
+
+def _qk_norm_rope(q, k, gamma_q, gamma_k, positions, plan, eps, q_out, k_out, stream):
+    desc, q_out, k_out = _qk_desc(q, k, gamma_q, gamma_k, positions, plan, eps, q_out, k_out)
+    _check(lib().vae_qk_norm_rope(desc, q.data_ptr(), k.data_ptr(), _ptr(gamma_q), _ptr(gamma_k), _ptr(positions),
+                                  None if plan is None else plan._at, q_out.data_ptr(), k_out.data_ptr(), stream))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward_workspace_bytes(b: int, s: int, hq: int, hk: int, d: int) -> int:
+    _sizes(b=b, s=s, hq=hq, hk=hk, d=d)
+    q, k = _dense(s, hq, d), _dense(s, hk, d)
+    return int(lib().vae_qk_norm_rope_backward_workspace_bytes(_QK_DESC.pack(1, b, s, hq, hk, d, 1.0, 0, 1, *q, *k, *q, *k, *q, *k)))
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q=None, gamma_k=None, positions=None,
+                          plan: Optional[RopePlan] = None, eps: float = 1e-6, weight_grads: bool = True, dq=None,
+                          dk=None, dgamma_q=None, dgamma_k=None, workspace=None, stream=None):
+    """The gradient of qk_norm_rope at q, k for dq_out, dk_out of their shapes: (dq, dk, dgamma_q, dgamma_k f32 [d]);
+    with ``weight_grads`` False the last two are None and not computed. dq may be dq_out or q, dk likewise."""
+    if dq_out is None or dk_out is None or q is None or k is None:
+        _given(dq_out=dq_out, dk_out=dk_out, q=q, k=k)
+    index = _device_of((("dq_out", dq_out), ("dk_out", dk_out), ("q", q), ("k", k), ("gamma_q", gamma_q),
+                        ("gamma_k", gamma_k), ("positions", positions), ("dq", dq), ("dk", dk), ("dgamma_q", dgamma_q),
+                        ("dgamma_k", dgamma_k), ("workspace", workspace)))
+    return _call(index, stream, _qk_norm_rope_backward, dq_out, dk_out, q, k, gamma_q, gamma_k, positions, plan, eps,
+                 weight_grads, dq, dk, dgamma_q, dgamma_k, workspace)
+
+
+def _qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, positions, plan, eps, weight_grads, dq, dk, dgamma_q,
+                           dgamma_k, workspace, stream):
+    desc, dq, dk = _qk_desc(q, k, gamma_q, gamma_k, positions, plan, eps, dq, dk, dq_out, dk_out)
+    L = lib()
+    if weight_grads:
+        d = q.shape[3]
+        if dgamma_q is None:
+            dgamma_q = _T.empty((d,), dtype=_T.f32, device=q.device)
+        else:
+            _tensor(dgamma_q, "dgamma_q", _T.f32, (d,))
+        if dgamma_k is None:
+            dgamma_k = _T.empty((d,), dtype=_T.f32, device=q.device)
+        else:
+            _tensor(dgamma_k, "dgamma_k", _T.f32, (d,))
+        if workspace is None:
+            workspace = _T.empty(max(L.vae_qk_norm_rope_backward_workspace_bytes(desc), 16), dtype=_T.u8, device=q.device)
+    elif dgamma_q is not None or dgamma_k is not None:
+        raise VaeError(-1, "dgamma_q and dgamma_k need weight_grads")
+    _check(L.vae_qk_norm_rope_backward(desc, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                       _ptr(gamma_q), _ptr(gamma_k), _ptr(positions), None if plan is None else plan._at,
+                                       dq.data_ptr(), dk.data_ptr(), _ptr(dgamma_q), _ptr(dgamma_k), *_work(workspace),
+                                       stream))
+    return dq, dk, dgamma_q, dgamma_k
 
 
 # ───────────────────────────── weight layouts ─────────────────────────────

@@ -1,0 +1,405 @@
+// The norm of query and key heads with their rotary positions, and its gradient
+// (public entry points at the end).
+//
+// A row is one head of one token, d channels: n = x (mean x^2 + eps)^-1/2,
+// y = R (n gamma). Backward, with u = R^T dy and v = u gamma: dx = r (v - n mean(v n)),
+// r the root, and dgamma = the sum of u n over the rows. A block takes some tokens,
+// forms the (cos, sin) of their pairs once in shared memory and works on every
+// query and key head of them: one read of each input and one write of each output,
+// which bounds the call.
+#include <algorithm>
+#include <cmath>
+
+#include "vae_overlap.h"
+#include "vae_rope.cuh"
+#include "vae_types.cuh"
+
+namespace vae {
+
+namespace {
+
+constexpr int kQkMaxD = 256;
+constexpr int kQkTokens = 8;     // tokens a block takes at a time, at most
+constexpr int kQkThreads = 128;
+constexpr int kQkWarps = kQkThreads / 32;
+constexpr int kQkBlocks = 608;   // of the gradient, at most: each leaves a row of partial sums for dgamma
+constexpr int kQkPitch = VAE_ROPE_MAX_PAIRS + 2;
+
+struct QkPart {  // queries or keys
+    const void *x, *dy;
+    void* y;
+    const float* gamma;
+    float* dgamma;
+    long long xs[3], gs[3], ys[3];
+    int h;
+};
+struct QkParams {
+    QkPart part[2];
+    const void* pos;
+    int tokens, s, d, tpb;
+    int pos_int, pos_batch;
+    float eps;
+    float* sums;  // [2][blocks][d]: each block's part of dgamma
+};
+
+__device__ __forceinline__ float qk_pos(const QkParams& p, const vae_rope_plan& plan, int token, int pair) {
+    const long long row = p.pos_batch > 1 ? token : token % p.s;
+    const long long i = row * plan.naxes + plan.axis[pair];
+    return p.pos_int ? static_cast<float>(static_cast<const int*>(p.pos)[i]) : static_cast<const float*>(p.pos)[i];
+}
+
+__device__ __forceinline__ long long qk_offset(const QkParams& p, int token, int head, const long long (&st)[3]) {
+    const int e = token / p.s;
+    return e * st[0] + (token - e * p.s) * st[1] + head * st[2];
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Any d and any strides: a warp takes a row, channel by channel.
+template <int T, bool kBack>
+__global__ void __launch_bounds__(kQkThreads) qk_plain_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan) {
+    using E = typename Elem<T>::type;
+    constexpr int kEach = kQkMaxD / 32;
+    __shared__ float2 cs[kQkTokens][kQkPitch];
+    __shared__ float row[kQkWarps][kQkMaxD];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pairs = plan.pairs, rot = 2 * pairs;
+    float acc[2][kEach] = {};
+    pdl_wait();
+    // the place of channel c's partner, and its pair
+    auto turned = [&](const float* z, const float2* t, int c) {
+        const float v = z[c];
+        if (c >= rot) return v;
+        const bool second = plan.interleaved ? (c & 1) != 0 : c >= pairs;
+        const float2 a = t[plan.interleaved ? c >> 1 : second ? c - pairs : c];
+        const float w = z[plan.interleaved ? c ^ 1 : second ? c - pairs : c + pairs];
+        const float sn = second != kBack ? a.y : -a.y;  // (turned back, the sines change sign)
+        return v * a.x + w * sn;
+    };
+    for (int t0 = static_cast<int>(blockIdx.x) * p.tpb; t0 < p.tokens; t0 += static_cast<int>(gridDim.x) * p.tpb) {
+        const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
+        __syncthreads();
+        for (int i = threadIdx.x; i < nt * pairs; i += kQkThreads) {
+            const int pr = i / nt, t = i - pr * nt;
+            cs[t][pr] = rope_cos_sin(plan, pr, qk_pos(p, plan, t0 + t, pr));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const QkPart& part = p.part[w];
+            for (int r = warp; r < nt * part.h; r += kQkWarps) {
+                const int t = r / part.h, head = r - t * part.h;
+                const E* x = static_cast<const E*>(part.x) + qk_offset(p, t0 + t, head, part.xs);
+                E* y = static_cast<E*>(part.y) + qk_offset(p, t0 + t, head, part.ys);
+                float v[kEach], ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int c = lane + 32 * i;
+                    v[i] = c < p.d ? to_f32<T>(x[c]) : 0.f;
+                    ss += v[i] * v[i];
+                }
+                const float rs = rsqrtf(warp_sum(ss) / static_cast<float>(p.d) + p.eps);
+                __syncwarp();
+                if constexpr (!kBack) {
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i)
+                        if (const int c = lane + 32 * i; c < p.d) row[warp][c] = v[i] * rs * (part.gamma != nullptr ? __ldg(part.gamma + c) : 1.f);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i)
+                        if (const int c = lane + 32 * i; c < p.d) y[c] = from_f32<T>(turned(row[warp], cs[t], c));
+                } else {
+                    const E* dy = static_cast<const E*>(part.dy) + qk_offset(p, t0 + t, head, part.gs);
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i)
+                        if (const int c = lane + 32 * i; c < p.d) row[warp][c] = to_f32<T>(dy[c]);
+                    __syncwarp();
+                    float along = 0.f, g[kEach];
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) {
+                        const int c = lane + 32 * i;
+                        g[i] = 0.f;
+                        v[i] *= rs;
+                        if (c < p.d) {
+                            const float u = turned(row[warp], cs[t], c);
+                            acc[w][i] += u * v[i];
+                            g[i] = u * (part.gamma != nullptr ? __ldg(part.gamma + c) : 1.f);
+                            along += g[i] * v[i];
+                        }
+                    }
+                    along = warp_sum(along) / static_cast<float>(p.d);
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i)
+                        if (const int c = lane + 32 * i; c < p.d) y[c] = from_f32<T>(rs * (g[i] - v[i] * along));
+                }
+            }
+        }
+    }
+    if constexpr (kBack) {
+        if (p.sums != nullptr)
+            for (int w = 0; w < 2; ++w) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) row[warp][lane + 32 * i] = acc[w][i];
+                __syncthreads();
+                for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
+                    float s = 0.f;
+                    for (int k = 0; k < kQkWarps; ++k) s += row[k][c];
+                    p.sums[(static_cast<long long>(w) * gridDim.x + blockIdx.x) * p.d + c] = s;
+                }
+            }
+    }
+    pdl_launch_dependents();
+}
+
+// dgamma: the blocks' sums, 32 channels a block, 32 runs of them side by side.
+__global__ void __launch_bounds__(1024) qk_join_kernel(const float* sums, int blocks, int d, float* dgamma_q, float* dgamma_k) {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+    const int w = blockIdx.y, c = static_cast<int>(blockIdx.x) * 32 + lane;
+    pdl_wait();
+    float s = 0.f;
+    if (c < d)
+        for (int b = run; b < blocks; b += 32) s += sums[(static_cast<long long>(w) * blocks + b) * d + c];
+    part[run][lane] = s;
+    __syncthreads();
+    s = warp_sum(part[lane][run]);  // (the transposed warp: run is the channel here)
+    if (const int ch = static_cast<int>(blockIdx.x) * 32 + run; lane == 0 && ch < d) (w == 0 ? dgamma_q : dgamma_k)[ch] = s;
+}
+
+template <bool kBack>
+cudaError_t qk_launch(int type, unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
+    const auto go = [&](auto k) { return launch_kernel(k, dim3(grid), dim3(kQkThreads), 0, s, p, plan); };
+    if (type == VAE_F32) return go(qk_plain_kernel<VAE_F32, kBack>);
+    return type == VAE_F16 ? go(qk_plain_kernel<VAE_F16, kBack>) : go(qk_plain_kernel<VAE_BF16, kBack>);
+}
+
+// A tensor of a call: what it is and whether it may be another one (given by its name and the same strides).
+struct QkTensor {
+    const char* name;
+    const void* p;
+    Extent at;
+    bool written;
+    const long long* stride;  // nullptr: dense
+    const void *own0, *own1;  // inputs that a written tensor may be
+    const long long *own0_stride, *own1_stride;
+};
+
+int qk_apart(const vae_qk_norm_rope_desc* a, const QkTensor* t, int count) {
+    for (int i = 0; i < count; ++i) {
+        if (t[i].p == nullptr || !t[i].written) continue;
+        for (int j = 0; j < count; ++j) {
+            if (j == i || t[j].p == nullptr || (t[j].written && j < i)) continue;
+            if (t[j].p == t[i].p && (t[j].p == t[i].own0 || t[j].p == t[i].own1)) {
+                const int dim[3] = {a->b, a->s, static_cast<int>(t[i].at.n[2])};
+                const long long* st = t[j].stride;
+                bool same = st != nullptr && t[j].at.n[2] == t[i].at.n[2] && (st == t[i].own0_stride || st == t[i].own1_stride);
+                for (int k = 0; same && k < 3; ++k) same = dim[k] == 1 || st[k] == t[i].stride[k];
+                if (same) continue;
+                if (st != nullptr && (st == t[i].own0_stride || st == t[i].own1_stride))
+                    return set_error(VAE_ERR_ARG, "qk norm: %s over %s needs the same strides", t[i].name, t[j].name);
+            }
+            if (extents_meet(t[i].at, t[j].at))
+                return set_error(VAE_ERR_ARG, "qk norm: %s may not overlap %s", t[i].name, t[j].name);
+        }
+    }
+    return VAE_OK;
+}
+
+int qk_check(const vae_qk_norm_rope_desc* a, bool backward) {
+    if (a == nullptr) return set_error(VAE_ERR_ARG, "qk norm: NULL desc");
+    if (!type_ok(a->type)) return set_error(VAE_ERR_ARG, "qk norm: unknown element type");
+    if (a->b < 1 || a->s < 1 || a->hq < 1 || a->hk < 1)
+        return set_error(VAE_ERR_SHAPE, "qk norm: b, s, hq, hk >= 1 are needed");
+    if (static_cast<long long>(a->b) * a->s > 0x7fffff00LL || static_cast<long long>(a->hq) + a->hk >= (1 << 20))
+        return set_error(VAE_ERR_SHAPE, "qk norm: over 2^31 - 256 tokens or 2^20 - 1 heads");
+    if (a->d < 1 || a->d > kQkMaxD) return set_error(VAE_ERR_SHAPE, "qk norm: 1 <= d <= %d, got %d", kQkMaxD, a->d);
+    if (!(a->eps > 0.f) || !std::isfinite(a->eps)) return set_error(VAE_ERR_ARG, "qk norm: eps must be > 0 and finite");
+    const struct {
+        const char* name;
+        const long long* st;
+        int h;
+        bool written;
+    } t[6] = {{"q", a->q_stride, a->hq, false},         {"k", a->k_stride, a->hk, false},
+              {"q_out", a->q_out_stride, a->hq, true},  {"k_out", a->k_out_stride, a->hk, true},
+              {"dq_out", a->dq_out_stride, a->hq, false}, {"dk_out", a->dk_out_stride, a->hk, false}};
+    for (int i = 0; i < (backward ? 6 : 4); ++i) {
+        const int dim[3] = {a->b, a->s, t[i].h};
+        for (int k = 0; k < 3; ++k)
+            if (t[i].st[k] < 0 || t[i].st[k] >= (1LL << 38) || (t[i].written && dim[k] > 1 && t[i].st[k] == 0))
+                return set_error(VAE_ERR_SHAPE, "qk norm: %s's strides must be >= 0 (> 0 where it is written) and below 2^38", t[i].name);
+        if (t[i].written && extent_folds(extent_tokens(nullptr, t[i].st, a->b, a->s, t[i].h, a->d, type_size(a->type))))
+            return set_error(VAE_ERR_SHAPE, "qk norm: rows of %s lie in one another", t[i].name);
+    }
+    return VAE_OK;
+}
+
+int qk_check_plan(const vae_qk_norm_rope_desc* a, const void* pos, const vae_rope_plan* plan) {
+    if ((pos == nullptr) != (plan == nullptr)) return set_error(VAE_ERR_ARG, "qk norm: positions and plan come together");
+    if (plan == nullptr) return VAE_OK;
+    if (plan->naxes < 1 || plan->naxes > 4 || plan->pairs < 1 || plan->pairs > VAE_ROPE_MAX_PAIRS)
+        return set_error(VAE_ERR_ARG, "qk norm: the plan was not initialised");
+    for (int i = 0; i < plan->pairs; ++i)
+        if (plan->axis[i] >= plan->naxes) return set_error(VAE_ERR_ARG, "qk norm: the plan was not initialised");
+    if (2 * plan->pairs > a->d)
+        return set_error(VAE_ERR_SHAPE, "qk norm: the plan turns %d channels of a head of %d", 2 * plan->pairs, a->d);
+    if (a->pos_batch != 1 && a->pos_batch != a->b)
+        return set_error(VAE_ERR_SHAPE, "qk norm: positions of %d batch entries for a batch of %d", a->pos_batch, a->b);
+    if (reinterpret_cast<uintptr_t>(pos) % 4) return set_error(VAE_ERR_ALIGN, "qk norm: positions are not aligned");
+    return VAE_OK;
+}
+
+int qk_tiles(const vae_qk_norm_rope_desc* a, int* tpb) {
+    const int tokens = a->b * a->s;
+    // as many tokens as share one table, down to one when there are too few to give every SM a block
+    *tpb = std::min(kQkTokens, std::max(1, tokens / 304));
+    return (tokens - 1) / *tpb + 1;
+}
+
+void qk_fill(const vae_qk_norm_rope_desc* a, QkParams* p, const void* q, const void* k, const void* gq, const void* gk, void* yq,
+             void* yk, const float* gamma_q, const float* gamma_k, const void* pos) {
+    const int dim[2][3] = {{a->b, a->s, a->hq}, {a->b, a->s, a->hk}};
+    const long long* st[2][3] = {{a->q_stride, a->dq_out_stride, a->q_out_stride}, {a->k_stride, a->dk_out_stride, a->k_out_stride}};
+    const void* x[2][2] = {{q, gq}, {k, gk}};
+    void* y[2] = {yq, yk};
+    for (int w = 0; w < 2; ++w) {
+        QkPart& t = p->part[w];
+        t.x = x[w][0];
+        t.dy = x[w][1];
+        t.y = y[w];
+        t.gamma = w == 0 ? gamma_q : gamma_k;
+        t.h = dim[w][2];
+        for (int i = 0; i < 3; ++i) {
+            const bool many = dim[w][i] > 1;
+            t.xs[i] = many ? st[w][0][i] : 0;
+            t.gs[i] = many && gq != nullptr ? st[w][1][i] : 0;
+            t.ys[i] = many ? st[w][2][i] : 0;
+        }
+    }
+    p->pos = pos;
+    p->tokens = a->b * a->s;
+    p->s = a->s;
+    p->d = a->d;
+    p->pos_int = a->pos_int != 0;
+    p->pos_batch = a->pos_batch;
+    p->eps = a->eps;
+}
+
+bool qk_aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+}  // namespace
+}  // namespace vae
+
+using namespace vae;
+
+extern "C" {
+
+int vae_qk_norm_rope(const vae_qk_norm_rope_desc* desc, const void* q_dev, const void* k_dev, const float* gamma_q_dev,
+                     const float* gamma_k_dev, const void* pos_dev, const vae_rope_plan* plan, void* q_out_dev,
+                     void* k_out_dev, vae_stream_t stream) {
+    clear_error();
+    int rc = qk_check(desc, false);
+    if (rc != VAE_OK) return rc;
+    if (q_dev == nullptr || k_dev == nullptr || q_out_dev == nullptr || k_out_dev == nullptr)
+        return set_error(VAE_ERR_ARG, "qk norm: NULL tensor");
+    rc = qk_check_plan(desc, pos_dev, plan);
+    if (rc != VAE_OK) return rc;
+    const vae_qk_norm_rope_desc& a = *desc;
+    const size_t es = type_size(a.type);
+    if (!qk_aligned(q_dev, es) || !qk_aligned(k_dev, es) || !qk_aligned(q_out_dev, es) || !qk_aligned(k_out_dev, es) ||
+        !qk_aligned(gamma_q_dev, 4) || !qk_aligned(gamma_k_dev, 4))
+        return set_error(VAE_ERR_ALIGN, "qk norm: a pointer is not aligned to its elements");
+    const auto heads = [&](const void* p, const long long* st, int h) { return extent_tokens(p, st, a.b, a.s, h, a.d, es); };
+    const QkTensor t[] = {
+        {"q_out", q_out_dev, heads(q_out_dev, a.q_out_stride, a.hq), true, a.q_out_stride, q_dev, nullptr, a.q_stride, nullptr},
+        {"k_out", k_out_dev, heads(k_out_dev, a.k_out_stride, a.hk), true, a.k_out_stride, k_dev, nullptr, a.k_stride, nullptr},
+        {"q", q_dev, heads(q_dev, a.q_stride, a.hq), false, a.q_stride},
+        {"k", k_dev, heads(k_dev, a.k_stride, a.hk), false, a.k_stride},
+        {"gamma_q", gamma_q_dev, extent_dense(gamma_q_dev, a.d * 4u), false},
+        {"gamma_k", gamma_k_dev, extent_dense(gamma_k_dev, a.d * 4u), false},
+        {"the positions", pos_dev, extent_dense(pos_dev, plan != nullptr ? static_cast<size_t>(a.pos_batch) * a.s * plan->naxes * 4 : 0), false}};
+    rc = qk_apart(desc, t, 7);
+    if (rc != VAE_OK) return rc;
+    rc = check_device();
+    if (rc != VAE_OK) return rc;
+    QkParams p{};
+    qk_fill(desc, &p, q_dev, k_dev, nullptr, nullptr, q_out_dev, k_out_dev, gamma_q_dev, gamma_k_dev, pos_dev);
+    const unsigned grid = static_cast<unsigned>(qk_tiles(desc, &p.tpb));
+    const vae_rope_plan none{};
+    const vae_rope_plan& pl = plan != nullptr ? *plan : none;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    VAE_CUDA_CHECK(qk_launch<false>(a.type, grid, st, p, pl));
+    return VAE_OK;
+}
+
+size_t vae_qk_norm_rope_backward_workspace_bytes(const vae_qk_norm_rope_desc* desc) {
+    clear_error();
+    if (qk_check(desc, true) != VAE_OK) return 0;
+    int tpb;
+    return static_cast<size_t>(std::min(qk_tiles(desc, &tpb), kQkBlocks)) * 2 * desc->d * sizeof(float);
+}
+
+int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_out_dev, const void* dk_out_dev,
+                              const void* q_dev, const void* k_dev, const float* gamma_q_dev, const float* gamma_k_dev,
+                              const void* pos_dev, const vae_rope_plan* plan, void* dq_dev, void* dk_dev,
+                              float* dgamma_q_dev, float* dgamma_k_dev, void* workspace_dev, size_t workspace_bytes,
+                              vae_stream_t stream) {
+    clear_error();
+    int rc = qk_check(desc, true);
+    if (rc != VAE_OK) return rc;
+    if (dq_out_dev == nullptr || dk_out_dev == nullptr || q_dev == nullptr || k_dev == nullptr || dq_dev == nullptr ||
+        dk_dev == nullptr)
+        return set_error(VAE_ERR_ARG, "qk norm: NULL tensor");
+    rc = qk_check_plan(desc, pos_dev, plan);
+    if (rc != VAE_OK) return rc;
+    const vae_qk_norm_rope_desc& a = *desc;
+    const bool weights = dgamma_q_dev != nullptr;
+    if (weights != (dgamma_k_dev != nullptr)) return set_error(VAE_ERR_ARG, "qk norm: dgamma_q and dgamma_k come together");
+    const size_t es = type_size(a.type), need = vae_qk_norm_rope_backward_workspace_bytes(desc);
+    if (!qk_aligned(dq_out_dev, es) || !qk_aligned(dk_out_dev, es) || !qk_aligned(q_dev, es) || !qk_aligned(k_dev, es) ||
+        !qk_aligned(dq_dev, es) || !qk_aligned(dk_dev, es) || !qk_aligned(gamma_q_dev, 4) || !qk_aligned(gamma_k_dev, 4) ||
+        !qk_aligned(dgamma_q_dev, 4) || !qk_aligned(dgamma_k_dev, 4))
+        return set_error(VAE_ERR_ALIGN, "qk norm: a pointer is not aligned to its elements");
+    if (weights) {
+        if (workspace_dev == nullptr) return set_error(VAE_ERR_ARG, "qk norm: a workspace is needed for dgamma");
+        if (workspace_bytes < need)
+            return set_error(VAE_ERR_NOMEM, "qk norm: workspace of %zu bytes, %zu are needed", workspace_bytes, need);
+        if (!aligned16(workspace_dev)) return set_error(VAE_ERR_ALIGN, "qk norm: the workspace must be 16-byte aligned");
+    }
+    const auto heads = [&](const void* p, const long long* st, int h) { return extent_tokens(p, st, a.b, a.s, h, a.d, es); };
+    const QkTensor t[] = {
+        {"dq", dq_dev, heads(dq_dev, a.q_out_stride, a.hq), true, a.q_out_stride, q_dev, dq_out_dev, a.q_stride, a.dq_out_stride},
+        {"dk", dk_dev, heads(dk_dev, a.k_out_stride, a.hk), true, a.k_out_stride, k_dev, dk_out_dev, a.k_stride, a.dk_out_stride},
+        {"dgamma_q", dgamma_q_dev, extent_dense(dgamma_q_dev, a.d * 4u), true},
+        {"dgamma_k", dgamma_k_dev, extent_dense(dgamma_k_dev, a.d * 4u), true},
+        {"the workspace", weights ? workspace_dev : nullptr, extent_dense(workspace_dev, need), true},
+        {"q", q_dev, heads(q_dev, a.q_stride, a.hq), false, a.q_stride},
+        {"k", k_dev, heads(k_dev, a.k_stride, a.hk), false, a.k_stride},
+        {"dq_out", dq_out_dev, heads(dq_out_dev, a.dq_out_stride, a.hq), false, a.dq_out_stride},
+        {"dk_out", dk_out_dev, heads(dk_out_dev, a.dk_out_stride, a.hk), false, a.dk_out_stride},
+        {"gamma_q", gamma_q_dev, extent_dense(gamma_q_dev, a.d * 4u), false},
+        {"gamma_k", gamma_k_dev, extent_dense(gamma_k_dev, a.d * 4u), false},
+        {"the positions", pos_dev, extent_dense(pos_dev, plan != nullptr ? static_cast<size_t>(a.pos_batch) * a.s * plan->naxes * 4 : 0), false}};
+    rc = qk_apart(desc, t, 12);
+    if (rc != VAE_OK) return rc;
+    rc = check_device();
+    if (rc != VAE_OK) return rc;
+    QkParams p{};
+    qk_fill(desc, &p, q_dev, k_dev, dq_out_dev, dk_out_dev, dq_dev, dk_dev, gamma_q_dev, gamma_k_dev, pos_dev);
+    const unsigned grid = static_cast<unsigned>(std::min(qk_tiles(desc, &p.tpb), kQkBlocks));
+    p.sums = weights ? static_cast<float*>(workspace_dev) : nullptr;
+    const vae_rope_plan none{};
+    const vae_rope_plan& pl = plan != nullptr ? *plan : none;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    VAE_CUDA_CHECK(qk_launch<true>(a.type, grid, st, p, pl));
+    if (weights)
+        VAE_CUDA_CHECK(launch_next(qk_join_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, st,
+                                   static_cast<const float*>(p.sums), static_cast<int>(grid), a.d, dgamma_q_dev, dgamma_k_dev));
+    return VAE_OK;
+}
+
+}  // extern "C"

@@ -1,13 +1,8 @@
 // Rotary positions over several axes (public entry points at the end).
 //
-// The angle of pair p at position t is 2 pi t f_p with f_p turns per position.
-// f_p comes from the host in two floats (hi + lo, 48 bits), so t f_hi is split
-// exactly by one fma into whole turns and a fraction, t f_lo is added to the
-// fraction, and sincospi of twice the fraction follows: far positions lose no
-// digits and no 64-bit arithmetic runs on the device. A block computes the
-// (cos, sin) of its tokens' pairs once in shared memory, then turns every head
-// of those tokens: one read and one write of the tensor, which bounds the call.
-// Measured on GB300 at 36864 tokens x 18 heads x 128 in f16 (340 MB): 70 us
+// A block computes the (cos, sin) of its tokens' pairs once in shared memory,
+// then turns every head of those tokens: one read and one write of the tensor,
+// which bounds the call. Measured on GB300 at 36864 tokens x 18 heads x 128 in f16 (340 MB): 70 us
 // interleaved (4.9 TB/s), 60 us in halves (5.7 TB/s). Small blocks, so that the
 // angles of some are formed while others move rows: 8 tokens, 128 threads, 12
 // blocks an SM and two rows a thread in flight; 32 tokens and four blocks of 256
@@ -17,6 +12,7 @@
 #include <type_traits>
 
 #include "vae_overlap.h"
+#include "vae_rope.cuh"
 #include "vae_types.cuh"
 
 namespace vae {
@@ -38,14 +34,6 @@ struct RopeParams {
     int pos_int, pos_batch, inverse;
     long long xs[3], ys[3];
 };
-
-// Turns (a, b) by (cos, sin).
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-    const float x = a * cs.x - b * cs.y;
-    b = a * cs.y + b * cs.x;
-    a = x;
-}
-
 
 // A unit as it lies in memory: sixteen or eight elements, or one.
 template <int T, int kN>
@@ -148,13 +136,8 @@ __global__ void __launch_bounds__(rope_threads(kN), 1536 / rope_threads(kN)) rop
         const long long i_pos = row * plan.naxes + plan.axis[pr];
         const float pos = p.pos_int ? static_cast<float>(static_cast<const int*>(p.pos)[i_pos])
                                     : static_cast<const float*>(p.pos)[i_pos];
-        // whole turns + fraction of pos * hi (the fma's product is exact), then the rest
-        const float hi = plan.turns_hi[pr];
-        const float whole = rintf(pos * hi);
-        const float frac = fmaf(pos, hi, -whole) + pos * plan.turns_lo[pr];
-        float sn, c;
-        sincospif(2.f * frac, &sn, &c);
-        cs[t][pr] = make_float2(c, p.inverse ? -sn : sn);
+        const float2 c = rope_cos_sin(plan, pr, pos);
+        cs[t][pr] = make_float2(c.x, p.inverse ? -c.y : c.y);
     }
     __syncthreads();
     while (at[0] >> 20 < nt) {

@@ -426,6 +426,52 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
              void* y_dev, const long long y_stride[3], vae_stream_t stream);
 
 /*
+ * The norm of query and key heads and their rotary positions, both tensors in
+ * one pass: for each head x of d channels,
+ *   n = x / sqrt(mean(x^2) + eps), z = n * gamma, y = the pairs of z turned by
+ *   the angles of its token (vae_rope's rule),
+ * in f32, rounded once.
+ *   q_dev [b][s][hq][d], k_dev [b][s][hk][d] of `type`, *_stride = {batch,
+ *   token, head} in elements, channels contiguous; q_out_dev, k_out_dev
+ *   likewise (each may be its own input, with the same strides). The keys may go
+ *   straight to their places in a cache.
+ *   gamma_q_dev, gamma_k_dev f32 [d], each or both NULL (1).
+ *   pos_dev [pos_batch][s][naxes], f32 or int32 (pos_int != 0), pos_batch = 1 or
+ *   b, and the plan; both NULL: the norm alone.
+ * vae_qk_norm_rope_backward: with u = dy turned back, v = u * gamma,
+ *   dx = (v - n * mean(v * n)) / sqrt(mean(x^2) + eps) and dgamma = the sum of
+ *   u * n over all tokens and heads, in a fixed order: the same inputs give the
+ *   same bits. dq_out_dev, dk_out_dev (the gradients of the outputs) have the
+ *   strides dq_out_stride, dk_out_stride; dq_dev, dk_dev are written with
+ *   q_out_stride, k_out_stride (each may be dy or x of its own tensor, with the
+ *   same strides). dgamma_q_dev, dgamma_k_dev f32 [d], both or neither.
+ * Requirements: b, s, hq, hk >= 1; b * s <= 2^31 - 256, hq + hk < 2^20;
+ * 1 <= d <= 256, 2 * plan pairs <= d; eps > 0 and finite; strides >= 0, those of
+ * written tensors > 0 where the dimension is over 1. What is written lies apart
+ * from what is read (but for the cases above) and from one another, and no two
+ * of its rows meet. workspace_dev of vae_qk_norm_rope_backward_workspace_bytes(desc)
+ * bytes, 16-byte aligned, contents ignored on entry, NULL is fine without dgamma.
+ */
+typedef struct {
+    int type;
+    int b, s, hq, hk, d;
+    float eps;
+    int pos_int, pos_batch;
+    long long q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+    /* backward only */
+    long long dq_out_stride[3], dk_out_stride[3];
+} vae_qk_norm_rope_desc;
+int vae_qk_norm_rope(const vae_qk_norm_rope_desc* desc, const void* q_dev, const void* k_dev, const float* gamma_q_dev,
+                     const float* gamma_k_dev, const void* pos_dev, const vae_rope_plan* plan, void* q_out_dev,
+                     void* k_out_dev, vae_stream_t stream);
+size_t vae_qk_norm_rope_backward_workspace_bytes(const vae_qk_norm_rope_desc* desc);
+int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_out_dev, const void* dk_out_dev,
+                              const void* q_dev, const void* k_dev, const float* gamma_q_dev, const float* gamma_k_dev,
+                              const void* pos_dev, const vae_rope_plan* plan, void* dq_dev, void* dk_dev,
+                              float* dgamma_q_dev, float* dgamma_k_dev, void* workspace_dev, size_t workspace_bytes,
+                              vae_stream_t stream);
+
+/*
  * Multi-head attention: o = softmax(scale * q k^T over the keys a query sees) v
  * and lse = log(sum of exp) of each row.
  *   q [b][sq][hq][d], k, v [b][sk][hkv][d], o [b][sq][hq][d], all of `type`

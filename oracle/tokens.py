@@ -155,3 +155,24 @@ def attention_backward_bounds(do, q, k, v, u, c, scale=None, q_len=None, k_len=N
             ek[e, :kl, h // g] += scale * (eds + c * ds).T @ np.abs(qq)
             ev[e, :kl, h // g] += (ep + c * p).T @ ad
     return eq, ek, ev
+
+
+def qk_norm_rope(x, gamma=None, positions=None, axes=(), theta: float = 10000.0, interleaved: bool = True, eps: float = 1e-6):
+    """One of the two tensors, x [b][s][h][d]: the norm of every head, its weight, the rotation."""
+    x = _f64(x)
+    z = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    if gamma is not None:
+        z = z * _f64(gamma)
+    return z if positions is None else rope(z, positions, axes, theta, interleaved)
+
+
+def qk_norm_rope_backward(dy, x, gamma=None, positions=None, axes=(), theta: float = 10000.0, interleaved: bool = True,
+                          eps: float = 1e-6):
+    """(dx, dgamma) of sum(dy * qk_norm_rope(x))."""
+    x, u = _f64(x), _f64(dy)
+    if positions is not None:
+        u = rope(u, positions, axes, theta, interleaved, inverse=True)
+    size = np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    n = x / size
+    v = u if gamma is None else u * _f64(gamma)
+    return (v - n * (v * n).mean(-1, keepdims=True)) / size, (u * n).sum((0, 1, 2))
