@@ -156,6 +156,221 @@ __global__ void __launch_bounds__(kQkThreads) qk_plain_kernel(const QkParams p, 
     pdl_launch_dependents();
 }
 
+// Rows in 16-byte vectors. A row lies over G lanes (a power of two, 16 at most), two
+// units of eight channels a lane, in one of three ways:
+//   kLocal: neighbouring units; interleaved pairs lie within a unit (or nothing turns);
+//   kHalves: pairs (c, c + R/2) with R a multiple of 16: a lane holds a unit of each half;
+//   kSwap: other halves: neighbouring units, the partners come through shared memory.
+// Two rows a lane are in flight; the first ones are on their way while the angles are formed.
+enum : int { kLocal, kHalves, kSwap };
+
+template <int T>
+struct QkUnit {  // eight channels as they lie in memory
+    uint4 r[T == VAE_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const typename Elem<T>::type* p) {
+        r[0] = *reinterpret_cast<const uint4*>(p);
+        if constexpr (T == VAE_F32) r[1] = *reinterpret_cast<const uint4*>(p + 4);
+    }
+    __device__ __forceinline__ void clear() {
+        r[0] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (T == VAE_F32) r[1] = r[0];
+    }
+    __device__ __forceinline__ void get(float* v) const { load8<T>(r, *reinterpret_cast<float(*)[8]>(v)); }
+};
+
+template <int T, int kForm, bool kBack>
+__global__ void __launch_bounds__(kQkThreads, kBack ? 4 : 8)
+    qk_vector_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
+    using E = typename Elem<T>::type;
+    constexpr int kBatch = kBack && T == VAE_F32 ? 1 : 2;
+    // (cos, sin) of pair 8 u + 2 i + j of a token at [i][u][j]: a lane's eight pairs are four vectors, and those of
+    // neighbouring lanes lie side by side
+    __shared__ __align__(16) float2 cs[kQkTokens][4][16][2];
+    __shared__ float swap[kForm == kSwap ? kQkThreads * 16 : 1];
+    __shared__ float part_sums[kBack ? kQkWarps * kQkMaxD : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pairs = plan.pairs, rot = 2 * pairs;
+    const int group = 1 << glog2, u = lane & (group - 1);
+    const int step = kQkThreads >> glog2;
+    const int nrot = pairs >> 3;  // kHalves: lanes whose units turn
+    const bool turns = kForm == kHalves && u < nrot;
+    const int ca = kForm == kHalves ? (turns ? 8 * u : rot + 16 * (u - nrot)) : 16 * u;
+    const int cb = turns ? pairs + 8 * u : ca + 8;
+    const bool has_a = ca < p.d, has_b = cb < p.d && has_a;
+    float acc[2][kBack ? 16 : 1] = {};
+    pdl_wait();
+
+    for (int t0 = static_cast<int>(blockIdx.x) * p.tpb; t0 < p.tokens; t0 += static_cast<int>(gridDim.x) * p.tpb) {
+        const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
+        const int b0 = t0 / p.s, s0 = t0 - b0 * p.s;
+        QkUnit<T> xa[kBatch], xb[kBatch], ga[kBack ? kBatch : 1], gb[kBack ? kBatch : 1];
+        int at[kBatch];  // the rows: token << 20 | head
+        int tk, hd;
+        auto offset = [&](int row, const long long (&st)[3]) {
+            int si = s0 + (row >> 20), bi = b0;
+            while (si >= p.s) {
+                si -= p.s;
+                ++bi;
+            }
+            return bi * st[0] + si * st[1] + (row & 0xfffff) * st[2];
+        };
+        auto settle = [&](int h) {
+            while (tk < nt && hd >= h) {
+                hd -= h;
+                ++tk;
+            }
+        };
+        auto load = [&](const QkPart& part) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                at[k] = tk << 20 | hd;
+                xa[k].clear();
+                xb[k].clear();
+                if constexpr (kBack) {
+                    ga[k].clear();
+                    gb[k].clear();
+                }
+                if (tk < nt) {
+                    const E* x = static_cast<const E*>(part.x) + offset(at[k], part.xs);
+                    if (has_a) xa[k].load(x + ca);
+                    if (has_b) xb[k].load(x + cb);
+                    if constexpr (kBack) {
+                        const E* g = static_cast<const E*>(part.dy) + offset(at[k], part.gs);
+                        if (has_a) ga[k].load(g + ca);
+                        if (has_b) gb[k].load(g + cb);
+                    }
+                    hd += step;
+                    settle(part.h);
+                }
+            }
+        };
+        auto begin = [&](const QkPart& part) {
+            hd = threadIdx.x >> glog2;
+            tk = 0;
+            settle(part.h);
+            load(part);
+        };
+        // the pairs of v turned by the angles of token t, or back
+        auto turn_all = [&](float (&v)[16], int t) {
+            const float2(*a)[16][2] = cs[t];
+            if constexpr (kForm == kSwap) {
+                float* z = swap + (threadIdx.x >> glog2 << glog2) * 16;
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[ca + e] = v[e];
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int c = ca + e;
+                    if (c < rot) {
+                        const bool second = c >= pairs;
+                        const int pr = second ? c - pairs : c;
+                        const float2 x = a[(pr & 7) >> 1][pr >> 3][pr & 1];
+                        v[e] = v[e] * x.x + z[second ? pr : c + pairs] * (second != kBack ? x.y : -x.y);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (kForm == kHalves ? !turns : (u >= 16 || 8 * u + 2 * i >= pairs)) continue;
+                    const float4 x = *reinterpret_cast<const float4*>(&a[i][u][0]);
+                    const float2 c0 = make_float2(x.x, kBack ? -x.y : x.y), c1 = make_float2(x.z, kBack ? -x.w : x.w);
+                    if constexpr (kForm == kHalves) {
+                        turn(v[2 * i], v[8 + 2 * i], c0);
+                        turn(v[2 * i + 1], v[9 + 2 * i], c1);
+                    } else {
+                        turn(v[4 * i], v[4 * i + 1], c0);
+                        if (8 * u + 2 * i + 1 < pairs) turn(v[4 * i + 2], v[4 * i + 3], c1);
+                    }
+                }
+            }
+        };
+        auto group_sum = [&](float x) {
+            for (int o = group >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            return x;
+        };
+        auto store = [&](E* y, const float (&v)[16]) {
+            if (has_a) store8<T>(y + ca, *reinterpret_cast<const float(*)[8]>(v));
+            if (has_b) store8<T>(y + cb, *reinterpret_cast<const float(*)[8]>(v + 8));
+        };
+
+        begin(p.part[0]);
+        __syncthreads();  // (the last tokens' angles have been read)
+        for (int i = threadIdx.x; i < nt * pairs; i += kQkThreads) {
+            // neighbours take the tokens of one pair: its entries of the plan are one address for them
+            const int pr = i / nt, t = i - pr * nt;
+            cs[t][(pr & 7) >> 1][pr >> 3][pr & 1] = rope_cos_sin(plan, pr, qk_pos(p, plan, t0 + t, pr));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const QkPart& part = p.part[w];
+            if (w == 1) begin(part);
+            float gamma[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const bool in = e < 8 ? has_a : has_b;
+                gamma[e] = in && part.gamma != nullptr ? __ldg(part.gamma + (e < 8 ? ca + e : cb + e - 8)) : 1.f;
+            }
+            while (__any_sync(0xffffffffu, at[0] >> 20 < nt)) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int t = at[k] >> 20;
+                    const bool live = t < nt;
+                    float v[16], ss = 0.f;
+                    xa[k].get(v);
+                    xb[k].get(v + 8);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) ss += v[e] * v[e];
+                    const float rs = rsqrtf(group_sum(ss) / static_cast<float>(p.d) + p.eps);
+                    if constexpr (!kBack) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = v[e] * rs * gamma[e];
+                        turn_all(v, live ? t : 0);
+                        if (live) store(static_cast<E*>(part.y) + offset(at[k], part.ys), v);
+                    } else {
+                        float g[16], along = 0.f;
+                        ga[k].get(g);
+                        gb[k].get(g + 8);
+                        turn_all(g, live ? t : 0);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            v[e] *= rs;
+                            acc[w][e] += g[e] * v[e];
+                            g[e] *= gamma[e];
+                            along += g[e] * v[e];
+                        }
+                        along = group_sum(along) / static_cast<float>(p.d);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) g[e] = rs * (g[e] - v[e] * along);
+                        if (live) store(static_cast<E*>(part.y) + offset(at[k], part.ys), g);
+                    }
+                }
+                load(part);
+            }
+        }
+    }
+    if constexpr (kBack) {
+        if (p.sums != nullptr)
+            for (int w = 0; w < 2; ++w) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float x = w == 0 ? acc[0][e] : acc[1][e];
+                    for (int o = group; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                    if (lane < group && (e < 8 ? has_a : has_b)) part_sums[warp * kQkMaxD + (e < 8 ? ca + e : cb + e - 8)] = x;
+                }
+                __syncthreads();
+                for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
+                    float x = 0.f;
+                    for (int k = 0; k < kQkWarps; ++k) x += part_sums[k * kQkMaxD + c];
+                    p.sums[(static_cast<long long>(w) * gridDim.x + blockIdx.x) * p.d + c] = x;
+                }
+            }
+    }
+    pdl_launch_dependents();
+}
+
 // dgamma: the blocks' sums, 32 channels a block, 32 runs of them side by side.
 __global__ void __launch_bounds__(1024) qk_join_kernel(const float* sums, int blocks, int d, float* dgamma_q, float* dgamma_k) {
     __shared__ float part[32][33];
@@ -171,11 +386,28 @@ __global__ void __launch_bounds__(1024) qk_join_kernel(const float* sums, int bl
     if (const int ch = static_cast<int>(blockIdx.x) * 32 + run; lane == 0 && ch < d) (w == 0 ? dgamma_q : dgamma_k)[ch] = s;
 }
 
+template <int T, bool kBack>
+cudaError_t qk_launch_type(unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
+    // Vectors where every row starts on 16 bytes and holds whole ones (a warp a row, channel by channel, otherwise)
+    bool v8 = p.d % 8 == 0;
+    for (const QkPart& t : p.part) {
+        v8 = v8 && aligned16(t.x) && aligned16(t.dy) && aligned16(t.y);
+        for (int i = 0; i < 3; ++i) v8 = v8 && t.xs[i] % 8 == 0 && t.gs[i] % 8 == 0 && t.ys[i] % 8 == 0;
+    }
+    if (!v8) return launch_kernel(qk_plain_kernel<T, kBack>, dim3(grid), dim3(kQkThreads), 0, s, p, plan);
+    const bool halves = plan.pairs > 0 && !plan.interleaved;
+    const int form = !halves ? kLocal : plan.pairs % 8 == 0 ? kHalves : kSwap;
+    const int lanes = form == kHalves ? plan.pairs / 8 + (p.d - 2 * plan.pairs + 15) / 16 : (p.d + 15) / 16;
+    int glog2 = 0;
+    while ((1 << glog2) < lanes) ++glog2;
+    const auto go = [&](auto k) { return launch_kernel(k, dim3(grid), dim3(kQkThreads), 0, s, p, plan, glog2); };
+    if (form == kLocal) return go(qk_vector_kernel<T, kLocal, kBack>);
+    return form == kHalves ? go(qk_vector_kernel<T, kHalves, kBack>) : go(qk_vector_kernel<T, kSwap, kBack>);
+}
 template <bool kBack>
 cudaError_t qk_launch(int type, unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
-    const auto go = [&](auto k) { return launch_kernel(k, dim3(grid), dim3(kQkThreads), 0, s, p, plan); };
-    if (type == VAE_F32) return go(qk_plain_kernel<VAE_F32, kBack>);
-    return type == VAE_F16 ? go(qk_plain_kernel<VAE_F16, kBack>) : go(qk_plain_kernel<VAE_BF16, kBack>);
+    if (type == VAE_F32) return qk_launch_type<VAE_F32, kBack>(grid, s, p, plan);
+    return type == VAE_F16 ? qk_launch_type<VAE_F16, kBack>(grid, s, p, plan) : qk_launch_type<VAE_BF16, kBack>(grid, s, p, plan);
 }
 
 // A tensor of a call: what it is and whether it may be another one (given by its name and the same strides).
