@@ -27,6 +27,7 @@ __all__ = [
     "groupnorm_workspace_bytes", "cast_f16", "mid_attention", "mid_attention_workspace_bytes",
     "layernorm", "layernorm_backward", "layernorm_backward_workspace_bytes", "RopePlan", "rope",
     "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_bytes",
+    "gated_ffn", "gated_ffn_workspace_bytes", "gated_ffn_backward", "gated_ffn_backward_workspace_bytes",
     "attention", "attention_workspace_bytes", "attention_backward", "attention_backward_workspace_bytes",
     "Decoder", "DecodeGraph", "pack_conv3x3", "pack_conv1x1",
     "UPSAMPLE2X", "PAD_REPLICATE", "PAD_REFLECT", "DOWNSAMPLE2X", "EPI_SILU", "OUT_F16", "FAMILY_GN", "FAMILY_RMS",
@@ -85,6 +86,10 @@ SIGNATURES = {
     "vae_qk_norm_rope": ([_P] * 9 + [_P], _I),
     "vae_qk_norm_rope_backward_workspace_bytes": ([_P], _SZ),
     "vae_qk_norm_rope_backward": ([_P] * 14 + [_SZ, _P], _I),
+    "vae_gated_ffn_workspace_bytes": ([_P], _SZ),
+    "vae_gated_ffn": ([_P] * 11 + [_SZ, _P], _I),
+    "vae_gated_ffn_backward_workspace_bytes": ([_P], _SZ),
+    "vae_gated_ffn_backward": ([_P] * 14 + [_SZ, _P], _I),
     "vae_attention_workspace_bytes": ([_P], _SZ),
     "vae_attention": ([_P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
     "vae_attention_backward_workspace_bytes": ([_P], _SZ),
@@ -924,6 +929,138 @@ def _qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, positions, pl
                                        dq.data_ptr(), dk.data_ptr(), _ptr(dgamma_q), _ptr(dgamma_k), *_work(workspace),
                                        stream))
     return dq, dk, dgamma_q, dgamma_k
+
+
+# struct vae_gated_ffn_desc: type, m, c, f, activation, y_type, save, dw_type
+_FFN_DESC = struct.Struct("=8i")
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _activation(name):
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise VaeError(-1, f"activation must be one of {', '.join(ACTIVATIONS)}, got {name}")
+    return code
+
+
+def _ffn_args(x, w_gate, w_up, w_down):
+    """(type, m, c, f) of a gated feed-forward block; checks x and the weights."""
+    if x.dim() != 2 or w_gate.dim() != 2:
+        raise VaeError(-2, f"x and w_gate must have 2 dims, got {x.dim()} and {w_gate.dim()}")
+    shape = x.shape
+    m, c = shape
+    f = w_gate.shape[0]
+    if m > _INT or c > _INT or f > _INT:
+        _sizes(m=m, c=c, f=f)
+    dtype = x.dtype
+    code = _type(dtype, "x")
+    _tensor(x, "x", dtype, shape)
+    _tensor(w_gate, "w_gate", dtype, (f, c))
+    _tensor(w_up, "w_up", dtype, (f, c))
+    _tensor(w_down, "w_down", dtype, (c, f))
+    return code, m, c, f
+
+
+def gated_ffn_workspace_bytes(m: int, c: int, f: int, save: bool = False) -> int:
+    _sizes(m=m, c=c, f=f)
+    return int(lib().vae_gated_ffn_workspace_bytes(_FFN_DESC.pack(1, m, c, f, 0, 1, save, 1)))
+
+
+def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", residual=None, save: bool = False, out_dtype=None, out=None,
+              workspace=None, stream=None):
+    """The gated feed-forward block of x [m][c] (f16 or bf16): (act(x w_gate^T) * (x w_up^T)) w_down^T with
+    w_gate, w_up [f][c] and w_down [c][f]; activation silu, gelu or gelu_tanh. The result [m][c] has x's type, or
+    f32 (``out_dtype``, or with ``residual`` f32 [m][c], which is added; ``out`` may be it). With ``save`` also
+    returns (gate, up, hidden) [m][f], which the gradient takes: (y, saved)."""
+    if x is None or w_gate is None or w_up is None or w_down is None:
+        _given(x=x, w_gate=w_gate, w_up=w_up, w_down=w_down)
+    index = _device_of((("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down), ("residual", residual),
+                        ("out", out), ("workspace", workspace)))
+    return _call(index, stream, _gated_ffn, x, w_gate, w_up, w_down, activation, residual, save, out_dtype, out, workspace)
+
+
+def _gated_ffn(x, w_gate, w_up, w_down, activation, residual, save, out_dtype, out, workspace, stream):
+    code, m, c, f = _ffn_args(x, w_gate, w_up, w_down)
+    dtype, device = x.dtype, x.device
+    if residual is not None:
+        _tensor(residual, "residual", _T.f32, (m, c))
+        out_dtype = out_dtype or _T.f32
+    if out is None:
+        out = _T.empty((m, c), dtype=out_dtype or dtype, device=device)
+    else:
+        _tensor(out, "out", out_dtype or out.dtype, (m, c))
+    desc = _FFN_DESC.pack(code, m, c, f, _activation(activation), _type(out.dtype, "out"), bool(save), code)
+    L = lib()
+    saved, at = None, (None, None, None)
+    if save:
+        both = _T.empty((3, m, f), dtype=dtype, device=device)
+        saved = (both[0], both[1], both[2])
+        at = (saved[0].data_ptr(), saved[1].data_ptr(), saved[2].data_ptr())
+    if workspace is None:
+        nb = L.vae_gated_ffn_workspace_bytes(desc)
+        workspace = _T.empty(nb, dtype=_T.u8, device=device) if nb else None
+    _check(L.vae_gated_ffn(desc, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), _ptr(residual),
+                           out.data_ptr(), *at, *_work(workspace), stream))
+    return (out, saved) if save else out
+
+
+def gated_ffn_backward_workspace_bytes(m: int, c: int, f: int) -> int:
+    _sizes(m=m, c=c, f=f)
+    return int(lib().vae_gated_ffn_backward_workspace_bytes(_FFN_DESC.pack(1, m, c, f, 0, 1, 0, 1)))
+
+
+def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, activation: str = "silu", weight_grads: bool = True,
+                       grad_dtype=None, dx=None, dw_gate=None, dw_up=None, dw_down=None, workspace=None, stream=None):
+    """The gradient of gated_ffn for dy [m][c] of x's type, from the (gate, up, hidden) that it saved:
+    (dx of x's type, dw_gate, dw_up [f][c], dw_down [c][f] of ``grad_dtype``: x's type or f32); with
+    ``weight_grads`` False the last three are None and not computed."""
+    if dy is None or x is None or w_gate is None or w_up is None or w_down is None or saved is None:
+        _given(dy=dy, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, saved=saved)
+    gate, up, hidden = saved
+    _given(gate=gate, up=up, hidden=hidden)
+    index = _device_of((("dy", dy), ("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down), ("gate", gate),
+                        ("up", up), ("hidden", hidden), ("dx", dx), ("dw_gate", dw_gate), ("dw_up", dw_up),
+                        ("dw_down", dw_down), ("workspace", workspace)))
+    return _call(index, stream, _gated_ffn_backward, dy, x, w_gate, w_up, w_down, gate, up, hidden, activation,
+                 weight_grads, grad_dtype, dx, dw_gate, dw_up, dw_down, workspace)
+
+
+def _gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, hidden, activation, weight_grads, grad_dtype, dx, dw_gate,
+                        dw_up, dw_down, workspace, stream):
+    code, m, c, f = _ffn_args(x, w_gate, w_up, w_down)
+    dtype, device = x.dtype, x.device
+    _tensor(dy, "dy", dtype, (m, c))
+    for t, name in ((gate, "gate"), (up, "up"), (hidden, "hidden")):
+        _tensor(t, name, dtype, (m, f))
+    if dx is None:
+        dx = _T.empty((m, c), dtype=dtype, device=device)
+    else:
+        _tensor(dx, "dx", dtype, (m, c))
+    given = [t for t in (dw_gate, dw_up, dw_down) if t is not None]
+    if not weight_grads and given:
+        raise VaeError(-1, "dw_gate, dw_up and dw_down need weight_grads")
+    wt = grad_dtype or (given[0].dtype if given else dtype)
+    if weight_grads:
+        if dw_gate is None and dw_up is None:
+            both = _T.empty((2, f, c), dtype=wt, device=device)
+            dw_gate, dw_up = both[0], both[1]
+        elif dw_gate is None:
+            dw_gate = _T.empty((f, c), dtype=wt, device=device)
+        elif dw_up is None:
+            dw_up = _T.empty((f, c), dtype=wt, device=device)
+        if dw_down is None:
+            dw_down = _T.empty((c, f), dtype=wt, device=device)
+        _tensor(dw_gate, "dw_gate", wt, (f, c))
+        _tensor(dw_up, "dw_up", wt, (f, c))
+        _tensor(dw_down, "dw_down", wt, (c, f))
+    desc = _FFN_DESC.pack(code, m, c, f, _activation(activation), code, 0, _type(wt, "grad_dtype"))
+    L = lib()
+    if workspace is None:
+        workspace = _T.empty(max(L.vae_gated_ffn_backward_workspace_bytes(desc), 16), dtype=_T.u8, device=device)
+    _check(L.vae_gated_ffn_backward(desc, dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                    w_down.data_ptr(), gate.data_ptr(), up.data_ptr(), hidden.data_ptr(), dx.data_ptr(),
+                                    _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), *_work(workspace), stream))
+    return dx, dw_gate, dw_up, dw_down
 
 
 # ───────────────────────────── weight layouts ─────────────────────────────

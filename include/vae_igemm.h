@@ -472,6 +472,56 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
                               vae_stream_t stream);
 
 /*
+ * The gated feed-forward block of m tokens of c channels over f hidden ones:
+ *   gate = x w_gate^T, up = x w_up^T, hidden = act(gate) * up,
+ *   y = hidden w_down^T (+ residual).
+ *   x_dev [m][c], w_gate_dev, w_up_dev [f][c] (they may be the halves of one
+ *   tensor), w_down_dev [c][f], all of `type` (VAE_F16 or VAE_BF16), contiguous.
+ *   y_dev [m][c] of y_type: `type`, or VAE_F32 with residual_dev f32 [m][c] or
+ *   NULL (y_dev may be residual_dev).
+ *   gate_dev, up_dev, hidden_dev [m][f] of `type`: written for the gradient with
+ *   save != 0, else NULL.
+ *   activation: VAE_ACT_SILU g / (1 + e^-g), VAE_ACT_GELU g Phi(g),
+ *   VAE_ACT_GELU_TANH g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).
+ * Products are summed in f32; hidden is formed from the f32 gate and up and
+ * rounded to `type` once for its product, which costs y 1.4 times its own
+ * rounding (in f16 |hidden| over 65504 is infinite).
+ * vae_gated_ffn_backward, from the saved gate, up and hidden:
+ *   dhidden = dy w_down, dup = dhidden * act(gate), dgate = dhidden * up * act'(gate),
+ *   dx = dgate w_gate + dup w_up, dw_gate = dgate^T x, dw_up = dup^T x,
+ *   dw_down = dy^T hidden.
+ *   dy_dev [m][c] and dx_dev [m][c] of `type`; dw_*_dev of dw_type (`type` or
+ *   VAE_F32), all three or none. dgate and dup are rounded to `type` for their
+ *   products, in f16 times the power of two that brings the largest |dy| to 4..8,
+ *   so that gradients of any size keep their digits.
+ * Sums run in a fixed order: the same inputs give the same bits.
+ * Requirements: m >= 1; c and f multiples of 8, 8 <= c <= 16384,
+ * 8 <= f <= 65536, m <= 2^24; tensors 16-byte aligned. What is written lies apart from
+ * what is read (but for y and residual) and from one another.
+ * workspace_dev: vae_gated_ffn_workspace_bytes(desc) /
+ * vae_gated_ffn_backward_workspace_bytes(desc) bytes, 16-byte aligned, contents
+ * ignored on entry, NULL where that is 0. Both depend on the desc alone.
+ */
+enum { VAE_ACT_SILU = 0, VAE_ACT_GELU = 1, VAE_ACT_GELU_TANH = 2 };
+typedef struct {
+    int type;
+    int m, c, f;
+    int activation;
+    int y_type;   /* forward: of y */
+    int save;     /* forward: gate, up and hidden are written */
+    int dw_type;  /* backward: of the weights' gradients */
+} vae_gated_ffn_desc;
+size_t vae_gated_ffn_workspace_bytes(const vae_gated_ffn_desc* desc);
+int vae_gated_ffn(const vae_gated_ffn_desc* desc, const void* x_dev, const void* w_gate_dev, const void* w_up_dev,
+                  const void* w_down_dev, const float* residual_dev, void* y_dev, void* gate_dev, void* up_dev,
+                  void* hidden_dev, void* workspace_dev, size_t workspace_bytes, vae_stream_t stream);
+size_t vae_gated_ffn_backward_workspace_bytes(const vae_gated_ffn_desc* desc);
+int vae_gated_ffn_backward(const vae_gated_ffn_desc* desc, const void* dy_dev, const void* x_dev, const void* w_gate_dev,
+                           const void* w_up_dev, const void* w_down_dev, const void* gate_dev, const void* up_dev,
+                           const void* hidden_dev, void* dx_dev, void* dw_gate_dev, void* dw_up_dev, void* dw_down_dev,
+                           void* workspace_dev, size_t workspace_bytes, vae_stream_t stream);
+
+/*
  * Multi-head attention: o = softmax(scale * q k^T over the keys a query sees) v
  * and lse = log(sum of exp) of each row.
  *   q [b][sq][hq][d], k, v [b][sk][hkv][d], o [b][sq][hq][d], all of `type`

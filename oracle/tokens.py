@@ -176,3 +176,31 @@ def qk_norm_rope_backward(dy, x, gamma=None, positions=None, axes=(), theta: flo
     n = x / size
     v = u if gamma is None else u * _f64(gamma)
     return (v - n * (v * n).mean(-1, keepdims=True)) / size, (u * n).sum((0, 1, 2))
+
+
+def activation(g, kind: str):
+    """(act(g), its derivative)."""
+    from scipy.special import erfc, expit
+    g = _f64(g)
+    if kind == "gelu":
+        cdf = 0.5 * erfc(-g / np.sqrt(2.0))
+        return g * cdf, cdf + g * np.exp(-0.5 * g * g) / np.sqrt(2.0 * np.pi)
+    k, a = (1.0, 0.0) if kind == "silu" else (2.0 * np.sqrt(2.0 / np.pi), 0.044715)
+    s = expit(k * (g + a * g ** 3))
+    return g * s, s + g * s * expit(-k * (g + a * g ** 3)) * k * (1.0 + 3.0 * a * g * g)
+
+
+def gated_ffn(x, w_gate, w_up, w_down, kind: str = "silu"):
+    """(y, gate, up, hidden) of (act(x w_gate^T) * (x w_up^T)) w_down^T."""
+    gate, up = _f64(x) @ _f64(w_gate).T, _f64(x) @ _f64(w_up).T
+    hidden = activation(gate, kind)[0] * up
+    return hidden @ _f64(w_down).T, gate, up, hidden
+
+
+def gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, hidden, kind: str = "silu"):
+    """(dx, dw_gate, dw_up, dw_down, dgate, dup) of sum(dy * y) at the given gate, up and hidden."""
+    dy, x, up = _f64(dy), _f64(x), _f64(up)
+    value, slope = activation(gate, kind)
+    dh = dy @ _f64(w_down)
+    dgate, dup = dh * up * slope, dh * value
+    return dgate @ _f64(w_gate) + dup @ _f64(w_up), dgate.T @ x, dup.T @ x, dy.T @ _f64(hidden), dgate, dup
