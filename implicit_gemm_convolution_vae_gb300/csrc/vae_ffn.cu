@@ -15,8 +15,9 @@
 #include <algorithm>
 #include <mutex>
 
+#include "vae_ffn.cuh"
+#include "vae_ffn_few.h"
 #include "vae_overlap.h"
-#include "vae_types.cuh"
 
 namespace vae {
 
@@ -285,28 +286,6 @@ __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
         (void)mbar_wait(smem_u32(s.drain), 0u, &never, p.timeout_ns, p.status, kWhereDrain);
     }
     __syncwarp();
-}
-
-// ───────────────────────────── activations ─────────────────────────────
-
-// act(g), and its derivative.
-template <int kAct>
-__device__ __forceinline__ float act_value(float g) {
-    if constexpr (kAct == VAE_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752440f));
-    const float z = kAct == VAE_ACT_SILU ? g : 1.59576912160573071176f * (g + 0.044715f * g * g * g);
-    return g * __fdividef(1.f, 1.f + __expf(-z));  // (1 + tanh(z / 2)) / 2 is the logistic function of z
-}
-template <int kAct>
-__device__ __forceinline__ float2 act_both(float g) {
-    if constexpr (kAct == VAE_ACT_GELU) {
-        const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752440f));
-        return make_float2(g * cdf, cdf + g * 0.39894228040143267794f * __expf(-0.5f * g * g));
-    }
-    constexpr bool silu = kAct == VAE_ACT_SILU;
-    const float z = silu ? g : 1.59576912160573071176f * (g + 0.044715f * g * g * g);
-    const float dz = silu ? 1.f : 1.59576912160573071176f * (1.f + 0.134145f * g * g);
-    const float s = __fdividef(1.f, 1.f + __expf(-z));
-    return make_float2(g * s, s * (1.f + g * dz * (1.f - s)));
 }
 
 // The power of two that brings the largest |dy| to 4..8 (1 where there is none, or it is not finite).
@@ -940,7 +919,7 @@ size_t vae_gated_ffn_workspace_bytes(const vae_gated_ffn_desc* desc) {
     clear_error();
     if (ffn_check(desc, false) != VAE_OK) return 0;
     // hidden, where it is not saved, and partial sums
-    return (desc->save ? 0 : up256(mf_bytes(*desc))) + parts_bytes(cut_down(*desc), desc->m, desc->c, 1);
+    return (desc->save ? 0 : up256(mf_bytes(*desc))) + (desc->m <= kFewTokens ? 0 : parts_bytes(cut_down(*desc), desc->m, desc->c, 1));
 }
 
 int vae_gated_ffn(const vae_gated_ffn_desc* desc, const void* x_dev, const void* w_gate_dev, const void* w_up_dev,
@@ -973,6 +952,8 @@ int vae_gated_ffn(const vae_gated_ffn_desc* desc, const void* x_dev, const void*
     VAE_TRY(check_device());
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* hidden = save ? hidden_dev : workspace_dev;
+    if (a.m <= kFewTokens)
+        return ffn_few(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, st);
     float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + (save ? 0 : up256(mf_bytes(a))));
     return a.type == VAE_F16
                ? ffn_forward<VAE_F16>(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, parts, st)

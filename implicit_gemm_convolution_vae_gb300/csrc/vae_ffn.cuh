@@ -1,0 +1,28 @@
+// The activations of the gated feed-forward block, for the kernels that form act(gate) * up.
+#pragma once
+
+#include "vae_types.cuh"
+
+namespace vae {
+
+// act(g), and its derivative.
+template <int kAct>
+__device__ __forceinline__ float act_value(float g) {
+    if constexpr (kAct == VAE_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752440f));
+    const float z = kAct == VAE_ACT_SILU ? g : 1.59576912160573071176f * (g + 0.044715f * g * g * g);
+    return g * __fdividef(1.f, 1.f + __expf(-z));  // (1 + tanh(z / 2)) / 2 is the logistic function of z
+}
+template <int kAct>
+__device__ __forceinline__ float2 act_both(float g) {
+    if constexpr (kAct == VAE_ACT_GELU) {
+        const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752440f));
+        return make_float2(g * cdf, cdf + g * 0.39894228040143267794f * __expf(-0.5f * g * g));
+    }
+    constexpr bool silu = kAct == VAE_ACT_SILU;
+    const float z = silu ? g : 1.59576912160573071176f * (g + 0.044715f * g * g * g);
+    const float dz = silu ? 1.f : 1.59576912160573071176f * (1.f + 0.134145f * g * g);
+    const float s = __fdividef(1.f, 1.f + __expf(-z));
+    return make_float2(g * s, s * (1.f + g * dz * (1.f - s)));
+}
+
+}  // namespace vae

@@ -59,7 +59,10 @@ CASES = [(1, 8, 8, "bf16", "silu"), (1, 64, 64, "f16", "gelu"), (3, 16, 40, "bf1
          (255, 200, 264, "bf16", "gelu"), (257, 136, 512, "bf16", "silu"), (256, 512, 2048, "f16", "silu"),
          (300, 576, 1000, "bf16", "gelu_tanh"), (513, 1152, 328, "f16", "silu"), (1000, 264, 520, "bf16", "silu"),
          (5000, 64, 1024, "f16", "gelu"), (20000, 64, 72, "bf16", "silu"), (3000, 520, 2048, "bf16", "silu"),
-         (70000, 8, 24, "f16", "gelu_tanh")]
+         (70000, 8, 24, "f16", "gelu_tanh"),
+         # few tokens: one piece of the contraction and many, rows that end inside a block, contractions over a cluster
+         (2, 8, 4608, "f16", "gelu"), (16, 1152, 1160, "f16", "gelu"), (32, 2304, 72, "bf16", "gelu_tanh"), (31, 24, 6008, "bf16", "silu"),
+         (9, 328, 40, "f16", "silu"), (33, 2304, 2056, "bf16", "silu")]
 
 
 def _case(case):
