@@ -24,8 +24,9 @@ namespace vae {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kAhead = 4;   // pieces of the contraction that a warp has on their way
+constexpr int kSums = 8;    // warps whose sums lie in shared memory
+// Pieces of the contraction that a warp has on their way: as many as leave two blocks an SM their registers.
+constexpr int ahead(int kn) { return kn == 1 ? 3 : 2; }
 constexpr int kRows = 16;
 constexpr int kMaxSplits = 8;
 
@@ -37,6 +38,8 @@ struct FewParams {
     void *gate, *up;         // or NULL
     int out_f32;
     const float* residual;
+    const void* next;        // the weights of the product behind this one, and their bytes: asked for by this one, into L2
+    long long next_bytes;
 };
 
 template <int T>
@@ -57,12 +60,12 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
     return v;
 }
 
-// kN: tokens in eights.
-template <int T, bool kGated, int kN, int kAct>
-__global__ void __launch_bounds__(kWarps * 32) few_kernel(const FewParams p) {
-    constexpr int kMats = kGated ? 2 : 1;
+// kN: tokens in eights; kWarps: 8 (two blocks an SM) or 16 (one).
+template <int T, bool kGated, int kN, int kAct, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_kernel(const FewParams p) {
+    constexpr int kMats = kGated ? 2 : 1, kAhead = ahead(kN);
     constexpr int kOut = kMats * kN * 8 * kRows;  // sums of a block: [matrix][token][row]
-    __shared__ float sums[kWarps][kOut];
+    __shared__ float sums[kSums][kOut];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int splits = static_cast<int>(gridDim.y), split = static_cast<int>(blockIdx.y);
@@ -94,6 +97,11 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const FewParams p) {
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) fetch(s, first + s * kWarps);
     if constexpr (!kGated) pdl_wait();
+    if (kGated && threadIdx.x == 0) {
+        const long long blocks = static_cast<long long>(gridDim.x) * splits, b = static_cast<long long>(blockIdx.x) * splits + split;
+        const long long from = p.next_bytes / 16 * b / blocks * 16, to = p.next_bytes / 16 * (b + 1) / blocks * 16;
+        if (to > from) prefetch_l2_bulk(static_cast<const char*>(p.next) + from, static_cast<uint32_t>(to - from));
+    }
 
     float d[kMats][kN][4] = {};
     const uint16_t* x = static_cast<const uint16_t*>(p.x);
@@ -121,18 +129,26 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const FewParams p) {
             fetch(s, piece + (s + kAhead) * kWarps);
         }
     }
-    // d: rows g, g + 8; tokens 2 t, 2 t + 1
+    // d: rows g, g + 8; tokens 2 t, 2 t + 1. Sixteen warps: the upper ones' first, which the lower ones add to theirs.
+    auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < kMats; ++i)
+        for (int i = 0; i < kMats; ++i)
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sums[warp][(i * kN * 8 + n * 8 + 2 * t + (e & 1)) * kRows + g + (e >> 1) * 8] = d[i][n][e];
+                for (int e = 0; e < 4; ++e)
+                    f(sums[warp % kSums][(i * kN * 8 + n * 8 + 2 * t + (e & 1)) * kRows + g + (e >> 1) * 8], d[i][n][e]);
+    };
+    if constexpr (kWarps > kSums) {
+        if (warp >= kSums) each([](float& at, float v) { at = v; });
+        __syncthreads();
+    }
+    if (warp < kSums) each([](float& at, float v) { at = kWarps > kSums ? v + at : v; });
     __syncthreads();
     for (int o = threadIdx.x; o < kOut; o += kWarps * 32) {
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) v += sums[k][o];
+        for (int k = 0; k < kSums; ++k) v += sums[k][o];
         sums[0][o] = v;
     }
     if (splits > 1) cluster_sync();
@@ -170,14 +186,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const FewParams p) {
     if (splits > 1) cluster_sync();  // the other blocks' sums have been read
 }
 
-template <int T, bool kGated, int kN, int kAct>
-int launch_n(const FewParams& p, cudaStream_t stream) {
-    const int groups = (p.rows + kRows - 1) / kRows, pieces = (p.k + 31) / 32;
-    // Two blocks an SM at least, as long as every warp of a block has a piece.
-    int splits = 1;
-    while (splits < kMaxSplits && groups * splits < 304 && pieces >= 2 * splits * kWarps) splits *= 2;
+template <int T, bool kGated, int kN, int kAct, int kWarps>
+int launch_warps(const FewParams& p, int splits, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(groups, splits);
+    cfg.gridDim = dim3((p.rows + kRows - 1) / kRows, splits);
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -189,8 +201,21 @@ int launch_n(const FewParams& p, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    VAE_CUDA_CHECK(cudaLaunchKernelEx(&cfg, few_kernel<T, kGated, kN, kAct>, p));
+    VAE_CUDA_CHECK(cudaLaunchKernelEx(&cfg, few_kernel<T, kGated, kN, kAct, kWarps>, p));
     return VAE_OK;
+}
+
+template <int T, bool kGated, int kN, int kAct>
+int launch_n(const FewParams& p, cudaStream_t stream) {
+    // One wave of blocks, sixteen warps an SM: a second wave costs more than it brings (1152 x 4608: 288 blocks of the
+    // first product 6.6 us, 576 10.1). Where the rows give at most one block an SM, it has all sixteen warps (512 x
+    // 2048: 6.4 us a call, with eight and twice the clusters 9.5); clusters share the contraction as long as they find
+    // SMs and every warp a piece.
+    const int groups = (p.rows + kRows - 1) / kRows, pieces = (p.k + 31) / 32;
+    if (groups > 152) return launch_warps<T, kGated, kN, kAct, 8>(p, 1, stream);
+    int splits = 1;
+    while (splits < kMaxSplits && groups * splits * 2 <= 152 && pieces >= 2 * splits * 16) splits *= 2;
+    return launch_warps<T, kGated, kN, kAct, 16>(p, splits, stream);
 }
 
 template <int T, bool kGated, int kAct>
@@ -212,6 +237,8 @@ int few_type(const vae_gated_ffn_desc& a, const void* x, const void* wg, const v
     p.out = hidden;
     p.gate = gate;
     p.up = up;
+    p.next = wd;
+    p.next_bytes = 2LL * a.c * a.f;
     const int rc = a.activation == VAE_ACT_SILU   ? launch_tokens<T, true, VAE_ACT_SILU>(p, stream)
                    : a.activation == VAE_ACT_GELU ? launch_tokens<T, true, VAE_ACT_GELU>(p, stream)
                                                   : launch_tokens<T, true, VAE_ACT_GELU_TANH>(p, stream);
