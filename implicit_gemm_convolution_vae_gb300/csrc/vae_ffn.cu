@@ -33,16 +33,15 @@ constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;     // two accumulators
 constexpr int kGroup = 8;               // row tiles that share their column tiles in L2
 constexpr int kPairs = 76;              // that the plan counts with
+constexpr int kAmaxBlocks = 128;        // that look for the largest |dy|, at most
 
 // The products. A and B stand as [rows][contraction] (K-major) or [contraction][rows].
 enum : int {
     kGate,      // x, (Wg, Wu) -> hidden (gate, up)
     kDown,      // hidden, Wd -> y
     kBackGate,  // dy, Wd^T -> dgate, dup
-    kDx,        // (dgate, dup), (Wg, Wu)^T -> dx
-    kDw,        // dgate^T, x^T -> dWg; dup^T, x^T -> dWu; hidden^T, dy^T -> dWd^T
+    kGrad,      // (dgate, dup), (Wg, Wu)^T -> dx; dgate^T, x^T -> dWg; dup^T, x^T -> dWu; hidden^T, dy^T -> dWd^T
 };
-__host__ __device__ constexpr bool a_mn(int kind) { return kind == kDw; }
 __host__ __device__ constexpr bool b_mn(int kind) { return kind >= kBackGate; }
 
 // Stages of the ring, and beside it what kBackGate's epilogue works in: boxes of 32 rows x 64 columns of gate and up,
@@ -57,27 +56,40 @@ __host__ __device__ constexpr int smem_bytes(int kind) { return 1024 + ring_stag
 static_assert(smem_bytes(kGate) <= 232448 && smem_bytes(kBackGate) <= 232448, "shared memory over 227 KB");
 
 struct Maps {
-    CUtensorMap a[3], b[3];
+    CUtensorMap a[3];          // kGrad: dgate, dup, hidden
+    CUtensorMap b[4];          // kGate: Wg, Wu; kGrad: Wg, Wu, x, dy
     CUtensorMap side[4];       // kBackGate: gate, up, dgate, dup
 };
 
-// How a product is cut: column tiles of `wide` and what is left of the columns (`rest`, 0: nothing), the
-// contraction in `splits`. `fit`: rest tiles that take about as long as a full one.
-struct Cut {
-    int wide, rest, splits, fit;
+// Products of one shape and how they are cut: column tiles of `wide` and what is left of the columns (`rest`, 0:
+// nothing), the contraction of `nk` stages in `splits`. kGrad has two of them (dx; the weights' gradients), the
+// others one.
+struct Group {
+    int rows, cols, problems, nk;
+    int wide, rest, splits;
+    int nm, nfull;             // row tiles, column tiles of full width
+};
+
+// Which pair computes what: the tiles of the four classes (group 0's full ones and rests, group 1's) go to the least
+// laden pairs, the longest ones first. Pairs that got the same lie side by side: `n` runs of them, with a count of each class.
+constexpr int kRuns = 6;
+struct Deal {
+    int n;
+    int order[4];
+    int pairs[kRuns], count[kRuns][4];
 };
 
 struct Params {
-    int rows, cols, problems;  // of D
-    Cut cut;
-    int nm, nfull;             // row tiles, column tiles of full width
-    int full, rests;           // tiles of full width, and of the rest
-    int nk, segments;          // stages of a tile (per segment: products that add up)
-    void* out[3];              // kGate: hidden, gate, up; kDown, kDx, kDw: D of each problem
-    float* parts;              // with splits: D of each problem and split, [problems * splits][rows][cols]
-    int out_f32;
+    Group group[2];
+    Deal deal;
+    int half;                  // kGrad: stages of dx's first segment
+    void* out[4];              // kGate: hidden, gate, up; kDown: y; kGrad: dx, dWg, dWu, dWd
+    float* parts[2];           // with splits: D of each problem and split, [problems * splits][rows][cols]
+    int out_f32[2];
     const float* residual;
-    const unsigned* amax;      // f16 gradients: the largest |dy|'s bits
+    const unsigned* amax;      // f16 gradients: the bits of the largest |dy|, from `amax_n` blocks
+    int amax_n;
+    int late;                  // kBackGate: only the epilogue needs the kernel before (that is the one that looks for the largest |dy|)
     int wide;                  // rows of D on 32 bytes
     DevStatus* status;
     unsigned long long timeout_ns;
@@ -109,49 +121,54 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
 }
 
 struct Tile {
-    int z, m0, n0, n;  // problem (and split: problem * splits + split), the pair's first row, the columns [n0, n0 + n)
+    int g, z, part;    // group, problem (in Params::out's order), partial sums
+    int m0, n0, n;     // the pair's first row, the columns [n0, n0 + n)
     int k0, k1;        // stages
 };
-// The i-th tile of pair `pair` of `pairs`; false behind its last. Tiles of full width are dealt out in turn;
-// what is left of the columns goes first to the pairs that have one full tile less (as many as fit into one), so
-// that it costs no turn of its own. Row tiles lie in groups of kGroup, their column tiles side by side: the
-// pairs at work share rows of A and of B in L2.
-__device__ __forceinline__ bool tile_at(const Params& p, int pair, int pairs, int i, Tile* r) {
-    const int q = p.full / pairs, heavy = p.full - q * pairs;
-    const int mine = q + (pair < heavy ? 1 : 0);
-    int t = -1;
-    if (i < mine) {
-        t = pair + i * pairs;
-    } else {
-        i -= mine;
-        const int light = heavy > 0 ? pairs - heavy : 0;
-        const int first = light * p.cut.fit < p.rests ? light * p.cut.fit : p.rests;
-        const int own = pair >= heavy && light > 0 && first > pair - heavy ? (first - (pair - heavy) + light - 1) / light : 0;
-        const int j = i < own ? pair - heavy + i * light : first + pair + (i - own) * pairs;
-        if (j >= p.rests) return false;
-        t = p.full + j;
+// The i-th tile of pair `pair`; false behind its last. Row tiles lie in groups of kGroup, their column tiles side by
+// side: the pairs at work share rows of A and of B in L2.
+__host__ __device__ __forceinline__ bool tile_at(const Params& p, int pair, int i, Tile* r) {
+    int run = 0, before = 0;
+    while (pair >= before + p.deal.pairs[run]) before += p.deal.pairs[run++];
+    int c = -1;
+    for (int o = 0; o < 4; ++o) {
+        const int n = p.deal.count[run][p.deal.order[o]];
+        if (i < n) {
+            c = p.deal.order[o];
+            break;
+        }
+        i -= n;
     }
+    if (c < 0) return false;
+    // the class's tiles are dealt out round by round, over the pairs that have as many
+    int t = pair - before;
+    for (int q = 0; q < p.deal.n; ++q) {
+        const int n = p.deal.count[q][c];
+        t += (n < i ? n : i) * p.deal.pairs[q] + (q < run && n > i ? p.deal.pairs[q] : 0);
+    }
+    const Group& g = p.group[c >> 1];
     int nt;
-    if (t < p.full) {
-        const int each = p.nm * p.nfull;
-        r->z = t / each;
-        t -= r->z * each;
-        const int g = t / (kGroup * p.nfull), in = t - g * kGroup * p.nfull;
-        const int tall = p.nm - g * kGroup < kGroup ? p.nm - g * kGroup : kGroup;
+    if ((c & 1) == 0) {
+        const int each = g.nm * g.nfull;
+        r->part = t / each;
+        t -= r->part * each;
+        const int w = t / (kGroup * g.nfull), in = t - w * kGroup * g.nfull;
+        const int tall = g.nm - w * kGroup < kGroup ? g.nm - w * kGroup : kGroup;
         nt = in / tall;
-        r->m0 = (g * kGroup + in - nt * tall) * 2 * kTile;
-        r->n = p.cut.wide;
+        r->m0 = (w * kGroup + in - nt * tall) * 2 * kTile;
+        r->n = g.wide;
     } else {
-        t -= p.full;
-        r->z = t / p.nm;
-        r->m0 = (t - r->z * p.nm) * 2 * kTile;
-        nt = p.nfull;
-        r->n = p.cut.rest;
+        r->part = t / g.nm;
+        r->m0 = (t - r->part * g.nm) * 2 * kTile;
+        nt = g.nfull;
+        r->n = g.rest;
     }
-    r->n0 = nt * p.cut.wide;
-    const int s = r->z % p.cut.splits, all = p.nk * p.segments;
-    r->k0 = static_cast<int>(static_cast<long long>(all) * s / p.cut.splits);
-    r->k1 = static_cast<int>(static_cast<long long>(all) * (s + 1) / p.cut.splits);
+    r->n0 = nt * g.wide;
+    r->g = c >> 1;
+    const int z = r->part / g.splits, s = r->part - z * g.splits;
+    r->z = r->g + z;
+    r->k0 = static_cast<int>(static_cast<long long>(g.nk) * s / g.splits);
+    r->k1 = static_cast<int>(static_cast<long long>(g.nk) * (s + 1) / g.splits);
     return true;
 }
 
@@ -169,15 +186,10 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// One operand of a stage: `rows` rows (a K-major map's boxes hold as many) from `row` on, 64 of the contraction from `k` on.
-template <bool kMn>
-__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int row, int rows, int k) {
-    if constexpr (kMn) {  // boxes of 64 rows each, as they lie
-        tma_load_2d_pair(smem_u32(dst), map, bar, row, k);
-        if (rows > 64) tma_load_2d_pair(smem_u32(dst + kOperand / 2), map, bar, row + 64, k);
-    } else {
-        tma_load_2d_pair(smem_u32(dst), map, bar, k, row);
-    }
+// Rows of an operand that lies MN-major, in boxes of 64, 64 of the contraction from `k` on.
+__device__ __forceinline__ void load_mn(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int row, int rows, int k) {
+    tma_load_2d_pair(smem_u32(dst), map, bar, row, k);
+    if (rows > 64) tma_load_2d_pair(smem_u32(dst + kOperand / 2), map, bar, row + 64, k);
 }
 
 // Descriptor of an MN-major operand: rows of 64 along M or N (128 bytes, swizzled), eight
@@ -199,26 +211,35 @@ __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, 
     int stage = 0;
     uint32_t phase = 0, armed = 0, arm_par = 0;
     bool ok = true;
-    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
-    // rows of B that a CTA loads, always those of a full tile
-    const int brows = kKind == kGate ? p.cut.wide : p.cut.wide / 2;
-    const uint32_t bytes = kOperand + (b_mn(kKind) ? (brows > 64 ? 2u : 1u) * 64 * 128 : static_cast<uint32_t>(brows) * 128);
+    const int pair = static_cast<int>(blockIdx.x >> 1);
     Tile ti;
-    for (int i = 0; ok && tile_at(p, pair, pairs, i, &ti); ++i) {
+    for (int i = 0; ok && tile_at(p, pair, i, &ti); ++i) {
         const int row = ti.m0 + rank * kTile, col = kKind == kGate ? ti.n0 : ti.n0 + rank * (ti.n / 2);
-        const int z = ti.z / p.cut.splits;
+        // rows of B that a CTA loads: those of a full tile where the map's box says so, else boxes of 64
+        const int brows = b_mn(kKind) ? ti.n / 2 : kKind == kGate ? p.group[0].wide : p.group[0].wide / 2;
+        const uint32_t bytes = kOperand + (b_mn(kKind) ? (brows > 64 ? 2u : 1u) * 64 * 128 : static_cast<uint32_t>(brows) * 128);
         for (int kk = ti.k0; kk < ti.k1; ++kk) {
-            const int seg = kKind == kDx && kk >= p.nk ? 1 : 0, k = kk - seg * p.nk;
-            const CUtensorMap* ma = &maps.a[kKind == kDx ? seg : z];
-            const CUtensorMap* mb = &maps.b[kKind == kDx ? seg : kKind == kGate ? rank : z];
             ok = mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, s.abort_flag, p.timeout_ns, p.status, kWhereProducerEmpty);
             if (!ok) break;
             const uint32_t fb = smem_u32(&s.full[stage]);
             if (rank == 0) mbar_arrive_expect_tx(fb, 2u * bytes);
             const uint32_t fb0 = mapa_shared(fb, 0u);
-            uint8_t* a = s.ring + stage * kStage;
-            load_operand<a_mn(kKind)>(a, ma, fb0, row, kTile, k * kBk);
-            load_operand<b_mn(kKind)>(a + kOperand, mb, fb0, col, brows, k * kBk);
+            uint8_t *a = s.ring + stage * kStage, *b = a + kOperand;
+            if constexpr (kKind == kGrad) {
+                if (ti.g == 0) {  // dx: rows of dgate or dup as they lie, in boxes of 64
+                    const int seg = kk >= p.half ? 1 : 0, k = (kk - seg * p.half) * kBk;
+                    tma_load_2d_pair(smem_u32(a), &maps.a[seg], fb0, k, row);
+                    tma_load_2d_pair(smem_u32(a + kOperand / 2), &maps.a[seg], fb0, k, row + 64);
+                    load_mn(b, &maps.b[seg], fb0, col, brows, k);
+                } else {
+                    load_mn(a, &maps.a[ti.z - 1], fb0, row, kTile, kk * kBk);
+                    load_mn(b, &maps.b[ti.z == 3 ? 3 : 2], fb0, col, brows, kk * kBk);
+                }
+            } else {
+                tma_load_2d_pair(smem_u32(a), &maps.a[0], fb0, kk * kBk, row);
+                if constexpr (kKind == kBackGate) load_mn(b, &maps.b[0], fb0, col, brows, kk * kBk);
+                else tma_load_2d_pair(smem_u32(b), &maps.b[kKind == kGate ? rank : 0], fb0, kk * kBk, col);
+            }
             armed |= 1u << stage;
             arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
             if (++stage == kStages) {
@@ -241,19 +262,21 @@ template <int T, int kKind>
 __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
     constexpr int kStages = ring_stages(kKind);
     constexpr uint32_t ab = T == VAE_BF16 ? 1u : 0u;
-    constexpr uint32_t idesc0 = (1u << 4) | (ab << 7) | (ab << 10) | ((a_mn(kKind) ? 1u : 0u) << 15) |
-                                ((b_mn(kKind) ? 1u : 0u) << 16) | ((2u * kTile >> 4) << 24);
-    constexpr uint32_t astep = a_mn(kKind) ? 2048 >> 4 : 2, bstep = b_mn(kKind) ? 2048 >> 4 : 2;
+    constexpr uint32_t idesc0 = (1u << 4) | (ab << 7) | (ab << 10) | ((b_mn(kKind) ? 1u : 0u) << 16) | ((2u * kTile >> 4) << 24);
+    constexpr uint32_t bstep = b_mn(kKind) ? 2048 >> 4 : 2;
     const uint32_t ring = smem_u32(s.ring);
-    const uint64_t ad = a_mn(kKind) ? mn_desc(ring) : sw128_kmajor_desc(ring);
+    const uint64_t ak = sw128_kmajor_desc(ring), am = mn_desc(ring);
     const uint64_t bd = b_mn(kKind) ? mn_desc(ring + kOperand) : sw128_kmajor_desc(ring + kOperand);
     int stage = 0, buf = 0;
     uint32_t phase = 0, accphase = 0;
     bool ok = true;
-    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    const int pair = static_cast<int>(blockIdx.x >> 1);
     Tile ti;
-    for (int i = 0; ok && tile_at(p, pair, pairs, i, &ti); ++i) {
-        const uint32_t idesc = idesc0 | static_cast<uint32_t>((kKind == kGate ? 2 * ti.n : ti.n) >> 3) << 17;
+    for (int i = 0; ok && tile_at(p, pair, i, &ti); ++i) {
+        const bool a_mn = kKind == kGrad && ti.g == 1;
+        const uint64_t ad = a_mn ? am : ak;
+        const uint32_t astep = a_mn ? 2048 >> 4 : 2;
+        const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u) | static_cast<uint32_t>((kKind == kGate ? 2 * ti.n : ti.n) >> 3) << 17;
         const int nk = ti.k1 - ti.k0;
         ok = warp_all(mbar_wait_cluster(smem_u32(&s.acce[buf]), accphase ^ 1u, s.abort_flag, p.timeout_ns, p.status, kWhereMmaAccEmpty));
         if (!ok) break;
@@ -288,10 +311,12 @@ __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
     __syncwarp();
 }
 
-// The power of two that brings the largest |dy| to 4..8 (1 where there is none, or it is not finite).
-__device__ __forceinline__ float dy_scale(const unsigned* amax) {
-    if (amax == nullptr) return 1.f;
-    const unsigned bits = *amax;
+// The power of two that brings the largest |dy| to 4..8 (1 where there is none, or it is not finite). The whole warp.
+__device__ __forceinline__ float dy_scale(const Params& p) {
+    if (p.amax == nullptr) return 1.f;
+    unsigned bits = 0u;
+    for (int i = threadIdx.x & 31; i < p.amax_n; i += 32) bits = max(bits, p.amax[i]);
+    bits = __reduce_max_sync(0xffffffffu, bits);
     const int e = static_cast<int>(bits >> 23) - 127;
     return bits == 0u || bits >= 0x7f800000u ? 1.f : __uint_as_float(static_cast<unsigned>(2 - e + 127) << 23);
 }
@@ -346,7 +371,7 @@ struct Boxes {
     bool more = false;
     int asked = 0, taken = 0;
 
-    __device__ __forceinline__ void ask(const Params& p, const Smem& s, const Maps& maps, int pair, int pairs, int quad, int lane, int rank) {
+    __device__ __forceinline__ void ask(const Params& p, const Smem& s, const Maps& maps, int pair, int quad, int lane, int rank) {
         if (!more) return;
         const int buf = quad * kBoxBufs + asked % kBoxBufs;
         if (lane == 0) {
@@ -364,7 +389,7 @@ struct Boxes {
         ++asked;
         if ((++box) * 64 >= ti.n) {
             box = 0;
-            more = tile_at(p, pair, pairs, ++i, &ti);
+            more = tile_at(p, pair, ++i, &ti);
         }
     }
 };
@@ -376,27 +401,27 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     int buf = 0;
     uint32_t phase = 0;
-    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    const int pair = static_cast<int>(blockIdx.x >> 1);
+    if (kKind == kBackGate && p.late) pdl_wait();
+    const float gain = kKind >= kBackGate ? dy_scale(p) : 1.f;
     Boxes boxes;
     if constexpr (kKind == kBackGate) {
-        boxes.more = half == 0 && tile_at(p, pair, pairs, 0, &boxes.ti);
-        for (int k = 0; k + 1 < kBoxBufs; ++k) boxes.ask(p, s, maps, pair, pairs, quad, lane, rank);
+        boxes.more = half == 0 && tile_at(p, pair, 0, &boxes.ti);
+        for (int k = 0; k + 1 < kBoxBufs; ++k) boxes.ask(p, s, maps, pair, quad, lane, rank);
     }
     bool ok = true;
     Tile ti;
-    for (int i = 0; ok && tile_at(p, pair, pairs, i, &ti); ++i) {
-        const int row = ti.m0 + rank * kTile + quad * 32 + lane, cols = p.cols;
-        const bool live = row < p.rows;
+    for (int i = 0; ok && tile_at(p, pair, i, &ti); ++i) {
+        const Group& gr = p.group[ti.g];
+        const int row = ti.m0 + rank * kTile + quad * 32 + lane, cols = gr.cols, rows = gr.rows;
+        const bool live = row < rows;
         const long long at0 = static_cast<long long>(row) * cols;
         const int mine = ti.n / 2, n0 = ti.n0 + half * mine;  // this warp's columns
         ok = warp_all(mbar_wait_cluster(smem_u32(&s.accf[buf]), phase, s.abort_flag, p.timeout_ns, p.status, kWhereEpiAccFull));
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem + lanes + static_cast<uint32_t>(buf * kMaxCols + half * mine);
-        const int z = ti.z / p.cut.splits;
-        float scale = 1.f;
-        if constexpr (kKind == kBackGate) scale = dy_scale(p.amax);
-        if constexpr (kKind == kDx || kKind == kDw) scale = z < 2 ? 1.f / dy_scale(p.amax) : 1.f;
+        const float scale = kKind == kBackGate ? gain : kKind == kGrad && ti.z < 3 ? 1.f / gain : 1.f;
         if constexpr (kKind == kBackGate) {
             const int row0 = ti.m0 + rank * kTile + quad * 32;
             const uint32_t at = tmem + lanes + static_cast<uint32_t>(buf * kMaxCols + half * 32);
@@ -435,14 +460,14 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
                     ok = warp_all(mbar_wait(smem_u32(&s.done[sbuf]), turn, s.abort_flag, p.timeout_ns, p.status, kWhereEpiAccFull));
                     if (!ok) break;
                     if (lane == 0) {
-                        if (ti.n0 + b * 64 < cols && row0 < p.rows) {
+                        if (ti.n0 + b * 64 < cols && row0 < rows) {
                             box_store(&maps.side[2], box, ti.n0 + b * 64, row0);
                             box_store(&maps.side[3], box + kBox, ti.n0 + b * 64, row0);
                         }
                         bulk_commit_group();
                         bulk_wait_read_1();  // the box before has left its buffer, which the next one takes
                     }
-                    boxes.ask(p, s, maps, pair, pairs, quad, lane, rank);
+                    boxes.ask(p, s, maps, pair, quad, lane, rank);
                 }
             }
         }
@@ -472,38 +497,38 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
                     store16(static_cast<uint16_t*>(p.out[2]) + at0 + n, pack16<T>(v), left, p.wide);
                 }
             } else {
-                    tmem_ld_wait_regs(x);
+                tmem_ld_wait_regs(x);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]) * scale;
-                    if (!live) continue;
-                    const bool split = p.cut.splits > 1;
-                    float* part = p.parts + static_cast<long long>(ti.z) * p.rows * cols;
-                    if (kKind == kDw && z == 2) {
-                        // D^T = hidden^T dy: lanes are neighbours along a row of dWd
-                        const long long at = static_cast<long long>(n) * p.rows + row;
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]) * scale;
+                if (!live) continue;
+                const bool split = gr.splits > 1, f32 = p.out_f32[ti.g] != 0;
+                float* part = p.parts[ti.g] + static_cast<long long>(ti.part) * rows * cols;
+                if (kKind == kGrad && ti.z == 3) {
+                    // D^T = hidden^T dy: lanes are neighbours along a row of dWd
+                    const long long at = static_cast<long long>(n) * rows + row;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            if (k >= left) continue;
-                            const long long o = at + static_cast<long long>(k) * p.rows;
-                            if (split) part[o] = v[k];
-                            else if (p.out_f32) static_cast<float*>(p.out[2])[o] = v[k];
-                            else static_cast<typename Elem<T>::type*>(p.out[2])[o] = from_f32<T>(v[k]);
-                        }
-                    } else if (split || p.out_f32) {
-                        float* y = split ? part : static_cast<float*>(p.out[z]);
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            if (k >= left) continue;
-                            float4 r = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                            if (kKind == kDown && !split && p.residual != nullptr) {
-                                const float4 o = *reinterpret_cast<const float4*>(p.residual + at0 + n + k);
-                                r = make_float4(r.x + o.x, r.y + o.y, r.z + o.z, r.w + o.w);
-                            }
-                            *reinterpret_cast<float4*>(y + at0 + n + k) = r;
-                        }
-                    } else {
-                        store16(static_cast<uint16_t*>(p.out[z]) + at0 + n, pack16<T>(v), left, p.wide);
+                    for (int k = 0; k < 16; ++k) {
+                        if (k >= left) continue;
+                        const long long o = at + static_cast<long long>(k) * rows;
+                        if (split) part[o] = v[k];
+                        else if (f32) static_cast<float*>(p.out[3])[o] = v[k];
+                        else static_cast<typename Elem<T>::type*>(p.out[3])[o] = from_f32<T>(v[k]);
                     }
+                } else if (split || f32) {
+                    float* y = split ? part : static_cast<float*>(p.out[ti.z]);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        if (k >= left) continue;
+                        float4 r = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                        if (kKind == kDown && !split && p.residual != nullptr) {
+                            const float4 o = *reinterpret_cast<const float4*>(p.residual + at0 + n + k);
+                            r = make_float4(r.x + o.x, r.y + o.y, r.z + o.z, r.w + o.w);
+                        }
+                        *reinterpret_cast<float4*>(y + at0 + n + k) = r;
+                    }
+                } else {
+                    store16(static_cast<uint16_t*>(p.out[ti.z]) + at0 + n, pack16<T>(v), left, p.wide);
+                }
             }
         }
         tc_fence_before();
@@ -557,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&maps.a[0]);
         tma_prefetch_desc(&maps.b[0]);
     }
-    pdl_wait();
+    if (kKind != kBackGate || !p.late) pdl_wait();
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers and TMEM exist before any remote arrive or pair product
@@ -587,11 +612,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// The largest |x| of f16 values, as the bits of an f32 (an atomic maximum has no order); *amax is 0 before.
-__global__ void __launch_bounds__(256) amax_kernel(const uint4* x, long long n8, unsigned* amax) {
+// The largest |x| of f16 values, as the bits of an f32, one from each block.
+__global__ void __launch_bounds__(512) amax_kernel(const uint4* x, long long n8, unsigned* amax) {
+    __shared__ unsigned tops[16];
     pdl_wait();
+    pdl_launch_dependents();  // the next kernel's products may start: only its epilogue waits for this one
     unsigned top = 0u;
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<long long>(gridDim.x) * 256) {
+    for (long long i = static_cast<long long>(blockIdx.x) * 512 + threadIdx.x; i < n8; i += static_cast<long long>(gridDim.x) * 512) {
         const uint4 v = __ldg(x + i);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -601,34 +628,45 @@ __global__ void __launch_bounds__(256) amax_kernel(const uint4* x, long long n8,
         }
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0 && top != 0u) atomicMax(amax, top);
-    pdl_launch_dependents();
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        top = __reduce_max_sync(0xffffffffu, threadIdx.x < 16 ? tops[threadIdx.x] : 0u);
+        if (threadIdx.x == 0) amax[blockIdx.x] = top;
+    }
 }
 
+struct JoinParams {
+    const float* parts[4];
+    void* out[4];
+    long long n8[4];
+    int splits[4], f32[4];
+    const float* residual;
+};
 // The splits' sums, in order, eight elements a thread: D of each problem in its type.
 template <int T>
-__global__ void __launch_bounds__(256) join_kernel(const float* parts, int splits, long long n8, int out_f32, void* out0, void* out1,
-                                                   void* out2, const float* residual) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p) {
     pdl_wait();
-    const int z = blockIdx.y;
-    void* out = z == 0 ? out0 : z == 1 ? out1 : out2;
+    const int z = blockIdx.y, splits = p.splits[z];
+    const long long n8 = p.n8[z];
+    const float* parts = p.parts[z];
     for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<long long>(gridDim.x) * 256) {
         float v[8];
-        load8<VAE_F32>(parts + (static_cast<long long>(z) * splits * n8 + i) * 8, v);
+        load8<VAE_F32>(parts + i * 8, v);
         for (int s = 1; s < splits; ++s) {
             float w[8];
-            load8<VAE_F32>(parts + ((static_cast<long long>(z) * splits + s) * n8 + i) * 8, w);
+            load8<VAE_F32>(parts + (s * n8 + i) * 8, w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += w[k];
         }
-        if (residual != nullptr) {
+        if (p.residual != nullptr) {
             float w[8];
-            load8<VAE_F32>(residual + i * 8, w);
+            load8<VAE_F32>(p.residual + i * 8, w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += w[k];
         }
-        if (out_f32) store8<VAE_F32>(static_cast<float*>(out) + i * 8, v);
-        else store8<T>(static_cast<typename Elem<T>::type*>(out) + i * 8, v);
+        if (p.f32[z]) store8<VAE_F32>(static_cast<float*>(p.out[z]) + i * 8, v);
+        else store8<T>(static_cast<typename Elem<T>::type*>(p.out[z]) + i * 8, v);
     }
     pdl_launch_dependents();
 }
@@ -646,44 +684,143 @@ int ffn_map(CUtensorMap* map, int type, const void* p, int rows, int inner, int 
 
 // Cycles that a pair takes for a stage of a tile of n accumulator columns, as measured: the stage's bytes from L2, 64 a
 // cycle and CTA, or below that the hand-over between loads and products.
-double stage_cycles(int n) { return std::max(430.0, 1.13 * (256 + n)); }
+int stage_cycles(int n) { return std::max(430, (256 + n) * 113 / 100); }
 
-// How D (rows x cols, `problems` of them) with `nk` stages in all is cut: the tile width and the number of splits with
-// the least time, counted in cycles of the busiest pair. Wide tiles read the least; narrow ones and splits give work
-// to more SMs. Splits cost a second kernel (4000 cycles) that reads the f32 sums that they write (2700 bytes a cycle
-// both ways).
-Cut plan_cut(int kind, int rows, int cols, int nk, int problems) {
-    const bool gated = kind == kGate || kind == kBackGate;
-    const int per = kind == kGate ? 2 : 1, unit = 32;  // accumulator columns per column; widths are multiples of it
-    const long long nm = (rows + 2 * kTile - 1) / (2 * kTile);
-    Cut best{};
-    double least = 0;
-    for (int wide = kMaxCols / per; wide >= 64 / per && wide >= unit; wide -= 64 / per) {
-        if (wide % unit != 0) continue;
-        for (int splits = 1; splits <= 8 && splits <= std::max(1, nk / 4) && (splits == 1 || !gated); ++splits) {
-            Cut c;
-            c.wide = wide;
-            c.splits = splits;
-            c.rest = (cols % wide + unit - 1) / unit * unit;
-            const long long each = nm * problems * splits, full = each * (cols / wide), rests = c.rest > 0 ? each : 0;
-            const double one = stage_cycles(wide * per), part = c.rest > 0 ? stage_cycles(c.rest * per) : one;
-            c.fit = c.rest > 0 ? std::max(1, static_cast<int>(one / part)) : 0;
-            const long long q = full / kPairs, heavy = full % kPairs, light = heavy > 0 ? kPairs - heavy : 0;
-            const long long first = std::min(rests, light * c.fit), over = rests - first;
-            double turns = std::max((q + (heavy > 0)) * one, q * one + (light > 0 ? (first + light - 1) / light : 0) * part);
-            turns += (over + kPairs - 1) / kPairs * part;
-            double t = turns * ((nk + splits - 1) / splits) + 10.0 * wide;  // (the last tile's epilogue)
-            if (splits > 1) t += 4000 + 8.0 * splits * problems * rows * cols / 2700;
-            if (best.wide == 0 || t < least) {
-                best = c;
-                least = t;
-            }
+int class_tiles(const Group& g, int rest) {
+    return rest != 0 ? (g.rest > 0 ? g.problems * g.splits * g.nm : 0) : g.problems * g.splits * g.nm * g.nfull;
+}
+// Deals the classes' tiles out over `pairs` pairs; returns the cycles of the one with the most.
+long long deal_out(const Group* groups, int count, int per, int pairs, Deal* d) {
+    long long cost[4] = {}, load[kRuns] = {};
+    int tiles[4] = {};
+    *d = Deal{};
+    d->n = 1;
+    d->pairs[0] = pairs;
+    for (int c = 0; c < 4; ++c) {
+        d->order[c] = c;
+        if (c >> 1 >= count) continue;
+        const Group& g = groups[c >> 1];
+        tiles[c] = class_tiles(g, c & 1);
+        cost[c] = 400 + static_cast<long long>(stage_cycles(((c & 1) != 0 ? g.rest : g.wide) * per)) * ((g.nk + g.splits - 1) / g.splits);
+    }
+    std::sort(d->order, d->order + 4, [&](int a, int b) { return cost[a] != cost[b] ? cost[a] > cost[b] : a < b; });
+    for (int c : d->order) {
+        if (tiles[c] == 0) continue;
+        const long long k = cost[c];
+        // the highest level that the pairs can be filled to with these tiles
+        long long lo = 0, hi = 0;
+        for (int r = 0; r < d->n; ++r) hi = std::max(hi, load[r]);
+        hi += k * (tiles[c] / pairs + 1) + 1;
+        const auto filled = [&](long long level) {
+            long long n = 0;
+            for (int r = 0; r < d->n; ++r) n += level > load[r] ? (level - load[r]) / k * d->pairs[r] : 0;
+            return n;
+        };
+        while (hi - lo > 1) {
+            const long long mid = (lo + hi) / 2;
+            (filled(mid) <= tiles[c] ? lo : hi) = mid;
         }
+        int left = tiles[c] - static_cast<int>(filled(lo));
+        for (int r = 0; r < d->n; ++r) {
+            const int n = lo > load[r] ? static_cast<int>((lo - load[r]) / k) : 0;
+            d->count[r][c] = n;
+            load[r] += n * k;
+        }
+        // one more each for the least laden
+        while (left > 0) {
+            int r = -1;
+            for (int q = 0; q < d->n; ++q)
+                if (d->count[q][c] >= 0 && (r < 0 || load[q] < load[r])) r = q;
+            if (d->pairs[r] > left) {  // a part of this run
+                for (int q = d->n++; q > r; --q) {
+                    d->pairs[q] = d->pairs[q - 1];
+                    load[q] = load[q - 1];
+                    std::copy(d->count[q - 1], d->count[q - 1] + 4, d->count[q]);
+                }
+                d->pairs[r] = left;
+                d->pairs[r + 1] -= left;
+            }
+            left -= d->pairs[r];
+            ++d->count[r][c];
+            load[r] += k;
+        }
+    }
+    return *std::max_element(load, load + d->n);
+}
+
+// How the products of a kernel are cut and dealt out.
+struct Plan {
+    Group group[2];
+    Deal deal;
+};
+Group cut_group(int rows, int cols, int problems, int nk, int wide, int splits) {
+    Group g{rows, cols, problems, nk, wide, (cols % wide + 31) / 32 * 32, splits};
+    g.nm = (rows - 1) / (2 * kTile) + 1;
+    g.nfull = cols / wide;
+    return g;
+}
+size_t parts_bytes(const Group& g) {
+    return g.splits > 1 ? static_cast<size_t>(g.splits) * g.problems * g.rows * g.cols * sizeof(float) : 0;
+}
+// The tile width and the splits with the least time, counted in cycles of the busiest pair. Wide tiles read the least;
+// narrow ones and splits give work to more SMs. Splits cost a second kernel (4000 cycles) that reads the f32 sums that
+// they write (2700 bytes a cycle both ways). `base`: the groups uncut.
+Plan make_plan(int kind, const Group* base, int count) {
+    const int per = kind == kGate ? 2 : 1;  // accumulator columns per column
+    const bool whole = kind == kGate || kind == kBackGate;  // (their epilogues need the whole sums)
+    Plan best{};
+    long long least = -1;
+    for (int wide = kMaxCols; wide >= 64; wide -= 64) {
+        const auto cut = [&](int g, int splits) {
+            return cut_group(base[g].rows, base[g].cols, base[g].problems, base[g].nk, wide / per, splits);
+        };
+        const auto most = [&](int g) { return whole ? 1 : std::min(8, std::max(1, base[g].nk / 4)); };
+        for (int s0 = 1; s0 <= most(0); ++s0)
+            for (int s1 = 1; s1 <= (count > 1 ? most(1) : 1); ++s1) {
+                Plan p{};
+                p.group[0] = cut(0, s0);
+                if (count > 1) p.group[1] = cut(1, s1);
+                long long t = deal_out(p.group, count, per, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
+                const size_t parts = parts_bytes(p.group[0]) + (count > 1 ? parts_bytes(p.group[1]) : 0);
+                if (parts > 0) t += 4000 + static_cast<long long>(2 * parts / 2700);
+                if (least < 0 || t < least) {
+                    best = p;
+                    least = t;
+                }
+                // with many tiles neither splits nor narrow ones can win
+                if (class_tiles(p.group[0], 0) + (count > 1 ? class_tiles(p.group[1], 0) : 0) >= 4 * kPairs) return best;
+            }
     }
     return best;
 }
-size_t parts_bytes(const Cut& c, int rows, int cols, int problems) {
-    return c.splits > 1 ? static_cast<size_t>(c.splits) * problems * rows * cols * sizeof(float) : 0;
+// A plan costs up to a hundred microseconds; it depends on the sizes alone, and calls of the same sizes follow one another.
+Plan plan_for(int kind, const vae_gated_ffn_desc& a) {
+    struct Known {
+        int kind = -1, m, c, f;
+        Plan plan;
+    };
+    thread_local Known known[8];
+    thread_local int next = 0;
+    for (const Known& k : known)
+        if (k.kind == kind && k.m == a.m && k.c == a.c && k.f == a.f) return k.plan;
+    const int kc = (a.c + kBk - 1) / kBk, kf = (a.f + kBk - 1) / kBk, km = (a.m + kBk - 1) / kBk;
+    Group g[2] = {};
+    if (kind == kGate || kind == kBackGate) {
+        g[0] = Group{a.m, a.f, 1, kc};
+    } else if (kind == kDown) {
+        g[0] = Group{a.m, a.c, 1, kf};
+    } else {
+        g[0] = Group{a.m, a.c, 1, 2 * kf};
+        g[1] = Group{a.f, a.c, 3, km};
+    }
+    Known& k = known[next];
+    next = (next + 1) % 8;
+    k.plan = make_plan(kind, g, kind == kGrad ? 2 : 1);
+    k.kind = kind;
+    k.m = a.m;
+    k.c = a.c;
+    k.f = a.f;
+    return k.plan;
 }
 
 std::mutex g_mu;
@@ -702,35 +839,52 @@ int ffn_setup() {
 }
 
 template <int T, int kKind, int kAct = VAE_ACT_SILU>
-int ffn_launch(const Maps& maps, Params& p, bool ahead, cudaStream_t stream) {
+int ffn_launch(const Maps& maps, const Plan& plan, Params& p, bool ahead, cudaStream_t stream) {
     int rc = ffn_setup<T, kKind, kAct>();
     if (rc != VAE_OK) return rc;
     p.status = device_status_ptr();
     if (p.status == nullptr) return VAE_ERR_CUDA;
     p.timeout_ns = wait_timeout_ns();
-    p.nm = (p.rows + 2 * kTile - 1) / (2 * kTile);
-    p.nfull = p.cols / p.cut.wide;
-    const int each = p.nm * p.problems * p.cut.splits;
-    p.full = each * p.nfull;
-    p.rests = p.cut.rest > 0 ? each : 0;
-    const int pairs = std::min(p.full + p.rests, sm_count() / 2);
+    p.group[0] = plan.group[0];
+    p.group[1] = plan.group[1];
+    p.deal = plan.deal;
+    const int count = plan.group[1].problems > 0 ? 2 : 1;
+    if (sm_count() < 2 * kPairs) deal_out(p.group, count, kKind == kGate ? 2 : 1, sm_count() / 2, &p.deal);
+    int pairs = 0, at = 0;  // up to the last one with work
+    for (int r = 0; r < p.deal.n; ++r) {
+        at += p.deal.pairs[r];
+        for (int c = 0; c < 4; ++c)
+            if (p.deal.count[r][c] > 0) pairs = at;
+    }
     VAE_CUDA_CHECK(launch_kernel_as(ahead || pdl_enabled(), ffn_kernel<T, kKind, kAct>, dim3(2 * pairs), dim3(kThreads), smem_bytes(kKind),
                                     stream, maps, p));
-    if (p.cut.splits > 1) {
-        const long long n8 = static_cast<long long>(p.rows) * p.cols / 8;
+    JoinParams join{};
+    int joins = 0;
+    for (int g = 0; g < count; ++g)
+        for (int z = 0; p.group[g].splits > 1 && z < p.group[g].problems; ++z, ++joins) {
+            const Group& gr = p.group[g];
+            join.n8[joins] = static_cast<long long>(gr.rows) * gr.cols / 8;
+            join.parts[joins] = p.parts[g] + join.n8[joins] * 8 * gr.splits * z;
+            join.out[joins] = p.out[g + z];
+            join.splits[joins] = gr.splits;
+            join.f32[joins] = p.out_f32[g];
+        }
+    if (joins > 0) {
+        join.residual = p.residual;
+        const long long n8 = *std::max_element(join.n8, join.n8 + joins);
         const unsigned grid = static_cast<unsigned>(std::min<long long>((n8 + 255) / 256, 152 * 8));
-        VAE_CUDA_CHECK(launch_next(join_kernel<T>, dim3(grid, p.problems), dim3(256), 0, stream, static_cast<const float*>(p.parts),
-                                   p.cut.splits, n8, p.out_f32, p.out[0], p.out[1], p.out[2], p.residual));
+        VAE_CUDA_CHECK(launch_next(join_kernel<T>, dim3(grid, joins), dim3(256), 0, stream, join));
     }
     return VAE_OK;
 }
+
 // The products whose epilogue knows the activation (a branch on it for every element took more of the instruction
 // cache than there is: 295 us instead of 100 at 16384 tokens).
 template <int T, int kKind>
-int ffn_launch_act(int act, const Maps& maps, Params& p, bool ahead, cudaStream_t stream) {
-    if (act == VAE_ACT_SILU) return ffn_launch<T, kKind, VAE_ACT_SILU>(maps, p, ahead, stream);
-    return act == VAE_ACT_GELU ? ffn_launch<T, kKind, VAE_ACT_GELU>(maps, p, ahead, stream)
-                               : ffn_launch<T, kKind, VAE_ACT_GELU_TANH>(maps, p, ahead, stream);
+int ffn_launch_act(int act, const Maps& maps, const Plan& plan, Params& p, bool ahead, cudaStream_t stream) {
+    if (act == VAE_ACT_SILU) return ffn_launch<T, kKind, VAE_ACT_SILU>(maps, plan, p, ahead, stream);
+    return act == VAE_ACT_GELU ? ffn_launch<T, kKind, VAE_ACT_GELU>(maps, plan, p, ahead, stream)
+                               : ffn_launch<T, kKind, VAE_ACT_GELU_TANH>(maps, plan, p, ahead, stream);
 }
 
 struct FfnTensor {
@@ -777,13 +931,6 @@ size_t cf_bytes(const vae_gated_ffn_desc& a) { return static_cast<size_t>(a.c) *
         if (rc_ != VAE_OK) return rc_; \
     } while (0)
 
-int stages(int k) { return (k + kBk - 1) / kBk; }
-Cut cut_gate(const vae_gated_ffn_desc& a) { return plan_cut(kGate, a.m, a.f, stages(a.c), 1); }
-Cut cut_down(const vae_gated_ffn_desc& a) { return plan_cut(kDown, a.m, a.c, stages(a.f), 1); }
-Cut cut_back_gate(const vae_gated_ffn_desc& a) { return plan_cut(kBackGate, a.m, a.f, stages(a.c), 1); }
-Cut cut_dx(const vae_gated_ffn_desc& a) { return plan_cut(kDx, a.m, a.c, 2 * stages(a.f), 1); }
-Cut cut_dw(const vae_gated_ffn_desc& a) { return plan_cut(kDw, a.f, a.c, stages(a.m), 3); }
-
 bool on32(const void* q) { return reinterpret_cast<uintptr_t>(q) % 32 == 0; }
 
 template <int T>
@@ -791,47 +938,39 @@ int ffn_forward(const vae_gated_ffn_desc& a, const void* x, const void* wg, cons
                 void* y, void* gate, void* up, void* hidden, float* parts, cudaStream_t stream) {
     Maps maps;
     Params p{};
-    p.cut = cut_gate(a);
+    Plan plan = plan_for(kGate, a);
     VAE_TRY(ffn_map(&maps.a[0], T, x, a.m, a.c, kTile));
-    VAE_TRY(ffn_map(&maps.b[0], T, wg, a.f, a.c, p.cut.wide));
-    VAE_TRY(ffn_map(&maps.b[1], T, wu, a.f, a.c, p.cut.wide));
-    p.rows = a.m;
-    p.cols = a.f;
-    p.problems = 1;
-    p.nk = stages(a.c);
-    p.segments = 1;
+    VAE_TRY(ffn_map(&maps.b[0], T, wg, a.f, a.c, plan.group[0].wide));
+    VAE_TRY(ffn_map(&maps.b[1], T, wu, a.f, a.c, plan.group[0].wide));
     p.out[0] = hidden;
     p.out[1] = gate;
     p.out[2] = up;
     p.wide = a.f % 16 == 0 && on32(hidden) && on32(gate) && on32(up);
-    VAE_TRY((ffn_launch_act<T, kGate>(a.activation, maps, p, false, stream)));
+    VAE_TRY((ffn_launch_act<T, kGate>(a.activation, maps, plan, p, false, stream)));
     p = Params{};
-    p.cut = cut_down(a);
+    plan = plan_for(kDown, a);
     VAE_TRY(ffn_map(&maps.a[0], T, hidden, a.m, a.f, kTile));
-    VAE_TRY(ffn_map(&maps.b[0], T, wd, a.c, a.f, p.cut.wide / 2));
-    p.rows = a.m;
-    p.cols = a.c;
-    p.problems = 1;
-    p.nk = stages(a.f);
-    p.segments = 1;
+    VAE_TRY(ffn_map(&maps.b[0], T, wd, a.c, a.f, plan.group[0].wide / 2));
     p.out[0] = y;
-    p.parts = parts;
-    p.out_f32 = a.y_type == VAE_F32;
+    p.parts[0] = parts;
+    p.out_f32[0] = a.y_type == VAE_F32;
     p.residual = residual;
     p.wide = a.c % 16 == 0 && on32(y);
-    return ffn_launch<T, kDown>(maps, p, true, stream);
+    return ffn_launch<T, kDown>(maps, plan, p, true, stream);
 }
 
 // Workspace of the gradient: the largest |dy|, dgate, dup, partial sums.
 struct BackSpace {
-    size_t dgate, dup, parts, bytes;
+    size_t dgate, dup, parts[2], bytes;
 };
 BackSpace back_space(const vae_gated_ffn_desc& a) {
     BackSpace s;
-    s.dgate = 256;
+    s.dgate = up256(kAmaxBlocks * sizeof(unsigned));
     s.dup = s.dgate + up256(mf_bytes(a));
-    s.parts = s.dup + up256(mf_bytes(a));
-    s.bytes = s.parts + std::max(parts_bytes(cut_dx(a), a.m, a.c, 1), parts_bytes(cut_dw(a), a.f, a.c, 3));
+    s.parts[0] = s.dup + up256(mf_bytes(a));
+    const Plan plan = plan_for(kGrad, a);
+    s.parts[1] = s.parts[0] + up256(parts_bytes(plan.group[0]));
+    s.bytes = s.parts[1] + parts_bytes(plan.group[1]);
     return s;
 }
 
@@ -840,72 +979,50 @@ int ffn_backward(const vae_gated_ffn_desc& a, const void* dy, const void* x, con
                  const void* gate, const void* up, const void* hidden, void* dx, void* dwg, void* dwu, void* dwd, char* ws,
                  cudaStream_t stream) {
     const BackSpace at = back_space(a);
-    unsigned* amax = nullptr;
     void *dgate = ws + at.dgate, *dup = ws + at.dup;
-    float* parts = reinterpret_cast<float*>(ws + at.parts);
-    bool ahead = false;
+    Params p{};
     if (T == VAE_F16) {
-        amax = reinterpret_cast<unsigned*>(ws);
-        VAE_CUDA_CHECK(cudaMemsetAsync(amax, 0, sizeof(unsigned), stream));
+        unsigned* amax = reinterpret_cast<unsigned*>(ws);
         const long long n8 = static_cast<long long>(a.m) * a.c / 8;
-        const unsigned grid = static_cast<unsigned>(std::min<long long>((n8 + 255) / 256, 152 * 8));
-        VAE_CUDA_CHECK(launch_kernel(amax_kernel, dim3(grid), dim3(256), 0, stream, static_cast<const uint4*>(dy), n8, amax));
-        ahead = true;
+        p.amax = amax;
+        p.amax_n = static_cast<int>(std::min<long long>((n8 + 511) / 512, kAmaxBlocks));
+        p.late = 1;
+        VAE_CUDA_CHECK(launch_kernel(amax_kernel, dim3(p.amax_n), dim3(512), 0, stream, static_cast<const uint4*>(dy), n8, amax));
     }
     Maps maps;
-    Params p{};
-    p.cut = cut_back_gate(a);
     VAE_TRY(ffn_map(&maps.a[0], T, dy, a.m, a.c, kTile));
     VAE_TRY(ffn_map(&maps.b[0], T, wd, a.c, a.f, kBk));
-    p.rows = a.m;
-    p.cols = a.f;
-    p.problems = 1;
-    p.nk = stages(a.c);
-    p.segments = 1;
     VAE_TRY(ffn_map(&maps.side[0], T, gate, a.m, a.f, 32));
     VAE_TRY(ffn_map(&maps.side[1], T, up, a.m, a.f, 32));
     VAE_TRY(ffn_map(&maps.side[2], T, dgate, a.m, a.f, 32));
     VAE_TRY(ffn_map(&maps.side[3], T, dup, a.m, a.f, 32));
-    p.amax = amax;
-    VAE_TRY((ffn_launch_act<T, kBackGate>(a.activation, maps, p, ahead, stream)));
-    p = Params{};
-    p.cut = cut_dx(a);
-    VAE_TRY(ffn_map(&maps.a[0], T, dgate, a.m, a.f, kTile));
-    VAE_TRY(ffn_map(&maps.a[1], T, dup, a.m, a.f, kTile));
-    VAE_TRY(ffn_map(&maps.b[0], T, wg, a.f, a.c, kBk));
-    VAE_TRY(ffn_map(&maps.b[1], T, wu, a.f, a.c, kBk));
-    p.rows = a.m;
-    p.cols = a.c;
-    p.problems = 1;
-    p.nk = stages(a.f);
-    p.segments = 2;
-    p.out[0] = dx;
-    p.parts = parts;
-    p.amax = amax;
-    p.wide = a.c % 16 == 0 && on32(dx);
-    VAE_TRY((ffn_launch<T, kDx>(maps, p, true, stream)));
-    if (dwg == nullptr) return VAE_OK;
-    p = Params{};
-    p.cut = cut_dw(a);
+    VAE_TRY((ffn_launch_act<T, kBackGate>(a.activation, maps, plan_for(kBackGate, a), p, p.late != 0, stream)));
+    const bool weights = dwg != nullptr;
     VAE_TRY(ffn_map(&maps.a[0], T, dgate, a.m, a.f, kBk));
     VAE_TRY(ffn_map(&maps.a[1], T, dup, a.m, a.f, kBk));
-    VAE_TRY(ffn_map(&maps.a[2], T, hidden, a.m, a.f, kBk));
-    VAE_TRY(ffn_map(&maps.b[0], T, x, a.m, a.c, kBk));
-    maps.b[1] = maps.b[0];
-    VAE_TRY(ffn_map(&maps.b[2], T, dy, a.m, a.c, kBk));
-    p.rows = a.f;
-    p.cols = a.c;
-    p.problems = 3;
-    p.nk = stages(a.m);
-    p.segments = 1;
-    p.out[0] = dwg;
-    p.out[1] = dwu;
-    p.out[2] = dwd;
-    p.parts = parts;
-    p.out_f32 = a.dw_type == VAE_F32;
-    p.amax = amax;
-    p.wide = a.c % 16 == 0 && on32(dwg) && on32(dwu);
-    return ffn_launch<T, kDw>(maps, p, true, stream);
+    VAE_TRY(ffn_map(&maps.b[0], T, wg, a.f, a.c, kBk));
+    VAE_TRY(ffn_map(&maps.b[1], T, wu, a.f, a.c, kBk));
+    if (weights) {
+        VAE_TRY(ffn_map(&maps.a[2], T, hidden, a.m, a.f, kBk));
+        VAE_TRY(ffn_map(&maps.b[2], T, x, a.m, a.c, kBk));
+        VAE_TRY(ffn_map(&maps.b[3], T, dy, a.m, a.c, kBk));
+    }
+    p.late = 0;
+    p.half = (a.f + kBk - 1) / kBk;
+    p.out[0] = dx;
+    p.out[1] = dwg;
+    p.out[2] = dwu;
+    p.out[3] = dwd;
+    p.parts[0] = reinterpret_cast<float*>(ws + at.parts[0]);
+    p.parts[1] = reinterpret_cast<float*>(ws + at.parts[1]);
+    p.out_f32[1] = a.dw_type == VAE_F32;
+    p.wide = a.c % 16 == 0 && on32(dx) && on32(dwg) && on32(dwu);
+    Plan plan = plan_for(kGrad, a);
+    if (!weights) {  // dx alone, cut the same way: the same bits
+        plan.group[1] = Group{};
+        deal_out(plan.group, 1, 1, kPairs, &plan.deal);
+    }
+    return ffn_launch<T, kGrad>(maps, plan, p, true, stream);
 }
 
 }  // namespace
@@ -919,7 +1036,7 @@ size_t vae_gated_ffn_workspace_bytes(const vae_gated_ffn_desc* desc) {
     clear_error();
     if (ffn_check(desc, false) != VAE_OK) return 0;
     // hidden, where it is not saved, and partial sums
-    return (desc->save ? 0 : up256(mf_bytes(*desc))) + (desc->m <= kFewTokens ? 0 : parts_bytes(cut_down(*desc), desc->m, desc->c, 1));
+    return (desc->save ? 0 : up256(mf_bytes(*desc))) + (desc->m <= kFewTokens ? 0 : parts_bytes(plan_for(kDown, *desc).group[0]));
 }
 
 int vae_gated_ffn(const vae_gated_ffn_desc* desc, const void* x_dev, const void* w_gate_dev, const void* w_up_dev,
