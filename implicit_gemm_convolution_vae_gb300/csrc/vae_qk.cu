@@ -19,7 +19,7 @@ namespace vae {
 namespace {
 
 constexpr int kQkMaxD = 256;
-constexpr int kQkTokens = 8;     // tokens a block takes at a time, at most
+constexpr int kQkTokens = 8;     // tokens a block takes at a time, at most (a power of two, as fewer are)
 constexpr int kQkThreads = 128;
 constexpr int kQkWarps = kQkThreads / 32;
 constexpr int kQkBlocks = 608;   // of the gradient, at most: each leaves a row of partial sums for dgamma
@@ -38,8 +38,9 @@ struct QkParams {
     const void* pos;
     int tokens, s, d, tpb;
     int pos_int, pos_batch;
+    int qblocks;  // the gradient's blocks of queries; the others are the keys'
     float eps;
-    float* sums;  // [2][blocks][d]: each block's part of dgamma
+    float* sums;  // a row of d for each block (in the plain form two, the queries' first): its part of dgamma
 };
 
 __device__ __forceinline__ float qk_pos(const QkParams& p, const vae_rope_plan& plan, int token, int pair) {
@@ -161,7 +162,11 @@ __global__ void __launch_bounds__(kQkThreads) qk_plain_kernel(const QkParams p, 
 //   kLocal: neighbouring units; interleaved pairs lie within a unit (or nothing turns);
 //   kHalves: pairs (c, c + R/2) with R a multiple of 16: a lane holds a unit of each half;
 //   kSwap: other halves: neighbouring units, the partners come through shared memory.
-// Two rows a lane are in flight; the first ones are on their way while the angles are formed.
+// The tokens of a block are a power of two, so a group of G lanes stays with one token: its
+// angles lie in registers, and the rows that it meets, every few heads, are a fixed step
+// apart. kDeep rows a lane are on their way beside the one that it works on.
+// (Rows dealt out over tokens and heads in turn, angles read from shared memory for each: 414
+// instructions a warp and four rows, which bound the call: 139 us for 36864 tokens of 36 heads.)
 enum : int { kLocal, kHalves, kSwap };
 
 template <int T>
@@ -175,14 +180,37 @@ struct QkUnit {  // eight channels as they lie in memory
         r[0] = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (T == VAE_F32) r[1] = r[0];
     }
-    __device__ __forceinline__ void get(float* v) const { load8<T>(r, *reinterpret_cast<float(*)[8]>(v)); }
+    __device__ __forceinline__ void get(float2* v) const {
+        if constexpr (T == VAE_F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[2 * i] = make_float2(__uint_as_float(r[i].x), __uint_as_float(r[i].y));
+                v[2 * i + 1] = make_float2(__uint_as_float(r[i].z), __uint_as_float(r[i].w));
+            }
+        } else {
+            v[0] = unpack2<T>(r[0].x);
+            v[1] = unpack2<T>(r[0].y);
+            v[2] = unpack2<T>(r[0].z);
+            v[3] = unpack2<T>(r[0].w);
+        }
+    }
+    __device__ __forceinline__ static void put(typename Elem<T>::type* p, const float2* v) {
+        if constexpr (T == VAE_F32) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0].x, v[0].y), pack2<T>(v[1].x, v[1].y), pack2<T>(v[2].x, v[2].y),
+                                                      pack2<T>(v[3].x, v[3].y));
+        }
+    }
 };
 
 template <int T, int kForm, bool kBack>
-__global__ void __launch_bounds__(kQkThreads, kBack ? 4 : 8)
+__global__ void __launch_bounds__(kQkThreads, kBack ? 4 : 5)
     qk_vector_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
     using E = typename Elem<T>::type;
-    constexpr int kBatch = kBack && T == VAE_F32 ? 1 : 2;
+    using Unit = QkUnit<T>;
+    constexpr int kDeep = kBack || T == VAE_F32 ? 1 : 2;
     // (cos, sin) of pair 8 u + 2 i + j of a token at [i][u][j]: a lane's eight pairs are four vectors, and those of
     // neighbouring lanes lie side by side
     __shared__ __align__(16) float2 cs[kQkTokens][4][16][2];
@@ -191,210 +219,225 @@ __global__ void __launch_bounds__(kQkThreads, kBack ? 4 : 8)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int pairs = plan.pairs, rot = 2 * pairs;
     const int group = 1 << glog2, u = lane & (group - 1);
-    const int step = kQkThreads >> glog2;
     const int nrot = pairs >> 3;  // kHalves: lanes whose units turn
     const bool turns = kForm == kHalves && u < nrot;
     const int ca = kForm == kHalves ? (turns ? 8 * u : rot + 16 * (u - nrot)) : 16 * u;
     const int cb = turns ? pairs + 8 * u : ca + 8;
     const bool has_a = ca < p.d, has_b = cb < p.d && has_a;
-    float acc[2][kBack ? 16 : 1] = {};
+    const int mine = threadIdx.x >> glog2;                // this group of lanes
+    const int token = mine & (p.tpb - 1), first = mine / p.tpb, step = (kQkThreads >> glog2) / p.tpb;  // its heads: first, first + step, ...
+    const float inv_d = 1.f / static_cast<float>(p.d);
+    float2 acc[kBack ? 8 : 1] = {};
     pdl_wait();
 
-    for (int t0 = static_cast<int>(blockIdx.x) * p.tpb; t0 < p.tokens; t0 += static_cast<int>(gridDim.x) * p.tpb) {
+    // the gradient's blocks are the queries' or the keys', so that a thread sums one dgamma
+    const int only = kBack ? (static_cast<int>(blockIdx.x) >= p.qblocks ? 1 : 0) : -1;
+    const int block = only == 1 ? static_cast<int>(blockIdx.x) - p.qblocks : static_cast<int>(blockIdx.x);
+    const int blocks = only == 1 ? static_cast<int>(gridDim.x) - p.qblocks : only == 0 ? p.qblocks : static_cast<int>(gridDim.x);
+    auto group_sum = [&](float x) {
+        for (int o = group >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    };
+
+    for (int t0 = block * p.tpb; t0 < p.tokens; t0 += blocks * p.tpb) {
         const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
-        const int b0 = t0 / p.s, s0 = t0 - b0 * p.s;
-        QkUnit<T> xa[kBatch], xb[kBatch], ga[kBack ? kBatch : 1], gb[kBack ? kBatch : 1];
-        int at[kBatch];  // the rows: token << 20 | head
-        int tk, hd;
-        auto offset = [&](int row, const long long (&st)[3]) {
-            int si = s0 + (row >> 20), bi = b0;
-            while (si >= p.s) {
-                si -= p.s;
-                ++bi;
-            }
-            return bi * st[0] + si * st[1] + (row & 0xfffff) * st[2];
-        };
-        auto settle = [&](int h) {
-            while (tk < nt && hd >= h) {
-                hd -= h;
-                ++tk;
-            }
-        };
-        auto load = [&](const QkPart& part) {
+        const bool here = token < nt;
+        const int e = (t0 + token) / p.s, si = t0 + token - e * p.s;
+        __syncthreads();  // (the last tokens' angles have been read)
+        for (int i = threadIdx.x; i < nt * pairs; i += kQkThreads) {
+            // neighbours take the tokens of one pair: its entries of the plan are one address for them
+            const int pr = i / nt, t = i - pr * nt;
+            const float2 c = rope_cos_sin(plan, pr, qk_pos(p, plan, t0 + t, pr));
+            cs[t][(pr & 7) >> 1][pr >> 3][pr & 1] = make_float2(c.x, kBack ? -c.y : c.y);  // (turned back: the other way)
+        }
+        __syncthreads();
+        float2 c2[4], s2[4];  // kHalves: the cosines and sines of two pairs; kLocal: (cos, sin) of each pair
+        if constexpr (kForm != kSwap) {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                at[k] = tk << 20 | hd;
+            for (int i = 0; i < 4; ++i) {
+                const float4 a = *reinterpret_cast<const float4*>(&cs[here ? token : 0][i][u][0]);
+                c2[i] = kForm == kHalves ? make_float2(a.x, a.z) : make_float2(a.x, a.y);
+                s2[i] = kForm == kHalves ? make_float2(a.y, a.w) : make_float2(a.z, a.w);
+            }
+        }
+        // the pairs of v turned
+        auto turn_all = [&](float2 (&v)[8]) {
+            if constexpr (kForm == kHalves) {
+                if (turns) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 t = mul2(v[4 + i], s2[i]);
+                        const float2 b = fma2(v[i], s2[i], mul2(v[4 + i], c2[i]));
+                        v[i] = fma2(v[i], c2[i], make_float2(-t.x, -t.y));
+                        v[4 + i] = b;
+                    }
+                }
+            } else if constexpr (kForm == kLocal) {
+                const int left = pairs - 8 * u;  // pairs of this lane that turn
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (2 * i < left) turn(v[2 * i].x, v[2 * i].y, c2[i]);
+                    if (2 * i + 1 < left) turn(v[2 * i + 1].x, v[2 * i + 1].y, s2[i]);
+                }
+            } else {
+                float2* z = reinterpret_cast<float2*>(swap + (threadIdx.x >> glog2 << glog2) * 16);
+                const float* zf = reinterpret_cast<const float*>(z);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[8 * u + i] = v[i];
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int c = ca + k;
+                    if (c < rot) {
+                        const bool second = c >= pairs;
+                        const int pr = second ? c - pairs : c;
+                        const float2 a = cs[here ? token : 0][(pr & 7) >> 1][pr >> 3][pr & 1];
+                        float& x = (k & 1) != 0 ? v[k >> 1].y : v[k >> 1].x;
+                        x = x * a.x + zf[second ? pr : c + pairs] * (second ? a.y : -a.y);
+                    }
+                }
+            }
+        };
+#pragma unroll 1
+        for (int w = kBack ? only : 0; w <= (kBack ? only : 1); ++w) {
+            const QkPart& part = p.part[w];
+            const E* x = static_cast<const E*>(part.x) + e * part.xs[0] + si * part.xs[1] + first * part.xs[2];
+            const E* g = kBack ? static_cast<const E*>(part.dy) + e * part.gs[0] + si * part.gs[1] + first * part.gs[2] : nullptr;
+            E* y = static_cast<E*>(part.y) + e * part.ys[0] + si * part.ys[1] + first * part.ys[2];
+            const long long xstep = step * part.xs[2], gstep = step * part.gs[2], ystep = step * part.ys[2];
+            const int rows = here && first < part.h ? (part.h - first + step - 1) / step : 0;
+            const int most = (part.h + step - 1) / step;  // (of any group: the warp stays together)
+            Unit xa[kDeep + 1], xb[kDeep + 1], ga[kBack ? kDeep + 1 : 1], gb[kBack ? kDeep + 1 : 1];
+            auto load = [&](int k, int row) {
                 xa[k].clear();
                 xb[k].clear();
                 if constexpr (kBack) {
                     ga[k].clear();
                     gb[k].clear();
                 }
-                if (tk < nt) {
-                    const E* x = static_cast<const E*>(part.x) + offset(at[k], part.xs);
+                if (row < rows) {
                     if (has_a) xa[k].load(x + ca);
                     if (has_b) xb[k].load(x + cb);
+                    x += xstep;
                     if constexpr (kBack) {
-                        const E* g = static_cast<const E*>(part.dy) + offset(at[k], part.gs);
                         if (has_a) ga[k].load(g + ca);
                         if (has_b) gb[k].load(g + cb);
-                    }
-                    hd += step;
-                    settle(part.h);
-                }
-            }
-        };
-        auto begin = [&](const QkPart& part) {
-            hd = threadIdx.x >> glog2;
-            tk = 0;
-            settle(part.h);
-            load(part);
-        };
-        // the pairs of v turned by the angles of token t, or back
-        auto turn_all = [&](float (&v)[16], int t) {
-            const float2(*a)[16][2] = cs[t];
-            if constexpr (kForm == kSwap) {
-                float* z = swap + (threadIdx.x >> glog2 << glog2) * 16;
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) z[ca + e] = v[e];
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int c = ca + e;
-                    if (c < rot) {
-                        const bool second = c >= pairs;
-                        const int pr = second ? c - pairs : c;
-                        const float2 x = a[(pr & 7) >> 1][pr >> 3][pr & 1];
-                        v[e] = v[e] * x.x + z[second ? pr : c + pairs] * (second != kBack ? x.y : -x.y);
+                        g += gstep;
                     }
                 }
-            } else {
+            };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (kForm == kHalves ? !turns : (u >= 16 || 8 * u + 2 * i >= pairs)) continue;
-                    const float4 x = *reinterpret_cast<const float4*>(&a[i][u][0]);
-                    const float2 c0 = make_float2(x.x, kBack ? -x.y : x.y), c1 = make_float2(x.z, kBack ? -x.w : x.w);
-                    if constexpr (kForm == kHalves) {
-                        turn(v[2 * i], v[8 + 2 * i], c0);
-                        turn(v[2 * i + 1], v[9 + 2 * i], c1);
-                    } else {
-                        turn(v[4 * i], v[4 * i + 1], c0);
-                        if (8 * u + 2 * i + 1 < pairs) turn(v[4 * i + 2], v[4 * i + 3], c1);
-                    }
-                }
+            for (int k = 0; k < kDeep; ++k) load(k, k);
+            float2 gamma[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = part.gamma != nullptr && (i < 4 ? has_a : has_b);
+                const float* at = part.gamma + (i < 4 ? ca + 2 * i : cb + 2 * i - 8);
+                gamma[i] = in ? make_float2(__ldg(at), __ldg(at + 1)) : make_float2(1.f, 1.f);
             }
-        };
-        auto group_sum = [&](float x) {
-            for (int o = group >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            return x;
-        };
-        auto store = [&](E* y, const float (&v)[16]) {
-            if (has_a) store8<T>(y + ca, *reinterpret_cast<const float(*)[8]>(v));
-            if (has_b) store8<T>(y + cb, *reinterpret_cast<const float(*)[8]>(v + 8));
-        };
-
-        begin(p.part[0]);
-        __syncthreads();  // (the last tokens' angles have been read)
-        for (int i = threadIdx.x; i < nt * pairs; i += kQkThreads) {
-            // neighbours take the tokens of one pair: its entries of the plan are one address for them
-            const int pr = i / nt, t = i - pr * nt;
-            cs[t][(pr & 7) >> 1][pr >> 3][pr & 1] = rope_cos_sin(plan, pr, qk_pos(p, plan, t0 + t, pr));
-        }
-        __syncthreads();
+            for (int r0 = 0; r0 < most; r0 += kDeep + 1) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const QkPart& part = p.part[w];
-            if (w == 1) begin(part);
-            float gamma[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const bool in = e < 8 ? has_a : has_b;
-                gamma[e] = in && part.gamma != nullptr ? __ldg(part.gamma + (e < 8 ? ca + e : cb + e - 8)) : 1.f;
-            }
-            while (__any_sync(0xffffffffu, at[0] >> 20 < nt)) {
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int t = at[k] >> 20;
-                    const bool live = t < nt;
-                    float v[16], ss = 0.f;
+                for (int k = 0; k <= kDeep; ++k) {
+                    const int row = r0 + k;
+                    load((k + kDeep) % (kDeep + 1), row + kDeep);
+                    if (row >= most) break;
+                    float2 v[8], ss = make_float2(0.f, 0.f), tt = ss;
                     xa[k].get(v);
-                    xb[k].get(v + 8);
+                    xb[k].get(v + 4);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) ss += v[e] * v[e];
-                    const float rs = rsqrtf(group_sum(ss) / static_cast<float>(p.d) + p.eps);
+                    for (int i = 0; i < 8; i += 2) {
+                        ss = fma2(v[i], v[i], ss);
+                        tt = fma2(v[i + 1], v[i + 1], tt);
+                    }
+                    ss = add2(ss, tt);
+                    const float rs = rsqrtf(group_sum(ss.x + ss.y) * inv_d + p.eps);
+                    const float2 rs2 = make_float2(rs, rs);
                     if constexpr (!kBack) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = v[e] * rs * gamma[e];
-                        turn_all(v, live ? t : 0);
-                        if (live) store(static_cast<E*>(part.y) + offset(at[k], part.ys), v);
-                    } else {
-                        float g[16], along = 0.f;
-                        ga[k].get(g);
-                        gb[k].get(g + 8);
-                        turn_all(g, live ? t : 0);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            v[e] *= rs;
-                            acc[w][e] += g[e] * v[e];
-                            g[e] *= gamma[e];
-                            along += g[e] * v[e];
+                        for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], rs2), gamma[i]);
+                        turn_all(v);
+                        if (row < rows) {
+                            if (has_a) Unit::put(y + ca, v);
+                            if (has_b) Unit::put(y + cb, v + 4);
+                            y += ystep;
                         }
-                        along = group_sum(along) / static_cast<float>(p.d);
+                    } else {
+                        float2 q[8], along = make_float2(0.f, 0.f);
+                        ga[k].get(q);
+                        gb[k].get(q + 4);
+                        turn_all(q);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) g[e] = rs * (g[e] - v[e] * along);
-                        if (live) store(static_cast<E*>(part.y) + offset(at[k], part.ys), g);
+                        for (int i = 0; i < 8; ++i) {
+                            v[i] = mul2(v[i], rs2);
+                            acc[i] = fma2(q[i], v[i], acc[i]);
+                            q[i] = mul2(q[i], gamma[i]);
+                            along = fma2(q[i], v[i], along);
+                        }
+                        const float m = -group_sum(along.x + along.y) * inv_d;
+                        const float2 m2 = make_float2(m, m);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) q[i] = mul2(fma2(v[i], m2, q[i]), rs2);
+                        if (row < rows) {
+                            if (has_a) Unit::put(y + ca, q);
+                            if (has_b) Unit::put(y + cb, q + 4);
+                            y += ystep;
+                        }
                     }
                 }
-                load(part);
             }
         }
     }
     if constexpr (kBack) {
-        if (p.sums != nullptr)
-            for (int w = 0; w < 2; ++w) {
-                __syncthreads();
+        if (p.sums != nullptr) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float x = w == 0 ? acc[0][e] : acc[1][e];
-                    for (int o = group; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                    if (lane < group && (e < 8 ? has_a : has_b)) part_sums[warp * kQkMaxD + (e < 8 ? ca + e : cb + e - 8)] = x;
-                }
-                __syncthreads();
-                for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
-                    float x = 0.f;
-                    for (int k = 0; k < kQkWarps; ++k) x += part_sums[k * kQkMaxD + c];
-                    p.sums[(static_cast<long long>(w) * gridDim.x + blockIdx.x) * p.d + c] = x;
-                }
+            for (int k = 0; k < 16; ++k) {
+                float x = (k & 1) != 0 ? acc[k >> 1].y : acc[k >> 1].x;
+                for (int o = group; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (lane < group && (k < 8 ? has_a : has_b)) part_sums[warp * kQkMaxD + (k < 8 ? ca + k : cb + k - 8)] = x;
             }
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
+                float x = 0.f;
+                for (int k = 0; k < kQkWarps; ++k) x += part_sums[k * kQkMaxD + c];
+                p.sums[static_cast<long long>(blockIdx.x) * p.d + c] = x;
+            }
+        }
     }
     pdl_launch_dependents();
 }
 
-// dgamma: the blocks' sums, 32 channels a block, 32 runs of them side by side.
-__global__ void __launch_bounds__(1024) qk_join_kernel(const float* sums, int blocks, int d, float* dgamma_q, float* dgamma_k) {
+// dgamma: the blocks' sums, 32 channels a block, 32 runs of them side by side. The queries' sums are the first `qblocks`
+// rows, the keys' those from `kfirst` to `kend`.
+__global__ void __launch_bounds__(1024) qk_join_kernel(const float* sums, int qblocks, int kfirst, int kend, int d, float* dgamma_q,
+                                                       float* dgamma_k) {
     __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int w = blockIdx.y, c = static_cast<int>(blockIdx.x) * 32 + lane;
+    const int end = w == 0 ? qblocks : kend;
     pdl_wait();
     float s = 0.f;
     if (c < d)
-        for (int b = run; b < blocks; b += 32) s += sums[(static_cast<long long>(w) * blocks + b) * d + c];
+        for (int b = (w == 0 ? 0 : kfirst) + run; b < end; b += 32) s += sums[static_cast<long long>(b) * d + c];
     part[run][lane] = s;
     __syncthreads();
     s = warp_sum(part[lane][run]);  // (the transposed warp: run is the channel here)
     if (const int ch = static_cast<int>(blockIdx.x) * 32 + run; lane == 0 && ch < d) (w == 0 ? dgamma_q : dgamma_k)[ch] = s;
 }
 
-template <int T, bool kBack>
-cudaError_t qk_launch_type(unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
+bool qk_vectors(const QkParams& p) {
     // Vectors where every row starts on 16 bytes and holds whole ones (a warp a row, channel by channel, otherwise)
     bool v8 = p.d % 8 == 0;
     for (const QkPart& t : p.part) {
         v8 = v8 && aligned16(t.x) && aligned16(t.dy) && aligned16(t.y);
         for (int i = 0; i < 3; ++i) v8 = v8 && t.xs[i] % 8 == 0 && t.gs[i] % 8 == 0 && t.ys[i] % 8 == 0;
     }
-    if (!v8) return launch_kernel(qk_plain_kernel<T, kBack>, dim3(grid), dim3(kQkThreads), 0, s, p, plan);
+    return v8;
+}
+
+template <int T, bool kBack>
+cudaError_t qk_launch_type(unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
+    if (!qk_vectors(p)) return launch_kernel(qk_plain_kernel<T, kBack>, dim3(grid), dim3(kQkThreads), 0, s, p, plan);
     const bool halves = plan.pairs > 0 && !plan.interleaved;
     const int form = !halves ? kLocal : plan.pairs % 8 == 0 ? kHalves : kSwap;
     const int lanes = form == kHalves ? plan.pairs / 8 + (p.d - 2 * plan.pairs + 15) / 16 : (p.d + 15) / 16;
@@ -488,7 +531,8 @@ int qk_check_plan(const vae_qk_norm_rope_desc* a, const void* pos, const vae_rop
 int qk_tiles(const vae_qk_norm_rope_desc* a, int* tpb) {
     const int tokens = a->b * a->s;
     // as many tokens as share one table, down to one when there are too few to give every SM a block
-    *tpb = std::min(kQkTokens, std::max(1, tokens / 304));
+    *tpb = kQkTokens;
+    while (*tpb > 1 && tokens / 304 < *tpb) *tpb /= 2;
     return (tokens - 1) / *tpb + 1;
 }
 
@@ -622,15 +666,24 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
     if (rc != VAE_OK) return rc;
     QkParams p{};
     qk_fill(desc, &p, q_dev, k_dev, dq_out_dev, dk_out_dev, dq_dev, dk_dev, gamma_q_dev, gamma_k_dev, pos_dev);
-    const unsigned grid = static_cast<unsigned>(std::min(qk_tiles(desc, &p.tpb), kQkBlocks));
+    const int tiles = qk_tiles(desc, &p.tpb);
+    // In vectors the queries and the keys have blocks of their own, as many as their share of the heads.
+    int grid = std::min(tiles, kQkBlocks), qblocks = grid, kend = 2 * grid;
+    if (qk_vectors(p)) {
+        const int all = static_cast<int>(std::min<long long>(2LL * tiles, kQkBlocks));
+        qblocks = static_cast<int>((static_cast<long long>(all) * a.hq + (a.hq + a.hk) / 2) / (a.hq + a.hk));
+        qblocks = std::min(std::max(qblocks, 1), std::min(all - 1, tiles));
+        grid = kend = qblocks + std::min(all - qblocks, tiles);
+    }
+    p.qblocks = qblocks;
     p.sums = weights ? static_cast<float*>(workspace_dev) : nullptr;
     const vae_rope_plan none{};
     const vae_rope_plan& pl = plan != nullptr ? *plan : none;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    VAE_CUDA_CHECK(qk_launch<true>(a.type, grid, st, p, pl));
+    VAE_CUDA_CHECK(qk_launch<true>(a.type, static_cast<unsigned>(grid), st, p, pl));
     if (weights)
         VAE_CUDA_CHECK(launch_next(qk_join_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, st,
-                                   static_cast<const float*>(p.sums), static_cast<int>(grid), a.d, dgamma_q_dev, dgamma_k_dev));
+                                   static_cast<const float*>(p.sums), qblocks, qblocks, kend, a.d, dgamma_q_dev, dgamma_k_dev));
     return VAE_OK;
 }
 
