@@ -159,26 +159,42 @@ __global__ void __launch_bounds__(kQkThreads) qk_plain_kernel(const QkParams p, 
 
 // Rows in 16-byte vectors. A row lies over G lanes (a power of two, 16 at most), two
 // units of eight channels a lane, in one of three ways:
-//   kLocal: neighbouring units; interleaved pairs lie within a unit (or nothing turns);
+//   kLocal: units u and u + n of n lanes; interleaved pairs lie within a unit (or nothing turns);
 //   kHalves: pairs (c, c + R/2) with R a multiple of 16: a lane holds a unit of each half;
-//   kSwap: other halves: neighbouring units, the partners come through shared memory.
+//   kSwap: other halves: units u and u + n, the partners come through shared memory.
+// Neighbouring lanes take neighbouring units, so that every access covers whole sectors
+// (two neighbouring units a lane: 137 us instead of 127 for 36864 tokens of 36 heads of 128).
 // The tokens of a block are a power of two, so a group of G lanes stays with one token: its
 // angles lie in registers, and the rows that it meets, every few heads, are a fixed step
-// apart. kDeep rows a lane are on their way beside the one that it works on.
-// (Rows dealt out over tokens and heads in turn, angles read from shared memory for each: 414
-// instructions a warp and four rows, which bound the call: 139 us for 36864 tokens of 36 heads.)
+// apart. (Rows dealt out over tokens and heads in turn, angles read from shared memory for each:
+// 414 instructions a warp and four rows, which bound the call.)
 enum : int { kLocal, kHalves, kSwap };
 
+// Eight channels as they lie in memory.
 template <int T>
-struct QkUnit {  // eight channels as they lie in memory
-    uint4 r[T == VAE_F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const typename Elem<T>::type* p) {
+struct QkUnit {
+    static constexpr int kVecs = T == VAE_F32 ? 2 : 1;
+    using E = typename Elem<T>::type;
+    uint4 r[kVecs];
+    __device__ __forceinline__ void load(const E* p) {
         r[0] = *reinterpret_cast<const uint4*>(p);
         if constexpr (T == VAE_F32) r[1] = *reinterpret_cast<const uint4*>(p + 4);
     }
     __device__ __forceinline__ void clear() {
         r[0] = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (T == VAE_F32) r[1] = r[0];
+    }
+    // In shared memory the vectors of a unit lie kQkThreads apart. Without `in` zeros come.
+    __device__ __forceinline__ static void fetch(uint4* at, const E* p, bool in) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at + i * kQkThreads)), "l"(p + i * 4),
+                         "r"(in ? 16 : 0)
+                         : "memory");
+    }
+    __device__ __forceinline__ void take(const uint4* at) {
+        r[0] = at[0];
+        if constexpr (T == VAE_F32) r[1] = at[kQkThreads];
     }
     __device__ __forceinline__ void get(float2* v) const {
         if constexpr (T == VAE_F32) {
@@ -194,7 +210,7 @@ struct QkUnit {  // eight channels as they lie in memory
             v[3] = unpack2<T>(r[0].w);
         }
     }
-    __device__ __forceinline__ static void put(typename Elem<T>::type* p, const float2* v) {
+    __device__ __forceinline__ static void put(E* p, const float2* v) {
         if constexpr (T == VAE_F32) {
             *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
             *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
@@ -205,203 +221,339 @@ struct QkUnit {  // eight channels as they lie in memory
     }
 };
 
-template <int T, int kForm, bool kBack>
-__global__ void __launch_bounds__(kQkThreads, kBack ? 4 : 5)
-    qk_vector_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
-    using E = typename Elem<T>::type;
-    using Unit = QkUnit<T>;
-    constexpr int kDeep = kBack || T == VAE_F32 ? 1 : 2;
-    // (cos, sin) of pair 8 u + 2 i + j of a token at [i][u][j]: a lane's eight pairs are four vectors, and those of
-    // neighbouring lanes lie side by side
-    __shared__ __align__(16) float2 cs[kQkTokens][4][16][2];
-    __shared__ float swap[kForm == kSwap ? kQkThreads * 16 : 1];
-    __shared__ float part_sums[kBack ? kQkWarps * kQkMaxD : 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int pairs = plan.pairs, rot = 2 * pairs;
-    const int group = 1 << glog2, u = lane & (group - 1);
-    const int nrot = pairs >> 3;  // kHalves: lanes whose units turn
-    const bool turns = kForm == kHalves && u < nrot;
-    const int ca = kForm == kHalves ? (turns ? 8 * u : rot + 16 * (u - nrot)) : 16 * u;
-    const int cb = turns ? pairs + 8 * u : ca + 8;
-    const bool has_a = ca < p.d, has_b = cb < p.d && has_a;
-    const int mine = threadIdx.x >> glog2;                // this group of lanes
-    const int token = mine & (p.tpb - 1), first = mine / p.tpb, step = (kQkThreads >> glog2) / p.tpb;  // its heads: first, first + step, ...
-    const float inv_d = 1.f / static_cast<float>(p.d);
-    float2 acc[kBack ? 8 : 1] = {};
-    pdl_wait();
+// The tokens' (cos, sin): of pair 4 q + 2 i + j of a token at [i][q][j].
+using QkAngles = float2[2][VAE_ROPE_MAX_PAIRS / 4][2];
 
-    // the gradient's blocks are the queries' or the keys', so that a thread sums one dgamma
-    const int only = kBack ? (static_cast<int>(blockIdx.x) >= p.qblocks ? 1 : 0) : -1;
-    const int block = only == 1 ? static_cast<int>(blockIdx.x) - p.qblocks : static_cast<int>(blockIdx.x);
-    const int blocks = only == 1 ? static_cast<int>(gridDim.x) - p.qblocks : only == 0 ? p.qblocks : static_cast<int>(gridDim.x);
-    auto group_sum = [&](float x) {
+// A lane's place in its row and among the rows of a block.
+template <int kForm>
+struct QkLane {
+    int u, group, units, ca, cb, left_a, left_b, token, first, step;
+    bool turns, has_a, has_b;
+    __device__ __forceinline__ QkLane(const QkParams& p, int pairs, int glog2) {
+        const int rot = 2 * pairs, nrot = pairs >> 3;
+        group = 1 << glog2;
+        u = threadIdx.x & (group - 1);
+        units = (p.d + 15) / 16;  // lanes of a row
+        turns = kForm == kHalves && u < nrot;
+        if constexpr (kForm == kHalves) {
+            units = nrot + (p.d - rot + 15) / 16;
+            ca = turns ? 8 * u : rot + 8 * (u - nrot);
+            cb = turns ? pairs + 8 * u : ca + 8 * (units - nrot);
+        } else {
+            ca = 8 * u;
+            cb = 8 * (u + units);
+        }
+        has_a = u < units && ca < p.d;
+        has_b = u < units && cb < p.d;
+        left_a = pairs - ca / 2;  // kLocal: pairs that turn from this unit's first on
+        left_b = pairs - cb / 2;
+        const int mine = threadIdx.x >> glog2;
+        token = mine & (p.tpb - 1);
+        first = mine / p.tpb;  // its heads: first, first + step, ...
+        step = (kQkThreads >> glog2) / p.tpb;
+    }
+    __device__ __forceinline__ float sum(float x) const {
         for (int o = group >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         return x;
-    };
+    }
+};
 
-    for (int t0 = block * p.tpb; t0 < p.tokens; t0 += blocks * p.tpb) {
-        const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
-        const bool here = token < nt;
-        const int e = (t0 + token) / p.s, si = t0 + token - e * p.s;
-        __syncthreads();  // (the last tokens' angles have been read)
-        for (int i = threadIdx.x; i < nt * pairs; i += kQkThreads) {
-            // neighbours take the tokens of one pair: its entries of the plan are one address for them
-            const int pr = i / nt, t = i - pr * nt;
-            const float2 c = rope_cos_sin(plan, pr, qk_pos(p, plan, t0 + t, pr));
-            cs[t][(pr & 7) >> 1][pr >> 3][pr & 1] = make_float2(c.x, kBack ? -c.y : c.y);  // (turned back: the other way)
-        }
-        __syncthreads();
-        float2 c2[4], s2[4];  // kHalves: the cosines and sines of two pairs; kLocal: (cos, sin) of each pair
-        if constexpr (kForm != kSwap) {
+// The angles of a lane's token, and the turn of a row's pairs by them (the table's sines have the direction's sign).
+template <int kForm>
+struct QkTurn {
+    float2 c[4], s[4];  // kHalves: cosines and sines of two pairs each; kLocal: (cos, sin) of the pairs of both units
+    __device__ __forceinline__ void take(const QkAngles& a, const QkLane<kForm>& l) {
+        if constexpr (kForm == kHalves) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 a = *reinterpret_cast<const float4*>(&cs[here ? token : 0][i][u][0]);
-                c2[i] = kForm == kHalves ? make_float2(a.x, a.z) : make_float2(a.x, a.y);
-                s2[i] = kForm == kHalves ? make_float2(a.y, a.w) : make_float2(a.z, a.w);
+                const float4 x = *reinterpret_cast<const float4*>(&a[i & 1][l.turns ? 2 * l.u + (i >> 1) : 0][0]);
+                c[i] = make_float2(x.x, x.z);
+                s[i] = make_float2(x.y, x.w);
+            }
+        } else if constexpr (kForm == kLocal) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 x = *reinterpret_cast<const float4*>(&a[i][l.u][0]);
+                const float4 y = *reinterpret_cast<const float4*>(&a[i][l.has_b ? l.u + l.units : 0][0]);
+                c[2 * i] = make_float2(x.x, x.y);
+                c[2 * i + 1] = make_float2(x.z, x.w);
+                s[2 * i] = make_float2(y.x, y.y);
+                s[2 * i + 1] = make_float2(y.z, y.w);
             }
         }
-        // the pairs of v turned
-        auto turn_all = [&](float2 (&v)[8]) {
-            if constexpr (kForm == kHalves) {
-                if (turns) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 t = mul2(v[4 + i], s2[i]);
-                        const float2 b = fma2(v[i], s2[i], mul2(v[4 + i], c2[i]));
-                        v[i] = fma2(v[i], c2[i], make_float2(-t.x, -t.y));
-                        v[4 + i] = b;
-                    }
-                }
-            } else if constexpr (kForm == kLocal) {
-                const int left = pairs - 8 * u;  // pairs of this lane that turn
+    }
+    __device__ __forceinline__ void apply(float2 (&v)[8], const QkAngles& a, const QkLane<kForm>& l, int pairs, float* swap) const {
+        if constexpr (kForm == kHalves) {
+            if (l.turns) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (2 * i < left) turn(v[2 * i].x, v[2 * i].y, c2[i]);
-                    if (2 * i + 1 < left) turn(v[2 * i + 1].x, v[2 * i + 1].y, s2[i]);
-                }
-            } else {
-                float2* z = reinterpret_cast<float2*>(swap + (threadIdx.x >> glog2 << glog2) * 16);
-                const float* zf = reinterpret_cast<const float*>(z);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[8 * u + i] = v[i];
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int c = ca + k;
-                    if (c < rot) {
-                        const bool second = c >= pairs;
-                        const int pr = second ? c - pairs : c;
-                        const float2 a = cs[here ? token : 0][(pr & 7) >> 1][pr >> 3][pr & 1];
-                        float& x = (k & 1) != 0 ? v[k >> 1].y : v[k >> 1].x;
-                        x = x * a.x + zf[second ? pr : c + pairs] * (second ? a.y : -a.y);
-                    }
+                    const float2 t = mul2(v[4 + i], s[i]);
+                    const float2 b = fma2(v[i], s[i], mul2(v[4 + i], c[i]));
+                    v[i] = fma2(v[i], c[i], make_float2(-t.x, -t.y));
+                    v[4 + i] = b;
                 }
             }
-        };
-#pragma unroll 1
-        for (int w = kBack ? only : 0; w <= (kBack ? only : 1); ++w) {
-            const QkPart& part = p.part[w];
-            const E* x = static_cast<const E*>(part.x) + e * part.xs[0] + si * part.xs[1] + first * part.xs[2];
-            const E* g = kBack ? static_cast<const E*>(part.dy) + e * part.gs[0] + si * part.gs[1] + first * part.gs[2] : nullptr;
-            E* y = static_cast<E*>(part.y) + e * part.ys[0] + si * part.ys[1] + first * part.ys[2];
-            const long long xstep = step * part.xs[2], gstep = step * part.gs[2], ystep = step * part.ys[2];
-            const int rows = here && first < part.h ? (part.h - first + step - 1) / step : 0;
-            const int most = (part.h + step - 1) / step;  // (of any group: the warp stays together)
-            Unit xa[kDeep + 1], xb[kDeep + 1], ga[kBack ? kDeep + 1 : 1], gb[kBack ? kDeep + 1 : 1];
-            auto load = [&](int k, int row) {
-                xa[k].clear();
-                xb[k].clear();
-                if constexpr (kBack) {
-                    ga[k].clear();
-                    gb[k].clear();
-                }
-                if (row < rows) {
-                    if (has_a) xa[k].load(x + ca);
-                    if (has_b) xb[k].load(x + cb);
-                    x += xstep;
-                    if constexpr (kBack) {
-                        if (has_a) ga[k].load(g + ca);
-                        if (has_b) gb[k].load(g + cb);
-                        g += gstep;
-                    }
-                }
-            };
+        } else if constexpr (kForm == kLocal) {
 #pragma unroll
-            for (int k = 0; k < kDeep; ++k) load(k, k);
-            float2 gamma[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool in = part.gamma != nullptr && (i < 4 ? has_a : has_b);
-                const float* at = part.gamma + (i < 4 ? ca + 2 * i : cb + 2 * i - 8);
-                gamma[i] = in ? make_float2(__ldg(at), __ldg(at + 1)) : make_float2(1.f, 1.f);
+            for (int i = 0; i < 4; ++i) {
+                if (i < l.left_a) turn(v[i].x, v[i].y, c[i]);
+                if (i < l.left_b) turn(v[4 + i].x, v[4 + i].y, s[i]);
             }
-            for (int r0 = 0; r0 < most; r0 += kDeep + 1) {
+        } else {
+            float* z = swap + (threadIdx.x & ~(l.group - 1)) * 16;
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k <= kDeep; ++k) {
-                    const int row = r0 + k;
-                    load((k + kDeep) % (kDeep + 1), row + kDeep);
-                    if (row >= most) break;
-                    float2 v[8], ss = make_float2(0.f, 0.f), tt = ss;
-                    xa[k].get(v);
-                    xb[k].get(v + 4);
+            for (int i = 0; i < 4; ++i) {
+                if (l.has_a) *reinterpret_cast<float2*>(z + l.ca + 2 * i) = v[i];
+                if (l.has_b) *reinterpret_cast<float2*>(z + l.cb + 2 * i) = v[4 + i];
+            }
+            __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        ss = fma2(v[i], v[i], ss);
-                        tt = fma2(v[i + 1], v[i + 1], tt);
-                    }
-                    ss = add2(ss, tt);
-                    const float rs = rsqrtf(group_sum(ss.x + ss.y) * inv_d + p.eps);
-                    const float2 rs2 = make_float2(rs, rs);
-                    if constexpr (!kBack) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], rs2), gamma[i]);
-                        turn_all(v);
-                        if (row < rows) {
-                            if (has_a) Unit::put(y + ca, v);
-                            if (has_b) Unit::put(y + cb, v + 4);
-                            y += ystep;
-                        }
-                    } else {
-                        float2 q[8], along = make_float2(0.f, 0.f);
-                        ga[k].get(q);
-                        gb[k].get(q + 4);
-                        turn_all(q);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            v[i] = mul2(v[i], rs2);
-                            acc[i] = fma2(q[i], v[i], acc[i]);
-                            q[i] = mul2(q[i], gamma[i]);
-                            along = fma2(q[i], v[i], along);
-                        }
-                        const float m = -group_sum(along.x + along.y) * inv_d;
-                        const float2 m2 = make_float2(m, m);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) q[i] = mul2(fma2(v[i], m2, q[i]), rs2);
-                        if (row < rows) {
-                            if (has_a) Unit::put(y + ca, q);
-                            if (has_b) Unit::put(y + cb, q + 4);
-                            y += ystep;
-                        }
-                    }
+            for (int k = 0; k < 16; ++k) {
+                const int ch = (k < 8 ? l.ca : l.cb - 8) + k;
+                if ((k < 8 ? l.has_a : l.has_b) && ch < 2 * pairs) {
+                    const bool second = ch >= pairs;
+                    const int pr = second ? ch - pairs : ch;
+                    const float2 t = a[(pr >> 1) & 1][pr >> 2][pr & 1];
+                    float& x = (k & 1) != 0 ? v[k >> 1].y : v[k >> 1].x;
+                    x = x * t.x + z[second ? pr : ch + pairs] * (second ? t.y : -t.y);
                 }
             }
         }
     }
-    if constexpr (kBack) {
-        if (p.sums != nullptr) {
+};
+
+// The angles of the tokens from t0 on, by the whole block; turned back, the sines change sign.
+template <bool kBack>
+__device__ __forceinline__ void qk_angles(QkAngles* cs, const QkParams& p, const vae_rope_plan& plan, int t0, int nt) {
+    for (int i = threadIdx.x; i < nt * plan.pairs; i += kQkThreads) {
+        // neighbours take the tokens of one pair: its entries of the plan are one address for them
+        const int pr = i / nt, t = i - pr * nt;
+        const float2 c = rope_cos_sin(plan, pr, qk_pos(p, plan, t0 + t, pr));
+        cs[t][(pr >> 1) & 1][pr >> 2][pr & 1] = make_float2(c.x, kBack ? -c.y : c.y);
+    }
+}
+
+__device__ __forceinline__ void qk_gamma(float2 (&gamma)[8], const float* at, int ca, bool has_a, int cb, bool has_b) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                float x = (k & 1) != 0 ? acc[k >> 1].y : acc[k >> 1].x;
-                for (int o = group; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (lane < group && (k < 8 ? has_a : has_b)) part_sums[warp * kQkMaxD + (k < 8 ? ca + k : cb + k - 8)] = x;
+    for (int i = 0; i < 8; ++i) {
+        const float* x = at + (i < 4 ? ca + 2 * i : cb + 2 * i - 8);
+        gamma[i] = at != nullptr && (i < 4 ? has_a : has_b) ? make_float2(__ldg(x), __ldg(x + 1)) : make_float2(1.f, 1.f);
+    }
+}
+__device__ __forceinline__ float qk_square(const float2 (&v)[8]) {
+    float2 s = make_float2(0.f, 0.f), t = s;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        s = fma2(v[i], v[i], s);
+        t = fma2(v[i + 1], v[i + 1], t);
+    }
+    s = add2(s, t);
+    return s.x + s.y;
+}
+
+// Forward: a block takes p.tpb tokens, its threads the next kDeep rows' units into registers.
+template <int T, int kForm>
+__global__ void __launch_bounds__(kQkThreads, 6) qk_vector_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
+    using E = typename Elem<T>::type;
+    using Unit = QkUnit<T>;
+    constexpr int kDeep = T == VAE_F32 ? 1 : 2;
+    __shared__ __align__(16) QkAngles cs[kQkTokens];
+    __shared__ float swap[kForm == kSwap ? kQkThreads * 16 : 1];
+    const QkLane<kForm> l(p, plan.pairs, glog2);
+    const float inv_d = 1.f / static_cast<float>(p.d);
+    pdl_wait();
+    const int t0 = static_cast<int>(blockIdx.x) * p.tpb;
+    const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
+    const bool here = l.token < nt;
+    const int e = (t0 + l.token) / p.s, si = t0 + l.token - e * p.s;
+    const QkAngles& angles = cs[here ? l.token : 0];
+    QkTurn<kForm> turned;
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        const QkPart& part = p.part[w];
+        const E* x = static_cast<const E*>(part.x) + e * part.xs[0] + si * part.xs[1] + l.first * part.xs[2];
+        E* y = static_cast<E*>(part.y) + e * part.ys[0] + si * part.ys[1] + l.first * part.ys[2];
+        const long long xstep = l.step * part.xs[2], ystep = l.step * part.ys[2];
+        const int rows = here && l.first < part.h ? (part.h - l.first + l.step - 1) / l.step : 0;
+        const int most = (part.h + l.step - 1) / l.step;  // (of any group: the warp stays together)
+        Unit xa[kDeep + 1], xb[kDeep + 1];
+        auto load = [&](int k, int row) {
+            xa[k].clear();
+            xb[k].clear();
+            if (row < rows) {
+                if (l.has_a) xa[k].load(x + l.ca);
+                if (l.has_b) xb[k].load(x + l.cb);
+                x += xstep;
             }
+        };
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) load(k, k);
+        float2 gamma[8];
+        qk_gamma(gamma, part.gamma, l.ca, l.has_a, l.cb, l.has_b);
+        if (w == 0) {  // the first rows are on their way
+            qk_angles<false>(cs, p, plan, t0, nt);
             __syncthreads();
-            for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
-                float x = 0.f;
-                for (int k = 0; k < kQkWarps; ++k) x += part_sums[k * kQkMaxD + c];
-                p.sums[static_cast<long long>(blockIdx.x) * p.d + c] = x;
+            turned.take(angles, l);
+        }
+        for (int r0 = 0; r0 < most; r0 += kDeep + 1) {
+#pragma unroll
+            for (int k = 0; k <= kDeep; ++k) {
+                const int row = r0 + k;
+                load((k + kDeep) % (kDeep + 1), row + kDeep);
+                if (row >= most) break;
+                float2 v[8];
+                xa[k].get(v);
+                xb[k].get(v + 4);
+                const float rs = rsqrtf(l.sum(qk_square(v)) * inv_d + p.eps);
+                const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], rs2), gamma[i]);
+                turned.apply(v, angles, l, plan.pairs, swap);
+                if (row < rows) {
+                    if (l.has_a) Unit::put(y + l.ca, v);
+                    if (l.has_b) Unit::put(y + l.cb, v + 4);
+                    y += ystep;
+                }
             }
+        }
+    }
+    pdl_launch_dependents();
+}
+
+// The gradient: blocks stay for many tokens, each with the queries or the keys, so that a thread sums its channels of
+// one dgamma. A thread has the next kDeep rows' units on their way into shared memory, which nobody else reads, over the
+// ends of its tokens (rows ahead in registers: 184 us for 36864 tokens of 24 heads, 142 so).
+template <int T>
+struct QkRing {
+    static constexpr int kDeep = 2;
+    static constexpr int kVecs = 4 * QkUnit<T>::kVecs;  // of a row and thread
+    static constexpr int kBytes = kDeep * kVecs * kQkThreads * 16;
+    // tokens a turn: each costs two barriers and the angles' latency (4: 193 us, 8: 151, 16: 142)
+    static constexpr int kTokens = T == VAE_F32 ? kQkTokens : 2 * kQkTokens;
+    static_assert(kBytes + kTokens * sizeof(QkAngles) + kQkThreads * 64 <= 48 * 1024, "more shared memory than a kernel has without asking");
+    static_assert(kBytes >= kQkWarps * kQkMaxD * 4, "the ring takes a row of sums for each warp at the end");
+};
+
+template <int T, int kForm>
+__global__ void __launch_bounds__(kQkThreads, 4) qk_vector_backward_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
+    using E = typename Elem<T>::type;
+    using Unit = QkUnit<T>;
+    using Ring = QkRing<T>;
+    constexpr int kDeep = Ring::kDeep, kVecs = Ring::kVecs;
+    extern __shared__ __align__(16) uint4 ring[];  // [kDeep][kVecs][threads]
+    __shared__ __align__(16) QkAngles cs[Ring::kTokens];
+    __shared__ float swap[kForm == kSwap ? kQkThreads * 16 : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const QkLane<kForm> l(p, plan.pairs, glog2);
+    const float inv_d = 1.f / static_cast<float>(p.d);
+    const bool keys = static_cast<int>(blockIdx.x) >= p.qblocks;
+    const QkPart& part = p.part[keys ? 1 : 0];
+    const int stride = (keys ? static_cast<int>(gridDim.x) - p.qblocks : p.qblocks) * p.tpb;  // tokens from one turn of a block to the next
+    const int t00 = (keys ? static_cast<int>(blockIdx.x) - p.qblocks : static_cast<int>(blockIdx.x)) * p.tpb;
+    const int most = (part.h + l.step - 1) / l.step;  // rows of a turn, of any group: the warp stays together
+    const int heads = l.first < part.h ? (part.h - l.first + l.step - 1) / l.step : 0;
+    pdl_wait();
+
+    // the next row to ask for
+    int nt0 = t00, nrow = 0;
+    const E *x = static_cast<const E*>(part.x), *g = static_cast<const E*>(part.dy);
+    bool more = false;
+    auto open = [&]() {
+        nrow = 0;
+        more = nt0 < p.tokens && nt0 + l.token < p.tokens;
+        if (!more) return;
+        const int e = (nt0 + l.token) / p.s, si = nt0 + l.token - e * p.s;
+        x = static_cast<const E*>(part.x) + e * part.xs[0] + si * part.xs[1] + l.first * part.xs[2];
+        g = static_cast<const E*>(part.dy) + e * part.gs[0] + si * part.gs[1] + l.first * part.gs[2];
+    };
+    auto fetch = [&](int slot) {
+        constexpr int kUnit = Unit::kVecs * kQkThreads;
+        uint4* at = ring + slot * kVecs * kQkThreads + threadIdx.x;
+        const bool in = more && nrow < heads, a = in && l.has_a, b = in && l.has_b;
+        Unit::fetch(at, x + (a ? l.ca : 0), a);
+        Unit::fetch(at + kUnit, x + (b ? l.cb : 0), b);
+        Unit::fetch(at + 2 * kUnit, g + (a ? l.ca : 0), a);
+        Unit::fetch(at + 3 * kUnit, g + (b ? l.cb : 0), b);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (in) {
+            x += l.step * part.xs[2];
+            g += l.step * part.gs[2];
+        }
+        if (++nrow == most && nt0 < p.tokens) {
+            nt0 = p.tokens - nt0 > stride ? nt0 + stride : p.tokens;
+            open();
+        }
+    };
+    open();
+#pragma unroll 1
+    for (int k = 0; k < kDeep; ++k) fetch(k);
+    float2 gamma[8], acc[8] = {};
+    qk_gamma(gamma, part.gamma, l.ca, l.has_a, l.cb, l.has_b);
+    int slot = 0;
+    for (int t0 = t00; t0 < p.tokens; t0 = p.tokens - t0 > stride ? t0 + stride : p.tokens) {
+        const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
+        const bool here = l.token < nt;
+        __syncthreads();  // (the last tokens' angles have been read)
+        qk_angles<true>(cs, p, plan, t0, nt);
+        __syncthreads();
+        const QkAngles& angles = cs[here ? l.token : 0];
+        QkTurn<kForm> turned;
+        turned.take(angles, l);
+        const int e = (t0 + l.token) / p.s;
+        E* y = static_cast<E*>(part.y) + e * part.ys[0] + (t0 + l.token - e * p.s) * part.ys[1] + l.first * part.ys[2];
+        const int rows = here ? heads : 0;
+#pragma unroll 1
+        for (int row = 0; row < most; ++row) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");  // (this thread's own copies: no barrier)
+            const uint4* at = ring + slot * kVecs * kQkThreads + threadIdx.x;
+            Unit r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i].take(at + i * Unit::kVecs * kQkThreads);
+            float2 v[8], q[8];
+            r[0].get(v);
+            r[1].get(v + 4);
+            r[2].get(q);
+            r[3].get(q + 4);
+            fetch(slot);
+            if (++slot == kDeep) slot = 0;
+            const float rs = rsqrtf(l.sum(qk_square(v)) * inv_d + p.eps);
+            const float2 rs2 = make_float2(rs, rs);
+            float2 along = make_float2(0.f, 0.f);
+            turned.apply(q, angles, l, plan.pairs, swap);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = mul2(v[i], rs2);
+                acc[i] = fma2(q[i], v[i], acc[i]);
+                q[i] = mul2(q[i], gamma[i]);
+                along = fma2(q[i], v[i], along);
+            }
+            const float m = -l.sum(along.x + along.y) * inv_d;
+            const float2 m2 = make_float2(m, m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = mul2(fma2(v[i], m2, q[i]), rs2);
+            if (row < rows) {
+                if (l.has_a) Unit::put(y + l.ca, q);
+                if (l.has_b) Unit::put(y + l.cb, q + 4);
+                y += l.step * part.ys[2];
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (p.sums != nullptr) {
+        float* sums = reinterpret_cast<float*>(ring);  // [warps][kQkMaxD]
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            float s = (k & 1) != 0 ? acc[k >> 1].y : acc[k >> 1].x;
+            for (int o = l.group; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane < l.group && (k < 8 ? l.has_a : l.has_b)) sums[warp * kQkMaxD + (k < 8 ? l.ca + k : l.cb + k - 8)] = s;
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
+            float s = 0.f;
+            for (int k = 0; k < kQkWarps; ++k) s += sums[k * kQkMaxD + c];
+            p.sums[static_cast<long long>(blockIdx.x) * p.d + c] = s;
         }
     }
     pdl_launch_dependents();
@@ -435,17 +587,30 @@ bool qk_vectors(const QkParams& p) {
     return v8;
 }
 
+// The form that takes a plan's pairs, and log2 of the lanes that a row of d channels lies over.
+struct QkForm {
+    int form, glog2;
+};
+QkForm qk_form(int d, const vae_rope_plan& plan) {
+    const bool halves = plan.pairs > 0 && !plan.interleaved;
+    QkForm f{!halves ? kLocal : plan.pairs % 8 == 0 ? kHalves : kSwap, 0};
+    const int lanes = f.form == kHalves ? plan.pairs / 8 + (d - 2 * plan.pairs + 15) / 16 : (d + 15) / 16;
+    while ((1 << f.glog2) < lanes) ++f.glog2;
+    return f;
+}
+
 template <int T, bool kBack>
 cudaError_t qk_launch_type(unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
     if (!qk_vectors(p)) return launch_kernel(qk_plain_kernel<T, kBack>, dim3(grid), dim3(kQkThreads), 0, s, p, plan);
-    const bool halves = plan.pairs > 0 && !plan.interleaved;
-    const int form = !halves ? kLocal : plan.pairs % 8 == 0 ? kHalves : kSwap;
-    const int lanes = form == kHalves ? plan.pairs / 8 + (p.d - 2 * plan.pairs + 15) / 16 : (p.d + 15) / 16;
-    int glog2 = 0;
-    while ((1 << glog2) < lanes) ++glog2;
-    const auto go = [&](auto k) { return launch_kernel(k, dim3(grid), dim3(kQkThreads), 0, s, p, plan, glog2); };
-    if (form == kLocal) return go(qk_vector_kernel<T, kLocal, kBack>);
-    return form == kHalves ? go(qk_vector_kernel<T, kHalves, kBack>) : go(qk_vector_kernel<T, kSwap, kBack>);
+    const auto [form, glog2] = qk_form(p.d, plan);
+    const auto go = [&, lanes = glog2](auto k) { return launch_kernel(k, dim3(grid), dim3(kQkThreads), kBack ? QkRing<T>::kBytes : 0, s, p, plan, lanes); };
+    if constexpr (kBack) {
+        if (form == kLocal) return go(qk_vector_backward_kernel<T, kLocal>);
+        return form == kHalves ? go(qk_vector_backward_kernel<T, kHalves>) : go(qk_vector_backward_kernel<T, kSwap>);
+    } else {
+        if (form == kLocal) return go(qk_vector_kernel<T, kLocal>);
+        return form == kHalves ? go(qk_vector_kernel<T, kHalves>) : go(qk_vector_kernel<T, kSwap>);
+    }
 }
 template <bool kBack>
 cudaError_t qk_launch(int type, unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
@@ -666,10 +831,16 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
     if (rc != VAE_OK) return rc;
     QkParams p{};
     qk_fill(desc, &p, q_dev, k_dev, dq_out_dev, dk_out_dev, dq_dev, dk_dev, gamma_q_dev, gamma_k_dev, pos_dev);
-    const int tiles = qk_tiles(desc, &p.tpb);
+    int tiles = qk_tiles(desc, &p.tpb);
     // In vectors the queries and the keys have blocks of their own, as many as their share of the heads.
     int grid = std::min(tiles, kQkBlocks), qblocks = grid, kend = 2 * grid;
+    const vae_rope_plan none{};
+    const vae_rope_plan& pl = plan != nullptr ? *plan : none;
     if (qk_vectors(p)) {
+        if (p.tpb == kQkTokens && p.tokens / 608 >= kQkTokens && a.type != VAE_F32 && qk_form(a.d, pl).glog2 <= 3) {
+            p.tpb = 2 * kQkTokens;
+            tiles = (p.tokens - 1) / p.tpb + 1;
+        }
         const int all = static_cast<int>(std::min<long long>(2LL * tiles, kQkBlocks));
         qblocks = static_cast<int>((static_cast<long long>(all) * a.hq + (a.hq + a.hk) / 2) / (a.hq + a.hk));
         qblocks = std::min(std::max(qblocks, 1), std::min(all - 1, tiles));
@@ -677,8 +848,6 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
     }
     p.qblocks = qblocks;
     p.sums = weights ? static_cast<float*>(workspace_dev) : nullptr;
-    const vae_rope_plan none{};
-    const vae_rope_plan& pl = plan != nullptr ? *plan : none;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     VAE_CUDA_CHECK(qk_launch<true>(a.type, static_cast<unsigned>(grid), st, p, pl));
     if (weights)

@@ -68,7 +68,10 @@ CASES = [(1, 1, 1, 1, 1, None, "f32", True, True, False, True), (2, 3, 2, 1, 2, 
          (1, 37, 1, 1, 8, (8,), "bf16", False, False, False, True), (1, 37, 1, 1, 16, (16,), "f16", False, False, False, True),
          (1, 37, 2, 3, 24, (8,), "f32", False, False, False, True), (3, 1500, 4, 2, 80, (0, 40, 40), "f32", False, False, True, True),
          (3, 1500, 4, 2, 80, (0, 20, 20), "bf16", False, False, True, True), (2, 100, 3, 2, 64, None, "bf16", True, False, False, True),
-         (2, 100, 3, 2, 120, None, "f16", False, False, False, False), (1, 2600, 9, 9, 128, (16, 56, 56), "bf16", False, True, True, True)]
+         (2, 100, 3, 2, 120, None, "f16", False, False, False, False), (1, 2600, 9, 9, 128, (16, 56, 56), "bf16", False, True, True, True),
+         # enough tokens for the gradient's longest turns, the last one short, each way of lying over lanes
+         (2, 2601, 5, 2, 64, (0, 32, 32), "bf16", False, True, True, True), (1, 5003, 3, 1, 72, (8, 24, 24), "f16", False, False, False, True),
+         (1, 5003, 2, 3, 96, (8, 24, 24), "f16", True, False, False, True), (1, 10007, 1, 1, 256, (128, 64, 64), "bf16", True, True, False, True)]
 
 
 def _case(case):
