@@ -823,47 +823,52 @@ _QK_DESC = struct.Struct("=6if2i4x18q")
 
 def _qk_desc(q, k, gamma_q, gamma_k, positions, plan, eps, q_out, k_out, dq_out=None, dk_out=None):
     """The desc of the call (with new outputs where q_out, k_out are None) and the outputs; checks the tensors."""
-    dtype = q.dtype
+    dtype, shape, kshape = q.dtype, q.shape, k.shape
     code = _type(dtype, "q")
-    if k.dtype != dtype:
+    if k.dtype is not dtype:
         raise VaeError(-1, f"k must be {dtype}, got {k.dtype}")
-    if q.dim() != 4 or k.dim() != 4:
-        raise VaeError(-2, f"q and k must have 4 dims, got {q.dim()} and {k.dim()}")
-    b, s, hq, d = q.shape
-    hk = k.shape[2]
+    if len(shape) != 4 or len(kshape) != 4:
+        raise VaeError(-2, f"q and k must have 4 dims, got {len(shape)} and {len(kshape)}")
+    b, s, hq, d = shape
+    kb, ks, hk, kd = kshape
     if b > _INT or s > _INT or hq > _INT or hk > _INT or d > _INT:
         _sizes(b=b, s=s, hq=hq, hk=hk, d=d)
-    if k.shape != (b, s, hk, d):
-        raise VaeError(-2, f"k must be {(b, s, hk, d)}, got {tuple(k.shape)}")
+    if kb != b or ks != s or kd != d:
+        raise VaeError(-2, f"k must be {(b, s, hk, d)}, got {tuple(kshape)}")
     if gamma_q is not None:
         _tensor(gamma_q, "gamma_q", _T.f32, (d,))
     if gamma_k is not None:
         _tensor(gamma_k, "gamma_k", _T.f32, (d,))
-    if (positions is None) != (plan is None):
-        raise VaeError(-1, "positions and plan come together")
     ints, pb = False, 1
     if positions is not None:
-        ints = positions.dtype == _T.i32
-        if not ints and positions.dtype != _T.f32:
-            raise VaeError(-1, f"positions must be float32 or int32, got {positions.dtype}")
-        pb = positions.shape[0] if positions.dim() == 3 else 1
+        if plan is None:
+            raise VaeError(-1, "positions and plan come together")
+        pt, pshape = positions.dtype, positions.shape
+        ints = pt is _T.i32
+        if not ints and pt is not _T.f32:
+            raise VaeError(-1, f"positions must be float32 or int32, got {pt}")
         na = len(plan.axes)
-        _tensor(positions, "positions", positions.dtype, (pb, s, na) if positions.dim() == 3 else (s, na))
+        if len(pshape) == 3:
+            pb = pshape[0]
+            _tensor(positions, "positions", pt, (pb, s, na))
+        else:
+            _tensor(positions, "positions", pt, (s, na))
+    elif plan is not None:
+        raise VaeError(-1, "positions and plan come together")
     if q_out is None:
-        q_out = _T.empty(q.shape, dtype=dtype, device=q.device)
+        q_out, qs = _T.empty(shape, dtype=dtype, device=q.device), _dense(s, hq, d)
     else:
-        _like(q_out, q, "q's output", None)
+        qs = _strides3(_like(q_out, q, "q's output", None), "q's output")
     if k_out is None:
-        k_out = _T.empty(k.shape, dtype=dtype, device=q.device)
+        k_out, ks = _T.empty(kshape, dtype=dtype, device=q.device), _dense(s, hk, d)
     else:
-        _like(k_out, k, "k's output", None)
-    more = _NO_STRIDES[:6]
-    if dq_out is not None:
-        _like(dq_out, q, "dq_out", None)
-        _like(dk_out, k, "dk_out", None)
-        more = (*_strides3(dq_out, "dq_out"), *_strides3(dk_out, "dk_out"))
-    return _QK_DESC.pack(code, b, s, hq, hk, d, eps, ints, pb, *_strides3(q, "q"), *_strides3(k, "k"),
-                         *_strides3(q_out, "q's output"), *_strides3(k_out, "k's output"), *more), q_out, k_out
+        ks = _strides3(_like(k_out, k, "k's output", None), "k's output")
+    if dq_out is None:
+        more = _NO_STRIDES[:6]
+    else:
+        more = (*_strides3(_like(dq_out, q, "dq_out", None), "dq_out"), *_strides3(_like(dk_out, k, "dk_out", None), "dk_out"))
+    return _QK_DESC.pack(code, b, s, hq, hk, d, eps, ints, pb, *_strides3(q, "q"), *_strides3(k, "k"), *qs, *ks,
+                         *more), q_out, k_out
 
 
 def qk_norm_rope(q, k, gamma_q=None, gamma_k=None, positions=None, plan: Optional[RopePlan] = None, eps: float = 1e-6,
@@ -993,8 +998,9 @@ def _gated_ffn(x, w_gate, w_up, w_down, activation, residual, save, out_dtype, o
     L = lib()
     saved, at = None, (None, None, None)
     if save:
-        both = _T.empty((3, m, f), dtype=dtype, device=device)
-        saved = (both[0], both[1], both[2])
+        mf = (m, f)
+        saved = (_T.empty(mf, dtype=dtype, device=device), _T.empty(mf, dtype=dtype, device=device),
+                 _T.empty(mf, dtype=dtype, device=device))
         at = (saved[0].data_ptr(), saved[1].data_ptr(), saved[2].data_ptr())
     if workspace is None:
         nb = L.vae_gated_ffn_workspace_bytes(desc)
@@ -1029,30 +1035,33 @@ def _gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, hidden, activatio
                         dw_up, dw_down, workspace, stream):
     code, m, c, f = _ffn_args(x, w_gate, w_up, w_down)
     dtype, device = x.dtype, x.device
-    _tensor(dy, "dy", dtype, (m, c))
-    for t, name in ((gate, "gate"), (up, "up"), (hidden, "hidden")):
-        _tensor(t, name, dtype, (m, f))
+    mc, mf = x.shape, (m, f)
+    _tensor(dy, "dy", dtype, mc)
+    _tensor(gate, "gate", dtype, mf)
+    _tensor(up, "up", dtype, mf)
+    _tensor(hidden, "hidden", dtype, mf)
     if dx is None:
-        dx = _T.empty((m, c), dtype=dtype, device=device)
+        dx = _T.empty(mc, dtype=dtype, device=device)
     else:
-        _tensor(dx, "dx", dtype, (m, c))
-    given = [t for t in (dw_gate, dw_up, dw_down) if t is not None]
-    if not weight_grads and given:
+        _tensor(dx, "dx", dtype, mc)
+    given = dw_gate if dw_gate is not None else dw_up if dw_up is not None else dw_down
+    if given is not None and not weight_grads:
         raise VaeError(-1, "dw_gate, dw_up and dw_down need weight_grads")
-    wt = grad_dtype or (given[0].dtype if given else dtype)
+    wt = grad_dtype or (dtype if given is None else given.dtype)
     if weight_grads:
-        if dw_gate is None and dw_up is None:
-            both = _T.empty((2, f, c), dtype=wt, device=device)
-            dw_gate, dw_up = both[0], both[1]
-        elif dw_gate is None:
-            dw_gate = _T.empty((f, c), dtype=wt, device=device)
-        elif dw_up is None:
-            dw_up = _T.empty((f, c), dtype=wt, device=device)
+        fc = w_gate.shape
+        if dw_gate is None:
+            dw_gate = _T.empty(fc, dtype=wt, device=device)
+        else:
+            _tensor(dw_gate, "dw_gate", wt, fc)
+        if dw_up is None:
+            dw_up = _T.empty(fc, dtype=wt, device=device)
+        else:
+            _tensor(dw_up, "dw_up", wt, fc)
         if dw_down is None:
-            dw_down = _T.empty((c, f), dtype=wt, device=device)
-        _tensor(dw_gate, "dw_gate", wt, (f, c))
-        _tensor(dw_up, "dw_up", wt, (f, c))
-        _tensor(dw_down, "dw_down", wt, (c, f))
+            dw_down = _T.empty(w_down.shape, dtype=wt, device=device)
+        else:
+            _tensor(dw_down, "dw_down", wt, w_down.shape)
     desc = _FFN_DESC.pack(code, m, c, f, _activation(activation), code, 0, _type(wt, "grad_dtype"))
     L = lib()
     if workspace is None:

@@ -85,6 +85,9 @@ struct Params {
     int half;                  // kGrad: stages of dx's first segment
     void* out[4];              // kGate: hidden, gate, up; kDown: y; kGrad: dx, dWg, dWu, dWd
     float* parts[2];           // with splits: D of each problem and split, [problems * splits][rows][cols]
+    unsigned* arrived[2];      // with splits: how many of them have stored a warp's part of a tile, [tile][CTA of the pair][warp]
+    unsigned* clear;           // counters of the kernel behind this one: set to 0 here
+    int clear_n;
     int out_f32[2];
     const float* residual;
     const unsigned* amax;      // f16 gradients: the bits of the largest |dy|, from `amax_n` blocks
@@ -394,6 +397,96 @@ struct Boxes {
     }
 };
 
+// Sixteen columns (eight where `left` is less) of a row of D from column n on, in its type. dWd comes as D^T = hidden^T dy:
+// lanes are neighbours along its rows.
+template <int T, int kKind>
+__device__ __forceinline__ void put_out(const Params& p, const Tile& ti, int row, int n, int left, const float (&v)[16]) {
+    const Group& gr = p.group[ti.g];
+    const long long at = static_cast<long long>(row) * gr.cols + n;
+    void* out = p.out[ti.z];
+    if (kKind == kGrad && ti.z == 3) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if (k >= left) continue;
+            const long long o = static_cast<long long>(n + k) * gr.rows + row;
+            if (p.out_f32[1]) static_cast<float*>(out)[o] = v[k];
+            else static_cast<typename Elem<T>::type*>(out)[o] = from_f32<T>(v[k]);
+        }
+    } else if (p.out_f32[ti.g]) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            if (k >= left) continue;
+            float4 r = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            if (kKind == kDown && p.residual != nullptr) {
+                const float4 o = *reinterpret_cast<const float4*>(p.residual + at + k);
+                r = make_float4(r.x + o.x, r.y + o.y, r.z + o.z, r.w + o.w);
+            }
+            *reinterpret_cast<float4*>(static_cast<float*>(out) + at + k) = r;
+        }
+    } else {
+        store16(static_cast<uint16_t*>(out) + at, pack16<T>(v), left, p.wide);
+    }
+}
+// The same of a split's sums, kept as D is.
+template <int kKind>
+__device__ __forceinline__ void put_part(const Group& gr, const Tile& ti, float* part, int row, int n, int left, const float (&v)[16]) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) {
+        if (k >= left) continue;
+        if (kKind == kGrad && ti.z == 3) {
+#pragma unroll
+            for (int q = k; q < k + 4; ++q) part[static_cast<long long>(n + q) * gr.rows + row] = v[q];
+        } else {
+            *reinterpret_cast<float4*>(part + static_cast<long long>(row) * gr.cols + n + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        }
+    }
+}
+// Adds up the splits' parts, `each` apart, of a warp's 32 rows from row0 on and `mine` columns from n0 on, in their order,
+// and writes D. Four lanes take a row's sixteen columns (a lane a row's: every 16 bytes a request of their own, 35 us
+// instead of 17 for 256 tokens of 512 x 2048); of dWd, which lies transposed, a lane takes a row.
+constexpr int kMaxSplits = 8;
+template <int T, int kKind>
+__device__ __forceinline__ void join_parts(const Params& p, const Tile& ti, const float* parts, long long each, int row0, int n0, int mine, int lane) {
+    const Group& gr = p.group[ti.g];
+    if (kKind == kGrad && ti.z == 3) {
+        const int row = row0 + lane;
+        for (int n = n0; n < n0 + mine && n < gr.cols && row < gr.rows; ++n) {
+            const long long at = static_cast<long long>(n) * gr.rows + row;
+            float r[kMaxSplits], v = 0.f;
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s) r[s] = s < gr.splits ? __ldcg(parts + each * s + at) : 0.f;
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s) v += r[s];
+            if (p.out_f32[1]) static_cast<float*>(p.out[3])[at] = v;
+            else static_cast<typename Elem<T>::type*>(p.out[3])[at] = from_f32<T>(v);
+        }
+        return;
+    }
+    for (int c = (lane & 3) * 4; c < mine; c += 16) {
+#pragma unroll 4
+        for (int i = 0; i < 4; ++i) {
+            const int row = row0 + i * 8 + (lane >> 2), n = n0 + c;
+            if (row >= gr.rows || n >= gr.cols) continue;
+            const long long at = static_cast<long long>(row) * gr.cols + n;
+            float4 r[kMaxSplits], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s)
+                r[s] = s < gr.splits ? __ldcg(reinterpret_cast<const float4*>(parts + each * s + at)) : v;
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s) v = make_float4(v.x + r[s].x, v.y + r[s].y, v.z + r[s].z, v.w + r[s].w);
+            if (!p.out_f32[ti.g]) {
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out[ti.z]) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+                continue;
+            }
+            if (kKind == kDown && p.residual != nullptr) {
+                const float4 o = *reinterpret_cast<const float4*>(p.residual + at);
+                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            }
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out[ti.z]) + at) = v;
+        }
+    }
+}
+
 // Warp w: lane quadrant w % 4 of TMEM (a row per lane), half w / 4 of the columns.
 template <int T, int kKind, int kAct>
 __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, uint32_t tmem, int warp, int lane, int rank) {
@@ -404,6 +497,9 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
     const int pair = static_cast<int>(blockIdx.x >> 1);
     if (kKind == kBackGate && p.late) pdl_wait();
     const float gain = kKind >= kBackGate ? dy_scale(p) : 1.f;
+    if (kKind == kGate || kKind == kBackGate)
+        for (int i = static_cast<int>(blockIdx.x) * kEpiWarps * 32 + warp * 32 + lane; i < p.clear_n; i += static_cast<int>(gridDim.x) * kEpiWarps * 32)
+            p.clear[i] = 0u;
     Boxes boxes;
     if constexpr (kKind == kBackGate) {
         boxes.more = half == 0 && tile_at(p, pair, 0, &boxes.ti);
@@ -501,34 +597,8 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]) * scale;
                 if (!live) continue;
-                const bool split = gr.splits > 1, f32 = p.out_f32[ti.g] != 0;
-                float* part = p.parts[ti.g] + static_cast<long long>(ti.part) * rows * cols;
-                if (kKind == kGrad && ti.z == 3) {
-                    // D^T = hidden^T dy: lanes are neighbours along a row of dWd
-                    const long long at = static_cast<long long>(n) * rows + row;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        if (k >= left) continue;
-                        const long long o = at + static_cast<long long>(k) * rows;
-                        if (split) part[o] = v[k];
-                        else if (f32) static_cast<float*>(p.out[3])[o] = v[k];
-                        else static_cast<typename Elem<T>::type*>(p.out[3])[o] = from_f32<T>(v[k]);
-                    }
-                } else if (split || f32) {
-                    float* y = split ? part : static_cast<float*>(p.out[ti.z]);
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        if (k >= left) continue;
-                        float4 r = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                        if (kKind == kDown && !split && p.residual != nullptr) {
-                            const float4 o = *reinterpret_cast<const float4*>(p.residual + at0 + n + k);
-                            r = make_float4(r.x + o.x, r.y + o.y, r.z + o.z, r.w + o.w);
-                        }
-                        *reinterpret_cast<float4*>(y + at0 + n + k) = r;
-                    }
-                } else {
-                    store16(static_cast<uint16_t*>(p.out[ti.z]) + at0 + n, pack16<T>(v), left, p.wide);
-                }
+                if (gr.splits > 1) put_part<kKind>(gr, ti, p.parts[ti.g] + static_cast<long long>(ti.part) * rows * cols, row, n, left, v);
+                else put_out<T, kKind>(p, ti, row, n, left, v);
             }
         }
         tc_fence_before();
@@ -536,6 +606,22 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acce[buf]), 0u));
         buf ^= 1;
         if (buf == 0) phase ^= 1u;
+        if constexpr (kKind == kDown || kKind == kGrad) {
+            if (gr.splits > 1) {
+                // The last split to store this warp's part of the tile adds them all up, in their order: nobody waits, and
+                // the sum does not depend on who is last.
+                __threadfence();
+                __syncwarp();
+                const int z = ti.part / gr.splits, tile = (z * gr.nm + ti.m0 / (2 * kTile)) * (gr.nfull + (gr.rest > 0 ? 1 : 0)) + ti.n0 / gr.wide;
+                unsigned before = 0u;
+                if (lane == 0) before = atomicAdd(p.arrived[ti.g] + (tile * 2 + rank) * kEpiWarps + warp, 1u);
+                if (__shfl_sync(0xffffffffu, before, 0) + 1u != static_cast<unsigned>(gr.splits)) continue;
+                __threadfence();
+                const long long each = static_cast<long long>(rows) * cols;
+                join_parts<T, kKind>(p, ti, p.parts[ti.g] + each * z * gr.splits, each, row - lane, n0, mine, lane);
+                __syncwarp();
+            }
+        }
     }
     if constexpr (kKind == kBackGate) {
         if (half == 0) {  // boxes that a wait that ran out left on their way land before the CTA exits
@@ -636,41 +722,6 @@ __global__ void __launch_bounds__(512) amax_kernel(const uint4* x, long long n8,
     }
 }
 
-struct JoinParams {
-    const float* parts[4];
-    void* out[4];
-    long long n8[4];
-    int splits[4], f32[4];
-    const float* residual;
-};
-// The splits' sums, in order, eight elements a thread: D of each problem in its type.
-template <int T>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p) {
-    pdl_wait();
-    const int z = blockIdx.y, splits = p.splits[z];
-    const long long n8 = p.n8[z];
-    const float* parts = p.parts[z];
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<long long>(gridDim.x) * 256) {
-        float v[8];
-        load8<VAE_F32>(parts + i * 8, v);
-        for (int s = 1; s < splits; ++s) {
-            float w[8];
-            load8<VAE_F32>(parts + (s * n8 + i) * 8, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += w[k];
-        }
-        if (p.residual != nullptr) {
-            float w[8];
-            load8<VAE_F32>(p.residual + i * 8, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += w[k];
-        }
-        if (p.f32[z]) store8<VAE_F32>(static_cast<float*>(p.out[z]) + i * 8, v);
-        else store8<T>(static_cast<typename Elem<T>::type*>(p.out[z]) + i * 8, v);
-    }
-    pdl_launch_dependents();
-}
-
 // ───────────────────────────── host ─────────────────────────────
 
 // A matrix [rows][inner] as the boxes that a stage takes of it: 64 of the inner index, `box_rows` of the other.
@@ -762,9 +813,13 @@ Group cut_group(int rows, int cols, int problems, int nk, int wide, int splits) 
 size_t parts_bytes(const Group& g) {
     return g.splits > 1 ? static_cast<size_t>(g.splits) * g.problems * g.rows * g.cols * sizeof(float) : 0;
 }
+// Counters of a group's splits: for each tile, CTA of the pair and epilogue warp.
+int arrivals(const Group& g) { return g.splits > 1 ? g.problems * g.nm * (g.nfull + (g.rest > 0 ? 1 : 0)) * 2 * kEpiWarps : 0; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // The tile width and the splits with the least time, counted in cycles of the busiest pair. Wide tiles read the least;
-// narrow ones and splits give work to more SMs. Splits cost a second kernel (4000 cycles) that reads the f32 sums that
-// they write (2700 bytes a cycle both ways). `base`: the groups uncut.
+// narrow ones and splits give work to more SMs. Splits cost the last one's way through the f32 sums that all of them
+// write: 2000 cycles, and 40 for each column and split. (A second kernel for that way took 17.5 us instead of 18.0 for 256
+// tokens of 512 x 2048 in a graph, and 2 to 4 us more of the host in a call.) `base`: the groups uncut.
 Plan make_plan(int kind, const Group* base, int count) {
     const int per = kind == kGate ? 2 : 1;  // accumulator columns per column
     const bool whole = kind == kGate || kind == kBackGate;  // (their epilogues need the whole sums)
@@ -774,15 +829,14 @@ Plan make_plan(int kind, const Group* base, int count) {
         const auto cut = [&](int g, int splits) {
             return cut_group(base[g].rows, base[g].cols, base[g].problems, base[g].nk, wide / per, splits);
         };
-        const auto most = [&](int g) { return whole ? 1 : std::min(8, std::max(1, base[g].nk / 4)); };
+        const auto most = [&](int g) { return whole ? 1 : std::min(kMaxSplits, std::max(1, base[g].nk / 4)); };
         for (int s0 = 1; s0 <= most(0); ++s0)
             for (int s1 = 1; s1 <= (count > 1 ? most(1) : 1); ++s1) {
                 Plan p{};
                 p.group[0] = cut(0, s0);
                 if (count > 1) p.group[1] = cut(1, s1);
                 long long t = deal_out(p.group, count, per, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
-                const size_t parts = parts_bytes(p.group[0]) + (count > 1 ? parts_bytes(p.group[1]) : 0);
-                if (parts > 0) t += 4000 + static_cast<long long>(2 * parts / 2700);
+                if (s0 > 1 || s1 > 1) t += 2000 + 40LL * wide * std::max(s0, s1);
                 if (least < 0 || t < least) {
                     best = p;
                     least = t;
@@ -858,23 +912,6 @@ int ffn_launch(const Maps& maps, const Plan& plan, Params& p, bool ahead, cudaSt
     }
     VAE_CUDA_CHECK(launch_kernel_as(ahead || pdl_enabled(), ffn_kernel<T, kKind, kAct>, dim3(2 * pairs), dim3(kThreads), smem_bytes(kKind),
                                     stream, maps, p));
-    JoinParams join{};
-    int joins = 0;
-    for (int g = 0; g < count; ++g)
-        for (int z = 0; p.group[g].splits > 1 && z < p.group[g].problems; ++z, ++joins) {
-            const Group& gr = p.group[g];
-            join.n8[joins] = static_cast<long long>(gr.rows) * gr.cols / 8;
-            join.parts[joins] = p.parts[g] + join.n8[joins] * 8 * gr.splits * z;
-            join.out[joins] = p.out[g + z];
-            join.splits[joins] = gr.splits;
-            join.f32[joins] = p.out_f32[g];
-        }
-    if (joins > 0) {
-        join.residual = p.residual;
-        const long long n8 = *std::max_element(join.n8, join.n8 + joins);
-        const unsigned grid = static_cast<unsigned>(std::min<long long>((n8 + 255) / 256, 152 * 8));
-        VAE_CUDA_CHECK(launch_next(join_kernel<T>, dim3(grid, joins), dim3(256), 0, stream, join));
-    }
     return VAE_OK;
 }
 
@@ -920,7 +957,6 @@ int ffn_check(const vae_gated_ffn_desc* a, bool backward) {
     return VAE_OK;
 }
 
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 size_t mc_bytes(const vae_gated_ffn_desc& a) { return static_cast<size_t>(a.m) * a.c * 2; }
 size_t mf_bytes(const vae_gated_ffn_desc& a) { return static_cast<size_t>(a.m) * a.f * 2; }
 size_t cf_bytes(const vae_gated_ffn_desc& a) { return static_cast<size_t>(a.c) * a.f * 2; }
@@ -935,10 +971,14 @@ bool on32(const void* q) { return reinterpret_cast<uintptr_t>(q) % 32 == 0; }
 
 template <int T>
 int ffn_forward(const vae_gated_ffn_desc& a, const void* x, const void* wg, const void* wu, const void* wd, const float* residual,
-                void* y, void* gate, void* up, void* hidden, float* parts, cudaStream_t stream) {
+                void* y, void* gate, void* up, void* hidden, char* ws, cudaStream_t stream) {
     Maps maps;
     Params p{};
-    Plan plan = plan_for(kGate, a);
+    const Plan down = plan_for(kDown, a);
+    unsigned* arrived = reinterpret_cast<unsigned*>(ws);
+    p.clear = arrived;
+    p.clear_n = arrivals(down.group[0]);
+    const Plan plan = plan_for(kGate, a);
     VAE_TRY(ffn_map(&maps.a[0], T, x, a.m, a.c, kTile));
     VAE_TRY(ffn_map(&maps.b[0], T, wg, a.f, a.c, plan.group[0].wide));
     VAE_TRY(ffn_map(&maps.b[1], T, wu, a.f, a.c, plan.group[0].wide));
@@ -948,27 +988,29 @@ int ffn_forward(const vae_gated_ffn_desc& a, const void* x, const void* wg, cons
     p.wide = a.f % 16 == 0 && on32(hidden) && on32(gate) && on32(up);
     VAE_TRY((ffn_launch_act<T, kGate>(a.activation, maps, plan, p, false, stream)));
     p = Params{};
-    plan = plan_for(kDown, a);
     VAE_TRY(ffn_map(&maps.a[0], T, hidden, a.m, a.f, kTile));
-    VAE_TRY(ffn_map(&maps.b[0], T, wd, a.c, a.f, plan.group[0].wide / 2));
+    VAE_TRY(ffn_map(&maps.b[0], T, wd, a.c, a.f, down.group[0].wide / 2));
     p.out[0] = y;
-    p.parts[0] = parts;
+    p.arrived[0] = arrived;
+    p.parts[0] = reinterpret_cast<float*>(ws + up256(arrivals(down.group[0]) * sizeof(unsigned)));
     p.out_f32[0] = a.y_type == VAE_F32;
     p.residual = residual;
     p.wide = a.c % 16 == 0 && on32(y);
-    return ffn_launch<T, kDown>(maps, plan, p, true, stream);
+    return ffn_launch<T, kDown>(maps, down, p, true, stream);
 }
 
-// Workspace of the gradient: the largest |dy|, dgate, dup, partial sums.
+// Workspace of the gradient: the largest |dy|, dgate, dup, the counters of splits, partial sums.
 struct BackSpace {
-    size_t dgate, dup, parts[2], bytes;
+    size_t dgate, dup, arrived[2], parts[2], bytes;
 };
 BackSpace back_space(const vae_gated_ffn_desc& a) {
     BackSpace s;
     s.dgate = up256(kAmaxBlocks * sizeof(unsigned));
     s.dup = s.dgate + up256(mf_bytes(a));
-    s.parts[0] = s.dup + up256(mf_bytes(a));
     const Plan plan = plan_for(kGrad, a);
+    s.arrived[0] = s.dup + up256(mf_bytes(a));
+    s.arrived[1] = s.arrived[0] + arrivals(plan.group[0]) * sizeof(unsigned);
+    s.parts[0] = up256(s.arrived[1] + arrivals(plan.group[1]) * sizeof(unsigned));
     s.parts[1] = s.parts[0] + up256(parts_bytes(plan.group[0]));
     s.bytes = s.parts[1] + parts_bytes(plan.group[1]);
     return s;
@@ -996,6 +1038,9 @@ int ffn_backward(const vae_gated_ffn_desc& a, const void* dy, const void* x, con
     VAE_TRY(ffn_map(&maps.side[1], T, up, a.m, a.f, 32));
     VAE_TRY(ffn_map(&maps.side[2], T, dgate, a.m, a.f, 32));
     VAE_TRY(ffn_map(&maps.side[3], T, dup, a.m, a.f, 32));
+    Plan plan = plan_for(kGrad, a);
+    p.clear = reinterpret_cast<unsigned*>(ws + at.arrived[0]);
+    p.clear_n = arrivals(plan.group[0]) + arrivals(plan.group[1]);
     VAE_TRY((ffn_launch_act<T, kBackGate>(a.activation, maps, plan_for(kBackGate, a), p, p.late != 0, stream)));
     const bool weights = dwg != nullptr;
     VAE_TRY(ffn_map(&maps.a[0], T, dgate, a.m, a.f, kBk));
@@ -1015,9 +1060,10 @@ int ffn_backward(const vae_gated_ffn_desc& a, const void* dy, const void* x, con
     p.out[3] = dwd;
     p.parts[0] = reinterpret_cast<float*>(ws + at.parts[0]);
     p.parts[1] = reinterpret_cast<float*>(ws + at.parts[1]);
+    p.arrived[0] = reinterpret_cast<unsigned*>(ws + at.arrived[0]);
+    p.arrived[1] = reinterpret_cast<unsigned*>(ws + at.arrived[1]);
     p.out_f32[1] = a.dw_type == VAE_F32;
     p.wide = a.c % 16 == 0 && on32(dx) && on32(dwg) && on32(dwu);
-    Plan plan = plan_for(kGrad, a);
     if (!weights) {  // dx alone, cut the same way: the same bits
         plan.group[1] = Group{};
         deal_out(plan.group, 1, 1, kPairs, &plan.deal);
@@ -1035,8 +1081,11 @@ extern "C" {
 size_t vae_gated_ffn_workspace_bytes(const vae_gated_ffn_desc* desc) {
     clear_error();
     if (ffn_check(desc, false) != VAE_OK) return 0;
-    // hidden, where it is not saved, and partial sums
-    return (desc->save ? 0 : up256(mf_bytes(*desc))) + (desc->m <= kFewTokens ? 0 : parts_bytes(plan_for(kDown, *desc).group[0]));
+    // hidden, where it is not saved; partial sums and their counters
+    const size_t hidden = desc->save ? 0 : up256(mf_bytes(*desc));
+    if (desc->m <= kFewTokens) return hidden;
+    const Group g = plan_for(kDown, *desc).group[0];
+    return hidden + up256(arrivals(g) * sizeof(unsigned)) + parts_bytes(g);
 }
 
 int vae_gated_ffn(const vae_gated_ffn_desc* desc, const void* x_dev, const void* w_gate_dev, const void* w_up_dev,
@@ -1071,10 +1120,10 @@ int vae_gated_ffn(const vae_gated_ffn_desc* desc, const void* x_dev, const void*
     void* hidden = save ? hidden_dev : workspace_dev;
     if (a.m <= kFewTokens)
         return ffn_few(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, st);
-    float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + (save ? 0 : up256(mf_bytes(a))));
+    char* ws = static_cast<char*>(workspace_dev) + (save ? 0 : up256(mf_bytes(a)));
     return a.type == VAE_F16
-               ? ffn_forward<VAE_F16>(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, parts, st)
-               : ffn_forward<VAE_BF16>(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, parts, st);
+               ? ffn_forward<VAE_F16>(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, ws, st)
+               : ffn_forward<VAE_BF16>(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, ws, st);
 }
 
 size_t vae_gated_ffn_backward_workspace_bytes(const vae_gated_ffn_desc* desc) {
