@@ -752,7 +752,9 @@ long long deal_out(const Group* groups, int count, int per, int pairs, Deal* d) 
         if (c >> 1 >= count) continue;
         const Group& g = groups[c >> 1];
         tiles[c] = class_tiles(g, c & 1);
-        cost[c] = 400 + static_cast<long long>(stage_cycles(((c & 1) != 0 ? g.rest : g.wide) * per)) * ((g.nk + g.splits - 1) / g.splits);
+        // its stages, or where they are few its way out of TMEM (which runs under the next tile's stages)
+        const int n = ((c & 1) != 0 ? g.rest : g.wide) * per;
+        cost[c] = std::max(400 + static_cast<long long>(stage_cycles(n)) * ((g.nk + g.splits - 1) / g.splits), 600 + 12LL * n);
     }
     std::sort(d->order, d->order + 4, [&](int a, int b) { return cost[a] != cost[b] ? cost[a] > cost[b] : a < b; });
     for (int c : d->order) {
@@ -818,7 +820,7 @@ int arrivals(const Group& g) { return g.splits > 1 ? g.problems * g.nm * (g.nful
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // The tile width and the splits with the least time, counted in cycles of the busiest pair. Wide tiles read the least;
 // narrow ones and splits give work to more SMs. Splits cost the last one's way through the f32 sums that all of them
-// write: 2000 cycles, and 40 for each column and split. (A second kernel for that way took 17.5 us instead of 18.0 for 256
+// write: 4000 cycles, 80 for each column and 10 for each split of it. (A second kernel for that way took 17.5 us instead of 18.0 for 256
 // tokens of 512 x 2048 in a graph, and 2 to 4 us more of the host in a call.) `base`: the groups uncut.
 Plan make_plan(int kind, const Group* base, int count) {
     const int per = kind == kGate ? 2 : 1;  // accumulator columns per column
@@ -836,7 +838,7 @@ Plan make_plan(int kind, const Group* base, int count) {
                 p.group[0] = cut(0, s0);
                 if (count > 1) p.group[1] = cut(1, s1);
                 long long t = deal_out(p.group, count, per, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
-                if (s0 > 1 || s1 > 1) t += 2000 + 40LL * wide * std::max(s0, s1);
+                if (s0 > 1 || s1 > 1) t += 4000 + (80 + 10LL * std::max(s0, s1)) * wide;
                 if (least < 0 || t < least) {
                     best = p;
                     least = t;
