@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_kernel(c
     if (kGated && threadIdx.x == 0) {
         const long long blocks = static_cast<long long>(gridDim.x) * splits, b = static_cast<long long>(blockIdx.x) * splits + split;
         const long long from = p.next_bytes / 16 * b / blocks * 16, to = p.next_bytes / 16 * (b + 1) / blocks * 16;
-        if (to > from) prefetch_l2_bulk(static_cast<const char*>(p.next) + from, static_cast<uint32_t>(to - from));
+        const long long most = 1 << 16;  // (few blocks: the first part of their share)
+        if (to > from) prefetch_l2_bulk(static_cast<const char*>(p.next) + from, static_cast<uint32_t>(to - from < most ? to - from : most));
     }
 
     float d[kMats][kN][4] = {};

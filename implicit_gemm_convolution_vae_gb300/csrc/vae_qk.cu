@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_plain_kernel(const QkParams p, 
         const float sn = second != kBack ? a.y : -a.y;  // (turned back, the sines change sign)
         return v * a.x + w * sn;
     };
-    for (int t0 = static_cast<int>(blockIdx.x) * p.tpb; t0 < p.tokens; t0 += static_cast<int>(gridDim.x) * p.tpb) {
+    const int stride = static_cast<int>(gridDim.x) * p.tpb;  // (at most p.tokens and a turn: no sum below passes 31 bits)
+    for (int t0 = static_cast<int>(blockIdx.x) * p.tpb; t0 < p.tokens; t0 = p.tokens - t0 > stride ? t0 + stride : p.tokens) {
         const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
         __syncthreads();
         for (int i = threadIdx.x; i < nt * pairs; i += kQkThreads) {
