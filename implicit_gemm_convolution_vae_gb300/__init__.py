@@ -436,7 +436,7 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.torch, self.empty, self.zeros = torch, torch.empty, torch.zeros
+        self.torch, self.empty, self.zeros, self.like = torch, torch.empty, torch.zeros, torch.empty_like
         self.f32, self.i32, self.u8 = torch.float32, torch.int32, torch.uint8
         self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self.types = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -991,7 +991,7 @@ def _gated_ffn(x, w_gate, w_up, w_down, activation, residual, save, out_dtype, o
         _tensor(residual, "residual", _T.f32, (m, c))
         out_dtype = out_dtype or _T.f32
     if out is None:
-        out = _T.empty((m, c), dtype=out_dtype or dtype, device=device)
+        out = _T.like(x) if out_dtype is None else _T.empty((m, c), dtype=out_dtype, device=device)
     else:
         _tensor(out, "out", out_dtype or out.dtype, (m, c))
     desc = _FFN_DESC.pack(code, m, c, f, _activation(activation), _type(out.dtype, "out"), bool(save), code)
@@ -1041,7 +1041,7 @@ def _gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, hidden, activatio
     _tensor(up, "up", dtype, mf)
     _tensor(hidden, "hidden", dtype, mf)
     if dx is None:
-        dx = _T.empty(mc, dtype=dtype, device=device)
+        dx = _T.like(x)
     else:
         _tensor(dx, "dx", dtype, mc)
     given = dw_gate if dw_gate is not None else dw_up if dw_up is not None else dw_down
@@ -1051,15 +1051,15 @@ def _gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, hidden, activatio
     if weight_grads:
         fc = w_gate.shape
         if dw_gate is None:
-            dw_gate = _T.empty(fc, dtype=wt, device=device)
+            dw_gate = _T.like(w_gate, dtype=wt)
         else:
             _tensor(dw_gate, "dw_gate", wt, fc)
         if dw_up is None:
-            dw_up = _T.empty(fc, dtype=wt, device=device)
+            dw_up = _T.like(w_up, dtype=wt)
         else:
             _tensor(dw_up, "dw_up", wt, fc)
         if dw_down is None:
-            dw_down = _T.empty(w_down.shape, dtype=wt, device=device)
+            dw_down = _T.like(w_down, dtype=wt)
         else:
             _tensor(dw_down, "dw_down", wt, w_down.shape)
     desc = _FFN_DESC.pack(code, m, c, f, _activation(activation), code, 0, _type(wt, "grad_dtype"))
