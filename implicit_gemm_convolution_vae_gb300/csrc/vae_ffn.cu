@@ -27,7 +27,9 @@ constexpr int kTile = 128;              // rows of A per CTA
 constexpr int kMaxCols = 256;           // columns of the pair's accumulator
 constexpr int kBk = 64;                 // contraction per stage: one 128-byte swizzle row
 constexpr int kOperand = kTile * kBk * 2;  // bytes
-constexpr int kStage = 2 * kOperand;
+constexpr int kStage = 2 * kOperand;       // A, B
+constexpr int kTallStage = 3 * kOperand;   // A, B, the other 256 rows' A
+constexpr int kTallStages = 4;
 constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;     // two accumulators
@@ -53,6 +55,7 @@ constexpr int kBoxBufs = 3;
 __host__ __device__ constexpr int ring_stages(int kind) { return kind == kBackGate ? 4 : 7; }
 __host__ __device__ constexpr int side_bytes(int kind) { return kind == kBackGate ? 4 * kBoxBufs * 2 * kBox : 0; }
 __host__ __device__ constexpr int smem_bytes(int kind) { return 1024 + ring_stages(kind) * kStage + side_bytes(kind) + 512; }
+static_assert(kTallStages * kTallStage <= ring_stages(kGrad) * kStage, "the ring holds the tall stages");
 static_assert(smem_bytes(kGate) <= 232448 && smem_bytes(kBackGate) <= 232448, "shared memory over 227 KB");
 
 struct Maps {
@@ -67,6 +70,7 @@ struct Maps {
 struct Group {
     int rows, cols, problems, nk;
     int wide, rest, splits;
+    int tall;                  // tiles have 256 rows, or (2) 512, which read a quarter less
     int nm, nfull;             // row tiles, column tiles of full width
 };
 
@@ -94,6 +98,7 @@ struct Params {
     int amax_n;
     int late;                  // kBackGate: only the epilogue needs the kernel before (that is the one that looks for the largest |dy|)
     int wide;                  // rows of D on 32 bytes
+    int tall;                  // the launch has tiles of 512 rows: four stages of 48 KB, one accumulator for each 256 rows
     DevStatus* status;
     unsigned long long timeout_ns;
 };
@@ -126,6 +131,7 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
 struct Tile {
     int g, z, part;    // group, problem (in Params::out's order), partial sums
     int m0, n0, n;     // the pair's first row, the columns [n0, n0 + n)
+    int subs;          // times 256 rows (the last tile of 512 may have 256)
     int k0, k1;        // stages
 };
 // The i-th tile of pair `pair`; false behind its last. Row tiles lie in groups of kGroup, their column tiles side by
@@ -158,15 +164,16 @@ __host__ __device__ __forceinline__ bool tile_at(const Params& p, int pair, int 
         const int w = t / (kGroup * g.nfull), in = t - w * kGroup * g.nfull;
         const int tall = g.nm - w * kGroup < kGroup ? g.nm - w * kGroup : kGroup;
         nt = in / tall;
-        r->m0 = (w * kGroup + in - nt * tall) * 2 * kTile;
+        r->m0 = (w * kGroup + in - nt * tall) * g.tall * 2 * kTile;
         r->n = g.wide;
     } else {
         r->part = t / g.nm;
-        r->m0 = (t - r->part * g.nm) * 2 * kTile;
+        r->m0 = (t - r->part * g.nm) * g.tall * 2 * kTile;
         nt = g.nfull;
         r->n = g.rest;
     }
     r->n0 = nt * g.wide;
+    r->subs = r->m0 + 2 * kTile < g.rows ? g.tall : 1;
     r->g = c >> 1;
     const int z = r->part / g.splits, s = r->part - z * g.splits;
     r->z = r->g + z;
@@ -210,7 +217,8 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
 
 template <int kKind>
 __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, int rank) {
-    constexpr int kStages = ring_stages(kKind);
+    const bool tall = (kKind == kDown || kKind == kGrad) && p.tall != 0;
+    const int stages = tall ? kTallStages : ring_stages(kKind), stage_bytes = tall ? kTallStage : kStage;
     int stage = 0;
     uint32_t phase = 0, armed = 0, arm_par = 0;
     bool ok = true;
@@ -220,32 +228,37 @@ __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, 
         const int row = ti.m0 + rank * kTile, col = kKind == kGate ? ti.n0 : ti.n0 + rank * (ti.n / 2);
         // rows of B that a CTA loads: those of a full tile where the map's box says so, else boxes of 64
         const int brows = b_mn(kKind) ? ti.n / 2 : kKind == kGate ? p.group[0].wide : p.group[0].wide / 2;
-        const uint32_t bytes = kOperand + (b_mn(kKind) ? (brows > 64 ? 2u : 1u) * 64 * 128 : static_cast<uint32_t>(brows) * 128);
+        const uint32_t bytes = static_cast<uint32_t>(ti.subs) * kOperand + (b_mn(kKind) ? (brows > 64 ? 2u : 1u) * 64 * 128 : static_cast<uint32_t>(brows) * 128);
         for (int kk = ti.k0; kk < ti.k1; ++kk) {
             ok = mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, s.abort_flag, p.timeout_ns, p.status, kWhereProducerEmpty);
             if (!ok) break;
             const uint32_t fb = smem_u32(&s.full[stage]);
             if (rank == 0) mbar_arrive_expect_tx(fb, 2u * bytes);
             const uint32_t fb0 = mapa_shared(fb, 0u);
-            uint8_t *a = s.ring + stage * kStage, *b = a + kOperand;
-            if constexpr (kKind == kGrad) {
-                if (ti.g == 0) {  // dx: rows of dgate or dup as they lie, in boxes of 64
-                    const int seg = kk >= p.half ? 1 : 0, k = (kk - seg * p.half) * kBk;
-                    tma_load_2d_pair(smem_u32(a), &maps.a[seg], fb0, k, row);
-                    tma_load_2d_pair(smem_u32(a + kOperand / 2), &maps.a[seg], fb0, k, row + 64);
-                    load_mn(b, &maps.b[seg], fb0, col, brows, k);
+            uint8_t *a = s.ring + stage * stage_bytes, *b = a + kOperand;
+            for (int sub = 0; sub < ti.subs; ++sub) {
+                uint8_t* as = a + sub * kStage;
+                const int r = row + sub * 2 * kTile;
+                if constexpr (kKind == kGrad) {
+                    if (ti.g == 0) {  // dx: rows of dgate or dup as they lie, in boxes of 64
+                        const int seg = kk >= p.half ? 1 : 0, k = (kk - seg * p.half) * kBk;
+                        tma_load_2d_pair(smem_u32(as), &maps.a[seg], fb0, k, r);
+                        tma_load_2d_pair(smem_u32(as + kOperand / 2), &maps.a[seg], fb0, k, r + 64);
+                        if (sub == 0) load_mn(b, &maps.b[seg], fb0, col, brows, k);
+                    } else {
+                        load_mn(as, &maps.a[ti.z - 1], fb0, r, kTile, kk * kBk);
+                        if (sub == 0) load_mn(b, &maps.b[ti.z == 3 ? 3 : 2], fb0, col, brows, kk * kBk);
+                    }
                 } else {
-                    load_mn(a, &maps.a[ti.z - 1], fb0, row, kTile, kk * kBk);
-                    load_mn(b, &maps.b[ti.z == 3 ? 3 : 2], fb0, col, brows, kk * kBk);
+                    tma_load_2d_pair(smem_u32(as), &maps.a[0], fb0, kk * kBk, r);
+                    if (sub > 0) continue;
+                    if constexpr (kKind == kBackGate) load_mn(b, &maps.b[0], fb0, col, brows, kk * kBk);
+                    else tma_load_2d_pair(smem_u32(b), &maps.b[kKind == kGate ? rank : 0], fb0, kk * kBk, col);
                 }
-            } else {
-                tma_load_2d_pair(smem_u32(a), &maps.a[0], fb0, kk * kBk, row);
-                if constexpr (kKind == kBackGate) load_mn(b, &maps.b[0], fb0, col, brows, kk * kBk);
-                else tma_load_2d_pair(smem_u32(b), &maps.b[kKind == kGate ? rank : 0], fb0, kk * kBk, col);
             }
             armed |= 1u << stage;
             arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
-            if (++stage == kStages) {
+            if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -254,7 +267,7 @@ __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, 
     // Every copy lands before the CTA can exit: the even CTA sees them on its full barriers, the odd one
     // on its empty barriers (the products that read a slot complete after its copies).
     int never = 0;
-    for (int st = 0; st < kStages; ++st)
+    for (int st = 0; st < stages; ++st)
         if (armed & (1u << st))
             (void)mbar_wait(smem_u32(rank == 0 ? &s.full[st] : &s.empty[st]), (arm_par >> st) & 1u, &never, p.timeout_ns,
                             p.status, kWhereDrain);
@@ -263,7 +276,9 @@ __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, 
 // The whole warp runs the loop and one lane issues: descriptors stay in uniform registers.
 template <int T, int kKind>
 __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
-    constexpr int kStages = ring_stages(kKind);
+    const bool tall = (kKind == kDown || kKind == kGrad) && p.tall != 0;
+    const int stages = tall ? kTallStages : ring_stages(kKind);
+    const uint32_t stage_step = static_cast<uint32_t>(tall ? kTallStage : kStage) >> 4;
     constexpr uint32_t ab = T == VAE_BF16 ? 1u : 0u;
     constexpr uint32_t idesc0 = (1u << 4) | (ab << 7) | (ab << 10) | ((b_mn(kKind) ? 1u : 0u) << 16) | ((2u * kTile >> 4) << 24);
     constexpr uint32_t bstep = b_mn(kKind) ? 2048 >> 4 : 2;
@@ -289,21 +304,25 @@ __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
             ok = warp_all(mbar_wait(smem_u32(&s.full[stage]), phase, s.abort_flag, p.timeout_ns, p.status, kWhereMmaFull));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t off = static_cast<uint32_t>(stage) * (kStage >> 4);
+            const uint32_t off = static_cast<uint32_t>(stage) * stage_step;
             if (elect_one()) {
 #pragma unroll
-                for (uint32_t j = 0; j < kBk / 16; ++j)
+                for (uint32_t j = 0; j < kBk / 16; ++j) {
                     umma_f16_pair(d, ad + (off + j * astep), bd + (off + j * bstep), idesc, j != 0 || k != 0 ? 1u : 0u);
+                    if ((kKind == kDown || kKind == kGrad) && ti.subs > 1)
+                        umma_f16_pair(d + kMaxCols, ad + (off + (kStage >> 4) + j * astep), bd + (off + j * bstep), idesc,
+                                      j != 0 || k != 0 ? 1u : 0u);
+                }
                 umma_commit_pair(smem_u32(&s.empty[stage]));
                 if (k + 1 == nk) umma_commit_pair(smem_u32(&s.accf[buf]));
             }
             __syncwarp();
-            if (++stage == kStages) {
+            if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
-        buf ^= 1;
+        if (!tall) buf ^= 1;
         if (buf == 0) accphase ^= 1u;
     }
     if (elect_one()) {
@@ -567,16 +586,15 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
                 }
             }
         }
+        if constexpr (kKind == kGate) {
 #pragma unroll 1
-        for (int c = 0; kKind != kBackGate && c < mine; c += 16) {
-            const int n = n0 + c, left = cols - n;
-            if (left <= 0) break;  // (the same for the whole warp)
-            uint32_t x[16];
-            float v[16];
-            __syncwarp();
-            tmem_ld16(acc + static_cast<uint32_t>(c), x);
-            if constexpr (kKind == kGate) {
-                uint32_t y[16];
+            for (int c = 0; c < mine; c += 16) {
+                const int n = n0 + c, left = cols - n;
+                if (left <= 0) break;  // (the same for the whole warp)
+                uint32_t x[16], y[16];
+                float v[16];
+                __syncwarp();
+                tmem_ld16(acc + static_cast<uint32_t>(c), x);
                 tmem_ld16(acc + static_cast<uint32_t>(ti.n + c), y);
                 tmem_ld_wait_regs(x);
                 tmem_ld_wait_regs(y);
@@ -592,19 +610,32 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
                     for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(y[k]);
                     store16(static_cast<uint16_t*>(p.out[2]) + at0 + n, pack16<T>(v), left, p.wide);
                 }
-            } else {
-                tmem_ld_wait_regs(x);
+            }
+        }
+        if constexpr (kKind == kDown || kKind == kGrad) {
+            for (int sub = 0; sub < ti.subs; ++sub) {
+                const int r = row + sub * 2 * kTile;
+#pragma unroll 1
+                for (int c = 0; c < mine; c += 16) {
+                    const int n = n0 + c, left = cols - n;
+                    if (left <= 0) break;  // (the same for the whole warp)
+                    uint32_t x[16];
+                    float v[16];
+                    __syncwarp();
+                    tmem_ld16(acc + static_cast<uint32_t>(sub * kMaxCols + c), x);
+                    tmem_ld_wait_regs(x);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]) * scale;
-                if (!live) continue;
-                if (gr.splits > 1) put_part<kKind>(gr, ti, p.parts[ti.g] + static_cast<long long>(ti.part) * rows * cols, row, n, left, v);
-                else put_out<T, kKind>(p, ti, row, n, left, v);
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]) * scale;
+                    if (r >= rows) continue;
+                    if (gr.splits > 1) put_part<kKind>(gr, ti, p.parts[ti.g] + static_cast<long long>(ti.part) * rows * cols, r, n, left, v);
+                    else put_out<T, kKind>(p, ti, r, n, left, v);
+                }
             }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acce[buf]), 0u));
-        buf ^= 1;
+        if (!((kKind == kDown || kKind == kGrad) && p.tall != 0)) buf ^= 1;
         if (buf == 0) phase ^= 1u;
         if constexpr (kKind == kDown || kKind == kGrad) {
             if (gr.splits > 1) {
@@ -733,15 +764,20 @@ int ffn_map(CUtensorMap* map, int type, const void* p, int rows, int inner, int 
                         box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Cycles that a pair takes for a stage of a tile of n accumulator columns, as measured: the stage's bytes from L2, 64 a
-// cycle and CTA, or below that the hand-over between loads and products.
-int stage_cycles(int n) { return std::max(430, (256 + n) * 113 / 100); }
+// Cycles that a pair takes for a stage of a tile of n accumulator columns, as measured: the stage's bytes from L2 (with
+// every SM asking, 46 a cycle and CTA), or the hand-over between loads and products; of a tall tile the products
+// themselves. An operand that lies MN-major comes in boxes of 64 rows for each CTA.
+int stage_cycles(int kind, int n, int tall) {
+    const int rows = 256 * tall + (b_mn(kind) ? (n > 128 ? 256 : 128) : n);
+    return std::max(std::max(430, rows * 7 / 5), tall > 1 ? n * 17 / 4 : 0);
+}
 
 int class_tiles(const Group& g, int rest) {
     return rest != 0 ? (g.rest > 0 ? g.problems * g.splits * g.nm : 0) : g.problems * g.splits * g.nm * g.nfull;
 }
 // Deals the classes' tiles out over `pairs` pairs; returns the cycles of the one with the most.
-long long deal_out(const Group* groups, int count, int per, int pairs, Deal* d) {
+long long deal_out(int kind, const Group* groups, int count, int pairs, Deal* d) {
+    const int per = kind == kGate ? 2 : 1;  // accumulator columns per column
     long long cost[4] = {}, load[kRuns] = {};
     int tiles[4] = {};
     *d = Deal{};
@@ -752,23 +788,28 @@ long long deal_out(const Group* groups, int count, int per, int pairs, Deal* d) 
         if (c >> 1 >= count) continue;
         const Group& g = groups[c >> 1];
         tiles[c] = class_tiles(g, c & 1);
-        // its stages, or where they are few its way out of TMEM (which runs under the next tile's stages)
+        // its stages, or where they are few its way out of TMEM (which runs under the next tile's stages, but for the tall ones)
         const int n = ((c & 1) != 0 ? g.rest : g.wide) * per;
-        cost[c] = std::max(400 + static_cast<long long>(stage_cycles(n)) * ((g.nk + g.splits - 1) / g.splits), 600 + 12LL * n);
+        const long long in = 400 + static_cast<long long>(stage_cycles(kind, n, g.tall)) * ((g.nk + g.splits - 1) / g.splits), out = 600 + 12LL * n;
+        cost[c] = g.tall > 1 ? in + 2 * out : std::max(in, out);
     }
     std::sort(d->order, d->order + 4, [&](int a, int b) { return cost[a] != cost[b] ? cost[a] > cost[b] : a < b; });
     for (int c : d->order) {
         if (tiles[c] == 0) continue;
         const long long k = cost[c];
-        // the highest level that the pairs can be filled to with these tiles
-        long long lo = 0, hi = 0;
-        for (int r = 0; r < d->n; ++r) hi = std::max(hi, load[r]);
-        hi += k * (tiles[c] / pairs + 1) + 1;
+        // the highest level that the pairs can be filled to with these tiles: within two of them of what they all come to
+        long long most = 0, all = k * tiles[c];
+        for (int r = 0; r < d->n; ++r) {
+            most = std::max(most, load[r]);
+            all += load[r] * d->pairs[r];
+        }
+        long long lo = std::max(0LL, all / pairs - 2 * k), hi = std::max(all / pairs, most) + 2 * k;
         const auto filled = [&](long long level) {
             long long n = 0;
             for (int r = 0; r < d->n; ++r) n += level > load[r] ? (level - load[r]) / k * d->pairs[r] : 0;
             return n;
         };
+        if (filled(lo) > tiles[c]) lo = 0;
         while (hi - lo > 1) {
             const long long mid = (lo + hi) / 2;
             (filled(mid) <= tiles[c] ? lo : hi) = mid;
@@ -806,10 +847,10 @@ struct Plan {
     Group group[2];
     Deal deal;
 };
-Group cut_group(int rows, int cols, int problems, int nk, int wide, int splits) {
-    Group g{rows, cols, problems, nk, wide, (cols % wide + 31) / 32 * 32, splits};
-    g.nm = (rows - 1) / (2 * kTile) + 1;
-    g.nfull = cols / wide;
+Group cut_group(const Group& base, int wide, int splits, int tall) {
+    Group g{base.rows, base.cols, base.problems, base.nk, wide, (base.cols % wide + 31) / 32 * 32, splits, tall};
+    g.nm = (g.rows - 1) / (2 * kTile * tall) + 1;
+    g.nfull = g.cols / wide;
     return g;
 }
 size_t parts_bytes(const Group& g) {
@@ -827,29 +868,39 @@ Plan make_plan(int kind, const Group* base, int count) {
     const bool whole = kind == kGate || kind == kBackGate;  // (their epilogues need the whole sums)
     Plan best{};
     long long least = -1;
+    const auto look = [&](int wide, const int (&splits)[2], int tall) {
+        Plan p{};
+        for (int g = 0; g < count; ++g) p.group[g] = cut_group(base[g], wide / per, splits[g], tall);
+        long long t = deal_out(kind, p.group, count, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
+        const int most = std::max(splits[0], count > 1 ? splits[1] : 1);
+        if (most > 1) t += 4000 + (80 + 10LL * most) * wide;
+        if (least >= 0 && t >= least) return false;
+        best = p;
+        least = t;
+        return true;
+    };
+    if (!whole) look(kMaxCols, {1, 1}, 2);
     for (int wide = kMaxCols; wide >= 64; wide -= 64) {
-        const auto cut = [&](int g, int splits) {
-            return cut_group(base[g].rows, base[g].cols, base[g].problems, base[g].nk, wide / per, splits);
-        };
-        const auto most = [&](int g) { return whole ? 1 : std::min(kMaxSplits, std::max(1, base[g].nk / 4)); };
-        for (int s0 = 1; s0 <= most(0); ++s0)
-            for (int s1 = 1; s1 <= (count > 1 ? most(1) : 1); ++s1) {
-                Plan p{};
-                p.group[0] = cut(0, s0);
-                if (count > 1) p.group[1] = cut(1, s1);
-                long long t = deal_out(p.group, count, per, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
-                if (s0 > 1 || s1 > 1) t += 4000 + (80 + 10LL * std::max(s0, s1)) * wide;
-                if (least < 0 || t < least) {
-                    best = p;
-                    least = t;
-                }
-                // with many tiles neither splits nor narrow ones can win
-                if (class_tiles(p.group[0], 0) + (count > 1 ? class_tiles(p.group[1], 0) : 0) >= 4 * kPairs) return best;
+        int splits[2] = {1, 1};
+        look(wide, splits, 1);
+        bool many = true;  // with many tiles neither splits nor narrow ones can win
+        for (int g = count - 1; g >= 0; --g) {  // one group's splits, then the other's beside them
+            const Group cut = cut_group(base[g], wide / per, 1, 1);
+            if (class_tiles(cut, 0) + class_tiles(cut, 1) >= 4 * kPairs) continue;
+            many = false;
+            int own = 1;
+            for (int s : {2, 3, 4, 6, 8}) {
+                if (whole || s > kMaxSplits || s * 4 > base[g].nk) break;
+                splits[g] = s;
+                if (look(wide, splits, 1)) own = s;
             }
+            splits[g] = own;
+        }
+        if (many) break;
     }
     return best;
 }
-// A plan costs up to a hundred microseconds; it depends on the sizes alone, and calls of the same sizes follow one another.
+// A plan costs some tens of microseconds; it depends on the sizes alone, and calls of the same sizes follow one another.
 Plan plan_for(int kind, const vae_gated_ffn_desc& a) {
     struct Known {
         int kind = -1, m, c, f;
@@ -904,8 +955,9 @@ int ffn_launch(const Maps& maps, const Plan& plan, Params& p, bool ahead, cudaSt
     p.group[0] = plan.group[0];
     p.group[1] = plan.group[1];
     p.deal = plan.deal;
+    p.tall = plan.group[0].tall > 1;
     const int count = plan.group[1].problems > 0 ? 2 : 1;
-    if (sm_count() < 2 * kPairs) deal_out(p.group, count, kKind == kGate ? 2 : 1, sm_count() / 2, &p.deal);
+    if (sm_count() < 2 * kPairs) deal_out(kKind, p.group, count, sm_count() / 2, &p.deal);
     int pairs = 0, at = 0;  // up to the last one with work
     for (int r = 0; r < p.deal.n; ++r) {
         at += p.deal.pairs[r];
@@ -1068,7 +1120,7 @@ int ffn_backward(const vae_gated_ffn_desc& a, const void* dy, const void* x, con
     p.wide = a.c % 16 == 0 && on32(dx) && on32(dwg) && on32(dwu);
     if (!weights) {  // dx alone, cut the same way: the same bits
         plan.group[1] = Group{};
-        deal_out(plan.group, 1, 1, kPairs, &plan.deal);
+        deal_out(kGrad, plan.group, 1, kPairs, &plan.deal);
     }
     return ffn_launch<T, kGrad>(maps, plan, p, true, stream);
 }

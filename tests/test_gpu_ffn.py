@@ -62,7 +62,9 @@ CASES = [(1, 8, 8, "bf16", "silu"), (1, 64, 64, "f16", "gelu"), (3, 16, 40, "bf1
          (70000, 8, 24, "f16", "gelu_tanh"),
          # few tokens: one piece of the contraction and many, rows that end inside a block, contractions over a cluster
          (2, 8, 4608, "f16", "gelu"), (16, 1152, 1160, "f16", "gelu"), (32, 2304, 72, "bf16", "gelu_tanh"), (31, 24, 6008, "bf16", "silu"),
-         (9, 328, 40, "f16", "silu"), (33, 2304, 2056, "bf16", "silu")]
+         (9, 328, 40, "f16", "silu"), (33, 2304, 2056, "bf16", "silu"),
+         # tiles of 512 rows, the last ones half and hardly filled; long sums over few tiles beside short ones over many
+         (4100, 576, 2304, "f16", "gelu"), (4353, 640, 2568, "bf16", "silu"), (41001, 72, 136, "bf16", "gelu_tanh")]
 
 
 def _case(case):
