@@ -88,7 +88,7 @@ struct Params {
     Deal deal;
     int half;                  // kGrad: stages of dx's first segment
     void* out[4];              // kGate: hidden, gate, up; kDown: y; kGrad: dx, dWg, dWu, dWd
-    float* parts[2];           // with splits: D of each problem and split, [problems * splits][rows][cols]
+    float* parts[2];           // with splits: the sums of each problem and split (part_at)
     unsigned* arrived[2];      // with splits: how many of them have stored a warp's part of a tile, [tile][CTA of the pair][warp]
     unsigned* clear;           // counters of the kernel behind this one: set to 0 here
     int clear_n;
@@ -446,63 +446,41 @@ __device__ __forceinline__ void put_out(const Params& p, const Tile& ti, int row
         store16(static_cast<uint16_t*>(out) + at, pack16<T>(v), left, p.wide);
     }
 }
-// The same of a split's sums, kept as D is.
-template <int kKind>
-__device__ __forceinline__ void put_part(const Group& gr, const Tile& ti, float* part, int row, int n, int left, const float (&v)[16]) {
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-        if (k >= left) continue;
-        if (kKind == kGrad && ti.z == 3) {
-#pragma unroll
-            for (int q = k; q < k + 4; ++q) part[static_cast<long long>(n + q) * gr.rows + row] = v[q];
-        } else {
-            *reinterpret_cast<float4*>(part + static_cast<long long>(row) * gr.cols + n + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-        }
-    }
-}
-// Adds up the splits' parts, `each` apart, of a warp's 32 rows from row0 on and `mine` columns from n0 on, in their order,
-// and writes D. Four lanes take a row's sixteen columns (a lane a row's: every 16 bytes a request of their own, 35 us
-// instead of 17 for 256 tokens of 512 x 2048); of dWd, which lies transposed, a lane takes a row.
+// Partial sums of splits lie as the epilogue holds them, so that every access is 512 bytes in a row and the lane that adds
+// up has its row as from TMEM: [problem and split][tile of 256 rows][columns to the tile][CTA][warp], each warp's by
+// sixteen columns, [quad of columns][lane][4]. (As D lies: 16 bytes of each row apart, read by one quad of lanes a row,
+// 8 latencies one behind the other for 64 columns.)
 constexpr int kMaxSplits = 8;
-template <int T, int kKind>
-__device__ __forceinline__ void join_parts(const Params& p, const Tile& ti, const float* parts, long long each, int row0, int n0, int mine, int lane) {
-    const Group& gr = p.group[ti.g];
-    if (kKind == kGrad && ti.z == 3) {
-        const int row = row0 + lane;
-        for (int n = n0; n < n0 + mine && n < gr.cols && row < gr.rows; ++n) {
-            const long long at = static_cast<long long>(n) * gr.rows + row;
-            float r[kMaxSplits], v = 0.f;
+__host__ __device__ __forceinline__ int part_cols(const Group& g) { return g.nfull * g.wide + g.rest; }
+__host__ __device__ __forceinline__ long long part_size(const Group& g) { return static_cast<long long>(g.nm) * 2 * kTile * part_cols(g); }
+__device__ __forceinline__ long long part_at(const Group& g, const Tile& ti, int rank, int warp, int lane) {
+    return static_cast<long long>(ti.m0) * part_cols(g) + 2LL * kTile * ti.n0 + (rank * kEpiWarps + warp) * (32 * (ti.n / 2)) + lane * 4;
+}
+__device__ __forceinline__ void put_part(float* part, const float (&v)[16]) {
 #pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s) r[s] = s < gr.splits ? __ldcg(parts + each * s + at) : 0.f;
+    for (int k = 0; k < 16; k += 4) __stcg(reinterpret_cast<float4*>(part + k * 32), make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+}
+// The sum of the splits' parts, in their order; four splits' loads are on their way at once.
+__device__ __forceinline__ void add_parts(const float* part, long long each, int splits, float (&v)[16]) {
 #pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s) v += r[s];
-            if (p.out_f32[1]) static_cast<float*>(p.out[3])[at] = v;
-            else static_cast<typename Elem<T>::type*>(p.out[3])[at] = from_f32<T>(v);
-        }
-        return;
-    }
-    for (int c = (lane & 3) * 4; c < mine; c += 16) {
-#pragma unroll 4
-        for (int i = 0; i < 4; ++i) {
-            const int row = row0 + i * 8 + (lane >> 2), n = n0 + c;
-            if (row >= gr.rows || n >= gr.cols) continue;
-            const long long at = static_cast<long long>(row) * gr.cols + n;
-            float4 r[kMaxSplits], v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 16; ++k) v[k] = 0.f;
+#pragma unroll 1
+    for (int s = 0; s < splits; s += 4) {
+        float4 r[4][4];
 #pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s)
-                r[s] = s < gr.splits ? __ldcg(reinterpret_cast<const float4*>(parts + each * s + at)) : v;
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s) v = make_float4(v.x + r[s].x, v.y + r[s].y, v.z + r[s].z, v.w + r[s].w);
-            if (!p.out_f32[ti.g]) {
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out[ti.z]) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
-                continue;
+            for (int k = 0; k < 4; ++k)
+                r[q][k] = s + q < splits ? __ldcg(reinterpret_cast<const float4*>(part + (s + q) * each + k * 128)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[4 * k] += r[q][k].x;
+                v[4 * k + 1] += r[q][k].y;
+                v[4 * k + 2] += r[q][k].z;
+                v[4 * k + 3] += r[q][k].w;
             }
-            if (kKind == kDown && p.residual != nullptr) {
-                const float4 o = *reinterpret_cast<const float4*>(p.residual + at);
-                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-            }
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out[ti.z]) + at) = v;
-        }
     }
 }
 
@@ -627,7 +605,7 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]) * scale;
                     if (r >= rows) continue;
-                    if (gr.splits > 1) put_part<kKind>(gr, ti, p.parts[ti.g] + static_cast<long long>(ti.part) * rows * cols, r, n, left, v);
+                    if (gr.splits > 1) put_part(p.parts[ti.g] + ti.part * part_size(gr) + part_at(gr, ti, rank, warp, lane) + c * 32, v);
                     else put_out<T, kKind>(p, ti, r, n, left, v);
                 }
             }
@@ -648,8 +626,15 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
                 if (lane == 0) before = atomicAdd(p.arrived[ti.g] + (tile * 2 + rank) * kEpiWarps + warp, 1u);
                 if (__shfl_sync(0xffffffffu, before, 0) + 1u != static_cast<unsigned>(gr.splits)) continue;
                 __threadfence();
-                const long long each = static_cast<long long>(rows) * cols;
-                join_parts<T, kKind>(p, ti, p.parts[ti.g] + each * z * gr.splits, each, row - lane, n0, mine, lane);
+                if (row < rows) {
+                    const float* part = p.parts[ti.g] + z * gr.splits * part_size(gr) + part_at(gr, ti, rank, warp, lane);
+#pragma unroll 1
+                    for (int c = 0; c < mine && n0 + c < cols; c += 16) {
+                        float v[16];
+                        add_parts(part + c * 32, part_size(gr), gr.splits, v);
+                        put_out<T, kKind>(p, ti, row, n0 + c, cols - n0 - c, v);
+                    }
+                }
                 __syncwarp();
             }
         }
@@ -854,15 +839,15 @@ Group cut_group(const Group& base, int wide, int splits, int tall) {
     return g;
 }
 size_t parts_bytes(const Group& g) {
-    return g.splits > 1 ? static_cast<size_t>(g.splits) * g.problems * g.rows * g.cols * sizeof(float) : 0;
+    return g.splits > 1 ? g.splits * g.problems * part_size(g) * sizeof(float) : 0;
 }
 // Counters of a group's splits: for each tile, CTA of the pair and epilogue warp.
 int arrivals(const Group& g) { return g.splits > 1 ? g.problems * g.nm * (g.nfull + (g.rest > 0 ? 1 : 0)) * 2 * kEpiWarps : 0; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // The tile width and the splits with the least time, counted in cycles of the busiest pair. Wide tiles read the least;
 // narrow ones and splits give work to more SMs. Splits cost the last one's way through the f32 sums that all of them
-// write: 4000 cycles, 80 for each column and 10 for each split of it. (A second kernel for that way took 17.5 us instead of 18.0 for 256
-// tokens of 512 x 2048 in a graph, and 2 to 4 us more of the host in a call.) `base`: the groups uncut.
+// write: as measured 4000 cycles and 60 for each column (kDown: 256 tokens of 512 x 2048 19.7 us with four splits, 21.0
+// whole), of the gradients 80 and 10 for each split (one token of 512 x 2048 25.5 us; 28.2 with 60, which splits more).
 Plan make_plan(int kind, const Group* base, int count) {
     const int per = kind == kGate ? 2 : 1;  // accumulator columns per column
     const bool whole = kind == kGate || kind == kBackGate;  // (their epilogues need the whole sums)
@@ -873,7 +858,7 @@ Plan make_plan(int kind, const Group* base, int count) {
         for (int g = 0; g < count; ++g) p.group[g] = cut_group(base[g], wide / per, splits[g], tall);
         long long t = deal_out(kind, p.group, count, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
         const int most = std::max(splits[0], count > 1 ? splits[1] : 1);
-        if (most > 1) t += 4000 + (80 + 10LL * most) * wide;
+        if (most > 1) t += 4000 + (kind == kDown ? 60 : 80 + 10LL * most) * wide;
         if (least >= 0 && t >= least) return false;
         best = p;
         least = t;
