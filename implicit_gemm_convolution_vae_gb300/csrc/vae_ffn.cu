@@ -775,7 +775,9 @@ long long deal_out(int kind, const Group* groups, int count, int pairs, Deal* d)
         tiles[c] = class_tiles(g, c & 1);
         // its stages, or where they are few its way out of TMEM (which runs under the next tile's stages, but for the tall ones)
         const int n = ((c & 1) != 0 ? g.rest : g.wide) * per;
-        const long long in = 400 + static_cast<long long>(stage_cycles(kind, n, g.tall)) * ((g.nk + g.splits - 1) / g.splits), out = 600 + 12LL * n;
+        const long long part = g.splits > 1 ? 22LL * n : 0;  // a split's sums, written and read; beside much other work that hides
+        const long long in = 400 + (kind == kDown ? part : 0) + static_cast<long long>(stage_cycles(kind, n, g.tall)) * ((g.nk + g.splits - 1) / g.splits);
+        const long long out = 600 + part + 12LL * n;
         cost[c] = g.tall > 1 ? in + 2 * out : std::max(in, out);
     }
     std::sort(d->order, d->order + 4, [&](int a, int b) { return cost[a] != cost[b] ? cost[a] > cost[b] : a < b; });
@@ -845,9 +847,11 @@ size_t parts_bytes(const Group& g) {
 int arrivals(const Group& g) { return g.splits > 1 ? g.problems * g.nm * (g.nfull + (g.rest > 0 ? 1 : 0)) * 2 * kEpiWarps : 0; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // The tile width and the splits with the least time, counted in cycles of the busiest pair. Wide tiles read the least;
-// narrow ones and splits give work to more SMs. Splits cost the last one's way through the f32 sums that all of them
-// write: as measured 4000 cycles and 60 for each column (kDown: 256 tokens of 512 x 2048 19.7 us with four splits, 21.0
-// whole), of the gradients 80 and 10 for each split (one token of 512 x 2048 25.5 us; 28.2 with 60, which splits more).
+// narrow ones and splits give work to more SMs. Splits cost, beside each tile's sums, the last one's way through all of
+// them: as measured 4000 cycles and 40 for each column (kDown, with splits and without, bf16: 256 tokens of 512 x 2048
+// 19.7 and 21.0 us, of 1152 x 4608 25.7 and 36.1, 512 of 2048 x 5504 48 and 55; 4096 of 1152 x 4608, whole, 101 and not 109),
+// of the gradients 80 and 10 for each split (one token of 512 x 2048 25.5 us, 28 with fewer, which splits more; the
+// whole one 38).
 Plan make_plan(int kind, const Group* base, int count) {
     const int per = kind == kGate ? 2 : 1;  // accumulator columns per column
     const bool whole = kind == kGate || kind == kBackGate;  // (their epilogues need the whole sums)
@@ -858,7 +862,7 @@ Plan make_plan(int kind, const Group* base, int count) {
         for (int g = 0; g < count; ++g) p.group[g] = cut_group(base[g], wide / per, splits[g], tall);
         long long t = deal_out(kind, p.group, count, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
         const int most = std::max(splits[0], count > 1 ? splits[1] : 1);
-        if (most > 1) t += 4000 + (kind == kDown ? 60 : 80 + 10LL * most) * wide;
+        if (most > 1) t += 4000 + (kind == kDown ? 40 : 80 + 10LL * most) * wide;
         if (least >= 0 && t >= least) return false;
         best = p;
         least = t;
