@@ -11,7 +11,19 @@
 // inner one (Wd and Wg, Wu backward, all operands of the weights' gradients) is read
 // as it lies in memory, MN-major: nothing is transposed. The tile of the first product
 // holds 128 gate and 128 up columns of the same hidden channels (the even CTA loads
-// rows of Wg, the odd one of Wu), so act(gate) o up never leaves the registers.
+// rows of Wg, the odd one of Wu), so act(gate) o up never leaves the registers. The
+// three weights' gradients and dx are one launch, whose tiles are dealt out by what
+// they cost; rows of two tiles share one B where both accumulators can take them (512
+// rows, "tall"); few tiles become narrow ones, or splits of the contraction, whose last
+// one to finish adds them up.
+//
+// What bounds the products is the way from L2 to shared memory, 46 bytes a cycle and
+// CTA when every SM asks: a 256 x 256 x 64 stage (32 KB a CTA) takes 700 cycles of it and 512 of
+// the tensor cores. Tall tiles read a quarter less. 16384 tokens of 1152 x 4608, bf16,
+// in a graph: 312 us forward (1670 TFLOP/s), the gradient 675 to 720 on different machines
+// (1450 to 1545). Of the gradient's first kernel (174 us) the products alone take 91, its stages' way 124,
+// gate, up, dgate and dup 113. Small calls are chains of latencies: 256 tokens of 512 x
+// 2048 take 19.6 us, 8 of them in the first kernel.
 #include <algorithm>
 #include <mutex>
 

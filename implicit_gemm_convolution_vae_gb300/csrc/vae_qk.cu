@@ -23,6 +23,7 @@ constexpr int kQkTokens = 8;     // tokens a block takes at a time, at most (a p
 constexpr int kQkThreads = 128;
 constexpr int kQkWarps = kQkThreads / 32;
 constexpr int kQkBlocks = 608;   // of the gradient, at most: each leaves a row of partial sums for dgamma
+constexpr int kQkForward = 760;  // blocks of the forward, at most: five an SM
 constexpr int kQkPitch = VAE_ROPE_MAX_PAIRS + 2;
 
 struct QkPart {  // queries or keys
@@ -38,7 +39,7 @@ struct QkParams {
     const void* pos;
     int tokens, s, d, tpb;
     int pos_int, pos_batch;
-    int qblocks;  // the gradient's blocks of queries; the others are the keys'
+    int qblocks;  // in vectors: blocks of queries; the others are the keys'
     float eps;
     float* sums;  // a row of d for each block (in the plain form two, the queries' first): its part of dgamma
 };
@@ -164,7 +165,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_plain_kernel(const QkParams p, 
 //   kHalves: pairs (c, c + R/2) with R a multiple of 16: a lane holds a unit of each half;
 //   kSwap: other halves: units u and u + n, the partners come through shared memory.
 // Neighbouring lanes take neighbouring units, so that every access covers whole sectors
-// (two neighbouring units a lane: 137 us instead of 127 for 36864 tokens of 36 heads of 128).
+// (two neighbouring units a lane: 137 us instead of 127 for 36864 tokens of 36 heads of 128, when a
+// block took eight tokens and its threads the next rows in registers).
 // The tokens of a block are a power of two, so a group of G lanes stays with one token: its
 // angles lie in registers, and the rows that it meets, every few heads, are a fixed step
 // apart. (Rows dealt out over tokens and heads in turn, angles read from shared memory for each:
@@ -255,6 +257,11 @@ struct QkLane {
     }
     __device__ __forceinline__ float sum(float x) const {
         for (int o = group >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    }
+    __device__ __forceinline__ float2 sum2(float2 x) const {
+        for (int o = group >> 1; o > 0; o >>= 1)
+            x = add2(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
         return x;
     }
 };
@@ -353,95 +360,30 @@ __device__ __forceinline__ float qk_square(const float2 (&v)[8]) {
     return s.x + s.y;
 }
 
-// Forward: a block takes p.tpb tokens, its threads the next kDeep rows' units into registers.
-template <int T, int kForm>
-__global__ void __launch_bounds__(kQkThreads, 6) qk_vector_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
-    using E = typename Elem<T>::type;
-    using Unit = QkUnit<T>;
-    constexpr int kDeep = T == VAE_F32 ? 1 : 2;
-    __shared__ __align__(16) QkAngles cs[kQkTokens];
-    __shared__ float swap[kForm == kSwap ? kQkThreads * 16 : 1];
-    const QkLane<kForm> l(p, plan.pairs, glog2);
-    const float inv_d = 1.f / static_cast<float>(p.d);
-    pdl_wait();
-    const int t0 = static_cast<int>(blockIdx.x) * p.tpb;
-    const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
-    const bool here = l.token < nt;
-    const int e = (t0 + l.token) / p.s, si = t0 + l.token - e * p.s;
-    const QkAngles& angles = cs[here ? l.token : 0];
-    QkTurn<kForm> turned;
-#pragma unroll 1
-    for (int w = 0; w < 2; ++w) {
-        const QkPart& part = p.part[w];
-        const E* x = static_cast<const E*>(part.x) + e * part.xs[0] + si * part.xs[1] + l.first * part.xs[2];
-        E* y = static_cast<E*>(part.y) + e * part.ys[0] + si * part.ys[1] + l.first * part.ys[2];
-        const long long xstep = l.step * part.xs[2], ystep = l.step * part.ys[2];
-        const int rows = here && l.first < part.h ? (part.h - l.first + l.step - 1) / l.step : 0;
-        const int most = (part.h + l.step - 1) / l.step;  // (of any group: the warp stays together)
-        Unit xa[kDeep + 1], xb[kDeep + 1];
-        auto load = [&](int k, int row) {
-            xa[k].clear();
-            xb[k].clear();
-            if (row < rows) {
-                if (l.has_a) xa[k].load(x + l.ca);
-                if (l.has_b) xb[k].load(x + l.cb);
-                x += xstep;
-            }
-        };
-#pragma unroll
-        for (int k = 0; k < kDeep; ++k) load(k, k);
-        float2 gamma[8];
-        qk_gamma(gamma, part.gamma, l.ca, l.has_a, l.cb, l.has_b);
-        if (w == 0) {  // the first rows are on their way
-            qk_angles<false>(cs, p, plan, t0, nt);
-            __syncthreads();
-            turned.take(angles, l);
-        }
-        for (int r0 = 0; r0 < most; r0 += kDeep + 1) {
-#pragma unroll
-            for (int k = 0; k <= kDeep; ++k) {
-                const int row = r0 + k;
-                load((k + kDeep) % (kDeep + 1), row + kDeep);
-                if (row >= most) break;
-                float2 v[8];
-                xa[k].get(v);
-                xb[k].get(v + 4);
-                const float rs = rsqrtf(l.sum(qk_square(v)) * inv_d + p.eps);
-                const float2 rs2 = make_float2(rs, rs);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], rs2), gamma[i]);
-                turned.apply(v, angles, l, plan.pairs, swap);
-                if (row < rows) {
-                    if (l.has_a) Unit::put(y + l.ca, v);
-                    if (l.has_b) Unit::put(y + l.cb, v + 4);
-                    y += ystep;
-                }
-            }
-        }
-    }
-    pdl_launch_dependents();
-}
-
-// The gradient: blocks stay for many tokens, each with the queries or the keys, so that a thread sums its channels of
-// one dgamma. A thread has the next kDeep rows' units on their way into shared memory, which nobody else reads, over the
-// ends of its tokens (rows ahead in registers: 184 us for 36864 tokens of 24 heads, 142 so).
-template <int T>
+// Blocks stay for many tokens, each with the queries or the keys, so that a thread keeps its channels of one gamma and, in
+// the gradient, sums those of one dgamma. A thread has the next kDeep rows' units on their way into shared memory, which
+// nobody else reads, over the ends of its tokens: 36864 tokens of 36 heads 107 us (6.4 TB/s), the gradient of 24 heads 142
+// (4.8 TB/s; half of the issue slots, and each row a chain of two sums over its lanes). With rows ahead in registers 127
+// and 184. Forward with 4, 5, 6, 7 blocks an SM 110, 107, 116, 113 us, with eight, whose registers spill, 118; gradient with five 149.
+template <int T, bool kBack>
 struct QkRing {
-    static constexpr int kDeep = 2;
-    static constexpr int kVecs = 4 * QkUnit<T>::kVecs;  // of a row and thread
+    static constexpr int kDeep = kBack || T == VAE_F32 ? 2 : 3;
+    static constexpr int kVecs = (kBack ? 4 : 2) * QkUnit<T>::kVecs;  // of a row and thread
     static constexpr int kBytes = kDeep * kVecs * kQkThreads * 16;
-    // tokens a turn: each costs two barriers and the angles' latency (4: 193 us, 8: 151, 16: 142)
-    static constexpr int kTokens = T == VAE_F32 ? kQkTokens : 2 * kQkTokens;
+    // tokens a turn: each costs two barriers and the angles' latency (gradient, 4: 193 us, 8: 151, 16: 142)
+    static constexpr int kTokens = kBack && T != VAE_F32 ? 2 * kQkTokens : kQkTokens;
+    static constexpr int kResident = kBack ? 4 : 5;  // blocks an SM
     static_assert(kBytes + kTokens * sizeof(QkAngles) + kQkThreads * 64 <= 48 * 1024, "more shared memory than a kernel has without asking");
-    static_assert(kBytes >= kQkWarps * kQkMaxD * 4, "the ring takes a row of sums for each warp at the end");
+    static_assert(!kBack || kBytes >= kQkWarps * kQkMaxD * 4, "the ring takes a row of sums for each warp at the end");
 };
 
-template <int T, int kForm>
-__global__ void __launch_bounds__(kQkThreads, 4) qk_vector_backward_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
+template <int T, int kForm, bool kBack>
+__global__ void __launch_bounds__(kQkThreads, QkRing<T, kBack>::kResident)
+    qk_vector_kernel(const QkParams p, const __grid_constant__ vae_rope_plan plan, const int glog2) {
     using E = typename Elem<T>::type;
     using Unit = QkUnit<T>;
-    using Ring = QkRing<T>;
-    constexpr int kDeep = Ring::kDeep, kVecs = Ring::kVecs;
+    using Ring = QkRing<T, kBack>;
+    constexpr int kDeep = Ring::kDeep, kVecs = Ring::kVecs, kUnits = kBack ? 4 : 2;
     extern __shared__ __align__(16) uint4 ring[];  // [kDeep][kVecs][threads]
     __shared__ __align__(16) QkAngles cs[Ring::kTokens];
     __shared__ float swap[kForm == kSwap ? kQkThreads * 16 : 1];
@@ -466,7 +408,7 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_vector_backward_kernel(const
         if (!more) return;
         const int e = (nt0 + l.token) / p.s, si = nt0 + l.token - e * p.s;
         x = static_cast<const E*>(part.x) + e * part.xs[0] + si * part.xs[1] + l.first * part.xs[2];
-        g = static_cast<const E*>(part.dy) + e * part.gs[0] + si * part.gs[1] + l.first * part.gs[2];
+        if constexpr (kBack) g = static_cast<const E*>(part.dy) + e * part.gs[0] + si * part.gs[1] + l.first * part.gs[2];
     };
     auto fetch = [&](int slot) {
         constexpr int kUnit = Unit::kVecs * kQkThreads;
@@ -474,12 +416,14 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_vector_backward_kernel(const
         const bool in = more && nrow < heads, a = in && l.has_a, b = in && l.has_b;
         Unit::fetch(at, x + (a ? l.ca : 0), a);
         Unit::fetch(at + kUnit, x + (b ? l.cb : 0), b);
-        Unit::fetch(at + 2 * kUnit, g + (a ? l.ca : 0), a);
-        Unit::fetch(at + 3 * kUnit, g + (b ? l.cb : 0), b);
+        if constexpr (kBack) {
+            Unit::fetch(at + 2 * kUnit, g + (a ? l.ca : 0), a);
+            Unit::fetch(at + 3 * kUnit, g + (b ? l.cb : 0), b);
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (in) {
             x += l.step * part.xs[2];
-            g += l.step * part.gs[2];
+            if constexpr (kBack) g += l.step * part.gs[2];
         }
         if (++nrow == most && nt0 < p.tokens) {
             nt0 = p.tokens - nt0 > stride ? nt0 + stride : p.tokens;
@@ -489,14 +433,14 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_vector_backward_kernel(const
     open();
 #pragma unroll 1
     for (int k = 0; k < kDeep; ++k) fetch(k);
-    float2 gamma[8], acc[8] = {};
+    float2 gamma[8], acc[kBack ? 8 : 1] = {};
     qk_gamma(gamma, part.gamma, l.ca, l.has_a, l.cb, l.has_b);
     int slot = 0;
     for (int t0 = t00; t0 < p.tokens; t0 = p.tokens - t0 > stride ? t0 + stride : p.tokens) {
         const int nt = p.tokens - t0 < p.tpb ? p.tokens - t0 : p.tpb;
         const bool here = l.token < nt;
         __syncthreads();  // (the last tokens' angles have been read)
-        qk_angles<true>(cs, p, plan, t0, nt);
+        qk_angles<kBack>(cs, p, plan, t0, nt);
         __syncthreads();
         const QkAngles& angles = cs[here ? l.token : 0];
         QkTurn<kForm> turned;
@@ -508,31 +452,40 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_vector_backward_kernel(const
         for (int row = 0; row < most; ++row) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");  // (this thread's own copies: no barrier)
             const uint4* at = ring + slot * kVecs * kQkThreads + threadIdx.x;
-            Unit r[4];
+            Unit r[kUnits];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i].take(at + i * Unit::kVecs * kQkThreads);
+            for (int i = 0; i < kUnits; ++i) r[i].take(at + i * Unit::kVecs * kQkThreads);
             float2 v[8], q[8];
             r[0].get(v);
             r[1].get(v + 4);
-            r[2].get(q);
-            r[3].get(q + 4);
+            if constexpr (kBack) {
+                r[2].get(q);
+                r[3].get(q + 4);
+            }
             fetch(slot);
             if (++slot == kDeep) slot = 0;
-            const float rs = rsqrtf(l.sum(qk_square(v)) * inv_d + p.eps);
-            const float2 rs2 = make_float2(rs, rs);
-            float2 along = make_float2(0.f, 0.f);
-            turned.apply(q, angles, l, plan.pairs, swap);
+            if constexpr (kBack) {
+                // the two sums side by side: of x x and of v x, before r is known
+                turned.apply(q, angles, l, plan.pairs, swap);
+                float2 along = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = mul2(v[i], rs2);
-                acc[i] = fma2(q[i], v[i], acc[i]);
-                q[i] = mul2(q[i], gamma[i]);
-                along = fma2(q[i], v[i], along);
+                for (int i = 0; i < 8; ++i) along = fma2(mul2(q[i], gamma[i]), v[i], along);
+                const float2 sums = l.sum2(make_float2(qk_square(v), along.x + along.y));
+                const float rs = rsqrtf(sums.x * inv_d + p.eps), m = -(sums.y * rs) * inv_d;
+                const float2 rs2 = make_float2(rs, rs), m2 = make_float2(m, m);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = mul2(v[i], rs2);
+                    acc[i] = fma2(q[i], v[i], acc[i]);
+                    q[i] = mul2(fma2(v[i], m2, mul2(q[i], gamma[i])), rs2);
+                }
+            } else {
+                const float rs = rsqrtf(l.sum(qk_square(v)) * inv_d + p.eps);
+                const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = mul2(mul2(v[i], rs2), gamma[i]);
+                turned.apply(q, angles, l, plan.pairs, swap);
             }
-            const float m = -l.sum(along.x + along.y) * inv_d;
-            const float2 m2 = make_float2(m, m);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = mul2(fma2(v[i], m2, q[i]), rs2);
             if (row < rows) {
                 if (l.has_a) Unit::put(y + l.ca, q);
                 if (l.has_b) Unit::put(y + l.cb, q + 4);
@@ -541,20 +494,22 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_vector_backward_kernel(const
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (p.sums != nullptr) {
-        float* sums = reinterpret_cast<float*>(ring);  // [warps][kQkMaxD]
-        __syncthreads();
+    if constexpr (kBack) {
+        if (p.sums != nullptr) {
+            float* sums = reinterpret_cast<float*>(ring);  // [warps][kQkMaxD]
+            __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            float s = (k & 1) != 0 ? acc[k >> 1].y : acc[k >> 1].x;
-            for (int o = l.group; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane < l.group && (k < 8 ? l.has_a : l.has_b)) sums[warp * kQkMaxD + (k < 8 ? l.ca + k : l.cb + k - 8)] = s;
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
-            float s = 0.f;
-            for (int k = 0; k < kQkWarps; ++k) s += sums[k * kQkMaxD + c];
-            p.sums[static_cast<long long>(blockIdx.x) * p.d + c] = s;
+            for (int k = 0; k < 16; ++k) {
+                float s = (k & 1) != 0 ? acc[k >> 1].y : acc[k >> 1].x;
+                for (int o = l.group; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane < l.group && (k < 8 ? l.has_a : l.has_b)) sums[warp * kQkMaxD + (k < 8 ? l.ca + k : l.cb + k - 8)] = s;
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.d; c += kQkThreads) {
+                float s = 0.f;
+                for (int k = 0; k < kQkWarps; ++k) s += sums[k * kQkMaxD + c];
+                p.sums[static_cast<long long>(blockIdx.x) * p.d + c] = s;
+            }
         }
     }
     pdl_launch_dependents();
@@ -604,14 +559,9 @@ template <int T, bool kBack>
 cudaError_t qk_launch_type(unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
     if (!qk_vectors(p)) return launch_kernel(qk_plain_kernel<T, kBack>, dim3(grid), dim3(kQkThreads), 0, s, p, plan);
     const auto [form, glog2] = qk_form(p.d, plan);
-    const auto go = [&, lanes = glog2](auto k) { return launch_kernel(k, dim3(grid), dim3(kQkThreads), kBack ? QkRing<T>::kBytes : 0, s, p, plan, lanes); };
-    if constexpr (kBack) {
-        if (form == kLocal) return go(qk_vector_backward_kernel<T, kLocal>);
-        return form == kHalves ? go(qk_vector_backward_kernel<T, kHalves>) : go(qk_vector_backward_kernel<T, kSwap>);
-    } else {
-        if (form == kLocal) return go(qk_vector_kernel<T, kLocal>);
-        return form == kHalves ? go(qk_vector_kernel<T, kHalves>) : go(qk_vector_kernel<T, kSwap>);
-    }
+    const auto go = [&, lanes = glog2](auto k) { return launch_kernel(k, dim3(grid), dim3(kQkThreads), QkRing<T, kBack>::kBytes, s, p, plan, lanes); };
+    if (form == kLocal) return go(qk_vector_kernel<T, kLocal, kBack>);
+    return form == kHalves ? go(qk_vector_kernel<T, kHalves, kBack>) : go(qk_vector_kernel<T, kSwap, kBack>);
 }
 template <bool kBack>
 cudaError_t qk_launch(int type, unsigned grid, cudaStream_t s, const QkParams& p, const vae_rope_plan& plan) {
@@ -702,6 +652,14 @@ int qk_tiles(const vae_qk_norm_rope_desc* a, int* tpb) {
     return (tokens - 1) / *tpb + 1;
 }
 
+// In vectors the queries and the keys have blocks of their own, as many as their share of the heads, `most` in all.
+int qk_share(const vae_qk_norm_rope_desc& a, int tiles, int most, int* qblocks) {
+    const int all = static_cast<int>(std::min<long long>(2LL * tiles, most));
+    const int q = static_cast<int>((static_cast<long long>(all) * a.hq + (a.hq + a.hk) / 2) / (a.hq + a.hk));
+    *qblocks = std::min(std::max(q, 1), std::min(all - 1, tiles));
+    return *qblocks + std::min(all - *qblocks, tiles);
+}
+
 void qk_fill(const vae_qk_norm_rope_desc* a, QkParams* p, const void* q, const void* k, const void* gq, const void* gk, void* yq,
              void* yk, const float* gamma_q, const float* gamma_k, const void* pos) {
     const int dim[2][3] = {{a->b, a->s, a->hq}, {a->b, a->s, a->hk}};
@@ -770,11 +728,12 @@ int vae_qk_norm_rope(const vae_qk_norm_rope_desc* desc, const void* q_dev, const
     if (rc != VAE_OK) return rc;
     QkParams p{};
     qk_fill(desc, &p, q_dev, k_dev, nullptr, nullptr, q_out_dev, k_out_dev, gamma_q_dev, gamma_k_dev, pos_dev);
-    const unsigned grid = static_cast<unsigned>(qk_tiles(desc, &p.tpb));
+    int grid = qk_tiles(desc, &p.tpb);
     const vae_rope_plan none{};
     const vae_rope_plan& pl = plan != nullptr ? *plan : none;
+    if (qk_vectors(p)) grid = qk_share(a, grid, kQkForward, &p.qblocks);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    VAE_CUDA_CHECK(qk_launch<false>(a.type, grid, st, p, pl));
+    VAE_CUDA_CHECK(qk_launch<false>(a.type, static_cast<unsigned>(grid), st, p, pl));
     return VAE_OK;
 }
 
@@ -833,7 +792,6 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
     QkParams p{};
     qk_fill(desc, &p, q_dev, k_dev, dq_out_dev, dk_out_dev, dq_dev, dk_dev, gamma_q_dev, gamma_k_dev, pos_dev);
     int tiles = qk_tiles(desc, &p.tpb);
-    // In vectors the queries and the keys have blocks of their own, as many as their share of the heads.
     int grid = std::min(tiles, kQkBlocks), qblocks = grid, kend = 2 * grid;
     const vae_rope_plan none{};
     const vae_rope_plan& pl = plan != nullptr ? *plan : none;
@@ -842,10 +800,7 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
             p.tpb = 2 * kQkTokens;
             tiles = (p.tokens - 1) / p.tpb + 1;
         }
-        const int all = static_cast<int>(std::min<long long>(2LL * tiles, kQkBlocks));
-        qblocks = static_cast<int>((static_cast<long long>(all) * a.hq + (a.hq + a.hk) / 2) / (a.hq + a.hk));
-        qblocks = std::min(std::max(qblocks, 1), std::min(all - 1, tiles));
-        grid = kend = qblocks + std::min(all - qblocks, tiles);
+        grid = kend = qk_share(a, tiles, kQkBlocks, &qblocks);
     }
     p.qblocks = qblocks;
     p.sums = weights ? static_cast<float*>(workspace_dev) : nullptr;
