@@ -1136,9 +1136,9 @@ extern "C" {
 size_t vae_gated_ffn_workspace_bytes(const vae_gated_ffn_desc* desc) {
     clear_error();
     if (ffn_check(desc, false) != VAE_OK) return 0;
-    // hidden, where it is not saved; partial sums and their counters
+    // hidden, where it is not saved; of few tokens what its rounding left, else partial sums and their counters
     const size_t hidden = desc->save ? 0 : up256(mf_bytes(*desc));
-    if (desc->m <= kFewTokens) return hidden;
+    if (desc->m <= kFewTokens) return hidden + mf_bytes(*desc);
     const Group g = plan_for(kDown, *desc).group[0];
     return hidden + up256(arrivals(g) * sizeof(unsigned)) + parts_bytes(g);
 }
@@ -1173,9 +1173,9 @@ int vae_gated_ffn(const vae_gated_ffn_desc* desc, const void* x_dev, const void*
     VAE_TRY(check_device());
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* hidden = save ? hidden_dev : workspace_dev;
-    if (a.m <= kFewTokens)
-        return ffn_few(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, st);
     char* ws = static_cast<char*>(workspace_dev) + (save ? 0 : up256(mf_bytes(a)));
+    if (a.m <= kFewTokens)
+        return ffn_few(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, ws, st);
     return a.type == VAE_F16
                ? ffn_forward<VAE_F16>(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, ws, st)
                : ffn_forward<VAE_BF16>(a, x_dev, w_gate_dev, w_up_dev, w_down_dev, residual_dev, y_dev, gate_dev, up_dev, hidden, ws, st);

@@ -15,6 +15,10 @@
 // warps' sums join in shared memory, the blocks' in the first one's, in order. The second
 // product's blocks are launched while the first's run and have their first weights on
 // their way before they wait for hidden.
+//
+// hidden goes on as two values of the type, the rounded one and what the rounding left
+// (in f16 times 2^11, which keeps it off the subnormal numbers): the second product takes both with the
+// weights that it has anyway, and y carries its own rounding alone.
 #include <algorithm>
 
 #include "vae_ffn.cuh"
@@ -35,6 +39,7 @@ struct FewParams {
     const void* x;           // [m][k]
     int m, rows, k;
     void* out;               // [m][rows]
+    void* rest;              // gated: [m][rows], what the rounding of `out` left; else that of x
     void *gate, *up;         // or NULL
     int out_f32;
     const float* residual;
@@ -60,10 +65,13 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
     return v;
 }
 
+template <int T>
+constexpr float kRest = T == VAE_F16 ? 2048.f : 1.f;
+
 // kN: tokens in eights; kWarps: 8 (two blocks an SM) or 16 (one).
 template <int T, bool kGated, int kN, int kAct, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_kernel(const FewParams p) {
-    constexpr int kMats = kGated ? 2 : 1, kAhead = ahead(kN);
+    constexpr int kMats = kGated ? 2 : 1, kAhead = ahead(kN);  // matrices
     constexpr int kOut = kMats * kN * 8 * kRows;  // sums of a block: [matrix][token][row]
     __shared__ float sums[kSums][kOut];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -104,31 +112,39 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_kernel(c
         if (to > from) prefetch_l2_bulk(static_cast<const char*>(p.next) + from, static_cast<uint32_t>(to - from < most ? to - from : most));
     }
 
-    float d[kMats][kN][4] = {};
-    const uint16_t* x = static_cast<const uint16_t*>(p.x);
+    float d[2][kN][4] = {};  // of gate and up, or of hidden and its rest
+    const uint16_t *x = static_cast<const uint16_t*>(p.x), *y = static_cast<const uint16_t*>(p.rest);
     for (int piece = first; piece < last; piece += kAhead * kWarps) {
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) {
             const int k = (piece + s * kWarps) * 32 + t * 8;
-            uint4 b[kN];
+            uint4 b[kN], c[kGated ? 1 : kN];
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
                 const int token = n * 8 + g;
-                b[n] = token < p.m && k < p.k && piece + s * kWarps < last
-                           ? *reinterpret_cast<const uint4*>(x + static_cast<long long>(token) * p.k + k)
-                           : make_uint4(0u, 0u, 0u, 0u);
+                const bool in = token < p.m && k < p.k && piece + s * kWarps < last;
+                const long long at = static_cast<long long>(token) * p.k + k;
+                b[n] = in ? *reinterpret_cast<const uint4*>(x + at) : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (!kGated) c[n] = in ? *reinterpret_cast<const uint4*>(y + at) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
-            for (int i = 0; i < kMats; ++i) {
-                const uint4 u = a[s][i][0], v = a[s][i][1];
+            for (int i = 0; i < 2; ++i) {
+                const uint4 u = a[s][i % kMats][0], v = a[s][i % kMats][1];
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
-                    mma16816<T>(d[i][n], u.x, v.x, u.y, v.y, b[n].x, b[n].y);
-                    mma16816<T>(d[i][n], u.z, v.z, u.w, v.w, b[n].z, b[n].w);
+                    const uint4 e = kGated || i == 0 ? b[n] : c[kGated ? 0 : n];
+                    mma16816<T>(d[i][n], u.x, v.x, u.y, v.y, e.x, e.y);
+                    mma16816<T>(d[i][n], u.z, v.z, u.w, v.w, e.z, e.w);
                 }
             }
             fetch(s, piece + (s + kAhead) * kWarps);
         }
+    }
+    if constexpr (!kGated) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[0][n][e] = fmaf(d[1][n][e], 1.f / kRest<T>, d[0][n][e]);
     }
     // d: rows g, g + 8; tokens 2 t, 2 t + 1. Sixteen warps: the upper ones' first, which the lower ones add to theirs.
     auto each = [&](auto f) {
@@ -172,7 +188,11 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_kernel(c
             const long long at = static_cast<long long>(token) * p.rows + row;
             using E = typename Elem<T>::type;
             if constexpr (kGated) {
-                static_cast<E*>(p.out)[at] = from_f32<T>(act_value<kAct>(v[0]) * v[1]);
+                const float h = act_value<kAct>(v[0]) * v[1];
+                const E near = from_f32<T>(h);
+                const float rest = (h - to_f32<T>(near)) * kRest<T>;
+                static_cast<E*>(p.out)[at] = near;
+                static_cast<E*>(p.rest)[at] = from_f32<T>(rest - rest == 0.f ? rest : 0.f);  // (of what is not finite: 0)
                 if (p.gate != nullptr) {
                     static_cast<E*>(p.gate)[at] = from_f32<T>(v[0]);
                     static_cast<E*>(p.up)[at] = from_f32<T>(v[1]);
@@ -227,7 +247,7 @@ int launch_tokens(const FewParams& p, cudaStream_t stream) {
 
 template <int T>
 int few_type(const vae_gated_ffn_desc& a, const void* x, const void* wg, const void* wu, const void* wd, const float* residual, void* y,
-             void* gate, void* up, void* hidden, cudaStream_t stream) {
+             void* gate, void* up, void* hidden, void* rest, cudaStream_t stream) {
     FewParams p{};
     p.w0 = wg;
     p.w1 = wu;
@@ -236,6 +256,7 @@ int few_type(const vae_gated_ffn_desc& a, const void* x, const void* wg, const v
     p.rows = a.f;
     p.k = a.c;
     p.out = hidden;
+    p.rest = rest;
     p.gate = gate;
     p.up = up;
     p.next = wd;
@@ -247,6 +268,7 @@ int few_type(const vae_gated_ffn_desc& a, const void* x, const void* wg, const v
     p = FewParams{};
     p.w0 = wd;
     p.x = hidden;
+    p.rest = rest;
     p.m = a.m;
     p.rows = a.c;
     p.k = a.f;
@@ -259,9 +281,9 @@ int few_type(const vae_gated_ffn_desc& a, const void* x, const void* wg, const v
 }  // namespace
 
 int ffn_few(const vae_gated_ffn_desc& a, const void* x, const void* wg, const void* wu, const void* wd, const float* residual, void* y,
-            void* gate, void* up, void* hidden, cudaStream_t stream) {
-    return a.type == VAE_F16 ? few_type<VAE_F16>(a, x, wg, wu, wd, residual, y, gate, up, hidden, stream)
-                             : few_type<VAE_BF16>(a, x, wg, wu, wd, residual, y, gate, up, hidden, stream);
+            void* gate, void* up, void* hidden, void* rest, cudaStream_t stream) {
+    return a.type == VAE_F16 ? few_type<VAE_F16>(a, x, wg, wu, wd, residual, y, gate, up, hidden, rest, stream)
+                             : few_type<VAE_BF16>(a, x, wg, wu, wd, residual, y, gate, up, hidden, rest, stream);
 }
 
 }  // namespace vae

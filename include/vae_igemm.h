@@ -485,7 +485,8 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
  *   VAE_ACT_GELU_TANH g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).
  * Products are summed in f32; hidden is formed from the f32 gate and up and
  * rounded to `type` once for its product, which costs y 1.4 times its own
- * rounding (in f16 |hidden| over 65504 is infinite).
+ * rounding; of up to 32 tokens the product takes what that rounding left as
+ * well (in f16 |hidden| over 65504 is infinite).
  * vae_gated_ffn_backward, from the saved gate, up and hidden:
  *   dhidden = dy w_down, dup = dhidden * act(gate), dgate = dhidden * up * act'(gate),
  *   dx = dgate w_gate + dup w_up, dw_gate = dgate^T x, dw_up = dup^T x,

@@ -117,6 +117,32 @@ def test_gated_ffn(case):
     _check_forward(case, x64, wg64, wu64, wd64, r, None, "f32", r64)
 
 
+@pytest.mark.parametrize("case", [c for c in CASES if c[0] <= 32])
+def test_few_tokens_keep_what_the_rounding_of_hidden_left(case):
+    """Up to 32 tokens the second product takes hidden in two parts. The second part is rounded too: U^2 of hidden, in f16
+    (where it is held times 2^11) at least 2^-36. Both parts' sums are joined by one more rounding each."""
+    torch = torch_mod()
+    m, c, f, t, act = case
+    (x, x64), (wg, wg64), (wu, wu64), (wd, wd64) = _case(case)
+    ref, gate, up, hidden = ot.gated_ffn(x64, wg64, wu64, wd64, act)
+    _, _, eh, _ = _forward_bounds(case, x64, wg64, wu64, wd64, gate, up, hidden)
+    a = np.abs
+    e = (eh + U[t] ** 2 * (a(hidden) + eh) + FLOOR[t] / 2048) @ a(wd64).T + SUM(f) * ((1 + 2 * U[t]) * (a(hidden) + eh) @ a(wd64).T)
+    _within(vg.gated_ffn(x, wg, wu, wd, activation=act, out_dtype=torch.float32), ref, e + 2.0 ** -22 * (a(ref) + e))
+    y, _ = vg.gated_ffn(x, wg, wu, wd, activation=act, save=True)
+    assert torch.equal(y, vg.gated_ffn(x, wg, wu, wd, activation=act))
+    _within(y, ref, e + U[t] * (a(ref) + e) + FLOOR[t] + 2.0 ** -22 * a(ref))
+
+
+def test_few_tokens_whose_hidden_passes_f16():
+    torch = torch_mod()
+    x = torch.ones(2, 8, dtype=torch.float16, device="cuda")
+    wg, wu = torch.full((16, 8), 64.0, dtype=torch.float16, device="cuda"), torch.full((16, 8), 64.0, dtype=torch.float16, device="cuda")
+    wd = torch.full((8, 16), 2.0 ** -10, dtype=torch.float16, device="cuda")
+    y, saved = vg.gated_ffn(x, wg, wu, wd, save=True, out_dtype=torch.float32)
+    assert torch.isinf(saved[2]).all() and torch.isinf(y).all()  # 512 * 512 is no f16: infinite, and no NaN from its rest
+
+
 def _check_backward(case, dy, x, wg, wu, wd, gate, up, hidden, got, w_type):
     m, c, f, t, act = case
     dx, dwg, dwu, dwd, dgate, dup = ot.gated_ffn_backward(dy, x, wg, wu, wd, gate, up, hidden, act)
