@@ -362,15 +362,16 @@ __device__ __forceinline__ float qk_square(const float2 (&v)[8]) {
 
 // Blocks stay for many tokens, each with the queries or the keys, so that a thread keeps its channels of one gamma and, in
 // the gradient, sums those of one dgamma. A thread has the next kDeep rows' units on their way into shared memory, which
-// nobody else reads, over the ends of its tokens: 36864 tokens of 36 heads 107 us (6.4 TB/s), the gradient of 24 heads 142
-// (4.8 TB/s; half of the issue slots, and each row a chain of two sums over its lanes). With rows ahead in registers 127
-// and 184. Forward with 4, 5, 6, 7 blocks an SM 110, 107, 116, 113 us, with eight, whose registers spill, 118; gradient with five 149.
+// nobody else reads, over the ends of its tokens: 36864 tokens of 36 heads 107 us (6.4 TB/s), the gradient of 24 heads 122
+// (5.6 TB/s; each row a chain of sums over its lanes, and registers for four blocks an SM). With rows ahead in registers 127
+// and 184. Forward with 4, 5, 6, 7 blocks an SM 110, 107, 116, 113 us, with eight, whose registers spill, 118; gradient, when
+// it took 142 with four (queries and keys shared out by heads alone), with five 149.
 template <int T, bool kBack>
 struct QkRing {
     static constexpr int kDeep = kBack || T == VAE_F32 ? 2 : 3;
     static constexpr int kVecs = (kBack ? 4 : 2) * QkUnit<T>::kVecs;  // of a row and thread
     static constexpr int kBytes = kDeep * kVecs * kQkThreads * 16;
-    // tokens a turn: each costs two barriers and the angles' latency (gradient, 4: 193 us, 8: 151, 16: 142)
+    // tokens a turn: each costs two barriers and the angles' latency (gradient, then: 4: 193 us, 8: 151, 16: 142)
     static constexpr int kTokens = kBack && T != VAE_F32 ? 2 * kQkTokens : kQkTokens;
     static constexpr int kResident = kBack ? 4 : 5;  // blocks an SM
     static_assert(kBytes + kTokens * sizeof(QkAngles) + kQkThreads * 64 <= 48 * 1024, "more shared memory than a kernel has without asking");
@@ -652,10 +653,16 @@ int qk_tiles(const vae_qk_norm_rope_desc* a, int* tpb) {
     return (tokens - 1) / *tpb + 1;
 }
 
-// In vectors the queries and the keys have blocks of their own, as many as their share of the heads, `most` in all.
-int qk_share(const vae_qk_norm_rope_desc& a, int tiles, int most, int* qblocks) {
+// In vectors the queries and the keys have blocks of their own, `most` in all, shared out by what their turns cost: the rows
+// of a group of lanes, and as much as kTurnRows rows for the angles and the barriers (36864 tokens of 32 heads and one of
+// 128, bf16, with 0, 2, 4, 8: 245, 133, 110, 111 us, the gradient 461, 219, 176, 163; of 24 and 8 heads 119, 106, 104, 101
+// and 174, 164, 161, 154).
+constexpr int kTurnRows = 8;
+int qk_share(const vae_qk_norm_rope_desc& a, const vae_rope_plan& plan, int tpb, int tiles, int most, int* qblocks) {
+    const int step = (kQkThreads >> qk_form(a.d, plan).glog2) / tpb;
+    const long long wq = (a.hq - 1) / step + 1 + kTurnRows, wk = (a.hk - 1) / step + 1 + kTurnRows;
     const int all = static_cast<int>(std::min<long long>(2LL * tiles, most));
-    const int q = static_cast<int>((static_cast<long long>(all) * a.hq + (a.hq + a.hk) / 2) / (a.hq + a.hk));
+    const int q = static_cast<int>((all * wq + (wq + wk) / 2) / (wq + wk));
     *qblocks = std::min(std::max(q, 1), std::min(all - 1, tiles));
     return *qblocks + std::min(all - *qblocks, tiles);
 }
@@ -731,7 +738,7 @@ int vae_qk_norm_rope(const vae_qk_norm_rope_desc* desc, const void* q_dev, const
     int grid = qk_tiles(desc, &p.tpb);
     const vae_rope_plan none{};
     const vae_rope_plan& pl = plan != nullptr ? *plan : none;
-    if (qk_vectors(p)) grid = qk_share(a, grid, kQkForward, &p.qblocks);
+    if (qk_vectors(p)) grid = qk_share(a, pl, p.tpb, grid, kQkForward, &p.qblocks);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     VAE_CUDA_CHECK(qk_launch<false>(a.type, static_cast<unsigned>(grid), st, p, pl));
     return VAE_OK;
@@ -800,7 +807,7 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
             p.tpb = 2 * kQkTokens;
             tiles = (p.tokens - 1) / p.tpb + 1;
         }
-        grid = kend = qk_share(a, tiles, kQkBlocks, &qblocks);
+        grid = kend = qk_share(a, pl, p.tpb, tiles, kQkBlocks, &qblocks);
     }
     p.qblocks = qblocks;
     p.sums = weights ? static_cast<float*>(workspace_dev) : nullptr;
