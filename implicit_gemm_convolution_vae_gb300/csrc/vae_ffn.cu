@@ -25,6 +25,7 @@
 // gate, up, dgate and dup 113. Small calls are chains of latencies: 256 tokens of 512 x
 // 2048 take 19.6 us, 8 of them in the first kernel.
 #include <algorithm>
+#include <cfloat>
 #include <mutex>
 
 #include "vae_ffn.cuh"
@@ -108,6 +109,8 @@ struct Params {
     const float* residual;
     const unsigned* amax;      // f16 gradients: the bits of the largest |dy|, from `amax_n` blocks
     int amax_n;
+    unsigned* top;             // f16 gradients: the bits of the largest finite |dgate| or |dup| at that scale
+    int again;                 // kBackGate: the second run, at the scale that `top` asks for
     int late;                  // kBackGate: only the epilogue needs the kernel before (that is the one that looks for the largest |dy|)
     int wide;                  // rows of D on 32 bytes
     int tall;                  // the launch has tiles of 512 rows: four stages of 48 KB, one accumulator for each 256 rows
@@ -355,6 +358,21 @@ __device__ __forceinline__ float dy_scale(const Params& p) {
     return bits == 0u || bits >= 0x7f800000u ? 1.f : __uint_as_float(static_cast<unsigned>(2 - e + 127) << 23);
 }
 
+// The scale of dgate and dup: that of dy, or, where the largest of them would pass f16's range with it or lie so low that
+// most are subnormal, the power of two that brings it to 2^14..2^15. (Nothing known ahead bounds dhidden up act' closely:
+// the sum over c of |dy w_down| is some hundred times what dhidden comes to, and up may be any number of f16. So the first
+// run looks, and a second one, which otherwise returns at once (2.4 us of a call), forms them anew.)
+__device__ __forceinline__ unsigned far_top(const Params& p) {  // the largest, or 0 where the scale of dy serves
+    if (p.top == nullptr) return 0u;
+    const unsigned top = __ldcg(p.top);
+    return top > __float_as_uint(65504.f) || top < __float_as_uint(0x1p-10f) ? top : 0u;
+}
+__device__ __forceinline__ float kept_scale(const Params& p) {
+    const unsigned top = far_top(p);
+    const float gain = dy_scale(p);
+    return top == 0u ? gain : gain * __uint_as_float((127u + 14u + 127u - max(top >> 23, 127u - 60u)) << 23);
+}
+
 // ───────────────────────────── epilogue ─────────────────────────────
 
 struct B32 {
@@ -505,7 +523,8 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
     uint32_t phase = 0;
     const int pair = static_cast<int>(blockIdx.x >> 1);
     if (kKind == kBackGate && p.late) pdl_wait();
-    const float gain = kKind >= kBackGate ? dy_scale(p) : 1.f;
+    const float gain = kKind == kGrad || (kKind == kBackGate && p.again) ? kept_scale(p) : kKind == kBackGate ? dy_scale(p) : 1.f;
+    float top = 0.f;
     if (kKind == kGate || kKind == kBackGate)
         for (int i = static_cast<int>(blockIdx.x) * kEpiWarps * 32 + warp * 32 + lane; i < p.clear_n; i += static_cast<int>(gridDim.x) * kEpiWarps * 32)
             p.clear[i] = 0u;
@@ -553,6 +572,20 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
                         v[2 * k + 1] = d1 * u2.y * a1.y;
                         w[2 * k] = d0 * a0.x;
                         w[2 * k + 1] = d1 * a1.x;
+                    }
+                    if constexpr (T == VAE_F16) {
+                        float most = 0.f;  // (columns and rows outside the tensors have gate = up = 0; fmaxf passes over NaN)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) most = fmaxf(most, fmaxf(fabsf(v[k]), fabsf(w[k])));
+                        if (most > FLT_MAX) {  // an infinity, from one of the inputs: the finite ones
+                            most = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                if (fabsf(v[k]) <= FLT_MAX) most = fmaxf(most, fabsf(v[k]));
+                                if (fabsf(w[k]) <= FLT_MAX) most = fmaxf(most, fabsf(w[k]));
+                            }
+                        }
+                        top = fmaxf(top, most);
                     }
                     box_write(box, lane, half * 2 + h, pack16<T>(v));
                     box_write(box + kBox, lane, half * 2 + h, pack16<T>(w));
@@ -652,6 +685,10 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
         }
     }
     if constexpr (kKind == kBackGate) {
+        if (T == VAE_F16 && !p.again) {
+            const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            if (lane == 0 && bits != 0u) atomicMax(p.top, bits);
+        }
         if (half == 0) {  // boxes that a wait that ran out left on their way land before the CTA exits
             int never = 0;
             for (; boxes.taken < boxes.asked; ++boxes.taken)
@@ -668,6 +705,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     constexpr int kStages = ring_stages(kKind);
+    if constexpr (kKind == kBackGate && T == VAE_F16) {
+        if (p.again) {  // (every thread of every CTA sees the same)
+            pdl_wait();
+            if (far_top(p) == 0u) return;
+        }
+    }
     const Smem s = carve<kKind>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -726,10 +769,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// The largest |x| of f16 values, as the bits of an f32, one from each block.
-__global__ void __launch_bounds__(512) amax_kernel(const uint4* x, long long n8, unsigned* amax) {
+// The largest |x| of f16 values, as the bits of an f32, one from each block; sets `zero` to 0.
+__global__ void __launch_bounds__(512) amax_kernel(const uint4* x, long long n8, unsigned* amax, unsigned* zero) {
     __shared__ unsigned tops[16];
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *zero = 0u;
     pdl_launch_dependents();  // the next kernel's products may start: only its epilogue waits for this one
     unsigned top = 0u;
     for (long long i = static_cast<long long>(blockIdx.x) * 512 + threadIdx.x; i < n8; i += static_cast<long long>(gridDim.x) * 512) {
@@ -1054,13 +1098,13 @@ int ffn_forward(const vae_gated_ffn_desc& a, const void* x, const void* wg, cons
     return ffn_launch<T, kDown>(maps, down, p, true, stream);
 }
 
-// Workspace of the gradient: the largest |dy|, dgate, dup, the counters of splits, partial sums.
+// Workspace of the gradient: the largest |dy|, the largest of dgate and dup, dgate, dup, the counters of splits, partial sums.
 struct BackSpace {
     size_t dgate, dup, arrived[2], parts[2], bytes;
 };
 BackSpace back_space(const vae_gated_ffn_desc& a) {
     BackSpace s;
-    s.dgate = up256(kAmaxBlocks * sizeof(unsigned));
+    s.dgate = up256((kAmaxBlocks + 1) * sizeof(unsigned));
     s.dup = s.dgate + up256(mf_bytes(a));
     const Plan plan = plan_for(kGrad, a);
     s.arrived[0] = s.dup + up256(mf_bytes(a));
@@ -1082,9 +1126,10 @@ int ffn_backward(const vae_gated_ffn_desc& a, const void* dy, const void* x, con
         unsigned* amax = reinterpret_cast<unsigned*>(ws);
         const long long n8 = static_cast<long long>(a.m) * a.c / 8;
         p.amax = amax;
+        p.top = amax + kAmaxBlocks;
         p.amax_n = static_cast<int>(std::min<long long>((n8 + 511) / 512, kAmaxBlocks));
         p.late = 1;
-        VAE_CUDA_CHECK(launch_kernel(amax_kernel, dim3(p.amax_n), dim3(512), 0, stream, static_cast<const uint4*>(dy), n8, amax));
+        VAE_CUDA_CHECK(launch_kernel(amax_kernel, dim3(p.amax_n), dim3(512), 0, stream, static_cast<const uint4*>(dy), n8, amax, p.top));
     }
     Maps maps;
     VAE_TRY(ffn_map(&maps.a[0], T, dy, a.m, a.c, kTile));
@@ -1096,7 +1141,14 @@ int ffn_backward(const vae_gated_ffn_desc& a, const void* dy, const void* x, con
     Plan plan = plan_for(kGrad, a);
     p.clear = reinterpret_cast<unsigned*>(ws + at.arrived[0]);
     p.clear_n = arrivals(plan.group[0]) + arrivals(plan.group[1]);
-    VAE_TRY((ffn_launch_act<T, kBackGate>(a.activation, maps, plan_for(kBackGate, a), p, p.late != 0, stream)));
+    const Plan first = plan_for(kBackGate, a);
+    VAE_TRY((ffn_launch_act<T, kBackGate>(a.activation, maps, first, p, p.late != 0, stream)));
+    p.late = 0;
+    if (T == VAE_F16) {
+        p.clear_n = 0;
+        p.again = 1;
+        VAE_TRY((ffn_launch_act<T, kBackGate>(a.activation, maps, first, p, true, stream)));
+    }
     const bool weights = dwg != nullptr;
     VAE_TRY(ffn_map(&maps.a[0], T, dgate, a.m, a.f, kBk));
     VAE_TRY(ffn_map(&maps.a[1], T, dup, a.m, a.f, kBk));
@@ -1107,7 +1159,6 @@ int ffn_backward(const vae_gated_ffn_desc& a, const void* dy, const void* x, con
         VAE_TRY(ffn_map(&maps.b[2], T, x, a.m, a.c, kBk));
         VAE_TRY(ffn_map(&maps.b[3], T, dy, a.m, a.c, kBk));
     }
-    p.late = 0;
     p.half = (a.f + kBk - 1) / kBk;
     p.out[0] = dx;
     p.out[1] = dwg;

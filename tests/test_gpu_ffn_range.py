@@ -1,0 +1,135 @@
+"""The gated feed-forward block far from values of order one: f16 gradients whose dgate
+and dup leave f16's range at the scale of dy. Against the float64 oracle; the
+bounds are those of test_gpu_ffn.py but where a test derives its own."""
+import numpy as np
+import pytest
+
+import implicit_gemm_convolution_vae_gb300 as vg
+import test_gpu_ffn as ffn
+from gpu_common import torch_mod
+from oracle import tokens as ot
+from vae_inputs import rng_for
+
+pytestmark = pytest.mark.gpu
+
+U, FLOOR, SUM = ffn.U, ffn.FLOOR, ffn.SUM
+
+
+def _put(a, t):
+    torch = torch_mod()
+    x = torch.from_numpy(np.ascontiguousarray(a)).to(ffn._t(t)).cuda()
+    return x, ffn._np(x)
+
+
+def _check_f16_backward(dy, x, wg, wu, wd, saved, act, got, w_type):
+    """As test_gpu_ffn's, but for what f16 cuts off dgate and dup: 2^-25 at the scale that brings the largest |dy| to 4..8, or,
+    where the largest of them then lies outside 2^-10..65504, at the one that brings that to 2^14..2^15.
+
+    And SUM counts an operand as no less than f16's smallest normal number, 2^-14. The tensor cores bring the products
+    of a step to one exponent, the largest by the operands' exponent fields, and cut off what lies 2^-23 below; a subnormal
+    operand's field says 2^-14 whatever its value. So what is cut is 2^-23 of max(|a|, 2^-14) max(|b|, 2^-14): of a dy
+    mostly subnormal beside a hidden of 367 it is some sixty times 2^-23 |a b|."""
+    gate, up, hidden = saved
+    m, c = x.shape
+    f = wg.shape[0]
+    dx, dwg, dwu, dwd, dgate, dup = ot.gated_ffn_backward(dy, x, wg, wu, wd, gate, up, hidden, act)
+    a = np.abs
+    n = lambda v, scale=1.0: np.where(v != 0, np.maximum(a(v), 2.0 ** -14 / scale), 0)  # noqa: E731
+    value, slope = ot.activation(gate, act)
+    dh = dy @ wd
+    edh = SUM(c) * (n(dy) @ n(wd))
+    gain = 2.0 ** (2 - np.floor(np.log2(a(dy).max())))
+    top = max(a(dgate).max(), a(dup).max())
+    kept = gain if 2.0 ** -10 <= top * gain <= 65504 else 2.0 ** 14 / top
+    tiny = 2.0 ** -25 / kept
+    u = U["f16"]
+    ev, es = 2.0 ** -21 * a(gate), 2.0 ** -20 * (1 + a(gate) * (1 + gate * gate / 4))
+    eup = edh * (a(value) + ev) + a(dh) * ev
+    eup = eup + (u + 2.0 ** -22) * (a(dup) + eup) + tiny
+    egate = a(up) * (edh * (a(slope) + es) + a(dh) * es)
+    egate = egate + (u + 2.0 ** -22) * (a(dgate) + egate) + tiny
+    ng, nu = n(a(dgate) + egate, kept), n(a(dup) + eup, kept)
+    e = egate @ a(wg) + eup @ a(wu) + SUM(2 * f) * (ng @ n(wg) + nu @ n(wu))
+    assert a(dx).max() < 6e4  # (the result itself is a number of f16)
+    ffn._within(got[0], dx, e + u * (a(dx) + e) + FLOOR["f16"])
+    if got[1] is None:
+        return top * gain
+    for g, ref, e in ((got[1], dwg, egate.T @ a(x) + SUM(m) * (ng.T @ n(x))),
+                      (got[2], dwu, eup.T @ a(x) + SUM(m) * (nu.T @ n(x))),
+                      (got[3], dwd, SUM(m) * (n(dy).T @ n(hidden)))):
+        ffn._within(g, ref, e + U[w_type] * (a(ref) + e) + FLOOR[w_type])
+    return top * gain
+
+
+def _large(kind, m, c, f, act):
+    """Operands of f16 and the saved gate, up and hidden; at the scale of dy the largest of dgate and dup is too large or too
+    small for f16 (but for "plain")."""
+    r = rng_for(3, f"ffn.range.{kind}.{m}.{c}.{f}.{act}")
+    x = r.standard_normal((m, c))
+    wg, wu = r.standard_normal((f, c)) / np.sqrt(c) / 64, r.standard_normal((f, c)) / np.sqrt(c) / 64
+    gate, up = r.standard_normal((m, f)) * 1.5, r.standard_normal((m, f))
+    wd, dy = r.standard_normal((c, f)) / np.sqrt(f), r.standard_normal((m, c)) * 2.0 ** -14
+    if kind == "constant":  # dgate and hidden are ordinary numbers of f16, dgate at the scale of dy is none
+        dy, wd = np.full((m, c), 2.0 ** -14), np.full((c, f), 2.0 ** -6)
+        gate, up = np.full((m, f), 8.0), np.full((m, f), 1024.0)
+    elif kind == "up":  # gates near 0 beside a few large ups
+        gate = gate / 64
+        up[r.random((m, f)) < 0.02] = 1e4
+        wd = np.abs(wd)
+        dy = np.abs(dy)
+    elif kind == "down":  # large weights
+        wd, dy = wd * 0 + 16.0, np.full((m, c), 2.0 ** -20)
+        gate, up = gate * 0 + 6.0, up * 0 + 50.0
+    elif kind == "one":  # a single element
+        gate[m // 2, f // 2], up[m // 2, f // 2], dy[m // 2] = 100.0, 600.0, 2.0 ** -12
+        wd[:, f // 2] = 1.0
+    elif kind == "small":
+        gate, up, wd = gate * 2.0 ** -12, up * 2.0 ** -12, wd * 2.0 ** -4
+    t = {"x": x, "wg": wg, "wu": wu, "wd": wd, "dy": dy, "gate": gate, "up": up}
+    dev, host = {}, {}
+    for k, v in t.items():
+        dev[k], host[k] = _put(v, "f16")
+    dev["hidden"], host["hidden"] = _put(np.clip(ot.activation(host["gate"], act)[0] * host["up"], -6e4, 6e4), "f16")
+    return dev, host
+
+
+def _backward(v, act, **kw):
+    return vg.gated_ffn_backward(v["dy"], v["x"], v["wg"], v["wu"], v["wd"], (v["gate"], v["up"], v["hidden"]), activation=act, **kw)
+
+
+@pytest.mark.parametrize("kind", ["constant", "up", "down", "one", "small"])
+@pytest.mark.parametrize("m,c,f,act", [(1, 1152, 40, "silu"), (40, 1152, 264, "gelu"), (300, 1160, 136, "gelu_tanh"), (4300, 1152, 72, "silu")])
+def test_f16_gradient_whose_parts_leave_the_range_at_the_scale_of_dy(kind, m, c, f, act):
+    torch = torch_mod()
+    dev, h = _large(kind, m, c, f, act)
+    saved = (h["gate"], h["up"], h["hidden"])
+    args = (h["dy"], h["x"], h["wg"], h["wu"], h["wd"], saved, act)
+    got = _backward(dev, act, grad_dtype=torch.float32)
+    top = _check_f16_backward(*args, got, "f32")
+    assert top < 7e-4 if kind == "small" else top > 7e4
+    one = _backward(dev, act, weight_grads=False)
+    assert torch.equal(one[0], got[0])
+    assert all(torch.equal(a, b) for a, b in zip(got, _backward(dev, act, grad_dtype=torch.float32)))
+
+
+def test_f16_gradient_takes_its_scale_anew_in_every_call():
+    """One workspace and one graph for operands that pass the range and for ordinary ones, in turn."""
+    torch = torch_mod()
+    m, c, f, act = 300, 1160, 136, "silu"
+    sets = [_large(k, m, c, f, act)[0] for k in ("plain", "up", "plain", "small", "constant", "plain")]
+    refs = [_backward(v, act, grad_dtype=torch.float32) for v in sets]
+    assert all(torch.isfinite(g).all() for r in refs for g in r)
+    ws = torch.full((vg.gated_ffn_backward_workspace_bytes(m, c, f),), 255, dtype=torch.uint8, device="cuda")
+    for v, r in zip(sets, refs):
+        assert all(torch.equal(a, b) for a, b in zip(_backward(v, act, grad_dtype=torch.float32, workspace=ws), r))
+    held = {k: t.clone() for k, t in sets[0].items()}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = _backward(held, act, grad_dtype=torch.float32, workspace=ws)
+    for v, r in zip(sets, refs):
+        for k, t in held.items():
+            t.copy_(v[k])
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, r))
+    vg.sync_status()
