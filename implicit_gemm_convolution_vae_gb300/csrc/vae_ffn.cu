@@ -107,7 +107,7 @@ struct Params {
     int clear_n;
     int out_f32[2];
     const float* residual;
-    const unsigned* amax;      // f16 gradients: the bits of the largest |dy|, from `amax_n` blocks
+    const unsigned* amax;      // f16 gradients: the bits of the largest finite |dy|, from `amax_n` blocks
     int amax_n;
     unsigned* top;             // f16 gradients: the bits of the largest finite |dgate| or |dup| at that scale
     int again;                 // kBackGate: the second run, at the scale that `top` asks for
@@ -348,14 +348,14 @@ __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
     __syncwarp();
 }
 
-// The power of two that brings the largest |dy| to 4..8 (1 where there is none, or it is not finite). The whole warp.
+// The power of two that brings the largest finite |dy| to 4..8 (1 where there is none but 0). The whole warp.
 __device__ __forceinline__ float dy_scale(const Params& p) {
     if (p.amax == nullptr) return 1.f;
     unsigned bits = 0u;
     for (int i = threadIdx.x & 31; i < p.amax_n; i += 32) bits = max(bits, p.amax[i]);
     bits = __reduce_max_sync(0xffffffffu, bits);
     const int e = static_cast<int>(bits >> 23) - 127;
-    return bits == 0u || bits >= 0x7f800000u ? 1.f : __uint_as_float(static_cast<unsigned>(2 - e + 127) << 23);
+    return bits == 0u ? 1.f : __uint_as_float(static_cast<unsigned>(2 - e + 127) << 23);
 }
 
 // The scale of dgate and dup: that of dy, or, where the largest of them would pass f16's range with it or lie so low that
@@ -769,7 +769,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// The largest |x| of f16 values, as the bits of an f32, one from each block; sets `zero` to 0.
+// (what is not finite counts as 0: it stays in its row, and the other rows keep their scale)
+__device__ __forceinline__ unsigned finite_bits(float x) { return x <= FLT_MAX ? __float_as_uint(x) : 0u; }
+// The largest finite |x| of f16 values, as the bits of an f32, one from each block; sets `zero` to 0.
 __global__ void __launch_bounds__(512) amax_kernel(const uint4* x, long long n8, unsigned* amax, unsigned* zero) {
     __shared__ unsigned tops[16];
     pdl_wait();
@@ -782,7 +784,7 @@ __global__ void __launch_bounds__(512) amax_kernel(const uint4* x, long long n8,
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 f = unpack2<VAE_F16>(u[k] & 0x7fff7fffu);
-            top = max(top, max(__float_as_uint(f.x), __float_as_uint(f.y)));
+            top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
         }
     }
     top = __reduce_max_sync(0xffffffffu, top);

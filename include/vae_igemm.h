@@ -493,10 +493,10 @@ int vae_qk_norm_rope_backward(const vae_qk_norm_rope_desc* desc, const void* dq_
  *   dw_down = dy^T hidden.
  *   dy_dev [m][c] and dx_dev [m][c] of `type`; dw_*_dev of dw_type (`type` or
  *   VAE_F32), all three or none. dgate and dup are rounded to `type` for their
- *   products, in f16 times the power of two that brings the largest |dy| to 4..8,
- *   or, where the largest of dgate and dup would pass f16's range so or fall below
- *   2^-10, that one to 2^14..2^15: none is lost to an infinity, and what f16 cuts off
- *   small ones is at most 2^-15 of the largest.
+ *   products, in f16 times the power of two that brings the largest finite |dy| to
+ *   4..8, or, where the largest of dgate and dup would pass f16's range so or fall
+ *   below 2^-10, that one to 2^14..2^15: none is lost to an infinity, and what f16
+ *   cuts off small ones is at most 2^-15 of the largest.
  * Sums run in a fixed order: the same inputs give the same bits.
  * Requirements: m >= 1; c and f multiples of 8, 8 <= c <= 16384,
  * 8 <= f <= 65536, m <= 2^24; tensors 16-byte aligned. What is written lies apart from

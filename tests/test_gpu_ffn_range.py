@@ -1,6 +1,6 @@
 """The gated feed-forward block far from values of order one: f16 gradients whose dgate
-and dup leave f16's range at the scale of dy. Against the float64 oracle; the
-bounds are those of test_gpu_ffn.py but where a test derives its own."""
+and dup leave f16's range at the scale of dy, elements of dy that are not finite. Against
+the float64 oracle; the bounds are those of test_gpu_ffn.py but where a test derives its own."""
 import numpy as np
 import pytest
 
@@ -133,3 +133,29 @@ def test_f16_gradient_takes_its_scale_anew_in_every_call():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, r))
     vg.sync_status()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("size", [2.0 ** -20, 1.0])
+def test_f16_gradient_of_rows_beside_one_that_is_not_finite(bad, size):
+    """Whatever stands in one element of dy, the other rows' dx, and the parts of dw_down that it does not enter, are those
+    of a call without it, bit for bit."""
+    torch = torch_mod()
+    case = (300, 72, 264, "f16", "silu")
+    (x, x64), (wg, wg64), (wu, wu64), (wd, _) = ffn._case(case)
+    saved, _ = ffn._saved(case, x64, wg64, wu64)
+    dy = ffn._draw(7, "range.dy", (300, 72), "f16")[0].clamp(-4, 4) * size
+    dy[17, 3] = 5.0 * size  # the largest stays where it is
+    ref = vg.gated_ffn_backward(dy, x, wg, wu, wd, saved, grad_dtype=torch.float32)
+    assert all(torch.isfinite(g).all() for g in ref)
+    bdy = dy.clone()
+    bdy[201, 70] = bad
+    got = vg.gated_ffn_backward(bdy, x, wg, wu, wd, saved, grad_dtype=torch.float32)
+    keep = torch.ones(300, dtype=torch.bool, device="cuda")
+    keep[201] = False
+    assert torch.equal(got[0][keep], ref[0][keep]) and not torch.isfinite(got[0][201]).any()
+    cols = torch.ones(72, dtype=torch.bool, device="cuda")
+    cols[70] = False
+    assert torch.equal(got[3][cols], ref[3][cols]) and not torch.isfinite(got[3][70]).any()
+    nothing = vg.gated_ffn_backward(torch.full_like(dy, float("nan")), x, wg, wu, wd, saved)
+    assert all(g.isnan().all() for g in nothing)
