@@ -26,11 +26,15 @@ __device__ __forceinline__ float2 act_both(float g) {
         const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752440f));
         return make_float2(g * cdf, cdf + g * 0.39894228040143267794f * __expf(-0.5f * g * g));
     }
-    constexpr bool silu = kAct == VAE_ACT_SILU;
-    const float z = silu ? g : 1.59576912160573071176f * (g + 0.044715f * g * g * g);
-    const float dz = silu ? 1.f : 1.59576912160573071176f * (1.f + 0.134145f * g * g);
-    const float s = logistic(z);
-    return make_float2(g * s, s * (1.f + g * dz * (1.f - s)));
+    if constexpr (kAct == VAE_ACT_SILU) {
+        const float s = logistic(g);
+        return make_float2(g * s, s * (1.f + g * (1.f - s)));
+    }
+    // the slope's g z' (1 - s) at |g| <= 16: beyond, s is exactly 0 or 1 and so is the slope, but g z' grows as g^3 and would
+    // meet 1 - s = 0, or s = 0, as an infinity
+    const float z = 1.59576912160573071176f * (g + 0.044715f * g * g * g), s = logistic(z);
+    const float h = fminf(fmaxf(g, -16.f), 16.f), dz = 1.59576912160573071176f * (1.f + 0.134145f * h * h);
+    return make_float2(g * s, s * (1.f + h * dz * (1.f - s)));
 }
 
 }  // namespace vae

@@ -1,6 +1,7 @@
 """The gated feed-forward block far from values of order one: f16 gradients whose dgate
-and dup leave f16's range at the scale of dy, elements of dy that are not finite. Against
-the float64 oracle; the bounds are those of test_gpu_ffn.py but where a test derives its own."""
+and dup leave f16's range at the scale of dy, elements of dy that are not finite, gates
+at either end of the activations. Against the float64 oracle; the bounds are those of
+test_gpu_ffn.py but where a test derives its own."""
 import numpy as np
 import pytest
 
@@ -159,3 +160,27 @@ def test_f16_gradient_of_rows_beside_one_that_is_not_finite(bad, size):
     assert torch.equal(got[3][cols], ref[3][cols]) and not torch.isfinite(got[3][70]).any()
     nothing = vg.gated_ffn_backward(torch.full_like(dy, float("nan")), x, wg, wu, wd, saved)
     assert all(g.isnan().all() for g in nothing)
+
+
+@pytest.mark.parametrize("m", [5, 300])
+def test_gelu_tanh_at_the_ends_of_bf16(m):
+    """Far from 0 the activation is g or 0 and its slope 1 or 0: with dhidden = up = 1 and w_gate = 1/16, dx is a
+    sixteenth of the slopes' sum, a number of bf16."""
+    torch = torch_mod()
+    c, f = 8, 16
+    ends = np.array([1e14, -1e14, 2e19, -2e19, 3e38, -3e38, 1e12, -1e12])
+    gate = ends[rng_for(5, f"ffn.ends.{m}").integers(0, 8, (m, f))]
+    gate, g64 = _put(gate, "bf16")
+    one = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    slope = (g64 > 0).astype(np.float64)
+    got = vg.gated_ffn_backward(one(m, c), one(m, c), one(f, c) / 16, one(f, c) * 0, one(c, f) / 8, (gate, one(m, f), one(m, f)),
+                                activation="gelu_tanh", grad_dtype=torch.float32)
+    assert np.array_equal(ffn._np(got[0]), np.repeat(slope.sum(1, keepdims=True) / 16, c, 1))
+    assert np.array_equal(ffn._np(got[1]), np.repeat(slope.sum(0)[:, None], c, 1))
+    # and forward: gate = x w_gate of one channel, up = 1
+    x = torch.zeros(m, c, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = gate[:, 0], 1.0
+    wg, wu = one(f, c) * 0, one(f, c) * 0
+    wg[:, 0], wu[:, 1] = 1.0, 1.0
+    hidden = vg.gated_ffn(x, wg, wu, one(c, f) * 0, activation="gelu_tanh", save=True)[1][2]
+    assert np.array_equal(ffn._np(hidden), np.repeat((g64 * slope)[:, :1], f, 1))
