@@ -184,3 +184,39 @@ def test_gelu_tanh_at_the_ends_of_bf16(m):
     wg[:, 0], wu[:, 1] = 1.0, 1.0
     hidden = vg.gated_ffn(x, wg, wu, one(c, f) * 0, activation="gelu_tanh", save=True)[1][2]
     assert np.array_equal(ffn._np(hidden), np.repeat((g64 * slope)[:, :1], f, 1))
+
+
+@pytest.mark.parametrize("t,low,up", [("bf16", -12.0, 1.0), ("f16", -6.5, 2.0 ** 14)])
+def test_gelu_keeps_its_digits_far_below_zero(t, low, up):
+    """g Phi(g) and its slope within a relative bound. The tail is e^(-g^2/2) times a polynomial that is fitted to 2^-22.5, in
+    some ten roundings (of which the last ones count, 2^-21.5) and two approximate instructions (2^-22): less than 2^-20.
+    The exponent is off by 2.5 units of 2^-24 of g^2 / 2 at most, and the exponential by as much relative: under 2^-23 g^2.
+    The density has the exponential's part of that. Then one rounding to the type; up and dhidden are powers of two."""
+    torch = torch_mod()
+    m, c, f = 257, 8, 8
+    g, g64 = _put(np.linspace(low, 3.0, m), t)
+    value, slope = ot.activation(g64, "gelu")
+    pdf = np.exp(-0.5 * g64 * g64) / np.sqrt(2 * np.pi)
+    ev = (2.0 ** -20 + 2.0 ** -23 * g64 ** 2) * np.abs(value)
+    es = (2.0 ** -20 + 2.0 ** -23 * g64 ** 2) * np.abs(value / np.where(g64 == 0, 1, g64)) + (2.0 ** -21 + 2.0 ** -23 * g64 ** 2) * np.abs(g64) * pdf
+    zero = lambda *s: torch.zeros(s, dtype=ffn._t(t), device="cuda")  # noqa: E731
+    wg, wu = zero(f, c), zero(f, c)
+    wg[:, 0], wu[:, 1] = 1.0, 1.0
+    for rows in (slice(0, m), slice(0, 20), slice(100, 132)):  # many tokens and few
+        x = zero(m, c)
+        x[:, 0], x[:, 1] = g, up
+        hidden = vg.gated_ffn(x[rows], wg, wu, zero(c, f), activation="gelu", save=True)[1][2]
+        ffn._within(hidden[:, 3], (value * up)[rows], up * (ev + U[t] * (np.abs(value) + ev))[rows] + FLOOR[t])
+    # dx takes dgate from one channel and dup from another: dhidden = 1, up = 2^4
+    dy, wd = zero(m, c), zero(c, f)
+    dy[:, 0], wd[0] = 1.0, 1.0
+    wg, wu = zero(f, c), zero(f, c)
+    wg[0, 0], wu[0, 1] = 1.0, 1.0
+    saved = (g[:, None].repeat(1, f), zero(m, f) + 16, zero(m, f))
+    dx = vg.gated_ffn_backward(dy, zero(m, c), wg, wu, wd, saved, activation="gelu", weight_grads=False)[0]
+    # 2^-22: the sums' and the scale's way through f32. In f16 two roundings: of dgate and dup at four times their size (dy is
+    # 1), where the floor is 2^-25 / 4, and of dx; of a subnormal dx they are different ones (-8.606e-8 comes out as
+    # -1.19e-7, 1.11 times a single rounding's bound off)
+    tol = lambda ref, e: e + (U[t] + 2.0 ** -22) * (np.abs(ref) + e) + FLOOR[t] * 1.25  # noqa: E731
+    ffn._within(dx[:, 0], 16 * slope, tol(16 * slope, 16 * es))
+    ffn._within(dx[:, 1], value, tol(value, ev))
