@@ -20,6 +20,7 @@
 // (in f16 times 2^11, which keeps it off the subnormal numbers): the second product takes both with the
 // weights that it has anyway, and y carries its own rounding alone.
 #include <algorithm>
+#include <cfloat>
 
 #include "vae_ffn.cuh"
 #include "vae_ffn_few.h"
@@ -141,10 +142,13 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_kernel(c
         }
     }
     if constexpr (!kGated) {
+        // (a sum that is infinite or NaN without the rest stays so: an infinite weight times a rest of 0, or of the other sign,
+        // would make a NaN of it)
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[0][n][e] = fmaf(d[1][n][e], 1.f / kRest<T>, d[0][n][e]);
+            for (int e = 0; e < 4; ++e)
+                if (fabsf(d[0][n][e]) <= FLT_MAX) d[0][n][e] = fmaf(d[1][n][e], 1.f / kRest<T>, d[0][n][e]);
     }
     // d: rows g, g + 8; tokens 2 t, 2 t + 1. Sixteen warps: the upper ones' first, which the lower ones add to theirs.
     auto each = [&](auto f) {

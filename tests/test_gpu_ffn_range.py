@@ -1,6 +1,6 @@
 """The gated feed-forward block far from values of order one: f16 gradients whose dgate
 and dup leave f16's range at the scale of dy, elements of dy that are not finite, gates
-at either end of the activations. Against the float64 oracle; the bounds are those of
+at either end of the activations, infinite weights. Against the float64 oracle; the bounds are those of
 test_gpu_ffn.py but where a test derives its own."""
 import numpy as np
 import pytest
@@ -220,3 +220,23 @@ def test_gelu_keeps_its_digits_far_below_zero(t, low, up):
     tol = lambda ref, e: e + (U[t] + 2.0 ** -22) * (np.abs(ref) + e) + FLOOR[t] * 1.25  # noqa: E731
     ffn._within(dx[:, 0], 16 * slope, tol(16 * slope, 16 * es))
     ffn._within(dx[:, 1], value, tol(value, ev))
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [1, 20, 40])
+def test_infinite_weights_reach_their_outputs_alone(t, m):
+    """An infinite element of w_down makes its column of y infinite, with the sign of hidden; of few tokens too, whose second
+    part of hidden may be 0 or have the other sign."""
+    torch = torch_mod()
+    case = (m, 72, 136, t, "silu")
+    (x, _), (wg, _), (wu, _), (wd, _) = ffn._case(case)
+    y, saved = vg.gated_ffn(x, wg, wu, wd, save=True)
+    bad = wd.clone()
+    bad[5, 100], bad[70, 3] = float("inf"), float("-inf")
+    z = vg.gated_ffn(x, wg, wu, bad)
+    keep = torch.ones(72, dtype=torch.bool, device="cuda")
+    keep[5] = keep[70] = False
+    assert torch.equal(z[:, keep], y[:, keep])
+    hidden = saved[2].float()
+    assert (hidden[:, 100] != 0).all() and (hidden[:, 3] != 0).all()
+    assert torch.equal(z[:, 5].float(), hidden[:, 100] * float("inf")) and torch.equal(z[:, 70].float(), hidden[:, 3] * float("-inf"))
