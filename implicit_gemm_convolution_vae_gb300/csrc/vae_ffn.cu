@@ -54,7 +54,7 @@ constexpr int kAmaxBlocks = 128;        // that look for the largest |dy|, at mo
 // 64-byte rows 93; the number of requests counts.)
 constexpr int kBox = 32 * 128;
 constexpr int kBoxBufs = 3;
-__host__ __device__ constexpr int ring_stages(int kind) { return kind == kBackGate ? 4 : 7; }
+__host__ __device__ constexpr int ring_stages(int kind, bool tall = false) { return tall ? kTallStages : kind == kBackGate ? 4 : 7; }
 __host__ __device__ constexpr int side_bytes(int kind) { return kind == kBackGate ? 4 * kBoxBufs * 2 * kBox : 0; }
 __host__ __device__ constexpr int smem_bytes(int kind) { return 1024 + ring_stages(kind) * kStage + side_bytes(kind) + 512; }
 static_assert(kTallStages * kTallStage <= ring_stages(kGrad) * kStage, "the ring holds the tall stages");
@@ -83,7 +83,6 @@ struct Params {
     int again;                 // kBackGate: the second run, at the scale that `top` asks for
     int late;                  // kBackGate: only the epilogue needs the kernel before (that is the one that looks for the largest |dy|)
     int wide;                  // rows of D on 32 bytes
-    int tall;                  // the launch has tiles of 512 rows: four stages of 48 KB, one accumulator for each 256 rows
     DevStatus* status;
     unsigned long long timeout_ns;
 };
@@ -146,10 +145,13 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
     return d;
 }
 
-template <int kKind>
+// A launch's tiles have 256 rows, or (kTall) up to 512: four stages of 48 KB, one accumulator for each 256 rows. (One kernel
+// for both, with the stages and the second rows' loads and products looked up at run time: 1024 tokens of 2048 x 5504, no tall
+// tiles, second product 34 us and 28, dx and the weights' gradients 107 and 90; a loop over the rows in every kind: 16384
+// tokens of 1152 x 4608, first product 225 us and 197.)
+template <int kKind, bool kTall>
 __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, int rank) {
-    const bool tall = (kKind == kDown || kKind == kGrad) && p.tall != 0;
-    const int stages = tall ? kTallStages : ring_stages(kKind), stage_bytes = tall ? kTallStage : kStage;
+    constexpr int stages = ring_stages(kKind, kTall), stage_bytes = kTall ? kTallStage : kStage;
     int stage = 0;
     uint32_t phase = 0, armed = 0, arm_par = 0;
     bool ok = true;
@@ -159,7 +161,7 @@ __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, 
         const int row = ti.m0 + rank * kTile, col = kKind == kGate ? ti.n0 : ti.n0 + rank * (ti.n / 2);
         // rows of B that a CTA loads: those of a full tile where the map's box says so, else boxes of 64
         const int brows = b_mn(kKind) ? ti.n / 2 : kKind == kGate ? p.group[0].wide : p.group[0].wide / 2;
-        const uint32_t bytes = static_cast<uint32_t>(ti.subs) * kOperand + (b_mn(kKind) ? (brows > 64 ? 2u : 1u) * 64 * 128 : static_cast<uint32_t>(brows) * 128);
+        const uint32_t bytes = static_cast<uint32_t>(kTall ? ti.subs : 1) * kOperand + (b_mn(kKind) ? (brows > 64 ? 2u : 1u) * 64 * 128 : static_cast<uint32_t>(brows) * 128);
         for (int kk = ti.k0; kk < ti.k1; ++kk) {
             ok = mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, s.abort_flag, p.timeout_ns, p.status, kWhereProducerEmpty);
             if (!ok) break;
@@ -167,25 +169,24 @@ __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, 
             if (rank == 0) mbar_arrive_expect_tx(fb, 2u * bytes);
             const uint32_t fb0 = mapa_shared(fb, 0u);
             uint8_t *a = s.ring + stage * stage_bytes, *b = a + kOperand;
-            for (int sub = 0; sub < ti.subs; ++sub) {
-                uint8_t* as = a + sub * kStage;
-                const int r = row + sub * 2 * kTile;
-                if constexpr (kKind == kGrad) {
-                    if (ti.g == 0) {  // dx: rows of dgate or dup as they lie, in boxes of 64
-                        const int seg = kk >= p.half ? 1 : 0, k = (kk - seg * p.half) * kBk;
-                        tma_load_2d_pair(smem_u32(as), &maps.a[seg], fb0, k, r);
-                        tma_load_2d_pair(smem_u32(as + kOperand / 2), &maps.a[seg], fb0, k, r + 64);
-                        if (sub == 0) load_mn(b, &maps.b[seg], fb0, col, brows, k);
-                    } else {
-                        load_mn(as, &maps.a[ti.z - 1], fb0, r, kTile, kk * kBk);
-                        if (sub == 0) load_mn(b, &maps.b[ti.z == 3 ? 3 : 2], fb0, col, brows, kk * kBk);
-                    }
-                } else {
-                    tma_load_2d_pair(smem_u32(as), &maps.a[0], fb0, kk * kBk, r);
-                    if (sub > 0) continue;
-                    if constexpr (kKind == kBackGate) load_mn(b, &maps.b[0], fb0, col, brows, kk * kBk);
-                    else tma_load_2d_pair(smem_u32(b), &maps.b[kKind == kGate ? rank : 0], fb0, kk * kBk, col);
-                }
+            if constexpr (kKind == kGrad) {
+                const int seg = kk >= p.half ? 1 : 0, k = (kk - seg * p.half) * kBk;  // (dx)
+                // dx: rows of dgate or dup as they lie, in boxes of 64
+                const auto rows = [&](uint8_t* at, int r) {
+                    if (ti.g != 0) return load_mn(at, &maps.a[ti.z - 1], fb0, r, kTile, kk * kBk);
+                    tma_load_2d_pair(smem_u32(at), &maps.a[seg], fb0, k, r);
+                    tma_load_2d_pair(smem_u32(at + kOperand / 2), &maps.a[seg], fb0, k, r + 64);
+                };
+                rows(a, row);
+                if (ti.g == 0) load_mn(b, &maps.b[seg], fb0, col, brows, k);
+                else load_mn(b, &maps.b[ti.z == 3 ? 3 : 2], fb0, col, brows, kk * kBk);
+                if (kTall && ti.subs > 1) rows(a + kStage, row + 2 * kTile);
+            } else {
+                tma_load_2d_pair(smem_u32(a), &maps.a[0], fb0, kk * kBk, row);
+                if constexpr (kKind == kBackGate) load_mn(b, &maps.b[0], fb0, col, brows, kk * kBk);
+                else tma_load_2d_pair(smem_u32(b), &maps.b[kKind == kGate ? rank : 0], fb0, kk * kBk, col);
+                if constexpr (kTall)
+                    if (ti.subs > 1) tma_load_2d_pair(smem_u32(a + kStage), &maps.a[0], fb0, kk * kBk, row + 2 * kTile);
             }
             armed |= 1u << stage;
             arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
@@ -205,11 +206,10 @@ __device__ void role_producer(const Params& p, const Smem& s, const Maps& maps, 
 }
 
 // The whole warp runs the loop and one lane issues: descriptors stay in uniform registers.
-template <int T, int kKind>
+template <int T, int kKind, bool kTall>
 __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
-    const bool tall = (kKind == kDown || kKind == kGrad) && p.tall != 0;
-    const int stages = tall ? kTallStages : ring_stages(kKind);
-    const uint32_t stage_step = static_cast<uint32_t>(tall ? kTallStage : kStage) >> 4;
+    constexpr int stages = ring_stages(kKind, kTall);
+    constexpr uint32_t stage_step = static_cast<uint32_t>(kTall ? kTallStage : kStage) >> 4;
     constexpr uint32_t ab = T == VAE_BF16 ? 1u : 0u;
     constexpr uint32_t idesc0 = (1u << 4) | (ab << 7) | (ab << 10) | ((b_mn(kKind) ? 1u : 0u) << 16) | ((2u * kTile >> 4) << 24);
     constexpr uint32_t bstep = b_mn(kKind) ? 2048 >> 4 : 2;
@@ -238,12 +238,15 @@ __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
             const uint32_t off = static_cast<uint32_t>(stage) * stage_step;
             if (elect_one()) {
 #pragma unroll
-                for (uint32_t j = 0; j < kBk / 16; ++j) {
+                for (uint32_t j = 0; j < kBk / 16; ++j)
                     umma_f16_pair(d, ad + (off + j * astep), bd + (off + j * bstep), idesc, j != 0 || k != 0 ? 1u : 0u);
-                    if ((kKind == kDown || kKind == kGrad) && ti.subs > 1)
-                        umma_f16_pair(d + kMaxCols, ad + (off + (kStage >> 4) + j * astep), bd + (off + j * bstep), idesc,
-                                      j != 0 || k != 0 ? 1u : 0u);
-                }
+                if constexpr (kTall)
+                    if (ti.subs > 1) {
+#pragma unroll
+                        for (uint32_t j = 0; j < kBk / 16; ++j)
+                            umma_f16_pair(d + kMaxCols, ad + (off + (kStage >> 4) + j * astep), bd + (off + j * bstep), idesc,
+                                          j != 0 || k != 0 ? 1u : 0u);
+                    }
                 umma_commit_pair(smem_u32(&s.empty[stage]));
                 if (k + 1 == nk) umma_commit_pair(smem_u32(&s.accf[buf]));
             }
@@ -253,7 +256,7 @@ __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
                 phase ^= 1u;
             }
         }
-        if (!tall) buf ^= 1;
+        if (!kTall) buf ^= 1;
         if (buf == 0) accphase ^= 1u;
     }
     if (elect_one()) {
@@ -428,7 +431,7 @@ __device__ __forceinline__ void add_parts(const float* part, long long each, int
 }
 
 // Warp w: lane quadrant w % 4 of TMEM (a row per lane), half w / 4 of the columns.
-template <int T, int kKind, int kAct>
+template <int T, int kKind, int kAct, bool kTall>
 __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, uint32_t tmem, int warp, int lane, int rank) {
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -549,7 +552,7 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
             }
         }
         if constexpr (kKind == kDown || kKind == kGrad) {
-            for (int sub = 0; sub < ti.subs; ++sub) {
+            for (int sub = 0; sub < (kTall ? ti.subs : 1); ++sub) {
                 const int r = row + sub * 2 * kTile;
 #pragma unroll 1
                 for (int c = 0; c < mine; c += 16) {
@@ -563,7 +566,7 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]) * scale;
                     if (r >= rows) continue;
-                    if (gr.splits > 1) put_part(p.parts[ti.g] + ti.part * part_size(gr) + part_at(gr, ti, rank, warp, lane) + c * 32, v);
+                    if (!kTall && gr.splits > 1) put_part(p.parts[ti.g] + ti.part * part_size(gr) + part_at(gr, ti, rank, warp, lane) + c * 32, v);
                     else put_out<T, kKind>(p, ti, r, n, left, v);
                 }
             }
@@ -571,9 +574,9 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acce[buf]), 0u));
-        if (!((kKind == kDown || kKind == kGrad) && p.tall != 0)) buf ^= 1;
+        if (!kTall) buf ^= 1;
         if (buf == 0) phase ^= 1u;
-        if constexpr (kKind == kDown || kKind == kGrad) {
+        if constexpr ((kKind == kDown || kKind == kGrad) && !kTall) {
             if (gr.splits > 1) {
                 // The last split to store this warp's part of the tile adds them all up, in their order: nobody waits, and
                 // the sum does not depend on who is last.
@@ -613,7 +616,7 @@ __device__ void role_epilogue(const Params& p, const Smem& s, const Maps& maps, 
     }
 }
 
-template <int T, int kKind, int kAct>
+template <int T, int kKind, int kAct, bool kTall>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -659,12 +662,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *s.tmem_slot;
     if (warp < kEpiWarps) {
-        role_epilogue<T, kKind, kAct>(p, s, maps, tmem, warp, lane, rank);
+        role_epilogue<T, kKind, kAct, kTall>(p, s, maps, tmem, warp, lane, rank);
     } else if (warp == kTmaWarp) {
-        if (lane == 0) role_producer<kKind>(p, s, maps, rank);
+        if (lane == 0) role_producer<kKind, kTall>(p, s, maps, rank);
         __syncwarp();
     } else if (rank == 0) {
-        role_mma<T, kKind>(p, s, tmem);
+        role_mma<T, kKind, kTall>(p, s, tmem);
     }
     pdl_launch_dependents();
     tc_fence_before();
@@ -743,22 +746,24 @@ Plan plan_for(int kind, const vae_gated_ffn_desc& a) {
 
 std::mutex g_mu;
 
-template <int T, int kKind, int kAct>
+template <int T, int kKind, int kAct, bool kTall>
 int ffn_setup() {
     static CtxOnce once;
     int dev = 0;
     VAE_CUDA_CHECK(cudaGetDevice(&dev));
     std::lock_guard<std::mutex> lk(g_mu);
     if (!once.done(dev)) {
-        VAE_CUDA_CHECK(cudaFuncSetAttribute(ffn_kernel<T, kKind, kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kKind)));
+        VAE_CUDA_CHECK(cudaFuncSetAttribute(ffn_kernel<T, kKind, kAct, kTall>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kKind)));
         once.mark(dev);
     }
     return VAE_OK;
 }
 
-template <int T, int kKind, int kAct = VAE_ACT_SILU>
+template <int T, int kKind, int kAct = VAE_ACT_SILU, bool kTall = false>
 int ffn_launch(const Maps& maps, const Plan& plan, Params& p, bool ahead, cudaStream_t stream) {
-    int rc = ffn_setup<T, kKind, kAct>();
+    if constexpr ((kKind == kDown || kKind == kGrad) && !kTall)
+        if (plan.group[0].tall > 1) return ffn_launch<T, kKind, kAct, true>(maps, plan, p, ahead, stream);
+    int rc = ffn_setup<T, kKind, kAct, kTall>();
     if (rc != VAE_OK) return rc;
     p.status = device_status_ptr();
     if (p.status == nullptr) return VAE_ERR_CUDA;
@@ -766,7 +771,6 @@ int ffn_launch(const Maps& maps, const Plan& plan, Params& p, bool ahead, cudaSt
     p.group[0] = plan.group[0];
     p.group[1] = plan.group[1];
     p.deal = plan.deal;
-    p.tall = plan.group[0].tall > 1;
     const int count = plan.group[1].problems > 0 ? 2 : 1;
     if (sm_count() < 2 * kPairs) deal_out(kKind, p.group, count, sm_count() / 2, &p.deal);
     int pairs = 0, at = 0;  // up to the last one with work
@@ -775,7 +779,7 @@ int ffn_launch(const Maps& maps, const Plan& plan, Params& p, bool ahead, cudaSt
         for (int c = 0; c < 4; ++c)
             if (p.deal.count[r][c] > 0) pairs = at;
     }
-    VAE_CUDA_CHECK(launch_kernel_as(ahead || pdl_enabled(), ffn_kernel<T, kKind, kAct>, dim3(2 * pairs), dim3(kThreads), smem_bytes(kKind),
+    VAE_CUDA_CHECK(launch_kernel_as(ahead || pdl_enabled(), ffn_kernel<T, kKind, kAct, kTall>, dim3(2 * pairs), dim3(kThreads), smem_bytes(kKind),
                                     stream, maps, p));
     return VAE_OK;
 }
