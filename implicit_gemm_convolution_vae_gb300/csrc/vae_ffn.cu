@@ -237,16 +237,17 @@ __device__ void role_mma(const Params& p, const Smem& s, uint32_t tmem) {
             tc_fence_after();
             const uint32_t off = static_cast<uint32_t>(stage) * stage_step;
             if (elect_one()) {
+                if (kTall && ti.subs > 1) {
 #pragma unroll
-                for (uint32_t j = 0; j < kBk / 16; ++j)
-                    umma_f16_pair(d, ad + (off + j * astep), bd + (off + j * bstep), idesc, j != 0 || k != 0 ? 1u : 0u);
-                if constexpr (kTall)
-                    if (ti.subs > 1) {
-#pragma unroll
-                        for (uint32_t j = 0; j < kBk / 16; ++j)
-                            umma_f16_pair(d + kMaxCols, ad + (off + (kStage >> 4) + j * astep), bd + (off + j * bstep), idesc,
-                                          j != 0 || k != 0 ? 1u : 0u);
+                    for (uint32_t j = 0; j < kBk / 16; ++j) {
+                        umma_f16_pair(d, ad + (off + j * astep), bd + (off + j * bstep), idesc, j != 0 || k != 0 ? 1u : 0u);
+                        umma_f16_pair(d + kMaxCols, ad + (off + (kStage >> 4) + j * astep), bd + (off + j * bstep), idesc, j != 0 || k != 0 ? 1u : 0u);
                     }
+                } else {
+#pragma unroll
+                    for (uint32_t j = 0; j < kBk / 16; ++j)
+                        umma_f16_pair(d, ad + (off + j * astep), bd + (off + j * bstep), idesc, j != 0 || k != 0 ? 1u : 0u);
+                }
                 umma_commit_pair(smem_u32(&s.empty[stage]));
                 if (k + 1 == nk) umma_commit_pair(smem_u32(&s.accf[buf]));
             }

@@ -107,12 +107,12 @@ VAE_BOTH bool tile_at(const Group* groups, const Deal& deal, int pair, int i, Ti
 VAE_BOTH int part_cols(const Group& g) { return g.nfull * g.wide + g.rest; }
 VAE_BOTH long long part_size(const Group& g) { return static_cast<long long>(g.nm) * 2 * kTile * part_cols(g); }
 
-// Cycles that a pair takes for a stage of a tile of n accumulator columns, as measured: the stage's bytes from L2 (with
-// every SM asking, 46 a cycle and CTA), or the hand-over between loads and products; of a tall tile the products
-// themselves. An operand that lies MN-major comes in boxes of 64 rows for each CTA.
-inline int stage_cycles(int kind, int n, int tall) {
-    const int rows = 256 * tall + (b_mn(kind) ? (n > 128 ? 256 : 128) : n);
-    return std::max(std::max(430, rows * 7 / 5), tall > 1 ? n * 17 / 4 : 0);
+// Cycles that a pair takes for a stage of a tile of n accumulator columns, as measured: the stage's bytes from L2, 57 a
+// cycle and CTA, or the hand-over between loads and products; of a tall tile the products themselves. An operand that lies
+// MN-major comes in boxes of 64 rows for each CTA, the others as the rows of a full tile (`wide`).
+inline int stage_cycles(int kind, int n, int wide, int tall) {
+    const int rows = 256 * tall + (b_mn(kind) ? (n > 128 ? 256 : 128) : wide);
+    return std::max(std::max(430, rows * 113 / 100), tall > 1 ? n * 17 / 4 : 0);
 }
 
 inline int class_tiles(const Group& g, int rest) {
@@ -134,9 +134,11 @@ inline long long deal_out(int kind, const Group* groups, int count, int pairs, D
         // its stages, or where they are few its way out of TMEM (which runs under the next tile's stages, but for the tall ones)
         const int n = ((c & 1) != 0 ? g.rest : g.wide) * per;
         const long long part = g.splits > 1 ? 22LL * n : 0;  // a split's sums, written and read; beside much other work that hides
-        const long long in = 400 + (kind == kDown ? part : 0) + static_cast<long long>(stage_cycles(kind, n, g.tall)) * ((g.nk + g.splits - 1) / g.splits);
+        const long long in = 400 + (kind == kDown ? part : 0) + static_cast<long long>(stage_cycles(kind, n, g.wide * per, g.tall)) * ((g.nk + g.splits - 1) / g.splits);
         const long long out = 600 + part + 12LL * n;
-        cost[c] = g.tall > 1 ? in + 2 * out : std::max(in, out);
+        // (a tall tile takes a little less, of dx and the weights' gradients a seventh: with every SM asking for long sums the
+        // others' stages come slower than counted, and these read a quarter less)
+        cost[c] = g.tall > 1 ? (in + out) * (kind == kGrad ? 86 : 94) / 100 : std::max(in, out);
     }
     std::sort(d->order, d->order + 4, [&](int a, int b) { return cost[a] != cost[b] ? cost[a] > cost[b] : a < b; });
     for (int c : d->order) {
@@ -203,12 +205,15 @@ inline size_t parts_bytes(const Group& g) {
 }
 // Counters of a group's splits: for each tile, CTA of the pair and epilogue warp.
 inline int arrivals(const Group& g) { return g.splits > 1 ? g.problems * g.nm * (g.nfull + (g.rest > 0 ? 1 : 0)) * 2 * kEpiWarps : 0; }
-// The tile width and the splits with the least time, counted in cycles of the busiest pair. Wide tiles read the least;
+// The tile widths and the splits with the least time, counted in cycles of the busiest pair. Wide tiles read the least;
 // narrow ones and splits give work to more SMs. Splits cost, beside each tile's sums, the last one's way through all of
-// them: as measured 4000 cycles and 40 for each column (kDown, with splits and without, bf16: 256 tokens of 512 x 2048
-// 19.7 and 21.0 us, of 1152 x 4608 25.7 and 36.1, 512 of 2048 x 5504 48 and 55; 4096 of 1152 x 4608, whole, 101 and not 109),
-// of the gradients 80 and 10 for each split (one token of 512 x 2048 25.5 us, 28 with fewer, which splits more; the
-// whole one 38).
+// them. Of the gradients each group has its own width and splits: dx is long sums over few tiles, the weights' gradients of
+// few tokens short ones over many, whose way out of TMEM counts. What splits and tall tiles cost is fitted to the measured
+// times of the widths with every number of splits at 174 shapes, 1 to 32768 tokens and 256 x 1024 to 4096 x 11008 (bf16, in
+// a graph): the plan taken is 0.7 % over the best of them on average for the second product, 8 % at most, and 2.5 %, 13 %,
+// for the gradients. (One width for both groups of the gradients and a higher charge: one token of 1152 x 4608 52 us and 44,
+// 1024 tokens 95 and 68, 256 of 2048 x 5504 88 and 69; 256 of 512 x 2048 forward, in eight splits and in four, 19.0 us and
+// 17.4.)
 inline Plan make_plan(int kind, int m, int c, int f) {
     const int kc = (c + kBk - 1) / kBk, kf = (f + kBk - 1) / kBk, km = (m + kBk - 1) / kBk, count = kind == kGrad ? 2 : 1;
     Group base[2] = {};
@@ -222,37 +227,70 @@ inline Plan make_plan(int kind, int m, int c, int f) {
     }
     const int per = kind == kGate ? 2 : 1;  // accumulator columns per column
     const bool whole = kind == kGate || kind == kBackGate;  // (their epilogues need the whole sums)
+    struct Cut {
+        int wide[2], splits[2], tall;
+    };
+    const auto look = [&](const Cut& c, Plan* p) {
+        long long sums = 0, join = 0;
+        for (int g = 0; g < count; ++g) {
+            const Group& r = p->group[g] = cut_group(base[g], c.wide[g] / per, c.splits[g], c.tall);
+            if (r.splits == 1) continue;
+            sums += 1LL * r.splits * r.problems * r.rows * r.cols;
+            join = std::max(join, kind == kDown ? 3000 + (40LL + 8 * r.splits) * c.wide[g] : (8LL + 4 * r.splits) * c.wide[g]);
+        }
+        // (kGrad: the sums' way through L2, beside what else is on it; the others: the last tile's epilogue)
+        const long long end = kind == kGrad ? sums * 3 / (20 * kPairs) : kind == kDown ? 0 : 10LL * c.wide[0];
+        return deal_out(kind, p->group, count, kPairs, &p->deal) + join + end;
+    };
     Plan best{};
     long long least = -1;
-    const auto look = [&](int wide, const int (&splits)[2], int tall) {
+    const auto take = [&](const Cut& c) {
         Plan p{};
-        for (int g = 0; g < count; ++g) p.group[g] = cut_group(base[g], wide / per, splits[g], tall);
-        long long t = deal_out(kind, p.group, count, kPairs, &p.deal) + 10 * wide;  // (the last tile's epilogue)
-        const int most = std::max(splits[0], count > 1 ? splits[1] : 1);
-        if (most > 1) t += 4000 + (kind == kDown ? 40 : 80 + 10LL * most) * wide;
+        const long long t = look(c, &p);
         if (least >= 0 && t >= least) return false;
         best = p;
         least = t;
         return true;
     };
-    if (!whole) look(kMaxCols, {1, 1}, 2);
-    for (int wide = kMaxCols; wide >= 64; wide -= 64) {
-        int splits[2] = {1, 1};
-        look(wide, splits, 1);
-        bool many = true;  // with many tiles neither splits nor narrow ones can win
-        for (int g = count - 1; g >= 0; --g) {  // one group's splits, then the other's beside them
-            const Group cut = cut_group(base[g], wide / per, 1, 1);
-            if (class_tiles(cut, 0) + class_tiles(cut, 1) >= 4 * kPairs) continue;
-            many = false;
-            int own = 1;
-            for (int s : {2, 3, 4, 6, 8}) {
-                if (whole || s > kMaxSplits || s * 4 > base[g].nk) break;
-                splits[g] = s;
-                if (look(wide, splits, 1)) own = s;
-            }
-            splits[g] = own;
+    // with many tiles neither splits nor narrow ones can win
+    const auto many = [&](int g, int wide) {
+        const Group cut = cut_group(base[g], wide / per, 1, 1);
+        return class_tiles(cut, 0) + class_tiles(cut, 1) >= 4 * kPairs;
+    };
+    if (!whole) take({{kMaxCols, kMaxCols}, {1, 1}, 2});
+    if (count == 1) {
+        for (int wide = kMaxCols; wide >= 64; wide -= 64) {
+            take({{wide, wide}, {1, 1}, 1});
+            if (many(0, wide)) break;
+            for (int s : {2, 3, 4, 6, 8})
+                if (!whole && s <= kMaxSplits && s * 4 <= base[0].nk) take({{wide, wide}, {s, 1}, 1});
         }
-        if (many) break;
+        return best;
+    }
+    // both groups alike first, then one's width and splits beside the other's
+    Cut now{{kMaxCols, kMaxCols}, {1, 1}, 1};
+    for (int wide = kMaxCols; wide >= 64; wide -= 64)
+        if (const Cut c{{wide, wide}, {1, 1}, 1}; take(c)) now = c;
+    for (int g = count - 1; g >= 0; --g) {
+        Cut own = now;
+        long long t = -1;
+        for (int wide = kMaxCols; wide >= 64; wide -= 64)
+            for (int s : {1, 2, 3, 4, 6, 8}) {
+                if (s > 1 && (s > kMaxSplits || s * 4 > base[g].nk || many(g, wide))) break;
+                Cut c = now;
+                c.wide[g] = wide;
+                c.splits[g] = s;
+                Plan p{};
+                if (const long long k = look(c, &p); t < 0 || k < t) {
+                    t = k;
+                    own = c;
+                    if (k < least) {
+                        best = p;
+                        least = k;
+                    }
+                }
+            }
+        now = own;
     }
     return best;
 }
