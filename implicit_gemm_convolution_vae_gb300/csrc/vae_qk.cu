@@ -179,14 +179,6 @@ struct QkUnit {
     static constexpr int kVecs = T == VAE_F32 ? 2 : 1;
     using E = typename Elem<T>::type;
     uint4 r[kVecs];
-    __device__ __forceinline__ void load(const E* p) {
-        r[0] = *reinterpret_cast<const uint4*>(p);
-        if constexpr (T == VAE_F32) r[1] = *reinterpret_cast<const uint4*>(p + 4);
-    }
-    __device__ __forceinline__ void clear() {
-        r[0] = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (T == VAE_F32) r[1] = r[0];
-    }
     // In shared memory the vectors of a unit lie kQkThreads apart. Without `in` zeros come.
     __device__ __forceinline__ static void fetch(uint4* at, const E* p, bool in) {
 #pragma unroll
