@@ -1022,6 +1022,8 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, activation: str = "si
     ``weight_grads`` False the last three are None and not computed."""
     if dy is None or x is None or w_gate is None or w_up is None or w_down is None or saved is None:
         _given(dy=dy, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, saved=saved)
+    if not isinstance(saved, (tuple, list)) or len(saved) != 3:
+        raise VaeError(-1, "saved must be the (gate, up, hidden) that gated_ffn returned")
     gate, up, hidden = saved
     _given(gate=gate, up=up, hidden=hidden)
     index = _device_of((("dy", dy), ("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down), ("gate", gate),
