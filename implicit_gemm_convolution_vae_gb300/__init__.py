@@ -509,6 +509,7 @@ def _given(**tensors):
             raise VaeError(-1, f"{name} is needed")
 
 
+_F32_MAX = 3.4028234663852886e38
 _INT = (1 << 31) - 1  # the C ABI's sizes; ctypes would cut a larger one off without a word
 
 
@@ -850,11 +851,15 @@ def _qk_desc(q, k, gamma_q, gamma_k, positions, plan, eps, q_out, k_out, dq_out=
         na = len(plan.axes)
         if len(pshape) == 3:
             pb = pshape[0]
+            if pb != 1 and pb != b:
+                raise VaeError(-2, f"positions of {pb} batch entries for a batch of {b}")
             _tensor(positions, "positions", pt, (pb, s, na))
         else:
             _tensor(positions, "positions", pt, (s, na))
     elif plan is not None:
         raise VaeError(-1, "positions and plan come together")
+    if not -_F32_MAX <= eps <= _F32_MAX:
+        raise VaeError(-1, f"eps must be > 0 and finite, got {eps}")
     if q_out is None:
         q_out, qs = _T.empty(shape, dtype=dtype, device=q.device), _dense(s, hq, d)
     else:
