@@ -240,3 +240,71 @@ def test_infinite_weights_reach_their_outputs_alone(t, m):
     hidden = saved[2].float()
     assert (hidden[:, 100] != 0).all() and (hidden[:, 3] != 0).all()
     assert torch.equal(z[:, 5].float(), hidden[:, 100] * float("inf")) and torch.equal(z[:, 70].float(), hidden[:, 3] * float("-inf"))
+
+
+def test_the_largest_number_of_tokens():
+    """2^24 tokens: rows at the ends and around the middle as those of a short call, and zeros elsewhere; the weights'
+    gradients, sums of the same 160 terms in another order, each within SUM of the terms' absolute values."""
+    torch = torch_mod()
+    m, c, f = 1 << 24, 8, 16
+    places = [0, m // 2 - 20, 9_000_001, m - 40]
+    x, dy = (ffn._draw(11, "far." + n, (160, c), "bf16")[0] for n in ("x", "dy"))
+    wg, wu, wd = (ffn._draw(11, "far." + n, s, "bf16", 0.3)[0] for n, s in (("g", (f, c)), ("u", (f, c)), ("d", (c, f))))
+
+    def spread(short):
+        long = torch.zeros(m, c, dtype=torch.bfloat16, device="cuda")
+        for i, at in enumerate(places):
+            long[at:at + 40] = short[40 * i:40 * i + 40]
+        return long
+
+    gather = lambda t: torch.cat([t[at:at + 40] for at in places])  # noqa: E731
+    y, saved = vg.gated_ffn(spread(x), wg, wu, wd, save=True)
+    ry, rsaved = vg.gated_ffn(x, wg, wu, wd, save=True)
+    assert torch.equal(gather(y), ry) and all(torch.equal(gather(a), b) for a, b in zip(saved, rsaved))
+    assert int((y != 0).any(1).sum()) == int((ry != 0).any(1).sum())
+    got = vg.gated_ffn_backward(spread(dy), spread(x), wg, wu, wd, saved, grad_dtype=torch.float32)
+    ref = vg.gated_ffn_backward(dy, x, wg, wu, wd, rsaved, grad_dtype=torch.float32)
+    assert torch.equal(gather(got[0]), ref[0]) and int((got[0] != 0).any(1).sum()) == int((ref[0] != 0).any(1).sum())
+    g, u, h = (ffn._np(t) for t in rsaved)
+    *_, dgate, dup = ot.gated_ffn_backward(ffn._np(dy), ffn._np(x), ffn._np(wg), ffn._np(wu), ffn._np(wd), g, u, h)
+    for a, b, left, right in ((got[1], ref[1], dgate, ffn._np(x)), (got[2], ref[2], dup, ffn._np(x)), (got[3], ref[3], ffn._np(dy), h)):
+        assert (np.abs(ffn._np(a) - ffn._np(b)) <= 2 * SUM(160) * (np.abs(left).T @ np.abs(right))).all()
+
+
+@pytest.mark.parametrize("m", [20, 40])
+def test_the_largest_widths(m):
+    """16384 channels over 65536 hidden ones, few tokens and many, both ways, against torch in 64 bits on the GPU; the bounds are those of
+    test_gpu_ffn.py."""
+    torch = torch_mod()
+    c, f, u = 16384, 65536, U["bf16"]
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    draw = lambda *s, std=1.0: (torch.randn(s, generator=gen, device="cuda") * std).bfloat16()  # noqa: E731
+    x, dy, wg, wu, wd = draw(m, c), draw(m, c), draw(f, c, std=c ** -0.5), draw(f, c, std=c ** -0.5), draw(c, f, std=f ** -0.5)
+    y, saved = vg.gated_ffn(x, wg, wu, wd, save=True)
+    near = lambda got, ref, e: (got.double() - ref).abs() <= e + u * (ref.abs() + e)  # noqa: E731
+    d = lambda t: t.double()  # noqa: E731
+    gate, up, eg, eu = d(x) @ d(wg).T, d(x) @ d(wu).T, SUM(c) * (d(x).abs() @ d(wg).abs().T), SUM(c) * (d(x).abs() @ d(wu).abs().T)
+    s = torch.sigmoid(gate)
+    eh = up.abs() * (1.13 * eg + 2.0 ** -21 * gate.abs()) + ((gate * s).abs() + 1.13 * eg) * eu + 2.0 ** -23 * (gate * s * up).abs()
+    assert all(near(a, b, e).all() for a, b, e in zip(saved, (gate, up, gate * s * up), (eg, eu, eh)))
+    h = (gate * s * up).abs()
+    assert near(y, (gate * s * up) @ d(wd).T, (eh + u * (h + eh) + SUM(f) * h) @ d(wd).abs().T).all()
+    got = vg.gated_ffn_backward(dy, x, wg, wu, wd, saved)
+    gate, up, hidden = map(d, saved)
+    s = torch.sigmoid(gate)
+    value, slope = gate * s, s * (1 + gate * (1 - s))
+    dh, edh = d(dy) @ d(wd), SUM(c) * (d(dy).abs() @ d(wd).abs())
+    dgate, dup = dh * up * slope, dh * value
+    es = 2.0 ** -20 * (1 + gate.abs() * (1 + gate * gate / 4))
+    eup = edh * (value.abs() + 2.0 ** -21 * gate.abs()) + dh.abs() * 2.0 ** -21 * gate.abs()
+    eup = eup + (u + 2.0 ** -22) * (dup.abs() + eup)
+    egate = up.abs() * (edh * (slope.abs() + es) + dh.abs() * es)
+    egate = egate + (u + 2.0 ** -22) * (dgate.abs() + egate)
+    e = egate @ d(wg).abs() + eup @ d(wu).abs() + SUM(2 * f) * ((dgate.abs() + egate) @ d(wg).abs() + (dup.abs() + eup) @ d(wu).abs())
+    assert near(got[0], dgate @ d(wg) + dup @ d(wu), e).all()
+    for rows in (slice(0, 2048), slice(f // 2 - 300, f // 2 + 300), slice(f - 2048, f)):  # of hidden
+        ax, ad = d(x).abs(), d(dy).abs()
+        assert near(got[1][rows], dgate[:, rows].T @ d(x), egate[:, rows].T @ ax + SUM(m) * ((dgate.abs() + egate)[:, rows].T @ ax)).all()
+        assert near(got[2][rows], dup[:, rows].T @ d(x), eup[:, rows].T @ ax + SUM(m) * ((dup.abs() + eup)[:, rows].T @ ax)).all()
+        assert near(got[3][:, rows], d(dy).T @ hidden[:, rows], SUM(m) * (ad.T @ hidden[:, rows].abs())).all()
+    vg.sync_status()
