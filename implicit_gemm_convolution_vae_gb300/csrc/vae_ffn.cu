@@ -17,13 +17,13 @@
 // rows, "tall"); few tiles become narrow ones, or splits of the contraction, whose last
 // one to finish adds them up.
 //
-// What bounds the products is the way from L2 to shared memory, 46 bytes a cycle and
-// CTA when every SM asks: a 256 x 256 x 64 stage (32 KB a CTA) takes 700 cycles of it and 512 of
+// What bounds the products is the way from L2 to shared memory beside the tensor cores: a 256
+// x 256 x 64 stage (32 KB a CTA) takes 578 cycles of it, more with every SM asking for long, and 512 of
 // the tensor cores. Tall tiles read a quarter less. 16384 tokens of 1152 x 4608, bf16,
-// in a graph: 312 us forward (1670 TFLOP/s), the gradient 675 to 720 on different machines
-// (1450 to 1545). Of the gradient's first kernel (174 us) the products alone take 91, its stages' way 124,
-// gate, up, dgate and dup 113. Small calls are chains of latencies: 256 tokens of 512 x
-// 2048 take 19.6 us, 8 of them in the first kernel.
+// in a graph: 292 to 302 us forward (1740 TFLOP/s; the first product 197), the gradient 673 to 713 on
+// different machines (1460 to 1550). Of the gradient's first kernel (180 us) the products alone take
+// 91, its stages' way 124, gate, up, dgate and dup 113. Small calls are chains of latencies: 256
+// tokens of 512 x 2048 take 17.4 us, 8 of them in the first kernel.
 #include <algorithm>
 #include <cfloat>
 #include <mutex>

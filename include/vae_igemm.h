@@ -430,7 +430,8 @@ int vae_rope(const void* x_dev, int type, int b, int s, int h, int d, const long
  * one pass: for each head x of d channels,
  *   n = x / sqrt(mean(x^2) + eps), z = n * gamma, y = the pairs of z turned by
  *   the angles of its token (vae_rope's rule),
- * in f32, rounded once.
+ * in f32, rounded once (x^2 and its sum too: heads whose squares pass f32's
+ * range come out as 0 or NaN).
  *   q_dev [b][s][hq][d], k_dev [b][s][hk][d] of `type`, *_stride = {batch,
  *   token, head} in elements, channels contiguous; q_out_dev, k_out_dev
  *   likewise (each may be its own input, with the same strides). The keys may go
